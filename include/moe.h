@@ -380,6 +380,137 @@ moe_status moe_device_status(moe_handle* h, void* stream);
  * the context and the handle stay usable. Asynchronous on `stream`. */
 moe_status moe_selftest_timeout(moe_handle* h, void* stream);
 
+/* ---- The layer for a few tokens (serving) ----
+ * moe_forward runs row tiles of 128 tokens per expert; a decode step has a few
+ * tokens in all, and its time is the reading of the chosen experts' weights.
+ * moe_decode computes the same layer for up to MOE_DECODE_MAX_TOKENS tokens and
+ * reads each chosen expert's weights once. No backward, no saved state. */
+enum { MOE_DECODE_MAX_TOKENS = 64 };
+typedef struct moe_decoder moe_decoder;
+
+/* Bytes of device workspace a decoder for `cfg` needs. The fields of moe_config
+ * mean what they mean for a handle, except: max_tokens is at most
+ * MOE_DECODE_MAX_TOKENS; hidden and inter need only be multiples of 8 (MXFP8
+ * routed weights: of 32); recompute_dispatch must be 0; act_precision is not
+ * looked at (the activations between the products are kept in fp32, and reach
+ * the second product as two bf16 terms, as with MOE_ACT_FP32; MXFP8 weights are
+ * multiplied by unquantised activations). */
+moe_status moe_decode_size(const moe_config* cfg, size_t* bytes);
+
+/* Creates a decoder over caller-owned device workspace (256-byte aligned, >=
+ * moe_decode_size bytes, kept alive and unused by others until
+ * moe_decode_destroy). Calls of one decoder run on one stream, or are ordered by
+ * the caller. The current CUDA device at this call is the device of every call. */
+moe_status moe_decode_create(const moe_config* cfg, void* workspace, size_t workspace_bytes, moe_decoder** out);
+void moe_decode_destroy(moe_decoder* d);
+
+/* out[t] = gate[t] SharedSwiGLU(hidden[t]) + sum_s topk_probs[t,s] RoutedSwiGLU_{topk_ids[t,s]}(hidden[t])
+ *   hidden[T,H] bf16 with row stride hidden_stride, out[T,H] bf16 with row stride
+ *   out_stride (elements; hidden rows 16-byte aligned, hidden_stride a multiple of
+ *   8), topk_ids[T,k] int32 (-1: empty slot) and topk_probs[T,k] fp32 compact, as
+ *   for moe_forward_topk: a row with an id outside [-1, E) or the same id twice is
+ *   MOE_ERR_ROUTING (moe_decode_status) and keeps its shared part only.
+ *   0 <= T <= max_tokens. out must not overlap hidden.
+ * Weights as for moe_forward (views or per-expert tables, shared expert and output
+ * gate optional as configured); of MXFP8 views the rowwise payload and scales are
+ * read, the columnwise ones may be NULL, and moe_prepare_weights is not needed.
+ * Per-expert tables are uploaded when their pointers change; such a call cannot be
+ * captured into a CUDA graph. Results are deterministic: the sums' order depends
+ * on the shape and the routing alone. */
+moe_status moe_decode(moe_decoder* d, int64_t T, const void* hidden, int64_t hidden_stride,
+                      const int32_t* topk_ids, const float* topk_probs, const moe_weights* w, void* out,
+                      int64_t out_stride, void* stream);
+
+/* Synchronises `stream`, returns the status recorded since the last call (MOE_OK,
+ * MOE_ERR_ROUTING or MOE_ERR_TIMEOUT) and clears it. */
+moe_status moe_decode_status(moe_decoder* d, void* stream);
+
+/* ---- The norm in front of the layer ----
+ * Layer norm, or with MOE_NORM_RMS its form without the mean, over rows of
+ * `hidden` elements, with the residual add before it and the residual stream's
+ * gradient after it; 1 <= hidden <= 32768. Rows may have any stride >= hidden and
+ * any alignment of their element type; 16-byte aligned rows are the fast case. */
+typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
+typedef enum { MOE_T_BF16 = 0, MOE_T_FP32 = 1 } moe_dtype;
+typedef struct {
+    int64_t hidden;
+    float eps;        /* >= 0, added to the variance (mean square) */
+    int32_t kind;     /* moe_norm_kind */
+    int32_t x_type;   /* moe_dtype of x, residual, sum, dsum, dx (the residual stream) */
+    int32_t y_type;   /* moe_dtype of y and dy (the layer's input) */
+    int32_t w_type;   /* moe_dtype of weight and bias */
+} moe_norm_config;
+
+/* s = x + residual rounded to x_type (residual NULL: s = x); y = (s - mean) rstd weight + bias,
+ * mean 0 for MOE_NORM_RMS; bias NULL: none. x, residual, sum, y: [T, hidden] with
+ * row strides in elements; sum receives s (required with residual, else ignored;
+ * may be x or residual itself). mean[T] (layer norm only) and rstd[T] fp32 receive
+ * the statistics, both optional. Statistics and arithmetic in fp32. */
+moe_status moe_norm_forward(const moe_norm_config* cfg, int64_t T, const void* x, int64_t x_stride,
+                            const void* residual, int64_t residual_stride, const void* weight, const void* bias,
+                            void* sum, int64_t sum_stride, void* y, int64_t y_stride, float* mean, float* rstd,
+                            void* stream);
+
+/* Bytes of device workspace moe_norm_backward needs for T rows. */
+moe_status moe_norm_backward_size(const moe_norm_config* cfg, int64_t T, size_t* bytes);
+
+/* Gradients at the rows that were normalised (x = the forward's s) and its
+ * statistics: dx = rstd (g - mean(g) - xhat mean(g xhat)) + dsum, g = weight dy,
+ * xhat = (x - mean) rstd (no mean(g) for MOE_NORM_RMS); dsum (optional): the
+ * gradient that reaches s past the norm; dx may be dsum itself. dweight = sum_t dy xhat and
+ * dbias = sum_t dy, each optional, are written (accumulate 0) or added (accumulate
+ * 1) to [hidden] buffers of g_type (moe_gtype: fp32, or bf16 with
+ * main_grad = bf16(main_grad + bf16(dw)), as the layer's main_grads). Row sums and
+ * the sums over rows are fp32, in an order fixed by the shape. workspace:
+ * 256-byte aligned, >= moe_norm_backward_size bytes; calls that share it must be
+ * ordered. */
+moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* dy, int64_t dy_stride,
+                             const void* x, int64_t x_stride, const void* weight, const float* mean,
+                             const float* rstd, const void* dsum, int64_t dsum_stride, void* dx, int64_t dx_stride,
+                             void* dweight, void* dbias, int32_t g_type, int32_t accumulate, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* ---- The router: from logits to the ids and probs of moe_forward_topk / moe_decode ----
+ * score = softmax(logits) or sigmoid(logits), over the experts of a row. The topk
+ * experts with the largest logits (a score grows with its logit; equal logits: the
+ * lower id) are chosen, in falling order; with select_bias (fp32 [E], or NULL) the
+ * order is that of score + select_bias, which the probs do not see. A logit of
+ * -inf closes its expert to the token: a row with fewer than topk open experts has
+ * -1 and prob 0 in its last slots. probs = scale * score, with `normalise` divided by the
+ * sum of the row's chosen scores. A NaN logit is never chosen and makes its row's
+ * probs NaN. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef struct {
+    int64_t num_experts;  /* E, 1..1024 */
+    int64_t topk;         /* k, 1..min(E, 32) */
+    int32_t score;        /* moe_score */
+    int32_t normalise;    /* 0 or 1 */
+    float scale;
+    float aux_coeff;      /* balance loss: aux_coeff E sum_e (counts[e] / (k T)) (sum_t P[t,e] / T), */
+    float z_coeff;        /* P = score / its row sum; z loss: z_coeff / T sum_t logsumexp(logits[t])^2 */
+    int32_t x_type;       /* moe_dtype of logits and dlogits */
+} moe_router_config;
+
+/* Bytes of device workspace moe_router_forward needs for T tokens. */
+moe_status moe_router_size(const moe_router_config* cfg, int64_t T, size_t* bytes);
+
+/* logits[T,E] with row stride logits_stride (elements) -> ids[T,k] int32, probs[T,k]
+ * fp32, counts[E] int32 (routes per expert; may be NULL without losses) and losses[2]
+ * fp32 {balance, z} (NULL: not computed). Rows without an open expert add nothing to
+ * the losses. workspace as for moe_norm_backward. Sums over tokens are fp32, in an
+ * order fixed by the shape. */
+moe_status moe_router_forward(const moe_router_config* cfg, int64_t T, const void* logits, int64_t logits_stride,
+                              const float* select_bias, int32_t* ids, float* probs, int32_t* counts, float* losses,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* dlogits[T,E] (row stride dlogits_stride) of sum(dprobs * probs) + loss_grad *
+ * (balance + z), for the forward's ids (and its counts, needed when aux_coeff and
+ * loss_grad are not 0); the choice itself and the counts have no gradient. Closed experts
+ * get 0. dlogits may be logits itself. */
+moe_status moe_router_backward(const moe_router_config* cfg, int64_t T, const void* logits, int64_t logits_stride,
+                               const int32_t* ids, const float* dprobs, const int32_t* counts, float loss_grad,
+                               void* dlogits, int64_t dlogits_stride, void* stream);
+
 /* Number of kernels this library has launched in this process. */
 uint64_t moe_launch_count(void);
 

@@ -6,6 +6,7 @@ the library cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -18,6 +19,10 @@ MOE_ERR_ROUTING, MOE_ERR_TIMEOUT = 3, 5    # device-detected errors (moe_device_
 MOE_W_BF16, MOE_W_MXFP8 = 0, 1
 MOE_G_FP32, MOE_G_BF16 = 0, 1
 MOE_ACT_FP32, MOE_ACT_BF16 = 0, 1   # activations between the expert GEMMs (include/moe.h, moe_act)
+MOE_DECODE_MAX_TOKENS = 64
+MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
+MOE_T_BF16, MOE_T_FP32 = 0, 1       # element types of the norm's and the router's tensors (moe_dtype)
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_ROUTING",
                 4: "MOE_ERR_CUDA", 5: "MOE_ERR_TIMEOUT", 6: "MOE_ERR_STATE"}
 WEIGHT_NAMES = ("shared_gate", "shared_up", "shared_down", "routed_gate", "routed_up", "routed_down")
@@ -43,6 +48,16 @@ class moe_main_grads(ctypes.Structure):
                 [("shared_output_gate", c_void_p), ("dtype", c_int32), ("expert_ptrs", c_void_p * 3)])
 
 
+class moe_norm_config(ctypes.Structure):
+    _fields_ = [("hidden", c_int64), ("eps", c_float), ("kind", c_int32), ("x_type", c_int32), ("y_type", c_int32),
+                ("w_type", c_int32)]
+
+
+class moe_router_config(ctypes.Structure):
+    _fields_ = [("num_experts", c_int64), ("topk", c_int64), ("score", c_int32), ("normalise", c_int32),
+                ("scale", c_float), ("aux_coeff", c_float), ("z_coeff", c_float), ("x_type", c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -56,7 +71,10 @@ EXPORTED = ("moe_workspace_size", "moe_create", "moe_destroy", "moe_saved_size",
             "moe_launch_count", "moe_status_string", "moe_profile_enable", "moe_profile_read", "moe_kernel_name",
             "moe_route_noalloc", "moe_prepare_weights", "moe_quantize_mxfp8", "moe_profile_select",
             "moe_forward_topk", "moe_handle_config", "moe_host_pipe_size", "moe_host_pipe_create", "moe_host_step",
-            "moe_host_pipe_sync", "moe_host_pipe_destroy", "moe_selftest_timeout")
+            "moe_host_pipe_sync", "moe_host_pipe_destroy", "moe_selftest_timeout",
+            "moe_decode_size", "moe_decode_create", "moe_decode_destroy", "moe_decode", "moe_decode_status",
+            "moe_norm_forward", "moe_norm_backward_size", "moe_norm_backward",
+            "moe_router_size", "moe_router_forward", "moe_router_backward")
 MOE_K_COUNT = 20
 
 
@@ -115,6 +133,25 @@ def load(build_if_missing: bool = True):
         L.moe_host_pipe_sync.argtypes = [c_void_p]
         L.moe_host_pipe_destroy.argtypes = [c_void_p]
         L.moe_host_pipe_destroy.restype = None
+        V = c_void_p
+        L.moe_decode_size.argtypes = [P(moe_config), P(c_size_t)]
+        L.moe_decode_create.argtypes = [P(moe_config), V, c_size_t, P(V)]
+        L.moe_decode_destroy.argtypes = [V]
+        L.moe_decode_destroy.restype = None
+        L.moe_decode.argtypes = [V, c_int64, V, c_int64, V, V, P(moe_weights), V, c_int64, V]
+        L.moe_decode_status.argtypes = [V, V]
+        L.moe_norm_forward.argtypes = [P(moe_norm_config), c_int64, V, c_int64, V, c_int64, V, V, V, c_int64, V,
+                                       c_int64, V, V, V]
+        L.moe_norm_backward_size.argtypes = [P(moe_norm_config), c_int64, P(c_size_t)]
+        L.moe_norm_backward.argtypes = [P(moe_norm_config), c_int64, V, c_int64, V, c_int64, V, V, V, V, c_int64, V,
+                                        c_int64, V, V, c_int32, c_int32, V, c_size_t, V]
+        L.moe_router_size.argtypes = [P(moe_router_config), c_int64, P(c_size_t)]
+        L.moe_router_forward.argtypes = [P(moe_router_config), c_int64, V, c_int64, V, V, V, V, V, V, c_size_t, V]
+        L.moe_router_backward.argtypes = [P(moe_router_config), c_int64, V, c_int64, V, V, V, c_float, V, c_int64, V]
+        for name in ("moe_decode_size", "moe_decode_create", "moe_decode", "moe_decode_status", "moe_norm_forward",
+                     "moe_norm_backward_size", "moe_norm_backward", "moe_router_size", "moe_router_forward",
+                     "moe_router_backward"):
+            getattr(L, name).restype = c_int32
         for name in ("moe_workspace_size", "moe_saved_size", "moe_create", "moe_saved_create", "moe_forward",
                      "moe_backward", "moe_export_routing", "moe_device_status", "moe_profile_enable",
                      "moe_profile_read", "moe_route_noalloc", "moe_prepare_weights", "moe_quantize_mxfp8",
@@ -291,6 +328,95 @@ def mxfp8_view(payload, scale, col_payload, col_scale) -> moe_wview:
                      col_payload.data_ptr(), col_scale.data_ptr())
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _ld(t):
+    """Row stride of a [T, n] tensor with contiguous rows; a single row has none of its own."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _raw_stream(stream, device):
+    """cudaStream_t of a torch stream, or of the current stream of `device`."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def moe_decode_size(cfg: moe_config) -> int:
+    n = c_size_t(0)
+    _check(load().moe_decode_size(ctypes.byref(cfg), ctypes.byref(n)), "moe_decode_size")
+    return n.value
+
+
+def moe_decode_create(cfg: moe_config, workspace) -> c_void_p:
+    d = c_void_p()
+    _check(load().moe_decode_create(ctypes.byref(cfg), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                    ctypes.byref(d)), "moe_decode_create")
+    return d
+
+
+def moe_decode_destroy(d):
+    load().moe_decode_destroy(d)
+
+
+def moe_decode(d, T, hidden, topk_ids, topk_probs, weights: moe_weights, out, stream=None):
+    """The layer for up to 64 tokens; hidden and out are 2-D tensors whose rows may be strided."""
+    _check(load().moe_decode(d, T, hidden.data_ptr(), _ld(hidden), topk_ids.data_ptr(), topk_probs.data_ptr(),
+                             weights, out.data_ptr(), _ld(out), _raw_stream(stream, hidden.device)), "moe_decode")
+
+
+def moe_decode_status(d, stream=None) -> int:
+    return int(load().moe_decode_status(d, _stream_ptr(stream)))
+
+
+def moe_norm_forward(cfg: moe_norm_config, x, weight, y, bias=None, residual=None, sum=None, mean=None, rstd=None,
+                     stream=None):
+    _check(load().moe_norm_forward(cfg, x.shape[0], x.data_ptr(), _ld(x), _addr(residual),
+                                   0 if residual is None else _ld(residual), weight.data_ptr(), _addr(bias),
+                                   _addr(sum), 0 if sum is None else _ld(sum), y.data_ptr(), _ld(y),
+                                   _addr(mean), _addr(rstd), _raw_stream(stream, x.device)), "moe_norm_forward")
+
+
+def moe_norm_backward_size(cfg: moe_norm_config, T: int) -> int:
+    n = c_size_t(0)
+    _check(load().moe_norm_backward_size(cfg, T, ctypes.byref(n)), "moe_norm_backward_size")
+    return n.value
+
+
+def moe_norm_backward(cfg: moe_norm_config, dy, x, weight, mean, rstd, dx, dsum=None, dweight=None, dbias=None,
+                      g_type=MOE_G_FP32, accumulate=False, workspace=None, stream=None):
+    _check(load().moe_norm_backward(cfg, x.shape[0], dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x),
+                                    weight.data_ptr(), _addr(mean), rstd.data_ptr(), _addr(dsum),
+                                    0 if dsum is None else _ld(dsum), dx.data_ptr(), _ld(dx),
+                                    _addr(dweight), _addr(dbias), g_type, 1 if accumulate else 0, _addr(workspace),
+                                    0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                    _raw_stream(stream, x.device)), "moe_norm_backward")
+
+
+def moe_router_size(cfg: moe_router_config, T: int) -> int:
+    n = c_size_t(0)
+    _check(load().moe_router_size(cfg, T, ctypes.byref(n)), "moe_router_size")
+    return n.value
+
+
+def moe_router_forward(cfg: moe_router_config, logits, ids, probs, counts=None, losses=None, select_bias=None,
+                       workspace=None, stream=None):
+    _check(load().moe_router_forward(cfg, logits.shape[0], logits.data_ptr(), _ld(logits), _addr(select_bias),
+                                     ids.data_ptr(), probs.data_ptr(), _addr(counts), _addr(losses), _addr(workspace),
+                                     0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                     _raw_stream(stream, logits.device)), "moe_router_forward")
+
+
+def moe_router_backward(cfg: moe_router_config, logits, ids, dprobs, dlogits, counts=None, loss_grad=1.0,
+                        stream=None):
+    _check(load().moe_router_backward(cfg, logits.shape[0], logits.data_ptr(), _ld(logits), ids.data_ptr(),
+                                      dprobs.data_ptr(), _addr(counts), loss_grad, dlogits.data_ptr(),
+                                      _ld(dlogits), _raw_stream(stream, logits.device)), "moe_router_backward")
+
+
 def moe_launch_count() -> int:
     return int(load().moe_launch_count())
 
@@ -344,6 +470,25 @@ def weights_from_combined(shared_fc1, shared_fc2, routed_fc1, routed_fc2, shared
     shared = (moe_wview(), moe_wview(), moe_wview()) if shared_fc1 is None else \
         (wview(shared_fc1[:inter]), wview(shared_fc1[inter:]), wview(shared_fc2))
     return moe_weights(*shared, wview(routed_fc1[:, :inter]), wview(routed_fc1[:, inter:]), wview(routed_fc2),
+                       None if shared_output_gate is None else shared_output_gate.data_ptr())
+
+
+def weights_from_combined_mxfp8(shared_fc1, shared_fc2, routed_q1, routed_scale1, routed_q2, routed_scale2,
+                                shared_output_gate=None) -> moe_weights:
+    """weights_from_combined with MXFP8 routed weights given by their rowwise payloads
+    ([E,2I,H], [E,H,I] uint8) and compact E8M0 scales ([E,2I,H/32], [E,H,I/32]) alone:
+    what moe_decode reads (the layer's backward takes the columnwise ones as well)."""
+    inter = routed_q1.shape[1] // 2
+
+    def view(q, s):
+        if q.stride(-1) != 1 or s.stride(-1) != 1 or s.stride(0) * 32 != q.stride(0) or s.stride(1) * 32 != q.stride(1):
+            raise ValueError("MXFP8 scales must have the payload's strides / 32")
+        return moe_wview(q.data_ptr(), q.stride(0), q.stride(1), s.data_ptr())
+
+    shared = (moe_wview(), moe_wview(), moe_wview()) if shared_fc1 is None else \
+        (wview(shared_fc1[:inter]), wview(shared_fc1[inter:]), wview(shared_fc2))
+    return moe_weights(*shared, view(routed_q1[:, :inter], routed_scale1[:, :inter]),
+                       view(routed_q1[:, inter:], routed_scale1[:, inter:]), view(routed_q2, routed_scale2),
                        None if shared_output_gate is None else shared_output_gate.data_ptr())
 
 
@@ -565,3 +710,206 @@ class HostPipe:
         except Exception:
             pass
 
+
+
+def _allocate_on(stream):
+    """Context in which new tensors belong to `stream` (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(stream)
+
+
+def _require(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+class MoEDecoder:
+    """The layer for a few tokens (include/moe.h, moe_decode): holds a decoder and its workspace."""
+
+    def __init__(self, max_tokens, hidden, num_experts, topk, inter, device="cuda", routed_wtype=MOE_W_BF16,
+                 swiglu_limit=0.0, shared_expert=True):
+        import torch
+        self.cfg = moe_config(max_tokens, hidden, num_experts, topk, inter, routed_wtype, float(swiglu_limit), 0,
+                              MOE_ACT_FP32, 0 if shared_expert else 1)
+        self.hidden, self.topk = int(hidden), int(topk)
+        self.device = torch.device(device)
+        self._bf16, self._i32, self._f32 = torch.bfloat16, torch.int32, torch.float32
+        self._empty = torch.empty
+        self.workspace = torch.empty(moe_decode_size(self.cfg), dtype=torch.uint8, device=self.device)
+        with torch.cuda.device(self.device):
+            self.handle = moe_decode_create(self.cfg, self.workspace)
+
+    def forward_topk(self, hidden, topk_ids, topk_probs, weights: moe_weights, out=None, stream=None):
+        """out [T,H] of bf16 hidden [T,H] (rows may be strided), int32 ids [T,k] (-1 = empty
+        slot) and fp32 probs [T,k], for T up to max_tokens."""
+        T = hidden.shape[0]
+        _require(hidden.dtype == self._bf16 and hidden.dim() == 2 and hidden.shape[1] == self.hidden and
+                 (hidden.stride(1) == 1 or T == 0), "hidden must be [T, H] bf16 with contiguous rows")
+        _require(topk_ids.dtype == self._i32 and topk_probs.dtype == self._f32 and
+                 topk_ids.shape == (T, self.topk) and topk_probs.shape == (T, self.topk) and
+                 topk_ids.is_contiguous() and topk_probs.is_contiguous(),
+                 "topk_ids and topk_probs must be contiguous [T, k] int32 and fp32")
+        if out is None:
+            with _allocate_on(stream):
+                out = self._empty((T, self.hidden), dtype=self._bf16, device=hidden.device)
+        else:
+            _require(out.dtype == self._bf16 and out.shape == hidden.shape and out.stride(1) == 1,
+                     "out must be [T, H] bf16 with contiguous rows")
+        moe_decode(self.handle, T, hidden, topk_ids, topk_probs, weights, out, stream)
+        return out
+
+    def device_status(self, stream=None) -> int:
+        return moe_decode_status(self.handle, stream)
+
+    def close(self):
+        if getattr(self, "handle", None) is not None:
+            moe_decode_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class MoENorm:
+    """Layer norm or RMS norm in front of the layer (include/moe.h, moe_norm_forward)."""
+
+    def __init__(self, hidden, eps=1e-5, kind=MOE_NORM_LAYER, device="cuda"):
+        import torch
+        self.hidden, self.eps, self.kind, self.device = int(hidden), float(eps), int(kind), torch.device(device)
+        self._types = {torch.bfloat16: MOE_T_BF16, torch.float32: MOE_T_FP32}
+        self._cfgs, self._sizes = {}, {}
+        self._torch = torch
+
+    def _cfg(self, x, y, w):
+        key = (x, y, w)
+        c = self._cfgs.get(key)
+        if c is None:
+            _require(all(t in self._types for t in key), "tensors must be bf16 or fp32")
+            c = self._cfgs[key] = moe_norm_config(self.hidden, self.eps, self.kind, *(self._types[t] for t in key))
+        return c
+
+    def _rows(self, t, like, dtype, what):
+        _require(t.dim() == 2 and t.shape == like.shape and t.shape[1] == self.hidden and t.dtype == dtype and
+                 t.stride(1) == 1, what + " must be [T, hidden] rows of the right type")
+
+    def _weights(self, weight, bias):
+        for t in (weight, bias):
+            _require(t is None or (t.shape == (self.hidden,) and t.is_contiguous() and t.dtype == weight.dtype),
+                     "weight and bias must be contiguous [hidden] vectors of one type")
+
+    def forward(self, x, weight, bias=None, residual=None, out_dtype=None, stream=None):
+        """(y, s, mean, rstd): s = x + residual (x itself without one), y = norm(s) weight + bias in
+        out_dtype (x's by default); mean is None for RMS norm. s, mean and rstd are what backward takes."""
+        torch = self._torch
+        self._rows(x, x, x.dtype, "x")
+        self._weights(weight, bias)
+        if residual is not None:
+            self._rows(residual, x, x.dtype, "residual")
+        dtype = x.dtype if out_dtype is None else out_dtype
+        cfg = self._cfg(x.dtype, dtype, weight.dtype)
+        T = x.shape[0]
+        with _allocate_on(stream):
+            y = torch.empty(x.shape, dtype=dtype, device=x.device)
+            total = torch.empty(x.shape, dtype=x.dtype, device=x.device) if residual is not None else None
+            rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+            mean = torch.empty(T, dtype=torch.float32, device=x.device) if self.kind == MOE_NORM_LAYER else None
+        moe_norm_forward(cfg, x, weight, y, bias, residual, total, mean, rstd, stream)
+        return y, (x if total is None else total), mean, rstd
+
+    def backward(self, dy, s, weight, mean, rstd, dsum=None, bias=False, dweight=None, dbias=None, accumulate=False,
+                 stream=None):
+        """(ds, dweight, dbias) for the gradient dy of y, joined by dsum, the gradient that reaches s
+        past the norm. dweight (and, with `bias`, dbias) are new fp32 vectors, or the given
+        fp32 / bf16 buffers, overwritten or (accumulate) added to."""
+        torch = self._torch
+        self._rows(s, s, s.dtype, "s")
+        self._rows(dy, s, dy.dtype, "dy")
+        self._weights(weight, None)
+        if dsum is not None:
+            self._rows(dsum, s, s.dtype, "dsum")
+        T = s.shape[0]
+        for v, need in ((mean, self.kind == MOE_NORM_LAYER), (rstd, True)):
+            _require(not need or (v is not None and v.dtype == torch.float32 and v.shape == (T,) and
+                                  v.is_contiguous()), "mean and rstd must be the forward's [T] fp32")
+        _require(not accumulate or (dweight is not None and (dbias is not None or not bias)),
+                 "accumulate adds to given buffers")
+        cfg = self._cfg(s.dtype, dy.dtype, weight.dtype)
+        size = self._sizes.get(T)
+        if size is None:
+            size = self._sizes[T] = moe_norm_backward_size(cfg, T)
+        with _allocate_on(stream):
+            dx = torch.empty(s.shape, dtype=s.dtype, device=s.device)
+            if dweight is None:
+                dweight = torch.empty(self.hidden, dtype=torch.float32, device=s.device)
+            if bias and dbias is None:
+                dbias = torch.empty(self.hidden, dtype=dweight.dtype, device=s.device)
+            workspace = torch.empty(size, dtype=torch.uint8, device=s.device)
+        for g in (dweight, dbias):
+            _require(g is None or (g.shape == (self.hidden,) and g.is_contiguous() and g.dtype == dweight.dtype and
+                                   g.dtype in self._types), "dweight and dbias must be [hidden], both fp32 or both bf16")
+        moe_norm_backward(cfg, dy, s, weight, mean, rstd, dx, dsum, dweight, dbias,
+                          MOE_G_BF16 if dweight.dtype == torch.bfloat16 else MOE_G_FP32, accumulate, workspace, stream)
+        return dx, dweight, dbias
+
+
+class MoERouter:
+    """The choice of experts from the router's logits (include/moe.h, moe_router_forward)."""
+
+    def __init__(self, num_experts, topk, score=MOE_SCORE_SOFTMAX, normalise=True, scale=1.0, aux_coeff=0.0,
+                 z_coeff=0.0, device="cuda"):
+        import torch
+        self.E, self.k = int(num_experts), int(topk)
+        self.device = torch.device(device)
+        self._torch = torch
+        args = (self.E, self.k, int(score), int(bool(normalise)), float(scale), float(aux_coeff), float(z_coeff))
+        self._cfgs = {torch.bfloat16: moe_router_config(*args, MOE_T_BF16),
+                      torch.float32: moe_router_config(*args, MOE_T_FP32)}
+        self.losses_wanted = aux_coeff != 0 or z_coeff != 0
+        self._sizes = {}
+        moe_router_size(self._cfgs[torch.float32], 0)      # the library's check of the configuration
+
+    def _logits(self, logits):
+        _require(logits.dim() == 2 and logits.shape[1] == self.E and logits.dtype in self._cfgs and
+                 logits.stride(1) == 1, "logits must be [T, E] rows, bf16 or fp32")
+        return self._cfgs[logits.dtype]
+
+    def forward(self, logits, select_bias=None, stream=None):
+        """(ids [T,k] int32, probs [T,k] fp32, counts [E] int32, losses [2] fp32 or None): the input of
+        forward_topk, the routes per expert, and the balance and z losses where a coefficient asks for them."""
+        torch = self._torch
+        cfg = self._logits(logits)
+        _require(select_bias is None or (select_bias.shape == (self.E,) and select_bias.dtype == torch.float32 and
+                                         select_bias.is_contiguous()), "select_bias must be [E] fp32")
+        T, dev = logits.shape[0], logits.device
+        size = self._sizes.get(T)
+        if size is None:
+            size = self._sizes[T] = moe_router_size(cfg, T)
+        with _allocate_on(stream):
+            ids = torch.empty((T, self.k), dtype=torch.int32, device=dev)
+            probs = torch.empty((T, self.k), dtype=torch.float32, device=dev)
+            counts = torch.empty(self.E, dtype=torch.int32, device=dev)
+            losses = torch.empty(2, dtype=torch.float32, device=dev) if self.losses_wanted else None
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        moe_router_forward(cfg, logits, ids, probs, counts, losses, select_bias, workspace, stream)
+        return ids, probs, counts, losses
+
+    def backward(self, logits, ids, dprobs, counts=None, loss_grad=1.0, stream=None):
+        """dlogits of sum(dprobs * probs) + loss_grad * (balance + z); counts: the forward's (needed
+        with a balance loss)."""
+        torch = self._torch
+        cfg = self._logits(logits)
+        T = logits.shape[0]
+        for t, dt in ((ids, torch.int32), (dprobs, torch.float32)):
+            _require(t.shape == (T, self.k) and t.dtype == dt and t.is_contiguous(),
+                     "ids and dprobs must be contiguous [T, k] int32 and fp32")
+        _require(counts is None or (counts.shape == (self.E,) and counts.dtype == torch.int32 and
+                                    counts.is_contiguous()), "counts must be [E] int32")
+        with _allocate_on(stream):
+            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        moe_router_backward(cfg, logits, ids, dprobs, dlogits, counts, float(loss_grad), stream)
+        return dlogits
