@@ -391,7 +391,7 @@ typedef struct moe_decoder moe_decoder;
 /* Bytes of device workspace a decoder for `cfg` needs. The fields of moe_config
  * mean what they mean for a handle, except: max_tokens is at most
  * MOE_DECODE_MAX_TOKENS; hidden and inter need only be multiples of 8 (MXFP8
- * routed weights: of 32); recompute_dispatch must be 0; act_precision is not
+ * routed weights: of 32), up to 32768; recompute_dispatch must be 0; act_precision is not
  * looked at (the activations between the products are kept in fp32, and reach
  * the second product as two bf16 terms, as with MOE_ACT_FP32; MXFP8 weights are
  * multiplied by unquantised activations). */

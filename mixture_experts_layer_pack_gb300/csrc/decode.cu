@@ -1,8 +1,38 @@
-// The layer for a few tokens: out = gate * SharedSwiGLU(x) + sum_s p_s RoutedSwiGLU_s(x).
+// The layer for a few tokens in one launch:
+//   out[t] = gate[t] SharedSwiGLU(x_t) + sum_s p[t,s] RoutedSwiGLU_{id[t,s]}(x_t).
+//
+// What bounds it is the reading of the chosen experts' weights, once: 3 H I values
+// per expert for 6 H I operations per token that chose it. So the kernel is one
+// stream of weights: a persistent cooperative launch of one block per SM, in which
+// eight producer warps keep a ring of bulk copies (cp.async.bulk into shared memory,
+// one mbarrier per slot) full from their first instruction to their last, and eight
+// consumer warps each multiply the slots of their own row tile.
+//
+//  * A group is up to 8 NT tokens of one expert (the shared expert is one more
+//    expert, with every token). Every block sorts the routes into groups for itself.
+//  * A slot is 16 weight rows by KC columns, the weights as the 16-row operand of
+//    mma.m16n8k16, and one warp's. Up to eight tiles of one group form a set; the warps
+//    of a set share the columns' slice of the group's tokens, in a ring of its own.
+//  * First product: a tile holds 8 gate rows and the 8 up rows of the same i, which
+//    leaves g and u of a token in one thread: a = silu(g) u needs no exchange.
+//    Second product: a warp keeps its 16 rows of H for a set of tiles and adds up
+//    p y over the groups in shared memory. No warp waits for another's sums.
+//  * Each block takes an equal, contiguous share of the first product's tiles, and of the
+//    second product's slots. Row tiles that blocks share are summed by the block that
+//    finishes last, from partial sums in global memory, in block order.
+//  * Between the products the blocks wait for one another. The weights' producers do not:
+//    they fill the ring with the second product's weights meanwhile.
+//
+// A thread loads 8 consecutive elements of a weight row and the same 8 of a token's
+// row, which are the operands of two instructions if the sum's index is taken in that
+// order. Tensor rate is not what limits it (8 tokens a weight at most, most often one).
+// The activations a = silu(g) u go to the second product as two bf16 terms, hi + lo.
+// MXFP8 weights become bf16 in registers (exact) and their block scales multiply
+// the fp32 sums of 32 columns.
 #include <algorithm>
 #include <cmath>
+#include <memory>
 #include <new>
-#include <vector>
 
 #include "../../include/moe.h"
 #include "device_common.cuh"
@@ -13,6 +43,12 @@ namespace moe {
 namespace {
 
 constexpr size_t kDecodeAlign = 256;
+constexpr int kConsumers = 8;        // consumer warps: tiles of a set
+constexpr int kProducers = 8;        // producer warps
+constexpr int kDecodeThreads = 32 * (kConsumers + kProducers);
+constexpr int kSlots = 24;           // most slots of the weights' ring
+constexpr int kTokenSlots = 8;       // most slots of the tokens' ring
+constexpr int kSmemMax = 232448;     // shared memory a block can have (227 KB)
 
 // one weight matrix of every expert: expert e at base + e * expert_bytes, or at table[e]
 struct DecodeWeight {
@@ -34,7 +70,7 @@ enum : int { W_SHARED_GATE = 0, W_SHARED_UP, W_SHARED_DOWN, W_GATE, W_UP, W_DOWN
 
 struct DecodeArgs {
     int T, H, I, E, k;
-    bool mx, shared;
+    bool shared;
     float limit;
     const __nv_bfloat16* x;
     int64_t xs;
@@ -44,98 +80,822 @@ struct DecodeArgs {
     __nv_bfloat16* out;
     int64_t os;
     DecodeWeight w[W_COUNT];
-    float* a;  // [T][k + 1][I]: the activations of each slot, the shared expert's last
+    __nv_bfloat16* acts;      // by position (below): [chunks of I][2][chunk]: the activations' two terms
+    int act_row;              // elements of a position
+    float* gate;              // [T]
+    float* part;              // [blocks][2][8][T][16]: partial sums of shared sets of row tiles
+    unsigned* counters;       // per row tile: blocks done with it; 0 between launches
+    unsigned* barrier;        // top bit flips when every block has arrived
     int* status;
+    // shared memory plan
+    int max_groups;
+    int slots, token_slots, token_slot_bytes;
+    int tokens_off, ring_off;
 };
 
-// whether the k ids of a token are in [-1, E) and distinct
-__device__ __forceinline__ bool row_valid(const int* ids, int k, int E) {
-    for (int i = 0; i < k; ++i) {
-        if (ids[i] < -1 || ids[i] >= E) return false;
-        for (int j = 0; j < i; ++j)
-            if (ids[i] >= 0 && ids[i] == ids[j]) return false;
-    }
-    return true;
+// A build of the kernel: up to 8 NT tokens a group, slots of KC columns (with MXFP8 routed
+// weights: of E4M3 weights; the shared expert's bf16 rows take half the columns in the
+// same bytes). Row pitches are chosen so that the rows that one shared-memory pass of
+// a warp touches (two of 64 bytes, or four of 32) lie in different banks.
+template <int NT_, int KC_, bool MX_>
+struct Build {
+    static constexpr int NT = NT_, KC = KC_;
+    static constexpr bool MX = MX_;
+    static constexpr int CAP = 8 * NT;          // tokens of a group
+    static constexpr int KB = MX ? KC / 2 : KC; // columns of a slot of bf16 weights
+    static constexpr int P16 = 2 * KB + 64;     // pitch of a weight row of bf16
+    static constexpr int P8 = KC + 32;          // pitch of a weight row of E4M3
+    static constexpr int PS = KC / 32 + 4;      // pitch of a row's scale codes
+    static constexpr int SCALES = 16 * P8;      // offset of the scale codes in a slot
+    static constexpr int SLOT = MX ? (16 * (P8 + PS) > 16 * P16 ? 16 * (P8 + PS) : 16 * P16) : 16 * P16;
+    static_assert(SLOT % 64 == 0 && PS % 4 == 0, "slots start on 16 bytes");
+    static __device__ __forceinline__ int columns(bool mx) { return MX && mx ? KC : KB; }
+    // pitch of a token row of `terms` terms of kc columns
+    static __host__ __device__ constexpr int token_pitch(int kc, int terms) { return 2 * kc * terms + 64; }
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
 }
 
-// dot product of row n of an expert's matrix with v (fp32 or bf16), by one warp
-template <typename V>
-__device__ float warp_dot(const uint8_t* w, const uint8_t* sc, int64_t row_bytes, bool mx, int64_t n, const V* v,
-                          int K) {
-    float acc = 0.0f;
-    for (int i = threadIdx.x & 31; i < K; i += 32) {
-        float x;
-        if constexpr (sizeof(V) == 2)
-            x = __bfloat162float(v[i]);
-        else
-            x = v[i];
-        float wv;
-        if (mx)
-            wv = e4m3_value(w[n * row_bytes + i]) * e8m0_scale(sc[n * (row_bytes / 32) + i / 32]);
-        else
-            wv = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w + n * row_bytes)[i]);
-        acc = fmaf(wv, x, acc);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    return acc;
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// one warp per (token, slot, i)
-__global__ void __launch_bounds__(256) decode_up_kernel(DecodeArgs a) {
-    const int64_t n = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const int slots = a.k + 1;
-    if (n >= int64_t(a.T) * slots * a.I) return;
-    const int i = int(n % a.I);
-    const int s = int(n / a.I % slots);
-    const int t = int(n / a.I / slots);
-    const bool routed = s < a.k;
-    if (routed && !row_valid(a.ids + int64_t(t) * a.k, a.k, a.E)) {
-        if ((threadIdx.x & 31) == 0) atomicOr(a.status, kStatusRouting);
-        return;
-    }
-    const int e = routed ? a.ids[int64_t(t) * a.k + s] : 0;
-    if (e < 0 || (!routed && !a.shared)) return;
-    const DecodeWeight& wg = a.w[routed ? W_GATE : W_SHARED_GATE];
-    const DecodeWeight& wu = a.w[routed ? W_UP : W_SHARED_UP];
-    const bool mx = routed && a.mx;
-    const __nv_bfloat16* x = a.x + t * a.xs;
-    float g = warp_dot(wg.expert(e), mx ? wg.scales(e) : nullptr, wg.row_bytes, mx, i, x, a.H);
-    float u = warp_dot(wu.expert(e), mx ? wu.scales(e) : nullptr, wu.row_bytes, mx, i, x, a.H);
-    if (a.limit > 0.0f) {
-        g = fminf(g, a.limit);
-        u = fminf(fmaxf(u, -a.limit), a.limit);
-    }
-    if ((threadIdx.x & 31) == 0) a.a[(int64_t(t) * slots + s) * a.I + i] = g * sigmoidf_(g) * u;
+// 2^(code - 127) of an E8M0 code; 255 is NaN
+__device__ __forceinline__ float e8m0_value(uint32_t code) {
+    return code == 255u ? __uint_as_float(0x7fffffffu) : e8m0_scale(code);
 }
 
-// one warp per (token, h)
-__global__ void __launch_bounds__(256) decode_down_kernel(DecodeArgs a) {
-    const int64_t n = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    if (n >= int64_t(a.T) * a.H) return;
-    const int h = int(n % a.H);
-    const int t = int(n / a.H);
-    const int slots = a.k + 1;
-    const float* act = a.a + int64_t(t) * slots * a.I;
-    float out = 0.0f;
-    if (a.shared) {
-        const DecodeWeight& w = a.w[W_SHARED_DOWN];
-        out = warp_dot(w.base, nullptr, w.row_bytes, false, h, act + int64_t(a.k) * a.I, a.I);
-        if (a.gate_w)
-            out *= sigmoidf_(warp_dot(reinterpret_cast<const uint8_t*>(a.gate_w), nullptr, 0, false, 0, a.x + t * a.xs,
-                                      a.H));
-    }
-    if (row_valid(a.ids + int64_t(t) * a.k, a.k, a.E)) {
-        const DecodeWeight& w = a.w[W_DOWN];
-        for (int s = 0; s < a.k; ++s) {
-            const int e = a.ids[int64_t(t) * a.k + s];
-            if (e < 0) continue;
-            const float y = warp_dot(w.expert(e), a.mx ? w.scales(e) : nullptr, w.row_bytes, a.mx, h,
-                                     act + int64_t(s) * a.I, a.I);
-            out = fmaf(a.probs[int64_t(t) * a.k + s], y, out);
+// Four E4M3 codes -> two bf16 pairs, exact (4 significant bits), without the conversion
+// unit, which takes 16 values a cycle: a code's 7 magnitude bits under bf16's exponent are its
+// value times 2^-120 (subnormals included), so sign-extend each byte, shift it to its
+// place, keep sign and magnitude, multiply by 2^120. The NaN codes (0x7F, 0xFF) come out as
+// +-480, which no other code does: `top` keeps the largest magnitude seen.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t q, uint32_t select, __nv_bfloat162& top) {
+    uint32_t x;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(x) : "r"(q), "r"(select));
+    x = (x << 4) & 0x87f087f0u;
+    const __nv_bfloat162 scale = __halves2bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x), scale);
+    top = __hmax2(top, __habs2(v));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t q, uint32_t& lo, uint32_t& hi, __nv_bfloat162& top) {
+    lo = e4m3_pair(q, 0x9180u, top);
+    hi = e4m3_pair(q, 0xB3A2u, top);
+}
+// the sums of a weight row (spread over four lanes) with a NaN code in it are NaN for every token
+__device__ __forceinline__ bool row_has_nan(__nv_bfloat162 top) {
+    const bool bad = __low2float(top) > 448.0f || __high2float(top) > 448.0f;
+    const unsigned m = __ballot_sync(0xffffffffu, bad);
+    return (m >> (threadIdx.x & 28)) & 15u;
+}
+
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory"); }
+
+__device__ __forceinline__ unsigned load_acquire(const unsigned* p) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// waits until the grid barrier's top bit differs from `before`; bounded: past the limit it
+// records the timeout and goes on (every address that follows is valid either way)
+__device__ __forceinline__ void grid_wait(const unsigned* bar, unsigned before, int* status) {
+    const uint64_t t0 = globaltimer_ns();
+    while (((load_acquire(bar) ^ before) & 0x80000000u) == 0) {
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(status, kStatusTimeout);
+            return;
         }
     }
-    if ((threadIdx.x & 31) == 0) a.out[t * a.os + h] = __float2bfloat16_rn(out);
+}
+
+// An equal share: the first n mod blocks blocks have one item more than the others. Where
+// block c's items of n begin, and the block that owns item u.
+__device__ __forceinline__ int share(int n, int c, int blocks) {
+    const int each = n / blocks;
+    return each * c + min(c, n - each * blocks);
+}
+__device__ __forceinline__ int owner(int n, int u, int blocks) {
+    const int each = n / blocks, more = n - each * blocks, wide = more * (each + 1);
+    return u < wide ? u / (each + 1) : more + (u - wide) / each;
+}
+
+
+// The routes sorted by expert. Position p < T: token p of the shared expert (if any);
+// the routed positions follow, by (expert, token). Group g: `count` positions from `start`.
+struct Group {
+    int expert;  // E: the shared expert
+    int start;
+    int count;
+};
+
+struct Tables {
+    Group* groups;
+    int* tok;       // token of a position
+    float* coef;    // its weight in the sum: prob, or the output gate
+    int n_shared;   // groups of the shared expert, which come first
+    int n_groups;
+};
+
+// Sorts the routes, by the whole block. A token chooses an expert once, so an expert's
+// tokens are a 64-bit mask, whatever order its bits are set in; counts and ranks are
+// population counts. A row with a bad id keeps none of its routes.
+// scratch: E masks, E starts, T k ids, 40 ints; id, prob: of route tid, already under way.
+template <int CAP>
+__device__ __forceinline__ void sort_routes(const DecodeArgs& a, Tables& tb, uint8_t* scratch, int id, float prob) {
+    const int R = a.T * a.k, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kWarps = kDecodeThreads / 32;
+    auto* s_mask = reinterpret_cast<unsigned long long*>(scratch);
+    auto* s_bad = s_mask + a.E;
+    int* s_start = reinterpret_cast<int*>(s_bad + 1);
+    int* s_id = s_start + a.E;
+    int* s_warp = s_id + R;
+    for (int i = tid; i <= a.E; i += kDecodeThreads) s_mask[i] = 0;
+    for (int r = tid; r < R; r += kDecodeThreads) s_id[r] = r == tid ? id : a.ids[r];
+    __syncthreads();
+    for (int r = tid; r < R; r += kDecodeThreads) {
+        const int t = r / a.k, v = s_id[r];
+        bool ok = v >= -1 && v < a.E;
+        for (int i = t * a.k; i < r; ++i) ok &= v < 0 || s_id[i] != v;
+        if (!ok) {
+            atomicOr(s_bad, 1ull << t);
+            if (blockIdx.x == 0) atomicOr(a.status, kStatusRouting);
+        }
+    }
+    __syncthreads();
+    const unsigned long long bad = *s_bad;
+    for (int r = tid; r < R; r += kDecodeThreads) {
+        const int t = r / a.k, v = s_id[r];
+        if (v >= 0 && !((bad >> t) & 1)) atomicOr(s_mask + v, 1ull << t);
+    }
+    __syncthreads();
+    // exclusive sums over the experts of (routes << 16 | groups); a thread has two experts
+    int cnt[2], mine = 0;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int e = 2 * tid + q;
+        cnt[q] = e < a.E ? __popcll(s_mask[e]) : 0;
+        mine += cnt[q] << 16 | (cnt[q] + CAP - 1) / CAP;
+    }
+    static_assert(2 * kDecodeThreads >= 1024, "two experts a thread");
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    int before = sum - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const int x = s_warp[w];
+        if (w < warp) before += x;
+        total += x;
+    }
+    tb.n_shared = a.shared ? (a.T + CAP - 1) / CAP : 0;
+    tb.n_groups = tb.n_shared + (total & 0xffff);
+    const int base = a.shared ? a.T : 0;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int e = 2 * tid + q, start = base + (before >> 16), g = tb.n_shared + (before & 0xffff);
+        if (e < a.E) s_start[e] = start;
+        const int ng = (cnt[q] + CAP - 1) / CAP;
+        for (int i = 0; i < ng; ++i) tb.groups[g + i] = Group{e, start + i * CAP, min(CAP, cnt[q] - i * CAP)};
+        before += cnt[q] << 16 | ng;
+    }
+    if (tid < tb.n_shared) tb.groups[tid] = Group{a.E, tid * CAP, min(CAP, a.T - tid * CAP)};
+    __syncthreads();
+    for (int r = tid; r < R; r += kDecodeThreads) {
+        const int t = r / a.k, v = s_id[r];
+        if (v < 0 || ((bad >> t) & 1)) continue;
+        const int pos = s_start[v] + __popcll(s_mask[v] & ((1ull << t) - 1));
+        tb.tok[pos] = t;
+        tb.coef[pos] = r == tid ? prob : a.probs[r];
+    }
+    if (a.shared && tid < a.T) {
+        tb.tok[tid] = tid;
+        tb.coef[tid] = 1.0f;
+    }
+}
+
+// A block's share. First product: tiles u = group * it + tile of I, from u_begin to u_end.
+// Second product: slots of (set of 8 tiles of H, group, chunk, tile), the tile fastest.
+struct Plan {
+    int n_shared;
+    int c1_shared, c1, c2_shared, c2;  // chunks of H and of I: of the shared expert's groups, of routed ones
+    int it, ht;                // tiles of I and H
+    int u_begin, u_end;
+    int q_shared, q;           // chunks of I over the shared groups, over all groups
+    int n2, blocks2;           // slots of the second product, and the blocks that have any
+    int s_begin, s_end;
+};
+
+template <class B>
+__device__ __forceinline__ Plan make_plan(const DecodeArgs& a, const Tables& tb) {
+    Plan p;
+    const int c = blockIdx.x, n = gridDim.x, routed = tb.n_groups - tb.n_shared;
+    p.n_shared = tb.n_shared;
+    auto chunks = [](int n, bool mx) { return (n + B::columns(mx) - 1) / B::columns(mx); };
+    p.c1_shared = chunks(a.H, false);
+    p.c2_shared = chunks(a.I, false);
+    p.c1 = chunks(a.H, true);
+    p.c2 = chunks(a.I, true);
+    p.it = (a.I + 7) / 8;
+    p.ht = (a.H + 15) / 16;
+    // equal shares of slots, rounded up to tiles
+    const int slots_shared = p.it * tb.n_shared * p.c1_shared, slots = slots_shared + p.it * routed * p.c1;
+    auto tile = [&](int s) {
+        return s <= slots_shared ? (s + p.c1_shared - 1) / p.c1_shared
+                                 : p.it * tb.n_shared + (s - slots_shared + p.c1 - 1) / p.c1;
+    };
+    p.u_begin = tile(share(slots, c, n));
+    p.u_end = tile(share(slots, c + 1, n));
+    p.q_shared = tb.n_shared * p.c2_shared;
+    p.q = p.q_shared + routed * p.c2;
+    p.n2 = p.q * p.ht;
+    p.blocks2 = min(p.n2, n);
+    p.s_begin = c < p.blocks2 ? share(p.n2, c, p.blocks2) : p.n2;
+    p.s_end = c < p.blocks2 ? share(p.n2, c + 1, p.blocks2) : p.n2;
+    return p;
+}
+
+// The first product's walk: sets of up to eight tiles of one group.
+struct Tiles {
+    int u, g, tile, size;
+    __device__ __forceinline__ Tiles(const Plan& p) : u(p.u_begin), g(p.u_begin / p.it), tile(p.u_begin % p.it) { fit(p); }
+    __device__ __forceinline__ void fit(const Plan& p) { size = min(kConsumers, min(p.u_end - u, p.it - tile)); }
+    __device__ __forceinline__ bool more(const Plan& p) const { return u < p.u_end; }
+    __device__ __forceinline__ void next(const Plan& p) {
+        u += size;
+        if ((tile += size) == p.it) {
+            tile = 0;
+            ++g;
+        }
+        fit(p);
+    }
+};
+
+// The second product's walk: steps of (set, group, chunk), tiles [lo, hi) of the set.
+struct Steps {
+    int set, g, c, lo, hi, s;
+    __device__ __forceinline__ static int width(const Plan& p, int set) { return min(kConsumers, p.ht - set * kConsumers); }
+    __device__ __forceinline__ Steps(const Plan& p) : s(p.s_begin) {
+        const int per = kConsumers * p.q;
+        set = s / per;
+        const int r = s - set * per, wd = width(p, set), q = r / max(wd, 1);
+        lo = r - q * wd;
+        const bool routed = q >= p.q_shared;
+        const int in = routed ? q - p.q_shared : q, n = routed ? p.c2 : p.c2_shared;
+        g = in / n;
+        c = in - g * n;
+        if (routed) g += p.n_shared;
+        fit(p);
+    }
+    __device__ __forceinline__ void fit(const Plan& p) { hi = min(width(p, set), lo + p.s_end - s); }
+    __device__ __forceinline__ bool more(const Plan& p) const { return s < p.s_end; }
+    __device__ __forceinline__ void next(const Plan& p, int n_groups) {
+        s += hi - lo;
+        lo = 0;
+        if (++c == (g >= p.n_shared ? p.c2 : p.c2_shared)) {
+            c = 0;
+            if (++g == n_groups) {
+                g = 0;
+                ++set;
+            }
+        }
+        fit(p);
+    }
+};
+
+// One k-step: the 16 x 32 weights (wa: row r, wb: row r + 8, 8 elements each) times up to
+// 8 N tokens, whose elements start at px[t] (`there`: this thread's token exists). Two sets of
+// sums keep two chains of instructions going: of the two halves of the step, or with TERMS 2
+// of the two terms of a token's row, which lie `gap` bytes apart.
+template <int N, int TERMS>
+__device__ __forceinline__ void k_step(float (*acc0)[4], float (*acc1)[4], const uint4& wa, const uint4& wb,
+                                       const uint8_t* const (&px)[N], const bool (&there)[N], int k2, int gap) {
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term) {
+            uint4 x = *reinterpret_cast<const uint4*>(px[t] + k2 + term * gap);
+            if (!there[t]) x = make_uint4(0, 0, 0, 0);
+            float(&d0)[4] = term == 0 ? acc0[t] : acc1[t];
+            float(&d1)[4] = term == 0 && TERMS == 2 ? acc0[t] : acc1[t];
+            mma_16816(d0, wa.x, wb.x, wa.y, wb.y, x.x, x.y);
+            mma_16816(d1, wa.z, wb.z, wa.w, wb.w, x.z, x.w);
+        }
+}
+
+// acc += (16 weight rows at A) x (N tiles of 8 tokens at X), over n columns of a slot
+template <class B, int N, int TERMS>
+__device__ __forceinline__ void multiply_tiles(float (&acc)[2][B::NT][4], __nv_bfloat162 (&top)[2], const uint8_t* A,
+                                               const uint8_t* X, int pitch, int count, int n, bool mx, int lane) {
+    const int r = lane >> 2, c8 = (lane & 3) * 8;
+    const uint8_t* px[N];
+    bool there[N];
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        there[t] = 8 * t + r < count;
+        px[t] = X + (there[t] ? 8 * t + r : 0) * pitch + 2 * c8;
+    }
+    if (B::MX && mx) {
+        const uint8_t *pa = A + r * B::P8 + c8, *S = A + B::SCALES + r * B::PS;
+#pragma unroll 2
+        for (int k = 0; k < n; k += 32) {  // n is a multiple of 32
+            const uint2 qa = *reinterpret_cast<const uint2*>(pa + k);
+            const uint2 qb = *reinterpret_cast<const uint2*>(pa + 8 * B::P8 + k);
+            const float sa = e8m0_value(S[k >> 5]), sb = e8m0_value(S[8 * B::PS + (k >> 5)]);
+            uint4 wa, wb;
+            e4m3_to_bf16(qa.x, wa.x, wa.y, top[0]);
+            e4m3_to_bf16(qa.y, wa.z, wa.w, top[0]);
+            e4m3_to_bf16(qb.x, wb.x, wb.y, top[1]);
+            e4m3_to_bf16(qb.y, wb.z, wb.w, top[1]);
+            float d[2][N][4] = {};
+            k_step<N, TERMS>(d[0], d[1], wa, wb, px, there, 2 * k, 2 * B::KC);
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+                acc[0][t][0] = fmaf(sa, d[0][t][0] + d[1][t][0], acc[0][t][0]);
+                acc[0][t][1] = fmaf(sa, d[0][t][1] + d[1][t][1], acc[0][t][1]);
+                acc[0][t][2] = fmaf(sb, d[0][t][2] + d[1][t][2], acc[0][t][2]);
+                acc[0][t][3] = fmaf(sb, d[0][t][3] + d[1][t][3], acc[0][t][3]);
+            }
+        }
+        return;
+    }
+    const uint8_t* pa = A + r * B::P16 + 2 * c8;
+    const int whole = n & ~31;
+#pragma unroll 4
+    for (int k = 0; k < whole; k += 32)
+        k_step<N, TERMS>(acc[0], acc[1], *reinterpret_cast<const uint4*>(pa + 2 * k),
+                         *reinterpret_cast<const uint4*>(pa + 8 * B::P16 + 2 * k), px, there, 2 * k, 2 * B::KB);
+    if (whole < n) {  // some threads' columns lie past the end: zeros on both sides
+        const bool in = whole + c8 < n;
+        const int k2 = in ? 2 * whole : 0;
+        uint4 wa = *reinterpret_cast<const uint4*>(pa + k2), wb = *reinterpret_cast<const uint4*>(pa + 8 * B::P16 + k2);
+        if (!in) wa = wb = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < N; ++t) there[t] &= in;
+        k_step<N, TERMS>(acc[0], acc[1], wa, wb, px, there, k2, 2 * B::KB);
+    }
+}
+
+template <class B, int TERMS>
+__device__ __forceinline__ void multiply(float (&acc)[2][B::NT][4], __nv_bfloat162 (&top)[2], const uint8_t* A,
+                                         const uint8_t* X, int pitch, int count, int n, bool mx, int lane) {
+    if (B::NT == 1 || count <= 8)
+        multiply_tiles<B, 1, TERMS>(acc, top, A, X, pitch, count, n, mx, lane);
+    else
+        multiply_tiles<B, B::NT, TERMS>(acc, top, A, X, pitch, count, n, mx, lane);
+}
+
+// the two sets of sums as one (in acc[0]); a weight row with a NaN code is NaN for every token
+template <class B>
+__device__ __forceinline__ void join(float (&acc)[2][B::NT][4], const __nv_bfloat162 (&top)[2]) {
+    bool bad[2] = {false, false};
+    if (B::MX) {
+        bad[0] = row_has_nan(top[0]);
+        bad[1] = row_has_nan(top[1]);
+    }
+#pragma unroll
+    for (int t = 0; t < B::NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[0][t][i] = bad[i >> 1] ? __uint_as_float(0x7fffffffu) : acc[0][t][i] + acc[1][t][i];
+}
+
+// The rings' barriers, and the round (use) that each slot was last filled for. A barrier's
+// parity tells a round from its neighbours only, and a warp does not take every use of a
+// slot: so a warp looks for the round first, and then waits for the round's phase.
+struct Bars {
+    uint64_t full[kSlots], empty[kSlots], tfull[kTokenSlots], tempty[kTokenSlots];
+    int filled[kSlots], tfilled[kTokenSlots];
+};
+
+__device__ __forceinline__ int round_of(const int* p) {
+    int v;
+    asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void set_round(int* p, int v) {
+    asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
+}
+// waits for phase `round` of bar, whose slot was or will be filled for that round (bounded like mbar_wait)
+__device__ __forceinline__ void wait_round(const int* filled, uint64_t* bar, int round, volatile int* abort, int* status) {
+    if (round_of(filled) != round) {
+        const uint64_t t0 = globaltimer_ns();
+        while (round_of(filled) != round) {
+            if (*abort) return;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                *abort = 1;
+                atomicOr(status, kStatusTimeout);
+                return;
+            }
+        }
+    }
+    mbar_wait(bar, uint32_t(round) & 1, abort, status);
+}
+
+// the word of scale codes at c (any alignment), of which those below `end` are wanted
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* c, const uint8_t* end) {
+    const unsigned shift = unsigned(reinterpret_cast<uintptr_t>(c) & 3);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(c - shift);
+    const uint32_t lo = __ldg(w);
+    const uint32_t hi = shift && reinterpret_cast<const uint8_t*>(w + 1) < end ? __ldg(w + 1) : 0u;
+    return __funnelshift_r(lo, hi, 8 * shift);
+}
+
+// One producer warp. Items (a set's token slice, then its weight slots) go round the warps:
+// one warp issues a copy in about a hundred cycles, so it takes several to keep the memory
+// busy (152 blocks of 1, 2, 4, 8 warps with 1 KB copies and 192 KB in flight: 1.7, 3.3,
+// 6.6, 6.8 TB/s).
+template <class B>
+struct Producer {
+    const DecodeArgs& a;
+    const Tables& tb;
+    const Plan& p;
+    uint8_t *ring, *tokens;
+    Bars* bars;
+    volatile int* abort;
+    int pw, lane;
+    int turn = 0, slot = 0, round = 0, tslot = 0, tround = 0;
+    bool met = false;
+
+    __device__ __forceinline__ bool mine() {
+        const bool m = turn == pw;
+        turn = turn + 1 == kProducers ? 0 : turn + 1;
+        return m;
+    }
+    __device__ __forceinline__ void next_slot() {
+        if (++slot == a.slots) {
+            slot = 0;
+            ++round;
+        }
+    }
+    __device__ __forceinline__ void next_token_slot() {
+        if (++tslot == a.token_slots) {
+            tslot = 0;
+            ++tround;
+        }
+    }
+    // 16 rows (live: this lane has one, at src) of n columns into the next slot
+    template <typename F>
+    __device__ __forceinline__ void weights(bool mx, bool live, int rows, const uint8_t* src, int n, F codes) {
+        if (round) wait_round(bars->filled + slot, bars->empty + slot, round - 1, abort, a.status);
+        if (*abort) return;  // a wait gave up: nothing more is asked for
+        __syncwarp();
+        if (lane == 0) set_round(bars->filled + slot, round);
+        uint8_t* A = ring + slot * B::SLOT;
+        uint64_t* bar = bars->full + slot;
+        const int bytes = B::MX && mx ? n : 2 * n;
+        constexpr int W = (16 * B::KC / 128 + 31) / 32;  // words of scale codes of a lane
+        uint32_t code[W];
+        if (B::MX && mx) {
+#pragma unroll
+            for (int q = 0; q < W; ++q) {
+                const int i = q * 32 + lane, r = i / (B::KC / 128), wd = i % (B::KC / 128);
+                const uint8_t* c = codes(r);
+                code[q] = c != nullptr && 4 * wd < n / 32 ? load_codes(c + 4 * wd, c + n / 32) : 0u;
+            }
+        }
+        if (B::MX) fence_proxy_async_smem();  // copies may land where codes were written
+        if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(rows * bytes));
+        __syncwarp();
+        if (live) bulk_load(A + lane * (B::MX && mx ? B::P8 : B::P16), src, bytes, bar);
+        if (B::MX) {
+            if (mx) {
+#pragma unroll
+                for (int q = 0; q < W; ++q) {
+                    const int i = q * 32 + lane, r = i / (B::KC / 128), wd = i % (B::KC / 128);
+                    *reinterpret_cast<uint32_t*>(A + B::SCALES + r * B::PS + 4 * wd) = code[q];
+                }
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(bar);  // the codes are there
+        }
+    }
+    // this lane's token row (if it has one) into the next token slot
+    __device__ __forceinline__ void token_rows(int count, const __nv_bfloat16* src, int pitch, int bytes) {
+        if (tround) wait_round(bars->tfilled + tslot, bars->tempty + tslot, tround - 1, abort, a.status);
+        if (*abort) return;
+        __syncwarp();
+        if (lane == 0) set_round(bars->tfilled + tslot, tround);
+        uint64_t* bar = bars->tfull + tslot;
+        if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(count * bytes));
+        __syncwarp();
+        if (lane < count) bulk_load(tokens + tslot * a.token_slot_bytes + lane * pitch, src, bytes, bar);
+    }
+
+    __device__ __forceinline__ void run(unsigned before) {
+        static_assert(B::CAP <= 32, "a lane copies a row");
+        for (Tiles w(p); w.more(p); w.next(p)) {
+            const Group gr = tb.groups[w.g];
+            const bool routed = gr.expert < a.E, mx = B::MX && routed;
+            const DecodeWeight& wg = a.w[routed ? W_GATE : W_SHARED_GATE];
+            const DecodeWeight& wu = a.w[routed ? W_UP : W_SHARED_UP];
+            const int e = routed ? gr.expert : 0, es = mx ? 1 : 2, kc = B::columns(mx);
+            const uint8_t *bg = wg.expert(e), *bu = wu.expert(e);
+            const __nv_bfloat16* x = a.x + (lane < gr.count ? tb.tok[gr.start + lane] : 0) * a.xs;
+            for (int k0 = 0; k0 < a.H; k0 += kc) {
+                const int n = min(kc, a.H - k0);
+                if (mine()) token_rows(gr.count, x + k0, B::token_pitch(kc, 1), 2 * n);
+                next_token_slot();
+                for (int q = 0; q < w.size; ++q, next_slot()) {
+                    if (!mine()) continue;
+                    const int i0 = (w.tile + q) * 8, rows = min(8, a.I - i0), i = i0 + (lane & 7);
+                    const uint8_t* src = ((lane & 8) ? bu + i * wu.row_bytes : bg + i * wg.row_bytes) + int64_t(k0) * es;
+                    weights(mx, lane < 16 && (lane & 7) < rows, 2 * rows, src, n, [&](int r) -> const uint8_t* {
+                        if ((r & 7) >= rows) return nullptr;
+                        const int64_t ir = i0 + (r & 7);
+                        return ((r & 8) ? wu.scales(e) + ir * (wu.row_bytes / 32) : wg.scales(e) + ir * (wg.row_bytes / 32)) + k0 / 32;
+                    });
+                }
+            }
+        }
+        for (Steps w(p); w.more(p); w.next(p, tb.n_groups)) {
+            const Group gr = tb.groups[w.g];
+            const bool routed = gr.expert < a.E, mx = B::MX && routed;
+            const DecodeWeight& wd = a.w[routed ? W_DOWN : W_SHARED_DOWN];
+            const int e = routed ? gr.expert : 0, es = mx ? 1 : 2, kc = B::columns(mx);
+            const int k0 = w.c * kc, n = min(kc, a.I - k0);
+            if (mine()) {
+                if (!met) {  // the activations are there once the blocks have met
+                    if (lane == 0) grid_wait(a.barrier, before, a.status);
+                    __syncwarp();
+                    asm volatile("fence.proxy.async;" ::: "memory");
+                    met = true;
+                }
+                token_rows(gr.count, a.acts + int64_t(gr.start + lane) * a.act_row + 2 * k0, B::token_pitch(kc, 2), 2 * (kc + n));
+            }
+            next_token_slot();
+            const uint8_t* base = wd.expert(e);
+            for (int q = w.lo; q < w.hi; ++q, next_slot()) {
+                if (!mine()) continue;
+                const int h0 = (w.set * kConsumers + q) * 16, rows = min(16, a.H - h0);
+                weights(mx, lane < rows, rows, base + (h0 + lane) * wd.row_bytes + int64_t(k0) * es, n,
+                        [&](int r) -> const uint8_t* {
+                            return r < rows ? wd.scales(e) + (h0 + r) * (wd.row_bytes / 32) + k0 / 32 : nullptr;
+                        });
+            }
+        }
+        if (*abort) {  // copies in flight land while the block still has its memory
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 1000000) __nanosleep(1000);
+        }
+    }
+};
+
+// One consumer warp: tile `warp` of every set.
+template <class B>
+struct Consumer {
+    const DecodeArgs& a;
+    const Tables& tb;
+    const Plan& p;
+    const uint8_t *ring, *tokens;
+    Bars* bars;
+    volatile int* abort;
+    float* s_out;  // [T][16]: this warp's row tile of the second product
+    int warp, lane;
+    int slot = 0, round = 0, tslot = 0, tround = 0;
+
+    // the step of a set's chunk: `n` columns; f(A, X): multiply the warp's slot, if `at` (its number in the step) is one of `size`
+    template <typename F>
+    __device__ __forceinline__ void step(int at, int size, F f) {
+        mbar_wait(bars->tfull + tslot, tround & 1, abort, a.status);
+        if (at >= 0 && at < size) {
+            int s = slot + at, r = round;
+            if (s >= a.slots) {
+                s -= a.slots;
+                ++r;
+            }
+            wait_round(bars->filled + s, bars->full + s, r, abort, a.status);
+            f(ring + s * B::SLOT, tokens + tslot * a.token_slot_bytes);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars->empty + s);
+        }
+        if (lane == 0) mbar_arrive(bars->tempty + tslot);
+        if ((slot += size) >= a.slots) {
+            slot -= a.slots;
+            ++round;
+        }
+        if (++tslot == a.token_slots) {
+            tslot = 0;
+            ++tround;
+        }
+    }
+
+    __device__ __forceinline__ void gates() {  // the shared expert's output gates, one warp a token
+        for (int t = blockIdx.x * kConsumers + warp; t < a.T; t += gridDim.x * kConsumers) {
+            float v = 0.0f;
+            for (int i = lane * 8; i < a.H; i += 256) {
+                const uint4 x = *reinterpret_cast<const uint4*>(a.x + t * a.xs + i);
+                const uint4 w = *reinterpret_cast<const uint4*>(a.gate_w + i);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float x0, x1, w0, w1;
+                    unpack_bf16x2(xs[q], x0, x1);
+                    unpack_bf16x2(ws[q], w0, w1);
+                    v = fmaf(x0, w0, fmaf(x1, w1, v));
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == 0) a.gate[t] = sigmoidf_(v);
+        }
+    }
+
+    __device__ __forceinline__ void first() {
+        for (Tiles w(p); w.more(p); w.next(p)) {
+            const Group gr = tb.groups[w.g];
+            const bool mx = B::MX && gr.expert < a.E;
+            const int kc = B::columns(mx), pitch = B::token_pitch(kc, 1);
+            float acc[2][B::NT][4] = {};
+            __nv_bfloat162 top[2] = {__float2bfloat162_rn(0.0f), __float2bfloat162_rn(0.0f)};
+            for (int k0 = 0; k0 < a.H; k0 += kc)
+                step(warp, w.size, [&](const uint8_t* A, const uint8_t* X) {
+                    multiply<B, 1>(acc, top, A, X, pitch, gr.count, min(kc, a.H - k0), mx, lane);
+                });
+            if (warp >= w.size) continue;
+            join<B>(acc, top);
+            const int i = (w.tile + warp) * 8 + (lane >> 2);
+            if (i >= a.I) continue;
+            // this thread has g and u of row i for tokens 8 t + 2 (lane & 3), and the next
+#pragma unroll
+            for (int t = 0; t < B::NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int n = 8 * t + 2 * (lane & 3) + j;
+                    if (n >= gr.count) continue;
+                    float g = acc[0][t][j], u = acc[0][t][2 + j];
+                    if (a.limit > 0.0f) {  // comparisons, so that NaN passes through
+                        g = g > a.limit ? a.limit : g;
+                        u = u > a.limit ? a.limit : u < -a.limit ? -a.limit : u;
+                    }
+                    const float v = g * sigmoidf_(g) * u;
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+                    __nv_bfloat16* d = a.acts + int64_t(gr.start + n) * a.act_row + i / kc * (2 * kc) + i % kc;
+                    d[0] = hi;
+                    d[kc] = __float2bfloat16_rn(v - __bfloat162float(hi));
+                }
+        }
+    }
+
+    __device__ __forceinline__ void put_out(int h0, int n_out) const {
+        const int h = h0 + (lane & 15);
+        if (h < a.H)
+            for (int i = lane; i < n_out; i += 32) a.out[i / 16 * a.os + h] = __float2bfloat16_rn(s_out[i]);
+    }
+
+    // out = bf16(sum) of this warp's row tile; a set that other blocks share goes through global memory
+    __device__ __forceinline__ void flush(int set) {
+        const int tile = set * kConsumers + warp, n_out = a.T * 16;
+        __syncwarp();
+        if (tile < p.ht) {
+            const int h0 = tile * 16, s0 = set * kConsumers * p.q;
+            const int first = owner(p.n2, s0, p.blocks2);
+            const int last = owner(p.n2, s0 + p.q * Steps::width(p, set) - 1, p.blocks2);
+            if (first == last) {
+                put_out(h0, n_out);
+            } else {
+                // block b's partial sums of this set: in its first place if the set is where it begins
+                auto part = [&](int b, int begin) {
+                    const bool here = begin / (kConsumers * p.q) == set;
+                    return a.part + ((int64_t(b) * 2 + (here ? 0 : 1)) * kConsumers + warp) * n_out;
+                };
+                float* to = part(blockIdx.x, p.s_begin);
+                for (int i = lane; i < n_out / 4; i += 32)
+                    reinterpret_cast<float4*>(to)[i] = reinterpret_cast<const float4*>(s_out)[i];
+                __threadfence();
+                __syncwarp();
+                unsigned seen = 0;
+                if (lane == 0) seen = atomicAdd(a.counters + tile, 1u);
+                if (__shfl_sync(0xffffffffu, seen, 0) == unsigned(last - first)) {
+                    __threadfence();
+                    for (int i = lane; i < n_out; i += 32) s_out[i] = 0.0f;
+                    for (int b = first; b <= last; ++b) {
+                        const float4* from = reinterpret_cast<const float4*>(part(b, share(p.n2, b, p.blocks2)));
+#pragma unroll 4
+                        for (int i = lane; i < n_out / 4; i += 32) {
+                            const float4 v = __ldcg(from + i);
+                            float4* d = reinterpret_cast<float4*>(s_out) + i;
+                            *d = make_float4(d->x + v.x, d->y + v.y, d->z + v.z, d->w + v.w);
+                        }
+                    }
+                    __syncwarp();
+                    put_out(h0, n_out);
+                    if (lane == 0) a.counters[tile] = 0;
+                }
+            }
+        }
+        for (int i = lane; i < n_out; i += 32) s_out[i] = 0.0f;
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ void second() {
+        Steps w(p);
+        while (w.more(p)) {
+            const int g = w.g, set = w.set;
+            const Group gr = tb.groups[g];
+            const bool mx = B::MX && gr.expert < a.E;
+            const int kc = B::columns(mx), pitch = B::token_pitch(kc, 2);
+            float acc[2][B::NT][4] = {};
+            __nv_bfloat162 top[2] = {__float2bfloat162_rn(0.0f), __float2bfloat162_rn(0.0f)};
+            do {
+                step(warp - w.lo, w.hi - w.lo, [&](const uint8_t* A, const uint8_t* X) {
+                    multiply<B, 2>(acc, top, A, X, pitch, gr.count, min(kc, a.I - w.c * kc), mx, lane);
+                });
+                w.next(p, tb.n_groups);
+            } while (w.more(p) && w.g == g && w.set == set);
+            join<B>(acc, top);
+#pragma unroll
+            for (int t = 0; t < B::NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int n = 8 * t + 2 * (lane & 3) + j;
+                    if (n >= gr.count) continue;
+                    const float c = tb.coef[gr.start + n];
+                    float* d = s_out + tb.tok[gr.start + n] * 16 + (lane >> 2);
+                    d[0] = fmaf(c, acc[0][t][j], d[0]);
+                    d[8] = fmaf(c, acc[0][t][2 + j], d[8]);
+                }
+            __syncwarp();
+            if (!w.more(p) || w.set != set) flush(set);
+        }
+    }
+};
+
+template <class B>
+__global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    Bars* bars = reinterpret_cast<Bars*>(smem);
+    int* s_abort = reinterpret_cast<int*>(bars + 1);
+    Tables tb;
+    tb.groups = reinterpret_cast<Group*>(s_abort + 4);
+    tb.tok = reinterpret_cast<int*>(tb.groups + a.max_groups);
+    tb.coef = reinterpret_cast<float*>(tb.tok + a.T * a.k + a.T);
+    uint8_t *tokens = smem + a.tokens_off, *ring = smem + a.ring_off;
+    float* s_out = reinterpret_cast<float*>(tokens - kConsumers * a.T * 16 * sizeof(float));  // [8][T][16]
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int id = tid < a.T * a.k ? __ldg(a.ids + tid) : -1;
+    const float prob = tid < a.T * a.k ? __ldg(a.probs + tid) : 0.0f;
+    const unsigned before = __ldcg(a.barrier);  // no block can have passed: this one has not arrived
+    if (tid < kSlots) {
+        mbar_init(bars->full + tid, B::MX ? 2 : 1);  // the byte count's arrival, and the scale codes'
+        mbar_init(bars->empty + tid, 1);
+        bars->filled[tid] = -1;
+        if (tid < kTokenSlots) {
+            mbar_init(bars->tfull + tid, 1);
+            mbar_init(bars->tempty + tid, kConsumers);
+            bars->tfilled[tid] = -1;
+        }
+        fence_mbar_init();
+    }
+    if (tid == 0) *s_abort = 0;
+    for (int i = tid; i < kConsumers * a.T * 16; i += kDecodeThreads) s_out[i] = 0.0f;
+    sort_routes<B::CAP>(a, tb, tokens, id, prob);  // its scratch: the rings' space
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tb.n_groups == 0) {  // nothing chosen and nothing shared, for every block alike
+        for (int i = blockIdx.x * kDecodeThreads + tid; i < a.T * a.H; i += gridDim.x * kDecodeThreads)
+            a.out[i / a.H * a.os + i % a.H] = __float2bfloat16_rn(0.0f);
+        return;
+    }
+    const Plan p = make_plan<B>(a, tb);
+    if (warp >= kConsumers) {
+        Producer<B>{a, tb, p, ring, tokens, bars, s_abort, warp - kConsumers, lane}.run(before);
+        return;
+    }
+    Consumer<B> c{a, tb, p, ring, tokens, bars, s_abort, s_out + warp * a.T * 16, warp, lane};
+    if (a.gate_w) c.gates();
+    c.first();
+    // the blocks meet: every activation and gate is written
+    __threadfence();
+    asm volatile("fence.proxy.async;" ::: "memory");  // the activations are read by bulk copies
+    consumer_sync();
+    if (tid == 0) {
+        __threadfence();
+        atomicAdd(a.barrier, blockIdx.x == 0 ? 0x80000000u - (gridDim.x - 1) : 1u);
+    }
+    if (a.gate_w) {
+        if (tid == 0) grid_wait(a.barrier, before, a.status);
+        consumer_sync();
+        for (int t = tid; t < a.T; t += 32 * kConsumers) tb.coef[t] = __ldcg(a.gate + t);
+        consumer_sync();
+    }
+    c.second();
 }
 
 struct DecodeShape {
@@ -157,17 +917,23 @@ moe_status check_decode(const moe_config* c, DecodeShape* s) {
     if (c->max_tokens > MOE_DECODE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
     if (c->num_experts > 1024 || c->topk > 32 || c->topk > c->num_experts) return MOE_ERR_UNSUPPORTED;
     const int64_t step = mx ? 32 : 8;
-    if (c->hidden % step || c->inter % step || c->hidden > 65536 || c->inter > 65536) return MOE_ERR_UNSUPPORTED;
+    if (c->hidden % step || c->inter % step || c->hidden > 32768 || c->inter > 32768) return MOE_ERR_UNSUPPORTED;
     *s = DecodeShape{c->max_tokens, c->hidden, c->num_experts, c->topk, c->inter, mx, c->no_shared_expert == 0,
                      c->swiglu_limit};
     return MOE_OK;
 }
 
+constexpr int kMaxBlocks = 256;
+
 struct DecodeSpace {
-    int* status;
-    const void** tables;  // [6][E]: gate, up, down payloads, then their scales
-    float* a;
+    unsigned* state;      // [0] status, [1] barrier, then the row tiles' counters
+    const void** tables;  // [3][2][E]: gate, up, down: payloads, scales
+    float* gate;
+    __nv_bfloat16* acts;
+    float* part;
 };
+
+size_t state_words(const DecodeShape& s) { return 2 + size_t((s.H + 15) / 16); }
 
 size_t carve_decode(const DecodeShape& s, uint8_t* base, DecodeSpace* w) {
     size_t off = 0;
@@ -176,9 +942,12 @@ size_t carve_decode(const DecodeShape& s, uint8_t* base, DecodeSpace* w) {
         off += (bytes + kDecodeAlign - 1) / kDecodeAlign * kDecodeAlign;
         return p;
     };
-    w->status = reinterpret_cast<int*>(take(sizeof(int)));
+    const size_t T = size_t(s.Tmax), chunks = size_t((s.I + 511) / 512);
+    w->state = reinterpret_cast<unsigned*>(take(state_words(s) * sizeof(unsigned)));
     w->tables = reinterpret_cast<const void**>(take(6 * size_t(s.E) * sizeof(void*)));
-    w->a = reinterpret_cast<float*>(take(size_t(s.Tmax) * size_t(s.k + 1) * size_t(s.I) * sizeof(float)));
+    w->gate = reinterpret_cast<float*>(take(T * sizeof(float)));
+    w->acts = reinterpret_cast<__nv_bfloat16*>(take(T * size_t(s.k + 1) * chunks * 2 * 512 * sizeof(__nv_bfloat16)));
+    w->part = reinterpret_cast<float*>(take(size_t(kMaxBlocks) * 2 * kConsumers * T * 16 * sizeof(float)));
     return off;
 }
 
@@ -191,7 +960,10 @@ bool is16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 struct moe_decoder {
     moe::DecodeShape s;
     moe::DecodeSpace ws;
-    std::vector<const void*> host[3];  // the per-expert pointers last uploaded: gate, up, down
+    int blocks;
+    // the per-expert pointers last uploaded (gate, up, down: payloads, scales), and a new set being compared
+    std::unique_ptr<const void*[]> host[3], fresh;
+    bool uploaded[3];
 };
 
 namespace moe {
@@ -208,20 +980,24 @@ moe_status decode_weight(moe_decoder* d, const moe_wview& v, int64_t N, int64_t 
     out->row_bytes = v.row_stride * es;
     if (routed && v.expert_ptrs) {
         const int64_t E = d->s.E;
-        std::vector<const void*> want(size_t(2 * E), nullptr);
+        const size_t n = size_t(mx ? 2 * E : E);
+        const void** want = d->fresh.get();
         for (int64_t e = 0; e < E; ++e) {
-            want[size_t(e)] = v.expert_ptrs[e];
-            if (!want[size_t(e)] || !is16(want[size_t(e)])) return MOE_ERR_INVALID_ARG;
-            if (mx && !(want[size_t(E + e)] = v.expert_ptrs[2 * E + e])) return MOE_ERR_INVALID_ARG;
+            want[e] = v.expert_ptrs[e];
+            if (!want[e] || !is16(want[e])) return MOE_ERR_INVALID_ARG;
+            if (mx && !(want[E + e] = v.expert_ptrs[2 * E + e])) return MOE_ERR_INVALID_ARG;
         }
         const void** dev = d->ws.tables + size_t(2 * slot) * size_t(E);
-        if (want != d->host[slot]) {
-            d->host[slot].clear();
+        if (!d->uploaded[slot] || !std::equal(want, want + n, d->host[slot].get())) {
+            cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+            if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return MOE_ERR_CUDA;
+            if (cap != cudaStreamCaptureStatusNone) return MOE_ERR_STATE;
+            d->uploaded[slot] = false;
+            std::copy(want, want + n, d->host[slot].get());
             // pageable source: staged before the call returns
-            if (cudaMemcpyAsync(dev, want.data(), want.size() * sizeof(void*), cudaMemcpyHostToDevice, st) !=
-                cudaSuccess)
+            if (cudaMemcpyAsync(dev, d->host[slot].get(), n * sizeof(void*), cudaMemcpyHostToDevice, st) != cudaSuccess)
                 return MOE_ERR_CUDA;
-            d->host[slot] = std::move(want);
+            d->uploaded[slot] = true;
         }
         out->table = dev;
         if (mx) out->scale_table = dev + E;
@@ -236,6 +1012,46 @@ moe_status decode_weight(moe_decoder* d, const moe_wview& v, int64_t N, int64_t 
     }
     out->base = static_cast<const uint8_t*>(v.data);
     return MOE_OK;
+}
+
+using Few16 = Build<1, 512, false>;
+using More16 = Build<4, 256, false>;
+using Few8 = Build<1, 512, true>;
+using More8 = Build<2, 512, true>;
+
+template <typename F>
+cudaError_t by_build(bool mx, int64_t T, F f) {
+    if (mx) return T <= 8 ? f(Few8()) : f(More8());
+    return T <= 8 ? f(Few16()) : f(More16());
+}
+
+template <class B>
+cudaError_t launch_decode(DecodeArgs& a, int blocks, cudaStream_t st) {
+    const int R = a.T * a.k, cap = std::min(B::CAP, a.T);
+    auto up = [](int v) { return (v + 127) / 128 * 128; };
+    a.max_groups = std::min(a.E, R) + R / B::CAP + (a.T + B::CAP - 1) / B::CAP;
+    a.tokens_off = up(int(sizeof(Bars)) + 16 + a.max_groups * int(sizeof(Group)) + (R + a.T) * 8 +
+                      kConsumers * a.T * 16 * int(sizeof(float)));
+    // the tokens' ring: about 48 KB, two slots at least
+    a.token_slot_bytes = up(cap * B::token_pitch(B::KC, 2));
+    a.token_slots = std::min(kTokenSlots, std::max(2, 49152 / a.token_slot_bytes));
+    a.ring_off = a.tokens_off + a.token_slots * a.token_slot_bytes;
+    a.slots = std::min(kSlots, (kSmemMax - a.ring_off) / B::SLOT);
+    const int scratch = 12 * a.E + 8 + 4 * R + 160;
+    if (a.slots < kConsumers || a.tokens_off + scratch > kSmemMax) return cudaErrorInvalidConfiguration;
+    const int64_t wide = (a.I + 511) / 512 * 512;
+    a.act_row = int(2 * wide);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(blocks));
+    cfg.blockDim = dim3(kDecodeThreads);
+    cfg.dynamicSmemBytes = size_t(kSmemMax);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_kernel<B>, a);
 }
 
 }  // namespace
@@ -267,15 +1083,27 @@ moe_status moe_decode_create(const moe_config* cfg, void* workspace, size_t work
     if (!workspace || workspace_bytes < carve_decode(s, nullptr, &w) ||
         (reinterpret_cast<uintptr_t>(workspace) % kDecodeAlign))
         return MOE_ERR_INVALID_ARG;
-    moe_decoder* d = new (std::nothrow) moe_decoder;
+    std::unique_ptr<moe_decoder> d(new (std::nothrow) moe_decoder());
     if (!d) return MOE_ERR_INVALID_ARG;
     d->s = s;
-    carve_decode(s, static_cast<uint8_t*>(workspace), &d->ws);
-    if (cudaMemset(d->ws.status, 0, sizeof(int)) != cudaSuccess) {
-        delete d;
-        return MOE_ERR_CUDA;
+    for (auto* p : {&d->host[0], &d->host[1], &d->host[2], &d->fresh}) {
+        p->reset(new (std::nothrow) const void*[2 * size_t(s.E)]());
+        if (!*p) return MOE_ERR_INVALID_ARG;
     }
-    *out = d;
+    carve_decode(s, static_cast<uint8_t*>(workspace), &d->ws);
+    int device = 0, sms = 0;
+    if (cudaGetDevice(&device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+        cudaMemset(d->ws.state, 0, state_words(s) * sizeof(unsigned)) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    d->blocks = std::min(sms, kMaxBlocks);
+    for (const int64_t T : {int64_t(1), int64_t(MOE_DECODE_MAX_TOKENS)})
+        if (by_build(s.mx, T, [](auto b) {
+                return cudaFuncSetAttribute(decode_kernel<decltype(b)>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            kSmemMax);
+            }) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    *out = d.release();
     return MOE_OK;
 }
 
@@ -300,7 +1128,6 @@ moe_status moe_decode(moe_decoder* d, int64_t T, const void* hidden, int64_t hid
     a.I = int(s.I);
     a.E = int(s.E);
     a.k = int(s.k);
-    a.mx = s.mx;
     a.shared = s.shared;
     a.limit = s.limit;
     a.x = static_cast<const __nv_bfloat16*>(hidden);
@@ -310,8 +1137,12 @@ moe_status moe_decode(moe_decoder* d, int64_t T, const void* hidden, int64_t hid
     a.gate_w = static_cast<const __nv_bfloat16*>(w->shared_output_gate);
     a.out = static_cast<__nv_bfloat16*>(out);
     a.os = out_stride;
-    a.a = d->ws.a;
-    a.status = d->ws.status;
+    a.acts = d->ws.acts;
+    a.gate = d->ws.gate;
+    a.part = d->ws.part;
+    a.status = reinterpret_cast<int*>(d->ws.state);
+    a.barrier = d->ws.state + 1;
+    a.counters = d->ws.state + 2;
     const moe_wview* views[W_COUNT] = {&w->shared_gate, &w->shared_up,   &w->shared_down,
                                        &w->routed_gate, &w->routed_up, &w->routed_down};
     for (int i = s.shared ? 0 : 3; i < W_COUNT; ++i) {
@@ -319,11 +1150,10 @@ moe_status moe_decode(moe_decoder* d, int64_t T, const void* hidden, int64_t hid
         const moe_status r = decode_weight(d, *views[i], down ? s.H : s.I, down ? s.I : s.H, i >= 3, i % 3, st, &a.w[i]);
         if (r != MOE_OK) return r;
     }
-    const int64_t up = int64_t(a.T) * (a.k + 1) * a.I, down = int64_t(a.T) * a.H;
-    decode_up_kernel<<<unsigned((up + 7) / 8), 256, 0, st>>>(a);
-    decode_down_kernel<<<unsigned((down + 7) / 8), 256, 0, st>>>(a);
-    count_launch(2);
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    const cudaError_t e = by_build(s.mx, T, [&](auto b) { return launch_decode<decltype(b)>(a, d->blocks, st); });
+    if (e == cudaErrorInvalidConfiguration) return MOE_ERR_UNSUPPORTED;
+    count_launch();
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_decode_status(moe_decoder* d, void* stream) {
@@ -331,9 +1161,11 @@ moe_status moe_decode_status(moe_decoder* d, void* stream) {
     if (!d) return MOE_ERR_INVALID_ARG;
     int v = 0;
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess ||
-        cudaMemcpy(&v, d->ws.status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess ||
-        cudaMemset(d->ws.status, 0, sizeof(int)) != cudaSuccess)
+        cudaMemcpy(&v, d->ws.state, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
         return MOE_ERR_CUDA;
+    // after a wait that gave up the barrier and the counters start anew as well
+    const size_t words = (v & kStatusTimeout) ? state_words(d->s) : 1;
+    if (cudaMemset(d->ws.state, 0, words * sizeof(unsigned)) != cudaSuccess) return MOE_ERR_CUDA;
     if (v & kStatusTimeout) return MOE_ERR_TIMEOUT;
     if (v & kStatusRouting) return MOE_ERR_ROUTING;
     return MOE_OK;

@@ -293,6 +293,33 @@ def test_nan_stays_in_its_token_and_its_expert(mx):
 
 
 @gpu
+@pytest.mark.parametrize("T", [3, 20])
+def test_every_e4m3_code_and_scale(T):
+    """Payloads of all codes but NaN (subnormals among them) under scales from tiny to large, one row
+    of subnormals alone; a scale code of 255 is NaN."""
+    H, I, E, k = 512, 64, 3, 2
+    c = Layer(T, H, I, E, k, True, False, seed=60, missing=0.0)
+    codes = torch.tensor([v for v in range(256) if v & 0x7F != 0x7F], dtype=torch.uint8, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    pick = lambda t, vals: vals[torch.randint(0, len(vals), t.shape, generator=g, device="cuda")]  # noqa: E731
+    c.q1, c.q2 = pick(c.q1, codes), pick(c.q2, codes)
+    c.q2[:, 7] = pick(c.q2[:, 7], torch.tensor([0x01, 0x81, 0x07, 0x84, 0x00, 0x80], dtype=torch.uint8, device="cuda"))
+    c.s1 = pick(c.s1, torch.arange(106, 117, dtype=torch.uint8, device="cuda"))
+    c.s2 = pick(c.s2, torch.arange(60, 140, dtype=torch.uint8, device="cuda"))
+    c.fc1, c.fc2 = mx_values(c.q1, c.s1), mx_values(c.q2, c.s2)
+    dec = c.decoder()
+    out = dec.forward_topk(c.x, c.ids, c.probs, c.weights())
+    check(out, *c.reference())
+    assert out[:, 7].any()
+    c.s2[1, 9, 1] = 255
+    got = dec.forward_topk(c.x, c.ids, c.probs, c.weights())
+    hit = (c.ids == 1).any(1)
+    assert got[hit, 9].isnan().all() and torch.equal(got[~hit], out[~hit])
+    rest = [h for h in range(H) if h != 9]
+    assert torch.equal(got[:, rest], out[:, rest])
+
+
+@gpu
 def test_fewer_tokens_streams_graph_and_old_workspace_contents():
     c = Layer(33, 512, 160, 9, 4, seed=40)
     w = c.weights()
