@@ -87,6 +87,9 @@ struct DecodeArgs {
     unsigned* counters;       // per row tile: blocks done with it; 0 between launches
     unsigned* barrier;        // top bit flips when every block has arrived
     int* status;
+    // chunks of H and of I by weight type (the shared expert's, routed), tiles of I and H, and
+    // what a slot of the shared expert costs, in halves of a slot of a routed one
+    int c1_shared, c1, c2_shared, c2, it, ht, shared_cost;
     // shared memory plan
     int max_groups;
     int slots, token_slots, token_slot_bytes;
@@ -105,11 +108,11 @@ struct Build {
     static constexpr int KB = MX ? KC / 2 : KC; // columns of a slot of bf16 weights
     static constexpr int P16 = 2 * KB + 64;     // pitch of a weight row of bf16
     static constexpr int P8 = KC + 32;          // pitch of a weight row of E4M3
-    static constexpr int PS = KC / 32 + 4;      // pitch of a row's scale codes
-    static constexpr int SCALES = 16 * P8;      // offset of the scale codes in a slot
-    static constexpr int SLOT = MX ? (16 * (P8 + PS) > 16 * P16 ? 16 * (P8 + PS) : 16 * P16) : 16 * P16;
-    static_assert(SLOT % 64 == 0 && PS % 4 == 0, "slots start on 16 bytes");
-    static __device__ __forceinline__ int columns(bool mx) { return MX && mx ? KC : KB; }
+    static constexpr int PS = KC / 8 + 16;      // pitch of a row's block scales, in fp32
+    static constexpr int SCALES = 16 * P8;      // offset of the scales in a slot
+    static constexpr int SLOT = MX ? 16 * (P8 + PS) : 16 * P16;
+    static_assert(SLOT % 64 == 0 && SLOT >= 16 * P16, "slots start on 16 bytes and hold either type");
+    static __host__ __device__ constexpr int columns(bool mx) { return MX && mx ? KC : KB; }
     // pitch of a token row of `terms` terms of kc columns
     static __host__ __device__ constexpr int token_pitch(int kc, int terms) { return 2 * kc * terms + 64; }
 };
@@ -138,25 +141,25 @@ __device__ __forceinline__ float e8m0_value(uint32_t code) {
 // Four E4M3 codes -> two bf16 pairs, exact (4 significant bits), without the conversion
 // unit, which takes 16 values a cycle: a code's 7 magnitude bits under bf16's exponent are its
 // value times 2^-120 (subnormals included), so sign-extend each byte, shift it to its
-// place, keep sign and magnitude, multiply by 2^120. The NaN codes (0x7F, 0xFF) come out as
-// +-480, which no other code does: `top` keeps the largest magnitude seen.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t q, uint32_t select, __nv_bfloat162& top) {
+// place, keep sign and magnitude, multiply by 2^120.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t q, uint32_t select) {
     uint32_t x;
     asm("prmt.b32 %0, %1, 0, %2;" : "=r"(x) : "r"(q), "r"(select));
     x = (x << 4) & 0x87f087f0u;
     const __nv_bfloat162 scale = __halves2bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));
     const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x), scale);
-    top = __hmax2(top, __habs2(v));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ void e4m3_to_bf16(uint32_t q, uint32_t& lo, uint32_t& hi, __nv_bfloat162& top) {
-    lo = e4m3_pair(q, 0x9180u, top);
-    hi = e4m3_pair(q, 0xB3A2u, top);
+// The NaN codes (0x7F, 0xFF) come out as +-480: they alone carry into a byte's top bit when 1
+// is added to the magnitude, which `nan` collects.
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t q, uint32_t& lo, uint32_t& hi, uint32_t& nan) {
+    nan |= (q & 0x7f7f7f7fu) + 0x01010101u;
+    lo = e4m3_pair(q, 0x9180u);
+    hi = e4m3_pair(q, 0xB3A2u);
 }
 // the sums of a weight row (spread over four lanes) with a NaN code in it are NaN for every token
-__device__ __forceinline__ bool row_has_nan(__nv_bfloat162 top) {
-    const bool bad = __low2float(top) > 448.0f || __high2float(top) > 448.0f;
-    const unsigned m = __ballot_sync(0xffffffffu, bad);
+__device__ __forceinline__ bool row_has_nan(uint32_t nan) {
+    const unsigned m = __ballot_sync(0xffffffffu, (nan & 0x80808080u) != 0);
     return (m >> (threadIdx.x & 28)) & 15u;
 }
 
@@ -291,43 +294,56 @@ __device__ __forceinline__ void sort_routes(const DecodeArgs& a, Tables& tb, uin
 }
 
 // A block's share. First product: tiles u = group * it + tile of I, from u_begin to u_end.
-// Second product: slots of (set of 8 tiles of H, group, chunk, tile), the tile fastest.
+// Second product: slots of (set of 8 tiles of H, group, chunk, tile), the tile fastest. Shares
+// are equal in cost: a slot of a routed group counts 2, one of the shared expert shared_cost.
 struct Plan {
     int n_shared;
-    int c1_shared, c1, c2_shared, c2;  // chunks of H and of I: of the shared expert's groups, of routed ones
-    int it, ht;                // tiles of I and H
+    int c2_shared, c2, it, ht;
     int u_begin, u_end;
+    int shared_cost;
     int q_shared, q;           // chunks of I over the shared groups, over all groups
-    int n2, blocks2;           // slots of the second product, and the blocks that have any
+    int tile_cost;             // of one tile of H: all its chunks
+    int n2, cost2, blocks2;    // second product: slots, their cost, and the blocks that have any
     int s_begin, s_end;
+    // the cost of the slots before s, and the first slot before which the cost is at least x
+    __device__ __forceinline__ int cost_before(int s) const {
+        const int set = s / (kConsumers * q), in = s - set * kConsumers * q;
+        const int heavy = min(kConsumers, ht - set * kConsumers) * q_shared;
+        return set * kConsumers * tile_cost + min(in, heavy) * shared_cost + max(in - heavy, 0) * 2;
+    }
+    __device__ __forceinline__ int slot_at(int x) const {
+        const int set = x / (kConsumers * tile_cost), in = x - set * kConsumers * tile_cost;
+        const int heavy = min(kConsumers, ht - set * kConsumers) * q_shared, hc = heavy * shared_cost;
+        return set * kConsumers * q + (in <= hc ? (in + shared_cost - 1) / shared_cost : heavy + (in - hc + 1) / 2);
+    }
+    __device__ __forceinline__ int begin(int block) const { return slot_at(share(cost2, block, blocks2)); }
 };
 
-template <class B>
 __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, const Tables& tb) {
     Plan p;
     const int c = blockIdx.x, n = gridDim.x, routed = tb.n_groups - tb.n_shared;
     p.n_shared = tb.n_shared;
-    auto chunks = [](int n, bool mx) { return (n + B::columns(mx) - 1) / B::columns(mx); };
-    p.c1_shared = chunks(a.H, false);
-    p.c2_shared = chunks(a.I, false);
-    p.c1 = chunks(a.H, true);
-    p.c2 = chunks(a.I, true);
-    p.it = (a.I + 7) / 8;
-    p.ht = (a.H + 15) / 16;
-    // equal shares of slots, rounded up to tiles
-    const int slots_shared = p.it * tb.n_shared * p.c1_shared, slots = slots_shared + p.it * routed * p.c1;
-    auto tile = [&](int s) {
-        return s <= slots_shared ? (s + p.c1_shared - 1) / p.c1_shared
-                                 : p.it * tb.n_shared + (s - slots_shared + p.c1 - 1) / p.c1;
+    p.c2_shared = a.c2_shared;
+    p.c2 = a.c2;
+    p.it = a.it;
+    p.ht = a.ht;
+    p.shared_cost = a.shared_cost;
+    const int per_shared = a.c1_shared * a.shared_cost, per = a.c1 * 2;  // of a tile of I
+    const int cost_shared = a.it * tb.n_shared * per_shared, cost = cost_shared + a.it * routed * per;
+    auto tile = [&](int x) {
+        return x <= cost_shared ? (x + per_shared - 1) / per_shared
+                                : a.it * tb.n_shared + (x - cost_shared + per - 1) / per;
     };
-    p.u_begin = tile(share(slots, c, n));
-    p.u_end = tile(share(slots, c + 1, n));
-    p.q_shared = tb.n_shared * p.c2_shared;
-    p.q = p.q_shared + routed * p.c2;
-    p.n2 = p.q * p.ht;
-    p.blocks2 = min(p.n2, n);
-    p.s_begin = c < p.blocks2 ? share(p.n2, c, p.blocks2) : p.n2;
-    p.s_end = c < p.blocks2 ? share(p.n2, c + 1, p.blocks2) : p.n2;
+    p.u_begin = tile(share(cost, c, n));
+    p.u_end = tile(share(cost, c + 1, n));
+    p.q_shared = tb.n_shared * a.c2_shared;
+    p.q = p.q_shared + routed * a.c2;
+    p.tile_cost = p.q_shared * a.shared_cost + (p.q - p.q_shared) * 2;
+    p.n2 = p.q * a.ht;
+    p.cost2 = p.tile_cost * a.ht;
+    p.blocks2 = max(1, min(p.cost2 / a.shared_cost, n));  // no share is smaller than a slot: none is empty
+    p.s_begin = c < p.blocks2 ? p.begin(c) : p.n2;
+    p.s_end = c + 1 < p.blocks2 ? p.begin(c + 1) : p.n2;
     return p;
 }
 
@@ -401,7 +417,7 @@ __device__ __forceinline__ void k_step(float (*acc0)[4], float (*acc1)[4], const
 
 // acc += (16 weight rows at A) x (N tiles of 8 tokens at X), over n columns of a slot
 template <class B, int N, int TERMS>
-__device__ __forceinline__ void multiply_tiles(float (&acc)[2][B::NT][4], __nv_bfloat162 (&top)[2], const uint8_t* A,
+__device__ __forceinline__ void multiply_tiles(float (&acc)[2][B::NT][4], uint32_t (&nan)[2], const uint8_t* A,
                                                const uint8_t* X, int pitch, int count, int n, bool mx, int lane) {
     const int r = lane >> 2, c8 = (lane & 3) * 8;
     const uint8_t* px[N];
@@ -413,24 +429,34 @@ __device__ __forceinline__ void multiply_tiles(float (&acc)[2][B::NT][4], __nv_b
     }
     if (B::MX && mx) {
         const uint8_t *pa = A + r * B::P8 + c8, *S = A + B::SCALES + r * B::PS;
-#pragma unroll 2
-        for (int k = 0; k < n; k += 32) {  // n is a multiple of 32
-            const uint2 qa = *reinterpret_cast<const uint2*>(pa + k);
-            const uint2 qb = *reinterpret_cast<const uint2*>(pa + 8 * B::P8 + k);
-            const float sa = e8m0_value(S[k >> 5]), sb = e8m0_value(S[8 * B::PS + (k >> 5)]);
-            uint4 wa, wb;
-            e4m3_to_bf16(qa.x, wa.x, wa.y, top[0]);
-            e4m3_to_bf16(qa.y, wa.z, wa.w, top[0]);
-            e4m3_to_bf16(qb.x, wb.x, wb.y, top[1]);
-            e4m3_to_bf16(qb.y, wb.z, wb.w, top[1]);
-            float d[2][N][4] = {};
-            k_step<N, TERMS>(d[0], d[1], wa, wb, px, there, 2 * k, 2 * B::KC);
+        for (int k4 = 0; k4 < n; k4 += 128) {  // n is a multiple of 32
+            const float4 sa4 = *reinterpret_cast<const float4*>(S + k4 / 8);
+            const float4 sb4 = *reinterpret_cast<const float4*>(S + 8 * B::PS + k4 / 8);
+            const float sa[4] = {sa4.x, sa4.y, sa4.z, sa4.w}, sb[4] = {sb4.x, sb4.y, sb4.z, sb4.w};
 #pragma unroll
-            for (int t = 0; t < N; ++t) {
-                acc[0][t][0] = fmaf(sa, d[0][t][0] + d[1][t][0], acc[0][t][0]);
-                acc[0][t][1] = fmaf(sa, d[0][t][1] + d[1][t][1], acc[0][t][1]);
-                acc[0][t][2] = fmaf(sb, d[0][t][2] + d[1][t][2], acc[0][t][2]);
-                acc[0][t][3] = fmaf(sb, d[0][t][3] + d[1][t][3], acc[0][t][3]);
+            for (int j = 0; j < 4; ++j) {
+                const int k = k4 + 32 * j;
+                if (k >= n) break;
+                const uint2 qa = *reinterpret_cast<const uint2*>(pa + k);
+                const uint2 qb = *reinterpret_cast<const uint2*>(pa + 8 * B::P8 + k);
+                uint4 wa, wb;
+                e4m3_to_bf16(qa.x, wa.x, wa.y, nan[0]);
+                e4m3_to_bf16(qa.y, wa.z, wa.w, nan[0]);
+                e4m3_to_bf16(qb.x, wb.x, wb.y, nan[1]);
+                e4m3_to_bf16(qb.y, wb.z, wb.w, nan[1]);
+                float d[2][N][4] = {};
+                k_step<N, TERMS>(d[0], d[1], wa, wb, px, there, 2 * k, 2 * B::KC);
+#pragma unroll
+                for (int t = 0; t < N; ++t) {
+                    acc[0][t][0] = fmaf(sa[j], d[0][t][0], acc[0][t][0]);
+                    acc[0][t][1] = fmaf(sa[j], d[0][t][1], acc[0][t][1]);
+                    acc[0][t][2] = fmaf(sb[j], d[0][t][2], acc[0][t][2]);
+                    acc[0][t][3] = fmaf(sb[j], d[0][t][3], acc[0][t][3]);
+                    acc[1][t][0] = fmaf(sa[j], d[1][t][0], acc[1][t][0]);
+                    acc[1][t][1] = fmaf(sa[j], d[1][t][1], acc[1][t][1]);
+                    acc[1][t][2] = fmaf(sb[j], d[1][t][2], acc[1][t][2]);
+                    acc[1][t][3] = fmaf(sb[j], d[1][t][3], acc[1][t][3]);
+                }
             }
         }
         return;
@@ -453,21 +479,21 @@ __device__ __forceinline__ void multiply_tiles(float (&acc)[2][B::NT][4], __nv_b
 }
 
 template <class B, int TERMS>
-__device__ __forceinline__ void multiply(float (&acc)[2][B::NT][4], __nv_bfloat162 (&top)[2], const uint8_t* A,
+__device__ __forceinline__ void multiply(float (&acc)[2][B::NT][4], uint32_t (&nan)[2], const uint8_t* A,
                                          const uint8_t* X, int pitch, int count, int n, bool mx, int lane) {
     if (B::NT == 1 || count <= 8)
-        multiply_tiles<B, 1, TERMS>(acc, top, A, X, pitch, count, n, mx, lane);
+        multiply_tiles<B, 1, TERMS>(acc, nan, A, X, pitch, count, n, mx, lane);
     else
-        multiply_tiles<B, B::NT, TERMS>(acc, top, A, X, pitch, count, n, mx, lane);
+        multiply_tiles<B, B::NT, TERMS>(acc, nan, A, X, pitch, count, n, mx, lane);
 }
 
 // the two sets of sums as one (in acc[0]); a weight row with a NaN code is NaN for every token
 template <class B>
-__device__ __forceinline__ void join(float (&acc)[2][B::NT][4], const __nv_bfloat162 (&top)[2]) {
+__device__ __forceinline__ void join(float (&acc)[2][B::NT][4], const uint32_t (&nan)[2]) {
     bool bad[2] = {false, false};
     if (B::MX) {
-        bad[0] = row_has_nan(top[0]);
-        bad[1] = row_has_nan(top[1]);
+        bad[0] = row_has_nan(nan[0]);
+        bad[1] = row_has_nan(nan[1]);
     }
 #pragma unroll
     for (int t = 0; t < B::NT; ++t)
@@ -549,9 +575,34 @@ struct Producer {
             ++tround;
         }
     }
-    // 16 rows (live: this lane has one, at src) of n columns into the next slot
+    // 16 rows (live: this lane has one, at src) of n columns into the next slot; with mx also
+    // their scale codes: codes(r), row r's first (of rows past the end: any row's)
     template <typename F>
     __device__ __forceinline__ void weights(bool mx, bool live, int rows, const uint8_t* src, int n, F codes) {
+        constexpr int W = B::KC / 256;  // words of codes of a lane: two lanes a row
+        const uint8_t* first = nullptr;
+        const int left = n / 32 - (lane & 1) * 4 * W;  // codes that are this lane's
+        uint32_t code[W] = {};
+        if (B::MX && mx) {
+            first = codes(lane >> 1) + (lane & 1) * 4 * W;
+            if ((reinterpret_cast<uintptr_t>(first) & (4 * W - 1)) == 0 && left >= 4 * W) {
+                if (W == 4) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(first));
+                    code[0] = v.x;
+                    code[W > 1 ? 1 : 0] = v.y;
+                    code[W > 2 ? 2 : 0] = v.z;
+                    code[W > 3 ? 3 : 0] = v.w;
+                } else {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(first));
+                    code[0] = v.x;
+                    code[W > 1 ? 1 : 0] = v.y;
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < W; ++q)
+                    if (4 * q < left) code[q] = load_codes(first + 4 * q, first + left);
+            }
+        }
         if (round) wait_round(bars->filled + slot, bars->empty + slot, round - 1, abort, a.status);
         if (*abort) return;  // a wait gave up: nothing more is asked for
         __syncwarp();
@@ -559,30 +610,20 @@ struct Producer {
         uint8_t* A = ring + slot * B::SLOT;
         uint64_t* bar = bars->full + slot;
         const int bytes = B::MX && mx ? n : 2 * n;
-        constexpr int W = (16 * B::KC / 128 + 31) / 32;  // words of scale codes of a lane
-        uint32_t code[W];
-        if (B::MX && mx) {
-#pragma unroll
-            for (int q = 0; q < W; ++q) {
-                const int i = q * 32 + lane, r = i / (B::KC / 128), wd = i % (B::KC / 128);
-                const uint8_t* c = codes(r);
-                code[q] = c != nullptr && 4 * wd < n / 32 ? load_codes(c + 4 * wd, c + n / 32) : 0u;
-            }
-        }
-        if (B::MX) fence_proxy_async_smem();  // copies may land where codes were written
+        if (B::MX) fence_proxy_async_smem();  // copies may land where scales were written
         if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(rows * bytes));
         __syncwarp();
         if (live) bulk_load(A + lane * (B::MX && mx ? B::P8 : B::P16), src, bytes, bar);
         if (B::MX) {
             if (mx) {
+                float4* to = reinterpret_cast<float4*>(A + B::SCALES + (lane >> 1) * B::PS) + (lane & 1) * W;
 #pragma unroll
-                for (int q = 0; q < W; ++q) {
-                    const int i = q * 32 + lane, r = i / (B::KC / 128), wd = i % (B::KC / 128);
-                    *reinterpret_cast<uint32_t*>(A + B::SCALES + r * B::PS + 4 * wd) = code[q];
-                }
+                for (int q = 0; q < W; ++q)
+                    to[q] = make_float4(e8m0_value(code[q] & 255u), e8m0_value(code[q] >> 8 & 255u),
+                                        e8m0_value(code[q] >> 16 & 255u), e8m0_value(code[q] >> 24));
                 __syncwarp();
             }
-            if (lane == 0) mbar_arrive(bar);  // the codes are there
+            if (lane == 0) mbar_arrive(bar);  // the scales are there
         }
     }
     // this lane's token row (if it has one) into the next token slot
@@ -616,8 +657,7 @@ struct Producer {
                     const int i0 = (w.tile + q) * 8, rows = min(8, a.I - i0), i = i0 + (lane & 7);
                     const uint8_t* src = ((lane & 8) ? bu + i * wu.row_bytes : bg + i * wg.row_bytes) + int64_t(k0) * es;
                     weights(mx, lane < 16 && (lane & 7) < rows, 2 * rows, src, n, [&](int r) -> const uint8_t* {
-                        if ((r & 7) >= rows) return nullptr;
-                        const int64_t ir = i0 + (r & 7);
+                        const int64_t ir = i0 + min(r & 7, rows - 1);
                         return ((r & 8) ? wu.scales(e) + ir * (wu.row_bytes / 32) : wg.scales(e) + ir * (wg.row_bytes / 32)) + k0 / 32;
                     });
                 }
@@ -645,7 +685,7 @@ struct Producer {
                 const int h0 = (w.set * kConsumers + q) * 16, rows = min(16, a.H - h0);
                 weights(mx, lane < rows, rows, base + (h0 + lane) * wd.row_bytes + int64_t(k0) * es, n,
                         [&](int r) -> const uint8_t* {
-                            return r < rows ? wd.scales(e) + (h0 + r) * (wd.row_bytes / 32) + k0 / 32 : nullptr;
+                            return wd.scales(e) + (h0 + min(r, rows - 1)) * (wd.row_bytes / 32) + k0 / 32;
                         });
             }
         }
@@ -722,13 +762,13 @@ struct Consumer {
             const bool mx = B::MX && gr.expert < a.E;
             const int kc = B::columns(mx), pitch = B::token_pitch(kc, 1);
             float acc[2][B::NT][4] = {};
-            __nv_bfloat162 top[2] = {__float2bfloat162_rn(0.0f), __float2bfloat162_rn(0.0f)};
+            uint32_t nan[2] = {0, 0};
             for (int k0 = 0; k0 < a.H; k0 += kc)
                 step(warp, w.size, [&](const uint8_t* A, const uint8_t* X) {
-                    multiply<B, 1>(acc, top, A, X, pitch, gr.count, min(kc, a.H - k0), mx, lane);
+                    multiply<B, 1>(acc, nan, A, X, pitch, gr.count, min(kc, a.H - k0), mx, lane);
                 });
             if (warp >= w.size) continue;
-            join<B>(acc, top);
+            join<B>(acc, nan);
             const int i = (w.tile + warp) * 8 + (lane >> 2);
             if (i >= a.I) continue;
             // this thread has g and u of row i for tokens 8 t + 2 (lane & 3), and the next
@@ -764,8 +804,8 @@ struct Consumer {
         __syncwarp();
         if (tile < p.ht) {
             const int h0 = tile * 16, s0 = set * kConsumers * p.q;
-            const int first = owner(p.n2, s0, p.blocks2);
-            const int last = owner(p.n2, s0 + p.q * Steps::width(p, set) - 1, p.blocks2);
+            const int first = owner(p.cost2, p.cost_before(s0), p.blocks2);
+            const int last = owner(p.cost2, p.cost_before(s0 + p.q * Steps::width(p, set) - 1), p.blocks2);
             if (first == last) {
                 put_out(h0, n_out);
             } else {
@@ -785,7 +825,7 @@ struct Consumer {
                     __threadfence();
                     for (int i = lane; i < n_out; i += 32) s_out[i] = 0.0f;
                     for (int b = first; b <= last; ++b) {
-                        const float4* from = reinterpret_cast<const float4*>(part(b, share(p.n2, b, p.blocks2)));
+                        const float4* from = reinterpret_cast<const float4*>(part(b, p.begin(b)));
 #pragma unroll 4
                         for (int i = lane; i < n_out / 4; i += 32) {
                             const float4 v = __ldcg(from + i);
@@ -811,14 +851,14 @@ struct Consumer {
             const bool mx = B::MX && gr.expert < a.E;
             const int kc = B::columns(mx), pitch = B::token_pitch(kc, 2);
             float acc[2][B::NT][4] = {};
-            __nv_bfloat162 top[2] = {__float2bfloat162_rn(0.0f), __float2bfloat162_rn(0.0f)};
+            uint32_t nan[2] = {0, 0};
             do {
                 step(warp - w.lo, w.hi - w.lo, [&](const uint8_t* A, const uint8_t* X) {
-                    multiply<B, 2>(acc, top, A, X, pitch, gr.count, min(kc, a.I - w.c * kc), mx, lane);
+                    multiply<B, 2>(acc, nan, A, X, pitch, gr.count, min(kc, a.I - w.c * kc), mx, lane);
                 });
                 w.next(p, tb.n_groups);
             } while (w.more(p) && w.g == g && w.set == set);
-            join<B>(acc, top);
+            join<B>(acc, nan);
 #pragma unroll
             for (int t = 0; t < B::NT; ++t)
 #pragma unroll
@@ -853,7 +893,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
     const float prob = tid < a.T * a.k ? __ldg(a.probs + tid) : 0.0f;
     const unsigned before = __ldcg(a.barrier);  // no block can have passed: this one has not arrived
     if (tid < kSlots) {
-        mbar_init(bars->full + tid, B::MX ? 2 : 1);  // the byte count's arrival, and the scale codes'
+        mbar_init(bars->full + tid, B::MX ? 2 : 1);  // the byte count's arrival, and the scales'
         mbar_init(bars->empty + tid, 1);
         bars->filled[tid] = -1;
         if (tid < kTokenSlots) {
@@ -873,7 +913,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
             a.out[i / a.H * a.os + i % a.H] = __float2bfloat16_rn(0.0f);
         return;
     }
-    const Plan p = make_plan<B>(a, tb);
+    const Plan p = make_plan(a, tb);
     if (warp >= kConsumers) {
         Producer<B>{a, tb, p, ring, tokens, bars, s_abort, warp - kConsumers, lane}.run(before);
         return;
@@ -942,11 +982,11 @@ size_t carve_decode(const DecodeShape& s, uint8_t* base, DecodeSpace* w) {
         off += (bytes + kDecodeAlign - 1) / kDecodeAlign * kDecodeAlign;
         return p;
     };
-    const size_t T = size_t(s.Tmax), chunks = size_t((s.I + 511) / 512);
+    const size_t T = size_t(s.Tmax), chunks = size_t((s.I + 1023) / 1024);
     w->state = reinterpret_cast<unsigned*>(take(state_words(s) * sizeof(unsigned)));
     w->tables = reinterpret_cast<const void**>(take(6 * size_t(s.E) * sizeof(void*)));
     w->gate = reinterpret_cast<float*>(take(T * sizeof(float)));
-    w->acts = reinterpret_cast<__nv_bfloat16*>(take(T * size_t(s.k + 1) * chunks * 2 * 512 * sizeof(__nv_bfloat16)));
+    w->acts = reinterpret_cast<__nv_bfloat16*>(take(T * size_t(s.k + 1) * chunks * 2 * 1024 * sizeof(__nv_bfloat16)));
     w->part = reinterpret_cast<float*>(take(size_t(kMaxBlocks) * 2 * kConsumers * T * 16 * sizeof(float)));
     return off;
 }
@@ -1016,7 +1056,7 @@ moe_status decode_weight(moe_decoder* d, const moe_wview& v, int64_t N, int64_t 
 
 using Few16 = Build<1, 512, false>;
 using More16 = Build<4, 256, false>;
-using Few8 = Build<1, 512, true>;
+using Few8 = Build<1, 1024, true>;
 using More8 = Build<2, 512, true>;
 
 template <typename F>
@@ -1039,8 +1079,15 @@ cudaError_t launch_decode(DecodeArgs& a, int blocks, cudaStream_t st) {
     a.slots = std::min(kSlots, (kSmemMax - a.ring_off) / B::SLOT);
     const int scratch = 12 * a.E + 8 + 4 * R + 160;
     if (a.slots < kConsumers || a.tokens_off + scratch > kSmemMax) return cudaErrorInvalidConfiguration;
-    const int64_t wide = (a.I + 511) / 512 * 512;
-    a.act_row = int(2 * wide);
+    a.act_row = 2 * ((a.I + 1023) / 1024 * 1024);
+    auto chunks = [](int n, bool mx) { return (n + B::columns(mx) - 1) / B::columns(mx); };
+    a.c1_shared = chunks(a.H, false);
+    a.c2_shared = chunks(a.I, false);
+    a.c1 = chunks(a.H, true);
+    a.c2 = chunks(a.I, true);
+    a.it = (a.I + 7) / 8;
+    a.ht = (a.H + 15) / 16;
+    a.shared_cost = a.T > 8 ? 3 : 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(blocks));
     cfg.blockDim = dim3(kDecodeThreads);
