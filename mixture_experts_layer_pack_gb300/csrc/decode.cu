@@ -105,6 +105,7 @@ struct Build {
     static constexpr int NT = NT_, KC = KC_;
     static constexpr bool MX = MX_;
     static constexpr int CAP = 8 * NT;          // tokens of a group
+    static constexpr int CH = NT == 1 ? 8 : 2;  // sets of sums: an instruction's result is late, its successor another's
     static constexpr int KB = MX ? KC / 2 : KC; // columns of a slot of bf16 weights
     static constexpr int P16 = 2 * KB + 64;     // pitch of a weight row of bf16
     static constexpr int P8 = KC + 32;          // pitch of a weight row of E4M3
@@ -417,7 +418,7 @@ __device__ __forceinline__ void k_step(float (*acc0)[4], float (*acc1)[4], const
 
 // acc += (16 weight rows at A) x (N tiles of 8 tokens at X), over n columns of a slot
 template <class B, int N, int TERMS>
-__device__ __forceinline__ void multiply_tiles(float (&acc)[2][B::NT][4], uint32_t (&nan)[2], const uint8_t* A,
+__device__ __forceinline__ void multiply_tiles(float (&acc)[B::CH][B::NT][4], uint32_t (&nan)[2], const uint8_t* A,
                                                const uint8_t* X, int pitch, int count, int n, bool mx, int lane) {
     const int r = lane >> 2, c8 = (lane & 3) * 8;
     const uint8_t* px[N];
@@ -463,8 +464,15 @@ __device__ __forceinline__ void multiply_tiles(float (&acc)[2][B::NT][4], uint32
     }
     const uint8_t* pa = A + r * B::P16 + 2 * c8;
     const int whole = n & ~31;
-#pragma unroll 4
-    for (int k = 0; k < whole; k += 32)
+    int k = 0;
+    for (; k + 128 <= n; k += 128)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            k_step<N, TERMS>(acc[2 * j % B::CH], acc[(2 * j + 1) % B::CH],
+                             *reinterpret_cast<const uint4*>(pa + 2 * (k + 32 * j)),
+                             *reinterpret_cast<const uint4*>(pa + 8 * B::P16 + 2 * (k + 32 * j)), px, there,
+                             2 * (k + 32 * j), 2 * B::KB);
+    for (; k < whole; k += 32)
         k_step<N, TERMS>(acc[0], acc[1], *reinterpret_cast<const uint4*>(pa + 2 * k),
                          *reinterpret_cast<const uint4*>(pa + 8 * B::P16 + 2 * k), px, there, 2 * k, 2 * B::KB);
     if (whole < n) {  // some threads' columns lie past the end: zeros on both sides
@@ -479,7 +487,7 @@ __device__ __forceinline__ void multiply_tiles(float (&acc)[2][B::NT][4], uint32
 }
 
 template <class B, int TERMS>
-__device__ __forceinline__ void multiply(float (&acc)[2][B::NT][4], uint32_t (&nan)[2], const uint8_t* A,
+__device__ __forceinline__ void multiply(float (&acc)[B::CH][B::NT][4], uint32_t (&nan)[2], const uint8_t* A,
                                          const uint8_t* X, int pitch, int count, int n, bool mx, int lane) {
     if (B::NT == 1 || count <= 8)
         multiply_tiles<B, 1, TERMS>(acc, nan, A, X, pitch, count, n, mx, lane);
@@ -487,9 +495,9 @@ __device__ __forceinline__ void multiply(float (&acc)[2][B::NT][4], uint32_t (&n
         multiply_tiles<B, B::NT, TERMS>(acc, nan, A, X, pitch, count, n, mx, lane);
 }
 
-// the two sets of sums as one (in acc[0]); a weight row with a NaN code is NaN for every token
+// the sets of sums as one (in acc[0]); a weight row with a NaN code is NaN for every token
 template <class B>
-__device__ __forceinline__ void join(float (&acc)[2][B::NT][4], const uint32_t (&nan)[2]) {
+__device__ __forceinline__ void join(float (&acc)[B::CH][B::NT][4], const uint32_t (&nan)[2]) {
     bool bad[2] = {false, false};
     if (B::MX) {
         bad[0] = row_has_nan(nan[0]);
@@ -498,7 +506,11 @@ __device__ __forceinline__ void join(float (&acc)[2][B::NT][4], const uint32_t (
 #pragma unroll
     for (int t = 0; t < B::NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[0][t][i] = bad[i >> 1] ? __uint_as_float(0x7fffffffu) : acc[0][t][i] + acc[1][t][i];
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int c = 1; c < B::CH; ++c) acc[0][t][i] += acc[c][t][i];
+            if (bad[i >> 1]) acc[0][t][i] = __uint_as_float(0x7fffffffu);
+        }
 }
 
 // The rings' barriers, and the round (use) that each slot was last filled for. A barrier's
@@ -507,6 +519,7 @@ __device__ __forceinline__ void join(float (&acc)[2][B::NT][4], const uint32_t (
 struct Bars {
     uint64_t full[kSlots], empty[kSlots], tfull[kTokenSlots], tempty[kTokenSlots];
     int filled[kSlots], tfilled[kTokenSlots];
+    int met;  // 1 once the blocks have met: one thread of a block asks global memory
 };
 
 __device__ __forceinline__ int round_of(const int* p) {
@@ -517,7 +530,7 @@ __device__ __forceinline__ int round_of(const int* p) {
 __device__ __forceinline__ void set_round(int* p, int v) {
     asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
 }
-// waits for phase `round` of bar, whose slot was or will be filled for that round (bounded like mbar_wait)
+// waits for phase `round` of bar (if any), whose slot was or will be filled for that round; bounded like mbar_wait
 __device__ __forceinline__ void wait_round(const int* filled, uint64_t* bar, int round, volatile int* abort, int* status) {
     if (round_of(filled) != round) {
         const uint64_t t0 = globaltimer_ns();
@@ -530,7 +543,7 @@ __device__ __forceinline__ void wait_round(const int* filled, uint64_t* bar, int
             }
         }
     }
-    mbar_wait(bar, uint32_t(round) & 1, abort, status);
+    if (bar) mbar_wait(bar, uint32_t(round) & 1, abort, status);
 }
 
 // the word of scale codes at c (any alignment), of which those below `end` are wanted
@@ -638,7 +651,7 @@ struct Producer {
         if (lane < count) bulk_load(tokens + tslot * a.token_slot_bytes + lane * pitch, src, bytes, bar);
     }
 
-    __device__ __forceinline__ void run(unsigned before) {
+    __device__ __forceinline__ void run() {
         static_assert(B::CAP <= 32, "a lane copies a row");
         for (Tiles w(p); w.more(p); w.next(p)) {
             const Group gr = tb.groups[w.g];
@@ -671,7 +684,7 @@ struct Producer {
             const int k0 = w.c * kc, n = min(kc, a.I - k0);
             if (mine()) {
                 if (!met) {  // the activations are there once the blocks have met
-                    if (lane == 0) grid_wait(a.barrier, before, a.status);
+                    wait_round(&bars->met, nullptr, 1, abort, a.status);
                     __syncwarp();
                     asm volatile("fence.proxy.async;" ::: "memory");
                     met = true;
@@ -761,7 +774,7 @@ struct Consumer {
             const Group gr = tb.groups[w.g];
             const bool mx = B::MX && gr.expert < a.E;
             const int kc = B::columns(mx), pitch = B::token_pitch(kc, 1);
-            float acc[2][B::NT][4] = {};
+            float acc[B::CH][B::NT][4] = {};
             uint32_t nan[2] = {0, 0};
             for (int k0 = 0; k0 < a.H; k0 += kc)
                 step(warp, w.size, [&](const uint8_t* A, const uint8_t* X) {
@@ -850,7 +863,7 @@ struct Consumer {
             const Group gr = tb.groups[g];
             const bool mx = B::MX && gr.expert < a.E;
             const int kc = B::columns(mx), pitch = B::token_pitch(kc, 2);
-            float acc[2][B::NT][4] = {};
+            float acc[B::CH][B::NT][4] = {};
             uint32_t nan[2] = {0, 0};
             do {
                 step(warp - w.lo, w.hi - w.lo, [&](const uint8_t* A, const uint8_t* X) {
@@ -903,7 +916,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
         }
         fence_mbar_init();
     }
-    if (tid == 0) *s_abort = 0;
+    if (tid == 0) {
+        *s_abort = 0;
+        bars->met = 0;
+    }
     for (int i = tid; i < kConsumers * a.T * 16; i += kDecodeThreads) s_out[i] = 0.0f;
     sort_routes<B::CAP>(a, tb, tokens, id, prob);  // its scratch: the rings' space
     fence_proxy_async_smem();
@@ -915,22 +931,22 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
     }
     const Plan p = make_plan(a, tb);
     if (warp >= kConsumers) {
-        Producer<B>{a, tb, p, ring, tokens, bars, s_abort, warp - kConsumers, lane}.run(before);
+        Producer<B>{a, tb, p, ring, tokens, bars, s_abort, warp - kConsumers, lane}.run();
         return;
     }
     Consumer<B> c{a, tb, p, ring, tokens, bars, s_abort, s_out + warp * a.T * 16, warp, lane};
     if (a.gate_w) c.gates();
     c.first();
     // the blocks meet: every activation and gate is written
-    __threadfence();
-    asm volatile("fence.proxy.async;" ::: "memory");  // the activations are read by bulk copies
+    asm volatile("fence.proxy.async.global;" ::: "memory");  // the activations are read by bulk copies
     consumer_sync();
     if (tid == 0) {
         __threadfence();
         atomicAdd(a.barrier, blockIdx.x == 0 ? 0x80000000u - (gridDim.x - 1) : 1u);
+        grid_wait(a.barrier, before, a.status);
+        set_round(&bars->met, 1);
     }
     if (a.gate_w) {
-        if (tid == 0) grid_wait(a.barrier, before, a.status);
         consumer_sync();
         for (int t = tid; t < a.T; t += 32 * kConsumers) tb.coef[t] = __ldcg(a.gate + t);
         consumer_sync();
