@@ -27,12 +27,17 @@
 // row, which are the operands of two instructions if the sum's index is taken in that
 // order. Tensor rate is not what limits it (8 tokens a weight at most, most often one).
 // The activations a = silu(g) u go to the second product as two bf16 terms, hi + lo.
-// MXFP8 weights become bf16 in registers (exact) and their block scales multiply
-// the fp32 sums of 32 columns.
+// MXFP8 weights become f16 in registers (exact, one instruction a pair; bf16 takes
+// four) and their block scales multiply the fp32 sums of 32 columns. Their tokens are
+// f16 too: a slice of a token's row is scaled by the power of two that brings its
+// largest value under 2^15, so that x (8 significant bits) fits one f16 term and a two, with
+// an error of at most 2^-38 of the slice's largest value, and the scale is taken back per slot.
 #include <algorithm>
 #include <cmath>
 #include <memory>
 #include <new>
+
+#include <cuda_fp16.h>
 
 #include "../../include/moe.h"
 #include "device_common.cuh"
@@ -80,8 +85,10 @@ struct DecodeArgs {
     __nv_bfloat16* out;
     int64_t os;
     DecodeWeight w[W_COUNT];
-    __nv_bfloat16* acts;      // by position (below): [chunks of I][2][chunk]: the activations' two terms
-    int act_row;              // elements of a position
+    // the activations by position (below): bf16 routed weights: [chunks of I][2][chunk], their two bf16
+    // terms; MXFP8 ones: [I] fp32
+    void* acts;
+    int act_row;              // 4-byte words of a position
     float* gate;              // [T]
     float* part;              // [blocks][2][8][T][16]: partial sums of shared sets of row tiles
     unsigned* counters;       // per row tile: blocks done with it; 0 between launches
@@ -116,6 +123,8 @@ struct Build {
     static __host__ __device__ constexpr int columns(bool mx) { return MX && mx ? KC : KB; }
     // pitch of a token row of `terms` terms of kc columns
     static __host__ __device__ constexpr int token_pitch(int kc, int terms) { return 2 * kc * terms + 64; }
+    static constexpr int TS = MX ? 128 : 0;     // a token slot starts with its tokens' scales
+    static_assert(4 * CAP <= 128, "the scales fit");
 };
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes, uint64_t* bar) {
@@ -125,13 +134,21 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes,
                  : "memory");
 }
 
+template <bool F16>
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
-        "%2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+            "%2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
+            "%1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // 2^(code - 127) of an E8M0 code; 255 is NaN
@@ -139,30 +156,19 @@ __device__ __forceinline__ float e8m0_value(uint32_t code) {
     return code == 255u ? __uint_as_float(0x7fffffffu) : e8m0_scale(code);
 }
 
-// Four E4M3 codes -> two bf16 pairs, exact (4 significant bits), without the conversion
-// unit, which takes 16 values a cycle: a code's 7 magnitude bits under bf16's exponent are its
-// value times 2^-120 (subnormals included), so sign-extend each byte, shift it to its
-// place, keep sign and magnitude, multiply by 2^120.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t q, uint32_t select) {
-    uint32_t x;
-    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(x) : "r"(q), "r"(select));
-    x = (x << 4) & 0x87f087f0u;
-    const __nv_bfloat162 scale = __halves2bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));
-    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x), scale);
+// four E4M3 codes -> two f16 pairs (exact; NaN stays NaN)
+__device__ __forceinline__ void e4m3_to_f16(uint32_t q, uint32_t& lo, uint32_t& hi) {
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(q & 0xffffu), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(q >> 16), __NV_E4M3);
+    lo = uint32_t(a.x) | uint32_t(a.y) << 16;
+    hi = uint32_t(b.x) | uint32_t(b.y) << 16;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// The NaN codes (0x7F, 0xFF) come out as +-480: they alone carry into a byte's top bit when 1
-// is added to the magnitude, which `nan` collects.
-__device__ __forceinline__ void e4m3_to_bf16(uint32_t q, uint32_t& lo, uint32_t& hi, uint32_t& nan) {
-    nan |= (q & 0x7f7f7f7fu) + 0x01010101u;
-    lo = e4m3_pair(q, 0x9180u);
-    hi = e4m3_pair(q, 0xB3A2u);
-}
-// the sums of a weight row (spread over four lanes) with a NaN code in it are NaN for every token
-__device__ __forceinline__ bool row_has_nan(uint32_t nan) {
-    const unsigned m = __ballot_sync(0xffffffffu, (nan & 0x80808080u) != 0);
-    return (m >> (threadIdx.x & 28)) & 15u;
-}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory"); }
 
@@ -400,7 +406,7 @@ struct Steps {
 // 8 N tokens, whose elements start at px[t] (`there`: this thread's token exists). Two sets of
 // sums keep two chains of instructions going: of the two halves of the step, or with TERMS 2
 // of the two terms of a token's row, which lie `gap` bytes apart.
-template <int N, int TERMS>
+template <bool F16, int N, int TERMS>
 __device__ __forceinline__ void k_step(float (*acc0)[4], float (*acc1)[4], const uint4& wa, const uint4& wb,
                                        const uint8_t* const (&px)[N], const bool (&there)[N], int k2, int gap) {
 #pragma unroll
@@ -411,14 +417,14 @@ __device__ __forceinline__ void k_step(float (*acc0)[4], float (*acc1)[4], const
             if (!there[t]) x = make_uint4(0, 0, 0, 0);
             float(&d0)[4] = term == 0 ? acc0[t] : acc1[t];
             float(&d1)[4] = term == 0 && TERMS == 2 ? acc0[t] : acc1[t];
-            mma_16816(d0, wa.x, wb.x, wa.y, wb.y, x.x, x.y);
-            mma_16816(d1, wa.z, wb.z, wa.w, wb.w, x.z, x.w);
+            mma_16816<F16>(d0, wa.x, wb.x, wa.y, wb.y, x.x, x.y);
+            mma_16816<F16>(d1, wa.z, wb.z, wa.w, wb.w, x.z, x.w);
         }
 }
 
 // acc += (16 weight rows at A) x (N tiles of 8 tokens at X), over n columns of a slot
 template <class B, int N, int TERMS>
-__device__ __forceinline__ void multiply_tiles(float (&acc)[B::CH][B::NT][4], uint32_t (&nan)[2], const uint8_t* A,
+__device__ __forceinline__ void multiply_tiles(float (&acc)[B::CH][B::NT][4], const uint8_t* A,
                                                const uint8_t* X, int pitch, int count, int n, bool mx, int lane) {
     const int r = lane >> 2, c8 = (lane & 3) * 8;
     const uint8_t* px[N];
@@ -430,6 +436,7 @@ __device__ __forceinline__ void multiply_tiles(float (&acc)[B::CH][B::NT][4], ui
     }
     if (B::MX && mx) {
         const uint8_t *pa = A + r * B::P8 + c8, *S = A + B::SCALES + r * B::PS;
+        float sum[2][N][4] = {};  // of this slot, in the tokens' scales
         for (int k4 = 0; k4 < n; k4 += 128) {  // n is a multiple of 32
             const float4 sa4 = *reinterpret_cast<const float4*>(S + k4 / 8);
             const float4 sb4 = *reinterpret_cast<const float4*>(S + 8 * B::PS + k4 / 8);
@@ -441,24 +448,29 @@ __device__ __forceinline__ void multiply_tiles(float (&acc)[B::CH][B::NT][4], ui
                 const uint2 qa = *reinterpret_cast<const uint2*>(pa + k);
                 const uint2 qb = *reinterpret_cast<const uint2*>(pa + 8 * B::P8 + k);
                 uint4 wa, wb;
-                e4m3_to_bf16(qa.x, wa.x, wa.y, nan[0]);
-                e4m3_to_bf16(qa.y, wa.z, wa.w, nan[0]);
-                e4m3_to_bf16(qb.x, wb.x, wb.y, nan[1]);
-                e4m3_to_bf16(qb.y, wb.z, wb.w, nan[1]);
+                e4m3_to_f16(qa.x, wa.x, wa.y);
+                e4m3_to_f16(qa.y, wa.z, wa.w);
+                e4m3_to_f16(qb.x, wb.x, wb.y);
+                e4m3_to_f16(qb.y, wb.z, wb.w);
                 float d[2][N][4] = {};
-                k_step<N, TERMS>(d[0], d[1], wa, wb, px, there, 2 * k, 2 * B::KC);
+                k_step<true, N, TERMS>(d[0], d[1], wa, wb, px, there, 2 * k, 2 * B::KC);
 #pragma unroll
-                for (int t = 0; t < N; ++t) {
-                    acc[0][t][0] = fmaf(sa[j], d[0][t][0], acc[0][t][0]);
-                    acc[0][t][1] = fmaf(sa[j], d[0][t][1], acc[0][t][1]);
-                    acc[0][t][2] = fmaf(sb[j], d[0][t][2], acc[0][t][2]);
-                    acc[0][t][3] = fmaf(sb[j], d[0][t][3], acc[0][t][3]);
-                    acc[1][t][0] = fmaf(sa[j], d[1][t][0], acc[1][t][0]);
-                    acc[1][t][1] = fmaf(sa[j], d[1][t][1], acc[1][t][1]);
-                    acc[1][t][2] = fmaf(sb[j], d[1][t][2], acc[1][t][2]);
-                    acc[1][t][3] = fmaf(sb[j], d[1][t][3], acc[1][t][3]);
-                }
+                for (int t = 0; t < N; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        sum[h][t][0] = fmaf(sa[j], d[h][t][0], sum[h][t][0]);
+                        sum[h][t][1] = fmaf(sa[j], d[h][t][1], sum[h][t][1]);
+                        sum[h][t][2] = fmaf(sb[j], d[h][t][2], sum[h][t][2]);
+                        sum[h][t][3] = fmaf(sb[j], d[h][t][3], sum[h][t][3]);
+                    }
             }
+        }
+        const float* scale = reinterpret_cast<const float*>(X - B::TS) + 2 * (lane & 3);  // of this thread's tokens
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+            const float2 f = *reinterpret_cast<const float2*>(scale + 8 * t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[0][t][i] = fmaf(i & 1 ? f.y : f.x, sum[0][t][i] + sum[1][t][i], acc[0][t][i]);
         }
         return;
     }
@@ -468,12 +480,12 @@ __device__ __forceinline__ void multiply_tiles(float (&acc)[B::CH][B::NT][4], ui
     for (; k + 128 <= n; k += 128)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            k_step<N, TERMS>(acc[2 * j % B::CH], acc[(2 * j + 1) % B::CH],
+            k_step<false, N, TERMS>(acc[2 * j % B::CH], acc[(2 * j + 1) % B::CH],
                              *reinterpret_cast<const uint4*>(pa + 2 * (k + 32 * j)),
                              *reinterpret_cast<const uint4*>(pa + 8 * B::P16 + 2 * (k + 32 * j)), px, there,
                              2 * (k + 32 * j), 2 * B::KB);
     for (; k < whole; k += 32)
-        k_step<N, TERMS>(acc[0], acc[1], *reinterpret_cast<const uint4*>(pa + 2 * k),
+        k_step<false, N, TERMS>(acc[0], acc[1], *reinterpret_cast<const uint4*>(pa + 2 * k),
                          *reinterpret_cast<const uint4*>(pa + 8 * B::P16 + 2 * k), px, there, 2 * k, 2 * B::KB);
     if (whole < n) {  // some threads' columns lie past the end: zeros on both sides
         const bool in = whole + c8 < n;
@@ -482,35 +494,28 @@ __device__ __forceinline__ void multiply_tiles(float (&acc)[B::CH][B::NT][4], ui
         if (!in) wa = wb = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int t = 0; t < N; ++t) there[t] &= in;
-        k_step<N, TERMS>(acc[0], acc[1], wa, wb, px, there, k2, 2 * B::KB);
+        k_step<false, N, TERMS>(acc[0], acc[1], wa, wb, px, there, k2, 2 * B::KB);
     }
 }
 
 template <class B, int TERMS>
-__device__ __forceinline__ void multiply(float (&acc)[B::CH][B::NT][4], uint32_t (&nan)[2], const uint8_t* A,
+__device__ __forceinline__ void multiply(float (&acc)[B::CH][B::NT][4], const uint8_t* A,
                                          const uint8_t* X, int pitch, int count, int n, bool mx, int lane) {
     if (B::NT == 1 || count <= 8)
-        multiply_tiles<B, 1, TERMS>(acc, nan, A, X, pitch, count, n, mx, lane);
+        multiply_tiles<B, 1, TERMS>(acc, A, X, pitch, count, n, mx, lane);
     else
-        multiply_tiles<B, B::NT, TERMS>(acc, nan, A, X, pitch, count, n, mx, lane);
+        multiply_tiles<B, B::NT, TERMS>(acc, A, X, pitch, count, n, mx, lane);
 }
 
-// the sets of sums as one (in acc[0]); a weight row with a NaN code is NaN for every token
+// the sets of sums as one, in acc[0]
 template <class B>
-__device__ __forceinline__ void join(float (&acc)[B::CH][B::NT][4], const uint32_t (&nan)[2]) {
-    bool bad[2] = {false, false};
-    if (B::MX) {
-        bad[0] = row_has_nan(nan[0]);
-        bad[1] = row_has_nan(nan[1]);
-    }
+__device__ __forceinline__ void join(float (&acc)[B::CH][B::NT][4]) {
 #pragma unroll
     for (int t = 0; t < B::NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 1; c < B::CH; ++c) acc[0][t][i] += acc[c][t][i];
-            if (bad[i >> 1]) acc[0][t][i] = __uint_as_float(0x7fffffffu);
-        }
 }
 
 // The rings' barriers, and the round (use) that each slot was last filled for. A barrier's
@@ -639,16 +644,77 @@ struct Producer {
             if (lane == 0) mbar_arrive(bar);  // the scales are there
         }
     }
-    // this lane's token row (if it has one) into the next token slot
-    __device__ __forceinline__ void token_rows(int count, const __nv_bfloat16* src, int pitch, int bytes) {
+    // the next token slot, free; null after a wait that gave up
+    __device__ __forceinline__ uint8_t* token_slot() {
         if (tround) wait_round(bars->tfilled + tslot, bars->tempty + tslot, tround - 1, abort, a.status);
-        if (*abort) return;
+        if (*abort) return nullptr;
         __syncwarp();
         if (lane == 0) set_round(bars->tfilled + tslot, tround);
+        return tokens + tslot * a.token_slot_bytes;
+    }
+    // this lane's token row (if it has one) into the next token slot, as it is
+    __device__ __forceinline__ void token_rows(int count, const void* src, int pitch, int bytes) {
+        uint8_t* to = token_slot();
+        if (to == nullptr) return;
         uint64_t* bar = bars->tfull + tslot;
+        if (B::MX) fence_proxy_async_smem();  // copies may land where converted rows were written
         if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(count * bytes));
         __syncwarp();
-        if (lane < count) bulk_load(tokens + tslot * a.token_slot_bytes + lane * pitch, src, bytes, bar);
+        if (lane < count) bulk_load(to + B::TS + lane * pitch, src, bytes, bar);
+    }
+    // MXFP8: n columns of `count` rows into the next token slot as TERMS terms of f16 under a scale,
+    // or (not F16) of bf16; load(r, c, v): 8 values of row r from column c
+    template <bool F16, int TERMS, typename F>
+    __device__ __forceinline__ void token_values(int count, int kc, int n, F load) {
+        uint8_t* to = token_slot();
+        if (to == nullptr) return;
+        constexpr int V = B::KC / 256;  // 8-column pieces of a lane
+        const int pitch = B::token_pitch(kc, TERMS);
+        for (int r = 0; r < count; ++r) {
+            float v[V][8], top = 0.0f;
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const int c = (q * 32 + lane) * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[q][i] = 0.0f;
+                if (c < n) load(r, c, v[q]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[q][i]));  // fmaxf passes over NaN
+            }
+            float mul = 1.0f;
+            if (F16) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int e = max(-113, min(126, 141 - int(__float_as_uint(top) >> 23)));  // top 2^e < 2^15
+                mul = __uint_as_float(uint32_t(127 + e) << 23);
+                if (lane == 0) reinterpret_cast<float*>(to)[r] = __uint_as_float(uint32_t(127 - e) << 23);
+            }
+            uint8_t* row = to + B::TS + r * pitch;
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const int c = (q * 32 + lane) * 8;
+                if (c >= n) continue;
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x0 = v[q][2 * i] * mul, x1 = v[q][2 * i + 1] * mul;
+                    if (F16) {
+                        hi[i] = pack_f16x2(x0, x1);
+                        const float2 h = unpack_f16x2(hi[i]);
+                        lo[i] = pack_f16x2(x0 - h.x, x1 - h.y);
+                    } else {
+                        hi[i] = pack_bf16x2(x0, x1);
+                        float h0, h1;
+                        unpack_bf16x2(hi[i], h0, h1);
+                        lo[i] = pack_bf16x2(x0 - h0, x1 - h1);
+                    }
+                }
+                *reinterpret_cast<uint4*>(row + 2 * c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                if (TERMS == 2) *reinterpret_cast<uint4*>(row + 2 * (kc + c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars->tfull + tslot);
     }
 
     __device__ __forceinline__ void run() {
@@ -663,7 +729,18 @@ struct Producer {
             const __nv_bfloat16* x = a.x + (lane < gr.count ? tb.tok[gr.start + lane] : 0) * a.xs;
             for (int k0 = 0; k0 < a.H; k0 += kc) {
                 const int n = min(kc, a.H - k0);
-                if (mine()) token_rows(gr.count, x + k0, B::token_pitch(kc, 1), 2 * n);
+                if (mine()) {
+                    if (mx)
+                        token_values<true, 1>(gr.count, kc, n, [&](int r, int c, float (&v)[8]) {
+                            const uint4 q = __ldg(reinterpret_cast<const uint4*>(a.x + tb.tok[gr.start + r] * a.xs + k0 + c));
+                            unpack_bf16x2(q.x, v[0], v[1]);
+                            unpack_bf16x2(q.y, v[2], v[3]);
+                            unpack_bf16x2(q.z, v[4], v[5]);
+                            unpack_bf16x2(q.w, v[6], v[7]);
+                        });
+                    else
+                        token_rows(gr.count, x + k0, B::token_pitch(kc, 1), 2 * n);
+                }
                 next_token_slot();
                 for (int q = 0; q < w.size; ++q, next_slot()) {
                     if (!mine()) continue;
@@ -689,7 +766,19 @@ struct Producer {
                     asm volatile("fence.proxy.async;" ::: "memory");
                     met = true;
                 }
-                token_rows(gr.count, a.acts + int64_t(gr.start + lane) * a.act_row + 2 * k0, B::token_pitch(kc, 2), 2 * (kc + n));
+                const float* act = static_cast<const float*>(a.acts) + int64_t(gr.start) * a.act_row + k0;
+                auto load = [&](int r, int c, float (&v)[8]) {
+                    const float4* f = reinterpret_cast<const float4*>(act + int64_t(r) * a.act_row + c);
+                    const float4 lo = __ldcg(f), hi = __ldcg(f + 1);
+                    v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+                    v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+                };
+                if (!B::MX)  // two bf16 terms of a chunk take the chunk's words
+                    token_rows(gr.count, act + int64_t(lane) * a.act_row, B::token_pitch(kc, 2), 2 * (kc + n));
+                else if (mx)
+                    token_values<true, 2>(gr.count, kc, n, load);
+                else
+                    token_values<false, 2>(gr.count, kc, n, load);
             }
             next_token_slot();
             const uint8_t* base = wd.expert(e);
@@ -733,7 +822,7 @@ struct Consumer {
                 ++r;
             }
             wait_round(bars->filled + s, bars->full + s, r, abort, a.status);
-            f(ring + s * B::SLOT, tokens + tslot * a.token_slot_bytes);
+            f(ring + s * B::SLOT, tokens + tslot * a.token_slot_bytes + B::TS);
             __syncwarp();
             if (lane == 0) mbar_arrive(bars->empty + s);
         }
@@ -775,13 +864,12 @@ struct Consumer {
             const bool mx = B::MX && gr.expert < a.E;
             const int kc = B::columns(mx), pitch = B::token_pitch(kc, 1);
             float acc[B::CH][B::NT][4] = {};
-            uint32_t nan[2] = {0, 0};
             for (int k0 = 0; k0 < a.H; k0 += kc)
                 step(warp, w.size, [&](const uint8_t* A, const uint8_t* X) {
-                    multiply<B, 1>(acc, nan, A, X, pitch, gr.count, min(kc, a.H - k0), mx, lane);
+                    multiply<B, 1>(acc, A, X, pitch, gr.count, min(kc, a.H - k0), mx, lane);
                 });
             if (warp >= w.size) continue;
-            join<B>(acc, nan);
+            join<B>(acc);
             const int i = (w.tile + warp) * 8 + (lane >> 2);
             if (i >= a.I) continue;
             // this thread has g and u of row i for tokens 8 t + 2 (lane & 3), and the next
@@ -797,10 +885,15 @@ struct Consumer {
                         u = u > a.limit ? a.limit : u < -a.limit ? -a.limit : u;
                     }
                     const float v = g * sigmoidf_(g) * u;
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                    __nv_bfloat16* d = a.acts + int64_t(gr.start + n) * a.act_row + i / kc * (2 * kc) + i % kc;
-                    d[0] = hi;
-                    d[kc] = __float2bfloat16_rn(v - __bfloat162float(hi));
+                    float* row = static_cast<float*>(a.acts) + int64_t(gr.start + n) * a.act_row;
+                    if (B::MX) {
+                        row[i] = v;
+                    } else {
+                        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+                        __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(row + i / kc * kc) + i % kc;
+                        d[0] = hi;
+                        d[kc] = __float2bfloat16_rn(v - __bfloat162float(hi));
+                    }
                 }
         }
     }
@@ -864,14 +957,13 @@ struct Consumer {
             const bool mx = B::MX && gr.expert < a.E;
             const int kc = B::columns(mx), pitch = B::token_pitch(kc, 2);
             float acc[B::CH][B::NT][4] = {};
-            uint32_t nan[2] = {0, 0};
             do {
                 step(warp - w.lo, w.hi - w.lo, [&](const uint8_t* A, const uint8_t* X) {
-                    multiply<B, 2>(acc, nan, A, X, pitch, gr.count, min(kc, a.I - w.c * kc), mx, lane);
+                    multiply<B, 2>(acc, A, X, pitch, gr.count, min(kc, a.I - w.c * kc), mx, lane);
                 });
                 w.next(p, tb.n_groups);
             } while (w.more(p) && w.g == g && w.set == set);
-            join<B>(acc, nan);
+            join<B>(acc);
 #pragma unroll
             for (int t = 0; t < B::NT; ++t)
 #pragma unroll
@@ -985,7 +1077,7 @@ struct DecodeSpace {
     unsigned* state;      // [0] status, [1] barrier, then the row tiles' counters
     const void** tables;  // [3][2][E]: gate, up, down: payloads, scales
     float* gate;
-    __nv_bfloat16* acts;
+    void* acts;
     float* part;
 };
 
@@ -1002,7 +1094,7 @@ size_t carve_decode(const DecodeShape& s, uint8_t* base, DecodeSpace* w) {
     w->state = reinterpret_cast<unsigned*>(take(state_words(s) * sizeof(unsigned)));
     w->tables = reinterpret_cast<const void**>(take(6 * size_t(s.E) * sizeof(void*)));
     w->gate = reinterpret_cast<float*>(take(T * sizeof(float)));
-    w->acts = reinterpret_cast<__nv_bfloat16*>(take(T * size_t(s.k + 1) * chunks * 2 * 1024 * sizeof(__nv_bfloat16)));
+    w->acts = take(T * size_t(s.k + 1) * chunks * 1024 * sizeof(float));
     w->part = reinterpret_cast<float*>(take(size_t(kMaxBlocks) * 2 * kConsumers * T * 16 * sizeof(float)));
     return off;
 }
@@ -1089,13 +1181,13 @@ cudaError_t launch_decode(DecodeArgs& a, int blocks, cudaStream_t st) {
     a.tokens_off = up(int(sizeof(Bars)) + 16 + a.max_groups * int(sizeof(Group)) + (R + a.T) * 8 +
                       kConsumers * a.T * 16 * int(sizeof(float)));
     // the tokens' ring: about 48 KB, two slots at least
-    a.token_slot_bytes = up(cap * B::token_pitch(B::KC, 2));
+    a.token_slot_bytes = up(B::TS + cap * B::token_pitch(B::KC, 2));
     a.token_slots = std::min(kTokenSlots, std::max(2, 49152 / a.token_slot_bytes));
     a.ring_off = a.tokens_off + a.token_slots * a.token_slot_bytes;
     a.slots = std::min(kSlots, (kSmemMax - a.ring_off) / B::SLOT);
     const int scratch = 12 * a.E + 8 + 4 * R + 160;
     if (a.slots < kConsumers || a.tokens_off + scratch > kSmemMax) return cudaErrorInvalidConfiguration;
-    a.act_row = 2 * ((a.I + 1023) / 1024 * 1024);
+    a.act_row = (a.I + 1023) / 1024 * 1024;
     auto chunks = [](int n, bool mx) { return (n + B::columns(mx) - 1) / B::columns(mx); };
     a.c1_shared = chunks(a.H, false);
     a.c2_shared = chunks(a.I, false);
