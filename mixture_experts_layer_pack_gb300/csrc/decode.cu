@@ -123,6 +123,7 @@ struct Build {
     static __host__ __device__ constexpr int columns(bool mx) { return MX && mx ? KC : KB; }
     // pitch of a token row of `terms` terms of kc columns
     static __host__ __device__ constexpr int token_pitch(int kc, int terms) { return 2 * kc * terms + 64; }
+    static constexpr int ZEROS = 4 * KC;        // a token row of zeros, two terms
     static constexpr int TS = MX ? 128 : 0;     // a token slot starts with its tokens' scales
     static_assert(4 * CAP <= 128, "the scales fit");
 };
@@ -134,21 +135,22 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes,
                  : "memory");
 }
 
+// d = a b + c on 16 x 16 weights and 16 x 8 tokens
 template <bool F16>
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
+                                          uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
     if (F16)
         asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
-            "%2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, "
+            "%12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     else
         asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
-            "%1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, "
+            "%11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // 2^(code - 127) of an E8M0 code; 255 is NaN
@@ -158,10 +160,12 @@ __device__ __forceinline__ float e8m0_value(uint32_t code) {
 
 // four E4M3 codes -> two f16 pairs (exact; NaN stays NaN)
 __device__ __forceinline__ void e4m3_to_f16(uint32_t q, uint32_t& lo, uint32_t& hi) {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(q & 0xffffu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(q >> 16), __NV_E4M3);
-    lo = uint32_t(a.x) | uint32_t(a.y) << 16;
-    hi = uint32_t(b.x) | uint32_t(b.y) << 16;
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(q));
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -402,69 +406,74 @@ struct Steps {
     }
 };
 
-// One k-step: the 16 x 32 weights (wa: row r, wb: row r + 8, 8 elements each) times up to
-// 8 N tokens, whose elements start at px[t] (`there`: this thread's token exists). Two sets of
-// sums keep two chains of instructions going: of the two halves of the step, or with TERMS 2
-// of the two terms of a token's row, which lie `gap` bytes apart.
-template <bool F16, int N, int TERMS>
+// One k-step: the 16 x 32 weights (wa: row r, wb: row r + 8, 8 elements each) times 8 N tokens,
+// whose elements start at px[t]. Two sets of sums keep two chains of instructions going: of
+// the two halves of the step, or with TERMS 2 of the two terms of a token's row, which lie
+// `gap` bytes apart. ZERO: the sums start from zero here.
+template <bool F16, bool ZERO, int N, int TERMS>
 __device__ __forceinline__ void k_step(float (*acc0)[4], float (*acc1)[4], const uint4& wa, const uint4& wb,
-                                       const uint8_t* const (&px)[N], const bool (&there)[N], int k2, int gap) {
+                                       const uint8_t* const (&px)[N], int k2, int gap) {
 #pragma unroll
     for (int t = 0; t < N; ++t)
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
-            uint4 x = *reinterpret_cast<const uint4*>(px[t] + k2 + term * gap);
-            if (!there[t]) x = make_uint4(0, 0, 0, 0);
+            const uint4 x = *reinterpret_cast<const uint4*>(px[t] + k2 + term * gap);
             float(&d0)[4] = term == 0 ? acc0[t] : acc1[t];
             float(&d1)[4] = term == 0 && TERMS == 2 ? acc0[t] : acc1[t];
-            mma_16816<F16>(d0, wa.x, wb.x, wa.y, wb.y, x.x, x.y);
-            mma_16816<F16>(d1, wa.z, wb.z, wa.w, wb.w, x.z, x.w);
+            if (ZERO)
+                mma_16816<F16>(d0, wa.x, wb.x, wa.y, wb.y, x.x, x.y, 0.0f, 0.0f, 0.0f, 0.0f);
+            else
+                mma_16816<F16>(d0, wa.x, wb.x, wa.y, wb.y, x.x, x.y, d0[0], d0[1], d0[2], d0[3]);
+            if (ZERO && TERMS == 1)
+                mma_16816<F16>(d1, wa.z, wb.z, wa.w, wb.w, x.z, x.w, 0.0f, 0.0f, 0.0f, 0.0f);
+            else
+                mma_16816<F16>(d1, wa.z, wb.z, wa.w, wb.w, x.z, x.w, d1[0], d1[1], d1[2], d1[3]);
         }
 }
 
-// acc += (16 weight rows at A) x (N tiles of 8 tokens at X), over n columns of a slot
+// acc += (16 weight rows at A) x (N tiles of 8 tokens at X), over n columns of a slot; `none`
+// holds a row of zeros, for the tokens that a tile lacks
 template <class B, int N, int TERMS>
-__device__ __forceinline__ void multiply_tiles(float (&acc)[B::CH][B::NT][4], const uint8_t* A,
-                                               const uint8_t* X, int pitch, int count, int n, bool mx, int lane) {
+__device__ __forceinline__ void multiply_tiles(float (&acc)[B::CH][B::NT][4], const uint8_t* A, const uint8_t* X,
+                                               const uint8_t* none, int pitch, int count, int n, bool mx, int lane) {
     const int r = lane >> 2, c8 = (lane & 3) * 8;
     const uint8_t* px[N];
-    bool there[N];
 #pragma unroll
-    for (int t = 0; t < N; ++t) {
-        there[t] = 8 * t + r < count;
-        px[t] = X + (there[t] ? 8 * t + r : 0) * pitch + 2 * c8;
-    }
+    for (int t = 0; t < N; ++t) px[t] = (8 * t + r < count ? X + (8 * t + r) * pitch : none) + 2 * c8;
     if (B::MX && mx) {
         const uint8_t *pa = A + r * B::P8 + c8, *S = A + B::SCALES + r * B::PS;
         float sum[2][N][4] = {};  // of this slot, in the tokens' scales
-        for (int k4 = 0; k4 < n; k4 += 128) {  // n is a multiple of 32
-            const float4 sa4 = *reinterpret_cast<const float4*>(S + k4 / 8);
-            const float4 sb4 = *reinterpret_cast<const float4*>(S + 8 * B::PS + k4 / 8);
-            const float sa[4] = {sa4.x, sa4.y, sa4.z, sa4.w}, sb[4] = {sb4.x, sb4.y, sb4.z, sb4.w};
+        auto step = [&](int k, float sa, float sb) {
+            const uint2 qa = *reinterpret_cast<const uint2*>(pa + k);
+            const uint2 qb = *reinterpret_cast<const uint2*>(pa + 8 * B::P8 + k);
+            uint4 wa, wb;
+            e4m3_to_f16(qa.x, wa.x, wa.y);
+            e4m3_to_f16(qa.y, wa.z, wa.w);
+            e4m3_to_f16(qb.x, wb.x, wb.y);
+            e4m3_to_f16(qb.y, wb.z, wb.w);
+            float d[2][N][4];
+            k_step<true, true, N, TERMS>(d[0], d[1], wa, wb, px, 2 * k, 2 * B::KC);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = k4 + 32 * j;
-                if (k >= n) break;
-                const uint2 qa = *reinterpret_cast<const uint2*>(pa + k);
-                const uint2 qb = *reinterpret_cast<const uint2*>(pa + 8 * B::P8 + k);
-                uint4 wa, wb;
-                e4m3_to_f16(qa.x, wa.x, wa.y);
-                e4m3_to_f16(qa.y, wa.z, wa.w);
-                e4m3_to_f16(qb.x, wb.x, wb.y);
-                e4m3_to_f16(qb.y, wb.z, wb.w);
-                float d[2][N][4] = {};
-                k_step<true, N, TERMS>(d[0], d[1], wa, wb, px, there, 2 * k, 2 * B::KC);
+            for (int t = 0; t < N; ++t)
 #pragma unroll
-                for (int t = 0; t < N; ++t)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        sum[h][t][0] = fmaf(sa[j], d[h][t][0], sum[h][t][0]);
-                        sum[h][t][1] = fmaf(sa[j], d[h][t][1], sum[h][t][1]);
-                        sum[h][t][2] = fmaf(sb[j], d[h][t][2], sum[h][t][2]);
-                        sum[h][t][3] = fmaf(sb[j], d[h][t][3], sum[h][t][3]);
-                    }
-            }
+                for (int h = 0; h < 2; ++h) {
+                    sum[h][t][0] = fmaf(sa, d[h][t][0], sum[h][t][0]);
+                    sum[h][t][1] = fmaf(sa, d[h][t][1], sum[h][t][1]);
+                    sum[h][t][2] = fmaf(sb, d[h][t][2], sum[h][t][2]);
+                    sum[h][t][3] = fmaf(sb, d[h][t][3], sum[h][t][3]);
+                }
+        };
+        int k = 0;
+        for (; k + 128 <= n; k += 128) {  // four steps without a branch: with two warps a scheduler the loads have to overlap
+            const float4 sa = *reinterpret_cast<const float4*>(S + k / 8);
+            const float4 sb = *reinterpret_cast<const float4*>(S + 8 * B::PS + k / 8);
+            step(k, sa.x, sb.x);
+            step(k + 32, sa.y, sb.y);
+            step(k + 64, sa.z, sb.z);
+            step(k + 96, sa.w, sb.w);
         }
+        for (; k < n; k += 32)  // n is a multiple of 32
+            step(k, *reinterpret_cast<const float*>(S + k / 8), *reinterpret_cast<const float*>(S + 8 * B::PS + k / 8));
         const float* scale = reinterpret_cast<const float*>(X - B::TS) + 2 * (lane & 3);  // of this thread's tokens
 #pragma unroll
         for (int t = 0; t < N; ++t) {
@@ -480,31 +489,32 @@ __device__ __forceinline__ void multiply_tiles(float (&acc)[B::CH][B::NT][4], co
     for (; k + 128 <= n; k += 128)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            k_step<false, N, TERMS>(acc[2 * j % B::CH], acc[(2 * j + 1) % B::CH],
-                             *reinterpret_cast<const uint4*>(pa + 2 * (k + 32 * j)),
-                             *reinterpret_cast<const uint4*>(pa + 8 * B::P16 + 2 * (k + 32 * j)), px, there,
-                             2 * (k + 32 * j), 2 * B::KB);
+            k_step<false, false, N, TERMS>(acc[2 * j % B::CH], acc[(2 * j + 1) % B::CH],
+                                           *reinterpret_cast<const uint4*>(pa + 2 * (k + 32 * j)),
+                                           *reinterpret_cast<const uint4*>(pa + 8 * B::P16 + 2 * (k + 32 * j)), px,
+                                           2 * (k + 32 * j), 2 * B::KB);
     for (; k < whole; k += 32)
-        k_step<false, N, TERMS>(acc[0], acc[1], *reinterpret_cast<const uint4*>(pa + 2 * k),
-                         *reinterpret_cast<const uint4*>(pa + 8 * B::P16 + 2 * k), px, there, 2 * k, 2 * B::KB);
+        k_step<false, false, N, TERMS>(acc[0], acc[1], *reinterpret_cast<const uint4*>(pa + 2 * k),
+                                       *reinterpret_cast<const uint4*>(pa + 8 * B::P16 + 2 * k), px, 2 * k, 2 * B::KB);
     if (whole < n) {  // some threads' columns lie past the end: zeros on both sides
         const bool in = whole + c8 < n;
         const int k2 = in ? 2 * whole : 0;
         uint4 wa = *reinterpret_cast<const uint4*>(pa + k2), wb = *reinterpret_cast<const uint4*>(pa + 8 * B::P16 + k2);
         if (!in) wa = wb = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int t = 0; t < N; ++t) there[t] &= in;
-        k_step<false, N, TERMS>(acc[0], acc[1], wa, wb, px, there, k2, 2 * B::KB);
+        for (int t = 0; t < N; ++t)
+            if (!in) px[t] = none;
+        k_step<false, false, N, TERMS>(acc[0], acc[1], wa, wb, px, k2, 2 * B::KB);
     }
 }
 
 template <class B, int TERMS>
-__device__ __forceinline__ void multiply(float (&acc)[B::CH][B::NT][4], const uint8_t* A,
-                                         const uint8_t* X, int pitch, int count, int n, bool mx, int lane) {
+__device__ __forceinline__ void multiply(float (&acc)[B::CH][B::NT][4], const uint8_t* A, const uint8_t* X,
+                                         const uint8_t* none, int pitch, int count, int n, bool mx, int lane) {
     if (B::NT == 1 || count <= 8)
-        multiply_tiles<B, 1, TERMS>(acc, A, X, pitch, count, n, mx, lane);
+        multiply_tiles<B, 1, TERMS>(acc, A, X, none, pitch, count, n, mx, lane);
     else
-        multiply_tiles<B, B::NT, TERMS>(acc, A, X, pitch, count, n, mx, lane);
+        multiply_tiles<B, B::NT, TERMS>(acc, A, X, none, pitch, count, n, mx, lane);
 }
 
 // the sets of sums as one, in acc[0]
@@ -808,6 +818,7 @@ struct Consumer {
     Bars* bars;
     volatile int* abort;
     float* s_out;  // [T][16]: this warp's row tile of the second product
+    const uint8_t* none;
     int warp, lane;
     int slot = 0, round = 0, tslot = 0, tround = 0;
 
@@ -866,7 +877,7 @@ struct Consumer {
             float acc[B::CH][B::NT][4] = {};
             for (int k0 = 0; k0 < a.H; k0 += kc)
                 step(warp, w.size, [&](const uint8_t* A, const uint8_t* X) {
-                    multiply<B, 1>(acc, A, X, pitch, gr.count, min(kc, a.H - k0), mx, lane);
+                    multiply<B, 1>(acc, A, X, none, pitch, gr.count, min(kc, a.H - k0), mx, lane);
                 });
             if (warp >= w.size) continue;
             join<B>(acc);
@@ -959,7 +970,7 @@ struct Consumer {
             float acc[B::CH][B::NT][4] = {};
             do {
                 step(warp - w.lo, w.hi - w.lo, [&](const uint8_t* A, const uint8_t* X) {
-                    multiply<B, 2>(acc, A, X, pitch, gr.count, min(kc, a.I - w.c * kc), mx, lane);
+                    multiply<B, 2>(acc, A, X, none, pitch, gr.count, min(kc, a.I - w.c * kc), mx, lane);
                 });
                 w.next(p, tb.n_groups);
             } while (w.more(p) && w.g == g && w.set == set);
@@ -991,7 +1002,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
     tb.tok = reinterpret_cast<int*>(tb.groups + a.max_groups);
     tb.coef = reinterpret_cast<float*>(tb.tok + a.T * a.k + a.T);
     uint8_t *tokens = smem + a.tokens_off, *ring = smem + a.ring_off;
-    float* s_out = reinterpret_cast<float*>(tokens - kConsumers * a.T * 16 * sizeof(float));  // [8][T][16]
+    uint8_t* none = tokens - B::ZEROS;
+    float* s_out = reinterpret_cast<float*>(none - kConsumers * a.T * 16 * sizeof(float));  // [8][T][16]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int id = tid < a.T * a.k ? __ldg(a.ids + tid) : -1;
@@ -1012,7 +1024,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
         *s_abort = 0;
         bars->met = 0;
     }
-    for (int i = tid; i < kConsumers * a.T * 16; i += kDecodeThreads) s_out[i] = 0.0f;
+    for (int i = tid; i < kConsumers * a.T * 16 + B::ZEROS / 4; i += kDecodeThreads) s_out[i] = 0.0f;
     sort_routes<B::CAP>(a, tb, tokens, id, prob);  // its scratch: the rings' space
     fence_proxy_async_smem();
     __syncthreads();
@@ -1026,7 +1038,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
         Producer<B>{a, tb, p, ring, tokens, bars, s_abort, warp - kConsumers, lane}.run();
         return;
     }
-    Consumer<B> c{a, tb, p, ring, tokens, bars, s_abort, s_out + warp * a.T * 16, warp, lane};
+    Consumer<B> c{a, tb, p, ring, tokens, bars, s_abort, s_out + warp * a.T * 16, none, warp, lane};
     if (a.gate_w) c.gates();
     c.first();
     // the blocks meet: every activation and gate is written
@@ -1179,7 +1191,7 @@ cudaError_t launch_decode(DecodeArgs& a, int blocks, cudaStream_t st) {
     auto up = [](int v) { return (v + 127) / 128 * 128; };
     a.max_groups = std::min(a.E, R) + R / B::CAP + (a.T + B::CAP - 1) / B::CAP;
     a.tokens_off = up(int(sizeof(Bars)) + 16 + a.max_groups * int(sizeof(Group)) + (R + a.T) * 8 +
-                      kConsumers * a.T * 16 * int(sizeof(float)));
+                      kConsumers * a.T * 16 * int(sizeof(float)) + B::ZEROS);
     // the tokens' ring: about 48 KB, two slots at least
     a.token_slot_bytes = up(B::TS + cap * B::token_pitch(B::KC, 2));
     a.token_slots = std::min(kTokenSlots, std::max(2, 49152 / a.token_slot_bytes));
