@@ -6,8 +6,8 @@ the library cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -343,6 +343,13 @@ def _raw_stream(stream, device):
         return stream.cuda_stream
     import torch
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _current_stream_of():
+    """A function of a device index: its current cudaStream_t."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a twentieth of current_stream's time
+    return raw if raw is not None else (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def moe_decode_size(cfg: moe_config) -> int:
@@ -712,17 +719,21 @@ class HostPipe:
 
 
 
-def _allocate_on(stream):
-    """Context in which new tensors belong to `stream` (None: the current one)."""
-    if stream is None:
-        return contextlib.nullcontext()
-    import torch
-    return torch.cuda.stream(stream)
-
-
 def _require(ok, what):
     if not ok:
         raise ValueError(what)
+
+
+def _on_stream(call):
+    """Runs a method whose `stream` is given with that stream as the current one, so that new tensors belong to it."""
+    @functools.wraps(call)
+    def wrapped(self, *args, stream=None, **kw):
+        if stream is None:
+            return call(self, *args, **kw)
+        import torch
+        with torch.cuda.stream(stream):
+            return call(self, *args, **kw)
+    return wrapped
 
 
 class MoEDecoder:
@@ -735,29 +746,31 @@ class MoEDecoder:
                               MOE_ACT_FP32, 0 if shared_expert else 1)
         self.hidden, self.topk = int(hidden), int(topk)
         self.device = torch.device(device)
-        self._bf16, self._i32, self._f32 = torch.bfloat16, torch.int32, torch.float32
-        self._empty = torch.empty
+        self._torch, self._call, self._stream = torch, load().moe_decode, _current_stream_of()
         self.workspace = torch.empty(moe_decode_size(self.cfg), dtype=torch.uint8, device=self.device)
         with torch.cuda.device(self.device):
             self.handle = moe_decode_create(self.cfg, self.workspace)
 
-    def forward_topk(self, hidden, topk_ids, topk_probs, weights: moe_weights, out=None, stream=None):
+    @_on_stream
+    def forward_topk(self, hidden, topk_ids, topk_probs, weights: moe_weights, out=None):
         """out [T,H] of bf16 hidden [T,H] (rows may be strided), int32 ids [T,k] (-1 = empty
-        slot) and fp32 probs [T,k], for T up to max_tokens."""
-        T = hidden.shape[0]
-        _require(hidden.dtype == self._bf16 and hidden.dim() == 2 and hidden.shape[1] == self.hidden and
-                 (hidden.stride(1) == 1 or T == 0), "hidden must be [T, H] bf16 with contiguous rows")
-        _require(topk_ids.dtype == self._i32 and topk_probs.dtype == self._f32 and
-                 topk_ids.shape == (T, self.topk) and topk_probs.shape == (T, self.topk) and
-                 topk_ids.is_contiguous() and topk_probs.is_contiguous(),
-                 "topk_ids and topk_probs must be contiguous [T, k] int32 and fp32")
+        slot) and fp32 probs [T,k], for T up to max_tokens; `stream`: where (the current stream)."""
+        torch = self._torch
+        T, H = shape = hidden.shape
+        slots = (T, self.topk)
+        if hidden.dtype != torch.bfloat16 or H != self.hidden or hidden.stride(1) != 1:
+            raise ValueError("hidden must be [T, H] bf16 with contiguous rows")
+        if topk_ids.dtype != torch.int32 or topk_probs.dtype != torch.float32 or topk_ids.shape != slots or \
+                topk_probs.shape != slots or not topk_ids.is_contiguous() or not topk_probs.is_contiguous():
+            raise ValueError("topk_ids and topk_probs must be contiguous [T, k] int32 and fp32")
         if out is None:
-            with _allocate_on(stream):
-                out = self._empty((T, self.hidden), dtype=self._bf16, device=hidden.device)
-        else:
-            _require(out.dtype == self._bf16 and out.shape == hidden.shape and out.stride(1) == 1,
-                     "out must be [T, H] bf16 with contiguous rows")
-        moe_decode(self.handle, T, hidden, topk_ids, topk_probs, weights, out, stream)
+            out = torch.empty(shape, dtype=torch.bfloat16, device=hidden.device)
+        elif out.dtype != torch.bfloat16 or out.shape != shape or out.stride(1) != 1:
+            raise ValueError("out must be [T, H] bf16 with contiguous rows")
+        status = self._call(self.handle, T, hidden.data_ptr(), _ld(hidden), topk_ids.data_ptr(), topk_probs.data_ptr(),
+                            weights, out.data_ptr(), _ld(out), self._stream(hidden.get_device()))
+        if status:
+            raise MoeError(status, "moe_decode")
         return out
 
     def device_status(self, stream=None) -> int:
@@ -782,8 +795,11 @@ class MoENorm:
         import torch
         self.hidden, self.eps, self.kind, self.device = int(hidden), float(eps), int(kind), torch.device(device)
         self._types = {torch.bfloat16: MOE_T_BF16, torch.float32: MOE_T_FP32}
-        self._cfgs, self._sizes = {}, {}
-        self._torch = torch
+        self._cfgs = {}
+        self._torch, self._stream = torch, _current_stream_of()
+        self._forward, self._backward = load().moe_norm_forward, load().moe_norm_backward
+        _check(load().moe_norm_forward(moe_norm_config(self.hidden, self.eps, self.kind, 0, 0, 0), 0, None, self.hidden,
+                                       None, 0, None, None, None, 0, None, self.hidden, None, None, None), "MoENorm")
 
     def _cfg(self, x, y, w):
         key = (x, y, w)
@@ -793,68 +809,87 @@ class MoENorm:
             c = self._cfgs[key] = moe_norm_config(self.hidden, self.eps, self.kind, *(self._types[t] for t in key))
         return c
 
-    def _rows(self, t, like, dtype, what):
-        _require(t.dim() == 2 and t.shape == like.shape and t.shape[1] == self.hidden and t.dtype == dtype and
-                 t.stride(1) == 1, what + " must be [T, hidden] rows of the right type")
+    def _same(self, t, shape, dtype, what):
+        if t.shape != shape or t.dtype != dtype or t.stride(1) != 1:
+            raise ValueError(f"{what} must be [T, hidden] rows of the right type")
 
-    def _weights(self, weight, bias):
-        for t in (weight, bias):
-            _require(t is None or (t.shape == (self.hidden,) and t.is_contiguous() and t.dtype == weight.dtype),
-                     "weight and bias must be contiguous [hidden] vectors of one type")
+    def _vector(self, t, dtype):
+        if t.shape != (self.hidden,) or t.dtype != dtype or t.stride(0) != 1:
+            raise ValueError("weight and bias, and their gradients, must be [hidden] vectors of one type")
 
-    def forward(self, x, weight, bias=None, residual=None, out_dtype=None, stream=None):
+    @_on_stream
+    def forward(self, x, weight, bias=None, residual=None, out_dtype=None):
         """(y, s, mean, rstd): s = x + residual (x itself without one), y = norm(s) weight + bias in
-        out_dtype (x's by default); mean is None for RMS norm. s, mean and rstd are what backward takes."""
+        out_dtype (x's by default); mean is None for RMS norm. s, mean and rstd are what backward takes.
+        `stream`: where (the current stream)."""
         torch = self._torch
-        self._rows(x, x, x.dtype, "x")
-        self._weights(weight, bias)
-        if residual is not None:
-            self._rows(residual, x, x.dtype, "residual")
-        dtype = x.dtype if out_dtype is None else out_dtype
-        cfg = self._cfg(x.dtype, dtype, weight.dtype)
-        T = x.shape[0]
-        with _allocate_on(stream):
-            y = torch.empty(x.shape, dtype=dtype, device=x.device)
-            total = torch.empty(x.shape, dtype=x.dtype, device=x.device) if residual is not None else None
-            rstd = torch.empty(T, dtype=torch.float32, device=x.device)
-            mean = torch.empty(T, dtype=torch.float32, device=x.device) if self.kind == MOE_NORM_LAYER else None
-        moe_norm_forward(cfg, x, weight, y, bias, residual, total, mean, rstd, stream)
-        return y, (x if total is None else total), mean, rstd
+        T, H = shape = x.shape
+        xt, wt, dev = x.dtype, weight.dtype, x.device
+        yt = xt if out_dtype is None else out_dtype
+        if H != self.hidden or x.stride(1) != 1:
+            raise ValueError("x must be [T, hidden] rows")
+        self._vector(weight, wt)
+        if bias is not None:
+            self._vector(bias, wt)
+        cfg = self._cfgs.get((xt, yt, wt)) or self._cfg(xt, yt, wt)
+        y = torch.empty(shape, dtype=yt, device=dev)
+        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+        mean = torch.empty(T, dtype=torch.float32, device=dev) if self.kind == MOE_NORM_LAYER else None
+        if residual is None:
+            s, res, out = x, (None, 0), (None, 0)
+        else:
+            self._same(residual, shape, xt, "residual")
+            s = torch.empty(shape, dtype=xt, device=dev)
+            res, out = (residual.data_ptr(), _ld(residual)), (s.data_ptr(), H)
+        status = self._forward(cfg, T, x.data_ptr(), _ld(x), *res, weight.data_ptr(), _addr(bias), *out, y.data_ptr(), H,
+                               _addr(mean), rstd.data_ptr(), self._stream(x.get_device()))
+        if status:
+            raise MoeError(status, "moe_norm_forward")
+        return y, s, mean, rstd
 
-    def backward(self, dy, s, weight, mean, rstd, dsum=None, bias=False, dweight=None, dbias=None, accumulate=False,
-                 stream=None):
+    @_on_stream
+    def backward(self, dy, s, weight, mean, rstd, dsum=None, bias=False, dweight=None, dbias=None, accumulate=False):
         """(ds, dweight, dbias) for the gradient dy of y, joined by dsum, the gradient that reaches s
         past the norm. dweight (and, with `bias`, dbias) are new fp32 vectors, or the given
-        fp32 / bf16 buffers, overwritten or (accumulate) added to."""
+        fp32 / bf16 buffers, overwritten or (accumulate) added to. `stream`: where (the current stream)."""
         torch = self._torch
-        self._rows(s, s, s.dtype, "s")
-        self._rows(dy, s, dy.dtype, "dy")
-        self._weights(weight, None)
+        T, H = shape = s.shape
+        st, dev, f32 = s.dtype, s.device, torch.float32
+        if H != self.hidden or s.stride(1) != 1:
+            raise ValueError("s must be [T, hidden] rows")
+        self._same(dy, shape, dy.dtype, "dy")
+        self._vector(weight, weight.dtype)
+        for v in (mean, rstd):
+            if v is None:
+                if v is rstd or self.kind == MOE_NORM_LAYER:
+                    raise ValueError("mean and rstd must be the forward's [T] fp32")
+            elif v.dtype != f32 or v.shape != (T,) or not v.is_contiguous():
+                raise ValueError("mean and rstd must be the forward's [T] fp32")
+        if accumulate and (dweight is None or (bias and dbias is None)):
+            raise ValueError("accumulate adds to given buffers")
         if dsum is not None:
-            self._rows(dsum, s, s.dtype, "dsum")
-        T = s.shape[0]
-        for v, need in ((mean, self.kind == MOE_NORM_LAYER), (rstd, True)):
-            _require(not need or (v is not None and v.dtype == torch.float32 and v.shape == (T,) and
-                                  v.is_contiguous()), "mean and rstd must be the forward's [T] fp32")
-        _require(not accumulate or (dweight is not None and (dbias is not None or not bias)),
-                 "accumulate adds to given buffers")
-        cfg = self._cfg(s.dtype, dy.dtype, weight.dtype)
-        size = self._sizes.get(T)
-        if size is None:
-            size = self._sizes[T] = moe_norm_backward_size(cfg, T)
-        with _allocate_on(stream):
-            dx = torch.empty(s.shape, dtype=s.dtype, device=s.device)
-            if dweight is None:
-                dweight = torch.empty(self.hidden, dtype=torch.float32, device=s.device)
-            if bias and dbias is None:
-                dbias = torch.empty(self.hidden, dtype=dweight.dtype, device=s.device)
-            workspace = torch.empty(size, dtype=torch.uint8, device=s.device)
-        for g in (dweight, dbias):
-            _require(g is None or (g.shape == (self.hidden,) and g.is_contiguous() and g.dtype == dweight.dtype and
-                                   g.dtype in self._types), "dweight and dbias must be [hidden], both fp32 or both bf16")
-        moe_norm_backward(cfg, dy, s, weight, mean, rstd, dx, dsum, dweight, dbias,
-                          MOE_G_BF16 if dweight.dtype == torch.bfloat16 else MOE_G_FP32, accumulate, workspace, stream)
-        return dx, dweight, dbias
+            self._same(dsum, shape, st, "dsum")
+        cfg = self._cfg(st, dy.dtype, weight.dtype)
+        ds = torch.empty(shape, dtype=st, device=dev)
+        if dweight is None:
+            dweight = torch.empty(H, dtype=f32, device=dev)
+        gt = dweight.dtype
+        if bias and dbias is None:
+            dbias = torch.empty(H, dtype=gt, device=dev)
+        if gt not in self._types:
+            raise ValueError("dweight and dbias must be fp32 or bf16")
+        self._vector(dweight, gt)
+        if dbias is not None:
+            self._vector(dbias, gt)
+        size = moe_norm_backward_size(cfg, T)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        status = self._backward(cfg, T, dy.data_ptr(), _ld(dy), s.data_ptr(), _ld(s), weight.data_ptr(), _addr(mean),
+                                rstd.data_ptr(), _addr(dsum), 0 if dsum is None else _ld(dsum), ds.data_ptr(), H,
+                                dweight.data_ptr(), _addr(dbias), MOE_G_FP32 if gt == f32 else MOE_G_BF16,
+                                1 if accumulate else 0, workspace.data_ptr(), size, self._stream(s.get_device()))
+        if status:
+            raise MoeError(status, "moe_norm_backward")
+        return ds, dweight, dbias
 
 
 class MoERouter:
@@ -865,51 +900,62 @@ class MoERouter:
         import torch
         self.E, self.k = int(num_experts), int(topk)
         self.device = torch.device(device)
-        self._torch = torch
         args = (self.E, self.k, int(score), int(bool(normalise)), float(scale), float(aux_coeff), float(z_coeff))
         self._cfgs = {torch.bfloat16: moe_router_config(*args, MOE_T_BF16),
                       torch.float32: moe_router_config(*args, MOE_T_FP32)}
         self.losses_wanted = aux_coeff != 0 or z_coeff != 0
-        self._sizes = {}
+        self._torch, self._stream = torch, _current_stream_of()
+        self._forward, self._backward = load().moe_router_forward, load().moe_router_backward
         moe_router_size(self._cfgs[torch.float32], 0)      # the library's check of the configuration
 
-    def _logits(self, logits):
-        _require(logits.dim() == 2 and logits.shape[1] == self.E and logits.dtype in self._cfgs and
-                 logits.stride(1) == 1, "logits must be [T, E] rows, bf16 or fp32")
-        return self._cfgs[logits.dtype]
+    def _cfg(self, logits):
+        cfg = self._cfgs.get(logits.dtype)
+        if cfg is None or logits.shape[1] != self.E or logits.stride(1) != 1:
+            raise ValueError("logits must be [T, E] rows, bf16 or fp32")
+        return cfg
 
-    def forward(self, logits, select_bias=None, stream=None):
+    @_on_stream
+    def forward(self, logits, select_bias=None):
         """(ids [T,k] int32, probs [T,k] fp32, counts [E] int32, losses [2] fp32 or None): the input of
-        forward_topk, the routes per expert, and the balance and z losses where a coefficient asks for them."""
+        forward_topk, the routes per expert, and the balance and z losses where a coefficient asks for them.
+        `stream`: where (the current stream)."""
         torch = self._torch
-        cfg = self._logits(logits)
-        _require(select_bias is None or (select_bias.shape == (self.E,) and select_bias.dtype == torch.float32 and
-                                         select_bias.is_contiguous()), "select_bias must be [E] fp32")
+        cfg = self._cfg(logits)
         T, dev = logits.shape[0], logits.device
-        size = self._sizes.get(T)
-        if size is None:
-            size = self._sizes[T] = moe_router_size(cfg, T)
-        with _allocate_on(stream):
-            ids = torch.empty((T, self.k), dtype=torch.int32, device=dev)
-            probs = torch.empty((T, self.k), dtype=torch.float32, device=dev)
-            counts = torch.empty(self.E, dtype=torch.int32, device=dev)
-            losses = torch.empty(2, dtype=torch.float32, device=dev) if self.losses_wanted else None
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-        moe_router_forward(cfg, logits, ids, probs, counts, losses, select_bias, workspace, stream)
+        if select_bias is not None and (select_bias.shape != (self.E,) or select_bias.dtype != torch.float32 or
+                                        select_bias.stride(0) != 1):
+            raise ValueError("select_bias must be [E] fp32")
+        slots = (T, self.k)
+        ids = torch.empty(slots, dtype=torch.int32, device=dev)
+        probs = torch.empty(slots, dtype=torch.float32, device=dev)
+        counts = torch.empty(self.E, dtype=torch.int32, device=dev)
+        losses = torch.empty(2, dtype=torch.float32, device=dev) if self.losses_wanted else None
+        size = moe_router_size(cfg, T)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        status = self._forward(cfg, T, logits.data_ptr(), _ld(logits), _addr(select_bias), ids.data_ptr(),
+                               probs.data_ptr(), counts.data_ptr(), _addr(losses), workspace.data_ptr(), size,
+                               self._stream(logits.get_device()))
+        if status:
+            raise MoeError(status, "moe_router_forward")
         return ids, probs, counts, losses
 
-    def backward(self, logits, ids, dprobs, counts=None, loss_grad=1.0, stream=None):
+    @_on_stream
+    def backward(self, logits, ids, dprobs, counts=None, loss_grad=1.0):
         """dlogits of sum(dprobs * probs) + loss_grad * (balance + z); counts: the forward's (needed
-        with a balance loss)."""
+        with a balance loss). `stream`: where (the current stream)."""
         torch = self._torch
-        cfg = self._logits(logits)
-        T = logits.shape[0]
-        for t, dt in ((ids, torch.int32), (dprobs, torch.float32)):
-            _require(t.shape == (T, self.k) and t.dtype == dt and t.is_contiguous(),
-                     "ids and dprobs must be contiguous [T, k] int32 and fp32")
-        _require(counts is None or (counts.shape == (self.E,) and counts.dtype == torch.int32 and
-                                    counts.is_contiguous()), "counts must be [E] int32")
-        with _allocate_on(stream):
-            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        moe_router_backward(cfg, logits, ids, dprobs, dlogits, counts, float(loss_grad), stream)
+        cfg = self._cfg(logits)
+        shape = logits.shape
+        slots = (shape[0], self.k)
+        if ids.shape != slots or ids.dtype != torch.int32 or not ids.is_contiguous() or dprobs.shape != slots or \
+                dprobs.dtype != torch.float32 or not dprobs.is_contiguous():
+            raise ValueError("ids and dprobs must be contiguous [T, k] int32 and fp32")
+        if counts is not None and (counts.shape != (self.E,) or counts.dtype != torch.int32 or counts.stride(0) != 1):
+            raise ValueError("counts must be [E] int32")
+        dlogits = torch.empty(shape, dtype=logits.dtype, device=logits.device)
+        status = self._backward(cfg, shape[0], logits.data_ptr(), _ld(logits), ids.data_ptr(), dprobs.data_ptr(),
+                                _addr(counts), float(loss_grad), dlogits.data_ptr(), self.E,
+                                self._stream(logits.get_device()))
+        if status:
+            raise MoeError(status, "moe_router_backward")
         return dlogits

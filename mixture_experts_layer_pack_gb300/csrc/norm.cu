@@ -8,6 +8,7 @@
 //   dx = rstd (g - sum(g)/H - xhat sum(g xhat)/H) + dsum,
 //   dw = sum_t dy xhat, db = sum_t dy.
 // All statistics and sums are fp32.
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -20,37 +21,94 @@ namespace moe {
 namespace {
 
 constexpr int kMaxHidden = 32768;
-constexpr int kMaxChunks = 304;  // row chunks of the weight gradient's sums
+constexpr int kMaxChunks = 304;     // blocks of the backward that sum weight gradients: two per SM
+constexpr int kRowThreads = 512;    // most threads of a row: 128 registers each
+constexpr int kColumns = 16;        // columns of a thread in the backward, for rows up to kColumns * kRowThreads
+constexpr int kFewRows = 304;       // rows up to which the forward spreads a row over as many threads as it can
 
-__device__ __forceinline__ float load_f(const float* p) { return *p; }
-__device__ __forceinline__ float load_f(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store_f(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_f(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+// V consecutive elements as fp32: one 16-byte access (two for 8 fp32, one of 8 bytes for 4 bf16), or with V 1 a scalar
+template <int V>
+__device__ __forceinline__ void load_v(const __nv_bfloat16* p, float (&f)[V]) {
+    if constexpr (V == 8) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p);
+        unpack_bf16x2(w.x, f[0], f[1]);
+        unpack_bf16x2(w.y, f[2], f[3]);
+        unpack_bf16x2(w.z, f[4], f[5]);
+        unpack_bf16x2(w.w, f[6], f[7]);
+    } else if constexpr (V == 4) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
+        unpack_bf16x2(w.x, f[0], f[1]);
+        unpack_bf16x2(w.y, f[2], f[3]);
+    } else {
+        f[0] = __bfloat162float(*p);
+    }
+}
+template <int V>
+__device__ __forceinline__ void load_v(const float* p, float (&f)[V]) {
+    if constexpr (V == 1) {
+        f[0] = *p;
+    } else {
+#pragma unroll
+        for (int q = 0; q < V; q += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(p + q);
+            f[q] = w.x, f[q + 1] = w.y, f[q + 2] = w.z, f[q + 3] = w.w;
+        }
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_v(__nv_bfloat16* p, const float (&f)[V]) {
+    if constexpr (V == 8)
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                  pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    else if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+    else
+        *p = __float2bfloat16_rn(f[0]);
+}
+template <int V>
+__device__ __forceinline__ void store_v(float* p, const float (&f)[V]) {
+    if constexpr (V == 1) {
+        *p = f[0];
+    } else {
+#pragma unroll
+        for (int q = 0; q < V; q += 4) *reinterpret_cast<float4*>(p + q) = make_float4(f[q], f[q + 1], f[q + 2], f[q + 3]);
+    }
+}
+// weight and bias come in either type, a run-time branch: they are read from cache
+template <int V>
+__device__ __forceinline__ void load_w(const void* p, int i, bool bf16, float (&f)[V]) {
+    if (bf16)
+        load_v<V>(static_cast<const __nv_bfloat16*>(p) + i, f);
+    else
+        load_v<V>(static_cast<const float*>(p) + i, f);
+}
 __device__ __forceinline__ float round_to(float v, const float*) { return v; }
 __device__ __forceinline__ float round_to(float v, const __nv_bfloat16*) {
     return __bfloat162float(__float2bfloat16_rn(v));
 }
-// weight and bias come in either type; the row's sums dominate, so their type is a run-time branch
-__device__ __forceinline__ float load_w(const void* p, int64_t i, bool bf16) {
-    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
-}
 
-// sum over the block's threads, in an order fixed by the block size; every thread gets it
-__device__ float block_sum(float v) {
-    __shared__ float part[33];
+// Sums over the `tpr` threads (whole warps) of a row, several rows to a block; every thread of the
+// row gets them, in an order fixed by tpr. part: [2][32] per value, alternating, so that one
+// barrier a sum is enough.
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float* part) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+    if (tpr == 32) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = tpr >> 5, first = warp / per * per;
+    if (lane == 0)
+#pragma unroll
+        for (int n = 0; n < N; ++n) part[n * 32 + warp] = v[n];
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        float t = threadIdx.x < (blockDim.x >> 5) ? part[threadIdx.x] : 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        float t = lane < per ? part[n * 32 + first + lane] : 0.0f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        if (threadIdx.x == 0) part[32] = t;
+        v[n] = t;
     }
-    __syncthreads();
-    return part[32];
 }
 
 struct NormFwd {
@@ -58,41 +116,147 @@ struct NormFwd {
     void *s, *y;
     float *mean, *rstd;
     int64_t xs, rs, ss, ys;
-    int H;
+    int64_t T;
+    int H, tpr;
     float eps;
     bool w_bf16;
 };
 
-template <typename XT, typename YT, bool RMS>
-__global__ void __launch_bounds__(256) norm_forward_kernel(NormFwd a) {
+// A row stays in the registers of its threads, NV pieces of V elements each: read once,
+// written once, and the variance is of differences from the mean, not of squares.
+template <typename XT, typename YT, bool RMS, int V, int NV>
+__global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
+    __shared__ float part[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const int tpr = a.tpr, col = threadIdx.x % tpr;
+    const int64_t row = int64_t(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
+    const bool live = row < a.T;  // the block's last rows may not exist; their threads join the sums
+    const int64_t t = live ? row : a.T - 1;
+    const XT* x = static_cast<const XT*>(a.x) + t * a.xs;
+    float v[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = (col + j * tpr) * V;
+        if (i < a.H) load_v<V>(x + i, v[j]);
+    }
+    if (a.r) {
+        const XT* r = static_cast<const XT*>(a.r) + t * a.rs;
+        XT* s = static_cast<XT*>(a.s) + t * a.ss;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = (col + j * tpr) * V;
+            if (i >= a.H) continue;
+            float f[V];
+            load_v<V>(r + i, f);
+#pragma unroll
+            for (int q = 0; q < V; ++q) v[j][q] = round_to(v[j][q] + f[q], x);
+        }
+        if (live)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int i = (col + j * tpr) * V;
+                if (i < a.H) store_v<V>(s + i, v[j]);
+            }
+    }
+    float mean = 0.0f;
+    if (!RMS) {
+        float sum[1] = {0.0f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if ((col + j * tpr) * V < a.H)
+#pragma unroll
+                for (int q = 0; q < V; ++q) sum[0] += v[j][q];
+        row_sum<1>(sum, tpr, part[0]);
+        mean = sum[0] / a.H;
+    }
+    float sq[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if ((col + j * tpr) * V < a.H)
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                v[j][q] -= mean;
+                sq[0] = fmaf(v[j][q], v[j][q], sq[0]);
+            }
+    row_sum<1>(sq, tpr, part[1]);
+    const float rstd = rsqrtf(sq[0] / a.H + a.eps);
+    if (!live) return;
+    YT* y = static_cast<YT*>(a.y) + t * a.ys;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = (col + j * tpr) * V;
+        if (i >= a.H) continue;
+        float w[V], b[V], o[V];
+        load_w<V>(a.w, i, a.w_bf16, w);
+        if (a.b) load_w<V>(a.b, i, a.w_bf16, b);
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            o[q] = v[j][q] * rstd * w[q];
+            if (a.b) o[q] += b[q];
+        }
+        store_v<V>(y + i, o);
+    }
+    if (col == 0) {
+        if (!RMS && a.mean) a.mean[t] = mean;
+        if (a.rstd) a.rstd[t] = rstd;
+    }
+}
+
+// Rows too wide for that: row blockIdx.x read three times (the second and third from cache)
+template <typename XT, typename YT, bool RMS, int V>
+__global__ void __launch_bounds__(kRowThreads) norm_forward_wide_kernel(NormFwd a) {
+    __shared__ float part[2][32];
+    pdl_wait();
+    pdl_trigger();
     const int64_t t = blockIdx.x;
     const XT* x = static_cast<const XT*>(a.x) + t * a.xs;
     const XT* r = a.r ? static_cast<const XT*>(a.r) + t * a.rs : nullptr;
-    XT* s = static_cast<XT*>(a.s) + t * a.ss;
     YT* y = static_cast<YT*>(a.y) + t * a.ys;
-    auto value = [&](int i) {
-        const float v = load_f(x + i);
-        return r ? round_to(v + load_f(r + i), x) : v;
+    // sum may be x or residual itself: the rounded sum is written in the last pass, where it is last needed
+    auto value = [&](int i, float (&v)[V]) {
+        load_v<V>(x + i, v);
+        if (!r) return;
+        float f[V];
+        load_v<V>(r + i, f);
+#pragma unroll
+        for (int q = 0; q < V; ++q) v[q] = round_to(v[q] + f[q], x);
     };
-    float sum = 0.0f;
+    float mean = 0.0f, sum[1] = {0.0f};
     if (!RMS) {
-        for (int i = threadIdx.x; i < a.H; i += blockDim.x) sum += value(i);
-        sum = block_sum(sum);
+#pragma unroll 4
+        for (int i = threadIdx.x * V; i < a.H; i += blockDim.x * V) {
+            float v[V];
+            value(i, v);
+#pragma unroll
+            for (int q = 0; q < V; ++q) sum[0] += v[q];
+        }
+        row_sum<1>(sum, blockDim.x, part[0]);
+        mean = sum[0] / a.H;
     }
-    const float mean = RMS ? 0.0f : sum / a.H;
-    float sq = 0.0f;
-    for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
-        const float d = value(i) - mean;
-        sq = fmaf(d, d, sq);
+    float sq[1] = {0.0f};
+#pragma unroll 4
+    for (int i = threadIdx.x * V; i < a.H; i += blockDim.x * V) {
+        float v[V];
+        value(i, v);
+#pragma unroll
+        for (int q = 0; q < V; ++q) sq[0] = fmaf(v[q] - mean, v[q] - mean, sq[0]);
     }
-    sq = block_sum(sq);
-    const float rstd = rsqrtf(sq / a.H + a.eps);
-    for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
-        const float v = value(i);
-        float o = (v - mean) * rstd * load_w(a.w, i, a.w_bf16);
-        if (a.b) o += load_w(a.b, i, a.w_bf16);
-        if (r) store_f(s + i, v);
-        store_f(y + i, o);
+    row_sum<1>(sq, blockDim.x, part[1]);
+    const float rstd = rsqrtf(sq[0] / a.H + a.eps);
+#pragma unroll 4
+    for (int i = threadIdx.x * V; i < a.H; i += blockDim.x * V) {
+        float v[V], w[V], b[V], o[V];
+        value(i, v);
+        load_w<V>(a.w, i, a.w_bf16, w);
+        if (a.b) load_w<V>(a.b, i, a.w_bf16, b);
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            o[q] = (v[q] - mean) * rstd * w[q];
+            if (a.b) o[q] += b[q];
+        }
+        if (r) store_v<V>(static_cast<XT*>(a.s) + t * a.ss + i, v);
+        store_v<V>(y + i, o);
     }
     if (threadIdx.x == 0) {
         if (!RMS && a.mean) a.mean[t] = mean;
@@ -104,52 +268,174 @@ struct NormBwd {
     const void *dy, *x, *w, *ds;
     const float *mean, *rstd;
     void* dx;
-    float* part;  // [chunks][2][H]: dweight, dbias of a chunk of rows
+    float* part;  // [blocks][2][H]: a block's sums over its rows of dy xhat and of dy
     int64_t dys, xs, dss, dxs;
     int64_t T;
-    int H;
-    int chunks;
-    bool w_bf16, want_w, want_b;
+    int H, tpr;
+    bool w_bf16;
 };
 
-template <typename XT, typename YT, bool RMS>
-__global__ void __launch_bounds__(256) norm_backward_kernel(NormBwd a) {
-    const int64_t t = blockIdx.x;
-    const YT* dy = static_cast<const YT*>(a.dy) + t * a.dys;
-    const XT* x = static_cast<const XT*>(a.x) + t * a.xs;
-    const XT* ds = a.ds ? static_cast<const XT*>(a.ds) + t * a.dss : nullptr;
-    XT* dx = static_cast<XT*>(a.dx) + t * a.dxs;
-    const float mean = RMS ? 0.0f : a.mean[t];
-    const float rstd = a.rstd[t];
-    float sg = 0.0f, sgx = 0.0f;
-    for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
-        const float g = load_f(dy + i) * load_w(a.w, i, a.w_bf16);
-        const float xh = (load_f(x + i) - mean) * rstd;
-        sg += g;
-        sgx = fmaf(g, xh, sgx);
+// dx of a block's rows (blockIdx.x, + gridDim.x, ...), one row group of tpr threads per row; with SUMS
+// also the block's part of the weight gradients: a thread has the same columns in every row
+// and keeps their sums in registers, so x and dy are read once for all three gradients.
+template <typename XT, typename YT, bool RMS, int V, int NV, bool SUMS>
+__global__ void __launch_bounds__(kRowThreads) norm_backward_kernel(NormBwd a) {
+    __shared__ float part[2][2][32];
+    extern __shared__ float s_rows[];  // SUMS, several rows at a time: [2][H] per row group
+    pdl_wait();
+    pdl_trigger();
+    const int tpr = a.tpr, col = threadIdx.x % tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr;
+    float dw[SUMS ? NV : 1][V] = {}, db[SUMS ? NV : 1][V] = {};
+    int turn = 0;
+    for (int64_t t0 = int64_t(blockIdx.x) * groups; t0 < a.T; t0 += int64_t(gridDim.x) * groups, turn ^= 1) {
+        const bool live = t0 + group < a.T;
+        const int64_t t = live ? t0 + group : a.T - 1;
+        const XT* x = static_cast<const XT*>(a.x) + t * a.xs;
+        const YT* dy = static_cast<const YT*>(a.dy) + t * a.dys;
+        const XT* ds = a.ds ? static_cast<const XT*>(a.ds) + t * a.dss : nullptr;
+        float xh[NV][V], g[NV][V], d[NV][V];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = (col + j * tpr) * V;
+            if (i < a.H) {
+                load_v<V>(x + i, xh[j]);
+                load_v<V>(dy + i, g[j]);
+            }
+        }
+        const float mean = RMS ? 0.0f : a.mean[t], rstd = a.rstd[t];
+        if (ds)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int i = (col + j * tpr) * V;
+                if (i < a.H) load_v<V>(ds + i, d[j]);
+            }
+        float sum[2] = {0.0f, 0.0f};  // of g xhat, g
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = (col + j * tpr) * V;
+            if (i >= a.H) continue;
+            float w[V];
+            load_w<V>(a.w, i, a.w_bf16, w);
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                xh[j][q] = (xh[j][q] - mean) * rstd;
+                if (SUMS && live) {
+                    dw[SUMS ? j : 0][q] = fmaf(g[j][q], xh[j][q], dw[SUMS ? j : 0][q]);
+                    db[SUMS ? j : 0][q] += g[j][q];
+                }
+                g[j][q] *= w[q];
+                sum[0] = fmaf(g[j][q], xh[j][q], sum[0]);
+                sum[1] += g[j][q];
+            }
+        }
+        row_sum<2>(sum, tpr, part[turn][0]);
+        const float mgx = sum[0] / a.H, mg = RMS ? 0.0f : sum[1] / a.H;
+        if (!live) continue;
+        XT* dx = static_cast<XT*>(a.dx) + t * a.dxs;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = (col + j * tpr) * V;
+            if (i >= a.H) continue;
+            float o[V];
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                o[q] = rstd * (g[j][q] - mg - xh[j][q] * mgx);
+                if (ds) o[q] += d[j][q];
+            }
+            store_v<V>(dx + i, o);
+        }
     }
-    const float mg = RMS ? 0.0f : block_sum(sg) / a.H;
-    const float mgx = block_sum(sgx) / a.H;
-    for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
-        const float g = load_f(dy + i) * load_w(a.w, i, a.w_bf16);
-        const float xh = (load_f(x + i) - mean) * rstd;
-        float o = rstd * (g - mg - xh * mgx);
-        if (ds) o += load_f(ds + i);
-        store_f(dx + i, o);
+    if constexpr (SUMS) {
+        float* out = a.part + int64_t(blockIdx.x) * 2 * a.H;
+        if (groups > 1) {  // the row groups' sums, added in group order
+            for (int r = 0; r < groups; ++r) {
+                __syncthreads();
+                if (r != group) continue;
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int q = 0; q < V; ++q) {
+                        const int i = (col + j * tpr) * V + q;
+                        if (i >= a.H) continue;
+                        s_rows[i] = (r ? s_rows[i] : 0.0f) + dw[j][q];
+                        s_rows[a.H + i] = (r ? s_rows[a.H + i] : 0.0f) + db[j][q];
+                    }
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < 2 * a.H; i += blockDim.x) out[i] = s_rows[i];
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    const int i = (col + j * tpr) * V + q;
+                    if (i >= a.H) continue;
+                    out[i] = dw[j][q];
+                    out[a.H + i] = db[j][q];
+                }
+        }
     }
 }
 
-// part[c] = sums of chunk c's rows (c, c + chunks, ...) over dy xhat and dy; a thread owns a column
+// Rows too wide for that: dx of row blockIdx.x, read twice (the second time from cache)
+template <typename XT, typename YT, bool RMS, int V>
+__global__ void __launch_bounds__(kRowThreads) norm_backward_wide_kernel(NormBwd a) {
+    __shared__ float part[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const int64_t t = blockIdx.x;
+    const XT* x = static_cast<const XT*>(a.x) + t * a.xs;
+    const YT* dy = static_cast<const YT*>(a.dy) + t * a.dys;
+    const XT* ds = a.ds ? static_cast<const XT*>(a.ds) + t * a.dss : nullptr;
+    XT* dx = static_cast<XT*>(a.dx) + t * a.dxs;
+    const float mean = RMS ? 0.0f : a.mean[t], rstd = a.rstd[t];
+    float sum[2] = {0.0f, 0.0f};  // of g xhat, g
+#pragma unroll 4
+    for (int i = threadIdx.x * V; i < a.H; i += blockDim.x * V) {
+        float xv[V], g[V], w[V];
+        load_v<V>(x + i, xv);
+        load_v<V>(dy + i, g);
+        load_w<V>(a.w, i, a.w_bf16, w);
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            const float gq = g[q] * w[q];
+            sum[0] = fmaf(gq, (xv[q] - mean) * rstd, sum[0]);
+            sum[1] += gq;
+        }
+    }
+    row_sum<2>(sum, blockDim.x, part[0]);
+    const float mgx = sum[0] / a.H, mg = RMS ? 0.0f : sum[1] / a.H;
+#pragma unroll 4
+    for (int i = threadIdx.x * V; i < a.H; i += blockDim.x * V) {
+        float xv[V], g[V], w[V], d[V], o[V];
+        load_v<V>(x + i, xv);
+        load_v<V>(dy + i, g);
+        load_w<V>(a.w, i, a.w_bf16, w);
+        if (ds) load_v<V>(ds + i, d);
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            o[q] = rstd * (g[q] * w[q] - mg - (xv[q] - mean) * rstd * mgx);
+            if (ds) o[q] += d[q];
+        }
+        store_v<V>(dx + i, o);
+    }
+}
+
+// and their weight gradients: part[c] = sums of rows c, c + chunks, ...; a thread owns a column
 template <typename XT, typename YT, bool RMS>
 __global__ void __launch_bounds__(256) norm_wgrad_kernel(NormBwd a) {
+    pdl_wait();
+    pdl_trigger();
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= a.H) return;
     float dw = 0.0f, db = 0.0f;
-    for (int64_t t = blockIdx.y; t < a.T; t += a.chunks) {
-        const float d = load_f(static_cast<const YT*>(a.dy) + t * a.dys + i);
-        const float xh = (load_f(static_cast<const XT*>(a.x) + t * a.xs + i) - (RMS ? 0.0f : a.mean[t])) * a.rstd[t];
-        dw = fmaf(d, xh, dw);
-        db += d;
+#pragma unroll 8
+    for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
+        float d[1], x[1];
+        load_v<1>(static_cast<const YT*>(a.dy) + t * a.dys + i, d);
+        load_v<1>(static_cast<const XT*>(a.x) + t * a.xs + i, x);
+        dw = fmaf(d[0], (x[0] - (RMS ? 0.0f : a.mean[t])) * a.rstd[t], dw);
+        db += d[0];
     }
     float* p = a.part + int64_t(blockIdx.y) * 2 * a.H;
     p[i] = dw;
@@ -167,18 +453,28 @@ __device__ __forceinline__ void put_grad(void* g, int i, float v, bool bf16, boo
     }
 }
 
-// dweight, dbias from the chunks' sums, in chunk order
+// dweight (blockIdx.y 0) or dbias of 32 columns from the blocks' sums: warp w adds the blocks
+// w, w + 8, ... in order, then the warps' sums are added in warp order
 __global__ void __launch_bounds__(256) norm_wgrad_reduce_kernel(const float* __restrict__ part, int chunks, int H,
                                                                 void* dw, void* db, bool bf16, bool add) {
-    const int i = blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= H) return;
-    float w = 0.0f, b = 0.0f;
-    for (int c = 0; c < chunks; ++c) {
-        w += part[int64_t(c) * 2 * H + i];
-        b += part[int64_t(c) * 2 * H + H + i];
+    __shared__ float s_sum[8][32];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
+    void* out = blockIdx.y == 0 ? dw : db;
+    if (out == nullptr) return;
+    float v = 0.0f;
+    if (i < H) {
+        const float* p = part + int64_t(blockIdx.y) * H + i;
+#pragma unroll 8
+        for (int c = warp; c < chunks; c += 8) v += p[int64_t(c) * 2 * H];
     }
-    if (dw) put_grad(dw, i, w, bf16, add);
-    if (db) put_grad(db, i, b, bf16, add);
+    s_sum[warp][lane] = v;
+    __syncthreads();
+    if (warp || i >= H) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) v += s_sum[w][lane];
+    put_grad(out, i, v, bf16, add);
 }
 
 int norm_chunks(int64_t T) { return int(T < kMaxChunks ? (T < 1 ? 1 : T) : kMaxChunks); }
@@ -208,6 +504,50 @@ cudaError_t by_type(const moe_norm_config& c, F f) {
                                   : (rms ? f(0.0f, 0.0f, std::true_type()) : f(0.0f, 0.0f, std::false_type()));
 }
 
+bool rows_aligned(const void* p, int64_t stride, int32_t type, size_t bytes) {
+    const size_t es = type == MOE_T_BF16 ? 2 : 4;
+    return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | (size_t(stride) * es)) & (bytes - 1)) == 0;
+}
+
+// Threads of a row that takes `pieces` accesses, `each` to a thread, and of the block: rows of up
+// to 128 threads share a block of 256.
+struct RowShape {
+    int tpr, threads;
+};
+RowShape row_shape(int pieces, int each) {
+    int tpr = ((pieces + each - 1) / each + 31) / 32 * 32;
+    if (tpr <= 128) {
+        int p = 32;
+        while (p < tpr) p *= 2;
+        return {p, 256};
+    }
+    return {tpr, tpr};
+}
+
+template <typename XT, typename YT, bool RMS, int V, int NV>
+cudaError_t launch_norm_forward(NormFwd& a, cudaStream_t st) {
+    const RowShape r = row_shape(a.H / V + (a.H % V != 0), NV);
+    const int rows = r.threads / r.tpr;
+    a.tpr = r.tpr;
+    // a few rows: no threads without one
+    const int threads = a.T < rows ? int(a.T) * r.tpr : r.threads;
+    const int64_t blocks = (a.T + threads / r.tpr - 1) / (threads / r.tpr);
+    count_launch();
+    return launch_pdl(norm_forward_kernel<XT, YT, RMS, V, NV>, dim3(unsigned(blocks)), dim3(unsigned(threads)), 0, st, a);
+}
+
+template <typename XT, typename YT, bool RMS, int V, int NV, bool SUMS>
+cudaError_t launch_norm_backward(NormBwd& a, int chunks, cudaStream_t st) {
+    const RowShape r = row_shape((a.H + V - 1) / V, NV);
+    const int rows = r.threads / r.tpr;
+    a.tpr = r.tpr;
+    const int64_t blocks = SUMS ? chunks : (a.T + rows - 1) / rows;
+    const size_t smem = SUMS && rows > 1 ? 2 * size_t(a.H) * sizeof(float) : 0;
+    count_launch();
+    return launch_pdl(norm_backward_kernel<XT, YT, RMS, V, NV, SUMS>, dim3(unsigned(blocks)), dim3(unsigned(r.threads)),
+                      smem, st, a);
+}
+
 }  // namespace
 
 }  // namespace moe
@@ -230,14 +570,34 @@ moe_status moe_norm_forward(const moe_norm_config* cfg, int64_t T, const void* x
         !elem_aligned(bias, cfg->w_type) || !elem_aligned(residual, cfg->x_type) || !elem_aligned(mean, MOE_T_FP32) ||
         !elem_aligned(rstd, MOE_T_FP32) || (residual && !elem_aligned(sum, cfg->x_type)))
         return MOE_ERR_INVALID_ARG;
-    NormFwd a{x, residual, weight, bias, sum, y, mean, rstd, x_stride, residual_stride, sum_stride, y_stride,
-              int(H), cfg->eps, cfg->w_type == MOE_T_BF16};
+    NormFwd a{x, residual, weight, bias, sum, y, mean, rstd, x_stride, residual_stride, sum_stride, y_stride, T,
+              int(H), 0, cfg->eps, cfg->w_type == MOE_T_BF16};
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const cudaError_t e = by_type(*cfg, [&](auto xt, auto yt, auto rms) {
-        norm_forward_kernel<decltype(xt), decltype(yt), decltype(rms)::value>
-            <<<unsigned(T), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-        return cudaGetLastError();
+        using X = decltype(xt);
+        using Y = decltype(yt);
+        constexpr bool R = decltype(rms)::value;
+        constexpr int V = 16 / sizeof(X);
+        constexpr size_t YB = V * sizeof(Y) < 16 ? V * sizeof(Y) : 16;
+        const size_t wb = std::min<size_t>(16, V * (cfg->w_type == MOE_T_BF16 ? 2 : 4));
+        const bool wide = H % V == 0 && rows_aligned(x, x_stride, cfg->x_type, 16) &&
+                          rows_aligned(residual, residual_stride, cfg->x_type, 16) &&
+                          (!residual || rows_aligned(sum, sum_stride, cfg->x_type, 16)) &&
+                          rows_aligned(y, y_stride, cfg->y_type, YB) && rows_aligned(weight, 0, cfg->w_type, wb) &&
+                          rows_aligned(bias, 0, cfg->w_type, wb);
+        // few rows: one access a thread, for the shortest time of a row; many: several in flight
+        const bool few = T <= kFewRows;
+        if (wide) {
+            const int64_t pieces = H / V;
+            if (few && pieces <= kRowThreads) return launch_norm_forward<X, Y, R, V, 1>(a, cs);
+            if (pieces <= 4 * kRowThreads) return launch_norm_forward<X, Y, R, V, 4>(a, cs);
+        }
+        if (!wide && few && H <= 4 * kRowThreads) return launch_norm_forward<X, Y, R, 1, 4>(a, cs);
+        if (!wide && H <= 16 * kRowThreads) return launch_norm_forward<X, Y, R, 1, 16>(a, cs);
+        count_launch();
+        return wide ? launch_pdl(norm_forward_wide_kernel<X, Y, R, V>, dim3(unsigned(T)), dim3(kRowThreads), 0, cs, a)
+                    : launch_pdl(norm_forward_wide_kernel<X, Y, R, 1>, dim3(unsigned(T)), dim3(kRowThreads), 0, cs, a);
     });
-    count_launch();
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -276,27 +636,48 @@ moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* 
         !elem_aligned(rstd, MOE_T_FP32))
         return MOE_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int chunks = T == 0 ? 0 : norm_chunks(T);
     NormBwd a{dy, x, weight, dsum, mean, rstd, dx, static_cast<float*>(workspace), dy_stride, x_stride, dsum_stride,
-              dx_stride, T, int(H), chunks, cfg->w_type == MOE_T_BF16, dweight != nullptr, dbias != nullptr};
+              dx_stride, T, int(H), 0, cfg->w_type == MOE_T_BF16};
+    int chunks = 0;
     cudaError_t e = cudaSuccess;
     if (T > 0) {
         e = by_type(*cfg, [&](auto xt, auto yt, auto rms) {
             using X = decltype(xt);
             using Y = decltype(yt);
             constexpr bool R = decltype(rms)::value;
-            norm_backward_kernel<X, Y, R><<<unsigned(T), 256, 0, s>>>(a);
-            if (sums) norm_wgrad_kernel<X, Y, R><<<dim3(unsigned((H + 255) / 256), unsigned(chunks)), 256, 0, s>>>(a);
-            return cudaGetLastError();
+            constexpr int V = 16 / sizeof(X), NV = kColumns / V;
+            constexpr size_t YB = V * sizeof(Y) < 16 ? V * sizeof(Y) : 16;
+            const size_t wb = std::min<size_t>(16, V * (cfg->w_type == MOE_T_BF16 ? 2 : 4));
+            const bool wide = H % V == 0 && rows_aligned(x, x_stride, cfg->x_type, 16) &&
+                              rows_aligned(dsum, dsum_stride, cfg->x_type, 16) &&
+                              rows_aligned(dx, dx_stride, cfg->x_type, 16) &&
+                              rows_aligned(dy, dy_stride, cfg->y_type, YB) && rows_aligned(weight, 0, cfg->w_type, wb);
+            if (sums && H <= kColumns * kRowThreads) {
+                const RowShape r = row_shape(int((H + V - 1) / V), NV);
+                const int rows = wide ? r.threads / r.tpr : row_shape(int(H), kColumns).threads / row_shape(int(H), kColumns).tpr;
+                chunks = norm_chunks((T + rows - 1) / rows);
+                return wide ? launch_norm_backward<X, Y, R, V, NV, true>(a, chunks, s)
+                            : launch_norm_backward<X, Y, R, 1, kColumns, true>(a, chunks, s);
+            }
+            if (H <= kColumns * kRowThreads)
+                return wide ? launch_norm_backward<X, Y, R, V, NV, false>(a, 0, s)
+                            : launch_norm_backward<X, Y, R, 1, kColumns, false>(a, 0, s);
+            count_launch();
+            const dim3 grid{unsigned(T)}, block{kRowThreads};
+            const cudaError_t r = wide ? launch_pdl(norm_backward_wide_kernel<X, Y, R, V>, grid, block, 0, s, a)
+                                       : launch_pdl(norm_backward_wide_kernel<X, Y, R, 1>, grid, block, 0, s, a);
+            if (r != cudaSuccess || !sums) return r;
+            chunks = norm_chunks(T / 8);
+            count_launch();
+            return launch_pdl(norm_wgrad_kernel<X, Y, R>, dim3(unsigned((H + 255) / 256), unsigned(chunks)), dim3(256), 0,
+                              s, a);
         });
-        count_launch(sums ? 2 : 1);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
     }
     if (sums) {
-        norm_wgrad_reduce_kernel<<<unsigned((H + 255) / 256), 256, 0, s>>>(
-            static_cast<const float*>(workspace), chunks, int(H), dweight, dbias, g_type == MOE_G_BF16,
-            accumulate != 0);
-        e = cudaGetLastError();
+        e = launch_pdl(norm_wgrad_reduce_kernel, dim3(unsigned((H + 31) / 32), 2u), dim3(256), 0, s,
+                       static_cast<const float*>(workspace), chunks, int(H), dweight, dbias, g_type == MOE_G_BF16,
+                       accumulate != 0);
         count_launch();
     }
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
