@@ -9,6 +9,7 @@
 //   dw = sum_t dy xhat, db = sum_t dy.
 // All statistics and sums are fp32.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
@@ -21,7 +22,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxHidden = 32768;
-constexpr int kMaxChunks = 304;     // blocks of the backward that sum weight gradients: two per SM
+constexpr int kMaxChunks = 608;     // blocks of the backward that sum weight gradients: four per SM at most
 constexpr int kRowThreads = 512;    // most threads of a row: 128 registers each
 constexpr int kColumns = 16;        // columns of a thread in the backward, for rows up to kColumns * kRowThreads
 constexpr int kFewRows = 304;       // rows up to which the forward spreads a row over as many threads as it can
@@ -203,6 +204,163 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
     }
 }
 
+// ---- More rows: streamed through shared memory
+// A stage holds one row of each input for each row group of the block, brought by bulk copies;
+// `stages` of them are under way while one is worked on. A copy takes the 16-byte words that
+// cover its row, so rows may start anywhere; rows that start on 16 bytes are then read in
+// pieces of V elements, others one by one. One barrier of the block per sum serves the ring
+// too: after it, nobody still reads the rows before.
+constexpr int kMaxStages = 8;
+struct Stream {
+    int stages, arrays;
+    int row_bytes[3], slot[3];  // of each input: bytes of a row, and of its place in a stage
+    const char* from[3];
+    int64_t step[3];            // bytes from row to row
+    int group_bytes;            // of a row group's places
+};
+
+struct StreamRing {
+    const Stream& st;
+    uint8_t* mem;
+    uint64_t* full;
+    int64_t T;
+    int groups, s = 0;
+    uint32_t parity = 0;
+    // by the first warp: asks for the rows t0 ... t0 + groups - 1 (those below T) into stage `at`, a lane per row and input
+    __device__ __forceinline__ void ask(int at, int64_t t0) const {
+        const int lane = threadIdx.x & 31, n = int(T - t0 < groups ? T - t0 : groups) * st.arrays;
+        const int g = lane / st.arrays, i = lane - g * st.arrays;
+        const char* src = nullptr;
+        uint32_t bytes = 0;
+        if (lane < n) {
+            src = st.from[i] + (t0 + g) * st.step[i];
+            const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(src) & 15);
+            src -= off;
+            bytes = (off + uint32_t(st.row_bytes[i]) + 15) & ~15u;
+        }
+        const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+        if (lane == 0) mbar_arrive_expect_tx(full + at, total);
+        __syncwarp();
+        if (lane < n) {
+            uint8_t* to = mem + (int64_t(at) * groups + g) * st.group_bytes + (i > 0 ? st.slot[0] : 0) + (i > 1 ? st.slot[1] : 0);
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             smem_u32(to)),
+                         "l"(src), "r"(bytes), "r"(smem_u32(full + at))
+                         : "memory");
+        }
+    }
+    // the stage of the next rows, once they are there; bounded: a wait that gave up reads what is there
+    __device__ __forceinline__ void wait() const {
+        if (mbar_try_wait(full + s, parity)) return;
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(full + s, parity))
+            if (globaltimer_ns() - t0 > kWaitLimitNs) return;
+    }
+    // input i's row t of row group g in the current stage
+    template <typename E>
+    __device__ __forceinline__ const E* row(int g, int i, int64_t t) const {
+        const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(st.from[i] + t * st.step[i]) & 15);
+        const uint8_t* p = mem + (int64_t(s) * groups + g) * st.group_bytes + (i > 0 ? st.slot[0] : 0) + (i > 1 ? st.slot[1] : 0);
+        return reinterpret_cast<const E*>(p + off);
+    }
+    __device__ __forceinline__ void next() {
+        if (++s == st.stages) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+};
+
+template <typename XT, typename YT, bool RMS, int V, int NV>
+__global__ void __launch_bounds__(kRowThreads) norm_forward_stream_kernel(NormFwd a, const __grid_constant__ Stream st) {
+    __shared__ float part[2][2][32];
+    __shared__ uint64_t full[kMaxStages];
+    extern __shared__ __align__(128) uint8_t mem[];
+    if (threadIdx.x < st.stages) mbar_init(full + threadIdx.x, 1);
+    fence_mbar_init();
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const int tpr = a.tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, col = threadIdx.x - group * tpr;
+    const int64_t first = int64_t(blockIdx.x) * groups, step = int64_t(gridDim.x) * groups;
+    StreamRing ring{st, mem, full, a.T, groups};
+    if (threadIdx.x < 32)
+        for (int s = 0; s < st.stages; ++s)
+            if (first + s * step < a.T) ring.ask(s, first + s * step);
+    float w[NV][V], b[NV][V];  // a thread has the same columns in every row
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = (col + j * tpr) * V;
+#pragma unroll
+        for (int q = 0; q < V; ++q) w[j][q] = b[j][q] = 0.0f;
+        if (i >= a.H) continue;
+        load_w<V>(a.w, i, a.w_bf16, w[j]);
+        if (a.b) load_w<V>(a.b, i, a.w_bf16, b[j]);
+    }
+    int turn = 0;
+    for (int64_t t0 = first; t0 < a.T; t0 += step, turn ^= 1) {
+        const bool live = t0 + group < a.T;
+        const int64_t t = live ? t0 + group : t0;
+        ring.wait();
+        const XT* x = ring.row<XT>(t - t0, 0, t);
+        const XT* r = ring.row<XT>(t - t0, 1, t);
+        XT* sum_row = static_cast<XT*>(a.s) + t * a.ss;
+        float v[NV][V], sum[1] = {0.0f}, sq[1] = {0.0f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = (col + j * tpr) * V;
+            if (i >= a.H) continue;
+            load_v<V>(x + i, v[j]);
+            if (a.r) {
+                float f[V];
+                load_v<V>(r + i, f);
+#pragma unroll
+                for (int q = 0; q < V; ++q) v[j][q] = round_to(v[j][q] + f[q], x);
+                if (live) store_v<V>(sum_row + i, v[j]);
+            }
+#pragma unroll
+            for (int q = 0; q < V; ++q) sum[0] += v[j][q];
+        }
+        float mean = 0.0f;
+        if (!RMS) {
+            row_sum<1>(sum, tpr, part[turn][0]);
+            mean = sum[0] / a.H;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if ((col + j * tpr) * V < a.H)
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    v[j][q] -= mean;
+                    sq[0] = fmaf(v[j][q], v[j][q], sq[0]);
+                }
+        row_sum<1>(sq, tpr, part[turn][1]);
+        if (tpr == 32 && groups > 1) __syncthreads();  // the sums had no barrier
+        // the rows are in everybody's registers
+        if (threadIdx.x < 32 && t0 + st.stages * step < a.T) ring.ask(ring.s, t0 + st.stages * step);
+        ring.next();
+        if (!live) continue;
+        const float rstd = rsqrtf(sq[0] / a.H + a.eps);
+        YT* y = static_cast<YT*>(a.y) + t * a.ys;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = (col + j * tpr) * V;
+            if (i >= a.H) continue;
+            float o[V];
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                o[q] = v[j][q] * rstd * w[j][q];
+                if (a.b) o[q] += b[j][q];
+            }
+            store_v<V>(y + i, o);
+        }
+        if (col == 0) {
+            if (!RMS && a.mean) a.mean[t] = mean;
+            if (a.rstd) a.rstd[t] = rstd;
+        }
+    }
+}
+
 // Rows too wide for that: row blockIdx.x read three times (the second and third from cache)
 template <typename XT, typename YT, bool RMS, int V>
 __global__ void __launch_bounds__(kRowThreads) norm_forward_wide_kernel(NormFwd a) {
@@ -275,106 +433,126 @@ struct NormBwd {
     bool w_bf16;
 };
 
-// dx of a block's rows (blockIdx.x, + gridDim.x, ...), one row group of tpr threads per row; with SUMS
-// also the block's part of the weight gradients: a thread has the same columns in every row
-// and keeps their sums in registers, so x and dy are read once for all three gradients.
-template <typename XT, typename YT, bool RMS, int V, int NV, bool SUMS>
-__global__ void __launch_bounds__(kRowThreads) norm_backward_kernel(NormBwd a) {
+// dx of a block's rows, streamed like the forward's, and the block's part of the weight
+// gradients: a thread has the same columns in every row and keeps their sums in registers, so
+// x and dy are read once for all three gradients.
+template <typename XT, typename YT, bool RMS, int V, int NV>
+__global__ void __launch_bounds__(kRowThreads) norm_backward_kernel(NormBwd a, const __grid_constant__ Stream st) {
     __shared__ float part[2][2][32];
-    extern __shared__ float s_rows[];  // SUMS, several rows at a time: [2][H] per row group
+    __shared__ uint64_t full[kMaxStages];
+    extern __shared__ __align__(128) uint8_t mem[];
+    if (threadIdx.x < st.stages) mbar_init(full + threadIdx.x, 1);
+    fence_mbar_init();
+    __syncthreads();
     pdl_wait();
     pdl_trigger();
-    const int tpr = a.tpr, col = threadIdx.x % tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr;
-    float dw[SUMS ? NV : 1][V] = {}, db[SUMS ? NV : 1][V] = {};
-    int turn = 0;
-    for (int64_t t0 = int64_t(blockIdx.x) * groups; t0 < a.T; t0 += int64_t(gridDim.x) * groups, turn ^= 1) {
+    const int tpr = a.tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, col = threadIdx.x - group * tpr;
+    const int64_t first = int64_t(blockIdx.x) * groups, step = int64_t(gridDim.x) * groups;
+    StreamRing ring{st, mem, full, a.T, groups};
+    if (threadIdx.x < 32)
+        for (int s = 0; s < st.stages; ++s)
+            if (first + s * step < a.T) ring.ask(s, first + s * step);
+    float w[NV][V], dw[NV][V] = {}, db[NV][V] = {};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = (col + j * tpr) * V;
+#pragma unroll
+        for (int q = 0; q < V; ++q) w[j][q] = 0.0f;
+        if (i < a.H) load_w<V>(a.w, i, a.w_bf16, w[j]);
+    }
+    float mean = 0.0f, rstd = 0.0f;
+    if (first + group < a.T) {
+        if (!RMS) mean = a.mean[first + group];
+        rstd = a.rstd[first + group];
+    }
+    int turn = 0, before = -1;  // before: the stage of the rows before
+    for (int64_t t0 = first; t0 < a.T; t0 += step, turn ^= 1) {
         const bool live = t0 + group < a.T;
-        const int64_t t = live ? t0 + group : a.T - 1;
-        const XT* x = static_cast<const XT*>(a.x) + t * a.xs;
-        const YT* dy = static_cast<const YT*>(a.dy) + t * a.dys;
-        const XT* ds = a.ds ? static_cast<const XT*>(a.ds) + t * a.dss : nullptr;
-        float xh[NV][V], g[NV][V], d[NV][V];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = (col + j * tpr) * V;
-            if (i < a.H) {
-                load_v<V>(x + i, xh[j]);
-                load_v<V>(dy + i, g[j]);
-            }
+        const int64_t t = live ? t0 + group : t0;
+        float mean_after = 0.0f, rstd_after = 0.0f;  // under way during these rows
+        if (t0 + step + group < a.T) {
+            if (!RMS) mean_after = a.mean[t0 + step + group];
+            rstd_after = a.rstd[t0 + step + group];
         }
-        const float mean = RMS ? 0.0f : a.mean[t], rstd = a.rstd[t];
-        if (ds)
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int i = (col + j * tpr) * V;
-                if (i < a.H) load_v<V>(ds + i, d[j]);
-            }
-        float sum[2] = {0.0f, 0.0f};  // of g xhat, g
+        ring.wait();
+        const XT* x = ring.row<XT>(t - t0, 0, t);
+        const YT* dy = ring.row<YT>(t - t0, 1, t);
+        const XT* ds = ring.row<XT>(t - t0, 2, t);
+        float xh[NV][V], g[NV][V], sum[2] = {0.0f, 0.0f};  // of g xhat, g
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int i = (col + j * tpr) * V;
             if (i >= a.H) continue;
-            float w[V];
-            load_w<V>(a.w, i, a.w_bf16, w);
+            load_v<V>(x + i, xh[j]);
+            load_v<V>(dy + i, g[j]);
 #pragma unroll
             for (int q = 0; q < V; ++q) {
                 xh[j][q] = (xh[j][q] - mean) * rstd;
-                if (SUMS && live) {
-                    dw[SUMS ? j : 0][q] = fmaf(g[j][q], xh[j][q], dw[SUMS ? j : 0][q]);
-                    db[SUMS ? j : 0][q] += g[j][q];
+                if (live) {
+                    dw[j][q] = fmaf(g[j][q], xh[j][q], dw[j][q]);
+                    db[j][q] += g[j][q];
                 }
-                g[j][q] *= w[q];
+                g[j][q] *= w[j][q];
                 sum[0] = fmaf(g[j][q], xh[j][q], sum[0]);
                 sum[1] += g[j][q];
             }
         }
         row_sum<2>(sum, tpr, part[turn][0]);
+        if (tpr == 32 && groups > 1) __syncthreads();  // the sums had no barrier
+        // nobody reads the rows before any more
+        if (threadIdx.x < 32 && before >= 0 && t0 + (st.stages - 1) * step < a.T) ring.ask(before, t0 + (st.stages - 1) * step);
         const float mgx = sum[0] / a.H, mg = RMS ? 0.0f : sum[1] / a.H;
-        if (!live) continue;
         XT* dx = static_cast<XT*>(a.dx) + t * a.dxs;
+        if (live)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int i = (col + j * tpr) * V;
+                if (i >= a.H) continue;
+                float o[V], d[V];
+                if (a.ds) load_v<V>(ds + i, d);
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    o[q] = rstd * (g[j][q] - mg - xh[j][q] * mgx);
+                    if (a.ds) o[q] += d[q];
+                }
+                store_v<V>(dx + i, o);
+            }
+        mean = mean_after;
+        rstd = rstd_after;
+        before = ring.s;
+        ring.next();
+    }
+    if (a.part == nullptr) return;
+    float* out = a.part + int64_t(blockIdx.x) * 2 * a.H;
+    if (groups == 1) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int i = (col + j * tpr) * V;
             if (i >= a.H) continue;
-            float o[V];
 #pragma unroll
             for (int q = 0; q < V; ++q) {
-                o[q] = rstd * (g[j][q] - mg - xh[j][q] * mgx);
-                if (ds) o[q] += d[j][q];
+                out[i + q] = dw[j][q];
+                out[a.H + i + q] = db[j][q];
             }
-            store_v<V>(dx + i, o);
         }
+        return;
     }
-    if constexpr (SUMS) {
-        float* out = a.part + int64_t(blockIdx.x) * 2 * a.H;
-        if (groups > 1) {  // the row groups' sums, added in group order
-            for (int r = 0; r < groups; ++r) {
-                __syncthreads();
-                if (r != group) continue;
+    float* rows = reinterpret_cast<float*>(mem);  // the row groups' sums, added in group order
+    for (int r = 0; r < groups; ++r) {
+        __syncthreads();
+        if (r != group) continue;
 #pragma unroll
-                for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
-                    for (int q = 0; q < V; ++q) {
-                        const int i = (col + j * tpr) * V + q;
-                        if (i >= a.H) continue;
-                        s_rows[i] = (r ? s_rows[i] : 0.0f) + dw[j][q];
-                        s_rows[a.H + i] = (r ? s_rows[a.H + i] : 0.0f) + db[j][q];
-                    }
+            for (int q = 0; q < V; ++q) {
+                const int i = (col + j * tpr) * V + q;
+                if (i >= a.H) continue;
+                rows[i] = (r ? rows[i] : 0.0f) + dw[j][q];
+                rows[a.H + i] = (r ? rows[a.H + i] : 0.0f) + db[j][q];
             }
-            __syncthreads();
-            for (int i = threadIdx.x; i < 2 * a.H; i += blockDim.x) out[i] = s_rows[i];
-        } else {
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    const int i = (col + j * tpr) * V + q;
-                    if (i >= a.H) continue;
-                    out[i] = dw[j][q];
-                    out[a.H + i] = db[j][q];
-                }
-        }
     }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * a.H; i += blockDim.x) out[i] = rows[i];
 }
 
 // Rows too wide for that: dx of row blockIdx.x, read twice (the second time from cache)
@@ -524,6 +702,44 @@ RowShape row_shape(int pieces, int each) {
     return {tpr, tpr};
 }
 
+// The streamed kernels' shape, 16 columns a thread: row groups to a block of 256 threads (or one
+// of more), two such blocks an SM, the stages that its shared memory then holds, and no more blocks than have four rows a group
+// to themselves, so that the weight gradients' partial sums stay small beside the rows.
+constexpr int kStreamBytes = 212 << 10;  // of an SM's shared memory
+struct StreamShape {
+    int tpr, threads, blocks;
+    size_t smem;
+};
+void add_input(Stream& st, const void* p, int64_t stride, int32_t type, int64_t H) {
+    const int es = type == MOE_T_BF16 ? 2 : 4, i = st.arrays++;
+    st.from[i] = static_cast<const char*>(p);
+    st.step[i] = stride * es;
+    st.row_bytes[i] = int(H) * es;
+    st.slot[i] = (int(H) * es + 15 + 15) / 16 * 16;
+    st.group_bytes += st.slot[i];
+}
+StreamShape stream_shape(int64_t H, int V, int most, int64_t T, Stream& st) {
+    int sms = 152, device = 0;
+    if (cudaGetDevice(&device) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+    const RowShape r = row_shape(int((H + V - 1) / V), kColumns / V);
+    const int groups = r.threads / r.tpr, stage = groups * st.group_bytes;
+    int per = std::max(1, 512 / r.threads);  // up to 128 registers a thread
+    if (2 * stage * per > kStreamBytes) per = 1;
+    st.stages = std::min(kMaxStages, std::max(2, kStreamBytes / per / stage));
+    const int64_t blocks = std::min<int64_t>(std::min(per * sms, most), (T + 4 * groups - 1) / (4 * groups));
+    const size_t sums = groups > 1 ? 2 * size_t(H) * sizeof(float) : 0;
+    return {r.tpr, r.threads, int(blocks), std::max(size_t(st.stages) * size_t(stage), sums)};
+}
+
+template <typename... KArgs, typename A>
+cudaError_t launch_stream(void (*kernel)(KArgs...), const StreamShape& sh, A& a, Stream& st, cudaStream_t cs) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sh.smem));
+    if (e != cudaSuccess) return e;
+    a.tpr = sh.tpr;
+    count_launch();
+    return launch_pdl(kernel, dim3(unsigned(sh.blocks)), dim3(unsigned(sh.threads)), sh.smem, cs, a, st);
+}
+
 template <typename XT, typename YT, bool RMS, int V, int NV>
 cudaError_t launch_norm_forward(NormFwd& a, cudaStream_t st) {
     const RowShape r = row_shape(a.H / V + (a.H % V != 0), NV);
@@ -534,18 +750,6 @@ cudaError_t launch_norm_forward(NormFwd& a, cudaStream_t st) {
     const int64_t blocks = (a.T + threads / r.tpr - 1) / (threads / r.tpr);
     count_launch();
     return launch_pdl(norm_forward_kernel<XT, YT, RMS, V, NV>, dim3(unsigned(blocks)), dim3(unsigned(threads)), 0, st, a);
-}
-
-template <typename XT, typename YT, bool RMS, int V, int NV, bool SUMS>
-cudaError_t launch_norm_backward(NormBwd& a, int chunks, cudaStream_t st) {
-    const RowShape r = row_shape((a.H + V - 1) / V, NV);
-    const int rows = r.threads / r.tpr;
-    a.tpr = r.tpr;
-    const int64_t blocks = SUMS ? chunks : (a.T + rows - 1) / rows;
-    const size_t smem = SUMS && rows > 1 ? 2 * size_t(a.H) * sizeof(float) : 0;
-    count_launch();
-    return launch_pdl(norm_backward_kernel<XT, YT, RMS, V, NV, SUMS>, dim3(unsigned(blocks)), dim3(unsigned(r.threads)),
-                      smem, st, a);
 }
 
 }  // namespace
@@ -585,15 +789,20 @@ moe_status moe_norm_forward(const moe_norm_config* cfg, int64_t T, const void* x
                           (!residual || rows_aligned(sum, sum_stride, cfg->x_type, 16)) &&
                           rows_aligned(y, y_stride, cfg->y_type, YB) && rows_aligned(weight, 0, cfg->w_type, wb) &&
                           rows_aligned(bias, 0, cfg->w_type, wb);
-        // few rows: one access a thread, for the shortest time of a row; many: several in flight
+        // few rows: as many threads a row as can be, for the shortest time of a row; more: streamed
         const bool few = T <= kFewRows;
-        if (wide) {
-            const int64_t pieces = H / V;
-            if (few && pieces <= kRowThreads) return launch_norm_forward<X, Y, R, V, 1>(a, cs);
-            if (pieces <= 4 * kRowThreads) return launch_norm_forward<X, Y, R, V, 4>(a, cs);
-        }
+        const int64_t pieces = H / V;
+        if (wide && few && pieces <= kRowThreads) return launch_norm_forward<X, Y, R, V, 1>(a, cs);
         if (!wide && few && H <= 4 * kRowThreads) return launch_norm_forward<X, Y, R, 1, 4>(a, cs);
-        if (!wide && H <= 16 * kRowThreads) return launch_norm_forward<X, Y, R, 1, 16>(a, cs);
+        if (H <= kColumns * kRowThreads) {
+            Stream st{};
+            add_input(st, x, x_stride, cfg->x_type, H);
+            if (residual) add_input(st, residual, residual_stride, cfg->x_type, H);
+            const StreamShape sh = stream_shape(H, wide ? V : 1, INT_MAX, T, st);
+            return wide ? launch_stream(norm_forward_stream_kernel<X, Y, R, V, kColumns / V>, sh, a, st, cs)
+                        : launch_stream(norm_forward_stream_kernel<X, Y, R, 1, kColumns>, sh, a, st, cs);
+        }
+        if (wide && pieces <= 4 * kRowThreads) return launch_norm_forward<X, Y, R, V, 4>(a, cs);
         count_launch();
         return wide ? launch_pdl(norm_forward_wide_kernel<X, Y, R, V>, dim3(unsigned(T)), dim3(kRowThreads), 0, cs, a)
                     : launch_pdl(norm_forward_wide_kernel<X, Y, R, 1>, dim3(unsigned(T)), dim3(kRowThreads), 0, cs, a);
@@ -652,16 +861,19 @@ moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* 
                               rows_aligned(dsum, dsum_stride, cfg->x_type, 16) &&
                               rows_aligned(dx, dx_stride, cfg->x_type, 16) &&
                               rows_aligned(dy, dy_stride, cfg->y_type, YB) && rows_aligned(weight, 0, cfg->w_type, wb);
-            if (sums && H <= kColumns * kRowThreads) {
-                const RowShape r = row_shape(int((H + V - 1) / V), NV);
-                const int rows = wide ? r.threads / r.tpr : row_shape(int(H), kColumns).threads / row_shape(int(H), kColumns).tpr;
-                chunks = norm_chunks((T + rows - 1) / rows);
-                return wide ? launch_norm_backward<X, Y, R, V, NV, true>(a, chunks, s)
-                            : launch_norm_backward<X, Y, R, 1, kColumns, true>(a, chunks, s);
+            if (H <= kColumns * kRowThreads) {
+                Stream st{};
+                add_input(st, x, x_stride, cfg->x_type, H);
+                add_input(st, dy, dy_stride, cfg->y_type, H);
+                if (dsum) add_input(st, dsum, dsum_stride, cfg->x_type, H);
+                // dy is read from shared memory in pieces too: its rows start on 16 bytes as well, or none is
+                const bool w16 = wide && rows_aligned(dy, dy_stride, cfg->y_type, 16);
+                const StreamShape sh = stream_shape(H, w16 ? V : 1, kMaxChunks, T, st);
+                chunks = sh.blocks;
+                if (!sums) a.part = nullptr;
+                return w16 ? launch_stream(norm_backward_kernel<X, Y, R, V, NV>, sh, a, st, s)
+                           : launch_stream(norm_backward_kernel<X, Y, R, 1, kColumns>, sh, a, st, s);
             }
-            if (H <= kColumns * kRowThreads)
-                return wide ? launch_norm_backward<X, Y, R, V, NV, false>(a, 0, s)
-                            : launch_norm_backward<X, Y, R, 1, kColumns, false>(a, 0, s);
             count_launch();
             const dim3 grid{unsigned(T)}, block{kRowThreads};
             const cudaError_t r = wide ? launch_pdl(norm_backward_wide_kernel<X, Y, R, V>, grid, block, 0, s, a)
