@@ -24,7 +24,7 @@ namespace {
 constexpr int kMaxHidden = 32768;
 constexpr int kMaxChunks = 608;     // blocks of the backward that sum weight gradients: four per SM at most
 constexpr int kRowThreads = 512;    // most threads of a row: 128 registers each
-constexpr int kColumns = 16;        // columns of a thread in the backward, for rows up to kColumns * kRowThreads
+constexpr int kColumns = 16;        // columns of a thread where rows are streamed
 constexpr int kFewRows = 304;       // rows up to which the forward spreads a row over as many threads as it can
 
 // V consecutive elements as fp32: one 16-byte access (two for 8 fp32, one of 8 bytes for 4 bf16), or with V 1 a scalar
@@ -88,27 +88,41 @@ __device__ __forceinline__ float round_to(float v, const __nv_bfloat16*) {
     return __bfloat162float(__float2bfloat16_rn(v));
 }
 
-// Sums over the `tpr` threads (whole warps) of a row, several rows to a block; every thread of the
-// row gets them, in an order fixed by tpr. part: [2][32] per value, alternating, so that one
-// barrier a sum is enough.
+constexpr int kSumWarps = 32;  // places of a sum
+
+// Sums over the `warps` warps of a row (warps first, first + 1, ... of the block); every thread of
+// the row gets them, in an order fixed by the number of warps. part: 16 values for each sum, of
+// which the callers alternate two, so that one barrier a sum is enough; `threads`: of the barrier.
 template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float* part) {
+__device__ __forceinline__ void row_sum(float (&v)[N], int warps, int first, float* part) {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+    for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-    if (tpr == 32) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = tpr >> 5, first = warp / per * per;
-    if (lane == 0)
+        for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+    if (warps == 1) return;
+    if ((threadIdx.x & 31) == 0)
 #pragma unroll
-        for (int n = 0; n < N; ++n) part[n * 32 + warp] = v[n];
+        for (int n = 0; n < N; ++n) part[n * kSumWarps + (threadIdx.x >> 5)] = v[n];
     __syncthreads();
+    if (warps <= 4) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        float t = lane < per ? part[n * 32 + first + lane] : 0.0f;
+        for (int n = 0; n < N; ++n) {
+            float p[4];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        v[n] = t;
+            for (int w = 0; w < 4; ++w) p[w] = w < warps ? part[n * kSumWarps + first + w] : 0.0f;
+            v[n] = (p[0] + p[1]) + (p[2] + p[3]);
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            v[n] = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kSumWarps / 4; ++q)
+                if (4 * q < warps) {
+                    const float4 p = reinterpret_cast<const float4*>(part + n * kSumWarps)[q];
+                    v[n] += (p.x + p.y) + (p.z + p.w);
+                }
+        }
     }
 }
 
@@ -127,11 +141,13 @@ struct NormFwd {
 // written once, and the variance is of differences from the mean, not of squares.
 template <typename XT, typename YT, bool RMS, int V, int NV>
 __global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
-    __shared__ float part[2][32];
+    __shared__ __align__(16) float part[2][kSumWarps];
+    if (threadIdx.x < 32) part[0][threadIdx.x] = part[1][threadIdx.x] = 0.0f;
+    __syncthreads();
     pdl_wait();
     pdl_trigger();
-    const int tpr = a.tpr, col = threadIdx.x % tpr;
-    const int64_t row = int64_t(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
+    const int tpr = a.tpr, group = threadIdx.x / tpr, col = threadIdx.x - group * tpr, warps = tpr >> 5;
+    const int64_t row = int64_t(blockIdx.x) * (blockDim.x / tpr) + group;
     const bool live = row < a.T;  // the block's last rows may not exist; their threads join the sums
     const int64_t t = live ? row : a.T - 1;
     const XT* x = static_cast<const XT*>(a.x) + t * a.xs;
@@ -160,6 +176,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
                 if (i < a.H) store_v<V>(s + i, v[j]);
             }
     }
+    const float inv = 1.0f / a.H;
     float mean = 0.0f;
     if (!RMS) {
         float sum[1] = {0.0f};
@@ -168,8 +185,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
             if ((col + j * tpr) * V < a.H)
 #pragma unroll
                 for (int q = 0; q < V; ++q) sum[0] += v[j][q];
-        row_sum<1>(sum, tpr, part[0]);
-        mean = sum[0] / a.H;
+        row_sum<1>(sum, warps, group * warps, part[0]);
+        mean = sum[0] * inv;
     }
     float sq[1] = {0.0f};
 #pragma unroll
@@ -180,8 +197,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
                 v[j][q] -= mean;
                 sq[0] = fmaf(v[j][q], v[j][q], sq[0]);
             }
-    row_sum<1>(sq, tpr, part[1]);
-    const float rstd = rsqrtf(sq[0] / a.H + a.eps);
+    row_sum<1>(sq, warps, group * warps, part[1]);
+    const float rstd = rsqrtf(sq[0] * inv + a.eps);
     if (!live) return;
     YT* y = static_cast<YT*>(a.y) + t * a.ys;
 #pragma unroll
@@ -206,62 +223,78 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
 
 // ---- More rows: streamed through shared memory
 // A stage holds one row of each input for each row group of the block, brought by bulk copies;
-// `stages` of them are under way while one is worked on. A copy takes the 16-byte words that
-// cover its row, so rows may start anywhere; rows that start on 16 bytes are then read in
-// pieces of V elements, others one by one. One barrier of the block per sum serves the ring
-// too: after it, nobody still reads the rows before.
+// `stages` of them are under way while one is worked on. A copy takes the 16-byte words that cover
+// its row, so rows may start anywhere; rows that start on 16 bytes are then read in pieces of V
+// elements, others one by one. The barrier of a row's sums also says that nobody reads the rows
+// before any more: one warp, each in its turn, then asks for the rows that take their place. (A warp of its own for
+// that leaves 96 registers a thread where there are 128 now, and the sums of the weights' gradients
+// no longer fit: 16384 x 4096 backward 153 us against 100.)
 constexpr int kMaxStages = 8;
+// threads of a block: several row groups or one of up to 256 threads, two blocks an SM; or one of up to 512
+constexpr int kNarrow = 256, kWide = 512;
+constexpr int kStreamed = kColumns * kWide;  // the widest row that is streamed
 struct Stream {
     int stages, arrays;
-    int row_bytes[3], slot[3];  // of each input: bytes of a row, and of its place in a stage
+    int row_bytes[3], at[3];  // of each input: bytes of a row, and its place in a row group's part of a stage
     const char* from[3];
-    int64_t step[3];            // bytes from row to row
-    int group_bytes;            // of a row group's places
+    int64_t step[3];          // bytes from row to row
+    int group_bytes;          // a row group's part of a stage
+};
+
+// where a lane asks: the same input and row of a step every time (in shared memory: it is looked at once a row)
+struct Ask {
+    const char* from;
+    int64_t step;
+    int row_bytes, to;
 };
 
 struct StreamRing {
     const Stream& st;
-    uint8_t* mem;
     uint64_t* full;
-    int64_t T;
-    int groups, s = 0;
+    Ask* asks;
+    uint8_t* mem;
+    int groups;
+    int s = 0;
     uint32_t parity = 0;
-    // by the first warp: asks for the rows t0 ... t0 + groups - 1 (those below T) into stage `at`, a lane per row and input
-    __device__ __forceinline__ void ask(int at, int64_t t0) const {
-        const int lane = threadIdx.x & 31, n = int(T - t0 < groups ? T - t0 : groups) * st.arrays;
-        const int g = lane / st.arrays, i = lane - g * st.arrays;
-        const char* src = nullptr;
-        uint32_t bytes = 0;
-        if (lane < n) {
-            src = st.from[i] + (t0 + g) * st.step[i];
-            const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(src) & 15);
-            src -= off;
-            bytes = (off + uint32_t(st.row_bytes[i]) + 15) & ~15u;
+    __device__ __forceinline__ void init() const {
+        if (threadIdx.x < st.stages) mbar_init(full + threadIdx.x, 1);
+        if (threadIdx.x < 32) {
+            const int g = threadIdx.x / st.arrays, i = threadIdx.x - g * st.arrays;
+            asks[threadIdx.x] = g < groups ? Ask{st.from[i] + g * st.step[i], st.step[i], st.row_bytes[i], g * st.group_bytes + st.at[i]}
+                                           : Ask{nullptr, 0, 0, 0};
         }
+        fence_mbar_init();
+        __syncthreads();
+    }
+    // one warp: asks for the rows t0 ... t0 + groups - 1 (those below T) into stage `at`, a lane per row and input
+    __device__ __forceinline__ void ask(int at, unsigned t0, unsigned T) const {
+        const int lane = threadIdx.x & 31;
+        const Ask q = asks[lane];
+        const bool mine = q.row_bytes != 0 && unsigned(lane / st.arrays) < T - t0;
+        const char* src = q.from + t0 * q.step;
+        const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(src)) & 15u;
+        const uint32_t bytes = mine ? (off + uint32_t(q.row_bytes) + 15u) & ~15u : 0u;
         const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
         if (lane == 0) mbar_arrive_expect_tx(full + at, total);
         __syncwarp();
-        if (lane < n) {
-            uint8_t* to = mem + (int64_t(at) * groups + g) * st.group_bytes + (i > 0 ? st.slot[0] : 0) + (i > 1 ? st.slot[1] : 0);
+        if (mine)
             asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             smem_u32(to)),
-                         "l"(src), "r"(bytes), "r"(smem_u32(full + at))
+                             smem_u32(mem + at * groups * st.group_bytes + q.to)),
+                         "l"(src - off), "r"(bytes), "r"(smem_u32(full + at))
                          : "memory");
-        }
     }
-    // the stage of the next rows, once they are there; bounded: a wait that gave up reads what is there
+    // the next rows are there; bounded: a wait that gave up goes on with what is there (every copy ends)
     __device__ __forceinline__ void wait() const {
         if (mbar_try_wait(full + s, parity)) return;
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(full + s, parity))
             if (globaltimer_ns() - t0 > kWaitLimitNs) return;
     }
-    // input i's row t of row group g in the current stage
+    // input i's row t, of row group g in the current stage
     template <typename E>
-    __device__ __forceinline__ const E* row(int g, int i, int64_t t) const {
-        const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(st.from[i] + t * st.step[i]) & 15);
-        const uint8_t* p = mem + (int64_t(s) * groups + g) * st.group_bytes + (i > 0 ? st.slot[0] : 0) + (i > 1 ? st.slot[1] : 0);
-        return reinterpret_cast<const E*>(p + off);
+    __device__ __forceinline__ const E* row(int i, int g, unsigned t) const {
+        const uint32_t off = (uint32_t(reinterpret_cast<uintptr_t>(st.from[i])) + t * uint32_t(st.step[i])) & 15u;
+        return reinterpret_cast<const E*>(mem + (s * groups + g) * st.group_bytes + st.at[i] + off);
     }
     __device__ __forceinline__ void next() {
         if (++s == st.stages) {
@@ -271,23 +304,26 @@ struct StreamRing {
     }
 };
 
-template <typename XT, typename YT, bool RMS, int V, int NV>
-__global__ void __launch_bounds__(kRowThreads) norm_forward_stream_kernel(NormFwd a, const __grid_constant__ Stream st) {
-    __shared__ float part[2][2][32];
+template <typename XT, typename YT, bool RMS, int V, int NV, int NT>
+__global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_forward_stream_kernel(NormFwd a, const __grid_constant__ Stream st) {
+    __shared__ __align__(16) float part[2][2][kSumWarps];
     __shared__ uint64_t full[kMaxStages];
+    __shared__ Ask asks[32];
     extern __shared__ __align__(128) uint8_t mem[];
-    if (threadIdx.x < st.stages) mbar_init(full + threadIdx.x, 1);
-    fence_mbar_init();
-    __syncthreads();
+    if (threadIdx.x < 32)
+        part[0][0][threadIdx.x] = part[0][1][threadIdx.x] = part[1][0][threadIdx.x] = part[1][1][threadIdx.x] = 0.0f;
+    const int tpr = a.tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, col = threadIdx.x - group * tpr;
+    const unsigned T = unsigned(a.T), first = blockIdx.x * groups, step = gridDim.x * groups;  // T < 2^31
+    const int warps = tpr >> 5;
+    const float inv = 1.0f / a.H;
+    StreamRing ring{st, full, asks, mem, groups};
+    ring.init();
     pdl_wait();
     pdl_trigger();
-    const int tpr = a.tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, col = threadIdx.x - group * tpr;
-    const int64_t first = int64_t(blockIdx.x) * groups, step = int64_t(gridDim.x) * groups;
-    StreamRing ring{st, mem, full, a.T, groups};
-    if (threadIdx.x < 32)
-        for (int s = 0; s < st.stages; ++s)
-            if (first + s * step < a.T) ring.ask(s, first + s * step);
-    float w[NV][V], b[NV][V];  // a thread has the same columns in every row
+    const int warp = threadIdx.x >> 5;
+    if (warp == 0)
+        for (int s = 0; s < st.stages && first + s * step < T; ++s) ring.ask(s, first + s * step, T);
+    float w[NV][V], b[NV][V];  // a thread has the same columns in every row: their weights stay in registers
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int i = (col + j * tpr) * V;
@@ -297,34 +333,33 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_stream_kernel(NormFw
         load_w<V>(a.w, i, a.w_bf16, w[j]);
         if (a.b) load_w<V>(a.b, i, a.w_bf16, b[j]);
     }
-    int turn = 0;
-    for (int64_t t0 = first; t0 < a.T; t0 += step, turn ^= 1) {
-        const bool live = t0 + group < a.T;
-        const int64_t t = live ? t0 + group : t0;
+    int turn = 0, asker = 0;
+    for (unsigned t0 = first; t0 < T; t0 += step, turn ^= 1) {
+        const unsigned t = t0 + group;
+        const bool live = t < T;  // the last rows may not exist: their threads join the sums
         ring.wait();
-        const XT* x = ring.row<XT>(t - t0, 0, t);
-        const XT* r = ring.row<XT>(t - t0, 1, t);
-        XT* sum_row = static_cast<XT*>(a.s) + t * a.ss;
+        const XT* x = ring.row<XT>(0, group, t);
+        const XT* r = ring.row<XT>(1, group, t);
         float v[NV][V], sum[1] = {0.0f}, sq[1] = {0.0f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int i = (col + j * tpr) * V;
-            if (i >= a.H) continue;
+            if (i >= a.H || !live) continue;
             load_v<V>(x + i, v[j]);
             if (a.r) {
                 float f[V];
                 load_v<V>(r + i, f);
 #pragma unroll
                 for (int q = 0; q < V; ++q) v[j][q] = round_to(v[j][q] + f[q], x);
-                if (live) store_v<V>(sum_row + i, v[j]);
+                store_v<V>(static_cast<XT*>(a.s) + t * a.ss + i, v[j]);
             }
 #pragma unroll
             for (int q = 0; q < V; ++q) sum[0] += v[j][q];
         }
         float mean = 0.0f;
         if (!RMS) {
-            row_sum<1>(sum, tpr, part[turn][0]);
-            mean = sum[0] / a.H;
+            row_sum<1>(sum, warps, group * warps, part[turn][0]);
+            mean = sum[0] * inv;
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -334,13 +369,14 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_stream_kernel(NormFw
                     v[j][q] -= mean;
                     sq[0] = fmaf(v[j][q], v[j][q], sq[0]);
                 }
-        row_sum<1>(sq, tpr, part[turn][1]);
-        if (tpr == 32 && groups > 1) __syncthreads();  // the sums had no barrier
+        row_sum<1>(sq, warps, group * warps, part[turn][1]);
+        if (warps == 1) __syncthreads();  // the sums had no barrier
         // the rows are in everybody's registers
-        if (threadIdx.x < 32 && t0 + st.stages * step < a.T) ring.ask(ring.s, t0 + st.stages * step);
+        if (warp == asker && t0 + st.stages * step < T) ring.ask(ring.s, t0 + st.stages * step, T);
+        asker = asker + 1 == int(blockDim.x >> 5) ? 0 : asker + 1;
         ring.next();
         if (!live) continue;
-        const float rstd = rsqrtf(sq[0] / a.H + a.eps);
+        const float rstd = rsqrtf(sq[0] * inv + a.eps);
         YT* y = static_cast<YT*>(a.y) + t * a.ys;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -364,7 +400,9 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_stream_kernel(NormFw
 // Rows too wide for that: row blockIdx.x read three times (the second and third from cache)
 template <typename XT, typename YT, bool RMS, int V>
 __global__ void __launch_bounds__(kRowThreads) norm_forward_wide_kernel(NormFwd a) {
-    __shared__ float part[2][32];
+    __shared__ __align__(16) float part[2][kSumWarps];
+    if (threadIdx.x < 32) part[0][threadIdx.x] = part[1][threadIdx.x] = 0.0f;
+    __syncthreads();
     pdl_wait();
     pdl_trigger();
     const int64_t t = blockIdx.x;
@@ -389,7 +427,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_wide_kernel(NormFwd 
 #pragma unroll
             for (int q = 0; q < V; ++q) sum[0] += v[q];
         }
-        row_sum<1>(sum, blockDim.x, part[0]);
+        row_sum<1>(sum, blockDim.x >> 5, 0, part[0]);
         mean = sum[0] / a.H;
     }
     float sq[1] = {0.0f};
@@ -400,7 +438,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_wide_kernel(NormFwd 
 #pragma unroll
         for (int q = 0; q < V; ++q) sq[0] = fmaf(v[q] - mean, v[q] - mean, sq[0]);
     }
-    row_sum<1>(sq, blockDim.x, part[1]);
+    row_sum<1>(sq, blockDim.x >> 5, 0, part[1]);
     const float rstd = rsqrtf(sq[0] / a.H + a.eps);
 #pragma unroll 4
     for (int i = threadIdx.x * V; i < a.H; i += blockDim.x * V) {
@@ -436,89 +474,84 @@ struct NormBwd {
 // dx of a block's rows, streamed like the forward's, and the block's part of the weight
 // gradients: a thread has the same columns in every row and keeps their sums in registers, so
 // x and dy are read once for all three gradients.
-template <typename XT, typename YT, bool RMS, int V, int NV>
-__global__ void __launch_bounds__(kRowThreads) norm_backward_kernel(NormBwd a, const __grid_constant__ Stream st) {
-    __shared__ float part[2][2][32];
+template <typename XT, typename YT, bool RMS, int V, int NV, int NT>
+__global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_backward_kernel(NormBwd a, const __grid_constant__ Stream st) {
+    __shared__ __align__(16) float part[2][2][kSumWarps];
     __shared__ uint64_t full[kMaxStages];
+    __shared__ Ask asks[32];
     extern __shared__ __align__(128) uint8_t mem[];
-    if (threadIdx.x < st.stages) mbar_init(full + threadIdx.x, 1);
-    fence_mbar_init();
-    __syncthreads();
+    if (threadIdx.x < 32)
+        part[0][0][threadIdx.x] = part[0][1][threadIdx.x] = part[1][0][threadIdx.x] = part[1][1][threadIdx.x] = 0.0f;
+    const int tpr = a.tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, col = threadIdx.x - group * tpr;
+    const unsigned T = unsigned(a.T), first = blockIdx.x * groups, step = gridDim.x * groups;  // T < 2^31
+    const int warps = tpr >> 5;
+    const float inv = 1.0f / a.H;
+    StreamRing ring{st, full, asks, mem, groups};
+    ring.init();
     pdl_wait();
     pdl_trigger();
-    const int tpr = a.tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, col = threadIdx.x - group * tpr;
-    const int64_t first = int64_t(blockIdx.x) * groups, step = int64_t(gridDim.x) * groups;
-    StreamRing ring{st, mem, full, a.T, groups};
-    if (threadIdx.x < 32)
-        for (int s = 0; s < st.stages; ++s)
-            if (first + s * step < a.T) ring.ask(s, first + s * step);
-    float w[NV][V], dw[NV][V] = {}, db[NV][V] = {};
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int i = (col + j * tpr) * V;
-#pragma unroll
-        for (int q = 0; q < V; ++q) w[j][q] = 0.0f;
-        if (i < a.H) load_w<V>(a.w, i, a.w_bf16, w[j]);
-    }
+    const int warp = threadIdx.x >> 5;
+    if (warp == 0)
+        for (int s = 0; s < st.stages && first + s * step < T; ++s) ring.ask(s, first + s * step, T);
+    float dw[NV][V] = {}, db[NV][V] = {};
     float mean = 0.0f, rstd = 0.0f;
-    if (first + group < a.T) {
+    if (first + group < T) {
         if (!RMS) mean = a.mean[first + group];
         rstd = a.rstd[first + group];
     }
-    int turn = 0, before = -1;  // before: the stage of the rows before
-    for (int64_t t0 = first; t0 < a.T; t0 += step, turn ^= 1) {
-        const bool live = t0 + group < a.T;
-        const int64_t t = live ? t0 + group : t0;
+    int turn = 0, asker = 0, before = -1;  // before: the stage of the rows before
+    for (unsigned t0 = first; t0 < T; t0 += step, turn ^= 1) {
+        const unsigned t = t0 + group;
+        const bool live = t < T;  // the last rows may not exist: their threads join the sums
         float mean_after = 0.0f, rstd_after = 0.0f;  // under way during these rows
-        if (t0 + step + group < a.T) {
-            if (!RMS) mean_after = a.mean[t0 + step + group];
-            rstd_after = a.rstd[t0 + step + group];
+        if (t + step < T) {
+            if (!RMS) mean_after = a.mean[t + step];
+            rstd_after = a.rstd[t + step];
         }
         ring.wait();
-        const XT* x = ring.row<XT>(t - t0, 0, t);
-        const YT* dy = ring.row<YT>(t - t0, 1, t);
-        const XT* ds = ring.row<XT>(t - t0, 2, t);
+        const XT* x = ring.row<XT>(0, group, t);
+        const YT* dy = ring.row<YT>(1, group, t);
         float xh[NV][V], g[NV][V], sum[2] = {0.0f, 0.0f};  // of g xhat, g
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int i = (col + j * tpr) * V;
-            if (i >= a.H) continue;
+            if (i >= a.H || !live) continue;
             load_v<V>(x + i, xh[j]);
             load_v<V>(dy + i, g[j]);
+            float w[V];  // from cache every time: the registers go to the sums
+            load_w<V>(a.w, i, a.w_bf16, w);
 #pragma unroll
             for (int q = 0; q < V; ++q) {
                 xh[j][q] = (xh[j][q] - mean) * rstd;
-                if (live) {
-                    dw[j][q] = fmaf(g[j][q], xh[j][q], dw[j][q]);
-                    db[j][q] += g[j][q];
-                }
-                g[j][q] *= w[j][q];
+                dw[j][q] = fmaf(g[j][q], xh[j][q], dw[j][q]);
+                db[j][q] += g[j][q];
+                g[j][q] *= w[q];
                 sum[0] = fmaf(g[j][q], xh[j][q], sum[0]);
                 sum[1] += g[j][q];
             }
         }
-        row_sum<2>(sum, tpr, part[turn][0]);
-        if (tpr == 32 && groups > 1) __syncthreads();  // the sums had no barrier
+        row_sum<2>(sum, warps, group * warps, part[turn][0]);
+        if (warps == 1) __syncthreads();  // the sums had no barrier
         // nobody reads the rows before any more
-        if (threadIdx.x < 32 && before >= 0 && t0 + (st.stages - 1) * step < a.T) ring.ask(before, t0 + (st.stages - 1) * step);
-        const float mgx = sum[0] / a.H, mg = RMS ? 0.0f : sum[1] / a.H;
-        XT* dx = static_cast<XT*>(a.dx) + t * a.dxs;
+        if (warp == asker && before >= 0 && t0 + (st.stages - 1) * step < T) ring.ask(before, t0 + (st.stages - 1) * step, T);
+        const float mgx = sum[0] * inv, mg = RMS ? 0.0f : sum[1] * inv;
         if (live)
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int i = (col + j * tpr) * V;
                 if (i >= a.H) continue;
                 float o[V], d[V];
-                if (a.ds) load_v<V>(ds + i, d);
+                if (a.ds) load_v<V>(ring.row<XT>(2, group, t) + i, d);
 #pragma unroll
                 for (int q = 0; q < V; ++q) {
                     o[q] = rstd * (g[j][q] - mg - xh[j][q] * mgx);
                     if (a.ds) o[q] += d[q];
                 }
-                store_v<V>(dx + i, o);
+                store_v<V>(static_cast<XT*>(a.dx) + t * a.dxs + i, o);
             }
         mean = mean_after;
         rstd = rstd_after;
+        asker = asker + 1 == int(blockDim.x >> 5) ? 0 : asker + 1;
         before = ring.s;
         ring.next();
     }
@@ -558,7 +591,9 @@ __global__ void __launch_bounds__(kRowThreads) norm_backward_kernel(NormBwd a, c
 // Rows too wide for that: dx of row blockIdx.x, read twice (the second time from cache)
 template <typename XT, typename YT, bool RMS, int V>
 __global__ void __launch_bounds__(kRowThreads) norm_backward_wide_kernel(NormBwd a) {
-    __shared__ float part[2][32];
+    __shared__ __align__(16) float part[2][kSumWarps];
+    if (threadIdx.x < 32) part[0][threadIdx.x] = part[1][threadIdx.x] = 0.0f;
+    __syncthreads();
     pdl_wait();
     pdl_trigger();
     const int64_t t = blockIdx.x;
@@ -581,7 +616,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_backward_wide_kernel(NormBwd
             sum[1] += gq;
         }
     }
-    row_sum<2>(sum, blockDim.x, part[0]);
+    row_sum<2>(sum, blockDim.x >> 5, 0, part[0]);
     const float mgx = sum[0] / a.H, mg = RMS ? 0.0f : sum[1] / a.H;
 #pragma unroll 4
     for (int i = threadIdx.x * V; i < a.H; i += blockDim.x * V) {
@@ -705,7 +740,7 @@ RowShape row_shape(int pieces, int each) {
 // The streamed kernels' shape, 16 columns a thread: row groups to a block of 256 threads (or one
 // of more), two such blocks an SM, the stages that its shared memory then holds, and no more blocks than have four rows a group
 // to themselves, so that the weight gradients' partial sums stay small beside the rows.
-constexpr int kStreamBytes = 212 << 10;  // of an SM's shared memory
+constexpr int kStreamBytes = 176 << 10;  // of an SM's shared memory; what is left is cache, for the weights
 struct StreamShape {
     int tpr, threads, blocks;
     size_t smem;
@@ -715,15 +750,15 @@ void add_input(Stream& st, const void* p, int64_t stride, int32_t type, int64_t 
     st.from[i] = static_cast<const char*>(p);
     st.step[i] = stride * es;
     st.row_bytes[i] = int(H) * es;
-    st.slot[i] = (int(H) * es + 15 + 15) / 16 * 16;
-    st.group_bytes += st.slot[i];
+    st.at[i] = st.group_bytes;
+    st.group_bytes += (int(H) * es + 15 + 15) / 16 * 16;
 }
-StreamShape stream_shape(int64_t H, int V, int most, int64_t T, Stream& st) {
+StreamShape stream_shape(int64_t H, int most, int64_t T, Stream& st) {
     int sms = 152, device = 0;
     if (cudaGetDevice(&device) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
-    const RowShape r = row_shape(int((H + V - 1) / V), kColumns / V);
+    const RowShape r = row_shape(int((H + kColumns - 1) / kColumns), 1);
     const int groups = r.threads / r.tpr, stage = groups * st.group_bytes;
-    int per = std::max(1, 512 / r.threads);  // up to 128 registers a thread
+    int per = std::max(1, 512 / r.threads);  // 128 registers a thread
     if (2 * stage * per > kStreamBytes) per = 1;
     st.stages = std::min(kMaxStages, std::max(2, kStreamBytes / per / stage));
     const int64_t blocks = std::min<int64_t>(std::min(per * sms, most), (T + 4 * groups - 1) / (4 * groups));
@@ -794,13 +829,16 @@ moe_status moe_norm_forward(const moe_norm_config* cfg, int64_t T, const void* x
         const int64_t pieces = H / V;
         if (wide && few && pieces <= kRowThreads) return launch_norm_forward<X, Y, R, V, 1>(a, cs);
         if (!wide && few && H <= 4 * kRowThreads) return launch_norm_forward<X, Y, R, 1, 4>(a, cs);
-        if (H <= kColumns * kRowThreads) {
+        if (H <= kStreamed) {
             Stream st{};
             add_input(st, x, x_stride, cfg->x_type, H);
             if (residual) add_input(st, residual, residual_stride, cfg->x_type, H);
-            const StreamShape sh = stream_shape(H, wide ? V : 1, INT_MAX, T, st);
-            return wide ? launch_stream(norm_forward_stream_kernel<X, Y, R, V, kColumns / V>, sh, a, st, cs)
-                        : launch_stream(norm_forward_stream_kernel<X, Y, R, 1, kColumns>, sh, a, st, cs);
+            const StreamShape sh = stream_shape(H, INT_MAX, T, st);
+            if (sh.threads <= kNarrow)
+                return wide ? launch_stream(norm_forward_stream_kernel<X, Y, R, V, kColumns / V, kNarrow>, sh, a, st, cs)
+                            : launch_stream(norm_forward_stream_kernel<X, Y, R, 1, kColumns, kNarrow>, sh, a, st, cs);
+            return wide ? launch_stream(norm_forward_stream_kernel<X, Y, R, V, kColumns / V, kWide>, sh, a, st, cs)
+                        : launch_stream(norm_forward_stream_kernel<X, Y, R, 1, kColumns, kWide>, sh, a, st, cs);
         }
         if (wide && pieces <= 4 * kRowThreads) return launch_norm_forward<X, Y, R, V, 4>(a, cs);
         count_launch();
@@ -861,18 +899,21 @@ moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* 
                               rows_aligned(dsum, dsum_stride, cfg->x_type, 16) &&
                               rows_aligned(dx, dx_stride, cfg->x_type, 16) &&
                               rows_aligned(dy, dy_stride, cfg->y_type, YB) && rows_aligned(weight, 0, cfg->w_type, wb);
-            if (H <= kColumns * kRowThreads) {
+            if (H <= kStreamed) {
                 Stream st{};
                 add_input(st, x, x_stride, cfg->x_type, H);
                 add_input(st, dy, dy_stride, cfg->y_type, H);
                 if (dsum) add_input(st, dsum, dsum_stride, cfg->x_type, H);
                 // dy is read from shared memory in pieces too: its rows start on 16 bytes as well, or none is
                 const bool w16 = wide && rows_aligned(dy, dy_stride, cfg->y_type, 16);
-                const StreamShape sh = stream_shape(H, w16 ? V : 1, kMaxChunks, T, st);
+                const StreamShape sh = stream_shape(H, kMaxChunks, T, st);
                 chunks = sh.blocks;
                 if (!sums) a.part = nullptr;
-                return w16 ? launch_stream(norm_backward_kernel<X, Y, R, V, NV>, sh, a, st, s)
-                           : launch_stream(norm_backward_kernel<X, Y, R, 1, kColumns>, sh, a, st, s);
+                if (sh.threads <= kNarrow)
+                    return w16 ? launch_stream(norm_backward_kernel<X, Y, R, V, NV, kNarrow>, sh, a, st, s)
+                               : launch_stream(norm_backward_kernel<X, Y, R, 1, kColumns, kNarrow>, sh, a, st, s);
+                return w16 ? launch_stream(norm_backward_kernel<X, Y, R, V, NV, kWide>, sh, a, st, s)
+                           : launch_stream(norm_backward_kernel<X, Y, R, 1, kColumns, kWide>, sh, a, st, s);
             }
             count_launch();
             const dim3 grid{unsigned(T)}, block{kRowThreads};
