@@ -20,7 +20,7 @@ namespace moe {
 namespace {
 
 constexpr int kRouterWarps = 8;
-constexpr int kRouterBlocks = 304;  // most blocks of the forward, each with its own partial sums
+constexpr int kRouterBlocks = 304;  // most blocks of the forward, each with its own partial sums: two per SM
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -34,15 +34,21 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
-// order-preserving map of a float to an unsigned; 0 is kept for what cannot be chosen
+// order-preserving map of a float to an unsigned, and back; 0 is kept for what cannot be chosen
 // (-inf and NaN), both zeros get one key
 __device__ __forceinline__ uint32_t order_key(float v) {
     if (!(v > -INFINITY)) return 0u;
     const uint32_t b = __float_as_uint(v + 0.0f);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
+__device__ __forceinline__ float value_of(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+}
 
-__device__ __forceinline__ float sigmoid_exact(float z) { return 1.0f / (1.0f + expf(-z)); }
+// quotients by the hardware reciprocal: 1 ulp, a quarter of a rounded division's time
+__device__ __forceinline__ float reciprocal(float v) { return __fdividef(1.0f, v); }
+// 0 where exp(-z) overflows (the reciprocal's range ends at 2^126)
+__device__ __forceinline__ float sigmoid(float z) { return z < -87.0f ? 0.0f : reciprocal(1.0f + expf(-z)); }
 
 struct RouterArgs {
     const void* logits;
@@ -55,10 +61,9 @@ struct RouterArgs {
     // forward
     int* ids;
     float* probs;
-    float* part;  // per block: [E] score sums, [E] counts (as int), [1] sum of lse^2
+    float* part;  // per block: [E] counts (as int), [E] score sums, [1] sum of lse^2
     int* counts;
     float* losses;
-    int blocks;
     // backward
     const int* ids_in;
     const int* counts_in;
@@ -72,118 +77,153 @@ __device__ __forceinline__ float load_logit(const RouterArgs& a, int64_t t, int 
     return a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[t * a.ld + e])
                   : static_cast<const float*>(a.logits)[t * a.ld + e];
 }
-
-// a row's scores: p[j] = softmax or sigmoid of l[j] (0 where closed); returns the
-// log-sum-exp (0 for a row without an open expert); NaN anywhere makes lse NaN.
-// wanted: whether the log-sum-exp is needed with sigmoid scores
 template <int N>
-__device__ __forceinline__ float row_scores(const float (&l)[N], float (&p)[N], bool sigmoid, bool lse_wanted) {
-    float lse = 0.0f;
-    if (!sigmoid || lse_wanted) {
-        float m = -INFINITY;
+__device__ __forceinline__ void load_row(const RouterArgs& a, int64_t t, float (&l)[N]) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int j = 0; j < N; ++j) m = fmaxf(m, l[j]);  // fmaxf passes over NaN
-        m = warp_max(m);
-        const float base = m == -INFINITY ? 0.0f : m;
-        float z = 0.0f;
+    for (int j = 0; j < N; ++j) l[j] = lane + 32 * j < a.E ? load_logit(a, t, lane + 32 * j) : -INFINITY;
+}
+
+// A row's log-sum-exp parts: its largest logit m (0 for a row without an open expert), q[j] = exp(l[j] - m),
+// 1 / z with z = sum q (0 for such a row), and the log-sum-exp m + log z (0). NaN anywhere makes z NaN.
+struct RowSums {
+    float m, rz, lse;
+};
+template <int N>
+__device__ __forceinline__ RowSums row_exp(const float (&l)[N], float (&q)[N]) {
+    RowSums r;
+    r.m = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            p[j] = expf(l[j] - base);
-            z += p[j];
-        }
-        z = warp_sum(z);
-        if (z != 0.0f) {
-            lse = base + logf(z);
+    for (int j = 0; j < N; ++j) r.m = fmaxf(r.m, l[j]);  // fmaxf passes over NaN
+    r.m = warp_max(r.m);
+    if (r.m == -INFINITY) r.m = 0.0f;
+    float z = 0.0f;
 #pragma unroll
-            for (int j = 0; j < N; ++j) p[j] = p[j] / z;
-        }
+    for (int j = 0; j < N; ++j) {
+        q[j] = expf(l[j] - r.m);
+        z += q[j];
     }
-    if (sigmoid) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) p[j] = sigmoid_exact(l[j]);
-    }
-    return lse;
+    z = warp_sum(z);
+    const bool none = z == 0.0f;
+    r.rz = none ? 0.0f : reciprocal(z);
+    r.lse = none ? 0.0f : r.m + logf(z);
+    return r;
+}
+
+// losses from `term`, summed over the block's threads: counts times score sums, and from z; s_red: a place a warp
+__device__ __forceinline__ void put_losses(const RouterArgs& a, float term, float z, float* s_red) {
+    term = warp_sum(term);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = term;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    float total = 0.0f;
+    for (int w = 0; w < int(blockDim.x >> 5); ++w) total += s_red[w];
+    const float T = float(a.T);
+    a.losses[0] = a.T ? a.aux * float(a.E) / (float(a.k) * T) * (total / T) : 0.0f;
+    a.losses[1] = a.T ? a.z / T * z : 0.0f;
 }
 
 template <int N>
 __global__ void __launch_bounds__(32 * kRouterWarps) router_forward_kernel(RouterArgs a) {
-    extern __shared__ float smem[];  // [E] score sums, [E] counts, [warps] z terms
+    extern __shared__ float smem[];  // [E] counts, [E] score sums, [1] z terms, [warps]
+    pdl_wait();
+    pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int* s_counts = reinterpret_cast<int*>(smem);
     float* s_sum = smem + a.E;
-    const bool sums = a.counts != nullptr;
+    const bool sums = a.counts != nullptr, losses = a.losses != nullptr;
+    float psum[N] = {};
+    float zsum = 0.0f;
+    const int64_t step = int64_t(gridDim.x) * kRouterWarps;
+    int64_t t = int64_t(blockIdx.x) * kRouterWarps + warp;
+    float ahead[N];  // the next row, under way during this one
+    if (t < a.T) load_row<N>(a, t, ahead);
     if (sums) {
         for (int i = threadIdx.x; i < a.E; i += blockDim.x) s_counts[i] = 0;
         __syncthreads();
     }
-    const bool losses = a.losses != nullptr;
-    float psum[N] = {};
-    float zsum = 0.0f;
-    for (int64_t t = int64_t(blockIdx.x) * kRouterWarps + warp; t < a.T; t += int64_t(gridDim.x) * kRouterWarps) {
+    for (; t < a.T; t += step) {
         float l[N], p[N];
         bool bad = false;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int e = lane + 32 * j;
-            l[j] = e < a.E ? load_logit(a, t, e) : -INFINITY;
+            l[j] = ahead[j];
             bad |= isnan(l[j]);
         }
+        if (t + step < a.T) load_row<N>(a, t + step, ahead);
         bad = __any_sync(0xffffffffu, bad);
-        const float lse = row_scores<N>(l, p, a.sigmoid, losses);
-        if (losses) {
-            float total = 1.0f;
-            if (a.sigmoid) {
-                total = 0.0f;
+        RowSums r{0.0f, 0.0f, 0.0f};
+        if (!a.sigmoid || losses) r = row_exp<N>(l, p);
+        float rp = r.rz;  // a score's distribution over the experts: p * rp
+        if (a.sigmoid && (losses || a.bias)) {
+            float total = 0.0f;
 #pragma unroll
-                for (int j = 0; j < N; ++j) total += p[j];
-                total = warp_sum(total);
-                if (total == 0.0f) total = 1.0f;
+            for (int j = 0; j < N; ++j) {
+                p[j] = sigmoid(l[j]);
+                total += p[j];
             }
-#pragma unroll
-            for (int j = 0; j < N; ++j) psum[j] += p[j] / total;
-            zsum = fmaf(lse, lse, zsum);
+            if (losses) {
+                total = warp_sum(total);
+                rp = total == 0.0f ? 0.0f : reciprocal(total);
+            }
         }
+        if (losses) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) psum[j] = fmaf(p[j], rp, psum[j]);
+            zsum = fmaf(r.lse, r.lse, zsum);
+        }
+        // each lane's best key and its place; the lane that loses its best looks for the next
         uint32_t key[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int e = lane + 32 * j;
             key[j] = order_key(l[j]);
-            if (a.bias && key[j]) key[j] = order_key(p[j] + a.bias[e]);
+            if (a.bias && key[j]) key[j] = order_key((a.sigmoid ? p[j] : p[j] * r.rz) + a.bias[lane + 32 * j]);
         }
+        uint32_t best = 0;
+        int at = 0;
+#pragma unroll
+        for (int j = N - 1; j >= 0; --j)
+            if (key[j] >= best) {
+                best = key[j];
+                at = j;
+            }
         int my_id = -1;
-        float my_p = 0.0f;
+        uint32_t my_key = 0;
         for (int s = 0; s < a.k; ++s) {
-            uint32_t best = 0;
-#pragma unroll
-            for (int j = 0; j < N; ++j) best = max(best, key[j]);
-            best = __reduce_max_sync(0xffffffffu, best);
-            if (best == 0) break;
-            uint32_t at = 0xffffffffu;
-#pragma unroll
-            for (int j = N - 1; j >= 0; --j)
-                if (key[j] == best) at = lane + 32 * j;
-            at = __reduce_min_sync(0xffffffffu, at);
-            float v = 0.0f;
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (lane + 32 * j == int(at)) {
-                    v = p[j];
-                    key[j] = 0;
-                }
-            v = __shfl_sync(0xffffffffu, v, at & 31);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+            if (top == 0) break;
+            const uint32_t id = __reduce_min_sync(0xffffffffu, best == top ? uint32_t(lane + 32 * at) : 0xffffffffu);
             if (lane == s) {
-                my_id = int(at);
-                my_p = v;
+                my_id = int(id);
+                my_key = top;
+            }
+            if (uint32_t(lane + 32 * at) == id && best == top) {
+                best = 0;
+                int next = 0;
+#pragma unroll
+                for (int j = N - 1; j >= 0; --j) {
+                    if (j == at) key[j] = 0;
+                    if (key[j] >= best) {
+                        best = key[j];
+                        next = j;
+                    }
+                }
+                at = next;
             }
         }
+        // the chosen scores, one a lane: from the logit, which the key still is (not with a bias)
+        float my_l = value_of(my_key);
+        if (a.bias && my_id >= 0) my_l = load_logit(a, t, my_id);
+        float my_p = my_id < 0 ? 0.0f : a.sigmoid ? sigmoid(my_l) : expf(my_l - r.m) * r.rz;
         if (a.normalise) {
             const float total = warp_sum(my_p);
-            if (total != 0.0f) my_p = my_p / total;
+            if (total != 0.0f) my_p = my_p * reciprocal(total);
         }
         if (lane < a.k) {
             a.ids[t * a.k + lane] = my_id;
             a.probs[t * a.k + lane] = bad ? NAN : my_p * a.scale;
-            if (sums && my_id >= 0) atomicAdd(s_counts + my_id, 1);
+            if (sums && my_id >= 0) atomicAdd(s_counts + my_id, 1);  // integers: any order
         }
     }
     if (!sums) return;
@@ -200,6 +240,15 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_forward_kernel(Route
         }
     }
     __syncthreads();
+    if (gridDim.x == 1) {  // nothing to add up with
+        float term = 0.0f;
+        for (int i = threadIdx.x; i < a.E; i += blockDim.x) {
+            a.counts[i] = s_counts[i];
+            if (losses) term = fmaf(float(s_counts[i]), s_sum[i], term);
+        }
+        if (losses) put_losses(a, term, s_sum[a.E], s_sum + a.E + 1);
+        return;
+    }
     float* part = a.part + int64_t(blockIdx.x) * (2 * a.E + 1);
     for (int i = threadIdx.x; i < a.E; i += blockDim.x) {
         reinterpret_cast<int*>(part)[i] = s_counts[i];
@@ -208,108 +257,126 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_forward_kernel(Route
     if (threadIdx.x == 0 && losses) part[2 * a.E] = s_sum[a.E];
 }
 
-// counts and losses from the blocks' partial sums, in block order
-__global__ void __launch_bounds__(1024) router_finish_kernel(RouterArgs a) {
-    __shared__ float s_red[32];
-    const int e = threadIdx.x;
+// counts and losses from the blocks' partial sums: 1024 / experts threads an expert (a power of two), each adding
+// every such block in order, then their sums in order
+__global__ void __launch_bounds__(1024) router_finish_kernel(RouterArgs a, int blocks, int padded) {
+    __shared__ int s_n[1024];
+    __shared__ float s_p[1024], s_red[32];
+    pdl_wait();
+    pdl_trigger();
+    const int e = threadIdx.x & (padded - 1), slice = threadIdx.x / padded, slices = 1024 / padded;
     const int64_t step = 2 * a.E + 1;
-    float term = 0.0f;
+    int n = 0;
+    float p = 0.0f, z = 0.0f;
     if (e < a.E) {
-        int n = 0;
-        float p = 0.0f;
-        for (int b = 0; b < a.blocks; ++b) {
+#pragma unroll 8
+        for (int b = slice; b < blocks; b += slices) {
             n += reinterpret_cast<const int*>(a.part + b * step)[e];
             if (a.losses) p += a.part[b * step + a.E + e];
         }
-        a.counts[e] = n;
-        term = float(n) * p;
     }
-    if (!a.losses) return;
-    term = warp_sum(term);
-    if ((e & 31) == 0) s_red[e >> 5] = term;
+    if (a.losses && threadIdx.x < 32) {  // the z terms: lane l adds blocks l, l + 32, ...
+        for (int b = threadIdx.x; b < blocks; b += 32) z += a.part[b * step + 2 * a.E];
+        z = warp_sum(z);
+    }
+    s_n[threadIdx.x] = n;
+    s_p[threadIdx.x] = p;
     __syncthreads();
-    if (e == 0) {
-        float total = 0.0f, z = 0.0f;
-        for (int w = 0; w < 32; ++w) total += s_red[w];
-        for (int b = 0; b < a.blocks; ++b) z += a.part[b * step + 2 * a.E];
-        const float T = float(a.T);
-        a.losses[0] = a.T ? a.aux * float(a.E) / (float(a.k) * T) * (total / T) : 0.0f;
-        a.losses[1] = a.T ? a.z / T * z : 0.0f;
-    }
+    if (slice == 0)
+        for (int w = 1; w < slices; ++w) {
+            n += s_n[w * padded + e];
+            p += s_p[w * padded + e];
+        }
+    const bool mine = slice == 0 && e < a.E;
+    if (mine) a.counts[e] = n;
+    if (a.losses) put_losses(a, mine ? float(n) * p : 0.0f, z, s_red);
 }
 
 template <int N>
 __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(RouterArgs a) {
     extern __shared__ float smem[];  // per warp: [E] gradients of the chosen scores
+    pdl_wait();
+    pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = int64_t(blockIdx.x) * kRouterWarps + warp;
     if (t >= a.T) return;
     float* s_d = smem + warp * a.E;
     const bool aux = a.aux != 0.0f && a.loss_grad != 0.0f;
     const bool zl = a.z != 0.0f && a.loss_grad != 0.0f;
-    float l[N], p[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const int e = lane + 32 * j;
-        l[j] = e < a.E ? load_logit(a, t, e) : -INFINITY;
-        if (e < a.E) s_d[e] = 0.0f;
-    }
-    const float lse = row_scores<N>(l, p, a.sigmoid, zl);
-    __syncwarp();
+    float l[N], q[N];
+    load_row<N>(a, t, l);
     int id = lane < a.k ? a.ids_in[t * a.k + lane] : -1;
     if (id >= a.E) id = -1;
     float d = id >= 0 ? a.dprobs[t * a.k + lane] * a.scale : 0.0f;
-    float c = 0.0f;
-    if (id >= 0) {
-        const float v = load_logit(a, t, id);
-        c = a.sigmoid ? sigmoid_exact(v) : expf(v - lse);
-    }
+    const float my_l = id >= 0 ? load_logit(a, t, id) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (lane + 32 * j < a.E) s_d[lane + 32 * j] = 0.0f;
+    RowSums r{0.0f, 0.0f, 0.0f};
+    if (!a.sigmoid || zl) r = row_exp<N>(l, q);
+    __syncwarp();
+    const float c = id < 0 ? 0.0f : a.sigmoid ? sigmoid(my_l) : expf(my_l - r.m) * r.rz;
     if (a.normalise) {
-        float total = warp_sum(c);
-        if (total == 0.0f) total = 1.0f;
-        const float mean = warp_sum(d * (c / total));
-        d = id >= 0 ? (d - mean) / total : 0.0f;
+        const float total = warp_sum(c);
+        const float rt = total == 0.0f ? 1.0f : reciprocal(total);
+        const float mean = warp_sum(d * (c * rt));
+        d = id >= 0 ? (d - mean) * rt : 0.0f;
     }
     if (id >= 0) s_d[id] = d;
     __syncwarp();
     const float w_aux = aux ? a.loss_grad * a.aux * float(a.E) / (float(a.k) * float(a.T)) / float(a.T) : 0.0f;
-    float total = 1.0f;
-    if (a.sigmoid && aux) {
-        total = 0.0f;
+    const float w_z = zl ? a.loss_grad * 2.0f * a.z / float(a.T) * r.lse * r.rz : 0.0f;  // times exp(l - m)
+    float g[N];
+    if (a.sigmoid) {
+        float p[N], rp = 0.0f, dot = 0.0f;
 #pragma unroll
-        for (int j = 0; j < N; ++j) total += p[j];
-        total = warp_sum(total);
-        if (total == 0.0f) total = 1.0f;
-    }
-    // v: gradient of the score (softmax) or of the distribution over the experts (sigmoid)
-    float v[N], dot = 0.0f;
+        for (int j = 0; j < N; ++j) p[j] = sigmoid(l[j]);
+        if (aux) {
+            // with P = p / sum(p): gradient (w - sum(w P)) / sum(p) of the balance loss at each score
+            float total = 0.0f, wp = 0.0f;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const int e = lane + 32 * j;
-        v[j] = 0.0f;
-        if (e < a.E) {
-            v[j] = aux ? w_aux * float(a.counts_in[e]) : 0.0f;
-            if (!a.sigmoid) v[j] += s_d[e];
+            for (int j = 0; j < N; ++j) {
+                g[j] = lane + 32 * j < a.E ? w_aux * float(a.counts_in[lane + 32 * j]) : 0.0f;
+                total += p[j];
+                wp = fmaf(g[j], p[j], wp);
+            }
+            total = warp_sum(total);
+            rp = total == 0.0f ? 1.0f : reciprocal(total);
+            dot = warp_sum(wp) * rp;
         }
-        dot = fmaf(v[j], p[j] / total, dot);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (lane + 32 * j >= a.E) continue;
+            const float v = s_d[lane + 32 * j] + (aux ? (g[j] - dot) * rp : 0.0f);
+            g[j] = v * p[j] * (1.0f - p[j]);
+            if (zl) g[j] = fmaf(w_z, q[j], g[j]);
+        }
+    } else {
+        float dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            g[j] = 0.0f;
+            if (lane + 32 * j >= a.E) continue;
+            g[j] = s_d[lane + 32 * j];
+            if (aux) g[j] = fmaf(w_aux, float(a.counts_in[lane + 32 * j]), g[j]);
+            dot = fmaf(g[j], q[j], dot);
+        }
+        dot = warp_sum(dot) * r.rz;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            g[j] = q[j] * r.rz * (g[j] - dot);
+            if (zl) g[j] = fmaf(w_z, q[j], g[j]);
+        }
     }
-    dot = warp_sum(dot);
-    const float w_z = zl ? a.loss_grad * 2.0f * a.z / float(a.T) * lse : 0.0f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         const int e = lane + 32 * j;
         if (e >= a.E) continue;
-        float g;
-        if (a.sigmoid)
-            g = (s_d[e] + (v[j] - dot) / total) * p[j] * (1.0f - p[j]);
-        else
-            g = p[j] * (v[j] - dot);
-        if (zl) g += w_z * (a.sigmoid ? expf(l[j] - lse) : p[j]);
-        if (l[j] == -INFINITY) g = 0.0f;
+        const float v = l[j] == -INFINITY ? 0.0f : g[j];
         if (a.bf16)
-            static_cast<__nv_bfloat16*>(a.dlogits)[t * a.dld + e] = __float2bfloat16_rn(g);
+            static_cast<__nv_bfloat16*>(a.dlogits)[t * a.dld + e] = __float2bfloat16_rn(v);
         else
-            static_cast<float*>(a.dlogits)[t * a.dld + e] = g;
+            static_cast<float*>(a.dlogits)[t * a.dld + e] = v;
     }
 }
 
@@ -345,14 +412,18 @@ RouterArgs router_args(const moe_router_config* c, int64_t T, const void* logits
     return a;
 }
 
+// the build for E experts, 32 N of them at most
 template <typename F>
-void by_experts(int E, F f) {
-    if (E <= 32) f(std::integral_constant<int, 1>());
-    else if (E <= 64) f(std::integral_constant<int, 2>());
-    else if (E <= 128) f(std::integral_constant<int, 4>());
-    else if (E <= 256) f(std::integral_constant<int, 8>());
-    else if (E <= 512) f(std::integral_constant<int, 16>());
-    else f(std::integral_constant<int, 32>());
+cudaError_t by_experts(int E, F f) {
+    const int n = (E + 31) / 32;
+    if (n <= 1) return f(std::integral_constant<int, 1>());
+    if (n <= 2) return f(std::integral_constant<int, 2>());
+    if (n <= 3) return f(std::integral_constant<int, 3>());
+    if (n <= 4) return f(std::integral_constant<int, 4>());
+    if (n <= 8) return f(std::integral_constant<int, 8>());
+    if (n <= 12) return f(std::integral_constant<int, 12>());
+    if (n <= 16) return f(std::integral_constant<int, 16>());
+    return f(std::integral_constant<int, 32>());
 }
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -393,22 +464,25 @@ moe_status moe_router_forward(const moe_router_config* cfg, int64_t T, const voi
     a.part = static_cast<float*>(workspace);
     a.counts = counts;
     a.losses = losses;
-    a.blocks = router_blocks(T);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (T == 0) a.blocks = 0;
+    const int blocks = T == 0 ? 0 : router_blocks(T);
+    cudaError_t e = cudaSuccess;
     if (T > 0) {
-        const size_t smem = (2 * size_t(a.E) + 1) * sizeof(float);
-        by_experts(a.E, [&](auto n) {
-            router_forward_kernel<decltype(n)::value><<<a.blocks, 32 * kRouterWarps, smem, s>>>(a);
+        const size_t smem = (2 * size_t(a.E) + 1 + kRouterWarps) * sizeof(float);
+        e = by_experts(a.E, [&](auto n) {
+            return launch_pdl(router_forward_kernel<decltype(n)::value>, dim3(unsigned(blocks)), dim3(32 * kRouterWarps),
+                              smem, s, a);
         });
         count_launch();
-        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
     }
-    if (counts) {
-        router_finish_kernel<<<1, 1024, 0, s>>>(a);
+    if (counts && blocks != 1) {
+        int padded = 32;
+        while (padded < a.E) padded *= 2;
+        e = launch_pdl(router_finish_kernel, dim3(1), dim3(1024), 0, s, a, blocks, padded);
         count_launch();
     }
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_router_backward(const moe_router_config* cfg, int64_t T, const void* logits, int64_t logits_stride,
@@ -435,12 +509,12 @@ moe_status moe_router_backward(const moe_router_config* cfg, int64_t T, const vo
     a.dld = dlogits_stride;
     const int64_t blocks = (T + kRouterWarps - 1) / kRouterWarps;
     const size_t smem = size_t(kRouterWarps) * size_t(a.E) * sizeof(float);
-    by_experts(a.E, [&](auto n) {
-        router_backward_kernel<decltype(n)::value>
-            <<<unsigned(blocks), 32 * kRouterWarps, smem, static_cast<cudaStream_t>(stream)>>>(a);
+    const cudaError_t e = by_experts(a.E, [&](auto n) {
+        return launch_pdl(router_backward_kernel<decltype(n)::value>, dim3(unsigned(blocks)), dim3(32 * kRouterWarps), smem,
+                          static_cast<cudaStream_t>(stream), a);
     });
     count_launch();
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"
