@@ -7,7 +7,7 @@
 // The choice compares logits, mapped to unsigned integers of the same order, one
 // warp-wide maximum and one warp-wide minimum index per slot: exact, ties to the
 // lower id, whatever the scores round to.
-#include <cfloat>
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -19,8 +19,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kRouterWarps = 8;
+constexpr int kRouterWarps = 8;     // of a block of the backward
 constexpr int kRouterBlocks = 304;  // most blocks of the forward, each with its own partial sums: two per SM
+// warps of a block of the forward for rows of 32 n experts: as many as the registers of two blocks an SM allow
+constexpr int forward_warps(int n) { return n <= 4 ? 24 : n <= 8 ? 16 : 8; }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -61,7 +63,8 @@ struct RouterArgs {
     // forward
     int* ids;
     float* probs;
-    float* part;  // per block: [E] counts (as int), [E] score sums, [1] sum of lse^2
+    float* part;    // per block: [E] counts (as int), [E] score sums, [1] sum of lse^2
+    float* finish;  // see router_finish_kernel
     int* counts;
     float* losses;
     // backward
@@ -110,23 +113,18 @@ __device__ __forceinline__ RowSums row_exp(const float (&l)[N], float (&q)[N]) {
     return r;
 }
 
-// losses from `term`, summed over the block's threads: counts times score sums, and from z; s_red: a place a warp
-__device__ __forceinline__ void put_losses(const RouterArgs& a, float term, float z, float* s_red) {
-    term = warp_sum(term);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = term;
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-    float total = 0.0f;
-    for (int w = 0; w < int(blockDim.x >> 5); ++w) total += s_red[w];
+// losses from the sums over the experts (counts times score sums) and over the tokens (log-sum-exp squared)
+__device__ __forceinline__ void put_losses(const RouterArgs& a, float total, float z) {
     const float T = float(a.T);
     a.losses[0] = a.T ? a.aux * float(a.E) / (float(a.k) * T) * (total / T) : 0.0f;
     a.losses[1] = a.T ? a.z / T * z : 0.0f;
 }
 
 template <int N>
-__global__ void __launch_bounds__(32 * kRouterWarps) router_forward_kernel(RouterArgs a) {
-    extern __shared__ float smem[];  // [E] counts, [E] score sums, [1] z terms, [warps]
+__global__ void __launch_bounds__(32 * forward_warps(N)) router_forward_kernel(RouterArgs a) {
+    constexpr int kWarps = forward_warps(N);
+    __shared__ float s_z[kWarps];
+    extern __shared__ float smem[];  // [E] counts, [warps][E] score sums
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -135,10 +133,11 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_forward_kernel(Route
     const bool sums = a.counts != nullptr, losses = a.losses != nullptr;
     float psum[N] = {};
     float zsum = 0.0f;
-    const int64_t step = int64_t(gridDim.x) * kRouterWarps;
-    int64_t t = int64_t(blockIdx.x) * kRouterWarps + warp;
+    const int64_t step = int64_t(gridDim.x) * kWarps;
+    int64_t t = int64_t(blockIdx.x) * kWarps + warp;
     float ahead[N];  // the next row, under way during this one
     if (t < a.T) load_row<N>(a, t, ahead);
+    if (threadIdx.x == 0 && blockIdx.x == 0 && losses) reinterpret_cast<unsigned*>(a.finish)[0] = 0;
     if (sums) {
         for (int i = threadIdx.x; i < a.E; i += blockDim.x) s_counts[i] = 0;
         __syncthreads();
@@ -228,16 +227,21 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_forward_kernel(Route
     }
     if (!sums) return;
     // the warps' score sums, added in warp order
-    for (int w = 0; w < kRouterWarps && losses; ++w) {
-        __syncthreads();
-        if (warp == w) {
+    if (losses) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const int e = lane + 32 * j;
-                if (e < a.E) s_sum[e] = (w ? s_sum[e] : 0.0f) + psum[j];
-            }
-            if (lane == 0) s_sum[a.E] = (w ? s_sum[a.E] : 0.0f) + zsum;
+        for (int j = 0; j < N; ++j)
+            if (lane + 32 * j < a.E) s_sum[warp * a.E + lane + 32 * j] = psum[j];
+        if (lane == 0) s_z[warp] = zsum;
+    }
+    __syncthreads();
+    if (losses) {
+        for (int i = threadIdx.x; i < a.E; i += blockDim.x) {
+            float v = s_sum[i];
+            for (int w = 1; w < kWarps; ++w) v += s_sum[w * a.E + i];
+            s_sum[i] = v;
         }
+        if (threadIdx.x == 0)
+            for (int w = 1; w < kWarps; ++w) zsum += s_z[w];
     }
     __syncthreads();
     if (gridDim.x == 1) {  // nothing to add up with
@@ -246,7 +250,15 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_forward_kernel(Route
             a.counts[i] = s_counts[i];
             if (losses) term = fmaf(float(s_counts[i]), s_sum[i], term);
         }
-        if (losses) put_losses(a, term, s_sum[a.E], s_sum + a.E + 1);
+        if (losses) {
+            term = warp_sum(term);
+            if (lane == 0) s_z[warp] = term;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                for (int w = 1; w < kWarps; ++w) term += s_z[w];
+                put_losses(a, term, zsum);
+            }
+        }
         return;
     }
     float* part = a.part + int64_t(blockIdx.x) * (2 * a.E + 1);
@@ -254,42 +266,61 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_forward_kernel(Route
         reinterpret_cast<int*>(part)[i] = s_counts[i];
         if (losses) part[a.E + i] = s_sum[i];
     }
-    if (threadIdx.x == 0 && losses) part[2 * a.E] = s_sum[a.E];
+    if (threadIdx.x == 0 && losses) part[2 * a.E] = zsum;
 }
 
-// counts and losses from the blocks' partial sums: 1024 / experts threads an expert (a power of two), each adding
-// every such block in order, then their sums in order
-__global__ void __launch_bounds__(1024) router_finish_kernel(RouterArgs a, int blocks, int padded) {
-    __shared__ int s_n[1024];
-    __shared__ float s_p[1024], s_red[32];
+// Counts and losses from the blocks' partial sums. Block g: 32 experts, warp w adding the blocks w,
+// w + 8, ... in order, then the warps' sums in warp order; block 0 the z terms too. The block that
+// finishes last adds up the experts' parts of the balance loss, in block order.
+// a.finish: [0] blocks done (0 at the start), [1] z, [2 + g] block g's part.
+__global__ void __launch_bounds__(256) router_finish_kernel(RouterArgs a, int blocks) {
+    __shared__ int s_n[8][32];
+    __shared__ float s_p[8][32];
     pdl_wait();
     pdl_trigger();
-    const int e = threadIdx.x & (padded - 1), slice = threadIdx.x / padded, slices = 1024 / padded;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
     const int64_t step = 2 * a.E + 1;
     int n = 0;
-    float p = 0.0f, z = 0.0f;
+    float p = 0.0f;
     if (e < a.E) {
+        const float* from = a.part + e;
 #pragma unroll 8
-        for (int b = slice; b < blocks; b += slices) {
-            n += reinterpret_cast<const int*>(a.part + b * step)[e];
-            if (a.losses) p += a.part[b * step + a.E + e];
+        for (int b = warp; b < blocks; b += 8) {
+            n += reinterpret_cast<const int*>(from)[b * step];
+            if (a.losses) p += from[b * step + a.E];
         }
     }
-    if (a.losses && threadIdx.x < 32) {  // the z terms: lane l adds blocks l, l + 32, ...
-        for (int b = threadIdx.x; b < blocks; b += 32) z += a.part[b * step + 2 * a.E];
-        z = warp_sum(z);
-    }
-    s_n[threadIdx.x] = n;
-    s_p[threadIdx.x] = p;
+    s_n[warp][lane] = n;
+    s_p[warp][lane] = p;
     __syncthreads();
-    if (slice == 0)
-        for (int w = 1; w < slices; ++w) {
-            n += s_n[w * padded + e];
-            p += s_p[w * padded + e];
+    if (blockIdx.x == 0 && a.losses && warp == 1) {  // lane l: blocks l, l + 32, ...
+        float z = 0.0f;
+#pragma unroll 8
+        for (int b = lane; b < blocks; b += 32) z += a.part[b * step + 2 * a.E];
+        z = warp_sum(z);
+        if (lane == 0) {
+            a.finish[1] = z;
+            __threadfence();
         }
-    const bool mine = slice == 0 && e < a.E;
-    if (mine) a.counts[e] = n;
-    if (a.losses) put_losses(a, mine ? float(n) * p : 0.0f, z, s_red);
+    }
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+        n += s_n[w][lane];
+        p += s_p[w][lane];
+    }
+    if (e < a.E) a.counts[e] = n;
+    if (!a.losses) return;
+    const float term = warp_sum(e < a.E ? float(n) * p : 0.0f);
+    if (lane) return;
+    a.finish[2 + blockIdx.x] = term;
+    __threadfence();
+    if (atomicAdd(reinterpret_cast<unsigned*>(a.finish), 1u) != gridDim.x - 1) return;
+    __threadfence();
+    float total = 0.0f;
+    for (unsigned g = 0; g < gridDim.x; ++g) total += __ldcg(a.finish + 2 + g);
+    put_losses(a, total, __ldcg(a.finish + 1));
 }
 
 template <int N>
@@ -391,10 +422,11 @@ moe_status check_router(const moe_router_config* c, int64_t T) {
     return MOE_OK;
 }
 
-int router_blocks(int64_t T) {
-    const int64_t b = (T + kRouterWarps - 1) / kRouterWarps;
-    return int(b < 1 ? 1 : b > kRouterBlocks ? kRouterBlocks : b);
+int router_blocks(int64_t T, int E, int most) {
+    const int warps = forward_warps((E + 31) / 32);
+    return int(std::min<int64_t>(most, std::max<int64_t>(1, (T + warps - 1) / warps)));
 }
+constexpr int kFinish = 64;  // words of a.finish
 
 RouterArgs router_args(const moe_router_config* c, int64_t T, const void* logits, int64_t ld) {
     RouterArgs a{};
@@ -440,7 +472,7 @@ moe_status moe_router_size(const moe_router_config* cfg, int64_t T, size_t* byte
     *bytes = 0;
     const moe_status st = check_router(cfg, T);
     if (st != MOE_OK) return st;
-    *bytes = size_t(router_blocks(T)) * size_t(2 * cfg->num_experts + 1) * sizeof(float);
+    *bytes = (size_t(router_blocks(T, int(cfg->num_experts), kRouterBlocks)) * size_t(2 * cfg->num_experts + 1) + kFinish) * sizeof(float);
     return MOE_OK;
 }
 
@@ -461,25 +493,26 @@ moe_status moe_router_forward(const moe_router_config* cfg, int64_t T, const voi
     a.bias = select_bias;
     a.ids = ids;
     a.probs = probs;
-    a.part = static_cast<float*>(workspace);
+    a.finish = static_cast<float*>(workspace);
+    a.part = counts ? a.finish + kFinish : nullptr;
     a.counts = counts;
     a.losses = losses;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int blocks = T == 0 ? 0 : router_blocks(T);
+    const int blocks = T == 0 ? 0 : router_blocks(T, a.E, counts ? kRouterBlocks : 4 * kRouterBlocks);
     cudaError_t e = cudaSuccess;
     if (T > 0) {
-        const size_t smem = (2 * size_t(a.E) + 1 + kRouterWarps) * sizeof(float);
         e = by_experts(a.E, [&](auto n) {
-            return launch_pdl(router_forward_kernel<decltype(n)::value>, dim3(unsigned(blocks)), dim3(32 * kRouterWarps),
-                              smem, s, a);
+            constexpr int N = decltype(n)::value, W = forward_warps(N);
+            const size_t smem = size_t(a.E) * (1 + (losses ? W : 0)) * sizeof(float);
+            return launch_pdl(router_forward_kernel<N>, dim3(unsigned(blocks)), dim3(32 * W), smem, s, a);
         });
         count_launch();
         if (e != cudaSuccess) return MOE_ERR_CUDA;
     }
     if (counts && blocks != 1) {
-        int padded = 32;
-        while (padded < a.E) padded *= 2;
-        e = launch_pdl(router_finish_kernel, dim3(1), dim3(1024), 0, s, a, blocks, padded);
+        // without tokens nothing has set the counter of finished blocks
+        if (T == 0 && losses && cudaMemsetAsync(a.finish, 0, sizeof(float), s) != cudaSuccess) return MOE_ERR_CUDA;
+        e = launch_pdl(router_finish_kernel, dim3(unsigned((a.E + 31) / 32)), dim3(256), 0, s, a, blocks);
         count_launch();
     }
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
