@@ -562,11 +562,8 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_backward_kerne
         for (int j = 0; j < NV; ++j) {
             const int i = (col + j * tpr) * V;
             if (i >= a.H) continue;
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                out[i + q] = dw[j][q];
-                out[a.H + i + q] = db[j][q];
-            }
+            store_v<V>(out + i, dw[j]);  // V > 1: H is a multiple of V
+            store_v<V>(out + a.H + i, db[j]);
         }
         return;
     }
@@ -667,10 +664,12 @@ __device__ __forceinline__ void put_grad(void* g, int i, float v, bool bf16, boo
 }
 
 // dweight (blockIdx.y 0) or dbias of 32 columns from the blocks' sums: warp w adds the blocks
-// w, w + 8, ... in order, then the warps' sums are added in warp order
-__global__ void __launch_bounds__(256) norm_wgrad_reduce_kernel(const float* __restrict__ part, int chunks, int H,
-                                                                void* dw, void* db, bool bf16, bool add) {
-    __shared__ float s_sum[8][32];
+// w, w + 32, ... in order, then the warps' sums are added in warp order
+constexpr int kReduceWarps = 32;
+__global__ void __launch_bounds__(32 * kReduceWarps) norm_wgrad_reduce_kernel(const float* __restrict__ part, int chunks,
+                                                                              int H, void* dw, void* db, bool bf16,
+                                                                              bool add) {
+    __shared__ float s_sum[kReduceWarps][33];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
@@ -679,14 +678,14 @@ __global__ void __launch_bounds__(256) norm_wgrad_reduce_kernel(const float* __r
     float v = 0.0f;
     if (i < H) {
         const float* p = part + int64_t(blockIdx.y) * H + i;
-#pragma unroll 8
-        for (int c = warp; c < chunks; c += 8) v += p[int64_t(c) * 2 * H];
+#pragma unroll 10
+        for (int c = warp; c < chunks; c += kReduceWarps) v += p[int64_t(c) * 2 * H];
     }
     s_sum[warp][lane] = v;
     __syncthreads();
     if (warp || i >= H) return;
 #pragma unroll
-    for (int w = 1; w < 8; ++w) v += s_sum[w][lane];
+    for (int w = 1; w < kReduceWarps; ++w) v += s_sum[w][lane];
     put_grad(out, i, v, bf16, add);
 }
 
@@ -738,7 +737,7 @@ RowShape row_shape(int pieces, int each) {
 }
 
 // The streamed kernels' shape, 16 columns a thread: row groups to a block of 256 threads (or one
-// of more), two such blocks an SM, the stages that its shared memory then holds, and no more blocks than have four rows a group
+// of more), two such blocks an SM, the stages that its shared memory then holds, and no more blocks than have two rows a group
 // to themselves, so that the weight gradients' partial sums stay small beside the rows.
 constexpr int kStreamBytes = 176 << 10;  // of an SM's shared memory; what is left is cache, for the weights
 struct StreamShape {
@@ -761,7 +760,7 @@ StreamShape stream_shape(int64_t H, int most, int64_t T, Stream& st) {
     int per = std::max(1, 512 / r.threads);  // 128 registers a thread
     if (2 * stage * per > kStreamBytes) per = 1;
     st.stages = std::min(kMaxStages, std::max(2, kStreamBytes / per / stage));
-    const int64_t blocks = std::min<int64_t>(std::min(per * sms, most), (T + 4 * groups - 1) / (4 * groups));
+    const int64_t blocks = std::min<int64_t>(std::min(per * sms, most), (T + 2 * groups - 1) / (2 * groups));
     const size_t sums = groups > 1 ? 2 * size_t(H) * sizeof(float) : 0;
     return {r.tpr, r.threads, int(blocks), std::max(size_t(st.stages) * size_t(stage), sums)};
 }
@@ -928,7 +927,7 @@ moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* 
         if (e != cudaSuccess) return MOE_ERR_CUDA;
     }
     if (sums) {
-        e = launch_pdl(norm_wgrad_reduce_kernel, dim3(unsigned((H + 31) / 32), 2u), dim3(256), 0, s,
+        e = launch_pdl(norm_wgrad_reduce_kernel, dim3(unsigned((H + 31) / 32), 2u), dim3(32 * kReduceWarps), 0, s,
                        static_cast<const float*>(workspace), chunks, int(H), dweight, dbias, g_type == MOE_G_BF16,
                        accumulate != 0);
         count_launch();
