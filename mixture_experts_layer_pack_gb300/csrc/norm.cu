@@ -112,18 +112,56 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int warps, int first, flo
             for (int w = 0; w < 4; ++w) p[w] = w < warps ? part[n * kSumWarps + first + w] : 0.0f;
             v[n] = (p[0] + p[1]) + (p[2] + p[3]);
         }
+    } else if (warps <= 8) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const float4 p = reinterpret_cast<const float4*>(part + n * kSumWarps)[0];
+            const float4 q = reinterpret_cast<const float4*>(part + n * kSumWarps)[1];
+            v[n] = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
+        }
     } else {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             v[n] = 0.0f;
 #pragma unroll
-            for (int q = 0; q < kSumWarps / 4; ++q)
+            for (int q = 0; q < kRowThreads / 32 / 4; ++q)
                 if (4 * q < warps) {
                     const float4 p = reinterpret_cast<const float4*>(part + n * kSumWarps)[q];
                     v[n] += (p.x + p.y) + (p.z + p.w);
                 }
         }
     }
+}
+
+// Two fp32 operations an instruction, each rounded as by itself: the streamed rows are bound by the
+// instructions that their warps issue (16384 x 4096 bf16 without a residual: 58.5 -> 57 us, backward 80 -> 78)
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void un2(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+    float a, b;
+    un2(v, a, b);
+    return a + b;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 struct NormFwd {
@@ -290,10 +328,10 @@ struct StreamRing {
         while (!mbar_try_wait(full + s, parity))
             if (globaltimer_ns() - t0 > kWaitLimitNs) return;
     }
-    // input i's row t, of row group g in the current stage
-    template <typename E>
+    // input i's row t, of row group g in the current stage; whole: rows are known to begin on 16 bytes
+    template <typename E, bool Whole>
     __device__ __forceinline__ const E* row(int i, int g, unsigned t) const {
-        const uint32_t off = (uint32_t(reinterpret_cast<uintptr_t>(st.from[i])) + t * uint32_t(st.step[i])) & 15u;
+        const uint32_t off = Whole ? 0u : (uint32_t(reinterpret_cast<uintptr_t>(st.from[i])) + t * uint32_t(st.step[i])) & 15u;
         return reinterpret_cast<const E*>(mem + (s * groups + g) * st.group_bytes + st.at[i] + off);
     }
     __device__ __forceinline__ void next() {
@@ -315,6 +353,7 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_forward_stream
     const int tpr = a.tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, col = threadIdx.x - group * tpr;
     const unsigned T = unsigned(a.T), first = blockIdx.x * groups, step = gridDim.x * groups;  // T < 2^31
     const int warps = tpr >> 5;
+    constexpr bool kWhole = V > 1;
     const float inv = 1.0f / a.H;
     StreamRing ring{st, full, asks, mem, groups};
     ring.init();
@@ -338,37 +377,62 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_forward_stream
         const unsigned t = t0 + group;
         const bool live = t < T;  // the last rows may not exist: their threads join the sums
         ring.wait();
-        const XT* x = ring.row<XT>(0, group, t);
-        const XT* r = ring.row<XT>(1, group, t);
+        const XT* x = ring.row<XT, kWhole>(0, group, t);
         float v[NV][V], sum[1] = {0.0f}, sq[1] = {0.0f};
+        if (live && !a.r) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = (col + j * tpr) * V;
-            if (i >= a.H || !live) continue;
-            load_v<V>(x + i, v[j]);
-            if (a.r) {
+            for (int j = 0; j < NV; ++j) {
+                const int i = (col + j * tpr) * V;
+                if (i < a.H) load_v<V>(x + i, v[j]);
+            }
+        } else if (live) {
+            const XT* r = ring.row<XT, kWhole>(1, group, t);
+            XT* total = static_cast<XT*>(a.s) + t * a.ss;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int i = (col + j * tpr) * V;
+                if (i >= a.H) continue;
                 float f[V];
+                load_v<V>(x + i, v[j]);
                 load_v<V>(r + i, f);
 #pragma unroll
                 for (int q = 0; q < V; ++q) v[j][q] = round_to(v[j][q] + f[q], x);
-                store_v<V>(static_cast<XT*>(a.s) + t * a.ss + i, v[j]);
+                store_v<V>(total + i, v[j]);
             }
+        }
+        if (!RMS) {
+            uint64_t s2 = 0;
 #pragma unroll
-            for (int q = 0; q < V; ++q) sum[0] += v[j][q];
+            for (int j = 0; j < NV; ++j)
+                if ((col + j * tpr) * V < a.H) {
+                    if (V == 1) sum[0] += v[j][0];
+#pragma unroll
+                    for (int q = 0; q + 1 < V; q += 2) s2 = add2(s2, f2(v[j][q], v[j][q + 1]));
+                }
+            sum[0] += sum2(s2);
         }
         float mean = 0.0f;
         if (!RMS) {
             row_sum<1>(sum, warps, group * warps, part[turn][0]);
             mean = sum[0] * inv;
         }
+        uint64_t q2 = 0;
+        const uint64_t m2 = f2(-mean, -mean);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if ((col + j * tpr) * V < a.H)
-#pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    v[j][q] -= mean;
-                    sq[0] = fmaf(v[j][q], v[j][q], sq[0]);
+            if ((col + j * tpr) * V < a.H) {
+                if (V == 1) {
+                    v[j][0] -= mean;
+                    sq[0] = fmaf(v[j][0], v[j][0], sq[0]);
                 }
+#pragma unroll
+                for (int q = 0; q + 1 < V; q += 2) {
+                    const uint64_t d = add2(f2(v[j][q], v[j][q + 1]), m2);
+                    q2 = fma2(d, d, q2);
+                    un2(d, v[j][q], v[j][q + 1]);
+                }
+            }
+        sq[0] += sum2(q2);
         row_sum<1>(sq, warps, group * warps, part[turn][1]);
         if (warps == 1) __syncthreads();  // the sums had no barrier
         // the rows are in everybody's registers
@@ -384,10 +448,9 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_forward_stream
             if (i >= a.H) continue;
             float o[V];
 #pragma unroll
-            for (int q = 0; q < V; ++q) {
-                o[q] = v[j][q] * rstd * w[j][q];
-                if (a.b) o[q] += b[j][q];
-            }
+            for (int q = 0; q + 1 < V; q += 2)
+                un2(fma2(mul2(f2(v[j][q], v[j][q + 1]), f2(rstd, rstd)), f2(w[j][q], w[j][q + 1]), f2(b[j][q], b[j][q + 1])), o[q], o[q + 1]);
+            if (V == 1) o[0] = fmaf(v[j][0] * rstd, w[j][0], b[j][0]);
             store_v<V>(y + i, o);
         }
         if (col == 0) {
@@ -485,6 +548,7 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_backward_kerne
     const int tpr = a.tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, col = threadIdx.x - group * tpr;
     const unsigned T = unsigned(a.T), first = blockIdx.x * groups, step = gridDim.x * groups;  // T < 2^31
     const int warps = tpr >> 5;
+    constexpr bool kWhole = V > 1;
     const float inv = 1.0f / a.H;
     StreamRing ring{st, full, asks, mem, groups};
     ring.init();
@@ -509,9 +573,10 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_backward_kerne
             rstd_after = a.rstd[t + step];
         }
         ring.wait();
-        const XT* x = ring.row<XT>(0, group, t);
-        const YT* dy = ring.row<YT>(1, group, t);
+        const XT* x = ring.row<XT, kWhole>(0, group, t);
+        const YT* dy = ring.row<YT, (V > 1 && V * sizeof(YT) >= 16)>(1, group, t);
         float xh[NV][V], g[NV][V], sum[2] = {0.0f, 0.0f};  // of g xhat, g
+        uint64_t sa = 0, sb = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int i = (col + j * tpr) * V;
@@ -520,35 +585,59 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_backward_kerne
             load_v<V>(dy + i, g[j]);
             float w[V];  // from cache every time: the registers go to the sums
             load_w<V>(a.w, i, a.w_bf16, w);
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                xh[j][q] = (xh[j][q] - mean) * rstd;
-                dw[j][q] = fmaf(g[j][q], xh[j][q], dw[j][q]);
-                db[j][q] += g[j][q];
-                g[j][q] *= w[q];
-                sum[0] = fmaf(g[j][q], xh[j][q], sum[0]);
-                sum[1] += g[j][q];
+            if (V == 1) {
+                xh[j][0] = (xh[j][0] - mean) * rstd;
+                dw[j][0] = fmaf(g[j][0], xh[j][0], dw[j][0]);
+                db[j][0] += g[j][0];
+                g[j][0] *= w[0];
+                sum[0] = fmaf(g[j][0], xh[j][0], sum[0]);
+                sum[1] += g[j][0];
             }
+#pragma unroll
+            for (int q = 0; q + 1 < V; q += 2) {
+                const uint64_t h = mul2(add2(f2(xh[j][q], xh[j][q + 1]), f2(-mean, -mean)), f2(rstd, rstd));
+                uint64_t e = f2(g[j][q], g[j][q + 1]);
+                un2(fma2(e, h, f2(dw[j][q], dw[j][q + 1])), dw[j][q], dw[j][q + 1]);
+                un2(add2(e, f2(db[j][q], db[j][q + 1])), db[j][q], db[j][q + 1]);
+                e = mul2(e, f2(w[q], w[q + 1]));
+                sa = fma2(e, h, sa);
+                sb = add2(sb, e);
+                un2(h, xh[j][q], xh[j][q + 1]);
+                un2(e, g[j][q], g[j][q + 1]);
+            }
+        }
+        if (V > 1) {
+            sum[0] = sum2(sa);
+            sum[1] = sum2(sb);
         }
         row_sum<2>(sum, warps, group * warps, part[turn][0]);
         if (warps == 1) __syncthreads();  // the sums had no barrier
         // nobody reads the rows before any more
         if (warp == asker && before >= 0 && t0 + (st.stages - 1) * step < T) ring.ask(before, t0 + (st.stages - 1) * step, T);
-        const float mgx = sum[0] * inv, mg = RMS ? 0.0f : sum[1] * inv;
-        if (live)
+        const float cx = sum[0] * inv * rstd, c = RMS ? 0.0f : sum[1] * inv * rstd;
+        if (live) {
+            const XT* ds = ring.row<XT, kWhole>(2, group, t);
+            XT* dx = static_cast<XT*>(a.dx) + t * a.dxs;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int i = (col + j * tpr) * V;
                 if (i >= a.H) continue;
-                float o[V], d[V];
-                if (a.ds) load_v<V>(ring.row<XT>(2, group, t) + i, d);
+                float d[V];
 #pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    o[q] = rstd * (g[j][q] - mg - xh[j][q] * mgx);
-                    if (a.ds) o[q] += d[q];
+                for (int q = 0; q < V; ++q) d[q] = -c;
+                if (a.ds) {
+                    load_v<V>(ds + i, d);
+                    if (!RMS)
+#pragma unroll
+                        for (int q = 0; q < V; ++q) d[q] -= c;
                 }
-                store_v<V>(static_cast<XT*>(a.dx) + t * a.dxs + i, o);
+#pragma unroll
+                for (int q = 0; q + 1 < V; q += 2)
+                    un2(fma2(f2(g[j][q], g[j][q + 1]), f2(rstd, rstd), fma2(f2(xh[j][q], xh[j][q + 1]), f2(-cx, -cx), f2(d[q], d[q + 1]))), d[q], d[q + 1]);
+                if (V == 1) d[0] = fmaf(g[j][0], rstd, fmaf(-xh[j][0], cx, d[0]));
+                store_v<V>(dx + i, d);
             }
+        }
         mean = mean_after;
         rstd = rstd_after;
         asker = asker + 1 == int(blockDim.x >> 5) ? 0 : asker + 1;
@@ -737,9 +826,16 @@ RowShape row_shape(int pieces, int each) {
 }
 
 // The streamed kernels' shape, 16 columns a thread: row groups to a block of 256 threads (or one
-// of more), two such blocks an SM, the stages that its shared memory then holds, and no more blocks than have two rows a group
-// to themselves, so that the weight gradients' partial sums stay small beside the rows.
-constexpr int kStreamBytes = 176 << 10;  // of an SM's shared memory; what is left is cache, for the weights
+// of more), two such blocks an SM where shared memory holds two stages of each, and no more blocks than have two rows a
+// group to themselves, so that the weight gradients' partial sums stay small beside the rows.
+// Stages: `least`, and more up to `aim` bytes an SM. What is left is cache, for the weights that the backward reads
+// every row: 128 KB against 176: 4096 x 2048 bf16 20.0 against 21.9 us. And reads that run far ahead of the writes cost
+// memory rate once the rows do not stay in L2: the forward with a residual at 16384 x 4096 bf16 takes 84 us with two
+// stages (64 KB), 92 with three, 96 with five; at 16384 x 1024 24.3 with two and 22.9 with three. Without a residual
+// more is better: 4000 x 8192 fp32 45 us with 96 KB, 41 with 176.
+// 32 columns a thread: 52 against 57 us at 16384 x 4096 bf16, but 46 against 41 at 4000 x 8192 fp32 and 21.6 against
+// 17.3 at 32768 x 512 bf16; 8 columns: 86 us.
+constexpr int kStreamBytes = 176 << 10;  // most of an SM's shared memory that is asked for
 struct StreamShape {
     int tpr, threads, blocks;
     size_t smem;
@@ -752,14 +848,15 @@ void add_input(Stream& st, const void* p, int64_t stride, int32_t type, int64_t 
     st.at[i] = st.group_bytes;
     st.group_bytes += (int(H) * es + 15 + 15) / 16 * 16;
 }
-StreamShape stream_shape(int64_t H, int most, int64_t T, Stream& st) {
+StreamShape stream_shape(int64_t H, int most, int64_t T, int least, int aim, Stream& st) {
     int sms = 152, device = 0;
     if (cudaGetDevice(&device) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
     const RowShape r = row_shape(int((H + kColumns - 1) / kColumns), 1);
     const int groups = r.threads / r.tpr, stage = groups * st.group_bytes;
     int per = std::max(1, 512 / r.threads);  // 128 registers a thread
     if (2 * stage * per > kStreamBytes) per = 1;
-    st.stages = std::min(kMaxStages, std::max(2, kStreamBytes / per / stage));
+    const int most_stages = std::min(kMaxStages, std::max(2, kStreamBytes / per / stage));
+    st.stages = std::min(most_stages, std::max(least, aim / per / stage));
     const int64_t blocks = std::min<int64_t>(std::min(per * sms, most), (T + 2 * groups - 1) / (2 * groups));
     const size_t sums = groups > 1 ? 2 * size_t(H) * sizeof(float) : 0;
     return {r.tpr, r.threads, int(blocks), std::max(size_t(st.stages) * size_t(stage), sums)};
@@ -832,7 +929,10 @@ moe_status moe_norm_forward(const moe_norm_config* cfg, int64_t T, const void* x
             Stream st{};
             add_input(st, x, x_stride, cfg->x_type, H);
             if (residual) add_input(st, residual, residual_stride, cfg->x_type, H);
-            const StreamShape sh = stream_shape(H, INT_MAX, T, st);
+            const bool large = 4 * T * H * int64_t(sizeof(X)) > int64_t(256) << 20;  // twice what L2 holds
+            const StreamShape sh = !residual ? stream_shape(H, INT_MAX, T, 3, kStreamBytes, st)
+                                   : large   ? stream_shape(H, INT_MAX, T, 2, 96 << 10, st)
+                                             : stream_shape(H, INT_MAX, T, 3, 128 << 10, st);
             if (sh.threads <= kNarrow)
                 return wide ? launch_stream(norm_forward_stream_kernel<X, Y, R, V, kColumns / V, kNarrow>, sh, a, st, cs)
                             : launch_stream(norm_forward_stream_kernel<X, Y, R, 1, kColumns, kNarrow>, sh, a, st, cs);
@@ -905,7 +1005,7 @@ moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* 
                 if (dsum) add_input(st, dsum, dsum_stride, cfg->x_type, H);
                 // dy is read from shared memory in pieces too: its rows start on 16 bytes as well, or none is
                 const bool w16 = wide && rows_aligned(dy, dy_stride, cfg->y_type, 16);
-                const StreamShape sh = stream_shape(H, kMaxChunks, T, st);
+                const StreamShape sh = stream_shape(H, kMaxChunks, T, 3, 128 << 10, st);
                 chunks = sh.blocks;
                 if (!sums) a.part = nullptr;
                 if (sh.threads <= kNarrow)
