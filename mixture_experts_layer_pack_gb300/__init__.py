@@ -15,8 +15,9 @@ from .binding import (HostPipe, MoEDecoder, MoELayer, MoENorm, MoERouter, MoeErr
                       moe_norm_backward, moe_norm_backward_size, moe_norm_config, moe_norm_forward,
                       moe_router_backward, moe_router_config, moe_router_forward, moe_router_size,
                       weights_from_combined_mxfp8)
+from .block import BlockParams, MoEBlock
 
-__all__ = ["HostPipe", "MoEDecoder", "MoELayer", "MoENorm", "MoERouter", "MoeError", "load", "main_grads_from_combined", "moe_backward", "moe_config", "moe_create",
+__all__ = ["BlockParams", "HostPipe", "MoEBlock", "MoEDecoder", "MoELayer", "MoENorm", "MoERouter", "MoeError", "load", "main_grads_from_combined", "moe_backward", "moe_config", "moe_create",
            "moe_handle_config", "moe_host_pipe_create", "moe_host_pipe_destroy", "moe_host_pipe_size", "moe_host_pipe_sync",
            "moe_host_step",
            "moe_destroy", "moe_device_status", "moe_export_routing", "moe_forward", "moe_forward_topk", "moe_kernel_name",

@@ -1,0 +1,104 @@
+"""The expert block of a transformer: norm, router, experts and the residual stream around them.
+
+    s = x + residual            the residual stream, in x's type
+    y = norm(s) w + b           bf16, the experts' input
+    logits = y Wr^T             a plain library product, in Wr's type
+    ids, probs = top-k(logits)  with the routes' counts and the balance and z losses
+    out = experts(y, ids, probs)
+
+``forward`` returns (out, s): the next block's norm adds them up, as this one's
+added x and residual, so the stream is read and written once a block. The step
+for training runs on a ``MoELayer`` and is followed by ``backward``; ``decode``
+is the same function without anything kept for a backward pass: a
+``MoEDecoder`` takes batches of up to ``decode_tokens`` tokens, larger ones go
+to the layer.
+"""
+from __future__ import annotations
+
+import dataclasses
+
+from . import binding as B
+
+
+@dataclasses.dataclass
+class BlockParams:
+    """Parameters of a block: norm_weight and norm_bias [H] (norm_bias may be None), router_weight [E,H]
+    (fp32 logits from fp32, bf16 logits from bf16), select_bias [E] fp32 or None (moves the choice of
+    experts only) and the experts' moe_weights."""
+    norm_weight: object
+    router_weight: object
+    weights: B.moe_weights
+    norm_bias: object = None
+    select_bias: object = None
+
+
+class MoEBlock:
+    """One expert block; one forward at a time waits for its backward."""
+
+    def __init__(self, max_tokens, hidden, num_experts, topk, inter, device="cuda", norm=B.MOE_NORM_RMS, eps=1e-6,
+                 score=B.MOE_SCORE_SOFTMAX, normalise=True, scale=1.0, aux_coeff=0.0, z_coeff=0.0,
+                 routed_wtype=B.MOE_W_BF16, swiglu_limit=0.0, act_precision=None, shared_expert=True,
+                 decode_tokens=B.MOE_DECODE_MAX_TOKENS):
+        """max_tokens: of a training step, 0 for a block that only decodes; decode_tokens: of the decoder, 0 for none."""
+        if max_tokens <= 0 and decode_tokens <= 0:
+            raise ValueError("a block needs max_tokens, decode_tokens or both")
+        self.norm = B.MoENorm(hidden, eps, norm, device=device)
+        self.router = B.MoERouter(num_experts, topk, score, normalise, scale, aux_coeff, z_coeff, device=device)
+        self.layer = self.decoder = None
+        if max_tokens > 0:
+            self.layer = B.MoELayer(max_tokens, hidden, num_experts, topk, inter, device=device, routed_wtype=routed_wtype,
+                                    swiglu_limit=swiglu_limit, act_precision=act_precision, shared_expert=shared_expert)
+        if decode_tokens > 0:
+            self.decoder = B.MoEDecoder(decode_tokens, hidden, num_experts, topk, inter, device=device,
+                                        routed_wtype=routed_wtype, swiglu_limit=swiglu_limit, shared_expert=shared_expert)
+        self.decode_tokens = decode_tokens
+        self._kept = None
+
+    def _routed(self, x, residual, p):
+        import torch
+        y, s, mean, rstd = self.norm.forward(x, p.norm_weight, p.norm_bias, residual=residual, out_dtype=torch.bfloat16)
+        logits = torch.nn.functional.linear(y.to(p.router_weight.dtype), p.router_weight)
+        return y, s, mean, rstd, logits, self.router.forward(logits, p.select_bias)
+
+    def forward(self, x, params: BlockParams, residual=None):
+        """(out [T,H] bf16, s [T,H] in x's type, losses [2] fp32 or None) of x and residual [T,H], bf16 or fp32;
+        on the current stream. What backward needs is kept until it, or the next forward."""
+        if self.layer is None:
+            raise ValueError("the block was made for decoding only (max_tokens 0)")
+        y, s, mean, rstd, logits, (ids, probs, counts, losses) = self._routed(x, residual, params)
+        out = self.layer.forward_topk(y, ids, probs, params.weights)
+        self._kept = (params, y, s, mean, rstd, logits, ids, counts)
+        return out, s, losses
+
+    def backward(self, dout, main_grads: B.moe_main_grads, ds=None, loss_grad=1.0):
+        """(dx, grads) for the gradients dout of out and ds of s (None: zero) and loss_grad of the losses' sum.
+        dx is that of x and of residual alike. grads: norm_weight, norm_bias (None without one) and
+        router_weight; the experts' are added to main_grads."""
+        import torch
+        if self._kept is None:
+            raise ValueError("backward without a forward before it")
+        p, y, s, mean, rstd, logits, ids, counts = self._kept
+        self._kept = None
+        dy, dprobs = self.layer.backward(dout, main_grads)
+        dlogits = self.router.backward(logits, ids, dprobs, counts=counts, loss_grad=loss_grad)
+        drouter = dlogits.t() @ y.to(dlogits.dtype)
+        # one rounding of the sum of both paths to y
+        dy = torch.addmm(dy.to(dlogits.dtype), dlogits, p.router_weight)
+        dx, dw, db = self.norm.backward(dy, s, p.norm_weight, mean, rstd, dsum=ds, bias=p.norm_bias is not None)
+        return dx, {"norm_weight": dw, "norm_bias": db, "router_weight": drouter}
+
+    def decode(self, x, params: BlockParams, residual=None):
+        """(out, s) as forward's, with nothing kept; may be captured into a CUDA graph."""
+        y, s, _, _, _, (ids, probs, _, _) = self._routed(x, residual, params)
+        small = self.decoder is not None and x.shape[0] <= self.decode_tokens
+        if not small and self.layer is None:
+            raise ValueError(f"the block decodes up to {self.decode_tokens} tokens")
+        run = self.decoder if small else self.layer
+        if not small:
+            self._kept = None  # the layer's saved state is overwritten
+        return run.forward_topk(y, ids, probs, params.weights), s
+
+    def close(self):
+        for part in (self.layer, self.decoder):
+            if part is not None:
+                part.close()
