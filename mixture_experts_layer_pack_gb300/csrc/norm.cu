@@ -342,18 +342,51 @@ struct StreamRing {
     }
 };
 
+// A thread's columns of a row: NV pieces of V, a piece of each lane beside the next, so that a warp has
+// kColumns * 32 columns on end. The pieces' places are then constants beside one pointer, and a warp that has all its
+// columns (most do) looks at no bounds: f(true) runs there, f(false) in a warp where the row ends.
+template <int V, int NV>
+struct Columns {
+    static constexpr int kStep = 32 * V;  // from piece to piece
+    int base, limit;                      // the first column, and how many columns of the row come from there on
+    bool all;
+    __device__ __forceinline__ Columns(int col, int H) {
+        const int first = (col >> 5) * NV * kStep;
+        base = first + (threadIdx.x & 31) * V;
+        limit = H - base;
+        all = first + NV * kStep <= H;
+    }
+    template <typename F>
+    __device__ __forceinline__ void run(F f) const {
+        if (all)
+            f(std::true_type{});
+        else
+            f(std::false_type{});
+    }
+};
+// element e of a thread's columns
+template <int V, int NV>
+__device__ __forceinline__ float& at(float (&v)[NV][V], int e) { return v[e / V][e % V]; }
+template <int V, int NV>
+__device__ __forceinline__ uint64_t two(float (&v)[NV][V], int e) { return f2(at<V, NV>(v, e), at<V, NV>(v, e + 1)); }
+template <int V, int NV>
+__device__ __forceinline__ void put2(float (&v)[NV][V], int e, uint64_t x) { un2(x, at<V, NV>(v, e), at<V, NV>(v, e + 1)); }
+
 template <typename XT, typename YT, bool RMS, int V, int NV, int NT>
 __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_forward_stream_kernel(NormFwd a, const __grid_constant__ Stream st) {
     __shared__ __align__(16) float part[2][2][kSumWarps];
     __shared__ uint64_t full[kMaxStages];
     __shared__ Ask asks[32];
     extern __shared__ __align__(128) uint8_t mem[];
+    constexpr bool kWhole = V > 1;
+    constexpr int N = NV * V, kStep = Columns<V, NV>::kStep;
     if (threadIdx.x < 32)
         part[0][0][threadIdx.x] = part[0][1][threadIdx.x] = part[1][0][threadIdx.x] = part[1][1][threadIdx.x] = 0.0f;
     const int tpr = a.tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, col = threadIdx.x - group * tpr;
     const unsigned T = unsigned(a.T), first = blockIdx.x * groups, step = gridDim.x * groups;  // T < 2^31
     const int warps = tpr >> 5;
-    constexpr bool kWhole = V > 1;
+    const Columns<V, NV> cols(col, a.H);
+    const int limit = cols.limit;
     const float inv = 1.0f / a.H;
     StreamRing ring{st, full, asks, mem, groups};
     ring.init();
@@ -365,74 +398,74 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_forward_stream
     float w[NV][V], b[NV][V];  // a thread has the same columns in every row: their weights stay in registers
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int i = (col + j * tpr) * V;
 #pragma unroll
         for (int q = 0; q < V; ++q) w[j][q] = b[j][q] = 0.0f;
-        if (i >= a.H) continue;
-        load_w<V>(a.w, i, a.w_bf16, w[j]);
-        if (a.b) load_w<V>(a.b, i, a.w_bf16, b[j]);
+        if (j * kStep >= limit) continue;
+        load_w<V>(a.w, cols.base + j * kStep, a.w_bf16, w[j]);
+        if (a.b) load_w<V>(a.b, cols.base + j * kStep, a.w_bf16, b[j]);
     }
     int turn = 0, asker = 0;
     for (unsigned t0 = first; t0 < T; t0 += step, turn ^= 1) {
         const unsigned t = t0 + group;
         const bool live = t < T;  // the last rows may not exist: their threads join the sums
         ring.wait();
-        const XT* x = ring.row<XT, kWhole>(0, group, t);
+        const XT* x = ring.row<XT, kWhole>(0, group, t) + cols.base;
         float v[NV][V], sum[1] = {0.0f}, sq[1] = {0.0f};
-        if (live && !a.r) {
+        if (!live) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int i = (col + j * tpr) * V;
-                if (i < a.H) load_v<V>(x + i, v[j]);
-            }
-        } else if (live) {
-            const XT* r = ring.row<XT, kWhole>(1, group, t);
-            XT* total = static_cast<XT*>(a.s) + t * a.ss;
+            for (int e = 0; e < N; ++e) at<V, NV>(v, e) = 0.0f;
+        } else if (!a.r) {
+            cols.run([&](auto all) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int i = (col + j * tpr) * V;
-                if (i >= a.H) continue;
-                float f[V];
-                load_v<V>(x + i, v[j]);
-                load_v<V>(r + i, f);
+                for (int j = 0; j < NV; ++j) {
+                    if (all || j * kStep < limit)
+                        load_v<V>(x + j * kStep, v[j]);
+                    else
 #pragma unroll
-                for (int q = 0; q < V; ++q) v[j][q] = round_to(v[j][q] + f[q], x);
-                store_v<V>(total + i, v[j]);
-            }
-        }
-        if (!RMS) {
-            uint64_t s2 = 0;
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if ((col + j * tpr) * V < a.H) {
-                    if (V == 1) sum[0] += v[j][0];
-#pragma unroll
-                    for (int q = 0; q + 1 < V; q += 2) s2 = add2(s2, f2(v[j][q], v[j][q + 1]));
+                        for (int q = 0; q < V; ++q) v[j][q] = 0.0f;
                 }
-            sum[0] += sum2(s2);
+            });
+        } else {
+            const XT* r = ring.row<XT, kWhole>(1, group, t) + cols.base;
+            XT* total = static_cast<XT*>(a.s) + t * a.ss + cols.base;
+            cols.run([&](auto all) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+#pragma unroll
+                    for (int q = 0; q < V; ++q) v[j][q] = 0.0f;
+                    if (!all && j * kStep >= limit) continue;
+                    float f[V];
+                    load_v<V>(x + j * kStep, v[j]);
+                    load_v<V>(r + j * kStep, f);
+#pragma unroll
+                    for (int q = 0; q < V; ++q) v[j][q] = round_to(v[j][q] + f[q], x);
+                    store_v<V>(total + j * kStep, v[j]);
+                }
+            });
         }
         float mean = 0.0f;
         if (!RMS) {
+            uint64_t s2 = 0;
+#pragma unroll
+            for (int e = 0; e < N; e += 2) s2 = add2(s2, two<V, NV>(v, e));
+            sum[0] = sum2(s2);
             row_sum<1>(sum, warps, group * warps, part[turn][0]);
             mean = sum[0] * inv;
         }
-        uint64_t q2 = 0;
-        const uint64_t m2 = f2(-mean, -mean);
+        cols.run([&](auto all) {
+            const uint64_t m2 = f2(-mean, -mean);
+            uint64_t q2 = 0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if ((col + j * tpr) * V < a.H) {
-                if (V == 1) {
-                    v[j][0] -= mean;
-                    sq[0] = fmaf(v[j][0], v[j][0], sq[0]);
+            for (int e = 0; e < N; e += 2) {
+                if (!RMS) put2<V, NV>(v, e, add2(two<V, NV>(v, e), m2));
+                if (!all) {
+                    if (e / V * kStep >= limit) at<V, NV>(v, e) = 0.0f;
+                    if ((e + 1) / V * kStep >= limit) at<V, NV>(v, e + 1) = 0.0f;
                 }
-#pragma unroll
-                for (int q = 0; q + 1 < V; q += 2) {
-                    const uint64_t d = add2(f2(v[j][q], v[j][q + 1]), m2);
-                    q2 = fma2(d, d, q2);
-                    un2(d, v[j][q], v[j][q + 1]);
-                }
+                q2 = fma2(two<V, NV>(v, e), two<V, NV>(v, e), q2);
             }
-        sq[0] += sum2(q2);
+            sq[0] = sum2(q2);
+        });
         row_sum<1>(sq, warps, group * warps, part[turn][1]);
         if (warps == 1) __syncthreads();  // the sums had no barrier
         // the rows are in everybody's registers
@@ -441,18 +474,16 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_forward_stream
         ring.next();
         if (!live) continue;
         const float rstd = rsqrtf(sq[0] * inv + a.eps);
-        YT* y = static_cast<YT*>(a.y) + t * a.ys;
+        YT* y = static_cast<YT*>(a.y) + t * a.ys + cols.base;
+        cols.run([&](auto all) {
+            const uint64_t r2 = f2(rstd, rstd);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = (col + j * tpr) * V;
-            if (i >= a.H) continue;
-            float o[V];
+            for (int e = 0; e < N; e += 2)
+                put2<V, NV>(v, e, fma2(mul2(two<V, NV>(v, e), r2), two<V, NV>(w, e), two<V, NV>(b, e)));
 #pragma unroll
-            for (int q = 0; q + 1 < V; q += 2)
-                un2(fma2(mul2(f2(v[j][q], v[j][q + 1]), f2(rstd, rstd)), f2(w[j][q], w[j][q + 1]), f2(b[j][q], b[j][q + 1])), o[q], o[q + 1]);
-            if (V == 1) o[0] = fmaf(v[j][0] * rstd, w[j][0], b[j][0]);
-            store_v<V>(y + i, o);
-        }
+            for (int j = 0; j < NV; ++j)
+                if (all || j * kStep < limit) store_v<V>(y + j * kStep, v[j]);
+        });
         if (col == 0) {
             if (!RMS && a.mean) a.mean[t] = mean;
             if (a.rstd) a.rstd[t] = rstd;
@@ -536,27 +567,41 @@ struct NormBwd {
 
 // dx of a block's rows, streamed like the forward's, and the block's part of the weight
 // gradients: a thread has the same columns in every row and keeps their sums in registers, so
-// x and dy are read once for all three gradients.
+// x and dy are read once for all three gradients. The weights lie in shared memory as fp32: the registers go to the sums.
 template <typename XT, typename YT, bool RMS, int V, int NV, int NT>
 __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_backward_kernel(NormBwd a, const __grid_constant__ Stream st) {
     __shared__ __align__(16) float part[2][2][kSumWarps];
     __shared__ uint64_t full[kMaxStages];
     __shared__ Ask asks[32];
     extern __shared__ __align__(128) uint8_t mem[];
+    constexpr bool kWhole = V > 1;
+    constexpr int N = NV * V, kStep = Columns<V, NV>::kStep;
     if (threadIdx.x < 32)
         part[0][0][threadIdx.x] = part[0][1][threadIdx.x] = part[1][0][threadIdx.x] = part[1][1][threadIdx.x] = 0.0f;
     const int tpr = a.tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr, col = threadIdx.x - group * tpr;
     const unsigned T = unsigned(a.T), first = blockIdx.x * groups, step = gridDim.x * groups;  // T < 2^31
     const int warps = tpr >> 5;
-    constexpr bool kWhole = V > 1;
+    const Columns<V, NV> cols(col, a.H);
+    const int limit = cols.limit;
     const float inv = 1.0f / a.H;
-    StreamRing ring{st, full, asks, mem, groups};
+    float* weight = reinterpret_cast<float*>(mem);  // of all kColumns * tpr columns, zeros past the row
+    StreamRing ring{st, full, asks, mem + kColumns * tpr * sizeof(float), groups};
     ring.init();
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5;
     if (warp == 0)
         for (int s = 0; s < st.stages && first + s * step < T; ++s) ring.ask(s, first + s * step, T);
+    weight += cols.base;
+    if (group == 0) {
+        float f[NV][V] = {};
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (j * kStep < limit) load_w<V>(a.w, cols.base + j * kStep, a.w_bf16, f[j]);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) store_v<V>(weight + j * kStep, f[j]);
+    }
+    if (groups > 1) __syncthreads();  // else a thread reads its own only
     float dw[NV][V] = {}, db[NV][V] = {};
     float mean = 0.0f, rstd = 0.0f;
     if (first + group < T) {
@@ -573,40 +618,53 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_backward_kerne
             rstd_after = a.rstd[t + step];
         }
         ring.wait();
-        const XT* x = ring.row<XT, kWhole>(0, group, t);
-        const YT* dy = ring.row<YT, (V > 1 && V * sizeof(YT) >= 16)>(1, group, t);
-        float xh[NV][V], g[NV][V], sum[2] = {0.0f, 0.0f};  // of g xhat, g
-        uint64_t sa = 0, sb = 0;
+        const XT* x = ring.row<XT, kWhole>(0, group, t) + cols.base;
+        const YT* dy = ring.row<YT, (V > 1 && V * sizeof(YT) >= 16)>(1, group, t) + cols.base;
+        float xh[NV][V], g[NV][V], sum[2];  // of g xhat, g
+        if (!live) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = (col + j * tpr) * V;
-            if (i >= a.H || !live) continue;
-            load_v<V>(x + i, xh[j]);
-            load_v<V>(dy + i, g[j]);
-            float w[V];  // from cache every time: the registers go to the sums
-            load_w<V>(a.w, i, a.w_bf16, w);
-            if (V == 1) {
-                xh[j][0] = (xh[j][0] - mean) * rstd;
-                dw[j][0] = fmaf(g[j][0], xh[j][0], dw[j][0]);
-                db[j][0] += g[j][0];
-                g[j][0] *= w[0];
-                sum[0] = fmaf(g[j][0], xh[j][0], sum[0]);
-                sum[1] += g[j][0];
-            }
+            for (int e = 0; e < N; ++e) at<V, NV>(xh, e) = at<V, NV>(g, e) = 0.0f;
+        } else {
+            cols.run([&](auto all) {
 #pragma unroll
-            for (int q = 0; q + 1 < V; q += 2) {
-                const uint64_t h = mul2(add2(f2(xh[j][q], xh[j][q + 1]), f2(-mean, -mean)), f2(rstd, rstd));
-                uint64_t e = f2(g[j][q], g[j][q + 1]);
-                un2(fma2(e, h, f2(dw[j][q], dw[j][q + 1])), dw[j][q], dw[j][q + 1]);
-                un2(add2(e, f2(db[j][q], db[j][q + 1])), db[j][q], db[j][q + 1]);
-                e = mul2(e, f2(w[q], w[q + 1]));
-                sa = fma2(e, h, sa);
-                sb = add2(sb, e);
-                un2(h, xh[j][q], xh[j][q + 1]);
-                un2(e, g[j][q], g[j][q + 1]);
-            }
+                for (int j = 0; j < NV; ++j) {
+                    if (all || j * kStep < limit) {
+                        load_v<V>(x + j * kStep, xh[j]);
+                        load_v<V>(dy + j * kStep, g[j]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < V; ++q) xh[j][q] = g[j][q] = 0.0f;
+                    }
+                }
+            });
         }
-        if (V > 1) {
+        {
+            const uint64_t m2 = f2(-mean, -mean), r2 = f2(rstd, rstd);
+            uint64_t sa = 0, sb = 0;
+#pragma unroll
+            for (int j = 0; j < (V > 1 ? NV : NV / 2); ++j) {
+                constexpr int P = V > 1 ? V : 2;
+                float w[P];
+                if constexpr (V > 1) {
+                    load_v<V>(weight + j * kStep, w);
+                } else {
+                    w[0] = weight[2 * j * kStep];
+                    w[1] = weight[(2 * j + 1) * kStep];
+                }
+#pragma unroll
+                for (int q = 0; q < P; q += 2) {
+                    const int e = j * P + q;
+                    const uint64_t h = mul2(RMS ? two<V, NV>(xh, e) : add2(two<V, NV>(xh, e), m2), r2);
+                    uint64_t d = two<V, NV>(g, e);
+                    put2<V, NV>(dw, e, fma2(d, h, two<V, NV>(dw, e)));
+                    put2<V, NV>(db, e, add2(d, two<V, NV>(db, e)));
+                    d = mul2(d, f2(w[q], w[q + 1]));
+                    sa = fma2(d, h, sa);
+                    sb = add2(sb, d);
+                    put2<V, NV>(xh, e, h);
+                    put2<V, NV>(g, e, d);
+                }
+            }
             sum[0] = sum2(sa);
             sum[1] = sum2(sb);
         }
@@ -616,27 +674,25 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_backward_kerne
         if (warp == asker && before >= 0 && t0 + (st.stages - 1) * step < T) ring.ask(before, t0 + (st.stages - 1) * step, T);
         const float cx = sum[0] * inv * rstd, c = RMS ? 0.0f : sum[1] * inv * rstd;
         if (live) {
-            const XT* ds = ring.row<XT, kWhole>(2, group, t);
-            XT* dx = static_cast<XT*>(a.dx) + t * a.dxs;
+            const XT* ds = ring.row<XT, kWhole>(2, group, t) + cols.base;
+            XT* dx = static_cast<XT*>(a.dx) + t * a.dxs + cols.base;
+            cols.run([&](auto all) {
+                const uint64_t r2 = f2(rstd, rstd), cx2 = f2(-cx, -cx), c2 = f2(-c, -c);
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int i = (col + j * tpr) * V;
-                if (i >= a.H) continue;
-                float d[V];
+                for (int e = 0; e < N; e += 2)
+                    put2<V, NV>(g, e, fma2(two<V, NV>(g, e), r2, fma2(two<V, NV>(xh, e), cx2, c2)));
 #pragma unroll
-                for (int q = 0; q < V; ++q) d[q] = -c;
-                if (a.ds) {
-                    load_v<V>(ds + i, d);
-                    if (!RMS)
+                for (int j = 0; j < NV; ++j) {
+                    if (!all && j * kStep >= limit) continue;
+                    if (a.ds) {
+                        float d[V];
+                        load_v<V>(ds + j * kStep, d);
 #pragma unroll
-                        for (int q = 0; q < V; ++q) d[q] -= c;
+                        for (int q = 0; q < V; ++q) g[j][q] += d[q];
+                    }
+                    store_v<V>(dx + j * kStep, g[j]);
                 }
-#pragma unroll
-                for (int q = 0; q + 1 < V; q += 2)
-                    un2(fma2(f2(g[j][q], g[j][q + 1]), f2(rstd, rstd), fma2(f2(xh[j][q], xh[j][q + 1]), f2(-cx, -cx), f2(d[q], d[q + 1]))), d[q], d[q + 1]);
-                if (V == 1) d[0] = fmaf(g[j][0], rstd, fmaf(-xh[j][0], cx, d[0]));
-                store_v<V>(dx + i, d);
-            }
+            });
         }
         mean = mean_after;
         rstd = rstd_after;
@@ -649,10 +705,9 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_backward_kerne
     if (groups == 1) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int i = (col + j * tpr) * V;
-            if (i >= a.H) continue;
-            store_v<V>(out + i, dw[j]);  // V > 1: H is a multiple of V
-            store_v<V>(out + a.H + i, db[j]);
+            if (j * kStep >= limit) continue;
+            store_v<V>(out + cols.base + j * kStep, dw[j]);  // V > 1: H is a multiple of V
+            store_v<V>(out + a.H + cols.base + j * kStep, db[j]);
         }
         return;
     }
@@ -661,14 +716,15 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_backward_kerne
         __syncthreads();
         if (r != group) continue;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            if (j * kStep >= limit) continue;
 #pragma unroll
             for (int q = 0; q < V; ++q) {
-                const int i = (col + j * tpr) * V + q;
-                if (i >= a.H) continue;
+                const int i = cols.base + j * kStep + q;
                 rows[i] = (r ? rows[i] : 0.0f) + dw[j][q];
                 rows[a.H + i] = (r ? rows[a.H + i] : 0.0f) + db[j][q];
             }
+        }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * a.H; i += blockDim.x) out[i] = rows[i];
@@ -848,18 +904,19 @@ void add_input(Stream& st, const void* p, int64_t stride, int32_t type, int64_t 
     st.at[i] = st.group_bytes;
     st.group_bytes += (int(H) * es + 15 + 15) / 16 * 16;
 }
-StreamShape stream_shape(int64_t H, int most, int64_t T, int least, int aim, Stream& st) {
+StreamShape stream_shape(int64_t H, int most, int64_t T, int least, int aim, bool weights, Stream& st) {
     int sms = 152, device = 0;
     if (cudaGetDevice(&device) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
     const RowShape r = row_shape(int((H + kColumns - 1) / kColumns), 1);
     const int groups = r.threads / r.tpr, stage = groups * st.group_bytes;
     int per = std::max(1, 512 / r.threads);  // 128 registers a thread
     if (2 * stage * per > kStreamBytes) per = 1;
+    const size_t fixed = weights ? kColumns * r.tpr * sizeof(float) : 0;
     const int most_stages = std::min(kMaxStages, std::max(2, kStreamBytes / per / stage));
     st.stages = std::min(most_stages, std::max(least, aim / per / stage));
     const int64_t blocks = std::min<int64_t>(std::min(per * sms, most), (T + 2 * groups - 1) / (2 * groups));
     const size_t sums = groups > 1 ? 2 * size_t(H) * sizeof(float) : 0;
-    return {r.tpr, r.threads, int(blocks), std::max(size_t(st.stages) * size_t(stage), sums)};
+    return {r.tpr, r.threads, int(blocks), fixed + std::max(size_t(st.stages) * size_t(stage), sums)};
 }
 
 template <typename... KArgs, typename A>
@@ -930,9 +987,9 @@ moe_status moe_norm_forward(const moe_norm_config* cfg, int64_t T, const void* x
             add_input(st, x, x_stride, cfg->x_type, H);
             if (residual) add_input(st, residual, residual_stride, cfg->x_type, H);
             const bool large = 4 * T * H * int64_t(sizeof(X)) > int64_t(256) << 20;  // twice what L2 holds
-            const StreamShape sh = !residual ? stream_shape(H, INT_MAX, T, 3, kStreamBytes, st)
-                                   : large   ? stream_shape(H, INT_MAX, T, 2, 96 << 10, st)
-                                             : stream_shape(H, INT_MAX, T, 3, 128 << 10, st);
+            const StreamShape sh = !residual ? stream_shape(H, INT_MAX, T, 3, kStreamBytes, false, st)
+                                   : large   ? stream_shape(H, INT_MAX, T, 2, 96 << 10, false, st)
+                                             : stream_shape(H, INT_MAX, T, 3, 128 << 10, false, st);
             if (sh.threads <= kNarrow)
                 return wide ? launch_stream(norm_forward_stream_kernel<X, Y, R, V, kColumns / V, kNarrow>, sh, a, st, cs)
                             : launch_stream(norm_forward_stream_kernel<X, Y, R, 1, kColumns, kNarrow>, sh, a, st, cs);
@@ -1005,7 +1062,7 @@ moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* 
                 if (dsum) add_input(st, dsum, dsum_stride, cfg->x_type, H);
                 // dy is read from shared memory in pieces too: its rows start on 16 bytes as well, or none is
                 const bool w16 = wide && rows_aligned(dy, dy_stride, cfg->y_type, 16);
-                const StreamShape sh = stream_shape(H, kMaxChunks, T, 3, 128 << 10, st);
+                const StreamShape sh = stream_shape(H, kMaxChunks, T, 3, 128 << 10, true, st);
                 chunks = sh.blocks;
                 if (!sums) a.part = nullptr;
                 if (sh.threads <= kNarrow)
