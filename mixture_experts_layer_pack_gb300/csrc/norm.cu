@@ -88,6 +88,7 @@ __device__ __forceinline__ float round_to(float v, const __nv_bfloat16*) {
     return __bfloat162float(__float2bfloat16_rn(v));
 }
 
+constexpr int kWidest = 768;   // most threads of a row
 constexpr int kSumWarps = 32;  // places of a sum
 
 // Sums over the `warps` warps of a row (warps first, first + 1, ... of the block); every thread of
@@ -120,16 +121,17 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int warps, int first, flo
             v[n] = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
         }
     } else {
+        auto eight = [&](int n, int q) {
+            const float4 x = reinterpret_cast<const float4*>(part + n * kSumWarps)[q];
+            const float4 y = reinterpret_cast<const float4*>(part + n * kSumWarps)[q + 1];
+            return ((x.x + x.y) + (x.z + x.w)) + ((y.x + y.y) + (y.z + y.w));
+        };
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            v[n] = 0.0f;
+        for (int n = 0; n < N; ++n) v[n] = eight(n, 0) + eight(n, 2);
+        if (warps > 16)
 #pragma unroll
-            for (int q = 0; q < kRowThreads / 32 / 4; ++q)
-                if (4 * q < warps) {
-                    const float4 p = reinterpret_cast<const float4*>(part + n * kSumWarps)[q];
-                    v[n] += (p.x + p.y) + (p.z + p.w);
-                }
-        }
+            for (int n = 0; n < N; ++n) v[n] += eight(n, 4);
+        static_assert(kWidest <= 24 * 32, "24 warps a row");
     }
 }
 
@@ -268,9 +270,11 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
 // that leaves 96 registers a thread where there are 128 now, and the sums of the weights' gradients
 // no longer fit: 16384 x 4096 backward 153 us against 100.)
 constexpr int kMaxStages = 8;
-// threads of a block: several row groups or one of up to 256 threads, two blocks an SM; or one of up to 512
-constexpr int kNarrow = 256, kWide = 512;
-constexpr int kStreamed = kColumns * kWide;  // the widest row that is streamed
+// threads of a block: several row groups or one of up to 256 threads, two blocks an SM; or one of up to 512, or of 768
+// (80 registers a thread: the backward spills some 130 bytes)
+constexpr int kNarrow = 256, kWide = 512;  // and kWidest
+constexpr int kStreamed = kColumns * kWidest;  // the widest row that is streamed
+constexpr size_t kMostShared = 225 << 10;      // and the most shared memory for it beside what the kernels declare
 struct Stream {
     int stages, arrays;
     int row_bytes[3], at[3];  // of each input: bytes of a row, and its place in a row group's part of a stage
@@ -866,6 +870,9 @@ bool rows_aligned(const void* p, int64_t stride, int32_t type, size_t bytes) {
     return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | (size_t(stride) * es)) & (bytes - 1)) == 0;
 }
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
 // Threads of a row that takes `pieces` accesses, `each` to a thread, and of the block: rows of up
 // to 128 threads share a block of 256.
 struct RowShape {
@@ -990,11 +997,13 @@ moe_status moe_norm_forward(const moe_norm_config* cfg, int64_t T, const void* x
             const StreamShape sh = !residual ? stream_shape(H, INT_MAX, T, 3, kStreamBytes, false, st)
                                    : large   ? stream_shape(H, INT_MAX, T, 2, 96 << 10, false, st)
                                              : stream_shape(H, INT_MAX, T, 3, 128 << 10, false, st);
-            if (sh.threads <= kNarrow)
-                return wide ? launch_stream(norm_forward_stream_kernel<X, Y, R, V, kColumns / V, kNarrow>, sh, a, st, cs)
-                            : launch_stream(norm_forward_stream_kernel<X, Y, R, 1, kColumns, kNarrow>, sh, a, st, cs);
-            return wide ? launch_stream(norm_forward_stream_kernel<X, Y, R, V, kColumns / V, kWide>, sh, a, st, cs)
-                        : launch_stream(norm_forward_stream_kernel<X, Y, R, 1, kColumns, kWide>, sh, a, st, cs);
+            auto go = [&](auto nt) {
+                constexpr int NT = decltype(nt)::value;
+                return wide ? launch_stream(norm_forward_stream_kernel<X, Y, R, V, kColumns / V, NT>, sh, a, st, cs)
+                            : launch_stream(norm_forward_stream_kernel<X, Y, R, 1, kColumns, NT>, sh, a, st, cs);
+            };
+            if (sh.smem <= kMostShared)
+                return sh.threads <= kNarrow ? go(Int<kNarrow>{}) : sh.threads <= kWide ? go(Int<kWide>{}) : go(Int<kWidest>{});
         }
         if (wide && pieces <= 4 * kRowThreads) return launch_norm_forward<X, Y, R, V, 4>(a, cs);
         count_launch();
@@ -1063,13 +1072,16 @@ moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* 
                 // dy is read from shared memory in pieces too: its rows start on 16 bytes as well, or none is
                 const bool w16 = wide && rows_aligned(dy, dy_stride, cfg->y_type, 16);
                 const StreamShape sh = stream_shape(H, kMaxChunks, T, 3, 128 << 10, true, st);
-                chunks = sh.blocks;
-                if (!sums) a.part = nullptr;
-                if (sh.threads <= kNarrow)
-                    return w16 ? launch_stream(norm_backward_kernel<X, Y, R, V, NV, kNarrow>, sh, a, st, s)
-                               : launch_stream(norm_backward_kernel<X, Y, R, 1, kColumns, kNarrow>, sh, a, st, s);
-                return w16 ? launch_stream(norm_backward_kernel<X, Y, R, V, NV, kWide>, sh, a, st, s)
-                           : launch_stream(norm_backward_kernel<X, Y, R, 1, kColumns, kWide>, sh, a, st, s);
+                NormBwd b = a;
+                if (!sums) b.part = nullptr;
+                auto go = [&](auto nt) {
+                    constexpr int NT = decltype(nt)::value;
+                    chunks = sh.blocks;
+                    return w16 ? launch_stream(norm_backward_kernel<X, Y, R, V, NV, NT>, sh, b, st, s)
+                               : launch_stream(norm_backward_kernel<X, Y, R, 1, kColumns, NT>, sh, b, st, s);
+                };
+                if (sh.smem <= kMostShared)
+                    return sh.threads <= kNarrow ? go(Int<kNarrow>{}) : sh.threads <= kWide ? go(Int<kWide>{}) : go(Int<kWidest>{});
             }
             count_launch();
             const dim3 grid{unsigned(T)}, block{kRowThreads};

@@ -114,6 +114,18 @@ CASES = [
     (2, 32767, F32, F32, F32, True, True, 0.0, 1, 1),
     (700, 96, BF16, BF16, F32, True, True, 0.0, 0, 0),
     (2500, 40, F32, F32, F32, False, True, 0.0, 0, 0),
+    # many rows: every width of a block, whole and odd columns, rows that end inside a warp's share
+    (400, 513, BF16, BF16, F32, True, True, 0.0, 3, 1),
+    (400, 512, F32, F32, BF16, True, True, 2.0, 0, 0),
+    (350, 1544, BF16, F32, BF16, True, True, 0.0, 0, 0),
+    (320, 3001, F32, BF16, F32, True, False, 0.0, 1, 3),
+    (320, 5001, BF16, BF16, BF16, True, True, 0.0, 0, 0),
+    (310, 8192, F32, F32, F32, True, True, 0.0, 0, 0),
+    (310, 8200, F32, F32, F32, False, True, 0.0, 0, 0),
+    (310, 9001, BF16, BF16, F32, True, True, 0.0, 2, 1),
+    (310, 12288, BF16, BF16, BF16, True, True, 0.0, 0, 0),
+    (310, 12288, F32, BF16, F32, True, True, 0.0, 4, 4),
+    (8200, 4104, BF16, BF16, BF16, True, True, 0.0, 0, 0),
 ]
 
 
