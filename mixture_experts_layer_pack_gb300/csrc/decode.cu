@@ -836,6 +836,8 @@ struct Consumer {
             f(ring + s * B::SLOT, tokens + tslot * a.token_slot_bytes + B::TS);
             __syncwarp();
             if (lane == 0) mbar_arrive(bars->empty + s);
+        } else {
+            __syncwarp();  // every lane has seen this use of the token slot before it is given back
         }
         if (lane == 0) mbar_arrive(bars->tempty + tslot);
         if ((slot += size) >= a.slots) {
