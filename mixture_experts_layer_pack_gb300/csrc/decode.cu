@@ -182,6 +182,15 @@ __device__ __forceinline__ unsigned load_acquire(const unsigned* p) {
     return v;
 }
 
+__device__ __forceinline__ void add_release(unsigned* p, unsigned v) {
+    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ unsigned add_acq_rel(unsigned* p, unsigned v) {
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+
 // waits until the grid barrier's top bit differs from `before`; bounded: past the limit it
 // records the timeout and goes on (every address that follows is valid either way)
 __device__ __forceinline__ void grid_wait(const unsigned* bar, unsigned before, int* status) {
@@ -304,6 +313,44 @@ __device__ __forceinline__ void sort_routes(const DecodeArgs& a, Tables& tb, uin
     }
 }
 
+// The same for up to 32 routes, by one warp with a route a lane: no barrier of the block between its steps (a call for one
+// token 1.5 us shorter). The number of routed groups goes to *n_routed.
+template <int CAP>
+__device__ __forceinline__ void sort_few(const DecodeArgs& a, const Tables& tb, int id, float prob, int* n_routed) {
+    const int R = a.T * a.k, r = threadIdx.x & 31, t = r / a.k;
+    const unsigned row = (a.k == 32 ? 0xffffffffu : (1u << a.k) - 1) << (t * a.k & 31), lower = (1u << r) - 1;
+    const unsigned like = __match_any_sync(0xffffffffu, id);  // a lane past the routes has id -1
+    const bool ok = id == -1 || (id >= 0 && id < a.E && !(like & row & lower));
+    const unsigned bad = __ballot_sync(0xffffffffu, !ok);
+    if (bad && r == 0 && blockIdx.x == 0) atomicOr(a.status, kStatusRouting);
+    const bool live = r < R && id >= 0 && !(bad & row);
+    const unsigned alive = __ballot_sync(0xffffffffu, live);
+    const int same = __popc(like & alive), before = __popc(like & alive & lower);  // of this expert; and of a lower token
+    const bool lead = live && before % CAP == 0;                                   // a group's first route
+    const unsigned leads = __ballot_sync(0xffffffffu, lead);
+    const int mine = live ? id : 0x7fffffff;
+    int sum = 0;  // routes of lower experts, and << 16 their groups
+    for (int j0 = 0; j0 < R; j0 += 8)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int v = __shfl_sync(0xffffffffu, mine, j0 + j);
+            sum += v < mine ? 1 + (leads >> (j0 + j) << 16 & 0x10000) : 0;
+        }
+    const int less = sum & 0xffff, groups = sum >> 16;
+    const int base = a.shared ? a.T : 0, pos = base + less + before;
+    if (live) {
+        tb.tok[pos] = t;
+        tb.coef[pos] = prob;
+    }
+    if (lead) tb.groups[tb.n_shared + groups + before / CAP] = Group{id, pos, min(CAP, same - before)};
+    if (r < tb.n_shared) tb.groups[r] = Group{a.E, r * CAP, min(CAP, a.T - r * CAP)};
+    if (a.shared && r < a.T) {
+        tb.tok[r] = r;
+        tb.coef[r] = 1.0f;
+    }
+    if (r == 0) *n_routed = __popc(leads);
+}
+
 // A block's share. First product: tiles u = group * it + tile of I, from u_begin to u_end.
 // Second product: slots of (set of 8 tiles of H, group, chunk, tile), the tile fastest. Shares
 // are equal in cost: a slot of a routed group counts 2, one of the shared expert shared_cost.
@@ -328,6 +375,18 @@ struct Plan {
         return set * kConsumers * q + (in <= hc ? (in + shared_cost - 1) / shared_cost : heavy + (in - hc + 1) / 2);
     }
     __device__ __forceinline__ int begin(int block) const { return slot_at(share(cost2, block, blocks2)); }
+    // the second product's part: worked out when the first product's copies are under way
+    __device__ __forceinline__ void second(const DecodeArgs& a, const Tables& tb) {
+        const int c = blockIdx.x, n = gridDim.x;
+        q_shared = tb.n_shared * a.c2_shared;
+        q = q_shared + (tb.n_groups - tb.n_shared) * a.c2;
+        tile_cost = q_shared * a.shared_cost + (q - q_shared) * 2;
+        n2 = q * a.ht;
+        cost2 = tile_cost * a.ht;
+        blocks2 = max(1, min(cost2 / a.shared_cost, n));  // no share is smaller than a slot: none is empty
+        s_begin = c < blocks2 ? begin(c) : n2;
+        s_end = c + 1 < blocks2 ? begin(c + 1) : n2;
+    }
 };
 
 __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, const Tables& tb) {
@@ -347,14 +406,6 @@ __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, const Tables& tb)
     };
     p.u_begin = tile(share(cost, c, n));
     p.u_end = tile(share(cost, c + 1, n));
-    p.q_shared = tb.n_shared * a.c2_shared;
-    p.q = p.q_shared + routed * a.c2;
-    p.tile_cost = p.q_shared * a.shared_cost + (p.q - p.q_shared) * 2;
-    p.n2 = p.q * a.ht;
-    p.cost2 = p.tile_cost * a.ht;
-    p.blocks2 = max(1, min(p.cost2 / a.shared_cost, n));  // no share is smaller than a slot: none is empty
-    p.s_begin = c < p.blocks2 ? p.begin(c) : p.n2;
-    p.s_end = c + 1 < p.blocks2 ? p.begin(c + 1) : p.n2;
     return p;
 }
 
@@ -578,7 +629,7 @@ template <class B>
 struct Producer {
     const DecodeArgs& a;
     const Tables& tb;
-    const Plan& p;
+    Plan& p;
     uint8_t *ring, *tokens;
     Bars* bars;
     volatile int* abort;
@@ -763,6 +814,7 @@ struct Producer {
                 }
             }
         }
+        if (B::NT == 1) p.second(a, tb);
         for (Steps w(p); w.more(p); w.next(p, tb.n_groups)) {
             const Group gr = tb.groups[w.g];
             const bool routed = gr.expert < a.E, mx = B::MX && routed;
@@ -813,7 +865,7 @@ template <class B>
 struct Consumer {
     const DecodeArgs& a;
     const Tables& tb;
-    const Plan& p;
+    Plan& p;
     const uint8_t *ring, *tokens;
     Bars* bars;
     volatile int* abort;
@@ -917,40 +969,59 @@ struct Consumer {
             for (int i = lane; i < n_out; i += 32) a.out[i / 16 * a.os + h] = __float2bfloat16_rn(s_out[i]);
     }
 
+    // the blocks that share a set, and whether the first of them begins where the set does (the others begin inside it)
+    struct Sharing {
+        int first, last;
+        bool whole;
+    };
+    __device__ __forceinline__ Sharing sharing(int set) const {
+        const int s0 = set * kConsumers * p.q, first = owner(p.cost2, p.cost_before(s0), p.blocks2);
+        return {first, owner(p.cost2, p.cost_before(s0 + p.q * Steps::width(p, set) - 1), p.blocks2), p.begin(first) == s0};
+    }
     // out = bf16(sum) of this warp's row tile; a set that other blocks share goes through global memory
-    __device__ __forceinline__ void flush(int set) {
+    __device__ __forceinline__ void flush(int set, const Sharing& sh) {
         const int tile = set * kConsumers + warp, n_out = a.T * 16;
         __syncwarp();
         if (tile < p.ht) {
-            const int h0 = tile * 16, s0 = set * kConsumers * p.q;
-            const int first = owner(p.cost2, p.cost_before(s0), p.blocks2);
-            const int last = owner(p.cost2, p.cost_before(s0 + p.q * Steps::width(p, set) - 1), p.blocks2);
-            if (first == last) {
+            const int h0 = tile * 16;
+            if (sh.first == sh.last) {
                 put_out(h0, n_out);
             } else {
                 // block b's partial sums of this set: in its first place if the set is where it begins
-                auto part = [&](int b, int begin) {
-                    const bool here = begin / (kConsumers * p.q) == set;
-                    return a.part + ((int64_t(b) * 2 + (here ? 0 : 1)) * kConsumers + warp) * n_out;
+                auto part = [&](int b) {
+                    return reinterpret_cast<float4*>(a.part + ((int64_t(b) * 2 + (b > sh.first || sh.whole ? 0 : 1)) * kConsumers + warp) * n_out);
                 };
-                float* to = part(blockIdx.x, p.s_begin);
-                for (int i = lane; i < n_out / 4; i += 32)
-                    reinterpret_cast<float4*>(to)[i] = reinterpret_cast<const float4*>(s_out)[i];
-                __threadfence();
+                float4* to = part(blockIdx.x);
+                for (int i = lane; i < n_out / 4; i += 32) to[i] = reinterpret_cast<const float4*>(s_out)[i];
                 __syncwarp();
                 unsigned seen = 0;
-                if (lane == 0) seen = atomicAdd(a.counters + tile, 1u);
-                if (__shfl_sync(0xffffffffu, seen, 0) == unsigned(last - first)) {
-                    __threadfence();
-                    for (int i = lane; i < n_out; i += 32) s_out[i] = 0.0f;
-                    for (int b = first; b <= last; ++b) {
-                        const float4* from = reinterpret_cast<const float4*>(part(b, p.begin(b)));
+                if (lane == 0) seen = add_acq_rel(a.counters + tile, 1u);
+                if (__shfl_sync(0xffffffffu, seen, 0) == unsigned(sh.last - sh.first)) {
+                    __syncwarp();  // what lane 0 acquired, every lane may read
+                    float4* to_sum = reinterpret_cast<float4*>(s_out);
+                    if (B::NT > 1) {  // many values: four of a block's at a time
+                        for (int i = lane; i < n_out / 4; i += 32) to_sum[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        for (int b = sh.first; b <= sh.last; ++b) {
+                            const float4* from = part(b);
 #pragma unroll 4
-                        for (int i = lane; i < n_out / 4; i += 32) {
-                            const float4 v = __ldcg(from + i);
-                            float4* d = reinterpret_cast<float4*>(s_out) + i;
-                            *d = make_float4(d->x + v.x, d->y + v.y, d->z + v.z, d->w + v.w);
+                            for (int i = lane; i < n_out / 4; i += 32) {
+                                const float4 v = __ldcg(from + i), d = to_sum[i];
+                                to_sum[i] = make_float4(d.x + v.x, d.y + v.y, d.z + v.z, d.w + v.w);
+                            }
                         }
+                    }
+                    for (int i = lane; B::NT == 1 && i < n_out / 4; i += 32) {  // few: of four blocks at a time
+                        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        for (int b = sh.first; b <= sh.last; b += 4) {
+                            float4 v[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) v[j] = __ldcg(part(min(b + j, sh.last)) + i);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (b + j <= sh.last)
+                                    sum = make_float4(sum.x + v[j].x, sum.y + v[j].y, sum.z + v[j].z, sum.w + v[j].w);
+                        }
+                        to_sum[i] = sum;
                     }
                     __syncwarp();
                     put_out(h0, n_out);
@@ -958,12 +1029,13 @@ struct Consumer {
                 }
             }
         }
+        __syncwarp();
         for (int i = lane; i < n_out; i += 32) s_out[i] = 0.0f;
         __syncwarp();
     }
 
-    __device__ __forceinline__ void second() {
-        Steps w(p);
+    // w: at the block's first step; sh: of its set, worked out before it is needed where registers allow
+    __device__ __forceinline__ void second(Steps w, Sharing sh) {
         while (w.more(p)) {
             const int g = w.g, set = w.set;
             const Group gr = tb.groups[g];
@@ -989,7 +1061,11 @@ struct Consumer {
                     d[8] = fmaf(c, acc[0][t][2 + j], d[8]);
                 }
             __syncwarp();
-            if (!w.more(p) || w.set != set) flush(set);
+            if (!w.more(p) || w.set != set) {
+                if (B::NT > 1) sh = sharing(set);
+                flush(set, sh);
+                if (B::NT == 1 && w.more(p)) sh = sharing(w.set);
+            }
         }
     }
 };
@@ -1027,15 +1103,23 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
         bars->met = 0;
     }
     for (int i = tid; i < kConsumers * a.T * 16 + B::ZEROS / 4; i += kDecodeThreads) s_out[i] = 0.0f;
-    sort_routes<B::CAP>(a, tb, tokens, id, prob);  // its scratch: the rings' space
-    fence_proxy_async_smem();
+    const bool few = a.T * a.k <= 32;
+    if (!few) {
+        sort_routes<B::CAP>(a, tb, tokens, id, prob);  // its scratch: the rings' space
+        fence_proxy_async_smem();
+    } else {
+        tb.n_shared = a.shared ? (a.T + B::CAP - 1) / B::CAP : 0;
+        if (warp == 0) sort_few<B::CAP>(a, tb, id, prob, s_abort + 1);
+    }
     __syncthreads();
+    if (few) tb.n_groups = tb.n_shared + s_abort[1];
     if (tb.n_groups == 0) {  // nothing chosen and nothing shared, for every block alike
         for (int i = blockIdx.x * kDecodeThreads + tid; i < a.T * a.H; i += gridDim.x * kDecodeThreads)
             a.out[i / a.H * a.os + i % a.H] = __float2bfloat16_rn(0.0f);
         return;
     }
-    const Plan p = make_plan(a, tb);
+    Plan p = make_plan(a, tb);
+    if (B::NT > 1) p.second(a, tb);  // no later: the code in the loops' middle costs 3 us at T = 64
     if (warp >= kConsumers) {
         Producer<B>{a, tb, p, ring, tokens, bars, s_abort, warp - kConsumers, lane}.run();
         return;
@@ -1046,9 +1130,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
     // the blocks meet: every activation and gate is written
     asm volatile("fence.proxy.async.global;" ::: "memory");  // the activations are read by bulk copies
     consumer_sync();
+    if (tid == 0) add_release(a.barrier, blockIdx.x == 0 ? 0x80000000u - (gridDim.x - 1) : 1u);
+    if (B::NT == 1) p.second(a, tb);  // while the blocks arrive
+    Steps w(p);
+    typename Consumer<B>::Sharing sh{};
+    if (B::NT == 1 && w.more(p)) sh = c.sharing(w.set);
     if (tid == 0) {
-        __threadfence();
-        atomicAdd(a.barrier, blockIdx.x == 0 ? 0x80000000u - (gridDim.x - 1) : 1u);
         grid_wait(a.barrier, before, a.status);
         set_round(&bars->met, 1);
     }
@@ -1057,7 +1144,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
         for (int t = tid; t < a.T; t += 32 * kConsumers) tb.coef[t] = __ldcg(a.gate + t);
         consumer_sync();
     }
-    c.second();
+    c.second(w, sh);
 }
 
 struct DecodeShape {
