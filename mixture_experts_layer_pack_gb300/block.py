@@ -24,7 +24,7 @@ from . import binding as B
 class BlockParams:
     """Parameters of a block: norm_weight and norm_bias [H] (norm_bias may be None), router_weight [E,H]
     (fp32 logits from fp32, bf16 logits from bf16), select_bias [E] fp32 or None (moves the choice of
-    experts only) and the experts' moe_weights."""
+    experts only) and the experts' moe_weights, which are pointers: their tensors are the caller's to keep."""
     norm_weight: object
     router_weight: object
     weights: B.moe_weights

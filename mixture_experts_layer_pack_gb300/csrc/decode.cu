@@ -95,8 +95,8 @@ struct DecodeArgs {
     unsigned* barrier;        // top bit flips when every block has arrived
     int* status;
     // chunks of H and of I by weight type (the shared expert's, routed), tiles of I and H, and
-    // what a slot of the shared expert costs, in halves of a slot of a routed one
-    int c1_shared, c1, c2_shared, c2, it, ht, shared_cost;
+    // what a slot of the shared expert costs beside one of a routed one
+    int c1_shared, c1, c2_shared, c2, it, ht, shared_cost, routed_cost;
     // shared memory plan
     int max_groups;
     int slots, token_slots, token_slot_bytes;
@@ -353,12 +353,12 @@ __device__ __forceinline__ void sort_few(const DecodeArgs& a, const Tables& tb, 
 
 // A block's share. First product: tiles u = group * it + tile of I, from u_begin to u_end.
 // Second product: slots of (set of 8 tiles of H, group, chunk, tile), the tile fastest. Shares
-// are equal in cost: a slot of a routed group counts 2, one of the shared expert shared_cost.
+// are equal in cost: a slot of a routed group counts routed_cost, one of the shared expert shared_cost.
 struct Plan {
     int n_shared;
     int c2_shared, c2, it, ht;
     int u_begin, u_end;
-    int shared_cost;
+    int shared_cost, routed_cost;
     int q_shared, q;           // chunks of I over the shared groups, over all groups
     int tile_cost;             // of one tile of H: all its chunks
     int n2, cost2, blocks2;    // second product: slots, their cost, and the blocks that have any
@@ -367,12 +367,12 @@ struct Plan {
     __device__ __forceinline__ int cost_before(int s) const {
         const int set = s / (kConsumers * q), in = s - set * kConsumers * q;
         const int heavy = min(kConsumers, ht - set * kConsumers) * q_shared;
-        return set * kConsumers * tile_cost + min(in, heavy) * shared_cost + max(in - heavy, 0) * 2;
+        return set * kConsumers * tile_cost + min(in, heavy) * shared_cost + max(in - heavy, 0) * routed_cost;
     }
     __device__ __forceinline__ int slot_at(int x) const {
         const int set = x / (kConsumers * tile_cost), in = x - set * kConsumers * tile_cost;
         const int heavy = min(kConsumers, ht - set * kConsumers) * q_shared, hc = heavy * shared_cost;
-        return set * kConsumers * q + (in <= hc ? (in + shared_cost - 1) / shared_cost : heavy + (in - hc + 1) / 2);
+        return set * kConsumers * q + (in <= hc ? (in + shared_cost - 1) / shared_cost : heavy + (in - hc + routed_cost - 1) / routed_cost);
     }
     __device__ __forceinline__ int begin(int block) const { return slot_at(share(cost2, block, blocks2)); }
     // the second product's part: worked out when the first product's copies are under way
@@ -380,10 +380,10 @@ struct Plan {
         const int c = blockIdx.x, n = gridDim.x;
         q_shared = tb.n_shared * a.c2_shared;
         q = q_shared + (tb.n_groups - tb.n_shared) * a.c2;
-        tile_cost = q_shared * a.shared_cost + (q - q_shared) * 2;
+        tile_cost = q_shared * a.shared_cost + (q - q_shared) * routed_cost;
         n2 = q * a.ht;
         cost2 = tile_cost * a.ht;
-        blocks2 = max(1, min(cost2 / a.shared_cost, n));  // no share is smaller than a slot: none is empty
+        blocks2 = max(1, min(cost2 / max(a.shared_cost, a.routed_cost), n));  // no share is smaller than a slot: none is empty
         s_begin = c < blocks2 ? begin(c) : n2;
         s_end = c + 1 < blocks2 ? begin(c + 1) : n2;
     }
@@ -398,7 +398,8 @@ __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, const Tables& tb)
     p.it = a.it;
     p.ht = a.ht;
     p.shared_cost = a.shared_cost;
-    const int per_shared = a.c1_shared * a.shared_cost, per = a.c1 * 2;  // of a tile of I
+    p.routed_cost = a.routed_cost;
+    const int per_shared = a.c1_shared * a.shared_cost, per = a.c1 * a.routed_cost;  // of a tile of I
     const int cost_shared = a.it * tb.n_shared * per_shared, cost = cost_shared + a.it * routed * per;
     auto tile = [&](int x) {
         return x <= cost_shared ? (x + per_shared - 1) / per_shared
@@ -880,7 +881,7 @@ struct Consumer {
         mbar_wait(bars->tfull + tslot, tround & 1, abort, a.status);
         if (at >= 0 && at < size) {
             int s = slot + at, r = round;
-            if (s >= a.slots) {
+            while (s >= a.slots) {
                 s -= a.slots;
                 ++r;
             }
@@ -892,7 +893,8 @@ struct Consumer {
             __syncwarp();  // every lane has seen this use of the token slot before it is given back
         }
         if (lane == 0) mbar_arrive(bars->tempty + tslot);
-        if ((slot += size) >= a.slots) {
+        slot += size;
+        while (slot >= a.slots) {  // a ring of many tokens' block may have fewer slots than a set has tiles
             slot -= a.slots;
             ++round;
         }
@@ -1263,15 +1265,19 @@ moe_status decode_weight(moe_decoder* d, const moe_wview& v, int64_t N, int64_t 
     return MOE_OK;
 }
 
+// Groups of up to 8 tokens: an expert that more tokens chose is read again for every 8 of them, from L2. With bf16
+// weights groups of 32 (slots of half the columns, for the room that their tokens take) win once experts have more than
+// some 16 tokens each. us, groups of 8 against 32: T 64, H 2048, I 1024: E 128 k 4 235 / 248, E 8 k 2 62 / 63,
+// E 4 k 4 80 / 71; T 64, H 4096, I 2048, E 8 k 4 298 / 198; T 12, H 4096, I 1536, E 64 k 6 274 / 299. With MXFP8 weights
+// groups of 16 lost to 8 everywhere (T 64, H 4096, I 2048, E 8 k 4: 470 against 336).
 using Few16 = Build<1, 512, false>;
 using More16 = Build<4, 256, false>;
 using Few8 = Build<1, 1024, true>;
-using More8 = Build<2, 512, true>;
 
 template <typename F>
-cudaError_t by_build(bool mx, int64_t T, F f) {
-    if (mx) return T <= 8 ? f(Few8()) : f(More8());
-    return T <= 8 ? f(Few16()) : f(More16());
+cudaError_t by_build(bool mx, int64_t T, int64_t k, int64_t E, F f) {
+    if (mx) return f(Few8());
+    return T * k <= 16 * E ? f(Few16()) : f(More16());
 }
 
 template <class B>
@@ -1287,7 +1293,7 @@ cudaError_t launch_decode(DecodeArgs& a, int blocks, cudaStream_t st) {
     a.ring_off = a.tokens_off + a.token_slots * a.token_slot_bytes;
     a.slots = std::min(kSlots, (kSmemMax - a.ring_off) / B::SLOT);
     const int scratch = 12 * a.E + 8 + 4 * R + 160;
-    if (a.slots < kConsumers || a.tokens_off + scratch > kSmemMax) return cudaErrorInvalidConfiguration;
+    if (a.slots < 4 || a.tokens_off + scratch > kSmemMax) return cudaErrorInvalidConfiguration;
     a.act_row = (a.I + 1023) / 1024 * 1024;
     auto chunks = [](int n, bool mx) { return (n + B::columns(mx) - 1) / B::columns(mx); };
     a.c1_shared = chunks(a.H, false);
@@ -1296,7 +1302,10 @@ cudaError_t launch_decode(DecodeArgs& a, int blocks, cudaStream_t st) {
     a.c2 = chunks(a.I, true);
     a.it = (a.I + 7) / 8;
     a.ht = (a.H + 15) / 16;
-    a.shared_cost = a.T > 8 ? 3 : 2;
+    // E4M3 weights take more work a slot than the shared expert's bf16 ones: 4 tokens, H 7168, I 2048 with 24 routes
+    // 207 us at 3 : 4, 212 at 4 : 4, 251 at 2 : 4. In groups of 32 the shared expert's are the full ones.
+    a.shared_cost = B::MX || B::NT > 1 ? 3 : 2;
+    a.routed_cost = B::MX ? 4 : 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(blocks));
     cfg.blockDim = dim3(kDecodeThreads);
@@ -1353,8 +1362,8 @@ moe_status moe_decode_create(const moe_config* cfg, void* workspace, size_t work
         cudaMemset(d->ws.state, 0, state_words(s) * sizeof(unsigned)) != cudaSuccess)
         return MOE_ERR_CUDA;
     d->blocks = std::min(sms, kMaxBlocks);
-    for (const int64_t T : {int64_t(1), int64_t(MOE_DECODE_MAX_TOKENS)})
-        if (by_build(s.mx, T, [](auto b) {
+    for (const int64_t T : {int64_t(1), int64_t(MOE_DECODE_MAX_TOKENS)})  // few tokens an expert, and many: both builds
+        if (by_build(s.mx, T, 1, 1, [](auto b) {
                 return cudaFuncSetAttribute(decode_kernel<decltype(b)>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             kSmemMax);
             }) != cudaSuccess)
@@ -1406,7 +1415,7 @@ moe_status moe_decode(moe_decoder* d, int64_t T, const void* hidden, int64_t hid
         const moe_status r = decode_weight(d, *views[i], down ? s.H : s.I, down ? s.I : s.H, i >= 3, i % 3, st, &a.w[i]);
         if (r != MOE_OK) return r;
     }
-    const cudaError_t e = by_build(s.mx, T, [&](auto b) { return launch_decode<decltype(b)>(a, d->blocks, st); });
+    const cudaError_t e = by_build(s.mx, T, s.k, s.E, [&](auto b) { return launch_decode<decltype(b)>(a, d->blocks, st); });
     if (e == cudaErrorInvalidConfiguration) return MOE_ERR_UNSUPPORTED;
     count_launch();
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

@@ -149,7 +149,8 @@ def test_decode_is_the_forward(T, wr):
 def test_two_blocks_in_a_graph():
     """Two blocks one after the other, captured once and replayed over new input."""
     T, H, I, E, k = 3, 512, 128, 16, 4
-    ps = [params(H, I, E, torch.float32, False, seed=40 + i)[1] for i in range(2)]
+    made = [params(H, I, E, torch.float32, False, seed=40 + i) for i in range(2)]  # moe_weights are pointers: their tensors stay
+    ps = [m[1] for m in made]
     block = M.MoEBlock(0, H, E, k, I)
     x = torch.randn(T, H, device="cuda").bfloat16()
 

@@ -138,6 +138,15 @@ CASES = [
     (64, 512, 224, 12, 4, True, True, True, 0.0),
     (2, 7168, 2048, 3, 2, True, True, False, 0.0),
     (11, 4096, 1408, 5, 3, False, True, False, 0.0),
+    # experts with more tokens than a group, and with many; rings of few slots
+    (64, 520, 264, 2, 1, False, True, False, 0.0),
+    (64, 1024, 512, 4, 2, False, True, True, 0.0),
+    (50, 1040, 136, 48, 32, False, True, False, 0.0),
+    (64, 512, 136, 300, 32, False, True, False, 0.0),
+    (10, 1160, 424, 10, 3, False, True, False, 0.0),
+    (64, 1056, 224, 2, 2, True, True, False, 0.0),
+    (64, 512, 160, 260, 32, True, True, False, 0.0),
+    (12, 2080, 544, 20, 4, True, True, True, 1.0),
 ]
 
 
