@@ -387,6 +387,17 @@ def moe_norm_forward(cfg: moe_norm_config, x, weight, y, bias=None, residual=Non
                                    _addr(mean), _addr(rstd), _raw_stream(stream, x.device)), "moe_norm_forward")
 
 
+def _sized(size, sizes, cfg, T):
+    """size(cfg, T), which depends on nothing else, from the dict of those asked for before."""
+    key = (id(cfg), T)  # an object keeps its configurations as long as its sizes
+    n = sizes.get(key)
+    if n is None:
+        if len(sizes) > 4096:
+            sizes.clear()
+        n = sizes[key] = size(cfg, T)
+    return n
+
+
 def moe_norm_backward_size(cfg: moe_norm_config, T: int) -> int:
     n = c_size_t(0)
     _check(load().moe_norm_backward_size(cfg, T, ctypes.byref(n)), "moe_norm_backward_size")
@@ -795,7 +806,7 @@ class MoENorm:
         import torch
         self.hidden, self.eps, self.kind, self.device = int(hidden), float(eps), int(kind), torch.device(device)
         self._types = {torch.bfloat16: MOE_T_BF16, torch.float32: MOE_T_FP32}
-        self._cfgs = {}
+        self._cfgs, self._sizes = {}, {}
         self._torch, self._stream = torch, _current_stream_of()
         self._forward, self._backward = load().moe_norm_forward, load().moe_norm_backward
         _check(load().moe_norm_forward(moe_norm_config(self.hidden, self.eps, self.kind, 0, 0, 0), 0, None, self.hidden,
@@ -881,7 +892,7 @@ class MoENorm:
         self._vector(dweight, gt)
         if dbias is not None:
             self._vector(dbias, gt)
-        size = moe_norm_backward_size(cfg, T)
+        size = _sized(moe_norm_backward_size, self._sizes, cfg, T)
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
         status = self._backward(cfg, T, dy.data_ptr(), _ld(dy), s.data_ptr(), _ld(s), weight.data_ptr(), _addr(mean),
                                 rstd.data_ptr(), _addr(dsum), 0 if dsum is None else _ld(dsum), ds.data_ptr(), H,
@@ -901,6 +912,7 @@ class MoERouter:
         self.E, self.k = int(num_experts), int(topk)
         self.device = torch.device(device)
         args = (self.E, self.k, int(score), int(bool(normalise)), float(scale), float(aux_coeff), float(z_coeff))
+        self._sizes = {}
         self._cfgs = {torch.bfloat16: moe_router_config(*args, MOE_T_BF16),
                       torch.float32: moe_router_config(*args, MOE_T_FP32)}
         self.losses_wanted = aux_coeff != 0 or z_coeff != 0
@@ -930,7 +942,7 @@ class MoERouter:
         probs = torch.empty(slots, dtype=torch.float32, device=dev)
         counts = torch.empty(self.E, dtype=torch.int32, device=dev)
         losses = torch.empty(2, dtype=torch.float32, device=dev) if self.losses_wanted else None
-        size = moe_router_size(cfg, T)
+        size = _sized(moe_router_size, self._sizes, cfg, T)
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
         status = self._forward(cfg, T, logits.data_ptr(), _ld(logits), _addr(select_bias), ids.data_ptr(),
                                probs.data_ptr(), counts.data_ptr(), _addr(losses), workspace.data_ptr(), size,

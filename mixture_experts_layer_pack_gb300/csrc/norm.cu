@@ -9,6 +9,7 @@
 //   dw = sum_t dy xhat, db = sum_t dy.
 // All statistics and sums are fp32.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -926,13 +927,27 @@ StreamShape stream_shape(int64_t H, int most, int64_t T, int least, int aim, boo
     return {r.tpr, r.threads, int(blocks), fixed + std::max(size_t(st.stages) * size_t(stage), sums)};
 }
 
-template <typename... KArgs, typename A>
-cudaError_t launch_stream(void (*kernel)(KArgs...), const StreamShape& sh, A& a, Stream& st, cudaStream_t cs) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sh.smem));
+// the shared memory that a kernel may ask for, said once for each device
+template <auto Kernel>
+cudaError_t allow_shared() {
+    static std::atomic<uint64_t> said{0};
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (device & 63);
+    if (device < 64 && (said.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared));
+    if (e == cudaSuccess) said.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+template <auto Kernel, typename A>
+cudaError_t launch_stream(const StreamShape& sh, A& a, Stream& st, cudaStream_t cs) {
+    const cudaError_t e = allow_shared<Kernel>();
     if (e != cudaSuccess) return e;
     a.tpr = sh.tpr;
     count_launch();
-    return launch_pdl(kernel, dim3(unsigned(sh.blocks)), dim3(unsigned(sh.threads)), sh.smem, cs, a, st);
+    return launch_pdl(Kernel, dim3(unsigned(sh.blocks)), dim3(unsigned(sh.threads)), sh.smem, cs, a, st);
 }
 
 template <typename XT, typename YT, bool RMS, int V, int NV>
@@ -999,8 +1014,8 @@ moe_status moe_norm_forward(const moe_norm_config* cfg, int64_t T, const void* x
                                              : stream_shape(H, INT_MAX, T, 3, 128 << 10, false, st);
             auto go = [&](auto nt) {
                 constexpr int NT = decltype(nt)::value;
-                return wide ? launch_stream(norm_forward_stream_kernel<X, Y, R, V, kColumns / V, NT>, sh, a, st, cs)
-                            : launch_stream(norm_forward_stream_kernel<X, Y, R, 1, kColumns, NT>, sh, a, st, cs);
+                return wide ? launch_stream<norm_forward_stream_kernel<X, Y, R, V, kColumns / V, NT>>(sh, a, st, cs)
+                            : launch_stream<norm_forward_stream_kernel<X, Y, R, 1, kColumns, NT>>(sh, a, st, cs);
             };
             if (sh.smem <= kMostShared)
                 return sh.threads <= kNarrow ? go(Int<kNarrow>{}) : sh.threads <= kWide ? go(Int<kWide>{}) : go(Int<kWidest>{});
@@ -1077,8 +1092,8 @@ moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* 
                 auto go = [&](auto nt) {
                     constexpr int NT = decltype(nt)::value;
                     chunks = sh.blocks;
-                    return w16 ? launch_stream(norm_backward_kernel<X, Y, R, V, NV, NT>, sh, b, st, s)
-                               : launch_stream(norm_backward_kernel<X, Y, R, 1, kColumns, NT>, sh, b, st, s);
+                    return w16 ? launch_stream<norm_backward_kernel<X, Y, R, V, NV, NT>>(sh, b, st, s)
+                               : launch_stream<norm_backward_kernel<X, Y, R, 1, kColumns, NT>>(sh, b, st, s);
                 };
                 if (sh.smem <= kMostShared)
                     return sh.threads <= kNarrow ? go(Int<kNarrow>{}) : sh.threads <= kWide ? go(Int<kWide>{}) : go(Int<kWidest>{});
