@@ -20,9 +20,11 @@ namespace moe {
 namespace {
 
 constexpr int kRouterWarps = 8;     // of a block of the backward
-constexpr int kRouterBlocks = 304;  // most blocks of the forward, each with its own partial sums: two per SM
+// most blocks of the forward, each with its own partial sums: two per SM (a block for every few rows instead: 16384 x 128
+// k 8 without counts 12.7 us, not 12.1; 16384 x 512 40 us, not 37)
+constexpr int kRouterBlocks = 304;
 // warps of a block of the forward for rows of 32 n experts: as many as the registers of two blocks an SM allow
-constexpr int forward_warps(int n) { return n <= 4 ? 24 : n <= 8 ? 16 : 8; }
+constexpr int forward_warps(int n) { return n <= 4 ? 24 : n <= 8 ? 16 : n <= 12 ? 12 : n <= 16 ? 10 : 6; }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -120,6 +122,69 @@ __device__ __forceinline__ void put_losses(const RouterArgs& a, float total, flo
     a.losses[1] = a.T ? a.z / T * z : 0.0f;
 }
 
+// A lane's keys, from which its best is taken again and again. Up to four are sorted once (stable: equal keys stay in
+// the order of their experts), and the next is a shift away; more are looked through when their best goes. 16384 x 128
+// with k 8 and losses: 20.4 us sorted, 23.1 looked through.
+template <int N>
+struct LaneKeys {
+    uint32_t key[N];
+    uint32_t b;
+    int place;  // N <= 4: the places in order, a byte each
+    __device__ __forceinline__ explicit LaneKeys(const uint32_t (&k)[N]) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) key[j] = k[j];
+        if constexpr (N <= 4) {
+            uint32_t at[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) at[j] = j;
+#pragma unroll
+            for (int end = N - 1; end > 0; --end)
+#pragma unroll
+                for (int j = 0; j < end; ++j) {
+                    const bool swap = key[j] < key[j + 1];
+                    const uint32_t hi = max(key[j], key[j + 1]), lo = min(key[j], key[j + 1]);
+                    const uint32_t first = swap ? at[j + 1] : at[j];
+                    at[j + 1] = swap ? at[j] : at[j + 1];
+                    at[j] = first;
+                    key[j] = hi;
+                    key[j + 1] = lo;
+                }
+            place = 0;
+#pragma unroll
+            for (int j = 0; j < N; ++j) place |= at[j] << (8 * j);
+        } else {
+            place = -1;
+            look();
+        }
+    }
+    __device__ __forceinline__ uint32_t best() const { return N <= 4 ? key[0] : b; }
+    __device__ __forceinline__ int at() const { return N <= 4 ? place & 255 : place; }
+    __device__ __forceinline__ void next() {
+        if constexpr (N <= 4) {
+#pragma unroll
+            for (int j = 0; j + 1 < N; ++j) key[j] = key[j + 1];
+            key[N - 1] = 0;
+            place = int(uint32_t(place) >> 8);
+        } else {
+            look();
+        }
+    }
+    // the best without the one at `place`
+    __device__ __forceinline__ void look() {
+        b = 0;
+        int found = 0;
+#pragma unroll
+        for (int j = N - 1; j >= 0; --j) {
+            if (j == place) key[j] = 0;
+            if (key[j] >= b) {
+                b = key[j];
+                found = j;
+            }
+        }
+        place = found;
+    }
+};
+
 template <int N>
 __global__ void __launch_bounds__(32 * forward_warps(N)) router_forward_kernel(RouterArgs a) {
     constexpr int kWarps = forward_warps(N);
@@ -134,7 +199,8 @@ __global__ void __launch_bounds__(32 * forward_warps(N)) router_forward_kernel(R
     float psum[N] = {};
     float zsum = 0.0f;
     const int64_t step = int64_t(gridDim.x) * kWarps;
-    int64_t t = int64_t(blockIdx.x) * kWarps + warp;
+    // a block's rows lie gridDim apart: the last round's fall to every block, not to the first ones' warps
+    int64_t t = int64_t(warp) * gridDim.x + blockIdx.x;
     float ahead[N];  // the next row, under way during this one
     if (t < a.T) load_row<N>(a, t, ahead);
     if (threadIdx.x == 0 && blockIdx.x == 0 && losses) reinterpret_cast<unsigned*>(a.finish)[0] = 0;
@@ -172,44 +238,25 @@ __global__ void __launch_bounds__(32 * forward_warps(N)) router_forward_kernel(R
             for (int j = 0; j < N; ++j) psum[j] = fmaf(p[j], rp, psum[j]);
             zsum = fmaf(r.lse, r.lse, zsum);
         }
-        // each lane's best key and its place; the lane that loses its best looks for the next
         uint32_t key[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             key[j] = order_key(l[j]);
             if (a.bias && key[j]) key[j] = order_key((a.sigmoid ? p[j] : p[j] * r.rz) + a.bias[lane + 32 * j]);
         }
-        uint32_t best = 0;
-        int at = 0;
-#pragma unroll
-        for (int j = N - 1; j >= 0; --j)
-            if (key[j] >= best) {
-                best = key[j];
-                at = j;
-            }
+        LaneKeys<N> mine(key);
         int my_id = -1;
         uint32_t my_key = 0;
         for (int s = 0; s < a.k; ++s) {
-            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, mine.best());
             if (top == 0) break;
-            const uint32_t id = __reduce_min_sync(0xffffffffu, best == top ? uint32_t(lane + 32 * at) : 0xffffffffu);
+            const uint32_t here = uint32_t(lane + 32 * mine.at());
+            const uint32_t id = __reduce_min_sync(0xffffffffu, mine.best() == top ? here : 0xffffffffu);
             if (lane == s) {
                 my_id = int(id);
                 my_key = top;
             }
-            if (uint32_t(lane + 32 * at) == id && best == top) {
-                best = 0;
-                int next = 0;
-#pragma unroll
-                for (int j = N - 1; j >= 0; --j) {
-                    if (j == at) key[j] = 0;
-                    if (key[j] >= best) {
-                        best = key[j];
-                        next = j;
-                    }
-                }
-                at = next;
-            }
+            if (here == id) mine.next();  // a lane whose best is not the top has another place
         }
         // the chosen scores, one a lane: from the logit, which the key still is (not with a bias)
         float my_l = value_of(my_key);
@@ -237,11 +284,11 @@ __global__ void __launch_bounds__(32 * forward_warps(N)) router_forward_kernel(R
     if (losses) {
         for (int i = threadIdx.x; i < a.E; i += blockDim.x) {
             float v = s_sum[i];
+#pragma unroll
             for (int w = 1; w < kWarps; ++w) v += s_sum[w * a.E + i];
             s_sum[i] = v;
         }
-        if (threadIdx.x == 0)
-            for (int w = 1; w < kWarps; ++w) zsum += s_z[w];
+        if (warp == 0) zsum = warp_sum(lane < kWarps ? s_z[lane] : 0.0f);
     }
     __syncthreads();
     if (gridDim.x == 1) {  // nothing to add up with
@@ -270,12 +317,13 @@ __global__ void __launch_bounds__(32 * forward_warps(N)) router_forward_kernel(R
 }
 
 // Counts and losses from the blocks' partial sums. Block g: 32 experts, warp w adding the blocks w,
-// w + 8, ... in order, then the warps' sums in warp order; block 0 the z terms too. The block that
+// w + 32, ... in order, then the warps' sums in warp order; block 0 the z terms too. The block that
 // finishes last adds up the experts' parts of the balance loss, in block order.
 // a.finish: [0] blocks done (0 at the start), [1] z, [2 + g] block g's part.
-__global__ void __launch_bounds__(256) router_finish_kernel(RouterArgs a, int blocks) {
-    __shared__ int s_n[8][32];
-    __shared__ float s_p[8][32];
+constexpr int kFinishWarps = 32;
+__global__ void __launch_bounds__(32 * kFinishWarps) router_finish_kernel(RouterArgs a, int blocks) {
+    __shared__ int s_n[kFinishWarps][32];
+    __shared__ float s_p[kFinishWarps][32];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
@@ -284,8 +332,8 @@ __global__ void __launch_bounds__(256) router_finish_kernel(RouterArgs a, int bl
     float p = 0.0f;
     if (e < a.E) {
         const float* from = a.part + e;
-#pragma unroll 8
-        for (int b = warp; b < blocks; b += 8) {
+#pragma unroll 10
+        for (int b = warp; b < blocks; b += kFinishWarps) {
             n += reinterpret_cast<const int*>(from)[b * step];
             if (a.losses) p += from[b * step + a.E];
         }
@@ -295,7 +343,7 @@ __global__ void __launch_bounds__(256) router_finish_kernel(RouterArgs a, int bl
     __syncthreads();
     if (blockIdx.x == 0 && a.losses && warp == 1) {  // lane l: blocks l, l + 32, ...
         float z = 0.0f;
-#pragma unroll 8
+#pragma unroll 10
         for (int b = lane; b < blocks; b += 32) z += a.part[b * step + 2 * a.E];
         z = warp_sum(z);
         if (lane == 0) {
@@ -306,7 +354,7 @@ __global__ void __launch_bounds__(256) router_finish_kernel(RouterArgs a, int bl
     __syncthreads();
     if (warp) return;
 #pragma unroll
-    for (int w = 1; w < 8; ++w) {
+    for (int w = 1; w < kFinishWarps; ++w) {
         n += s_n[w][lane];
         p += s_p[w][lane];
     }
@@ -422,9 +470,9 @@ moe_status check_router(const moe_router_config* c, int64_t T) {
     return MOE_OK;
 }
 
-int router_blocks(int64_t T, int E, int most) {
+int router_blocks(int64_t T, int E) {
     const int warps = forward_warps((E + 31) / 32);
-    return int(std::min<int64_t>(most, std::max<int64_t>(1, (T + warps - 1) / warps)));
+    return int(std::min<int64_t>(kRouterBlocks, std::max<int64_t>(1, (T + warps - 1) / warps)));
 }
 constexpr int kFinish = 64;  // words of a.finish
 
@@ -472,7 +520,7 @@ moe_status moe_router_size(const moe_router_config* cfg, int64_t T, size_t* byte
     *bytes = 0;
     const moe_status st = check_router(cfg, T);
     if (st != MOE_OK) return st;
-    *bytes = (size_t(router_blocks(T, int(cfg->num_experts), kRouterBlocks)) * size_t(2 * cfg->num_experts + 1) + kFinish) * sizeof(float);
+    *bytes = (size_t(router_blocks(T, int(cfg->num_experts))) * size_t(2 * cfg->num_experts + 1) + kFinish) * sizeof(float);
     return MOE_OK;
 }
 
@@ -498,7 +546,7 @@ moe_status moe_router_forward(const moe_router_config* cfg, int64_t T, const voi
     a.counts = counts;
     a.losses = losses;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int blocks = T == 0 ? 0 : router_blocks(T, a.E, counts ? kRouterBlocks : 4 * kRouterBlocks);
+    const int blocks = T == 0 ? 0 : router_blocks(T, a.E);
     cudaError_t e = cudaSuccess;
     if (T > 0) {
         e = by_experts(a.E, [&](auto n) {
@@ -512,7 +560,7 @@ moe_status moe_router_forward(const moe_router_config* cfg, int64_t T, const voi
     if (counts && blocks != 1) {
         // without tokens nothing has set the counter of finished blocks
         if (T == 0 && losses && cudaMemsetAsync(a.finish, 0, sizeof(float), s) != cudaSuccess) return MOE_ERR_CUDA;
-        e = launch_pdl(router_finish_kernel, dim3(unsigned((a.E + 31) / 32)), dim3(256), 0, s, a, blocks);
+        e = launch_pdl(router_finish_kernel, dim3(unsigned((a.E + 31) / 32)), dim3(32 * kFinishWarps), 0, s, a, blocks);
         count_launch();
     }
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
