@@ -384,7 +384,7 @@ moe_status moe_selftest_timeout(moe_handle* h, void* stream);
  * moe_forward runs row tiles of 128 tokens per expert; a decode step has a few
  * tokens in all, and its time is the reading of the chosen experts' weights.
  * moe_decode computes the same layer for up to MOE_DECODE_MAX_TOKENS tokens and
- * reads each chosen expert's weights once. No backward, no saved state. */
+ * reads each chosen expert's weights from memory once. No backward, no saved state. */
 enum { MOE_DECODE_MAX_TOKENS = 64 };
 typedef struct moe_decoder moe_decoder;
 
@@ -429,7 +429,9 @@ moe_status moe_decode_status(moe_decoder* d, void* stream);
  * Layer norm, or with MOE_NORM_RMS its form without the mean, over rows of
  * `hidden` elements, with the residual add before it and the residual stream's
  * gradient after it; 1 <= hidden <= 32768. Rows may have any stride >= hidden and
- * any alignment of their element type; 16-byte aligned rows are the fast case. */
+ * any alignment of their element type; 16-byte aligned rows are the fast case. Rows
+ * are read in whole 16-byte words: those that a row shares with its neighbours are
+ * read with it (never written). */
 typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
 typedef enum { MOE_T_BF16 = 0, MOE_T_FP32 = 1 } moe_dtype;
 typedef struct {

@@ -32,6 +32,9 @@
 // f16 too: a slice of a token's row is scaled by the power of two that brings its
 // largest value under 2^15, so that x (8 significant bits) fits one f16 term and a two, with
 // an error of at most 2^-38 of the slice's largest value, and the scale is taken back per slot.
+//
+// Measured (graph replays): H 2048, I 1024, E 96 top-6 in BF16 with 1, 8, 64 tokens 26 us (3.4 TB/s), 87 us (5.7),
+// 204 us (5.9); H 7168, I 2048, E 128 top-6 in MXFP8 with 4 tokens 207 us (5.3).
 #include <algorithm>
 #include <cmath>
 #include <memory>

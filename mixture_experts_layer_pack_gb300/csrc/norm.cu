@@ -8,6 +8,10 @@
 //   dx = rstd (g - sum(g)/H - xhat sum(g xhat)/H) + dsum,
 //   dw = sum_t dy xhat, db = sum_t dy.
 // All statistics and sums are fp32.
+//
+// Bound by memory where rows are many: 16384 x 4096 bf16 with a residual, forward 84 us (6.4 TB/s), backward with the
+// joining gradient and the weights' 87 us (6.2 TB/s); 16384 x 2051, rows that start anywhere, 53 and 54 us (5.0 TB/s). One
+// row of 2048: 2.2 us. s and y are rounded once each, to the types that the next reader takes.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -93,8 +97,8 @@ constexpr int kWidest = 768;   // most threads of a row
 constexpr int kSumWarps = 32;  // places of a sum
 
 // Sums over the `warps` warps of a row (warps first, first + 1, ... of the block); every thread of
-// the row gets them, in an order fixed by the number of warps. part: 16 values for each sum, of
-// which the callers alternate two, so that one barrier a sum is enough; `threads`: of the barrier.
+// the row gets them, in an order fixed by the number of warps. part: kSumWarps values for each sum, zeros
+// where there is no warp, of which the callers alternate two, so that one barrier a sum is enough.
 template <int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], int warps, int first, float* part) {
 #pragma unroll
