@@ -30,7 +30,6 @@ constexpr int kMaxHidden = 32768;
 constexpr int kMaxChunks = 608;     // blocks of the backward that sum weight gradients: four per SM at most
 constexpr int kRowThreads = 512;    // most threads of a row: 128 registers each
 constexpr int kColumns = 16;        // columns of a thread where rows are streamed
-constexpr int kFewRows = 304;       // rows up to which the forward spreads a row over as many threads as it can
 
 // V consecutive elements as fp32: one 16-byte access (two for 8 fp32, one of 8 bytes for 4 bf16), or with V 1 a scalar
 template <int V>
@@ -182,7 +181,8 @@ struct NormFwd {
     bool w_bf16;
 };
 
-// A row stays in the registers of its threads, NV pieces of V elements each: read once,
+// ---- Rows of more than kStreamed columns in whole 16-byte pieces: a block a row
+// The row stays in the registers of its threads, NV pieces of V elements each: read once,
 // written once, and the variance is of differences from the mean, not of squares.
 template <typename XT, typename YT, bool RMS, int V, int NV>
 __global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
@@ -191,10 +191,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    const int tpr = a.tpr, group = threadIdx.x / tpr, col = threadIdx.x - group * tpr, warps = tpr >> 5;
-    const int64_t row = int64_t(blockIdx.x) * (blockDim.x / tpr) + group;
-    const bool live = row < a.T;  // the block's last rows may not exist; their threads join the sums
-    const int64_t t = live ? row : a.T - 1;
+    const int tpr = blockDim.x, col = threadIdx.x, warps = tpr >> 5;
+    const int64_t t = blockIdx.x;
     const XT* x = static_cast<const XT*>(a.x) + t * a.xs;
     float v[NV][V];
 #pragma unroll
@@ -213,13 +211,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
             load_v<V>(r + i, f);
 #pragma unroll
             for (int q = 0; q < V; ++q) v[j][q] = round_to(v[j][q] + f[q], x);
+            store_v<V>(s + i, v[j]);
         }
-        if (live)
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int i = (col + j * tpr) * V;
-                if (i < a.H) store_v<V>(s + i, v[j]);
-            }
     }
     const float inv = 1.0f / a.H;
     float mean = 0.0f;
@@ -230,7 +223,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
             if ((col + j * tpr) * V < a.H)
 #pragma unroll
                 for (int q = 0; q < V; ++q) sum[0] += v[j][q];
-        row_sum<1>(sum, warps, group * warps, part[0]);
+        row_sum<1>(sum, warps, 0, part[0]);
         mean = sum[0] * inv;
     }
     float sq[1] = {0.0f};
@@ -242,9 +235,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
                 v[j][q] -= mean;
                 sq[0] = fmaf(v[j][q], v[j][q], sq[0]);
             }
-    row_sum<1>(sq, warps, group * warps, part[1]);
+    row_sum<1>(sq, warps, 0, part[1]);
     const float rstd = rsqrtf(sq[0] * inv + a.eps);
-    if (!live) return;
     YT* y = static_cast<YT*>(a.y) + t * a.ys;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -266,7 +258,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(NormFwd a) {
     }
 }
 
-// ---- More rows: streamed through shared memory
+// ---- Rows of up to kStreamed columns: streamed through shared memory (one row of 2048 2.5 us, as without it)
 // A stage holds one row of each input for each row group of the block, brought by bulk copies;
 // `stages` of them are under way while one is worked on. A copy takes the 16-byte words that cover
 // its row, so rows may start anywhere; rows that start on 16 bytes are then read in pieces of V
@@ -878,13 +870,12 @@ bool rows_aligned(const void* p, int64_t stride, int32_t type, size_t bytes) {
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// Threads of a row that takes `pieces` accesses, `each` to a thread, and of the block: rows of up
-// to 128 threads share a block of 256.
+// Threads of a row of H columns, and of the block: rows of up to 128 threads share a block of 256.
 struct RowShape {
     int tpr, threads;
 };
-RowShape row_shape(int pieces, int each) {
-    int tpr = ((pieces + each - 1) / each + 31) / 32 * 32;
+RowShape row_shape(int64_t H) {
+    const int tpr = (int((H + kColumns - 1) / kColumns) + 31) / 32 * 32;
     if (tpr <= 128) {
         int p = 32;
         while (p < tpr) p *= 2;
@@ -919,14 +910,16 @@ void add_input(Stream& st, const void* p, int64_t stride, int32_t type, int64_t 
 StreamShape stream_shape(int64_t H, int most, int64_t T, int least, int aim, bool weights, Stream& st) {
     int sms = 152, device = 0;
     if (cudaGetDevice(&device) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
-    const RowShape r = row_shape(int((H + kColumns - 1) / kColumns), 1);
+    const RowShape r = row_shape(H);
     const int groups = r.threads / r.tpr, stage = groups * st.group_bytes;
     int per = std::max(1, 512 / r.threads);  // 128 registers a thread
     if (2 * stage * per > kStreamBytes) per = 1;
     const size_t fixed = weights ? kColumns * r.tpr * sizeof(float) : 0;
     const int most_stages = std::min(kMaxStages, std::max(2, kStreamBytes / per / stage));
     st.stages = std::min(most_stages, std::max(least, aim / per / stage));
-    const int64_t blocks = std::min<int64_t>(std::min(per * sms, most), (T + 2 * groups - 1) / (2 * groups));
+    // no more blocks than have rows. The backward's write partial sums: two rows a group, once there is a block for every SM
+    const int64_t single = (T + groups - 1) / groups;
+    const int64_t blocks = std::min<int64_t>(std::min(per * sms, most), weights && single > sms ? (single + 1) / 2 : single);
     const size_t sums = groups > 1 ? 2 * size_t(H) * sizeof(float) : 0;
     return {r.tpr, r.threads, int(blocks), fixed + std::max(size_t(st.stages) * size_t(stage), sums)};
 }
@@ -952,18 +945,6 @@ cudaError_t launch_stream(const StreamShape& sh, A& a, Stream& st, cudaStream_t 
     a.tpr = sh.tpr;
     count_launch();
     return launch_pdl(Kernel, dim3(unsigned(sh.blocks)), dim3(unsigned(sh.threads)), sh.smem, cs, a, st);
-}
-
-template <typename XT, typename YT, bool RMS, int V, int NV>
-cudaError_t launch_norm_forward(NormFwd& a, cudaStream_t st) {
-    const RowShape r = row_shape(a.H / V + (a.H % V != 0), NV);
-    const int rows = r.threads / r.tpr;
-    a.tpr = r.tpr;
-    // a few rows: no threads without one
-    const int threads = a.T < rows ? int(a.T) * r.tpr : r.threads;
-    const int64_t blocks = (a.T + threads / r.tpr - 1) / (threads / r.tpr);
-    count_launch();
-    return launch_pdl(norm_forward_kernel<XT, YT, RMS, V, NV>, dim3(unsigned(blocks)), dim3(unsigned(threads)), 0, st, a);
 }
 
 }  // namespace
@@ -1003,11 +984,6 @@ moe_status moe_norm_forward(const moe_norm_config* cfg, int64_t T, const void* x
                           (!residual || rows_aligned(sum, sum_stride, cfg->x_type, 16)) &&
                           rows_aligned(y, y_stride, cfg->y_type, YB) && rows_aligned(weight, 0, cfg->w_type, wb) &&
                           rows_aligned(bias, 0, cfg->w_type, wb);
-        // few rows: as many threads a row as can be, for the shortest time of a row; more: streamed
-        const bool few = T <= kFewRows;
-        const int64_t pieces = H / V;
-        if (wide && few && pieces <= kRowThreads) return launch_norm_forward<X, Y, R, V, 1>(a, cs);
-        if (!wide && few && H <= 4 * kRowThreads) return launch_norm_forward<X, Y, R, 1, 4>(a, cs);
         if (H <= kStreamed) {
             Stream st{};
             add_input(st, x, x_stride, cfg->x_type, H);
@@ -1024,8 +1000,9 @@ moe_status moe_norm_forward(const moe_norm_config* cfg, int64_t T, const void* x
             if (sh.smem <= kMostShared)
                 return sh.threads <= kNarrow ? go(Int<kNarrow>{}) : sh.threads <= kWide ? go(Int<kWide>{}) : go(Int<kWidest>{});
         }
-        if (wide && pieces <= 4 * kRowThreads) return launch_norm_forward<X, Y, R, V, 4>(a, cs);
         count_launch();
+        if (wide && H / V <= 4 * kRowThreads)
+            return launch_pdl(norm_forward_kernel<X, Y, R, V, 4>, dim3(unsigned(T)), dim3(unsigned((H / V + 127) / 128 * 32)), 0, cs, a);
         return wide ? launch_pdl(norm_forward_wide_kernel<X, Y, R, V>, dim3(unsigned(T)), dim3(kRowThreads), 0, cs, a)
                     : launch_pdl(norm_forward_wide_kernel<X, Y, R, 1>, dim3(unsigned(T)), dim3(kRowThreads), 0, cs, a);
     });

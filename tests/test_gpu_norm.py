@@ -126,6 +126,8 @@ CASES = [
     (310, 12288, BF16, BF16, BF16, True, True, 0.0, 0, 0),
     (310, 12288, F32, BF16, F32, True, True, 0.0, 4, 4),
     (8200, 4104, BF16, BF16, BF16, True, True, 0.0, 0, 0),
+    (40, 16384, BF16, BF16, F32, True, True, 0.0, 0, 0),
+    (40, 14008, BF16, F32, BF16, False, True, 1.0, 8, 8),
 ]
 
 
