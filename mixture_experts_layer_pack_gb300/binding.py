@@ -807,6 +807,7 @@ class MoENorm:
         self.hidden, self.eps, self.kind, self.device = int(hidden), float(eps), int(kind), torch.device(device)
         self._types = {torch.bfloat16: MOE_T_BF16, torch.float32: MOE_T_FP32}
         self._cfgs, self._sizes = {}, {}
+        self._empty, self._f32, self._row = torch.empty, torch.float32, torch.Size((self.hidden,))
         self._torch, self._stream = torch, _current_stream_of()
         self._forward, self._backward = load().moe_norm_forward, load().moe_norm_backward
         _check(load().moe_norm_forward(moe_norm_config(self.hidden, self.eps, self.kind, 0, 0, 0), 0, None, self.hidden,
@@ -825,7 +826,7 @@ class MoENorm:
             raise ValueError(f"{what} must be [T, hidden] rows of the right type")
 
     def _vector(self, t, dtype):
-        if t.shape != (self.hidden,) or t.dtype != dtype or t.stride(0) != 1:
+        if t.shape != self._row or t.dtype != dtype or t.stride(0) != 1:
             raise ValueError("weight and bias, and their gradients, must be [hidden] vectors of one type")
 
     @_on_stream
@@ -833,7 +834,7 @@ class MoENorm:
         """(y, s, mean, rstd): s = x + residual (x itself without one), y = norm(s) weight + bias in
         out_dtype (x's by default); mean is None for RMS norm. s, mean and rstd are what backward takes.
         `stream`: where (the current stream)."""
-        torch = self._torch
+        empty = self._empty
         T, H = shape = x.shape
         xt, wt, dev = x.dtype, weight.dtype, x.device
         yt = xt if out_dtype is None else out_dtype
@@ -843,17 +844,22 @@ class MoENorm:
         if bias is not None:
             self._vector(bias, wt)
         cfg = self._cfgs.get((xt, yt, wt)) or self._cfg(xt, yt, wt)
-        y = torch.empty(shape, dtype=yt, device=dev)
-        rstd = torch.empty(T, dtype=torch.float32, device=dev)
-        mean = torch.empty(T, dtype=torch.float32, device=dev) if self.kind == MOE_NORM_LAYER else None
+        y = empty(shape, dtype=yt, device=dev)
+        rstd = empty(T, dtype=self._f32, device=dev)
+        if self.kind == MOE_NORM_LAYER:
+            mean = empty(T, dtype=self._f32, device=dev)
+            mean_at = mean.data_ptr()
+        else:
+            mean = mean_at = None
         if residual is None:
-            s, res, out = x, (None, 0), (None, 0)
+            s, res_at, res_ld, s_at, s_ld = x, None, 0, None, 0
         else:
             self._same(residual, shape, xt, "residual")
-            s = torch.empty(shape, dtype=xt, device=dev)
-            res, out = (residual.data_ptr(), _ld(residual)), (s.data_ptr(), H)
-        status = self._forward(cfg, T, x.data_ptr(), _ld(x), *res, weight.data_ptr(), _addr(bias), *out, y.data_ptr(), H,
-                               _addr(mean), rstd.data_ptr(), self._stream(x.get_device()))
+            s = empty(shape, dtype=xt, device=dev)
+            res_at, res_ld, s_at, s_ld = residual.data_ptr(), _ld(residual), s.data_ptr(), H
+        status = self._forward(cfg, T, x.data_ptr(), x.stride(0) if T > 1 else H, res_at, res_ld, weight.data_ptr(),
+                               None if bias is None else bias.data_ptr(), s_at, s_ld, y.data_ptr(), H, mean_at,
+                               rstd.data_ptr(), self._stream(x.get_device()))
         if status:
             raise MoeError(status, "moe_norm_forward")
         return y, s, mean, rstd
@@ -863,40 +869,48 @@ class MoENorm:
         """(ds, dweight, dbias) for the gradient dy of y, joined by dsum, the gradient that reaches s
         past the norm. dweight (and, with `bias`, dbias) are new fp32 vectors, or the given
         fp32 / bf16 buffers, overwritten or (accumulate) added to. `stream`: where (the current stream)."""
-        torch = self._torch
+        torch, empty = self._torch, self._empty
         T, H = shape = s.shape
-        st, dev, f32 = s.dtype, s.device, torch.float32
+        st, yt, wt, dev, f32 = s.dtype, dy.dtype, weight.dtype, s.device, self._f32
         if H != self.hidden or s.stride(1) != 1:
             raise ValueError("s must be [T, hidden] rows")
-        self._same(dy, shape, dy.dtype, "dy")
-        self._vector(weight, weight.dtype)
-        for v in (mean, rstd):
-            if v is None:
-                if v is rstd or self.kind == MOE_NORM_LAYER:
-                    raise ValueError("mean and rstd must be the forward's [T] fp32")
-            elif v.dtype != f32 or v.shape != (T,) or not v.is_contiguous():
-                raise ValueError("mean and rstd must be the forward's [T] fp32")
+        if dy.shape != shape or dy.stride(1) != 1:
+            raise ValueError("dy must be [T, hidden] rows of the right type")
+        self._vector(weight, wt)
+        rows = (T,)
+        if rstd is None or rstd.dtype != f32 or rstd.shape != rows or not rstd.is_contiguous() or (
+                self.kind == MOE_NORM_LAYER if mean is None else
+                mean.dtype != f32 or mean.shape != rows or not mean.is_contiguous()):
+            raise ValueError("mean and rstd must be the forward's [T] fp32")
         if accumulate and (dweight is None or (bias and dbias is None)):
             raise ValueError("accumulate adds to given buffers")
         if dsum is not None:
             self._same(dsum, shape, st, "dsum")
-        cfg = self._cfg(st, dy.dtype, weight.dtype)
-        ds = torch.empty(shape, dtype=st, device=dev)
-        if dweight is None:
-            dweight = torch.empty(H, dtype=f32, device=dev)
-        gt = dweight.dtype
-        if bias and dbias is None:
-            dbias = torch.empty(H, dtype=gt, device=dev)
-        if gt not in self._types:
-            raise ValueError("dweight and dbias must be fp32 or bf16")
-        self._vector(dweight, gt)
-        if dbias is not None:
-            self._vector(dbias, gt)
+        cfg = self._cfgs.get((st, yt, wt)) or self._cfg(st, yt, wt)
+        ds = empty(shape, dtype=st, device=dev)
+        if dweight is None and dbias is None:
+            gt = f32
+            dweight = empty(H, dtype=f32, device=dev)
+            if bias:
+                dbias = empty(H, dtype=f32, device=dev)
+        else:
+            if dweight is None:
+                dweight = empty(H, dtype=f32, device=dev)
+            gt = dweight.dtype
+            if bias and dbias is None:
+                dbias = empty(H, dtype=gt, device=dev)
+            if gt not in self._types:
+                raise ValueError("dweight and dbias must be fp32 or bf16")
+            self._vector(dweight, gt)
+            if dbias is not None:
+                self._vector(dbias, gt)
         size = _sized(moe_norm_backward_size, self._sizes, cfg, T)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-        status = self._backward(cfg, T, dy.data_ptr(), _ld(dy), s.data_ptr(), _ld(s), weight.data_ptr(), _addr(mean),
-                                rstd.data_ptr(), _addr(dsum), 0 if dsum is None else _ld(dsum), ds.data_ptr(), H,
-                                dweight.data_ptr(), _addr(dbias), MOE_G_FP32 if gt == f32 else MOE_G_BF16,
+        workspace = empty(size, dtype=torch.uint8, device=dev)
+        many = T > 1  # a single row has no stride of its own
+        status = self._backward(cfg, T, dy.data_ptr(), dy.stride(0) if many else H, s.data_ptr(), s.stride(0) if many else H,
+                                weight.data_ptr(), None if mean is None else mean.data_ptr(), rstd.data_ptr(), _addr(dsum),
+                                0 if dsum is None else _ld(dsum), ds.data_ptr(), H, dweight.data_ptr(),
+                                None if dbias is None else dbias.data_ptr(), MOE_G_FP32 if gt is f32 else MOE_G_BF16,
                                 1 if accumulate else 0, workspace.data_ptr(), size, self._stream(s.get_device()))
         if status:
             raise MoeError(status, "moe_norm_backward")
@@ -912,7 +926,7 @@ class MoERouter:
         self.E, self.k = int(num_experts), int(topk)
         self.device = torch.device(device)
         args = (self.E, self.k, int(score), int(bool(normalise)), float(scale), float(aux_coeff), float(z_coeff))
-        self._sizes = {}
+        self._sizes, self._empty, self._f32 = {}, torch.empty, torch.float32
         self._cfgs = {torch.bfloat16: moe_router_config(*args, MOE_T_BF16),
                       torch.float32: moe_router_config(*args, MOE_T_FP32)}
         self.losses_wanted = aux_coeff != 0 or z_coeff != 0
@@ -931,22 +945,25 @@ class MoERouter:
         """(ids [T,k] int32, probs [T,k] fp32, counts [E] int32, losses [2] fp32 or None): the input of
         forward_topk, the routes per expert, and the balance and z losses where a coefficient asks for them.
         `stream`: where (the current stream)."""
-        torch = self._torch
-        cfg = self._cfg(logits)
-        T, dev = logits.shape[0], logits.device
-        if select_bias is not None and (select_bias.shape != (self.E,) or select_bias.dtype != torch.float32 or
-                                        select_bias.stride(0) != 1):
+        torch, empty, f32 = self._torch, self._empty, self._f32
+        cfg = self._cfgs.get(logits.dtype)
+        T, E = logits.shape
+        if cfg is None or E != self.E or logits.stride(1) != 1:
+            raise ValueError("logits must be [T, E] rows, bf16 or fp32")
+        dev = logits.device
+        if select_bias is not None and (select_bias.shape != (E,) or select_bias.dtype != f32 or select_bias.stride(0) != 1):
             raise ValueError("select_bias must be [E] fp32")
         slots = (T, self.k)
-        ids = torch.empty(slots, dtype=torch.int32, device=dev)
-        probs = torch.empty(slots, dtype=torch.float32, device=dev)
-        counts = torch.empty(self.E, dtype=torch.int32, device=dev)
-        losses = torch.empty(2, dtype=torch.float32, device=dev) if self.losses_wanted else None
+        ids = empty(slots, dtype=torch.int32, device=dev)
+        probs = empty(slots, dtype=f32, device=dev)
+        counts = empty(E, dtype=torch.int32, device=dev)
+        losses = empty(2, dtype=f32, device=dev) if self.losses_wanted else None
         size = _sized(moe_router_size, self._sizes, cfg, T)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-        status = self._forward(cfg, T, logits.data_ptr(), _ld(logits), _addr(select_bias), ids.data_ptr(),
-                               probs.data_ptr(), counts.data_ptr(), _addr(losses), workspace.data_ptr(), size,
-                               self._stream(logits.get_device()))
+        workspace = empty(size, dtype=torch.uint8, device=dev)
+        status = self._forward(cfg, T, logits.data_ptr(), logits.stride(0) if T > 1 else E,
+                               None if select_bias is None else select_bias.data_ptr(), ids.data_ptr(),
+                               probs.data_ptr(), counts.data_ptr(), None if losses is None else losses.data_ptr(),
+                               workspace.data_ptr(), size, self._stream(logits.get_device()))
         if status:
             raise MoeError(status, "moe_router_forward")
         return ids, probs, counts, losses

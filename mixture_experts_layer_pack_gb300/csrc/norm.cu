@@ -11,7 +11,7 @@
 //
 // Bound by memory where rows are many: 16384 x 4096 bf16 with a residual, forward 84 us (6.4 TB/s), backward with the
 // joining gradient and the weights' 87 us (6.2 TB/s); 16384 x 2051, rows that start anywhere, 53 and 54 us (5.0 TB/s). One
-// row of 2048: 2.2 us. s and y are rounded once each, to the types that the next reader takes.
+// row of 2048: 2.4 us. s and y are rounded once each, to the types that the next reader takes.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -885,15 +885,15 @@ RowShape row_shape(int64_t H) {
 }
 
 // The streamed kernels' shape, 16 columns a thread: row groups to a block of 256 threads (or one
-// of more), two such blocks an SM where shared memory holds two stages of each, and no more blocks than have two rows a
-// group to themselves, so that the weight gradients' partial sums stay small beside the rows.
-// Stages: `least`, and more up to `aim` bytes an SM. What is left is cache, for the weights that the backward reads
-// every row: 128 KB against 176: 4096 x 2048 bf16 20.0 against 21.9 us. And reads that run far ahead of the writes cost
-// memory rate once the rows do not stay in L2: the forward with a residual at 16384 x 4096 bf16 takes 84 us with two
-// stages (64 KB), 92 with three, 96 with five; at 16384 x 1024 24.3 with two and 22.9 with three. Without a residual
-// more is better: 4000 x 8192 fp32 45 us with 96 KB, 41 with 176.
+// of more), and two such blocks an SM where shared memory holds two stages of each.
+// Stages: `least`, and more up to `aim` bytes an SM. Reads that run far ahead of the writes cost memory rate once the
+// rows do not stay in L2: the forward with a residual at 16384 x 4096 bf16 takes 84 us with two stages (64 KB), 92
+// with three, 96 with five; at 16384 x 1024 24.3 with two and 22.9 with three. Without a residual more is better:
+// 4000 x 8192 fp32 45 us with 96 KB, 41 with 176. The backward: 16384 x 4096 75 us with 128 KB, 70 with 176;
+// 8192 x 7168 with a joining gradient 86 and 78; but 1500 x 4096 15.2 and 16.2, 3000 x 9001 75 and 85.
 // 32 columns a thread: 52 against 57 us at 16384 x 4096 bf16, but 46 against 41 at 4000 x 8192 fp32 and 21.6 against
 // 17.3 at 32768 x 512 bf16; 8 columns: 86 us.
+constexpr int64_t kLargeBytes = int64_t(256) << 20;  // read and written: twice what L2 holds
 constexpr int kStreamBytes = 176 << 10;  // most of an SM's shared memory that is asked for
 struct StreamShape {
     int tpr, threads, blocks;
@@ -917,7 +917,8 @@ StreamShape stream_shape(int64_t H, int most, int64_t T, int least, int aim, boo
     const size_t fixed = weights ? kColumns * r.tpr * sizeof(float) : 0;
     const int most_stages = std::min(kMaxStages, std::max(2, kStreamBytes / per / stage));
     st.stages = std::min(most_stages, std::max(least, aim / per / stage));
-    // no more blocks than have rows. The backward's write partial sums: two rows a group, once there is a block for every SM
+    // No more blocks than have rows. The backward's write partial sums, which have to stay small beside the rows: two rows
+    // a group once there is a block for every SM (608 x 2048 bf16 8.7 us, 10.9 with one; 64 x 2048 7.5, 6.5 with one)
     const int64_t single = (T + groups - 1) / groups;
     const int64_t blocks = std::min<int64_t>(std::min(per * sms, most), weights && single > sms ? (single + 1) / 2 : single);
     const size_t sums = groups > 1 ? 2 * size_t(H) * sizeof(float) : 0;
@@ -988,7 +989,7 @@ moe_status moe_norm_forward(const moe_norm_config* cfg, int64_t T, const void* x
             Stream st{};
             add_input(st, x, x_stride, cfg->x_type, H);
             if (residual) add_input(st, residual, residual_stride, cfg->x_type, H);
-            const bool large = 4 * T * H * int64_t(sizeof(X)) > int64_t(256) << 20;  // twice what L2 holds
+            const bool large = 4 * T * H * int64_t(sizeof(X)) > kLargeBytes;
             const StreamShape sh = !residual ? stream_shape(H, INT_MAX, T, 3, kStreamBytes, false, st)
                                    : large   ? stream_shape(H, INT_MAX, T, 2, 96 << 10, false, st)
                                              : stream_shape(H, INT_MAX, T, 3, 128 << 10, false, st);
@@ -1067,7 +1068,8 @@ moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* 
                 if (dsum) add_input(st, dsum, dsum_stride, cfg->x_type, H);
                 // dy is read from shared memory in pieces too: its rows start on 16 bytes as well, or none is
                 const bool w16 = wide && rows_aligned(dy, dy_stride, cfg->y_type, 16);
-                const StreamShape sh = stream_shape(H, kMaxChunks, T, 3, 128 << 10, true, st);
+                const bool large = (dsum ? 4 : 3) * T * H * int64_t(sizeof(X)) > kLargeBytes;
+                const StreamShape sh = stream_shape(H, kMaxChunks, T, 3, large ? kStreamBytes : 128 << 10, true, st);
                 NormBwd b = a;
                 if (!sums) b.part = nullptr;
                 auto go = [&](auto nt) {
