@@ -25,7 +25,7 @@
 //
 // A thread loads 8 consecutive elements of a weight row and the same 8 of a token's
 // row, which are the operands of two instructions if the sum's index is taken in that
-// order. Tensor rate is not what limits it (8 tokens a weight at most, most often one).
+// order. Tensor rate is not what limits it (most often a weight meets one token, and rarely more than 8).
 // The activations a = silu(g) u go to the second product as two bf16 terms, hi + lo.
 // MXFP8 weights become f16 in registers (exact, one instruction a pair; bf16 takes
 // four) and their block scales multiply the fp32 sums of 32 columns. Their tokens are

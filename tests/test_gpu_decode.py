@@ -247,6 +247,31 @@ def test_bad_ids_are_reported_and_their_rows_keep_the_shared_part():
 
 
 @gpu
+def test_new_tables_are_refused_under_capture():
+    """A table is uploaded when its pointers change: not in a graph, which would keep the upload's source. A known one is captured."""
+    c = Layer(3, 256, 64, 4, 2, seed=13)
+    dec = c.decoder(8)
+    parts = {n: [m[e].contiguous() for e in range(4)] for n, m in (("gate", c.b1[:, :64]), ("up", c.b1[:, 64:]), ("down", c.b2))}
+    w = M.set_expert_tables(c.weights(), **parts)
+    out = torch.empty(3, 256, dtype=torch.bfloat16, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(M.MoeError) as e:
+            dec.forward_topk(c.x, c.ids, c.probs, w, out=out)
+        kept = out + 0  # the capture goes on
+    assert e.value.status == 6  # MOE_ERR_STATE
+    want = dec.forward_topk(c.x, c.ids, c.probs, w)
+    check(want, *c.reference())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dec.forward_topk(c.x, c.ids, c.probs, w, out=out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    del kept
+
+
+@gpu
 @pytest.mark.parametrize("mx", [False, True])
 def test_strides_and_expert_tables(mx):
     """Rows of wider buffers with NaN around them, experts given one by one: the same bits."""
