@@ -399,7 +399,9 @@ moe_status moe_decode_size(const moe_config* cfg, size_t* bytes);
 
 /* Creates a decoder over caller-owned device workspace (256-byte aligned, >=
  * moe_decode_size bytes, kept alive and unused by others until
- * moe_decode_destroy). Calls of one decoder run on one stream, or are ordered by
+ * moe_decode_destroy: work queued on any stream that still touches that memory has
+ * ended before this call). Its state is cleared when this returns, so that the first
+ * call may be on any stream. Calls of one decoder run on one stream, or are ordered by
  * the caller. The current CUDA device at this call is the device of every call. */
 moe_status moe_decode_create(const moe_config* cfg, void* workspace, size_t workspace_bytes, moe_decoder** out);
 void moe_decode_destroy(moe_decoder* d);
@@ -421,8 +423,9 @@ moe_status moe_decode(moe_decoder* d, int64_t T, const void* hidden, int64_t hid
                       const int32_t* topk_ids, const float* topk_probs, const moe_weights* w, void* out,
                       int64_t out_stride, void* stream);
 
-/* Synchronises `stream`, returns the status recorded since the last call (MOE_OK,
- * MOE_ERR_ROUTING or MOE_ERR_TIMEOUT) and clears it. */
+/* Synchronises `stream` (that of the decoder's last call), returns the status recorded
+ * since the last status (MOE_OK, MOE_ERR_ROUTING or MOE_ERR_TIMEOUT) and clears it, on
+ * that stream and before it returns. */
 moe_status moe_decode_status(moe_decoder* d, void* stream);
 
 /* ---- The norm in front of the layer ----

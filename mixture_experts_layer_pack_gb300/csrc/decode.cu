@@ -1360,9 +1360,13 @@ moe_status moe_decode_create(const moe_config* cfg, void* workspace, size_t work
     }
     carve_decode(s, static_cast<uint8_t*>(workspace), &d->ws);
     int device = 0, sms = 0;
+    // A memset returns before it has run, and streams that do not wait for the default one would run a first call before
+    // or during it: so it is waited for here.
+    const cudaStream_t own = cudaStreamPerThread;
     if (cudaGetDevice(&device) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
-        cudaMemset(d->ws.state, 0, state_words(s) * sizeof(unsigned)) != cudaSuccess)
+        cudaMemsetAsync(d->ws.state, 0, state_words(s) * sizeof(unsigned), own) != cudaSuccess ||
+        cudaStreamSynchronize(own) != cudaSuccess)
         return MOE_ERR_CUDA;
     d->blocks = std::min(sms, kMaxBlocks);
     for (const int64_t T : {int64_t(1), int64_t(MOE_DECODE_MAX_TOKENS)})  // few tokens an expert, and many: both builds
@@ -1427,13 +1431,17 @@ moe_status moe_decode(moe_decoder* d, int64_t T, const void* hidden, int64_t hid
 moe_status moe_decode_status(moe_decoder* d, void* stream) {
     using namespace moe;
     if (!d) return MOE_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
     int v = 0;
-    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess ||
-        cudaMemcpy(&v, d->ws.state, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
+    if (cudaMemcpyAsync(&v, d->ws.state, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
         return MOE_ERR_CUDA;
-    // after a wait that gave up the barrier and the counters start anew as well
+    // After a wait that gave up the barrier and the counters start anew as well. Between this stream's calls, and done
+    // when this returns: the next call may be on another stream.
     const size_t words = (v & kStatusTimeout) ? state_words(d->s) : 1;
-    if (cudaMemset(d->ws.state, 0, words * sizeof(unsigned)) != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaMemsetAsync(d->ws.state, 0, words * sizeof(unsigned), st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return MOE_ERR_CUDA;
     if (v & kStatusTimeout) return MOE_ERR_TIMEOUT;
     if (v & kStatusRouting) return MOE_ERR_ROUTING;
     return MOE_OK;

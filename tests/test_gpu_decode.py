@@ -447,3 +447,45 @@ def test_call_refusals():
         dec.forward_topk(c.x, c.ids.long(), c.probs, w)
     with pytest.raises(ValueError):
         dec.forward_topk(c.x, c.ids[:, :1], c.probs, w)
+
+
+def _busy():
+    """Some milliseconds of work on the current stream."""
+    torch.cuda._sleep(20_000_000)
+
+
+@gpu
+@pytest.mark.parametrize("T", [3, 40])
+def test_created_on_a_side_stream_with_work_pending(T):
+    """The decoder's state is cleared after what its memory's last owner still had queued, and before the first
+    call, whichever stream that is on; so is the status."""
+    c = Layer(T, 512, 160, 9, 4, seed=41)
+    w = c.weights()
+    want = c.decoder(64).forward_topk(c.x, c.ids, c.probs, w)
+    check(want, *c.reference())
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    n = M.moe_decode_size(c.decoder(64).cfg)
+    _busy()                                            # the default stream
+    with torch.cuda.stream(side):
+        old = torch.empty(n, dtype=torch.uint8, device="cuda")
+        at = old.data_ptr()
+        _busy()
+        old.fill_(255)                                 # still to come when its memory is given away
+        del old
+        dec = c.decoder(64)
+        assert dec.workspace.data_ptr() == at
+        got = dec.forward_topk(c.x, c.ids, c.probs, w)
+        assert dec.device_status() == B.MOE_OK
+        bad = c.ids.clone()
+        bad[0, 0] = 9
+        dec.forward_topk(c.x, bad, c.probs, w)
+    torch.cuda.default_stream().synchronize()
+    _busy()
+    assert dec.device_status(side) == B.MOE_ERR_ROUTING and dec.device_status(side) == B.MOE_OK
+    with torch.cuda.stream(other):                     # at once on another stream, the default one busy
+        again = dec.forward_topk(c.x, c.ids, c.probs, w)
+        assert dec.device_status() == B.MOE_OK
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(again, want)
