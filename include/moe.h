@@ -385,7 +385,7 @@ moe_status moe_selftest_timeout(moe_handle* h, void* stream);
  * tokens in all, and its time is the reading of the chosen experts' weights.
  * moe_decode computes the same layer for up to MOE_DECODE_MAX_TOKENS tokens and
  * reads each chosen expert's weights from memory once. No backward, no saved state. */
-enum { MOE_DECODE_MAX_TOKENS = 64 };
+enum { MOE_DECODE_MAX_TOKENS = 64, MOE_DECODE_TABLE_SETS = 64 };
 typedef struct moe_decoder moe_decoder;
 
 /* Bytes of device workspace a decoder for `cfg` needs. The fields of moe_config
@@ -416,8 +416,13 @@ void moe_decode_destroy(moe_decoder* d);
  * Weights as for moe_forward (views or per-expert tables, shared expert and output
  * gate optional as configured); of MXFP8 views the rowwise payload and scales are
  * read, the columnwise ones may be NULL, and moe_prepare_weights is not needed.
- * Per-expert tables are uploaded when their pointers change; such a call cannot be
- * captured into a CUDA graph. Results are deterministic: the sums' order depends
+ * A decoder keeps up to MOE_DECODE_TABLE_SETS sets of per-expert tables for each of the
+ * routed matrices, told apart by their pointers, and uploads a set that it does not have,
+ * in place of the one used longest ago; such a call cannot be captured into a CUDA graph
+ * (MOE_ERR_STATE: run one call with the same tables before capturing). A set that was
+ * used under capture stays until moe_decode_destroy, so that replays run with the tables
+ * that were captured, whatever other calls use; with that many of them, a call with
+ * another set is MOE_ERR_STATE. Results are deterministic: the sums' order depends
  * on the shape and the routing alone. */
 moe_status moe_decode(moe_decoder* d, int64_t T, const void* hidden, int64_t hidden_stride,
                       const int32_t* topk_ids, const float* topk_probs, const moe_weights* w, void* out,

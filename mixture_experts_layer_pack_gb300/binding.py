@@ -20,6 +20,7 @@ MOE_W_BF16, MOE_W_MXFP8 = 0, 1
 MOE_G_FP32, MOE_G_BF16 = 0, 1
 MOE_ACT_FP32, MOE_ACT_BF16 = 0, 1   # activations between the expert GEMMs (include/moe.h, moe_act)
 MOE_DECODE_MAX_TOKENS = 64
+MOE_DECODE_TABLE_SETS = 64           # sets of per-expert tables that a decoder keeps
 MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
 MOE_T_BF16, MOE_T_FP32 = 0, 1       # element types of the norm's and the router's tensors (moe_dtype)
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1

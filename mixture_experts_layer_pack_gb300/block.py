@@ -88,7 +88,8 @@ class MoEBlock:
         return dx, {"norm_weight": dw, "norm_bias": db, "router_weight": drouter}
 
     def decode(self, x, params: BlockParams, residual=None):
-        """(out, s) as forward's, with nothing kept; may be captured into a CUDA graph."""
+        """(out, s) as forward's, with nothing kept; may be captured into a CUDA graph (experts given as per-expert
+        tables: after one call with the same tables)."""
         y, s, _, _, _, (ids, probs, _, _) = self._routed(x, residual, params)
         small = self.decoder is not None and x.shape[0] <= self.decode_tokens
         if not small and self.layer is None:

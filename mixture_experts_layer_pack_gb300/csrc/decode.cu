@@ -39,6 +39,7 @@
 #include <cmath>
 #include <memory>
 #include <new>
+#include <utility>
 
 #include <cuda_fp16.h>
 
@@ -1178,10 +1179,11 @@ moe_status check_decode(const moe_config* c, DecodeShape* s) {
 }
 
 constexpr int kMaxBlocks = 256;
+constexpr int kTableSets = MOE_DECODE_TABLE_SETS;
 
 struct DecodeSpace {
     unsigned* state;      // [0] status, [1] barrier, then the row tiles' counters
-    const void** tables;  // [3][2][E]: gate, up, down: payloads, scales
+    const void** tables;  // [3][kTableSets][2][E]: gate, up, down: payloads, scales
     float* gate;
     void* acts;
     float* part;
@@ -1198,7 +1200,7 @@ size_t carve_decode(const DecodeShape& s, uint8_t* base, DecodeSpace* w) {
     };
     const size_t T = size_t(s.Tmax), chunks = size_t((s.I + 1023) / 1024);
     w->state = reinterpret_cast<unsigned*>(take(state_words(s) * sizeof(unsigned)));
-    w->tables = reinterpret_cast<const void**>(take(6 * size_t(s.E) * sizeof(void*)));
+    w->tables = reinterpret_cast<const void**>(take(6 * size_t(kTableSets) * size_t(s.E) * sizeof(void*)));
     w->gate = reinterpret_cast<float*>(take(T * sizeof(float)));
     w->acts = take(T * size_t(s.k + 1) * chunks * 1024 * sizeof(float));
     w->part = reinterpret_cast<float*>(take(size_t(kMaxBlocks) * 2 * kConsumers * T * 16 * sizeof(float)));
@@ -1215,9 +1217,17 @@ struct moe_decoder {
     moe::DecodeShape s;
     moe::DecodeSpace ws;
     int blocks;
-    // the per-expert pointers last uploaded (gate, up, down: payloads, scales), and a new set being compared
-    std::unique_ptr<const void*[]> host[3], fresh;
-    bool uploaded[3];
+    // The sets of per-expert pointers that lie in the workspace, by matrix (gate, up, down), and the one being compared.
+    // A set has one place as long as it is kept: a captured graph reads its table there with every replay, so a set that
+    // was used under capture stays, and the others make room, the one used longest ago first.
+    struct TableSet {
+        std::unique_ptr<const void*[]> host;  // payloads, scales; null: the place is free
+        uint64_t used = 0;
+        bool captured = false;
+    } sets[3][moe::kTableSets];
+    std::unique_ptr<const void*[]> fresh;
+    int last[3] = {0, 0, 0};  // the set of the call before
+    uint64_t calls = 0;
 };
 
 namespace moe {
@@ -1241,18 +1251,40 @@ moe_status decode_weight(moe_decoder* d, const moe_wview& v, int64_t N, int64_t 
             if (!want[e] || !is16(want[e])) return MOE_ERR_INVALID_ARG;
             if (mx && !(want[E + e] = v.expert_ptrs[2 * E + e])) return MOE_ERR_INVALID_ARG;
         }
-        const void** dev = d->ws.tables + size_t(2 * slot) * size_t(E);
-        if (!d->uploaded[slot] || !std::equal(want, want + n, d->host[slot].get())) {
-            cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-            if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return MOE_ERR_CUDA;
-            if (cap != cudaStreamCaptureStatusNone) return MOE_ERR_STATE;
-            d->uploaded[slot] = false;
-            std::copy(want, want + n, d->host[slot].get());
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return MOE_ERR_CUDA;
+        const bool capturing = cap != cudaStreamCaptureStatusNone;
+        auto& sets = d->sets[slot];
+        auto same = [&](int i) { return sets[i].host && std::equal(want, want + n, sets[i].host.get()); };
+        int at = d->last[slot];
+        if (!same(at))
+            for (at = 0; at < kTableSets && !same(at);) ++at;
+        auto place = [&](int i) { return d->ws.tables + (size_t(slot) * kTableSets + size_t(i)) * 2 * size_t(E); };
+        if (at == kTableSets) {
+            if (capturing) return MOE_ERR_STATE;
+            for (int i = 0; i < kTableSets; ++i) {
+                if (sets[i].captured) continue;
+                if (!sets[i].host) {
+                    at = i;
+                    break;
+                }
+                if (at == kTableSets || sets[i].used < sets[at].used) at = i;
+            }
+            if (at == kTableSets) return MOE_ERR_STATE;
+            auto& set = sets[at];
+            std::unique_ptr<const void*[]> host = std::move(set.host);
+            if (!host) host.reset(new (std::nothrow) const void*[n]);
+            if (!host) return MOE_ERR_STATE;
+            std::copy(want, want + n, host.get());
             // pageable source: staged before the call returns
-            if (cudaMemcpyAsync(dev, d->host[slot].get(), n * sizeof(void*), cudaMemcpyHostToDevice, st) != cudaSuccess)
+            if (cudaMemcpyAsync(place(at), host.get(), n * sizeof(void*), cudaMemcpyHostToDevice, st) != cudaSuccess)
                 return MOE_ERR_CUDA;
-            d->uploaded[slot] = true;
+            set.host = std::move(host);
         }
+        sets[at].used = ++d->calls;
+        sets[at].captured |= capturing;
+        d->last[slot] = at;
+        const void* const* dev = place(at);
         out->table = dev;
         if (mx) out->scale_table = dev + E;
         return MOE_OK;
@@ -1354,10 +1386,8 @@ moe_status moe_decode_create(const moe_config* cfg, void* workspace, size_t work
     std::unique_ptr<moe_decoder> d(new (std::nothrow) moe_decoder());
     if (!d) return MOE_ERR_INVALID_ARG;
     d->s = s;
-    for (auto* p : {&d->host[0], &d->host[1], &d->host[2], &d->fresh}) {
-        p->reset(new (std::nothrow) const void*[2 * size_t(s.E)]());
-        if (!*p) return MOE_ERR_INVALID_ARG;
-    }
+    d->fresh.reset(new (std::nothrow) const void*[2 * size_t(s.E)]());
+    if (!d->fresh) return MOE_ERR_INVALID_ARG;
     carve_decode(s, static_cast<uint8_t*>(workspace), &d->ws);
     int device = 0, sms = 0;
     // A memset returns before it has run, and streams that do not wait for the default one would run a first call before

@@ -9,6 +9,7 @@ activation's exp and quotient), and, as two bf16 terms, 2^-16 |a|; each expert's
 its own dot product), and rounds to bf16 once: 2^-8 |out| covers it.
 Where a clamp bound lies within err_g of g its gradient does not matter: the value is continuous.
 """
+import itertools
 import math
 
 import numpy as np
@@ -489,3 +490,81 @@ def test_created_on_a_side_stream_with_work_pending(T):
         assert dec.device_status() == B.MOE_OK
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(again, want)
+
+
+def table_set(c, order):
+    """Tables whose entry e is expert order[e], the ids that name the same experts through them, and the tables' owner."""
+    E, I = c.E, c.I
+    own = lambda m: [m[e].contiguous() for e in order]  # noqa: E731
+    if c.mx:
+        parts = {n: (own(q), own(q), own(s), own(q)) for n, q, s in
+                 (("gate", c.q1[:, :I], c.s1[:, :I]), ("up", c.q1[:, I:], c.s1[:, I:]), ("down", c.q2, c.s2))}
+        w = M.set_mx_expert_tables(c.weights(), **parts)
+    else:
+        w = M.set_expert_tables(c.weights(), **{n: own(m) for n, m in (("gate", c.b1[:, :I]), ("up", c.b1[:, I:]), ("down", c.b2))})
+        parts = None
+    place = torch.tensor([order.index(e) for e in range(E)], device="cuda")
+    return w, torch.where(c.ids >= 0, place[c.ids.clamp(min=0).long()].int(), c.ids), parts
+
+
+@gpu
+@pytest.mark.parametrize("mx", [False, True])
+def test_a_captured_call_keeps_its_tables(mx):
+    """Calls with other tables, before and after: a replay runs with the tables that were captured; so do two sets in one graph."""
+    c = Layer(4, 288, 96, 5, 2, mx, seed=14)
+    ref = c.reference()
+    dec = c.decoder(8)
+    (wa, ia, ka), (wb, ib, kb) = table_set(c, [3, 1, 4, 0, 2]), table_set(c, [0, 4, 2, 1, 3])
+    a, b = dec.forward_topk(c.x, ia, c.probs, wa), dec.forward_topk(c.x, ib, c.probs, wb)
+    check(a, *ref), check(b, *ref)
+    one, two = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    dec.forward_topk(c.x, ia, c.probs, wa)
+    with torch.cuda.graph(one):
+        got = dec.forward_topk(c.x, ia, c.probs, wa)
+    for _ in range(2):
+        assert torch.equal(dec.forward_topk(c.x, ib, c.probs, wb), b)
+        got.zero_()
+        one.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, a)
+    with torch.cuda.graph(two):
+        ga, gb = dec.forward_topk(c.x, ia, c.probs, wa), dec.forward_topk(c.x, ib, c.probs, wb)
+    two.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(ga, a) and torch.equal(gb, b)
+
+
+@gpu
+def test_more_table_sets_than_a_decoder_keeps():
+    """The set used longest ago makes room; one that a graph reads does not: a set too many is refused."""
+    c = Layer(3, 64, 32, 5, 2, seed=15)
+    ref = c.reference()
+    dec = c.decoder()
+    sets = [table_set(c, list(p)) for p in itertools.islice(itertools.permutations(range(5)), 70)]
+    call = lambda s: dec.forward_topk(c.x, s[1], c.probs, s[0])  # noqa: E731
+    first = call(sets[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call(sets[0])
+    for _ in range(2):
+        for s in sets:
+            check(call(s), *ref)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, first)
+    n = B.MOE_DECODE_TABLE_SETS
+    assert n < 70
+    for s in sets[:n]:
+        call(s)
+    full = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(full):
+        outs = [call(s) for s in sets[:n]]
+    with pytest.raises(M.MoeError) as e:
+        call(sets[n])
+    assert e.value.status == 6  # MOE_ERR_STATE
+    check(call(sets[1]), *ref)
+    full.replay()
+    torch.cuda.synchronize()
+    for o in outs:
+        check(o, *ref)
+    assert dec.device_status() == B.MOE_OK
