@@ -402,7 +402,8 @@ moe_status moe_decode_size(const moe_config* cfg, size_t* bytes);
  * moe_decode_destroy: work queued on any stream that still touches that memory has
  * ended before this call). Its state is cleared when this returns, so that the first
  * call may be on any stream. Calls of one decoder run on one stream, or are ordered by
- * the caller. The current CUDA device at this call is the device of every call. */
+ * the caller. The current CUDA device at this call is the device of every call
+ * (moe_decode with another one current is MOE_ERR_INVALID_ARG). */
 moe_status moe_decode_create(const moe_config* cfg, void* workspace, size_t workspace_bytes, moe_decoder** out);
 void moe_decode_destroy(moe_decoder* d);
 

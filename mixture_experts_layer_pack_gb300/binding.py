@@ -346,6 +346,30 @@ def _raw_stream(stream, device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _on_one_device(first, *rest):
+    """A context with the CUDA device that every tensor given (None: absent) is on as the current one, where kernels go."""
+    import torch
+    index = first.get_device()
+    if index < 0 or any(t is not None and t.get_device() != index for t in rest):
+        raise ValueError("the tensors must be on one CUDA device")
+    return torch.cuda.device(index)
+
+
+def _call_on(current, index, call, args):
+    """call(*args) with device `index` as the current one; current(): the index of the one that is."""
+    if current() == index:
+        return call(*args)
+    import torch
+    with torch.cuda.device(index):
+        return call(*args)
+
+
+def _current_device_of():
+    """A function: the index of the current CUDA device."""
+    import torch
+    return getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _current_stream_of():
     """A function of a device index: its current cudaStream_t."""
     import torch
@@ -375,8 +399,9 @@ def moe_decode_destroy(d):
 
 def moe_decode(d, T, hidden, topk_ids, topk_probs, weights: moe_weights, out, stream=None):
     """The layer for up to 64 tokens; hidden and out are 2-D tensors whose rows may be strided."""
-    _check(load().moe_decode(d, T, hidden.data_ptr(), _ld(hidden), topk_ids.data_ptr(), topk_probs.data_ptr(),
-                             weights, out.data_ptr(), _ld(out), _raw_stream(stream, hidden.device)), "moe_decode")
+    with _on_one_device(hidden, topk_ids, topk_probs, out):
+        _check(load().moe_decode(d, T, hidden.data_ptr(), _ld(hidden), topk_ids.data_ptr(), topk_probs.data_ptr(),
+                                 weights, out.data_ptr(), _ld(out), _raw_stream(stream, hidden.device)), "moe_decode")
 
 
 def moe_decode_status(d, stream=None) -> int:
@@ -385,10 +410,11 @@ def moe_decode_status(d, stream=None) -> int:
 
 def moe_norm_forward(cfg: moe_norm_config, x, weight, y, bias=None, residual=None, sum=None, mean=None, rstd=None,
                      stream=None):
-    _check(load().moe_norm_forward(cfg, x.shape[0], x.data_ptr(), _ld(x), _addr(residual),
-                                   0 if residual is None else _ld(residual), weight.data_ptr(), _addr(bias),
-                                   _addr(sum), 0 if sum is None else _ld(sum), y.data_ptr(), _ld(y),
-                                   _addr(mean), _addr(rstd), _raw_stream(stream, x.device)), "moe_norm_forward")
+    with _on_one_device(x, weight, y, bias, residual, sum, mean, rstd):
+        _check(load().moe_norm_forward(cfg, x.shape[0], x.data_ptr(), _ld(x), _addr(residual),
+                                       0 if residual is None else _ld(residual), weight.data_ptr(), _addr(bias),
+                                       _addr(sum), 0 if sum is None else _ld(sum), y.data_ptr(), _ld(y),
+                                       _addr(mean), _addr(rstd), _raw_stream(stream, x.device)), "moe_norm_forward")
 
 
 def _sized(size, sizes, cfg, T):
@@ -410,12 +436,13 @@ def moe_norm_backward_size(cfg: moe_norm_config, T: int) -> int:
 
 def moe_norm_backward(cfg: moe_norm_config, dy, x, weight, mean, rstd, dx, dsum=None, dweight=None, dbias=None,
                       g_type=MOE_G_FP32, accumulate=False, workspace=None, stream=None):
-    _check(load().moe_norm_backward(cfg, x.shape[0], dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x),
-                                    weight.data_ptr(), _addr(mean), rstd.data_ptr(), _addr(dsum),
-                                    0 if dsum is None else _ld(dsum), dx.data_ptr(), _ld(dx),
-                                    _addr(dweight), _addr(dbias), g_type, 1 if accumulate else 0, _addr(workspace),
-                                    0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                    _raw_stream(stream, x.device)), "moe_norm_backward")
+    with _on_one_device(dy, x, weight, mean, rstd, dx, dsum, dweight, dbias, workspace):
+        _check(load().moe_norm_backward(cfg, x.shape[0], dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x),
+                                        weight.data_ptr(), _addr(mean), rstd.data_ptr(), _addr(dsum),
+                                        0 if dsum is None else _ld(dsum), dx.data_ptr(), _ld(dx),
+                                        _addr(dweight), _addr(dbias), g_type, 1 if accumulate else 0, _addr(workspace),
+                                        0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                        _raw_stream(stream, x.device)), "moe_norm_backward")
 
 
 def moe_router_size(cfg: moe_router_config, T: int) -> int:
@@ -426,17 +453,19 @@ def moe_router_size(cfg: moe_router_config, T: int) -> int:
 
 def moe_router_forward(cfg: moe_router_config, logits, ids, probs, counts=None, losses=None, select_bias=None,
                        workspace=None, stream=None):
-    _check(load().moe_router_forward(cfg, logits.shape[0], logits.data_ptr(), _ld(logits), _addr(select_bias),
-                                     ids.data_ptr(), probs.data_ptr(), _addr(counts), _addr(losses), _addr(workspace),
-                                     0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                     _raw_stream(stream, logits.device)), "moe_router_forward")
+    with _on_one_device(logits, ids, probs, counts, losses, select_bias, workspace):
+        _check(load().moe_router_forward(cfg, logits.shape[0], logits.data_ptr(), _ld(logits), _addr(select_bias),
+                                         ids.data_ptr(), probs.data_ptr(), _addr(counts), _addr(losses), _addr(workspace),
+                                         0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                         _raw_stream(stream, logits.device)), "moe_router_forward")
 
 
 def moe_router_backward(cfg: moe_router_config, logits, ids, dprobs, dlogits, counts=None, loss_grad=1.0,
                         stream=None):
-    _check(load().moe_router_backward(cfg, logits.shape[0], logits.data_ptr(), _ld(logits), ids.data_ptr(),
-                                      dprobs.data_ptr(), _addr(counts), loss_grad, dlogits.data_ptr(),
-                                      _ld(dlogits), _raw_stream(stream, logits.device)), "moe_router_backward")
+    with _on_one_device(logits, ids, dprobs, dlogits, counts):
+        _check(load().moe_router_backward(cfg, logits.shape[0], logits.data_ptr(), _ld(logits), ids.data_ptr(),
+                                          dprobs.data_ptr(), _addr(counts), loss_grad, dlogits.data_ptr(),
+                                          _ld(dlogits), _raw_stream(stream, logits.device)), "moe_router_backward")
 
 
 def moe_launch_count() -> int:
@@ -761,18 +790,22 @@ class MoEDecoder:
                               MOE_ACT_FP32, 0 if shared_expert else 1)
         self.hidden, self.topk = int(hidden), int(topk)
         self.device = torch.device(device)
-        self._torch, self._call, self._stream = torch, load().moe_decode, _current_stream_of()
+        self._torch, self._call, self._stream, self._current = torch, load().moe_decode, _current_stream_of(), _current_device_of()
         self.workspace = torch.empty(moe_decode_size(self.cfg), dtype=torch.uint8, device=self.device)
         with torch.cuda.device(self.device):
             self.handle = moe_decode_create(self.cfg, self.workspace)
+        self.index = self.workspace.get_device()
 
     @_on_stream
     def forward_topk(self, hidden, topk_ids, topk_probs, weights: moe_weights, out=None):
         """out [T,H] of bf16 hidden [T,H] (rows may be strided), int32 ids [T,k] (-1 = empty
         slot) and fp32 probs [T,k], for T up to max_tokens; `stream`: where (the current stream)."""
-        torch = self._torch
+        torch, index = self._torch, self.index
         T, H = shape = hidden.shape
         slots = (T, self.topk)
+        if hidden.get_device() != index or topk_ids.get_device() != index or topk_probs.get_device() != index or \
+                out is not None and out.get_device() != index:
+            raise ValueError("hidden, topk_ids, topk_probs and out must be on the decoder's device")
         if hidden.dtype != torch.bfloat16 or H != self.hidden or hidden.stride(1) != 1:
             raise ValueError("hidden must be [T, H] bf16 with contiguous rows")
         if topk_ids.dtype != torch.int32 or topk_probs.dtype != torch.float32 or topk_ids.shape != slots or \
@@ -782,14 +815,16 @@ class MoEDecoder:
             out = torch.empty(shape, dtype=torch.bfloat16, device=hidden.device)
         elif out.dtype != torch.bfloat16 or out.shape != shape or out.stride(1) != 1:
             raise ValueError("out must be [T, H] bf16 with contiguous rows")
-        status = self._call(self.handle, T, hidden.data_ptr(), _ld(hidden), topk_ids.data_ptr(), topk_probs.data_ptr(),
-                            weights, out.data_ptr(), _ld(out), self._stream(hidden.get_device()))
+        args = (self.handle, T, hidden.data_ptr(), _ld(hidden), topk_ids.data_ptr(), topk_probs.data_ptr(), weights,
+                out.data_ptr(), _ld(out), self._stream(index))
+        status = _call_on(self._current, index, self._call, args)
         if status:
             raise MoeError(status, "moe_decode")
         return out
 
     def device_status(self, stream=None) -> int:
-        return moe_decode_status(self.handle, stream)
+        with self._torch.cuda.device(self.index):
+            return moe_decode_status(self.handle, stream)
 
     def close(self):
         if getattr(self, "handle", None) is not None:
@@ -812,7 +847,7 @@ class MoENorm:
         self._types = {torch.bfloat16: MOE_T_BF16, torch.float32: MOE_T_FP32}
         self._cfgs, self._sizes = {}, {}
         self._empty, self._f32, self._row = torch.empty, torch.float32, torch.Size((self.hidden,))
-        self._torch, self._stream = torch, _current_stream_of()
+        self._torch, self._stream, self._current = torch, _current_stream_of(), _current_device_of()
         self._forward, self._backward = load().moe_norm_forward, load().moe_norm_backward
         _check(load().moe_norm_forward(moe_norm_config(self.hidden, self.eps, self.kind, 0, 0, 0), 0, None, self.hidden,
                                        None, 0, None, None, None, 0, None, self.hidden, None, None, None), "MoENorm")
@@ -840,8 +875,11 @@ class MoENorm:
         `stream`: where (the current stream)."""
         empty = self._empty
         T, H = shape = x.shape
-        xt, wt, dev = x.dtype, weight.dtype, x.device
+        xt, wt, dev, index = x.dtype, weight.dtype, x.device, x.get_device()
         yt = xt if out_dtype is None else out_dtype
+        if index < 0 or weight.get_device() != index or bias is not None and bias.get_device() != index or \
+                residual is not None and residual.get_device() != index:
+            raise ValueError("the tensors must be on one CUDA device")
         if H != self.hidden or x.stride(1) != 1:
             raise ValueError("x must be [T, hidden] rows")
         self._vector(weight, wt)
@@ -861,9 +899,10 @@ class MoENorm:
             self._same(residual, shape, xt, "residual")
             s = empty(shape, dtype=xt, device=dev)
             res_at, res_ld, s_at, s_ld = residual.data_ptr(), _ld(residual), s.data_ptr(), H
-        status = self._forward(cfg, T, x.data_ptr(), x.stride(0) if T > 1 else H, res_at, res_ld, weight.data_ptr(),
-                               None if bias is None else bias.data_ptr(), s_at, s_ld, y.data_ptr(), H, mean_at,
-                               rstd.data_ptr(), self._stream(x.get_device()))
+        args = (cfg, T, x.data_ptr(), x.stride(0) if T > 1 else H, res_at, res_ld, weight.data_ptr(),
+                None if bias is None else bias.data_ptr(), s_at, s_ld, y.data_ptr(), H, mean_at, rstd.data_ptr(),
+                self._stream(index))
+        status = _call_on(self._current, index, self._forward, args)
         if status:
             raise MoeError(status, "moe_norm_forward")
         return y, s, mean, rstd
@@ -875,7 +914,7 @@ class MoENorm:
         fp32 / bf16 buffers, overwritten or (accumulate) added to. `stream`: where (the current stream)."""
         torch, empty = self._torch, self._empty
         T, H = shape = s.shape
-        st, yt, wt, dev, f32 = s.dtype, dy.dtype, weight.dtype, s.device, self._f32
+        st, yt, wt, dev, f32, index = s.dtype, dy.dtype, weight.dtype, s.device, self._f32, s.get_device()
         if H != self.hidden or s.stride(1) != 1:
             raise ValueError("s must be [T, hidden] rows")
         if dy.shape != shape or dy.stride(1) != 1:
@@ -888,6 +927,10 @@ class MoENorm:
             raise ValueError("mean and rstd must be the forward's [T] fp32")
         if accumulate and (dweight is None or (bias and dbias is None)):
             raise ValueError("accumulate adds to given buffers")
+        if index < 0 or dy.get_device() != index or weight.get_device() != index or rstd.get_device() != index or \
+                mean is not None and mean.get_device() != index or dsum is not None and dsum.get_device() != index or \
+                dweight is not None and dweight.get_device() != index or dbias is not None and dbias.get_device() != index:
+            raise ValueError("the tensors must be on one CUDA device")
         if dsum is not None:
             self._same(dsum, shape, st, "dsum")
         cfg = self._cfgs.get((st, yt, wt)) or self._cfg(st, yt, wt)
@@ -911,11 +954,12 @@ class MoENorm:
         size = _sized(moe_norm_backward_size, self._sizes, cfg, T)
         workspace = empty(size, dtype=torch.uint8, device=dev)
         many = T > 1  # a single row has no stride of its own
-        status = self._backward(cfg, T, dy.data_ptr(), dy.stride(0) if many else H, s.data_ptr(), s.stride(0) if many else H,
-                                weight.data_ptr(), None if mean is None else mean.data_ptr(), rstd.data_ptr(), _addr(dsum),
-                                0 if dsum is None else _ld(dsum), ds.data_ptr(), H, dweight.data_ptr(),
-                                None if dbias is None else dbias.data_ptr(), MOE_G_FP32 if gt is f32 else MOE_G_BF16,
-                                1 if accumulate else 0, workspace.data_ptr(), size, self._stream(s.get_device()))
+        args = (cfg, T, dy.data_ptr(), dy.stride(0) if many else H, s.data_ptr(), s.stride(0) if many else H,
+                weight.data_ptr(), None if mean is None else mean.data_ptr(), rstd.data_ptr(), _addr(dsum),
+                0 if dsum is None else _ld(dsum), ds.data_ptr(), H, dweight.data_ptr(),
+                None if dbias is None else dbias.data_ptr(), MOE_G_FP32 if gt is f32 else MOE_G_BF16,
+                1 if accumulate else 0, workspace.data_ptr(), size, self._stream(index))
+        status = _call_on(self._current, index, self._backward, args)
         if status:
             raise MoeError(status, "moe_norm_backward")
         return ds, dweight, dbias
@@ -934,7 +978,7 @@ class MoERouter:
         self._cfgs = {torch.bfloat16: moe_router_config(*args, MOE_T_BF16),
                       torch.float32: moe_router_config(*args, MOE_T_FP32)}
         self.losses_wanted = aux_coeff != 0 or z_coeff != 0
-        self._torch, self._stream = torch, _current_stream_of()
+        self._torch, self._stream, self._current = torch, _current_stream_of(), _current_device_of()
         self._forward, self._backward = load().moe_router_forward, load().moe_router_backward
         moe_router_size(self._cfgs[torch.float32], 0)      # the library's check of the configuration
 
@@ -954,7 +998,9 @@ class MoERouter:
         T, E = logits.shape
         if cfg is None or E != self.E or logits.stride(1) != 1:
             raise ValueError("logits must be [T, E] rows, bf16 or fp32")
-        dev = logits.device
+        dev, index = logits.device, logits.get_device()
+        if index < 0 or select_bias is not None and select_bias.get_device() != index:
+            raise ValueError("the tensors must be on one CUDA device")
         if select_bias is not None and (select_bias.shape != (E,) or select_bias.dtype != f32 or select_bias.stride(0) != 1):
             raise ValueError("select_bias must be [E] fp32")
         slots = (T, self.k)
@@ -964,10 +1010,11 @@ class MoERouter:
         losses = empty(2, dtype=f32, device=dev) if self.losses_wanted else None
         size = _sized(moe_router_size, self._sizes, cfg, T)
         workspace = empty(size, dtype=torch.uint8, device=dev)
-        status = self._forward(cfg, T, logits.data_ptr(), logits.stride(0) if T > 1 else E,
-                               None if select_bias is None else select_bias.data_ptr(), ids.data_ptr(),
-                               probs.data_ptr(), counts.data_ptr(), None if losses is None else losses.data_ptr(),
-                               workspace.data_ptr(), size, self._stream(logits.get_device()))
+        args = (cfg, T, logits.data_ptr(), logits.stride(0) if T > 1 else E,
+                None if select_bias is None else select_bias.data_ptr(), ids.data_ptr(), probs.data_ptr(),
+                counts.data_ptr(), None if losses is None else losses.data_ptr(), workspace.data_ptr(), size,
+                self._stream(index))
+        status = _call_on(self._current, index, self._forward, args)
         if status:
             raise MoeError(status, "moe_router_forward")
         return ids, probs, counts, losses
@@ -985,10 +1032,14 @@ class MoERouter:
             raise ValueError("ids and dprobs must be contiguous [T, k] int32 and fp32")
         if counts is not None and (counts.shape != (self.E,) or counts.dtype != torch.int32 or counts.stride(0) != 1):
             raise ValueError("counts must be [E] int32")
+        index = logits.get_device()
+        if index < 0 or ids.get_device() != index or dprobs.get_device() != index or \
+                counts is not None and counts.get_device() != index:
+            raise ValueError("the tensors must be on one CUDA device")
         dlogits = torch.empty(shape, dtype=logits.dtype, device=logits.device)
-        status = self._backward(cfg, shape[0], logits.data_ptr(), _ld(logits), ids.data_ptr(), dprobs.data_ptr(),
-                                _addr(counts), float(loss_grad), dlogits.data_ptr(), self.E,
-                                self._stream(logits.get_device()))
+        args = (cfg, shape[0], logits.data_ptr(), _ld(logits), ids.data_ptr(), dprobs.data_ptr(), _addr(counts),
+                float(loss_grad), dlogits.data_ptr(), self.E, self._stream(index))
+        status = _call_on(self._current, index, self._backward, args)
         if status:
             raise MoeError(status, "moe_router_backward")
         return dlogits

@@ -1216,7 +1216,7 @@ bool is16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 struct moe_decoder {
     moe::DecodeShape s;
     moe::DecodeSpace ws;
-    int blocks;
+    int device, blocks;
     // The sets of per-expert pointers that lie in the workspace, by matrix (gate, up, down), and the one being compared.
     // A set has one place as long as it is kept: a captured graph reads its table there with every replay, so a set that
     // was used under capture stays, and the others make room, the one used longest ago first.
@@ -1389,12 +1389,12 @@ moe_status moe_decode_create(const moe_config* cfg, void* workspace, size_t work
     d->fresh.reset(new (std::nothrow) const void*[2 * size_t(s.E)]());
     if (!d->fresh) return MOE_ERR_INVALID_ARG;
     carve_decode(s, static_cast<uint8_t*>(workspace), &d->ws);
-    int device = 0, sms = 0;
+    int sms = 0;
     // A memset returns before it has run, and streams that do not wait for the default one would run a first call before
     // or during it: so it is waited for here.
     const cudaStream_t own = cudaStreamPerThread;
-    if (cudaGetDevice(&device) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+    if (cudaGetDevice(&d->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d->device) != cudaSuccess ||
         cudaMemsetAsync(d->ws.state, 0, state_words(s) * sizeof(unsigned), own) != cudaSuccess ||
         cudaStreamSynchronize(own) != cudaSuccess)
         return MOE_ERR_CUDA;
@@ -1423,6 +1423,9 @@ moe_status moe_decode(moe_decoder* d, int64_t T, const void* hidden, int64_t hid
         (reinterpret_cast<uintptr_t>(out) & 1))
         return MOE_ERR_INVALID_ARG;
     if (w->shared_output_gate && (!s.shared || !is16(w->shared_output_gate))) return MOE_ERR_INVALID_ARG;
+    int device = 0;  // a launch goes to the current device, and the workspace and the number of blocks are of the decoder's
+    if (cudaGetDevice(&device) != cudaSuccess) return MOE_ERR_CUDA;
+    if (device != d->device) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     DecodeArgs a{};
     a.T = int(T);

@@ -568,3 +568,22 @@ def test_more_table_sets_than_a_decoder_keeps():
     for o in outs:
         check(o, *ref)
     assert dec.device_status() == B.MOE_OK
+
+
+@gpu
+def test_tensors_on_two_devices_are_refused():
+    """Tensors in host memory come back as errors before anything is launched, in any place."""
+    c = Layer(3, 64, 32, 4, 2, seed=51)
+    dec, w = c.decoder(), c.weights()
+    out = torch.empty_like(c.x)
+    before = M.moe_launch_count()
+    for i in range(4):
+        args = [c.x, c.ids, c.probs, w, out]
+        args[i if i < 3 else 4] = args[i if i < 3 else 4].cpu()
+        with pytest.raises(ValueError, match="device"):
+            dec.forward_topk(*args)
+        with pytest.raises(ValueError, match="device"):
+            M.moe_decode(dec.handle, 3, *args)
+    assert M.moe_launch_count() == before
+    M.moe_decode(dec.handle, 3, c.x, c.ids, c.probs, w, out)
+    check(out, *c.reference())

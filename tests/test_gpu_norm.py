@@ -297,3 +297,42 @@ def test_refusals():
     for kw in (dict(T=-1), dict(dy=None), dict(x=None), dict(w=None), dict(mean=None), dict(rstd=None), dict(dx=None),
                dict(gt=2), dict(acc=2), dict(ws=None), dict(ws=264), dict(n=16), dict(ld=8), dict(dw=258), dict(mean=2)):
         assert g(c(), **kw) == 1, kw
+
+
+def test_tensors_elsewhere_are_refused():
+    """Tensors in host memory come back as errors before anything is launched, in any place."""
+    norm = M.MoENorm(16)
+    x, w, v = torch.zeros(2, 16), torch.zeros(16), torch.zeros(2)
+    with pytest.raises(ValueError, match="device"):
+        norm.forward(x, w)
+    with pytest.raises(ValueError, match="device"):
+        norm.backward(x, x, w, v, v)
+    cfg = norm._cfg(F32, F32, F32)
+    with pytest.raises(ValueError, match="device"):
+        M.moe_norm_forward(cfg, x, w, x)
+    with pytest.raises(ValueError, match="device"):
+        M.moe_norm_backward(cfg, x, x, w, v, v, x)
+
+
+@gpu
+def test_tensors_on_two_devices_are_refused():
+    norm = M.MoENorm(16)
+    x, w, v, g = torch.zeros(2, 16), torch.zeros(16), torch.zeros(2), torch.zeros(16)
+    X, W, V, G = (t.cuda() for t in (x, w, v, g))
+    before = M.moe_launch_count()
+    for args in ((x, W), (X, w), (X, W, w), (X, W, None, x)):
+        with pytest.raises(ValueError, match="device"):
+            norm.forward(*args)
+    for args in ((x, X, W, V, V), (X, x, W, V, V), (X, X, w, V, V), (X, X, W, v, V), (X, X, W, V, v), (X, X, W, V, V, x),
+                 (X, X, W, V, V, None, False, g), (X, X, W, V, V, None, True, G, g)):
+        with pytest.raises(ValueError, match="device"):
+            norm.backward(*args)
+    cfg = norm._cfg(F32, F32, F32)
+    for args in ((X, w, X), (X, W, x), (X, W, X, w), (X, W, X, None, x, X), (X, W, X, None, X, x), (X, W, X, None, None, None, v)):
+        with pytest.raises(ValueError, match="device"):
+            M.moe_norm_forward(cfg, *args)
+    with pytest.raises(ValueError, match="device"):
+        M.moe_norm_backward(cfg, X, X, W, V, V, X, None, G, None, workspace=torch.zeros(1 << 16, dtype=torch.uint8))
+    assert M.moe_launch_count() == before
+    norm.forward(X, W, stream=torch.cuda.Stream())
+    assert M.moe_launch_count() == before + 1

@@ -277,3 +277,36 @@ def test_refusals():
     for kw in (dict(l=None), dict(ids=None), dict(dp=None), dict(dl=None), dict(counts=None), dict(g=math.nan), dict(ld=3),
                dict(dld=15), dict(dl=257)):
         assert b(**kw) == 1, kw
+
+
+def test_tensors_elsewhere_are_refused():
+    """Tensors in host memory come back as errors before anything is launched."""
+    router = M.MoERouter(8, 2)
+    l, ids, d = torch.zeros(3, 8), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2)
+    with pytest.raises(ValueError, match="device"):
+        router.forward(l)
+    with pytest.raises(ValueError, match="device"):
+        router.backward(l, ids, d)
+    with pytest.raises(ValueError, match="device"):
+        M.moe_router_forward(router._cfgs[F32], l, ids, d)
+    with pytest.raises(ValueError, match="device"):
+        M.moe_router_backward(router._cfgs[F32], l, ids, d, l)
+
+
+@gpu
+def test_tensors_on_two_devices_are_refused():
+    router = M.MoERouter(8, 2, aux_coeff=0.1)
+    l, ids, d, n, b = torch.zeros(3, 8), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2), torch.zeros(8, dtype=torch.int32), torch.zeros(8)
+    L, I, D, N = (t.cuda() for t in (l, ids, d, n))
+    before = M.moe_launch_count()
+    for args in ((l, b.cuda()), (L, b)):
+        with pytest.raises(ValueError, match="device"):
+            router.forward(*args)
+    for args in ((l, I, D, N), (L, ids, D, N), (L, I, d, N), (L, I, D, n)):
+        with pytest.raises(ValueError, match="device"):
+            router.backward(*args)
+    cfg = router._cfgs[F32]
+    for args in ((L, ids, D), (L, I, d), (L, I, D, n), (L, I, D, N, d)):
+        with pytest.raises(ValueError, match="device"):
+            M.moe_router_forward(cfg, *args)
+    assert M.moe_launch_count() == before
