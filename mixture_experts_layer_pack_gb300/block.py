@@ -71,15 +71,17 @@ class MoEBlock:
         return out, s, losses
 
     def backward(self, dout, main_grads: B.moe_main_grads, ds=None, loss_grad=1.0):
-        """(dx, grads) for the gradients dout of out and ds of s (None: zero) and loss_grad of the losses' sum.
+        """(dx, grads) for the gradients dout of out (bf16, any strides) and ds of s (None: zero) and loss_grad of the losses' sum.
         dx is that of x and of residual alike. grads: norm_weight, norm_bias (None without one) and
         router_weight; the experts' are added to main_grads."""
         import torch
         if self._kept is None:
             raise ValueError("backward without a forward before it")
         p, y, s, mean, rstd, logits, ids, counts = self._kept
+        if dout.shape != y.shape or dout.dtype != y.dtype or dout.device != y.device:
+            raise ValueError("dout must be [T, H] bf16 on the block's device")
         self._kept = None
-        dy, dprobs = self.layer.backward(dout, main_grads)
+        dy, dprobs = self.layer.backward(dout.contiguous(), main_grads)  # the layer takes compact rows
         dlogits = self.router.backward(logits, ids, dprobs, counts=counts, loss_grad=loss_grad)
         drouter = dlogits.t() @ y.to(dlogits.dtype)
         # one rounding of the sum of both paths to y

@@ -174,3 +174,31 @@ def test_two_blocks_in_a_graph():
 def test_refuses_an_empty_block():
     with pytest.raises(ValueError):
         M.MoEBlock(0, 256, 8, 2, 128, decode_tokens=0)
+
+
+@gpu
+def test_gradients_of_any_layout():
+    """dout with rows of a wider buffer, transposed, or one row broadcast: as the same values in compact rows. Other
+    shapes, types and places are refused, and the step that waits is kept."""
+    T, H, I, E, k = 33, 256, 128, 8, 2
+    t, p = params(H, I, E, torch.float32, False, seed=3)
+    block = M.MoEBlock(T, H, E, k, I)
+    x = torch.randn(T, H, device="cuda", generator=torch.Generator(device="cuda").manual_seed(4)).bfloat16()
+    row = torch.randn(1, H, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5)).bfloat16()
+
+    def step(dout):
+        block.forward(x, p)
+        for bad in (dout.float(), dout[:-1], dout[:, :-8], dout.cpu()):
+            with pytest.raises(ValueError):
+                block.backward(bad, None)
+        mg = {n: torch.zeros(*t[n].shape, device="cuda") for n in ("shared1", "shared2", "fc1", "fc2")}
+        dx, gr = block.backward(dout, M.main_grads_from_combined(mg["shared1"], mg["shared2"], mg["fc1"], mg["fc2"]))
+        return [dx, gr["norm_weight"], gr["router_weight"], *mg.values()]
+
+    full = torch.randn(T, H, device="cuda", generator=torch.Generator(device="cuda").manual_seed(6)).bfloat16()
+    wide = torch.zeros(T, H + 8, device="cuda").bfloat16()
+    wide[:, :H] = full
+    want = step(full)
+    for view in (wide[:, :H], full.t().contiguous().t()):
+        assert all(torch.equal(a, b) for a, b in zip(step(view), want))
+    assert all(torch.equal(a, b) for a, b in zip(step(row.expand(T, H)), step(row.repeat(T, 1))))
