@@ -488,7 +488,8 @@ moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* 
  * order is that of score + select_bias, which the probs do not see. A logit of
  * -inf closes its expert to the token: a row with fewer than topk open experts has
  * -1 and prob 0 in its last slots. probs = scale * score, with `normalise` divided by the
- * sum of the row's chosen scores. A NaN logit is never chosen and makes its row's
+ * sum of the row's chosen scores, however small that is (sigmoid scores of logits below
+ * -700 count as 0). A NaN logit is never chosen and makes its row's
  * probs NaN. */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 typedef struct {

@@ -118,6 +118,22 @@ __device__ __forceinline__ RowSums row_exp(const float (&l)[N], float (&q)[N]) {
     return r;
 }
 
+// The share of a lane's chosen score in the sum of all of them (0 for a lane without one); `l`: its logit. A bias may choose
+// scores whose sum has no reciprocal, or that are too small for their ratio to be right: such rows take the exponents'
+// differences from the largest chosen logit, whose sum is 1 at least. (A sigmoid that small is exp(l).) Past kNoScore a
+// sigmoid counts as 0, as it does with 64 bits, and there is nothing to divide by.
+constexpr float kNoScore = -700.0f;
+__device__ __forceinline__ float share_of(float score, float l, bool chosen, bool sigmoid) {
+    float total = warp_sum(score);
+    if (total < 1e-30f) {  // the same in every lane; a NaN passes
+        const float top = warp_max(chosen ? l : -INFINITY);
+        score = !chosen || (sigmoid && top < kNoScore) ? 0.0f : expf(l - top);
+        total = warp_sum(score);
+        if (total == 0.0f) return 0.0f;
+    }
+    return score * reciprocal(total);
+}
+
 // losses from the sums over the experts (counts times score sums) and over the tokens (log-sum-exp squared)
 __device__ __forceinline__ void put_losses(const RouterArgs& a, float total, float z) {
     const float T = float(a.T);
@@ -265,10 +281,7 @@ __global__ void __launch_bounds__(32 * forward_warps(N)) router_forward_kernel(R
         float my_l = value_of(my_key);
         if (a.bias && my_id >= 0) my_l = load_logit(a, t, my_id);
         float my_p = my_id < 0 ? 0.0f : a.sigmoid ? sigmoid(my_l) : expf(my_l - r.m) * r.rz;
-        if (a.normalise) {
-            const float total = warp_sum(my_p);
-            if (total != 0.0f) my_p = my_p * reciprocal(total);
-        }
+        if (a.normalise) my_p = share_of(my_p, my_l, my_id >= 0, a.sigmoid);
         if (lane < a.k) {
             a.ids[t * a.k + lane] = my_id;
             a.probs[t * a.k + lane] = bad ? NAN : my_p * a.scale;
@@ -376,7 +389,7 @@ __global__ void __launch_bounds__(32 * kFinishWarps) router_finish_kernel(Router
 
 template <int N>
 __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(RouterArgs a) {
-    extern __shared__ float smem[];  // per warp: [E] gradients of the chosen scores
+    extern __shared__ float smem[];  // per warp: [E] gradients of the chosen scores, or with shares of the chosen logits
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -398,11 +411,10 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(Rout
     if (!a.sigmoid || zl) r = row_exp<N>(l, q);
     __syncwarp();
     const float c = id < 0 ? 0.0f : a.sigmoid ? sigmoid(my_l) : expf(my_l - r.m) * r.rz;
-    if (a.normalise) {
-        const float total = warp_sum(c);
-        const float rt = total == 0.0f ? 1.0f : reciprocal(total);
-        const float mean = warp_sum(d * (c * rt));
-        d = id >= 0 ? (d - mean) * rt : 0.0f;
+    if (a.normalise) {  // of shares: softmax share (d - mean), sigmoid the same times 1 - score; nothing to divide by
+        const float share = share_of(c, my_l, id >= 0, a.sigmoid);
+        const float mean = warp_sum(d * share);
+        d = share * (d - mean) * (a.sigmoid ? 1.0f - c : 1.0f);
     }
     if (id >= 0) s_d[id] = d;
     __syncwarp();
@@ -429,26 +441,37 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(Rout
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             if (lane + 32 * j >= a.E) continue;
-            const float v = s_d[lane + 32 * j] + (aux ? (g[j] - dot) * rp : 0.0f);
-            g[j] = v * p[j] * (1.0f - p[j]);
+            const float own = s_d[lane + 32 * j];
+            const float v = (a.normalise ? 0.0f : own) + (aux ? (g[j] - dot) * rp : 0.0f);
+            g[j] = fmaf(v, p[j] * (1.0f - p[j]), a.normalise ? own : 0.0f);
             if (zl) g[j] = fmaf(w_z, q[j], g[j]);
         }
     } else {
-        float dot = 0.0f;
+        auto softmax = [&](auto shares) {  // s_d: gradients of the chosen logits, not of their scores
+            const bool scores = !shares || aux;
+            float dot = 0.0f;
+            if (scores) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            g[j] = 0.0f;
-            if (lane + 32 * j >= a.E) continue;
-            g[j] = s_d[lane + 32 * j];
-            if (aux) g[j] = fmaf(w_aux, float(a.counts_in[lane + 32 * j]), g[j]);
-            dot = fmaf(g[j], q[j], dot);
-        }
-        dot = warp_sum(dot) * r.rz;
+                for (int j = 0; j < N; ++j) {
+                    g[j] = 0.0f;
+                    if (lane + 32 * j >= a.E) continue;
+                    if (!shares) g[j] = s_d[lane + 32 * j];
+                    if (aux) g[j] = fmaf(w_aux, float(a.counts_in[lane + 32 * j]), g[j]);
+                    dot = fmaf(g[j], q[j], dot);
+                }
+                dot = warp_sum(dot) * r.rz;
+            }
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            g[j] = q[j] * r.rz * (g[j] - dot);
-            if (zl) g[j] = fmaf(w_z, q[j], g[j]);
-        }
+            for (int j = 0; j < N; ++j) {
+                float v = shares && lane + 32 * j < a.E ? s_d[lane + 32 * j] : 0.0f;
+                if (scores) v = fmaf(q[j] * r.rz, g[j] - dot, v);
+                g[j] = zl ? fmaf(w_z, q[j], v) : v;
+            }
+        };
+        if (a.normalise)
+            softmax(std::true_type{});
+        else
+            softmax(std::false_type{});
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) {

@@ -310,3 +310,38 @@ def test_tensors_on_two_devices_are_refused():
         with pytest.raises(ValueError, match="device"):
             M.moe_router_forward(cfg, *args)
     assert M.moe_launch_count() == before
+
+
+def by_definition(l, router, c, bias=None, seed=0):
+    """A router's forward and backward against the definition, with the tolerances above and 2^-146 for results
+    below the normal range. Returns (ids, probs)."""
+    d = torch.randn(l.shape[0], c["k"], generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+    ref = reference(l.double(), c, bias=None if bias is None else bias.double(), dprobs=d.double(), loss_grad=1.0)
+    ids, probs, counts, losses = router.forward(l, select_bias=bias)
+    assert torch.equal(ids, ref["ids"]) and torch.equal(counts, ref["counts"])
+    lf = l.double().masked_fill(l == -math.inf, math.nan)
+    spread = float((lf.nan_to_num(-1e4).amax(-1) - lf.nan_to_num(1e4).amin(-1)).max())
+    r, tiny = (c["E"] / 32 + 64 + spread) * U, 2.0 ** -146
+    assert ((probs.double() - ref["probs"]).abs() <= 3 * r * ref["probs"] + tiny).all(), (probs, ref["probs"])
+    dl = router.backward(l, ids, d, counts=counts)
+    tol = 4 * r * ref["mag"] + (2.0 ** -8 * ref["dlogits"].abs() if l.dtype == BF16 else 0) + tiny
+    assert ((dl.double() - ref["dlogits"]).abs() <= tol).all()
+    if c["aux"] or c["z"]:
+        T, z = l.shape[0], c["z"] * ((ref["lse"].abs() + 1) ** 2).mean()
+        assert (losses[0].double() - ref["losses"][0]).abs() <= (3 * r + (T + c["E"]) * U) * ref["losses"][0].abs() + 1e-30
+        assert (losses[1].double() - ref["losses"][1]).abs() <= (3 * r + (T + c["E"]) * U) * z
+    return ids, probs
+
+
+@gpu
+@pytest.mark.parametrize("low", [-80.0, -88.5, -92.0, -100.0, -250.0])
+@pytest.mark.parametrize("k", [1, 2, 3])
+def test_normalised_probs_of_scores_far_below_the_largest(k, low):
+    """A bias that chooses experts whose softmax scores are tiny beside the row's largest: their share of each other is
+    what counts, in the probs and in the gradient."""
+    l = torch.tensor([[0.0, low, low - 1.5, 3.0, low - 0.25, -2.0], [low, 0.5, low + 1, 0.0, low - 4, low]], device="cuda")
+    bias = torch.tensor([[-10.0, 5.0, 6.0, -10.0, 7.0, -10.0]], device="cuda")[0].contiguous()
+    c = dict(E=6, k=k, score="softmax", normalise=True, scale=1.5, aux=0.0, z=0.0)
+    router = M.MoERouter(6, k, normalise=True, scale=1.5)
+    ids, probs = by_definition(l[:1].contiguous(), router, c, bias)
+    assert ids[0].tolist() == [4, 2, 1][:k] and abs(float(probs.sum()) - 1.5) < 1e-5
