@@ -54,8 +54,14 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 
 // quotients by the hardware reciprocal: 1 ulp, a quarter of a rounded division's time
 __device__ __forceinline__ float reciprocal(float v) { return __fdividef(1.0f, v); }
-// 0 where exp(-z) overflows (the reciprocal's range ends at 2^126)
-__device__ __forceinline__ float sigmoid(float z) { return z < -87.0f ? 0.0f : reciprocal(1.0f + expf(-z)); }
+// the smaller of sigmoid(z) and 1 - sigmoid(z), exp(-|z|) / (1 + exp(-|z|)): nothing overflows, and both are right to the
+// last bits at either end, down to the smallest that fp32 holds
+__device__ __forceinline__ float sigmoid_tail(float z) {
+    const float e = expf(-fabsf(z));
+    return e * reciprocal(1.0f + e);
+}
+__device__ __forceinline__ float sigmoid_of(float z, float tail) { return z < 0.0f ? tail : 1.0f - tail; }
+__device__ __forceinline__ float sigmoid(float z) { return sigmoid_of(z, sigmoid_tail(z)); }
 
 struct RouterArgs {
     const void* logits;
@@ -410,11 +416,12 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(Rout
     RowSums r{0.0f, 0.0f, 0.0f};
     if (!a.sigmoid || zl) r = row_exp<N>(l, q);
     __syncwarp();
-    const float c = id < 0 ? 0.0f : a.sigmoid ? sigmoid(my_l) : expf(my_l - r.m) * r.rz;
+    const float tail = a.sigmoid ? sigmoid_tail(my_l) : 0.0f;
+    const float c = id < 0 ? 0.0f : a.sigmoid ? sigmoid_of(my_l, tail) : expf(my_l - r.m) * r.rz;
     if (a.normalise) {  // of shares: softmax share (d - mean), sigmoid the same times 1 - score; nothing to divide by
         const float share = share_of(c, my_l, id >= 0, a.sigmoid);
         const float mean = warp_sum(d * share);
-        d = share * (d - mean) * (a.sigmoid ? 1.0f - c : 1.0f);
+        d = share * (d - mean) * (a.sigmoid ? sigmoid_of(-my_l, tail) : 1.0f);
     }
     if (id >= 0) s_d[id] = d;
     __syncwarp();
@@ -422,17 +429,18 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(Rout
     const float w_z = zl ? a.loss_grad * 2.0f * a.z / float(a.T) * r.lse * r.rz : 0.0f;  // times exp(l - m)
     float g[N];
     if (a.sigmoid) {
-        float p[N], rp = 0.0f, dot = 0.0f;
+        float tails[N], rp = 0.0f, dot = 0.0f;
 #pragma unroll
-        for (int j = 0; j < N; ++j) p[j] = sigmoid(l[j]);
+        for (int j = 0; j < N; ++j) tails[j] = sigmoid_tail(l[j]);
         if (aux) {
             // with P = p / sum(p): gradient (w - sum(w P)) / sum(p) of the balance loss at each score
             float total = 0.0f, wp = 0.0f;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 g[j] = lane + 32 * j < a.E ? w_aux * float(a.counts_in[lane + 32 * j]) : 0.0f;
-                total += p[j];
-                wp = fmaf(g[j], p[j], wp);
+                const float p = sigmoid_of(l[j], tails[j]);
+                total += p;
+                wp = fmaf(g[j], p, wp);
             }
             total = warp_sum(total);
             rp = total == 0.0f ? 1.0f : reciprocal(total);
@@ -443,7 +451,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(Rout
             if (lane + 32 * j >= a.E) continue;
             const float own = s_d[lane + 32 * j];
             const float v = (a.normalise ? 0.0f : own) + (aux ? (g[j] - dot) * rp : 0.0f);
-            g[j] = fmaf(v, p[j] * (1.0f - p[j]), a.normalise ? own : 0.0f);
+            g[j] = fmaf(v, tails[j] * (1.0f - tails[j]), a.normalise ? own : 0.0f);
             if (zl) g[j] = fmaf(w_z, q[j], g[j]);
         }
     } else {

@@ -345,3 +345,34 @@ def test_normalised_probs_of_scores_far_below_the_largest(k, low):
     router = M.MoERouter(6, k, normalise=True, scale=1.5)
     ids, probs = by_definition(l[:1].contiguous(), router, c, bias)
     assert ids[0].tolist() == [4, 2, 1][:k] and abs(float(probs.sum()) - 1.5) < 1e-5
+
+
+@gpu
+@pytest.mark.parametrize("normalise", [False, True])
+@pytest.mark.parametrize("low", [-60.0, -86.9, -87.5, -95.0, -120.0, -600.0])
+def test_sigmoid_scores_of_low_logits(low, normalise):
+    """Sigmoid scores down to fp32's smallest and below: close to the definition, and normalised by each other."""
+    l = torch.tensor([[low, low - 1.0, low - 0.5, low - 3.0], [low, 2.0, low, -math.inf], [low, low, -math.inf, low - 2.0]], device="cuda")
+    c = dict(E=4, k=2, score="sigmoid", normalise=normalise, scale=1.0, aux=0.0, z=0.0)
+    by_definition(l, M.MoERouter(4, 2, score=SCORES["sigmoid"], normalise=normalise), c)
+
+
+@gpu
+@pytest.mark.parametrize("normalise", [False, True])
+def test_sigmoid_gradients_of_high_logits(normalise):
+    """1 - score where the score is 1 in fp32: gradients relative to their own size, not to the scores'. The last two of
+    the three chosen take opposite parts of a normalised prob, so that no sum cancels: (d_i - mean) is -1, 1 and 0."""
+    l = torch.tensor([[h, h, h, -math.inf] for h in (5.0, 12.0, 17.0, 30.0, 60.0, 85.0)], device="cuda")
+    d = torch.tensor([[-1.0, 1.0, 0.0]] * 6, device="cuda")
+    c = dict(E=4, k=3, score="sigmoid", normalise=normalise, scale=1.0, aux=0.0, z=0.0)
+    ref = reference(l.double(), c, dprobs=d.double())
+    router = M.MoERouter(4, 3, score=SCORES["sigmoid"], normalise=normalise)
+    ids, _, counts, _ = router.forward(l)
+    assert torch.equal(ids, ref["ids"])
+    dl = router.backward(l, ids, d, counts=counts)
+    want = torch.exp(-l[:, :1].double()) / (1 + torch.exp(-l[:, :1].double())) ** 2 * torch.tensor([-1.0, 1.0, 0.0], device="cuda").double()
+    if normalise:  # share 1/3, times 1 - score alone
+        want = torch.exp(-l[:, :1].double()) / (1 + torch.exp(-l[:, :1].double())) / 3 * torch.tensor([-1.0, 1.0, 0.0], device="cuda").double()
+    r = (4 / 32 + 64) * U
+    assert ((dl[:, :3].double() - want).abs() <= 4 * r * want.abs() + 4 * r * want.abs().amax(1, keepdim=True)).all()
+    assert not dl[:, 3].any()
