@@ -489,8 +489,9 @@ moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* 
  * -inf closes its expert to the token: a row with fewer than topk open experts has
  * -1 and prob 0 in its last slots. probs = scale * score, with `normalise` divided by the
  * sum of the row's chosen scores, however small that is (sigmoid scores of logits below
- * -700 count as 0). A NaN logit is never chosen and makes its row's
- * probs NaN. */
+ * -700 count as 0). A NaN logit is never chosen and makes its row's probs NaN; so does
+ * a logit of +inf with softmax scores. Softmax rows of either kind have no scores to add a
+ * select_bias to: their order is that of the logits. */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 typedef struct {
     int64_t num_experts;  /* E, 1..1024 */

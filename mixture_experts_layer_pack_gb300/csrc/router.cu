@@ -265,9 +265,14 @@ __global__ void __launch_bounds__(32 * forward_warps(N)) router_forward_kernel(R
         }
         uint32_t key[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            key[j] = order_key(l[j]);
-            if (a.bias && key[j]) key[j] = order_key((a.sigmoid ? p[j] : p[j] * r.rz) + a.bias[lane + 32 * j]);
+        for (int j = 0; j < N; ++j) key[j] = order_key(l[j]);
+        // a NaN, or +inf, leaves no softmax score of the row a number: its order stays the logits', and the chosen experts
+        // carry the NaN on in their probs
+        const float rk = a.sigmoid ? 1.0f : r.rz;
+        if (a.bias && !isnan(rk)) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (key[j]) key[j] = order_key(p[j] * rk + a.bias[lane + 32 * j]);
         }
         LaneKeys<N> mine(key);
         int my_id = -1;

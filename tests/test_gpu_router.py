@@ -376,3 +376,39 @@ def test_sigmoid_gradients_of_high_logits(normalise):
     r = (4 / 32 + 64) * U
     assert ((dl[:, :3].double() - want).abs() <= 4 * r * want.abs() + 4 * r * want.abs().amax(1, keepdim=True)).all()
     assert not dl[:, 3].any()
+
+
+@gpu
+@pytest.mark.parametrize("score", list(SCORES))
+@pytest.mark.parametrize("normalise", [False, True])
+@pytest.mark.parametrize("E", [24, 200])
+def test_nan_and_infinite_logits_keep_their_rows_ids_with_a_bias(score, normalise, E):
+    """A NaN logit is never chosen, the row's other experts are, with NaN probs, so that the NaN reaches the token's
+    result; so it is with +inf and softmax scores. Such a softmax row has no scores for the bias to move."""
+    k = 4
+    g = torch.Generator(device="cuda").manual_seed(8)
+    l = torch.stack([torch.randperm(E, generator=g, device="cuda") for _ in range(6)]).float() * 0.05
+    bias = torch.zeros(E, device="cuda")
+    bias[11] = 4.0
+    l[1, 5], l[2, 11], l[3, 7] = math.nan, math.nan, math.inf
+    l[4, 6], l[4, 3] = math.inf, math.nan
+    router = M.MoERouter(E, k, score=SCORES[score], normalise=normalise)
+    ids, probs, counts, _ = router.forward(l, select_bias=bias)
+    assert (ids >= 0).all() and int(counts.sum()) == 6 * k and all(len(set(r)) == k for r in ids.tolist())
+    assert 5 not in ids[1].tolist() and 11 not in ids[2].tolist() and 3 not in ids[4].tolist()
+    top = l.nan_to_num(nan=-math.inf, posinf=1e3).argsort(dim=-1, descending=True, stable=True)
+    for t in range(6):
+        rest = [e for e in top[t].tolist() if e != 11]
+        want = [11] + rest[:k - 1] if t != 2 else rest[:k]
+        if score == "softmax" and 1 <= t <= 4:     # no scores: by the logits alone
+            want = top[t].tolist()[:k]
+        assert ids[t].tolist() == want, t
+    assert probs[1].isnan().all() and probs[2].isnan().all() and probs[4].isnan().all()
+    assert not probs[[0, 5]].isnan().any()
+    if score == "softmax":
+        assert probs[3].isnan().all()
+    else:
+        assert float(probs[3, ids[3].tolist().index(7)]) == (1.0 if not normalise else float(probs[3].max()))
+    # without a bias the same rows, by their logits
+    ids, probs, counts, _ = router.forward(l)
+    assert (ids >= 0).all() and ids[3, 0] == 7 and ids[4, 0] == 6 and probs[4].isnan().all()
