@@ -176,6 +176,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+// a value as two bf16 terms, hi + lo. A value that rounds past bf16's range keeps its highest bits as they are, and an
+// infinity has no second term (inf - inf is NaN, which the sum would be then)
+__device__ __forceinline__ __nv_bfloat16 high_bf16(float v) {
+    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+    return __hisinf(hi) ? __float2bfloat16_rz(v) : hi;
+}
+__device__ __forceinline__ float low_part(float v, float hi) { return isinf(v) ? 0.0f : v - hi; }
 __device__ __forceinline__ float2 unpack_f16x2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory"); }
@@ -767,12 +774,11 @@ struct Producer {
                     if (F16) {
                         hi[i] = pack_f16x2(x0, x1);
                         const float2 h = unpack_f16x2(hi[i]);
-                        lo[i] = pack_f16x2(x0 - h.x, x1 - h.y);
+                        lo[i] = TERMS == 2 ? pack_f16x2(low_part(x0, h.x), low_part(x1, h.y)) : 0u;
                     } else {
-                        hi[i] = pack_bf16x2(x0, x1);
-                        float h0, h1;
-                        unpack_bf16x2(hi[i], h0, h1);
-                        lo[i] = pack_bf16x2(x0 - h0, x1 - h1);
+                        const float h0 = __bfloat162float(high_bf16(x0)), h1 = __bfloat162float(high_bf16(x1));
+                        hi[i] = pack_bf16x2(h0, h1);
+                        lo[i] = pack_bf16x2(low_part(x0, h0), low_part(x1, h1));
                     }
                 }
                 *reinterpret_cast<uint4*>(row + 2 * c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -960,10 +966,10 @@ struct Consumer {
                     if (B::MX) {
                         row[i] = v;
                     } else {
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+                        const __nv_bfloat16 hi = high_bf16(v);
                         __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(row + i / kc * kc) + i % kc;
                         d[0] = hi;
-                        d[kc] = __float2bfloat16_rn(v - __bfloat162float(hi));
+                        d[kc] = __float2bfloat16_rn(low_part(v, __bfloat162float(hi)));
                     }
                 }
         }

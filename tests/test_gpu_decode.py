@@ -587,3 +587,55 @@ def test_tensors_on_two_devices_are_refused():
     assert M.moe_launch_count() == before
     M.moe_decode(dec.handle, 3, c.x, c.ids, c.probs, w, out)
     check(out, *c.reference())
+
+
+def overflow_case(mx, shared, finite):
+    """One expert (the shared one, or expert 1) whose activation i = 3 of token 2 is 2^240, or, finite, 2^128 (1 - 2^-10):
+    the largest bf16 is less, the largest fp32 more. Every other activation of that token is 0."""
+    T, H, I, E, k = 5, 64, 32, 3, 1
+    c = Layer(T, H, I, E, k, mx, shared, seed=70, missing=0.0)
+    c.ids[:] = 1
+    c.probs[:] = 0.5
+    c.x[:] = 0
+    c.x[2, 0], c.x[2, 40] = 2.0 ** 32, 1.0
+    g, u = (2.0 ** 32, 2.0 ** 32) if finite else (2.0 ** 88, 2.0 ** 88)
+    fc1, fc2 = torch.zeros(2 * I, H, device="cuda"), torch.where(torch.arange(H, device="cuda") % 3 == 0, -1.0, 1.0)[:, None].repeat(1, I)
+    fc1[3, 0], fc1[I + 3, 0] = g, u
+    if finite:
+        fc1[I + 3, 40] = -2.0 ** 54
+        fc2 *= 2.0 ** -20
+    zero1, zero2 = torch.zeros_like(fc1), torch.zeros_like(fc2)
+    stack = lambda m, z: torch.stack([z, z if shared else m, z])  # noqa: E731
+    if mx:
+        (c.q1, c.s1), (c.q2, c.s2) = quantise(stack(fc1, zero1)), quantise(stack(fc2, zero2))
+        c.fc1, c.fc2 = mx_values(c.q1, c.s1), mx_values(c.q2, c.s2)
+    else:
+        c.b1, c.b2 = stack(fc1, zero1).bfloat16(), stack(fc2, zero2).bfloat16()
+        c.fc1, c.fc2 = c.b1.double(), c.b2.double()
+    if shared:
+        c.sfc1, c.sfc2 = fc1.bfloat16(), fc2.bfloat16()
+    return c
+
+
+@gpu
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("finite", [False, True])
+def test_activations_past_what_bf16_holds(mx, shared, finite):
+    """An activation that overflows gives the infinity that the definition's 2^240 rounds to, not NaN; one that fp32 holds
+    and bf16 does not is multiplied as it is."""
+    if mx and not shared:
+        finite = False       # two f16 terms under a scale of their own
+    c = overflow_case(mx, shared, finite)
+    out = c.decoder().forward_topk(c.x, c.ids, c.probs, c.weights())
+    x = c.x.double()
+    fc1, fc2, p = (c.sfc1.double(), c.sfc2.double(), 1.0) if shared else (c.fc1[1], c.fc2[1], 0.5)
+    gate, up = (x @ fc1.t()).chunk(2, -1)
+    ref = p * ((gate * torch.sigmoid(gate) * up) @ fc2.t())
+    if finite:
+        assert float(ref[2].abs().max()) < 1e33
+        check(out, ref, 2.0 ** -15 * ref.abs())
+    else:
+        assert float(ref[2].abs().min()) > 1e70
+        assert torch.equal(out, ref.bfloat16()) and torch.isinf(out[2]).all()
+    assert not out[[0, 1, 3, 4]].any()
