@@ -16,6 +16,7 @@ c_int64, c_int32, c_float, c_void_p, c_size_t = (ctypes.c_int64, ctypes.c_int32,
 
 MOE_OK = 0
 MOE_ERR_ROUTING, MOE_ERR_TIMEOUT = 3, 5    # device-detected errors (moe_device_status)
+MOE_ERR_STATE = 6
 MOE_W_BF16, MOE_W_MXFP8 = 0, 1
 MOE_G_FP32, MOE_G_BF16 = 0, 1
 MOE_ACT_FP32, MOE_ACT_BF16 = 0, 1   # activations between the expert GEMMs (include/moe.h, moe_act)
@@ -645,6 +646,7 @@ class MoELayer:
                               MOE_ACT_FP32 if act_precision is None else int(act_precision),
                               0 if shared_expert else 1)
         self.device = torch.device(device)
+        self.prepared = None
         ws = moe_workspace_size(self.cfg)
         sv = moe_saved_size(self.cfg)
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=self.device)
@@ -658,6 +660,7 @@ class MoELayer:
 
     def prepare_weights(self, weights: moe_weights, stream=None):
         moe_prepare_weights(self.handle, weights, stream)
+        self.prepared = bytes(weights)  # whose scales the handle holds
 
     def forward(self, hidden, probs, routing_map, weights: moe_weights, out=None, stream=None):
         import torch

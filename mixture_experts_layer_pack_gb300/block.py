@@ -12,6 +12,11 @@ for training runs on a ``MoELayer`` and is followed by ``backward``; ``decode``
 is the same function without anything kept for a backward pass: a
 ``MoEDecoder`` takes batches of up to ``decode_tokens`` tokens, larger ones go
 to the layer.
+
+With MXFP8 experts the layer multiplies by scales in a layout of its own, which
+it holds for one set of weights: ``prepare`` converts them, before the first
+forward with a set and after every change of its scales. The decoder reads the
+weights as they are.
 """
 from __future__ import annotations
 
@@ -52,7 +57,20 @@ class MoEBlock:
             self.decoder = B.MoEDecoder(decode_tokens, hidden, num_experts, topk, inter, device=device,
                                         routed_wtype=routed_wtype, swiglu_limit=swiglu_limit, shared_expert=shared_expert)
         self.decode_tokens = decode_tokens
+        self._mx = routed_wtype == B.MOE_W_MXFP8
         self._kept = None
+
+    def prepare(self, params: BlockParams):
+        """Converts the scales of params' MXFP8 experts for the layer (nothing to do for BF16 ones, or for a block that
+        only decodes); on the current stream. Weights need their columnwise payloads and scales for it."""
+        if self._mx and self.layer is not None:
+            self.layer.prepare_weights(params.weights)
+
+    def _layer_for(self, p):
+        """The layer, which must not hold the scales of other weights (holding none, it says so itself)."""
+        if self._mx and self.layer.prepared not in (None, bytes(p.weights)):
+            raise B.MoeError(B.MOE_ERR_STATE, "MoEBlock: prepare(params) comes first, the layer holds other weights' scales;")
+        return self.layer
 
     def _routed(self, x, residual, p):
         import torch
@@ -65,8 +83,9 @@ class MoEBlock:
         on the current stream. What backward needs is kept until it, or the next forward."""
         if self.layer is None:
             raise ValueError("the block was made for decoding only (max_tokens 0)")
+        layer = self._layer_for(params)
         y, s, mean, rstd, logits, (ids, probs, counts, losses) = self._routed(x, residual, params)
-        out = self.layer.forward_topk(y, ids, probs, params.weights)
+        out = layer.forward_topk(y, ids, probs, params.weights)
         self._kept = (params, y, s, mean, rstd, logits, ids, counts)
         return out, s, losses
 
@@ -80,8 +99,9 @@ class MoEBlock:
         p, y, s, mean, rstd, logits, ids, counts = self._kept
         if dout.shape != y.shape or dout.dtype != y.dtype or dout.device != y.device:
             raise ValueError("dout must be [T, H] bf16 on the block's device")
+        layer = self._layer_for(p)
         self._kept = None
-        dy, dprobs = self.layer.backward(dout.contiguous(), main_grads)  # the layer takes compact rows
+        dy, dprobs = layer.backward(dout.contiguous(), main_grads)  # the layer takes compact rows
         dlogits = self.router.backward(logits, ids, dprobs, counts=counts, loss_grad=loss_grad)
         drouter = dlogits.t() @ y.to(dlogits.dtype)
         # one rounding of the sum of both paths to y
@@ -92,11 +112,11 @@ class MoEBlock:
     def decode(self, x, params: BlockParams, residual=None):
         """(out, s) as forward's, with nothing kept; may be captured into a CUDA graph (experts given as per-expert
         tables: after one call with the same tables)."""
-        y, s, _, _, _, (ids, probs, _, _) = self._routed(x, residual, params)
         small = self.decoder is not None and x.shape[0] <= self.decode_tokens
         if not small and self.layer is None:
             raise ValueError(f"the block decodes up to {self.decode_tokens} tokens")
-        run = self.decoder if small else self.layer
+        run = self.decoder if small else self._layer_for(params)
+        y, s, _, _, _, (ids, probs, _, _) = self._routed(x, residual, params)
         if not small:
             self._kept = None  # the layer's saved state is overwritten
         return run.forward_topk(y, ids, probs, params.weights), s

@@ -202,3 +202,70 @@ def test_gradients_of_any_layout():
     for view in (wide[:, :H], full.t().contiguous().t()):
         assert all(torch.equal(a, b) for a, b in zip(step(view), want))
     assert all(torch.equal(a, b) for a, b in zip(step(row.expand(T, H)), step(row.repeat(T, 1))))
+
+
+def mx_params(H, I, E, seed):
+    """params with MXFP8 experts, and (wherever a comparison needs them) their tensors."""
+    t, p = params(H, I, E, torch.float32, False, seed)
+    t["mx"] = [M.mxfp8_weight(m) for m in (t["fc1"][:, :I], t["fc1"][:, I:], t["fc2"])]
+    p.weights.routed_gate, p.weights.routed_up, p.weights.routed_down = (M.mxfp8_view(*v) for v in t["mx"])
+    return t, p
+
+
+@gpu
+def test_mxfp8_experts():
+    """The block's steps are its parts run one by one, bit for bit, on the scales of the params that were prepared;
+    with other params, or none prepared, they are refused."""
+    T, H, I, E, k = 96, 256, 128, 8, 2
+    sets = [mx_params(H, I, E, seed) for seed in (21, 22)]
+    g = torch.Generator(device="cuda").manual_seed(23)
+    x, r, dout = (torch.randn(T, H, generator=g, device="cuda").bfloat16() for _ in range(3))
+    block = M.MoEBlock(T, H, E, k, I, routed_wtype=B.MOE_W_MXFP8)
+
+    def grads(t):
+        mg = {n: torch.zeros(*t[n].shape, device="cuda") for n in ("shared1", "shared2", "fc1", "fc2")}
+        return mg, M.main_grads_from_combined(mg["shared1"], mg["shared2"], mg["fc1"], mg["fc2"])
+
+    def refused(call):
+        with pytest.raises(M.MoeError) as e:
+            call()
+        assert e.value.status == B.MOE_ERR_STATE
+
+    refused(lambda: block.forward(x, sets[0][1], residual=r))
+    for t, p in sets:
+        block.prepare(p)
+        out, s, _ = block.forward(x, p, residual=r)
+        ids, counts = block._kept[6], block._kept[7]
+        mg, m = grads(t)
+        dx, gr = block.backward(dout, m)
+        # the parts
+        layer = M.MoELayer(T, H, E, k, I, routed_wtype=B.MOE_W_MXFP8)
+        layer.prepare_weights(p.weights)
+        y, s2, mean, rstd = block.norm.forward(x, p.norm_weight, residual=r, out_dtype=torch.bfloat16)
+        logits = torch.nn.functional.linear(y.float(), p.router_weight)
+        ids2, probs2, counts2, _ = block.router.forward(logits)
+        assert torch.equal(ids, ids2) and torch.equal(counts, counts2) and torch.equal(s, s2)
+        assert torch.equal(out, layer.forward_topk(y, ids2, probs2, p.weights))
+        mg2, m2 = grads(t)
+        dy, dprobs = layer.backward(dout, m2)
+        dl = block.router.backward(logits, ids2, dprobs, counts=counts2)
+        dx2, dw2, _ = block.norm.backward(torch.addmm(dy.float(), dl, p.router_weight), s2, p.norm_weight, mean, rstd)
+        assert torch.equal(dx, dx2) and torch.equal(gr["norm_weight"], dw2) and all(torch.equal(mg[n], mg2[n]) for n in mg)
+        # decoding reads the weights as they are; more tokens than the decoder takes go to the layer
+        few, _ = block.decode(x[:9], p, residual=r[:9])
+        scale = float(out.float().abs().max())
+        assert float((few.float() - out[:9].float()).abs().max()) <= 6e-2 * scale    # the layer quantises activations
+        assert torch.equal(block.decode(x, p, residual=r)[0], out)
+    # the layer holds the second set's scales
+    (_, p0), (t1, p1) = sets
+    refused(lambda: block.forward(x, p0, residual=r))
+    refused(lambda: block.decode(x, p0, residual=r))
+    block.decode(x[:9], p0, residual=r[:9])
+    out, _, _ = block.forward(x, p1, residual=r)
+    block.prepare(p0)
+    mg, m = grads(t1)
+    refused(lambda: block.backward(dout, m))
+    block.prepare(p1)
+    dx2, _ = block.backward(dout, m)
+    assert torch.equal(dx, dx2) and all(torch.equal(mg[n], mg2[n]) for n in mg)
+    M.MoEBlock(0, H, E, k, I, routed_wtype=B.MOE_W_MXFP8).prepare(p0)   # nothing to prepare
