@@ -181,7 +181,7 @@ struct NormFwd {
     bool w_bf16;
 };
 
-// ---- Rows of more than kStreamed columns in whole 16-byte pieces: a block a row
+// ---- bf16 rows of more than kStreamed columns, up to 16384, in whole 16-byte pieces: a block a row
 // The row stays in the registers of its threads, NV pieces of V elements each: read once,
 // written once, and the variance is of differences from the mean, not of squares.
 template <typename XT, typename YT, bool RMS, int V, int NV>
@@ -1002,8 +1002,11 @@ moe_status moe_norm_forward(const moe_norm_config* cfg, int64_t T, const void* x
                 return sh.threads <= kNarrow ? go(Int<kNarrow>{}) : sh.threads <= kWide ? go(Int<kWide>{}) : go(Int<kWidest>{});
         }
         count_launch();
-        if (wide && H / V <= 4 * kRowThreads)
-            return launch_pdl(norm_forward_kernel<X, Y, R, V, 4>, dim3(unsigned(T)), dim3(unsigned((H / V + 127) / 128 * 32)), 0, cs, a);
+        if constexpr (V * 4 * kRowThreads > kStreamed) {  // bf16: up to 16384 columns (fp32 rows of 8192 are streamed)
+            if (wide && H / V <= 4 * kRowThreads)
+                return launch_pdl(norm_forward_kernel<X, Y, R, V, 4>, dim3(unsigned(T)), dim3(unsigned((H / V + 127) / 128 * 32)), 0,
+                                  cs, a);
+        }
         return wide ? launch_pdl(norm_forward_wide_kernel<X, Y, R, V>, dim3(unsigned(T)), dim3(kRowThreads), 0, cs, a)
                     : launch_pdl(norm_forward_wide_kernel<X, Y, R, 1>, dim3(unsigned(T)), dim3(kRowThreads), 0, cs, a);
     });
