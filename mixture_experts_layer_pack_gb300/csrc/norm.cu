@@ -295,6 +295,7 @@ struct StreamRing {
     int groups;
     int s = 0;
     uint32_t parity = 0;
+    bool late = false;  // a wait gave up
     __device__ __forceinline__ void init() const {
         if (threadIdx.x < st.stages) mbar_init(full + threadIdx.x, 1);
         if (threadIdx.x < 32) {
@@ -309,12 +310,12 @@ struct StreamRing {
     __device__ __forceinline__ void ask(int at, unsigned t0, unsigned T) const {
         const int lane = threadIdx.x & 31;
         const Ask q = asks[lane];
-        const bool mine = q.row_bytes != 0 && unsigned(lane / st.arrays) < T - t0;
+        const bool mine = q.row_bytes != 0 && !late && unsigned(lane / st.arrays) < T - t0;
         const char* src = q.from + t0 * q.step;
         const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(src)) & 15u;
         const uint32_t bytes = mine ? (off + uint32_t(q.row_bytes) + 15u) & ~15u : 0u;
         const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
-        if (lane == 0) mbar_arrive_expect_tx(full + at, total);
+        if (lane == 0 && !late) mbar_arrive_expect_tx(full + at, total);
         __syncwarp();
         if (mine)
             asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -322,12 +323,22 @@ struct StreamRing {
                          "l"(src - off), "r"(bytes), "r"(smem_u32(full + at))
                          : "memory");
     }
-    // the next rows are there; bounded: a wait that gave up goes on with what is there (every copy ends)
-    __device__ __forceinline__ void wait() const {
+    // The next rows are there; bounded: after a wait that gave up the thread waits and asks for nothing more, and makes its
+    // results NaN (there is no status word to say it in).
+    __device__ __forceinline__ void wait() {
         if (mbar_try_wait(full + s, parity)) return;
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(full + s, parity))
-            if (globaltimer_ns() - t0 > kWaitLimitNs) return;
+            if (late || globaltimer_ns() - t0 > kWaitLimitNs) {
+                late = true;
+                return;
+            }
+    }
+    // before the block gives back its shared memory: the copies that were not waited for land in it
+    __device__ __forceinline__ void end() const {
+        if (!late) return;
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000) __nanosleep(1000);
     }
     // input i's row t, of row group g in the current stage; whole: rows are known to begin on 16 bytes
     template <typename E, bool Whole>
@@ -474,7 +485,7 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_forward_stream
         asker = asker + 1 == int(blockDim.x >> 5) ? 0 : asker + 1;
         ring.next();
         if (!live) continue;
-        const float rstd = rsqrtf(sq[0] * inv + a.eps);
+        const float rstd = rsqrtf(sq[0] * inv + (ring.late ? NAN : a.eps));
         YT* y = static_cast<YT*>(a.y) + t * a.ys + cols.base;
         cols.run([&](auto all) {
             const uint64_t r2 = f2(rstd, rstd);
@@ -490,6 +501,7 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_forward_stream
             if (a.rstd) a.rstd[t] = rstd;
         }
     }
+    ring.end();
 }
 
 // Rows too wide for that: row blockIdx.x read three times (the second and third from cache)
@@ -619,6 +631,7 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_backward_kerne
             rstd_after = a.rstd[t + step];
         }
         ring.wait();
+        if (ring.late) rstd = NAN;
         const XT* x = ring.row<XT, kWhole>(0, group, t) + cols.base;
         const YT* dy = ring.row<YT, (V > 1 && V * sizeof(YT) >= 16)>(1, group, t) + cols.base;
         float xh[NV][V], g[NV][V], sum[2];  // of g xhat, g
@@ -701,6 +714,7 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_backward_kerne
         before = ring.s;
         ring.next();
     }
+    ring.end();
     if (a.part == nullptr) return;
     float* out = a.part + int64_t(blockIdx.x) * 2 * a.H;
     if (groups == 1) {
