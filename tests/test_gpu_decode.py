@@ -639,3 +639,77 @@ def test_activations_past_what_bf16_holds(mx, shared, finite):
         assert float(ref[2].abs().min()) > 1e70
         assert torch.equal(out, ref.bfloat16()) and torch.isinf(out[2]).all()
     assert not out[[0, 1, 3, 4]].any()
+
+
+@gpu
+def test_two_decoders_on_two_streams():
+    """Launches of two decoders that nothing orders: each has its own barrier, and all of its blocks resident."""
+    c = Layer(5, 1160, 424, 10, 3, seed=42)
+    w = c.weights()
+    decs = [c.decoder(), c.decoder()]
+    want = decs[0].forward_topk(c.x, c.ids, c.probs, w)
+    check(want, *c.reference())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        for d, s in zip(decs, streams):
+            with torch.cuda.stream(s):
+                outs.append(d.forward_topk(c.x, c.ids, c.probs, w))
+    for d, s in zip(decs, streams):
+        assert d.device_status(s) == B.MOE_OK
+    assert all(torch.equal(o, want) for o in outs)
+
+
+@gpu
+def test_the_state_starts_anew_after_a_recorded_timeout():
+    """A status word that says that a wait gave up, a barrier and counters as such a launch may leave them (written
+    here: no wait runs out): the status is reported once, and the next call is right."""
+    c = Layer(6, 520, 136, 5, 3, seed=43)
+    dec, w = c.decoder(), c.weights()
+    want = dec.forward_topk(c.x, c.ids, c.probs, w)
+    assert dec.device_status() == B.MOE_OK
+    state = dec.workspace[:4 * (2 + (520 + 15) // 16)].view(torch.int32)
+    state[0] = 2                                       # the timeout bit
+    state[1] = 77
+    state[2:] = 3
+    assert dec.device_status() == B.MOE_ERR_TIMEOUT and dec.device_status() == B.MOE_OK
+    assert not state.any()
+    assert torch.equal(dec.forward_topk(c.x, c.ids, c.probs, w), want) and dec.device_status() == B.MOE_OK
+
+
+@gpu
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T,k", [(1, 4), (7, 3), (8, 4), (9, 3)])
+def test_bad_ids_among_few_routes(T, k, mx):
+    """Up to 32 routes are sorted by one warp: ids out of range and chosen twice, alone and beside good rows."""
+    c = Layer(T, 128, 64, 5, k, mx, seed=9, missing=0.0)
+    dec, w = c.decoder(), c.weights()
+    good = c.ids.clone()
+    for put in ([(0, 0, 5)], [(0, k - 1, -2)], [(0, 1, int(good[0, 0]))], [(T - 1, 0, 1 << 30), (0, k - 1, int(good[0, 0]))],
+                [(T - 1, k - 1, -(1 << 31))], [(0, 0, -1), (0, 1, -1)]):
+        bad = good.clone()
+        for t, s, v in put:
+            bad[t, s] = v
+        out = dec.forward_topk(c.x, bad, c.probs, w)
+        empty = all(v == -1 for _, _, v in put)
+        assert dec.device_status() == (B.MOE_OK if empty else B.MOE_ERR_ROUTING) and dec.device_status() == B.MOE_OK
+        kept = bad if empty else good.clone()
+        if not empty:
+            kept[[t for t, _, _ in put]] = -1
+        check(out, *c.reference(kept))
+        assert torch.equal(dec.forward_topk(c.x, kept, c.probs, w), out)
+
+
+@gpu
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T", [1, 10, 30])
+def test_no_route_and_no_shared_expert(T, mx):
+    """Nothing chosen and nothing shared: rows of zeros, in a wider buffer too, and nothing beside them written; the next
+    call is right."""
+    c = Layer(T, 96, 64, 5, 3, mx, shared=False, seed=10, missing=0.0)
+    dec, w = c.decoder(), c.weights()
+    into = torch.full((T, 104), 7.0, dtype=torch.bfloat16, device="cuda")
+    dec.forward_topk(c.x, torch.full_like(c.ids, -1), torch.full_like(c.probs, math.nan), w, out=into[:, :96])
+    assert not into[:, :96].any() and (into[:, 96:] == 7).all() and dec.device_status() == B.MOE_OK
+    check(dec.forward_topk(c.x, c.ids, c.probs, w), *c.reference())

@@ -412,3 +412,40 @@ def test_nan_and_infinite_logits_keep_their_rows_ids_with_a_bias(score, normalis
     # without a bias the same rows, by their logits
     ids, probs, counts, _ = router.forward(l)
     assert (ids >= 0).all() and ids[3, 0] == 7 and ids[4, 0] == 6 and probs[4].isnan().all()
+
+
+@gpu
+@pytest.mark.parametrize("score", list(SCORES))
+@pytest.mark.parametrize("T,E,k,xt", [(16384, 128, 8, F32), (7297, 70, 6, BF16), (8001, 384, 6, F32), (5003, 200, 4, BF16),
+                                      (3700, 500, 8, F32), (4001, 1000, 9, BF16)])
+def test_more_rows_than_the_grid_has_warps(T, E, k, xt, score):
+    """A warp takes several rows, the last round uneven, some experts closed and some rows empty, with losses: forward
+    and backward against the definition. Without counts the C entry gives the same choice."""
+    l, _ = logits_of(T, E, xt, T + E, closed=0.2, pad=3)
+    l[5], l[T - 1] = -math.inf, -math.inf
+    c = dict(E=E, k=k, score=score, normalise=True, scale=2.5, aux=float(torch.tensor(0.02, dtype=F32)), z=float(torch.tensor(0.003, dtype=F32)))
+    router = M.MoERouter(E, k, score=SCORES[score], scale=2.5, aux_coeff=0.02, z_coeff=0.003)
+    ids, probs = by_definition(l, router, c)
+    ids2, probs2 = torch.empty_like(ids), torch.empty_like(probs)
+    M.moe_router_forward(router._cfgs[xt], l, ids2, probs2)
+    assert torch.equal(ids, ids2) and torch.equal(probs, probs2)
+    plain = M.MoERouter(E, k, score=SCORES[score], scale=2.5).forward(l)
+    assert torch.equal(ids, plain[0]) and torch.equal(probs, plain[1]) and plain[3] is None
+    assert torch.equal(plain[2], router.forward(l)[2])
+
+
+@gpu
+@pytest.mark.parametrize("score", list(SCORES))
+@pytest.mark.parametrize("T,E,k,xt", [(300, 48, 5, F32), (200, 96, 6, BF16), (120, 256, 8, F32), (5000, 384, 6, BF16)])
+def test_select_bias_with_losses(T, E, k, xt, score):
+    """The bias moves the choice (and so the counts), not the scores, their distribution, the losses or the gradients.
+    Sums of score and bias are kept apart: scores of any size, the bias of an expert 1 more than that of the one before."""
+    l, _ = logits_of(T, E, xt, 3 * T + E, closed=0.1)
+    order = torch.randperm(E, generator=torch.Generator(device="cuda").manual_seed(E), device="cuda")
+    bias = order.float() * 1.0 - E / 2
+    l = l.clamp(max=1.0)
+    l[:, ::7] -= 3.0
+    c = dict(E=E, k=k, score=score, normalise=True, scale=1.5, aux=float(torch.tensor(0.02, dtype=F32)), z=float(torch.tensor(0.003, dtype=F32)))
+    router = M.MoERouter(E, k, score=SCORES[score], scale=1.5, aux_coeff=0.02, z_coeff=0.003)
+    ids, _ = by_definition(l, router, c, bias)
+    assert not torch.equal(ids, router.forward(l)[0])
