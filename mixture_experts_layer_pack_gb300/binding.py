@@ -798,6 +798,7 @@ class MoEDecoder:
         with torch.cuda.device(self.device):
             self.handle = moe_decode_create(self.cfg, self.workspace)
         self.index = self.workspace.get_device()
+        self._streams = {self._stream(self.index)}  # those that the allocator knows to use the workspace
 
     @_on_stream
     def forward_topk(self, hidden, topk_ids, topk_probs, weights: moe_weights, out=None):
@@ -818,8 +819,12 @@ class MoEDecoder:
             out = torch.empty(shape, dtype=torch.bfloat16, device=hidden.device)
         elif out.dtype != torch.bfloat16 or out.shape != shape or out.stride(1) != 1:
             raise ValueError("out must be [T, H] bf16 with contiguous rows")
+        stream = self._stream(index)
+        if stream not in self._streams:
+            self.workspace.record_stream(torch.cuda.current_stream(index))
+            self._streams.add(stream)
         args = (self.handle, T, hidden.data_ptr(), _ld(hidden), topk_ids.data_ptr(), topk_probs.data_ptr(), weights,
-                out.data_ptr(), _ld(out), self._stream(index))
+                out.data_ptr(), _ld(out), stream)
         status = _call_on(self._current, index, self._call, args)
         if status:
             raise MoeError(status, "moe_decode")

@@ -713,3 +713,29 @@ def test_no_route_and_no_shared_expert(T, mx):
     dec.forward_topk(c.x, torch.full_like(c.ids, -1), torch.full_like(c.probs, math.nan), w, out=into[:, :96])
     assert not into[:, :96].any() and (into[:, 96:] == 7).all() and dec.device_status() == B.MOE_OK
     check(dec.forward_topk(c.x, c.ids, c.probs, w), *c.reference())
+
+
+@gpu
+def test_given_up_while_a_call_on_another_stream_runs():
+    """A decoder that goes away with a call pending on a stream other than the one it was made on: its memory is not
+    handed out before that call has ended."""
+    c = Layer(5, 512, 160, 9, 4, seed=44)
+    w = c.weights()
+    keep = c.decoder()
+    want = keep.forward_topk(c.x, c.ids, c.probs, w)
+    check(want, *c.reference())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    for _ in range(3):
+        dec = c.decoder()
+        n, at = dec.workspace.numel(), dec.workspace.data_ptr()
+        with torch.cuda.stream(side):
+            _busy()
+            got = dec.forward_topk(c.x, c.ids, c.probs, w)
+        del dec
+        others = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        assert all(o.data_ptr() != at for o in others)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del others
