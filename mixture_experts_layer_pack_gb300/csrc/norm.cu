@@ -294,8 +294,8 @@ struct StreamRing {
     uint8_t* mem;
     int groups;
     int s = 0;
-    uint32_t parity = 0;
-    bool late = false;  // a wait gave up
+    uint32_t parity = 0;  // bit 0: of the current round; bit 1: a wait gave up (no register of its own: there is none to spare)
+    __device__ __forceinline__ bool late() const { return parity > 1; }
     __device__ __forceinline__ void init() const {
         if (threadIdx.x < st.stages) mbar_init(full + threadIdx.x, 1);
         if (threadIdx.x < 32) {
@@ -310,12 +310,12 @@ struct StreamRing {
     __device__ __forceinline__ void ask(int at, unsigned t0, unsigned T) const {
         const int lane = threadIdx.x & 31;
         const Ask q = asks[lane];
-        const bool mine = q.row_bytes != 0 && !late && unsigned(lane / st.arrays) < T - t0;
+        const bool mine = q.row_bytes != 0 && !late() && unsigned(lane / st.arrays) < T - t0;
         const char* src = q.from + t0 * q.step;
         const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(src)) & 15u;
         const uint32_t bytes = mine ? (off + uint32_t(q.row_bytes) + 15u) & ~15u : 0u;
         const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
-        if (lane == 0 && !late) mbar_arrive_expect_tx(full + at, total);
+        if (lane == 0 && !late()) mbar_arrive_expect_tx(full + at, total);
         __syncwarp();
         if (mine)
             asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -326,17 +326,17 @@ struct StreamRing {
     // The next rows are there; bounded: after a wait that gave up the thread waits and asks for nothing more, and makes its
     // results NaN (there is no status word to say it in).
     __device__ __forceinline__ void wait() {
-        if (mbar_try_wait(full + s, parity)) return;
+        if (mbar_try_wait(full + s, parity & 1)) return;
         const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(full + s, parity))
-            if (late || globaltimer_ns() - t0 > kWaitLimitNs) {
-                late = true;
+        while (!mbar_try_wait(full + s, parity & 1))
+            if (globaltimer_ns() - t0 > (late() ? 0 : kWaitLimitNs)) {
+                parity |= 2;
                 return;
             }
     }
     // before the block gives back its shared memory: the copies that were not waited for land in it
     __device__ __forceinline__ void end() const {
-        if (!late) return;
+        if (!late()) return;
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 1000000) __nanosleep(1000);
     }
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_forward_stream
         asker = asker + 1 == int(blockDim.x >> 5) ? 0 : asker + 1;
         ring.next();
         if (!live) continue;
-        const float rstd = rsqrtf(sq[0] * inv + (ring.late ? NAN : a.eps));
+        const float rstd = rsqrtf(sq[0] * inv + (ring.late() ? NAN : a.eps));
         YT* y = static_cast<YT*>(a.y) + t * a.ys + cols.base;
         cols.run([&](auto all) {
             const uint64_t r2 = f2(rstd, rstd);
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(NT, NT == kNarrow ? 2 : 1) norm_backward_kerne
             rstd_after = a.rstd[t + step];
         }
         ring.wait();
-        if (ring.late) rstd = NAN;
+        if (ring.late()) rstd = NAN;
         const XT* x = ring.row<XT, kWhole>(0, group, t) + cols.base;
         const YT* dy = ring.row<YT, (V > 1 && V * sizeof(YT) >= 16)>(1, group, t) + cols.base;
         float xh[NV][V], g[NV][V], sum[2];  // of g xhat, g
