@@ -391,10 +391,11 @@ typedef struct moe_decoder moe_decoder;
 /* Bytes of device workspace a decoder for `cfg` needs. The fields of moe_config
  * mean what they mean for a handle, except: max_tokens is at most
  * MOE_DECODE_MAX_TOKENS; hidden and inter need only be multiples of 8 (MXFP8
- * routed weights: of 32), up to 32768; recompute_dispatch must be 0; act_precision is not
- * looked at (the activations between the products are kept in fp32, and reach
- * the second product as two bf16 terms, as with MOE_ACT_FP32; MXFP8 weights are
- * multiplied by unquantised activations). */
+ * routed weights: of 32), up to 32768; recompute_dispatch must be 0; act_precision has to
+ * be valid and changes nothing: the activations a = silu(g) u are fp32 values that reach
+ * the second product, whatever it says, as two bf16 terms beside bf16 weights (16
+ * significant bits, as with MOE_ACT_FP32) and as two f16 terms beside MXFP8 weights (the
+ * routed ones; 22 bits of a slice's largest value). Nothing is quantised to E4M3. */
 moe_status moe_decode_size(const moe_config* cfg, size_t* bytes);
 
 /* Creates a decoder over caller-owned device workspace (256-byte aligned, >=
@@ -424,7 +425,7 @@ void moe_decode_destroy(moe_decoder* d);
  * used under capture stays until moe_decode_destroy, so that replays run with the tables
  * that were captured, whatever other calls use; with that many of them, a call with
  * another set is MOE_ERR_STATE. Results are deterministic: the sums' order depends
- * on the shape and the routing alone. */
+ * on the shape, the routing and the GPU's number of SMs alone. */
 moe_status moe_decode(moe_decoder* d, int64_t T, const void* hidden, int64_t hidden_stride,
                       const int32_t* topk_ids, const float* topk_probs, const moe_weights* w, void* out,
                       int64_t out_stride, void* stream);
@@ -472,7 +473,8 @@ moe_status moe_norm_backward_size(const moe_norm_config* cfg, int64_t T, size_t*
  * dbias = sum_t dy, each optional, are written (accumulate 0) or added (accumulate
  * 1) to [hidden] buffers of g_type (moe_gtype: fp32, or bf16 with
  * main_grad = bf16(main_grad + bf16(dw)), as the layer's main_grads). Row sums and
- * the sums over rows are fp32, in an order fixed by the shape. workspace:
+ * the sums over rows are fp32, in an order fixed by the shape and the GPU's number of
+ * SMs. workspace:
  * 256-byte aligned, >= moe_norm_backward_size bytes; calls that share it must be
  * ordered. */
 moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* dy, int64_t dy_stride,
@@ -485,8 +487,8 @@ moe_status moe_norm_backward(const moe_norm_config* cfg, int64_t T, const void* 
  * score = softmax(logits) or sigmoid(logits), over the experts of a row. The topk
  * experts with the largest logits (a score grows with its logit; equal logits: the
  * lower id) are chosen, in falling order; with select_bias (fp32 [E], or NULL) the
- * order is that of score + select_bias, which the probs do not see. A logit of
- * -inf closes its expert to the token: a row with fewer than topk open experts has
+ * order is that of score + select_bias, which the probs do not see (an expert whose bias is -inf or NaN is not
+ * chosen). A logit of -inf closes its expert to the token: a row with fewer than topk open experts has
  * -1 and prob 0 in its last slots. probs = scale * score, with `normalise` divided by the
  * sum of the row's chosen scores, however small that is (sigmoid scores of logits below
  * -700 count as 0). A NaN logit is never chosen and makes its row's probs NaN; so does

@@ -44,7 +44,9 @@ class MoEBlock:
                  score=B.MOE_SCORE_SOFTMAX, normalise=True, scale=1.0, aux_coeff=0.0, z_coeff=0.0,
                  routed_wtype=B.MOE_W_BF16, swiglu_limit=0.0, act_precision=None, shared_expert=True,
                  decode_tokens=B.MOE_DECODE_MAX_TOKENS):
-        """max_tokens: of a training step, 0 for a block that only decodes; decode_tokens: of the decoder, 0 for none."""
+        """max_tokens: of a training step, 0 for a block that only decodes; decode_tokens: of the decoder, 0 for none.
+        The decoder is made for few tokens an expert: where experts are few, the layer is faster from some 16 tokens
+        each on (64 tokens, H 4096, I 2048, 8 experts top-4: 102 us against 202), so decode_tokens may be less."""
         if max_tokens <= 0 and decode_tokens <= 0:
             raise ValueError("a block needs max_tokens, decode_tokens or both")
         self.norm = B.MoENorm(hidden, eps, norm, device=device)

@@ -26,15 +26,19 @@
 // A thread loads 8 consecutive elements of a weight row and the same 8 of a token's
 // row, which are the operands of two instructions if the sum's index is taken in that
 // order. Tensor rate is not what limits it (most often a weight meets one token, and rarely more than 8).
-// The activations a = silu(g) u go to the second product as two bf16 terms, hi + lo.
+// The activations a = silu(g) u go to the second product as two bf16 terms, hi + lo: off by at most 2^-16 of themselves,
+// which the rounding of `out` to bf16 (2^-8) hides but for one value in some hundreds, next to a rounding boundary (64
+// tokens: 344 of 131072 outputs are not the exact value's nearest, 115 of an fp32 evaluation's). A third term would cost
+// half as many instructions and token bytes again in the second product.
 // MXFP8 weights become f16 in registers (exact, one instruction a pair; bf16 takes
 // four) and their block scales multiply the fp32 sums of 32 columns. Their tokens are
 // f16 too: a slice of a token's row is scaled by the power of two that brings its
-// largest value under 2^15, so that x (8 significant bits) fits one f16 term and a two, with
-// an error of at most 2^-38 of the slice's largest value, and the scale is taken back per slot.
+// largest value under 2^15, and the scale is taken back per slot. x (8 significant bits) is one f16 term then, off by
+// at most 2^-39 of the slice's largest value (what lies under f16's smallest), and a, which is fp32, two, off by at
+// most 2^-23 of it (a low term of up to 8 beside a high one of 2^14 and more).
 //
-// Measured (graph replays): H 2048, I 1024, E 96 top-6 in BF16 with 1, 8, 64 tokens 26 us (3.4 TB/s), 87 us (5.7),
-// 204 us (5.9); H 7168, I 2048, E 128 top-6 in MXFP8 with 4 tokens 207 us (5.3).
+// Measured (graph replays): H 2048, I 1024, E 96 top-6 in BF16 with 1, 8, 64 tokens 24 us (3.7 TB/s), 83 us (6.0),
+// 205 us (5.8); H 7168, I 2048, E 128 top-6 in MXFP8 with 4 tokens 204 us (5.4).
 #include <algorithm>
 #include <cmath>
 #include <memory>
@@ -1343,8 +1347,10 @@ cudaError_t launch_decode(DecodeArgs& a, int blocks, cudaStream_t st) {
     a.c2 = chunks(a.I, true);
     a.it = (a.I + 7) / 8;
     a.ht = (a.H + 15) / 16;
-    // E4M3 weights take more work a slot than the shared expert's bf16 ones: 4 tokens, H 7168, I 2048 with 24 routes
-    // 207 us at 3 : 4, 212 at 4 : 4, 251 at 2 : 4. In groups of 32 the shared expert's are the full ones.
+    // E4M3 weights take more work a slot than the shared expert's bf16 ones. us at 4 : 4, 3 : 4, 2 : 4 of T, H, I, E, k:
+    // 4, 7168, 2048, 128, 6 210 / 203 / 251; 64, 4096, 2048, 8, 2 264 / 239 / 255; 2, 1024, 512, 32, 4 18.3 / 17.6 / 18.9;
+    // 1, 4096, 2048, 16, 2 34.9 / 34.0 / 34.0; 1, 2048, 1024, 64, 6 23.5 / 23.3 / 24.0; but 16, 4096, 1408, 64, 6
+    // 232 / 239 / 272 and 64, 2048, 768, 128, 8 207 / 211 / 248. In groups of 32 the shared expert's are the full ones.
     a.shared_cost = B::MX || B::NT > 1 ? 3 : 2;
     a.routed_cost = B::MX ? 4 : 2;
     cudaLaunchConfig_t cfg = {};

@@ -9,9 +9,9 @@
 //   dw = sum_t dy xhat, db = sum_t dy.
 // All statistics and sums are fp32.
 //
-// Bound by memory where rows are many: 16384 x 4096 bf16 with a residual, forward 84 us (6.4 TB/s), backward with the
-// joining gradient and the weights' 87 us (6.2 TB/s); 16384 x 2051, rows that start anywhere, 53 and 54 us (5.0 TB/s). One
-// row of 2048: 2.4 us. s and y are rounded once each, to the types that the next reader takes.
+// Bound by memory where rows are many: 16384 x 4096 bf16 with a residual, forward 85 us (6.3 TB/s), backward with the
+// joining gradient and the weights' 87 us (6.2 TB/s); 16384 x 2051, rows that start anywhere, 55 and 57 us (4.8 TB/s). One
+// row of 2048: 2.1 us. s and y are rounded once each, to the types that the next reader takes.
 #include <algorithm>
 #include <atomic>
 #include <climits>

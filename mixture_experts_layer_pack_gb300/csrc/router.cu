@@ -7,9 +7,11 @@
 // The choice compares logits, mapped to unsigned integers of the same order, one
 // warp-wide maximum and one warp-wide minimum index per slot: exact, ties to the
 // lower id, whatever the scores round to.
+// Sigmoid scores come from exp(-|l|) alike: the smaller of score and 1 - score is right to its last bits, and so are both.
 //
 // Bound by the instructions of the choice, not by memory: 16384 x 128 fp32, k 8, 12 us, with counts 16, with the losses
-// 20 us (0.5 TB/s); 16384 x 384, k 6, 25, 29 and 34 us; the backward at 8192 x 384 13.5 us (1.9 TB/s).
+// 20 us (0.5 TB/s); 16384 x 384, k 6, 23, 28 and 33 us; the backward with losses, sigmoid, at 8192 x 384 10.5 us
+// (2.4 TB/s), softmax at 16384 x 128 8.2 us (2.2 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
