@@ -198,7 +198,8 @@ moe_status moe_workspace_size(const moe_config* cfg, size_t* bytes);
 
 /* Creates a handle over caller-owned device workspace (256-byte aligned,
  * >= moe_workspace_size bytes, kept alive and unused by others until
- * moe_destroy). The handle itself is host memory owned by the library. The
+ * moe_destroy: work queued on any stream that still touches that memory has ended
+ * before this call). The handle itself is host memory owned by the library. The
  * current CUDA device at this call is the device of every later call.
  * Weight and main_grad views become per-expert TMA descriptor tables in this
  * workspace (with BF16 routed weights every view, the shared expert's as entry

@@ -201,6 +201,9 @@ def moe_saved_size(cfg: moe_config) -> int:
 
 
 def moe_create(cfg: moe_config, workspace) -> c_void_p:
+    import torch
+    # memory that the allocator hands out on this stream may have work of its last owner queued there
+    torch.cuda.current_stream(workspace.device).synchronize()
     h = c_void_p()
     _check(load().moe_create(ctypes.byref(cfg), _ptr(workspace), workspace.numel() * workspace.element_size(),
                              ctypes.byref(h)), "moe_create")

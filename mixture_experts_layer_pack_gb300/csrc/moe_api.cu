@@ -706,7 +706,9 @@ moe_status moe_create(const moe_config* cfg, void* workspace, size_t workspace_b
     carve_workspace(s, static_cast<uint8_t*>(workspace), &h->ws);
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
-        cudaMemset(h->ws.status, 0, sizeof(int)) != cudaSuccess) {
+        // waited for: the first call may be on a stream that does not wait for this one
+        cudaMemsetAsync(h->ws.status, 0, sizeof(int), cudaStreamPerThread) != cudaSuccess ||
+        cudaStreamSynchronize(cudaStreamPerThread) != cudaSuccess) {
         delete h;
         return MOE_ERR_CUDA;
     }
@@ -1420,9 +1422,10 @@ moe_status moe_device_status(moe_handle* h, void* stream) {
     if (!h) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int v = 0;
+    MOE_CU(cudaMemcpyAsync(&v, h->ws.status, sizeof(int), cudaMemcpyDeviceToHost, st));
     MOE_CU(cudaStreamSynchronize(st));
-    MOE_CU(cudaMemcpy(&v, h->ws.status, sizeof(int), cudaMemcpyDeviceToHost));
-    MOE_CU(cudaMemset(h->ws.status, 0, sizeof(int)));
+    MOE_CU(cudaMemsetAsync(h->ws.status, 0, sizeof(int), st));
+    MOE_CU(cudaStreamSynchronize(st));  // the next call may be on another stream
     if (v & kStatusTimeout) return MOE_ERR_TIMEOUT;
     if (v & kStatusRouting) return MOE_ERR_ROUTING;
     return MOE_OK;

@@ -383,3 +383,42 @@ def test_nan_in_one_token_stays_in_that_token():
             continue
         for n in ("routed_fc1", "routed_fc2"):
             assert torch.equal(bad.main_grads[n][e], clean.main_grads[n][e]), (n, e)
+
+
+def test_created_on_a_side_stream_with_work_pending():
+    """The status word is cleared after what its memory's last owner still had queued, and before the first call; the
+    status itself reads and clears it between the calls of its stream, with the default stream busy."""
+    import mixture_experts_layer_pack_gb300 as M
+    T, H, E, k, I = 64, 128, 8, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: (torch.randn(*s, generator=g, device="cuda") * 0.05).bfloat16()  # noqa: E731
+    t = [r(2 * I, H), r(H, I), r(E, 2 * I, H), r(E, H, I)]
+    w, x = M.weights_from_combined(*t), r(T, H)
+    ids = torch.stack([torch.randperm(E, generator=g, device="cuda")[:k] for _ in range(T)]).int()
+    probs = torch.rand(T, k, generator=g, device="cuda")
+    want = M.MoELayer(T, H, E, k, I).forward_topk(x, ids, probs, w)
+    n = M.moe_workspace_size(M.MoELayer(T, H, E, k, I).cfg)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)
+    with torch.cuda.stream(side):
+        old = torch.empty(n, dtype=torch.uint8, device="cuda")
+        at = old.data_ptr()
+        torch.cuda._sleep(20_000_000)
+        old.fill_(255)                       # still to come when its memory is given away
+        del old
+        layer = M.MoELayer(T, H, E, k, I)
+        assert layer.workspace.data_ptr() == at
+        got = layer.forward_topk(x, ids, probs, w)
+        assert layer.device_status() == 0
+        bad = ids.clone()
+        bad[0, 0] = E
+        layer.forward_topk(x, bad, probs, w)
+    torch.cuda._sleep(20_000_000)
+    assert layer.device_status(side) == 3 and layer.device_status(side) == 0    # MOE_ERR_ROUTING once
+    with torch.cuda.stream(side):
+        again = layer.forward_topk(x, ids, probs, w)
+        assert layer.device_status() == 0
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(again, want)
