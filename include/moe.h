@@ -208,7 +208,8 @@ moe_status moe_workspace_size(const moe_config* cfg, size_t* bytes);
  * change; such an upload (a host-to-device copy from library host memory)
  * waits for the work already queued on `stream` before it starts, and cannot
  * be captured into a CUDA graph: run one call with the same buffers before
- * capturing. */
+ * capturing. A captured call reads the tables at every replay: while its graph
+ * is in use, call the handle with the same buffers only. */
 moe_status moe_create(const moe_config* cfg, void* workspace, size_t workspace_bytes, moe_handle** out);
 void moe_destroy(moe_handle* h);
 

@@ -663,7 +663,8 @@ class MoELayer:
 
     def prepare_weights(self, weights: moe_weights, stream=None):
         moe_prepare_weights(self.handle, weights, stream)
-        self.prepared = bytes(weights)  # whose scales the handle holds
+        if self.cfg.routed_wtype == MOE_W_MXFP8:
+            self.prepared = bytes(weights)  # whose scales the handle holds
 
     def forward(self, hidden, probs, routing_map, weights: moe_weights, out=None, stream=None):
         import torch

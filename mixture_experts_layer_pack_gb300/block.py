@@ -17,6 +17,11 @@ With MXFP8 experts the layer multiplies by scales in a layout of its own, which
 it holds for one set of weights: ``prepare`` converts them, before the first
 forward with a set and after every change of its scales. The decoder reads the
 weights as they are.
+
+Steps may be captured into CUDA graphs. The decoder's replays keep the expert
+tables that were captured with them, whatever else it decodes; the layer has one
+set of tables, so a block that had a step through it captured takes no other
+weights there.
 """
 from __future__ import annotations
 
@@ -60,19 +65,32 @@ class MoEBlock:
                                         routed_wtype=routed_wtype, swiglu_limit=swiglu_limit, shared_expert=shared_expert)
         self.decode_tokens = decode_tokens
         self._mx = routed_wtype == B.MOE_W_MXFP8
-        self._kept = None
+        self._kept = self._captured = None
 
     def prepare(self, params: BlockParams):
         """Converts the scales of params' MXFP8 experts for the layer (nothing to do for BF16 ones, or for a block that
         only decodes); on the current stream. Weights need their columnwise payloads and scales for it."""
         if self._mx and self.layer is not None:
+            self._uncaptured(params)
             self.layer.prepare_weights(params.weights)
 
-    def _layer_for(self, p):
-        """The layer, which must not hold the scales of other weights (holding none, it says so itself)."""
-        if self._mx and self.layer.prepared not in (None, bytes(p.weights)):
+    def _uncaptured(self, p):
+        """Refuses other weights than those of a captured step: its replays read the layer's tables and scales."""
+        key = bytes(p.weights)
+        if self._captured not in (None, key):
+            raise B.MoeError(B.MOE_ERR_STATE, "MoEBlock: the layer keeps the weights of a captured step;")
+        return key
+
+    def _on_layer(self, p, call, *args):
+        """call(*args) of the layer, which must not hold the scales of other weights (holding none, it says so itself)."""
+        import torch
+        key = self._uncaptured(p)
+        if self.layer.prepared not in (None, key):
             raise B.MoeError(B.MOE_ERR_STATE, "MoEBlock: prepare(params) comes first, the layer holds other weights' scales;")
-        return self.layer
+        result = call(*args)
+        if torch.cuda.is_current_stream_capturing():
+            self._captured = key
+        return result
 
     def _routed(self, x, residual, p):
         import torch
@@ -85,9 +103,8 @@ class MoEBlock:
         on the current stream. What backward needs is kept until it, or the next forward."""
         if self.layer is None:
             raise ValueError("the block was made for decoding only (max_tokens 0)")
-        layer = self._layer_for(params)
         y, s, mean, rstd, logits, (ids, probs, counts, losses) = self._routed(x, residual, params)
-        out = layer.forward_topk(y, ids, probs, params.weights)
+        out = self._on_layer(params, self.layer.forward_topk, y, ids, probs, params.weights)
         self._kept = (params, y, s, mean, rstd, logits, ids, counts)
         return out, s, losses
 
@@ -101,9 +118,8 @@ class MoEBlock:
         p, y, s, mean, rstd, logits, ids, counts = self._kept
         if dout.shape != y.shape or dout.dtype != y.dtype or dout.device != y.device:
             raise ValueError("dout must be [T, H] bf16 on the block's device")
-        layer = self._layer_for(p)
+        dy, dprobs = self._on_layer(p, self.layer.backward, dout.contiguous(), main_grads)  # the layer takes compact rows
         self._kept = None
-        dy, dprobs = layer.backward(dout.contiguous(), main_grads)  # the layer takes compact rows
         dlogits = self.router.backward(logits, ids, dprobs, counts=counts, loss_grad=loss_grad)
         drouter = dlogits.t() @ y.to(dlogits.dtype)
         # one rounding of the sum of both paths to y
@@ -117,11 +133,12 @@ class MoEBlock:
         small = self.decoder is not None and x.shape[0] <= self.decode_tokens
         if not small and self.layer is None:
             raise ValueError(f"the block decodes up to {self.decode_tokens} tokens")
-        run = self.decoder if small else self._layer_for(params)
         y, s, _, _, _, (ids, probs, _, _) = self._routed(x, residual, params)
-        if not small:
-            self._kept = None  # the layer's saved state is overwritten
-        return run.forward_topk(y, ids, probs, params.weights), s
+        if small:
+            return self.decoder.forward_topk(y, ids, probs, params.weights), s
+        out = self._on_layer(params, self.layer.forward_topk, y, ids, probs, params.weights)
+        self._kept = None  # the layer's saved state is overwritten
+        return out, s
 
     def close(self):
         for part in (self.layer, self.decoder):

@@ -269,3 +269,34 @@ def test_mxfp8_experts():
     dx2, _ = block.backward(dout, m)
     assert torch.equal(dx, dx2) and all(torch.equal(mg[n], mg2[n]) for n in mg)
     M.MoEBlock(0, H, E, k, I, routed_wtype=B.MOE_W_MXFP8).prepare(p0)   # nothing to prepare
+
+
+@gpu
+@pytest.mark.parametrize("mx", [False, True])
+def test_a_captured_step_through_the_layer_keeps_its_weights(mx):
+    """More tokens than the decoder takes, captured: other weights through the layer are refused from then on, the same
+    ones and the decoder's are not, and replays give the captured weights' results."""
+    T, H, I, E, k = 24, 256, 128, 8, 2
+    made = [(mx_params(H, I, E, seed) if mx else params(H, I, E, torch.float32, False, seed)) for seed in (31, 32)]
+    (_, p0), (_, p1) = made
+    block = M.MoEBlock(T, H, E, k, I, decode_tokens=4, routed_wtype=B.MOE_W_MXFP8 if mx else B.MOE_W_BF16)
+    x = torch.randn(T, H, device="cuda", generator=torch.Generator(device="cuda").manual_seed(33)).bfloat16()
+    for p in (p1, p0):
+        block.prepare(p)
+        want, _ = block.decode(x, p)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, _ = block.decode(x, p0)
+    few, _ = block.decode(x[:4], p1)
+    for call in (lambda: block.decode(x, p1), lambda: block.forward(x, p1)) + ((lambda: block.prepare(p1),) if mx else ()):
+        with pytest.raises(M.MoeError) as e:
+            call()
+        assert e.value.status == B.MOE_ERR_STATE
+    assert torch.equal(block.decode(x, p0)[0], want)
+    block.prepare(p0)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert torch.equal(few, block.decode(x[:4], p1)[0])
