@@ -109,7 +109,8 @@ class MoEBlock:
         return out, s, losses
 
     def backward(self, dout, main_grads: B.moe_main_grads, ds=None, loss_grad=1.0):
-        """(dx, grads) for the gradients dout of out (bf16, any strides) and ds of s (None: zero) and loss_grad of the losses' sum.
+        """(dx, grads) for the gradients dout of out (bf16) and ds of s (x's type; None: zero), with any strides, and loss_grad of
+        the losses' sum.
         dx is that of x and of residual alike. grads: norm_weight, norm_bias (None without one) and
         router_weight; the experts' are added to main_grads."""
         import torch
@@ -118,6 +119,11 @@ class MoEBlock:
         p, y, s, mean, rstd, logits, ids, counts = self._kept
         if dout.shape != y.shape or dout.dtype != y.dtype or dout.device != y.device:
             raise ValueError("dout must be [T, H] bf16 on the block's device")
+        if ds is not None:  # looked at before anything is added to main_grads
+            if ds.shape != s.shape or ds.dtype != s.dtype or ds.device != s.device:
+                raise ValueError("ds must be [T, H] of x's type on the block's device")
+            if ds.stride(1) != 1 or ds.stride(0) < ds.shape[1]:
+                ds = ds.contiguous()
         dy, dprobs = self._on_layer(p, self.layer.backward, dout.contiguous(), main_grads)  # the layer takes compact rows
         self._kept = None
         dlogits = self.router.backward(logits, ids, dprobs, counts=counts, loss_grad=loss_grad)

@@ -300,3 +300,34 @@ def test_a_captured_step_through_the_layer_keeps_its_weights(mx):
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     assert torch.equal(few, block.decode(x[:4], p1)[0])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_stream_gradients_of_any_layout(dtype):
+    """ds transposed, broadcast, or with rows of a wider buffer: as the same values in compact rows. One of another shape,
+    type or place is refused before the experts' gradients are touched."""
+    T, H, I, E, k = 20, 256, 128, 8, 2
+    t, p = params(H, I, E, torch.float32, False, seed=6)
+    block = M.MoEBlock(T, H, E, k, I)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x, full, row = (torch.randn(n, H, generator=g, device="cuda").to(dtype) for n in (T, T, 1))
+    dout = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    mg = {n: torch.zeros(*t[n].shape, device="cuda") for n in ("shared1", "shared2", "fc1", "fc2")}
+    grads = M.main_grads_from_combined(mg["shared1"], mg["shared2"], mg["fc1"], mg["fc2"])
+
+    def step(ds):
+        block.forward(x, p)
+        before = [m.clone() for m in mg.values()]
+        other = torch.bfloat16 if dtype == torch.float32 else torch.float32
+        for bad in (ds[:-1], ds[:, :-8], ds.to(other), ds.cpu()):
+            with pytest.raises(ValueError):
+                block.backward(dout, grads, ds=bad)
+        assert all(torch.equal(a, b) for a, b in zip(before, mg.values()))
+        return block.backward(dout, grads, ds=ds)[0]
+
+    want = step(full)
+    wide = torch.zeros(T, H + 8, device="cuda", dtype=dtype)  # rows on 16 bytes: sums in the same order
+    wide[:, :H] = full
+    assert torch.equal(step(wide[:, :H]), want) and torch.equal(step(full.t().contiguous().t()), want)
+    assert torch.equal(step(row.expand(T, H)), step(row.repeat(T, 1)))
