@@ -359,15 +359,6 @@ def _on_one_device(first, *rest):
     return torch.cuda.device(index)
 
 
-def _call_on(current, index, call, args):
-    """call(*args) with device `index` as the current one; current(): the index of the one that is."""
-    if current() == index:
-        return call(*args)
-    import torch
-    with torch.cuda.device(index):
-        return call(*args)
-
-
 def _current_device_of():
     """A function: the index of the current CUDA device."""
     import torch
@@ -814,6 +805,9 @@ class MoEDecoder:
         if hidden.get_device() != index or topk_ids.get_device() != index or topk_probs.get_device() != index or \
                 out is not None and out.get_device() != index:
             raise ValueError("hidden, topk_ids, topk_probs and out must be on the decoder's device")
+        if self._current() != index:  # kernels go to the current device
+            with torch.cuda.device(index):
+                return self.forward_topk(hidden, topk_ids, topk_probs, weights, out)
         if hidden.dtype != torch.bfloat16 or H != self.hidden or hidden.stride(1) != 1:
             raise ValueError("hidden must be [T, H] bf16 with contiguous rows")
         if topk_ids.dtype != torch.int32 or topk_probs.dtype != torch.float32 or topk_ids.shape != slots or \
@@ -827,9 +821,8 @@ class MoEDecoder:
         if stream not in self._streams:
             self.workspace.record_stream(torch.cuda.current_stream(index))
             self._streams.add(stream)
-        args = (self.handle, T, hidden.data_ptr(), _ld(hidden), topk_ids.data_ptr(), topk_probs.data_ptr(), weights,
-                out.data_ptr(), _ld(out), stream)
-        status = _call_on(self._current, index, self._call, args)
+        status = self._call(self.handle, T, hidden.data_ptr(), _ld(hidden), topk_ids.data_ptr(), topk_probs.data_ptr(),
+                            weights, out.data_ptr(), _ld(out), stream)
         if status:
             raise MoeError(status, "moe_decode")
         return out
@@ -892,6 +885,9 @@ class MoENorm:
         if index < 0 or weight.get_device() != index or bias is not None and bias.get_device() != index or \
                 residual is not None and residual.get_device() != index:
             raise ValueError("the tensors must be on one CUDA device")
+        if self._current() != index:  # kernels go to the current device
+            with self._torch.cuda.device(index):
+                return self.forward(x, weight, bias, residual, out_dtype)
         if H != self.hidden or x.stride(1) != 1:
             raise ValueError("x must be [T, hidden] rows")
         self._vector(weight, wt)
@@ -911,10 +907,9 @@ class MoENorm:
             self._same(residual, shape, xt, "residual")
             s = empty(shape, dtype=xt, device=dev)
             res_at, res_ld, s_at, s_ld = residual.data_ptr(), _ld(residual), s.data_ptr(), H
-        args = (cfg, T, x.data_ptr(), x.stride(0) if T > 1 else H, res_at, res_ld, weight.data_ptr(),
-                None if bias is None else bias.data_ptr(), s_at, s_ld, y.data_ptr(), H, mean_at, rstd.data_ptr(),
-                self._stream(index))
-        status = _call_on(self._current, index, self._forward, args)
+        status = self._forward(cfg, T, x.data_ptr(), x.stride(0) if T > 1 else H, res_at, res_ld, weight.data_ptr(),
+                               None if bias is None else bias.data_ptr(), s_at, s_ld, y.data_ptr(), H, mean_at,
+                               rstd.data_ptr(), self._stream(index))
         if status:
             raise MoeError(status, "moe_norm_forward")
         return y, s, mean, rstd
@@ -943,6 +938,9 @@ class MoENorm:
                 mean is not None and mean.get_device() != index or dsum is not None and dsum.get_device() != index or \
                 dweight is not None and dweight.get_device() != index or dbias is not None and dbias.get_device() != index:
             raise ValueError("the tensors must be on one CUDA device")
+        if self._current() != index:
+            with torch.cuda.device(index):
+                return self.backward(dy, s, weight, mean, rstd, dsum, bias, dweight, dbias, accumulate)
         if dsum is not None:
             self._same(dsum, shape, st, "dsum")
         cfg = self._cfgs.get((st, yt, wt)) or self._cfg(st, yt, wt)
@@ -966,12 +964,11 @@ class MoENorm:
         size = _sized(moe_norm_backward_size, self._sizes, cfg, T)
         workspace = empty(size, dtype=torch.uint8, device=dev)
         many = T > 1  # a single row has no stride of its own
-        args = (cfg, T, dy.data_ptr(), dy.stride(0) if many else H, s.data_ptr(), s.stride(0) if many else H,
-                weight.data_ptr(), None if mean is None else mean.data_ptr(), rstd.data_ptr(), _addr(dsum),
-                0 if dsum is None else _ld(dsum), ds.data_ptr(), H, dweight.data_ptr(),
-                None if dbias is None else dbias.data_ptr(), MOE_G_FP32 if gt is f32 else MOE_G_BF16,
-                1 if accumulate else 0, workspace.data_ptr(), size, self._stream(index))
-        status = _call_on(self._current, index, self._backward, args)
+        status = self._backward(cfg, T, dy.data_ptr(), dy.stride(0) if many else H, s.data_ptr(), s.stride(0) if many else H,
+                                weight.data_ptr(), None if mean is None else mean.data_ptr(), rstd.data_ptr(), _addr(dsum),
+                                0 if dsum is None else _ld(dsum), ds.data_ptr(), H, dweight.data_ptr(),
+                                None if dbias is None else dbias.data_ptr(), MOE_G_FP32 if gt is f32 else MOE_G_BF16,
+                                1 if accumulate else 0, workspace.data_ptr(), size, self._stream(index))
         if status:
             raise MoeError(status, "moe_norm_backward")
         return ds, dweight, dbias
@@ -1013,6 +1010,9 @@ class MoERouter:
         dev, index = logits.device, logits.get_device()
         if index < 0 or select_bias is not None and select_bias.get_device() != index:
             raise ValueError("the tensors must be on one CUDA device")
+        if self._current() != index:  # kernels go to the current device
+            with torch.cuda.device(index):
+                return self.forward(logits, select_bias)
         if select_bias is not None and (select_bias.shape != (E,) or select_bias.dtype != f32 or select_bias.stride(0) != 1):
             raise ValueError("select_bias must be [E] fp32")
         slots = (T, self.k)
@@ -1022,11 +1022,10 @@ class MoERouter:
         losses = empty(2, dtype=f32, device=dev) if self.losses_wanted else None
         size = _sized(moe_router_size, self._sizes, cfg, T)
         workspace = empty(size, dtype=torch.uint8, device=dev)
-        args = (cfg, T, logits.data_ptr(), logits.stride(0) if T > 1 else E,
-                None if select_bias is None else select_bias.data_ptr(), ids.data_ptr(), probs.data_ptr(),
-                counts.data_ptr(), None if losses is None else losses.data_ptr(), workspace.data_ptr(), size,
-                self._stream(index))
-        status = _call_on(self._current, index, self._forward, args)
+        status = self._forward(cfg, T, logits.data_ptr(), logits.stride(0) if T > 1 else E,
+                               None if select_bias is None else select_bias.data_ptr(), ids.data_ptr(),
+                               probs.data_ptr(), counts.data_ptr(), None if losses is None else losses.data_ptr(),
+                               workspace.data_ptr(), size, self._stream(index))
         if status:
             raise MoeError(status, "moe_router_forward")
         return ids, probs, counts, losses
@@ -1048,10 +1047,12 @@ class MoERouter:
         if index < 0 or ids.get_device() != index or dprobs.get_device() != index or \
                 counts is not None and counts.get_device() != index:
             raise ValueError("the tensors must be on one CUDA device")
+        if self._current() != index:
+            with torch.cuda.device(index):
+                return self.backward(logits, ids, dprobs, counts, loss_grad)
         dlogits = torch.empty(shape, dtype=logits.dtype, device=logits.device)
-        args = (cfg, shape[0], logits.data_ptr(), _ld(logits), ids.data_ptr(), dprobs.data_ptr(), _addr(counts),
-                float(loss_grad), dlogits.data_ptr(), self.E, self._stream(index))
-        status = _call_on(self._current, index, self._backward, args)
+        status = self._backward(cfg, shape[0], logits.data_ptr(), _ld(logits), ids.data_ptr(), dprobs.data_ptr(),
+                                _addr(counts), float(loss_grad), dlogits.data_ptr(), self.E, self._stream(index))
         if status:
             raise MoeError(status, "moe_router_backward")
         return dlogits
