@@ -528,6 +528,90 @@ moe_status moe_router_backward(const moe_router_config* cfg, int64_t T, const vo
                                const int32_t* ids, const float* dprobs, const int32_t* counts, float loss_grad,
                                void* dlogits, int64_t dlogits_stride, void* stream);
 
+/* ---- Dense layers in 8-bit floating point ----
+ * A matrix is held as E4M3 codes with one fp32 scale for a block of 128: value = code * scale (rounded to fp32 where it
+ * is read as a number, exact inside the products).
+ * A block's scale is max(amax / 448, 2^-126) in fp32, amax the block's largest magnitude; a value's code is
+ * the E4M3 number nearest (ties to even, saturating at +-448) to its fp32 product with the scale's fp32
+ * reciprocal. Blocks at the edges are the smaller. A NaN becomes the NaN code in its own place; an infinity
+ * makes its whole block NaN.
+ *   MOE_B_ROW     blocks of 128 along a row        scales [ceil(cols/128), rows]   (a product along the columns)
+ *   MOE_B_COL     blocks of 128 down a column      scales [ceil(rows/128), cols]   (a product along the rows)
+ *   MOE_B_SQUARE  blocks of 128 x 128              scales [ceil(rows/128), ceil(cols/128)]   (a weight, both ways)
+ * (This is not the layer's MXFP8, whose blocks are of 32 and whose scales are powers of two.)
+ * Sums over a block of 128 are the tensor cores' fp32 ones, and their scaled sum is fp32 as well.
+ * A wait inside a product that gave up (2 s) leaves NaN in its results. */
+typedef enum { MOE_B_ROW = 0, MOE_B_COL = 1, MOE_B_SQUARE = 2 } moe_block;
+typedef struct {
+    void* q;       /* codes [rows, cols], 16-byte aligned */
+    int64_t ld;    /* row stride in bytes, a multiple of 16; bytes of a row past cols are never written */
+    float* scales; /* compact, shape above */
+} moe_fp8;
+
+/* Codes and scales of x[rows, cols] (x_type, any alignment, row stride x_stride >= cols in elements): any of the
+ * three is NULL where it is not wanted, and several are made from one reading of x. 0 <= rows <= 2^24,
+ * 1 <= cols <= 2^20. */
+moe_status moe_fp8_quantize(const void* x, int32_t x_type, int64_t rows, int64_t cols, int64_t x_stride,
+                            const moe_fp8* row, const moe_fp8* col, const moe_fp8* square, void* stream);
+
+/* out[rows, cols] = code * scale, rounded to out_type; `block` (moe_block) is v's. */
+moe_status moe_fp8_dequantize(const moe_fp8* v, int32_t block, int64_t rows, int64_t cols, void* out,
+                              int32_t out_type, int64_t out_stride, void* stream);
+
+/* A linear layer y = x W^T whose products are of 8-bit numbers: W[out_features, in_features] square blocks.
+ * Features 1 .. 2^20, 0 <= T <= 2^24. */
+typedef struct {
+    int64_t in_features, out_features;
+    int32_t x_type;  /* moe_dtype of x and dx */
+    int32_t y_type;  /* moe_dtype of y and dy */
+} moe_linear_config;
+
+/* Bytes of device workspace (256-byte aligned) that a call for T rows needs; calls that share one must be ordered. */
+moe_status moe_linear_size(const moe_linear_config* cfg, int64_t T, int32_t backward, size_t* bytes);
+
+/* y[T, out] = Qrow(x) W^T. `kept` (NULL: none): column blocks of x [T, in], the 8-bit copy of x that the backward
+ * takes in its place. Rows of x and y may have any stride and alignment of their type. y must not overlap x. */
+moe_status moe_linear_forward(const moe_linear_config* cfg, int64_t T, const void* x, int64_t x_stride, const moe_fp8* w,
+                              void* y, int64_t y_stride, const moe_fp8* kept, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* dx[T, in] = Qrow(dy) W (NULL: not computed); dweight[out, in] = Qcol(dy)^T kept (NULL: not computed), written
+ * (accumulate 0) or added (1) to a buffer of g_type (moe_gtype: fp32, or bf16 as the layer's main_grads).
+ * The sums' order depends on the sizes and the GPU's number of SMs alone. */
+moe_status moe_linear_backward(const moe_linear_config* cfg, int64_t T, const void* dy, int64_t dy_stride, const moe_fp8* w,
+                               const moe_fp8* kept, void* dx, int64_t dx_stride, void* dweight, int64_t dweight_stride,
+                               int32_t g_type, int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gated feed-forward network of a dense block, its products of 8-bit numbers:
+ *   g = Qrow(x) Wg^T, u = Qrow(x) Wu^T, h = silu(g) u, y = Qrow(h) Wd^T
+ * with bf16 x, y [T, hidden], square-block weights Wg, Wu [inter, hidden] and Wd [hidden, inter], and with
+ * swiglu_limit L > 0 the layer's clamp, h = silu(min(g, L)) min(max(u, -L), L). hidden and inter 1 .. 2^20. */
+typedef struct {
+    int64_t hidden, inter;
+    float swiglu_limit;
+} moe_ffn_config;
+typedef struct { moe_fp8 gate, up, down; } moe_ffn_weights;
+/* What the backward takes: column blocks of x [T, hidden], and row blocks of g and u [T, inter], before the clamp. */
+typedef struct { moe_fp8 x, gate, up; } moe_ffn_kept;
+typedef struct { void *gate, *up, *down; int64_t gate_stride, up_stride, down_stride; } moe_ffn_grads;
+
+moe_status moe_ffn_size(const moe_ffn_config* cfg, int64_t T, int32_t backward, size_t* bytes);
+
+/* kept NULL: nothing is kept. y must not overlap x. */
+moe_status moe_ffn_forward(const moe_ffn_config* cfg, int64_t T, const void* x, int64_t x_stride, const moe_ffn_weights* w,
+                           void* y, int64_t y_stride, const moe_ffn_kept* kept, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* At the kept x, g, u and h = silu(g) u of them:
+ *   dh = Qrow(dy) Wd, dg = dh u silu'(g), du = dh silu(g) (with the clamp: 0 where g > L, where |u| > L)
+ *   dx = Qrow(dg) Wg + Qrow(du) Wu
+ *   grads: gate Qcol(dg)^T x, up Qcol(du)^T x [inter, hidden], down Qcol(dy)^T Qcol(h) [hidden, inter], written or added
+ *   as moe_linear_backward's dweight.
+ * dx NULL, grads NULL: not computed. */
+moe_status moe_ffn_backward(const moe_ffn_config* cfg, int64_t T, const void* dy, int64_t dy_stride, const moe_ffn_weights* w,
+                            const moe_ffn_kept* kept, void* dx, int64_t dx_stride, const moe_ffn_grads* grads,
+                            int32_t g_type, int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Number of kernels this library has launched in this process. */
 uint64_t moe_launch_count(void);
 

@@ -14,6 +14,8 @@ from .binding import (HostPipe, MoEDecoder, MoELayer, MoENorm, MoERouter, MoeErr
                       moe_decode, moe_decode_create, moe_decode_destroy, moe_decode_size, moe_decode_status,
                       moe_norm_backward, moe_norm_backward_size, moe_norm_config, moe_norm_forward,
                       moe_router_backward, moe_router_config, moe_router_forward, moe_router_size,
+                      MOE_B_COL, MOE_B_ROW, MOE_B_SQUARE, FeedForwardWeights, MoEFeedForward, MoEFp8Linear, fp8_dequantize, fp8_quantize,
+                      fp8_scales_shape, moe_ffn_config, moe_ffn_size, moe_linear_config, moe_linear_size,
                       weights_from_combined_mxfp8)
 from .block import BlockParams, MoEBlock
 
@@ -28,4 +30,6 @@ __all__ = ["BlockParams", "HostPipe", "MoEBlock", "MoEDecoder", "MoELayer", "MoE
            "moe_decode", "moe_decode_create", "moe_decode_destroy", "moe_decode_size", "moe_decode_status",
            "moe_norm_backward", "moe_norm_backward_size", "moe_norm_config", "moe_norm_forward",
            "moe_router_backward", "moe_router_config", "moe_router_forward", "moe_router_size",
+           "MOE_B_COL", "MOE_B_ROW", "MOE_B_SQUARE", "FeedForwardWeights", "MoEFeedForward", "MoEFp8Linear", "fp8_dequantize", "fp8_quantize",
+           "fp8_scales_shape", "moe_ffn_config", "moe_ffn_size", "moe_linear_config", "moe_linear_size",
            "weights_from_combined_mxfp8"]

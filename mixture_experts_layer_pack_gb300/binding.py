@@ -25,6 +25,7 @@ MOE_DECODE_TABLE_SETS = 64           # sets of per-expert tables that a decoder 
 MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
 MOE_T_BF16, MOE_T_FP32 = 0, 1       # element types of the norm's and the router's tensors (moe_dtype)
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_B_ROW, MOE_B_COL, MOE_B_SQUARE = 0, 1, 2   # blocks of an 8-bit matrix's scales (moe_block)
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_ROUTING",
                 4: "MOE_ERR_CUDA", 5: "MOE_ERR_TIMEOUT", 6: "MOE_ERR_STATE"}
 WEIGHT_NAMES = ("shared_gate", "shared_up", "shared_down", "routed_gate", "routed_up", "routed_down")
@@ -60,6 +61,31 @@ class moe_router_config(ctypes.Structure):
                 ("scale", c_float), ("aux_coeff", c_float), ("z_coeff", c_float), ("x_type", c_int32)]
 
 
+class moe_fp8(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("ld", c_int64), ("scales", c_void_p)]
+
+
+class moe_linear_config(ctypes.Structure):
+    _fields_ = [("in_features", c_int64), ("out_features", c_int64), ("x_type", c_int32), ("y_type", c_int32)]
+
+
+class moe_ffn_config(ctypes.Structure):
+    _fields_ = [("hidden", c_int64), ("inter", c_int64), ("swiglu_limit", c_float)]
+
+
+class moe_ffn_weights(ctypes.Structure):
+    _fields_ = [("gate", moe_fp8), ("up", moe_fp8), ("down", moe_fp8)]
+
+
+class moe_ffn_kept(ctypes.Structure):
+    _fields_ = [("x", moe_fp8), ("gate", moe_fp8), ("up", moe_fp8)]
+
+
+class moe_ffn_grads(ctypes.Structure):
+    _fields_ = [("gate", c_void_p), ("up", c_void_p), ("down", c_void_p), ("gate_stride", c_int64), ("up_stride", c_int64),
+                ("down_stride", c_int64)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -76,7 +102,9 @@ EXPORTED = ("moe_workspace_size", "moe_create", "moe_destroy", "moe_saved_size",
             "moe_host_pipe_sync", "moe_host_pipe_destroy", "moe_selftest_timeout",
             "moe_decode_size", "moe_decode_create", "moe_decode_destroy", "moe_decode", "moe_decode_status",
             "moe_norm_forward", "moe_norm_backward_size", "moe_norm_backward",
-            "moe_router_size", "moe_router_forward", "moe_router_backward")
+            "moe_router_size", "moe_router_forward", "moe_router_backward",
+            "moe_fp8_quantize", "moe_fp8_dequantize", "moe_linear_size", "moe_linear_forward", "moe_linear_backward",
+            "moe_ffn_size", "moe_ffn_forward", "moe_ffn_backward")
 MOE_K_COUNT = 20
 
 
@@ -150,6 +178,20 @@ def load(build_if_missing: bool = True):
         L.moe_router_size.argtypes = [P(moe_router_config), c_int64, P(c_size_t)]
         L.moe_router_forward.argtypes = [P(moe_router_config), c_int64, V, c_int64, V, V, V, V, V, V, c_size_t, V]
         L.moe_router_backward.argtypes = [P(moe_router_config), c_int64, V, c_int64, V, V, V, c_float, V, c_int64, V]
+        I64, I32 = c_int64, c_int32
+        L.moe_fp8_quantize.argtypes = [V, I32, I64, I64, I64, P(moe_fp8), P(moe_fp8), P(moe_fp8), V]
+        L.moe_fp8_dequantize.argtypes = [P(moe_fp8), I32, I64, I64, V, I32, I64, V]
+        L.moe_linear_size.argtypes = [P(moe_linear_config), I64, I32, P(c_size_t)]
+        L.moe_linear_forward.argtypes = [P(moe_linear_config), I64, V, I64, P(moe_fp8), V, I64, P(moe_fp8), V, c_size_t, V]
+        L.moe_linear_backward.argtypes = [P(moe_linear_config), I64, V, I64, P(moe_fp8), P(moe_fp8), V, I64, V, I64, I32, I32,
+                                          V, c_size_t, V]
+        L.moe_ffn_size.argtypes = [P(moe_ffn_config), I64, I32, P(c_size_t)]
+        L.moe_ffn_forward.argtypes = [P(moe_ffn_config), I64, V, I64, P(moe_ffn_weights), V, I64, P(moe_ffn_kept), V, c_size_t, V]
+        L.moe_ffn_backward.argtypes = [P(moe_ffn_config), I64, V, I64, P(moe_ffn_weights), P(moe_ffn_kept), V, I64,
+                                       P(moe_ffn_grads), I32, I32, V, c_size_t, V]
+        for name in ("moe_fp8_quantize", "moe_fp8_dequantize", "moe_linear_size", "moe_linear_forward", "moe_linear_backward",
+                     "moe_ffn_size", "moe_ffn_forward", "moe_ffn_backward"):
+            getattr(L, name).restype = c_int32
         for name in ("moe_decode_size", "moe_decode_create", "moe_decode", "moe_decode_status", "moe_norm_forward",
                      "moe_norm_backward_size", "moe_norm_backward", "moe_router_size", "moe_router_forward",
                      "moe_router_backward"):
@@ -461,6 +503,18 @@ def moe_router_backward(cfg: moe_router_config, logits, ids, dprobs, dlogits, co
         _check(load().moe_router_backward(cfg, logits.shape[0], logits.data_ptr(), _ld(logits), ids.data_ptr(),
                                           dprobs.data_ptr(), _addr(counts), loss_grad, dlogits.data_ptr(),
                                           _ld(dlogits), _raw_stream(stream, logits.device)), "moe_router_backward")
+
+
+def moe_linear_size(cfg: moe_linear_config, T: int, backward=False) -> int:
+    n = c_size_t(0)
+    _check(load().moe_linear_size(cfg, T, 1 if backward else 0, ctypes.byref(n)), "moe_linear_size")
+    return n.value
+
+
+def moe_ffn_size(cfg: moe_ffn_config, T: int, backward=False) -> int:
+    n = c_size_t(0)
+    _check(load().moe_ffn_size(cfg, T, 1 if backward else 0, ctypes.byref(n)), "moe_ffn_size")
+    return n.value
 
 
 def moe_launch_count() -> int:
@@ -1056,3 +1110,310 @@ class MoERouter:
         if status:
             raise MoeError(status, "moe_router_backward")
         return dlogits
+
+
+# ------------------------------------------------------------------ dense layers in 8-bit floating point
+def fp8_scales_shape(rows, cols, block):
+    """Shape of the scales of an 8-bit [rows, cols] matrix (include/moe.h, moe_block)."""
+    r, c = -(-rows // 128), -(-cols // 128)
+    return (c, rows) if block == MOE_B_ROW else (r, cols) if block == MOE_B_COL else (r, c)
+
+
+def _new_codes(torch, rows, cols, block, device):
+    """A new (codes, scales) pair: codes uint8 [rows, cols] whose row stride is a multiple of 16."""
+    ld = (cols + 15) // 16 * 16
+    q = torch.empty((rows, ld), dtype=torch.uint8, device=device)
+    return (q if ld == cols else q[:, :cols]), torch.empty(fp8_scales_shape(rows, cols, block), dtype=torch.float32, device=device)
+
+
+def _codes(torch, pair, rows, cols, block, index, what) -> moe_fp8:
+    """The moe_fp8 of a (codes, scales) pair of the given size on the device `index`."""
+    q, s = pair
+    ld = q.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+    if q.dtype is not torch.uint8 or q.shape != (rows, cols) or cols > 1 and q.stride(1) != 1 or ld % 16 or ld < cols or \
+            s.dtype is not torch.float32 or s.shape != fp8_scales_shape(rows, cols, block) or not s.is_contiguous():
+        raise ValueError(f"{what} must be (codes, scales): uint8 [{rows}, {cols}] with a row stride of a multiple of 16, and contiguous "
+                         f"fp32 {list(fp8_scales_shape(rows, cols, block))}")
+    if q.get_device() != index or s.get_device() != index:
+        raise ValueError("the tensors must be on one CUDA device")
+    return moe_fp8(q.data_ptr(), ld, s.data_ptr())
+
+
+_FP8_TYPES = {}
+
+
+def _fp8_types(torch):
+    if not _FP8_TYPES:
+        _FP8_TYPES.update({torch.bfloat16: MOE_T_BF16, torch.float32: MOE_T_FP32})
+    return _FP8_TYPES
+
+
+def _as_rows(t, what):
+    """t, a 2-D tensor of bf16 or fp32 rows, with contiguous elements in them."""
+    if t.dim() != 2 or t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{what} must be rows with contiguous elements, bf16 or fp32")
+
+
+def fp8_quantize(x, block, out=None, stream=None):
+    """(codes, scales) of x [rows, cols] (bf16 or fp32, rows of any stride) in blocks of 128: MOE_B_ROW along its rows, MOE_B_COL
+    down its columns, MOE_B_SQUARE both (a weight). codes uint8 [rows, cols] (E4M3), scales fp32 of fp8_scales_shape(rows,
+    cols, block); `out`: a pair to write. An activation kept like this for a later pass takes half of its bf16 bytes.
+    `stream`: where (the current stream)."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_quantize(x, block, out)
+    _as_rows(x, "x")
+    xt = _fp8_types(torch).get(x.dtype)
+    if xt is None or block not in (MOE_B_ROW, MOE_B_COL, MOE_B_SQUARE):
+        raise ValueError("x must be bf16 or fp32, and block one of MOE_B_ROW, MOE_B_COL, MOE_B_SQUARE")
+    with _on_one_device(x):
+        rows, cols = x.shape
+        pair = _new_codes(torch, rows, cols, block, x.device) if out is None else out
+        at = [None, None, None]
+        at[block] = _codes(torch, pair, rows, cols, block, x.get_device(), "out")
+        _check(load().moe_fp8_quantize(x.data_ptr(), xt, rows, cols, _ld(x), *at, _raw_stream(None, x.device)), "moe_fp8_quantize")
+    return pair
+
+
+def fp8_dequantize(codes, scales, block, dtype=None, out=None, stream=None):
+    """The values [rows, cols] that codes and scales stand for, in `dtype` (bf16 by default) or the type of `out`."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_dequantize(codes, scales, block, dtype, out)
+    with _on_one_device(codes, scales, out):
+        rows, cols = codes.shape
+        if out is None:
+            out = torch.empty((rows, cols), dtype=torch.bfloat16 if dtype is None else dtype, device=codes.device)
+        _as_rows(out, "out")
+        yt = _fp8_types(torch).get(out.dtype)
+        if yt is None or out.shape != codes.shape or dtype not in (None, out.dtype) or block not in (MOE_B_ROW, MOE_B_COL, MOE_B_SQUARE):
+            raise ValueError("out must be bf16 or fp32 of the codes' shape, and block one of MOE_B_ROW, MOE_B_COL, MOE_B_SQUARE")
+        v = _codes(torch, (codes, scales), rows, cols, block, codes.get_device(), "codes and scales")
+        _check(load().moe_fp8_dequantize(v, block, rows, cols, out.data_ptr(), yt, _ld(out), _raw_stream(None, codes.device)),
+               "moe_fp8_dequantize")
+    return out
+
+
+def _grad_buffer(t, shape, what):
+    """moe_gtype of a weight's gradient buffer."""
+    _as_rows(t, what)
+    if t.shape != shape:
+        raise ValueError(f"{what} must be {list(shape)}")
+
+
+class MoEFp8Linear:
+    """y = x W^T with 8-bit products, a scale for each block of 128 (include/moe.h, moe_linear_forward). A weight is a (codes, scales)
+    pair of fp8_quantize(w, MOE_B_SQUARE), w [out_features, in_features]."""
+
+    def __init__(self, in_features, out_features, device="cuda"):
+        import torch
+        self.K, self.N, self.device = int(in_features), int(out_features), torch.device(device)
+        self._torch, self._stream, self._current = torch, _current_stream_of(), _current_device_of()
+        self._cfgs, self._sizes, self._back_sizes = {}, {}, {}
+        self._forward, self._backward = load().moe_linear_forward, load().moe_linear_backward
+        moe_linear_size(self._cfg(torch.bfloat16, torch.bfloat16), 0)   # the library's check of the configuration
+
+    def _cfg(self, xt, yt):
+        c = self._cfgs.get((xt, yt))
+        if c is None:
+            types = _fp8_types(self._torch)
+            _require(xt in types and yt in types, "tensors must be bf16 or fp32")
+            c = self._cfgs[xt, yt] = moe_linear_config(self.K, self.N, types[xt], types[yt])
+        return c
+
+    @_on_stream
+    def forward(self, x, weight, keep=True, out_dtype=None):
+        """(y, kept): y [T, out] in out_dtype (x's by default) of x [T, in] bf16 or fp32; kept, what backward takes in x's place, is
+        x in 8 bits, column blocks (None without `keep`). `stream`: where (the current stream)."""
+        torch = self._torch
+        T, K = x.shape
+        index = x.get_device()
+        if index < 0:
+            raise ValueError("the tensors must be on one CUDA device")
+        if self._current() != index:  # kernels go to the current device
+            with torch.cuda.device(index):
+                return self.forward(x, weight, keep, out_dtype)
+        if K != self.K:
+            raise ValueError("x must be [T, in_features] rows")
+        _as_rows(x, "x")
+        xt, dev = x.dtype, x.device
+        yt = xt if out_dtype is None else out_dtype
+        cfg = self._cfgs.get((xt, yt)) or self._cfg(xt, yt)
+        w = _codes(torch, weight, self.N, K, MOE_B_SQUARE, index, "weight")
+        y = torch.empty((T, self.N), dtype=yt, device=dev)
+        kept = _new_codes(torch, T, K, MOE_B_COL, dev) if keep else None
+        size = _sized(moe_linear_size, self._sizes, cfg, T)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        status = self._forward(cfg, T, x.data_ptr(), _ld(x), w, y.data_ptr(), self.N,
+                               _codes(torch, kept, T, K, MOE_B_COL, index, "kept") if keep else None, workspace.data_ptr(), size,
+                               self._stream(index))
+        if status:
+            raise MoeError(status, "moe_linear_forward")
+        return y, kept
+
+    @_on_stream
+    def backward(self, dy, weight, kept, dx_dtype=None, dweight=None, accumulate=False, need_dx=True, need_dweight=True):
+        """(dx, dweight) for the gradient dy [T, out] of y and the forward's `kept`: dx [T, in] in dx_dtype (dy's by default), dweight
+        [out, in], a new fp32 matrix or the given fp32 / bf16 buffer, overwritten or (accumulate) added to. What is not
+        needed is None. `stream`: where (the current stream)."""
+        torch = self._torch
+        T, N = dy.shape
+        index = dy.get_device()
+        if index < 0 or dweight is not None and dweight.get_device() != index:
+            raise ValueError("the tensors must be on one CUDA device")
+        if self._current() != index:
+            with torch.cuda.device(index):
+                return self.backward(dy, weight, kept, dx_dtype, dweight, accumulate, need_dx, need_dweight)
+        if N != self.N:
+            raise ValueError("dy must be [T, out_features] rows")
+        _as_rows(dy, "dy")
+        if accumulate and dweight is None:
+            raise ValueError("accumulate adds to a given buffer")
+        if dweight is not None and not need_dweight:
+            raise ValueError("a buffer for a gradient that is not needed")
+        yt, dev, K = dy.dtype, dy.device, self.K
+        xt = yt if dx_dtype is None else dx_dtype
+        cfg = self._cfgs.get((xt, yt)) or self._cfg(xt, yt)
+        w = _codes(torch, weight, N, K, MOE_B_SQUARE, index, "weight") if need_dx else None
+        k = _codes(torch, kept, T, K, MOE_B_COL, index, "kept") if need_dweight else None
+        dx = torch.empty((T, K), dtype=xt, device=dev) if need_dx else None
+        gt = MOE_G_FP32
+        if need_dweight:
+            if dweight is None:
+                dweight = torch.empty((N, K), dtype=torch.float32, device=dev)
+            else:
+                _grad_buffer(dweight, (N, K), "dweight")
+                gt = _fp8_types(torch).get(dweight.dtype)
+                if gt is None:
+                    raise ValueError("dweight must be fp32 or bf16")
+                gt = MOE_G_BF16 if gt == MOE_T_BF16 else MOE_G_FP32
+        size = _sized(_linear_back_size, self._back_sizes, cfg, T)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        status = self._backward(cfg, T, dy.data_ptr(), _ld(dy), w, k, _addr(dx), K, _addr(dweight), _ld(dweight) if need_dweight else 0,
+                                gt, 1 if accumulate else 0, workspace.data_ptr(), size, self._stream(index))
+        if status:
+            raise MoeError(status, "moe_linear_backward")
+        return dx, dweight
+
+
+def _linear_back_size(cfg, T):
+    return moe_linear_size(cfg, T, True)
+
+
+def _ffn_back_size(cfg, T):
+    return moe_ffn_size(cfg, T, True)
+
+
+class FeedForwardWeights:
+    """The weights of a MoEFeedForward: (codes, scales) pairs of fp8_quantize(w, MOE_B_SQUARE), gate and up [inter, hidden], down
+    [hidden, inter]. It holds the tensors; their contents may change, their places may not."""
+
+    def __init__(self, gate, up, down):
+        import torch
+        I, H = gate[0].shape
+        index = gate[0].get_device()
+        self.tensors = (gate, up, down)
+        self.hidden, self.inter, self.index = H, I, index
+        self.views = moe_ffn_weights(_codes(torch, gate, I, H, MOE_B_SQUARE, index, "gate"),
+                                     _codes(torch, up, I, H, MOE_B_SQUARE, index, "up"),
+                                     _codes(torch, down, H, I, MOE_B_SQUARE, index, "down"))
+
+
+class MoEFeedForward:
+    """The gated feed-forward network of a dense block with 8-bit products (include/moe.h, moe_ffn_forward):
+    y = (silu(x Wg^T) (x Wu^T)) Wd^T, with the layer's clamp where swiglu_limit > 0."""
+
+    def __init__(self, hidden, inter, swiglu_limit=0.0, device="cuda"):
+        import torch
+        self.cfg = moe_ffn_config(int(hidden), int(inter), float(swiglu_limit))
+        self.H, self.I, self.device = int(hidden), int(inter), torch.device(device)
+        self._torch, self._stream, self._current = torch, _current_stream_of(), _current_device_of()
+        self._sizes, self._back_sizes = {}, {}
+        self._forward, self._backward = load().moe_ffn_forward, load().moe_ffn_backward
+        moe_ffn_size(self.cfg, 0)   # the library's check of the configuration
+
+    def _weights(self, weights, index):
+        if weights.hidden != self.H or weights.inter != self.I:
+            raise ValueError("the weights are of another size")
+        if index < 0 or weights.index != index:
+            raise ValueError("the tensors must be on one CUDA device")
+        return weights.views
+
+    @_on_stream
+    def forward(self, x, weights: FeedForwardWeights, keep=True):
+        """(y, kept): y [T, hidden] bf16 of x [T, hidden] bf16 (rows of any stride); kept, what backward takes: x, g and u in 8 bits,
+        three (codes, scales) pairs in column, row and row blocks (None without `keep`). `stream`: where (the current stream)."""
+        torch = self._torch
+        T, H = x.shape
+        index = x.get_device()
+        w = self._weights(weights, index)
+        if self._current() != index:  # kernels go to the current device
+            with torch.cuda.device(index):
+                return self.forward(x, weights, keep)
+        if H != self.H or x.dtype != torch.bfloat16:
+            raise ValueError("x must be [T, hidden] bf16 rows")
+        _as_rows(x, "x")
+        dev, I = x.device, self.I
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        kept = views = None
+        if keep:
+            kept = (_new_codes(torch, T, H, MOE_B_COL, dev), _new_codes(torch, T, I, MOE_B_ROW, dev), _new_codes(torch, T, I, MOE_B_ROW, dev))
+            views = self._kept(kept, T, index)
+        size = _sized(moe_ffn_size, self._sizes, self.cfg, T)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        status = self._forward(self.cfg, T, x.data_ptr(), _ld(x), w, y.data_ptr(), H, views, workspace.data_ptr(), size, self._stream(index))
+        if status:
+            raise MoeError(status, "moe_ffn_forward")
+        return y, kept
+
+    def _kept(self, kept, T, index):
+        torch = self._torch
+        return moe_ffn_kept(_codes(torch, kept[0], T, self.H, MOE_B_COL, index, "kept x"),
+                            _codes(torch, kept[1], T, self.I, MOE_B_ROW, index, "kept gate"),
+                            _codes(torch, kept[2], T, self.I, MOE_B_ROW, index, "kept up"))
+
+    @_on_stream
+    def backward(self, dy, weights: FeedForwardWeights, kept, grads=None, accumulate=False, need_dx=True, need_grads=True):
+        """(dx, (dgate, dup, ddown)) for the gradient dy [T, hidden] bf16 of y and the forward's `kept`: dx bf16, the weights' gradients
+        new fp32 matrices or the given ones (`grads`: three buffers, all fp32 or all bf16), overwritten or (accumulate)
+        added to. What is not needed is None. `stream`: where (the current stream)."""
+        torch = self._torch
+        T, H = dy.shape
+        index = dy.get_device()
+        w = self._weights(weights, index)
+        if self._current() != index:
+            with torch.cuda.device(index):
+                return self.backward(dy, weights, kept, grads, accumulate, need_dx, need_grads)
+        if H != self.H or dy.dtype != torch.bfloat16:
+            raise ValueError("dy must be [T, hidden] bf16 rows")
+        _as_rows(dy, "dy")
+        if accumulate and grads is None:
+            raise ValueError("accumulate adds to given buffers")
+        if grads is not None and not need_grads:
+            raise ValueError("buffers for gradients that are not needed")
+        dev, I = dy.device, self.I
+        views = self._kept(kept, T, index)
+        dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if need_dx else None
+        at, gt = None, MOE_G_FP32
+        if need_grads:
+            shapes = ((I, H), (I, H), (H, I))
+            if grads is None:
+                grads = tuple(torch.empty(n, dtype=torch.float32, device=dev) for n in shapes)
+            for t, n, what in zip(grads, shapes, ("dgate", "dup", "ddown")):
+                _grad_buffer(t, n, what)
+                if t.get_device() != index:
+                    raise ValueError("the tensors must be on one CUDA device")
+            dtypes = {t.dtype for t in grads}
+            if dtypes not in ({torch.float32}, {torch.bfloat16}) or len(grads) != 3:
+                raise ValueError("grads must be three buffers, all fp32 or all bf16")
+            gt = MOE_G_BF16 if torch.bfloat16 in dtypes else MOE_G_FP32
+            at = moe_ffn_grads(*[t.data_ptr() for t in grads], *[_ld(t) for t in grads])
+        size = _sized(_ffn_back_size, self._back_sizes, self.cfg, T)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        status = self._backward(self.cfg, T, dy.data_ptr(), _ld(dy), w, views, _addr(dx), H, at, gt, 1 if accumulate else 0,
+                                workspace.data_ptr(), size, self._stream(index))
+        if status:
+            raise MoeError(status, "moe_ffn_backward")
+        return dx, grads

@@ -1,0 +1,791 @@
+// Dense layers in 8-bit floating point with one fp32 scale for a block of 128: the codes, the pieces between the
+// products (fp8_gemm.cu), and the calls.
+#include "fp8.h"
+#include "fp8_device.cuh"
+#include "internal.h"
+
+#include <algorithm>
+#include <cmath>
+
+namespace moe {
+
+namespace {
+
+constexpr int64_t kMostRows = int64_t(1) << 24, kMostCols = int64_t(1) << 20;
+constexpr int kQuantThreads = 256;
+constexpr int kGatedThreads = 512;
+
+struct Codes {          // codes and compact scales; q null: not wanted
+    uint8_t* q;
+    int64_t ld;
+    float* s;
+};
+
+// ---------------------------------------------------------------- reading and writing eight columns
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, int n, bool wide, float (&v)[8]) {
+    if (wide && n >= 8) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+        unpack_bf16x2(w.x, v[0], v[1]), unpack_bf16x2(w.y, v[2], v[3]);
+        unpack_bf16x2(w.z, v[4], v[5]), unpack_bf16x2(w.w, v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? __bfloat162float(p[j]) : 0.0f;
+    }
+}
+__device__ __forceinline__ void load8(const float* p, int n, bool wide, float (&v)[8]) {
+    if (wide && n >= 8) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? p[j] : 0.0f;
+    }
+}
+
+// eight codes of a row (8-byte aligned); its bytes past n are not ours
+__device__ __forceinline__ void store8(uint8_t* p, int n, uint32_t lo, uint32_t hi) {
+    if (n >= 8) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) p[j] = uint8_t((j < 4 ? lo : hi) >> (8 * (j & 3)));
+    }
+}
+
+__device__ __forceinline__ float most8(const float (&v)[8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+    return m;
+}
+
+__device__ __forceinline__ float most_of16(float m) {  // over 16 lanes that share a row
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    return m;
+}
+
+__device__ __forceinline__ void put8(uint8_t* p, int n, const float (&v)[8], const float (&r)[8]) {
+    store8(p, n, e4m3x4(v[0] * r[0], v[1] * r[1], v[2] * r[2], v[3] * r[3]), e4m3x4(v[4] * r[4], v[5] * r[5], v[6] * r[6], v[7] * r[7]));
+}
+__device__ __forceinline__ void put8(uint8_t* p, int n, const float (&v)[8], float r) {
+    store8(p, n, e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r));
+}
+
+// ---------------------------------------------------------------- codes of a matrix
+// A block takes 128 x 128 elements, which it reads once and holds in registers: 16 threads a row with eight columns
+// each, a thread eight rows 16 apart. Rows' maxima go through 16 lanes, columns' through registers and shared memory.
+template <typename X>
+__global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const X* __restrict__ x, int64_t rows, int cols, int64_t ld, bool wide,
+                                                                     Codes row, Codes col, Codes square) {
+    constexpr int W = kQuantThreads / 32;
+    __shared__ float part[W][128];
+    __shared__ float scale[128], inv[128], row_scale[128];
+    pdl_wait();
+    pdl_trigger();
+    const int col_blocks = (cols + 127) >> 7;
+    const int64_t rb = blockIdx.x / col_blocks;
+    const int cb = int(blockIdx.x - rb * col_blocks);
+    const int c8 = threadIdx.x & 15, rg = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c0 = cb * 128 + c8 * 8, n = cols - c0;  // n columns of this thread's (8 or more: all)
+    float v[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = rb * 128 + rg + 16 * i;
+        if (r < rows && n > 0)
+            load8(x + r * ld + c0, n, wide, v[i]);
+        else
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    }
+    if (row.q) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = rb * 128 + rg + 16 * i;
+            const float s = block_scale(most_of16(most8(v[i])));
+            if (c8 == 0) row_scale[rg + 16 * i] = s;
+            if (r < rows && n > 0) put8(row.q + r * row.ld + c0, n, v[i], __frcp_rn(s));
+        }
+    }
+    if (col.q || square.q) {
+        float m[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            m[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[j] = fmaxf(m[j], fabsf(v[i][j]));
+            m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+        }
+        if (lane < 16)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) part[warp][c8 * 8 + j] = m[j];
+    }
+    __syncthreads();
+    if (row.q && threadIdx.x < 128 && rb * 128 + threadIdx.x < rows)
+        row.s[cb * rows + rb * 128 + threadIdx.x] = row_scale[threadIdx.x];
+    if (!col.q && !square.q) return;
+    if (threadIdx.x < 128) {
+        float m = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) m = fmaxf(m, part[w][threadIdx.x]);
+        const float s = block_scale(m);
+        scale[threadIdx.x] = s;
+        inv[threadIdx.x] = __frcp_rn(s);
+        if (col.q && cb * 128 + int(threadIdx.x) < cols) col.s[rb * cols + cb * 128 + threadIdx.x] = s;
+    }
+    __syncthreads();
+    if (col.q) {
+        float r8[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r8[j] = inv[c8 * 8 + j];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = rb * 128 + rg + 16 * i;
+            if (r < rows && n > 0) put8(col.q + r * col.ld + c0, n, v[i], r8);
+        }
+    }
+    if (square.q) {
+        float s = scale[lane];  // the columns' scales grow with their maxima
+#pragma unroll
+        for (int z = 1; z < 4; ++z) s = fmaxf(s, scale[lane + 32 * z]);
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, d));
+        if (threadIdx.x == 0) square.s[rb * col_blocks + cb] = s;
+        const float rs = __frcp_rn(s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = rb * 128 + rg + 16 * i;
+            if (r < rows && n > 0) put8(square.q + r * square.ld + c0, n, v[i], rs);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- values of codes
+__device__ __forceinline__ void values8(const uint8_t* p, int n, float (&v)[8]) {
+    uint32_t w[2] = {0, 0};
+    if (n >= 8) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+        w[0] = x.x, w[1] = x.y;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) w[j >> 2] |= uint32_t(p[j]) << (8 * (j & 3));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = e4m3_value(w[j >> 2] >> (8 * (j & 3)));
+}
+
+template <typename Y>
+__global__ void __launch_bounds__(kQuantThreads) fp8_dequantize_kernel(const uint8_t* __restrict__ q, int64_t ldq, const float* __restrict__ s,
+                                                                       int block, int64_t rows, int cols, Y* __restrict__ out, int64_t ld, bool wide) {
+    pdl_wait();
+    pdl_trigger();
+    const int col_blocks = (cols + 127) >> 7;
+    const int64_t rb = blockIdx.x / col_blocks;
+    const int cb = int(blockIdx.x - rb * col_blocks);
+    const int c8 = threadIdx.x & 15, rg = threadIdx.x >> 4;
+    const int c0 = cb * 128 + c8 * 8, n = cols - c0;
+    if (n <= 0) return;
+    float s8[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        s8[j] = block == MOE_B_SQUARE ? s[rb * col_blocks + cb] : block == MOE_B_COL && j < n ? s[rb * cols + c0 + j] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = rb * 128 + rg + 16 * i;
+        if (r >= rows) break;
+        float v[8];
+        values8(q + r * ldq + c0, n, v);
+        const float rs = block == MOE_B_ROW ? s[cb * rows + r] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= block == MOE_B_ROW ? rs : s8[j];
+        Y* dst = out + r * ld + c0;
+        if (wide && n >= 8) {
+            if constexpr (sizeof(Y) == 2) {
+                *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+            } else {
+                reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) dst[j] = Y(v[j]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- the gate's backward pass
+struct GatedBack {
+    const float* dh;  // [T, I], row stride ld_dh
+    int64_t ld_dh;
+    Codes g, u;       // kept, row blocks
+    Codes dg_row, du_row, dg_col, du_col, h_col;
+    int64_t T;
+    int I;
+    float limit;
+};
+
+// dg, du and h of eight columns of a row
+__device__ __forceinline__ void gated_back8(const float (&dh)[8], const float (&gq)[8], float sg, const float (&uq)[8], float su,
+                                            float limit, float (&dg)[8], float (&du)[8], float (&h)[8]) {
+    const bool clamp = limit > 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float g = gq[j] * sg, u = uq[j] * su;
+        const float gc = clamp ? clamp_top(g, limit) : g, uc = clamp ? clamp_both(u, limit) : u;
+        const float sig = sigmoidf_(gc), silu = gc * sig;
+        h[j] = silu * uc;
+        dg[j] = clamp && g > limit ? 0.0f : dh[j] * uc * (sig * (1.0f + gc * (1.0f - sig)));
+        du[j] = clamp && fabsf(u) > limit ? 0.0f : dh[j] * silu;
+    }
+}
+
+// dh and the kept g, u -> dg and du as row blocks (for dx) and column blocks, h as column blocks (for the weights' gradients).
+// 128 tokens x 128 columns a block; its inputs stay in registers, and the three results are computed twice, for the
+// maxima and for the codes (holding them would take 96 registers more).
+__global__ void __launch_bounds__(kGatedThreads) fp8_gated_back_kernel(const GatedBack a) {
+    constexpr int W = kGatedThreads / 32, R = 128 * 16 / kGatedThreads;
+    __shared__ float part[3][W][128];
+    __shared__ float inv[3][128], row_scale[2][128];
+    pdl_wait();
+    pdl_trigger();
+    const int col_blocks = (a.I + 127) >> 7;
+    const int64_t rb = blockIdx.x / col_blocks;
+    const int cb = int(blockIdx.x - rb * col_blocks);
+    const int c8 = threadIdx.x & 15, rg = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c0 = cb * 128 + c8 * 8, n = a.I - c0;
+    float dh[R][8], sg[R], su[R];
+    uint2 gq[R], uq[R];
+    float mc[3][8] = {};
+    auto eight = [](uint2 w, float (&v)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = e4m3_value((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+    };
+    auto codes8 = [&](const uint8_t* p) {
+        if (n >= 8) return __ldg(reinterpret_cast<const uint2*>(p));
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) w[j >> 2] |= uint32_t(p[j]) << (8 * (j & 3));
+        return make_uint2(w[0], w[1]);
+    };
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t r = rb * 128 + rg + (128 / R) * i;
+        const bool in = r < a.T && n > 0;
+        gq[i] = uq[i] = make_uint2(0, 0);
+        sg[i] = su[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dh[i][j] = 0.0f;
+        if (in) {
+            load8(a.dh + r * a.ld_dh + c0, n, true, dh[i]);
+            gq[i] = codes8(a.g.q + r * a.g.ld + c0);
+            uq[i] = codes8(a.u.q + r * a.u.ld + c0);
+            sg[i] = __ldg(a.g.s + cb * a.T + r);
+            su[i] = __ldg(a.u.s + cb * a.T + r);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        float g[8], u[8], dg[8], du[8], h[8];
+        eight(gq[i], g), eight(uq[i], u);
+        gated_back8(dh[i], g, sg[i], u, su[i], a.limit, dg, du, h);
+        const float s0 = block_scale(most_of16(most8(dg))), s1 = block_scale(most_of16(most8(du)));
+        if (c8 == 0) row_scale[0][rg + (128 / R) * i] = s0, row_scale[1][rg + (128 / R) * i] = s1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            mc[0][j] = fmaxf(mc[0][j], fabsf(dg[j]));
+            mc[1][j] = fmaxf(mc[1][j], fabsf(du[j]));
+            mc[2][j] = fmaxf(mc[2][j], fabsf(h[j]));
+        }
+    }
+#pragma unroll
+    for (int z = 0; z < 3; ++z)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float m = fmaxf(mc[z][j], __shfl_xor_sync(0xffffffffu, mc[z][j], 16));
+            if (lane < 16) part[z][warp][c8 * 8 + j] = m;
+        }
+    __syncthreads();
+    if (threadIdx.x < 384) {
+        const int z = threadIdx.x >> 7, c = threadIdx.x & 127;
+        float m = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) m = fmaxf(m, part[z][w][c]);
+        const float s = block_scale(m);
+        inv[z][c] = __frcp_rn(s);
+        float* to = z == 0 ? a.dg_col.s : z == 1 ? a.du_col.s : a.h_col.s;
+        if (to && cb * 128 + c < a.I) to[rb * a.I + cb * 128 + c] = s;
+    }
+    if (threadIdx.x < 256 && a.dg_row.q) {
+        const int z = threadIdx.x >> 7, r = threadIdx.x & 127;
+        if (rb * 128 + r < a.T) (z ? a.du_row.s : a.dg_row.s)[cb * a.T + rb * 128 + r] = row_scale[z][r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t r = rb * 128 + rg + (128 / R) * i;
+        if (r >= a.T || n <= 0) continue;
+        float g[8], u[8], dg[8], du[8], h[8];
+        eight(gq[i], g), eight(uq[i], u);
+        gated_back8(dh[i], g, sg[i], u, su[i], a.limit, dg, du, h);
+        if (a.dg_row.q) {
+            put8(a.dg_row.q + r * a.dg_row.ld + c0, n, dg, __frcp_rn(row_scale[0][rg + (128 / R) * i]));
+            put8(a.du_row.q + r * a.du_row.ld + c0, n, du, __frcp_rn(row_scale[1][rg + (128 / R) * i]));
+        }
+        if (a.dg_col.q) {
+            auto cols = [&](int z, const Codes& c, const float (&v)[8]) {
+                float r8[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r8[j] = inv[z][c8 * 8 + j];
+                put8(c.q + r * c.ld + c0, n, v, r8);
+            };
+            cols(0, a.dg_col, dg), cols(1, a.du_col, du), cols(2, a.h_col, h);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- launches
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t blocks(int64_t n) { return (n + 127) / 128; }
+
+bool aligned(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+bool rows_on(const void* p, int64_t stride, size_t elem, size_t bytes) {
+    return ((reinterpret_cast<uintptr_t>(p) | (size_t(stride) * elem)) & (bytes - 1)) == 0;
+}
+size_t size_of(int32_t type) { return type == MOE_T_BF16 ? 2 : 4; }
+bool is_type(int32_t t) { return t == MOE_T_BF16 || t == MOE_T_FP32; }
+
+cudaError_t quantize(const void* x, int32_t type, int64_t rows, int64_t cols, int64_t ld, Codes row, Codes col, Codes square,
+                     cudaStream_t st) {
+    const dim3 grid(unsigned(blocks(rows) * blocks(cols)));
+    const bool wide = rows_on(x, ld, size_of(type), 16);
+    count_launch();
+    if (type == MOE_T_BF16)
+        return launch_pdl(fp8_quantize_kernel<__nv_bfloat16>, grid, dim3(kQuantThreads), 0, st, static_cast<const __nv_bfloat16*>(x),
+                          rows, int(cols), ld, wide, row, col, square);
+    return launch_pdl(fp8_quantize_kernel<float>, grid, dim3(kQuantThreads), 0, st, static_cast<const float*>(x), rows, int(cols), ld,
+                      wide, row, col, square);
+}
+
+int sm_count() {
+    int sms = 152, device = 0;
+    if (cudaGetDevice(&device) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+    return sms;
+}
+
+// Pieces of a workspace, or (base null) their size
+struct Arena {
+    char* base;
+    size_t at = 0;
+    explicit Arena(void* p) : base(static_cast<char*>(p)) {}
+    void* take(int64_t bytes) {
+        void* p = base ? base + at : nullptr;
+        at += size_t(up(bytes, 256));
+        return p;
+    }
+    Codes codes(int64_t rows, int64_t cols, bool by_row) {
+        Codes c;
+        c.ld = up(cols, 16);
+        c.q = static_cast<uint8_t*>(take(rows * c.ld));
+        c.s = static_cast<float*>(take(4 * (by_row ? blocks(cols) * rows : blocks(rows) * cols)));
+        return c;
+    }
+};
+
+// How a product is cut up
+struct Plan {
+    int bn, cg, splits;
+};
+
+Plan plan(int op, const F8Args& a) {
+    const int sms = sm_count();
+    auto tiles = [&](int rows, int cols) {
+        int64_t n = 0;
+        for (int p = 0; p < a.products; ++p)
+            n += ((int64_t(a.o[p].M) + rows - 1) / rows) * ((int64_t(a.o[p].N) + cols - 1) / cols);
+        return n;
+    };
+    if (op == F8_GU) return {256, tiles(256, 128) >= sms / 2 ? 2 : 1, 1};
+    if (tiles(256, 256) >= sms / 2) return {256, 2, 1};
+    if (tiles(128, 256) >= sms) return {256, 1, 1};
+    const int64_t n = tiles(128, 128);
+    int splits = 1;
+    while (splits < 16 && n * (splits + 1) <= sms && a.k_blocks >= 4 * (splits + 1)) ++splits;
+    return {128, 1, splits};
+}
+
+void set_out(F8Out& o, void* out, int64_t ld, bool bf16, bool accumulate, int64_t M, int64_t N) {
+    o = F8Out{out, ld, nullptr, up(N, 4), int(M), int(N), 0, 0, bf16 ? 1 : 0, accumulate ? 1 : 0};
+}
+
+// completes `a` and takes the partial sums' memory from `ws`
+Plan prepare(int op, F8Args& a, Arena& ws) {
+    const Plan pl = plan(op, a);
+    const int tm = 128 * pl.cg, tn = op == F8_GU ? 128 : pl.bn;
+    a.splits = pl.splits;
+    for (int p = 0; p < a.products; ++p) {
+        F8Out& o = a.o[p];
+        o.m_tiles = (o.M + tm - 1) / tm;
+        o.n_tiles = (o.N + tn - 1) / tn;
+        if (pl.splits > 1) o.partial = static_cast<float*>(ws.take(4 * int64_t(pl.splits) * o.M * o.ld_partial));
+    }
+    return pl;
+}
+
+// boxes of 128 bytes (columns) x 128 rows
+bool map_of(CUtensorMap& m, const void* q, int64_t ld, int64_t rows, int64_t cols) {
+    const uint64_t dims[2] = {uint64_t(cols), uint64_t(rows)}, strides[1] = {uint64_t(ld)};
+    const uint32_t box[2] = {128, 128};
+    return encode_map(&m, q, 2, dims, strides, box, MAP_U8);
+}
+
+cudaError_t multiply(int op, const Plan& pl, const F8Maps& maps, const F8Args& a, cudaStream_t st) {
+    const cudaError_t e = launch_f8_gemm(op, pl.bn, pl.cg, maps, a, sm_count(), st);
+    return e != cudaSuccess || pl.splits == 1 ? e : launch_f8_reduce(a, st);
+}
+
+// A product of a linear layer. x, w: the operands' codes; sizes as in fp8.h. `run` false: its workspace alone.
+cudaError_t product(int op, Codes x, int64_t xr, int64_t xc, Codes w, int64_t wr, int64_t wc, void* out, int64_t ld, bool bf16,
+                    bool accumulate, Arena& ws, bool run, cudaStream_t st) {
+    F8Args a = {};
+    a.products = 1;
+    const int64_t M = op == F8_TN ? xc : xr, N = op == F8_NT ? wr : wc, K = op == F8_TN ? xr : xc;
+    a.k_blocks = a.k_part = int(blocks(K));
+    set_out(a.o[0], out, ld, bf16, accumulate, M, N);
+    a.s[0] = {x.s, w.s, op == F8_TN ? xc : xr, op == F8_TN ? wc : blocks(wc)};
+    const Plan pl = prepare(op, a, ws);
+    if (!run) return cudaSuccess;
+    F8Maps m;
+    if (!map_of(m.a[0], x.q, x.ld, xr, xc) || !map_of(m.b[0], w.q, w.ld, wr, wc)) return cudaErrorInvalidValue;
+    return multiply(op, pl, m, a, st);
+}
+
+// ---------------------------------------------------------------- checks
+bool ok_codes(const moe_fp8* v, int64_t cols) {
+    return v && v->q && v->scales && v->ld >= cols && v->ld % 16 == 0 && aligned(v->q, 16) && aligned(v->scales, 4);
+}
+Codes codes_of(const moe_fp8& v) { return {static_cast<uint8_t*>(v.q), v.ld, v.scales}; }
+constexpr Codes kNone = {nullptr, 0, nullptr};
+
+bool ok_size(int64_t T, int64_t a, int64_t b) {
+    return T >= 0 && T <= kMostRows && a >= 1 && a <= kMostCols && b >= 1 && b <= kMostCols;
+}
+bool ok_rows(const void* p, int32_t type, int64_t stride, int64_t cols) { return p && aligned(p, size_of(type)) && stride >= cols; }
+bool ok_workspace(const void* p, size_t have, size_t need) { return need == 0 || (p && have >= need && aligned(p, 256)); }
+bool ok_linear(const moe_linear_config* c, int64_t T) {
+    return c && ok_size(T, c->in_features, c->out_features) && is_type(c->x_type) && is_type(c->y_type);
+}
+bool ok_ffn(const moe_ffn_config* c, int64_t T) {
+    return c && ok_size(T, c->hidden, c->inter) && std::isfinite(c->swiglu_limit) && c->swiglu_limit >= 0.0f;
+}
+bool ok_grad(int32_t g_type, int32_t accumulate) {
+    return (g_type == MOE_G_FP32 || g_type == MOE_G_BF16) && (accumulate == 0 || accumulate == 1);
+}
+moe_status answer(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+// gradients of no rows: nothing to add, or zeros
+cudaError_t no_rows(void* out, int64_t ld, int64_t rows, int64_t cols, int32_t g_type, int32_t accumulate, cudaStream_t st) {
+    if (!out || accumulate) return cudaSuccess;
+    const size_t es = g_type == MOE_G_BF16 ? 2 : 4;
+    return cudaMemset2DAsync(out, size_t(ld) * es, 0, size_t(cols) * es, size_t(rows), st);
+}
+
+// ---------------------------------------------------------------- the calls' work; `run` false: the workspace alone
+struct LinearCall {
+    const moe_linear_config* c;
+    int64_t T;
+    const void* in;  // x or dy
+    int64_t in_stride;
+    Codes w, kept;
+    void* out;  // y or dx
+    int64_t out_stride;
+    void* dw;
+    int64_t dw_stride;
+    int32_t g_type, accumulate;
+};
+
+cudaError_t linear_forward(const LinearCall& k, Arena& ws, bool run, cudaStream_t st) {
+    const int64_t T = k.T, K = k.c->in_features, N = k.c->out_features;
+    const Codes xq = ws.codes(T, K, true);
+    if (run) {
+        const cudaError_t e = quantize(k.in, k.c->x_type, T, K, k.in_stride, xq, k.kept, kNone, st);
+        if (e != cudaSuccess) return e;
+    }
+    return product(F8_NT, xq, T, K, k.w, N, K, k.out, k.out_stride, k.c->y_type == MOE_T_BF16, false, ws, run, st);
+}
+
+cudaError_t linear_backward(const LinearCall& k, Arena& ws, bool run, cudaStream_t st) {
+    const int64_t T = k.T, K = k.c->in_features, N = k.c->out_features;
+    const bool x = !run || k.out, w = !run || k.dw;
+    const Codes row = x ? ws.codes(T, N, true) : kNone, col = w ? ws.codes(T, N, false) : kNone;
+    cudaError_t e = cudaSuccess;
+    if (run && (x || w)) e = quantize(k.in, k.c->y_type, T, N, k.in_stride, row, col, kNone, st);
+    if (x && e == cudaSuccess)
+        e = product(F8_NN, row, T, N, k.w, N, K, k.out, k.out_stride, k.c->x_type == MOE_T_BF16, false, ws, run, st);
+    if (w && e == cudaSuccess)
+        e = product(F8_TN, col, T, N, k.kept, T, K, k.dw, k.dw_stride, k.g_type == MOE_G_BF16, k.accumulate, ws, run, st);
+    return e;
+}
+
+struct FfnCall {
+    const moe_ffn_config* c;
+    int64_t T;
+    const void* in;
+    int64_t in_stride;
+    Codes gate, up, down;
+    Codes kx, kg, ku;
+    void* out;
+    int64_t out_stride;
+    const moe_ffn_grads* grads;
+    int32_t g_type, accumulate;
+};
+
+cudaError_t ffn_forward(const FfnCall& k, Arena& ws, bool run, cudaStream_t st) {
+    const int64_t T = k.T, H = k.c->hidden, I = k.c->inter;
+    const Codes xq = ws.codes(T, H, true), h = ws.codes(T, I, true);
+    F8Args a = {};
+    a.products = 1;
+    a.k_blocks = a.k_part = int(blocks(H));
+    set_out(a.o[0], nullptr, 0, false, false, T, I);
+    const Plan pl = prepare(F8_GU, a, ws);
+    if (run) {
+        cudaError_t e = quantize(k.in, MOE_T_BF16, T, H, k.in_stride, xq, k.kx, kNone, st);
+        if (e != cudaSuccess) return e;
+        a.s[0] = {xq.s, k.gate.s, T, blocks(H)};
+        a.s[1] = {xq.s, k.up.s, T, blocks(H)};
+        a.h = h.q, a.hs = h.s, a.ld_h = h.ld;
+        a.g = k.kg.q, a.gs = k.kg.s, a.ld_g = k.kg.ld;
+        a.u = k.ku.q, a.us = k.ku.s, a.ld_u = k.ku.ld;
+        a.limit = k.c->swiglu_limit;
+        F8Maps m;
+        if (!map_of(m.a[0], xq.q, xq.ld, T, H) || !map_of(m.b[0], k.gate.q, k.gate.ld, I, H) ||
+            !map_of(m.b[1], k.up.q, k.up.ld, I, H))
+            return cudaErrorInvalidValue;
+        e = multiply(F8_GU, pl, m, a, st);
+        if (e != cudaSuccess) return e;
+    }
+    return product(F8_NT, h, T, I, k.down, H, I, k.out, k.out_stride, true, false, ws, run, st);
+}
+
+cudaError_t ffn_backward(const FfnCall& k, Arena& ws, bool run, cudaStream_t st) {
+    const int64_t T = k.T, H = k.c->hidden, I = k.c->inter;
+    const bool x = !run || k.out, w = !run || k.grads;
+    if (!x && !w) return cudaSuccess;
+    const Codes dy = ws.codes(T, H, true), dyc = w ? ws.codes(T, H, false) : kNone;
+    const int64_t ld_dh = up(I, 4);
+    float* dh = static_cast<float*>(ws.take(4 * T * ld_dh));
+    GatedBack b = {dh, ld_dh, k.kg, k.ku, kNone, kNone, kNone, kNone, kNone, T, int(I), k.c->swiglu_limit};
+    if (x) b.dg_row = ws.codes(T, I, true), b.du_row = ws.codes(T, I, true);
+    if (w) b.dg_col = ws.codes(T, I, false), b.du_col = ws.codes(T, I, false), b.h_col = ws.codes(T, I, false);
+    cudaError_t e = cudaSuccess;
+    if (run) e = quantize(k.in, MOE_T_BF16, T, H, k.in_stride, dy, dyc, kNone, st);
+    if (e == cudaSuccess) e = product(F8_NN, dy, T, H, k.down, H, I, dh, ld_dh, false, false, ws, run, st);
+    if (e != cudaSuccess) return e;
+    if (run) {
+        count_launch();
+        e = launch_pdl(fp8_gated_back_kernel, dim3(unsigned(blocks(T) * blocks(I))), dim3(kGatedThreads), 0, st, b);
+        if (e != cudaSuccess) return e;
+    }
+    if (x) {
+        F8Args a = {};
+        a.products = 1;
+        a.k_part = int(blocks(I));
+        a.k_blocks = 2 * a.k_part;
+        set_out(a.o[0], k.out, k.out_stride, true, false, T, H);
+        a.s[0] = {b.dg_row.s, k.gate.s, T, blocks(H)};
+        a.s[1] = {b.du_row.s, k.up.s, T, blocks(H)};
+        const Plan pl = prepare(F8_NN, a, ws);
+        if (run) {
+            F8Maps m;
+            if (!map_of(m.a[0], b.dg_row.q, b.dg_row.ld, T, I) || !map_of(m.a[1], b.du_row.q, b.du_row.ld, T, I) ||
+                !map_of(m.b[0], k.gate.q, k.gate.ld, I, H) || !map_of(m.b[1], k.up.q, k.up.ld, I, H))
+                return cudaErrorInvalidValue;
+            e = multiply(F8_NN, pl, m, a, st);
+            if (e != cudaSuccess) return e;
+        }
+    }
+    if (w) {
+        F8Args a = {};
+        a.products = 3;
+        a.k_blocks = a.k_part = int(blocks(T));
+        const moe_ffn_grads none = {};
+        const moe_ffn_grads& g = k.grads ? *k.grads : none;
+        const bool bf = k.g_type == MOE_G_BF16, add = k.accumulate;
+        set_out(a.o[0], g.gate, g.gate_stride, bf, add, I, H);
+        set_out(a.o[1], g.up, g.up_stride, bf, add, I, H);
+        set_out(a.o[2], g.down, g.down_stride, bf, add, H, I);
+        a.s[0] = {b.dg_col.s, k.kx.s, I, H};
+        a.s[1] = {b.du_col.s, k.kx.s, I, H};
+        a.s[2] = {dyc.s, b.h_col.s, H, I};
+        const Plan pl = prepare(F8_TN, a, ws);
+        if (run) {
+            F8Maps m;
+            if (!map_of(m.a[0], b.dg_col.q, b.dg_col.ld, T, I) || !map_of(m.a[1], b.du_col.q, b.du_col.ld, T, I) ||
+                !map_of(m.a[2], dyc.q, dyc.ld, T, H) || !map_of(m.b[0], k.kx.q, k.kx.ld, T, H) ||
+                !map_of(m.b[2], b.h_col.q, b.h_col.ld, T, I))
+                return cudaErrorInvalidValue;
+            m.b[1] = m.b[0];
+            e = multiply(F8_TN, pl, m, a, st);
+        }
+    }
+    return e;
+}
+
+}  // namespace
+
+}  // namespace moe
+
+extern "C" {
+
+moe_status moe_fp8_quantize(const void* x, int32_t x_type, int64_t rows, int64_t cols, int64_t x_stride,
+                            const moe_fp8* row, const moe_fp8* col, const moe_fp8* square, void* stream) {
+    using namespace moe;
+    if (!is_type(x_type) || !ok_size(rows, cols, 1) || x_stride < cols) return MOE_ERR_INVALID_ARG;
+    if (rows == 0 || (!row && !col && !square)) return MOE_OK;
+    if (!ok_rows(x, x_type, x_stride, cols)) return MOE_ERR_INVALID_ARG;
+    for (const moe_fp8* v : {row, col, square})
+        if (v && !ok_codes(v, cols)) return MOE_ERR_INVALID_ARG;
+    auto of = [](const moe_fp8* v) { return v ? codes_of(*v) : kNone; };
+    return answer(quantize(x, x_type, rows, cols, x_stride, of(row), of(col), of(square), static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_fp8_dequantize(const moe_fp8* v, int32_t block, int64_t rows, int64_t cols, void* out, int32_t out_type,
+                              int64_t out_stride, void* stream) {
+    using namespace moe;
+    if (!is_type(out_type) || !ok_size(rows, cols, 1) || out_stride < cols || block < MOE_B_ROW || block > MOE_B_SQUARE)
+        return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!ok_codes(v, cols) || !ok_rows(out, out_type, out_stride, cols)) return MOE_ERR_INVALID_ARG;
+    const dim3 grid(unsigned(blocks(rows) * blocks(cols)));
+    const bool wide = rows_on(out, out_stride, size_of(out_type), 16);
+    const uint8_t* q = static_cast<const uint8_t*>(v->q);
+    const float* s = v->scales;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    count_launch();
+    if (out_type == MOE_T_BF16)
+        return answer(launch_pdl(fp8_dequantize_kernel<__nv_bfloat16>, grid, dim3(kQuantThreads), 0, st, q, v->ld, s, block, rows, int(cols),
+                                 static_cast<__nv_bfloat16*>(out), out_stride, wide));
+    return answer(launch_pdl(fp8_dequantize_kernel<float>, grid, dim3(kQuantThreads), 0, st, q, v->ld, s, block, rows, int(cols),
+                             static_cast<float*>(out), out_stride, wide));
+}
+
+moe_status moe_linear_size(const moe_linear_config* cfg, int64_t T, int32_t backward, size_t* bytes) {
+    using namespace moe;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (!ok_linear(cfg, T) || (backward != 0 && backward != 1)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    LinearCall k = {};
+    k.c = cfg, k.T = T;
+    Arena ws(nullptr);
+    (void)(backward ? linear_backward(k, ws, false, nullptr) : linear_forward(k, ws, false, nullptr));
+    *bytes = ws.at;
+    return MOE_OK;
+}
+
+moe_status moe_linear_forward(const moe_linear_config* cfg, int64_t T, const void* x, int64_t x_stride, const moe_fp8* w, void* y,
+                              int64_t y_stride, const moe_fp8* kept, void* workspace, size_t workspace_bytes, void* stream) {
+    using namespace moe;
+    size_t need = 0;
+    const moe_status s = moe_linear_size(cfg, T, 0, &need);
+    if (s != MOE_OK) return s;
+    if (x_stride < cfg->in_features || y_stride < cfg->out_features) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!ok_rows(x, cfg->x_type, x_stride, cfg->in_features) || !ok_rows(y, cfg->y_type, y_stride, cfg->out_features) ||
+        !ok_codes(w, cfg->in_features) || (kept && !ok_codes(kept, cfg->in_features)) || !ok_workspace(workspace, workspace_bytes, need))
+        return MOE_ERR_INVALID_ARG;
+    const LinearCall k = {cfg, T, x, x_stride, codes_of(*w), kept ? codes_of(*kept) : kNone, y, y_stride, nullptr, 0, 0, 0};
+    Arena ws(workspace);
+    return answer(linear_forward(k, ws, true, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_linear_backward(const moe_linear_config* cfg, int64_t T, const void* dy, int64_t dy_stride, const moe_fp8* w,
+                               const moe_fp8* kept, void* dx, int64_t dx_stride, void* dweight, int64_t dweight_stride, int32_t g_type,
+                               int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+    using namespace moe;
+    size_t need = 0;
+    const moe_status s = moe_linear_size(cfg, T, 1, &need);
+    if (s != MOE_OK) return s;
+    const int64_t K = cfg->in_features, N = cfg->out_features;
+    const int32_t gt = g_type == MOE_G_BF16 ? MOE_T_BF16 : MOE_T_FP32;
+    if (!ok_grad(g_type, accumulate) || dy_stride < N || (dx && dx_stride < K)) return MOE_ERR_INVALID_ARG;
+    if (dweight && !ok_rows(dweight, gt, dweight_stride, K)) return MOE_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) return answer(no_rows(dweight, dweight_stride, N, K, g_type, accumulate, st));
+    if (!ok_rows(dy, cfg->y_type, dy_stride, N) || (dx && (!ok_rows(dx, cfg->x_type, dx_stride, K) || !ok_codes(w, K))) ||
+        (dweight && !ok_codes(kept, K)) || !ok_workspace(workspace, workspace_bytes, need))
+        return MOE_ERR_INVALID_ARG;
+    const LinearCall k = {cfg, T, dy, dy_stride, w ? codes_of(*w) : kNone, kept ? codes_of(*kept) : kNone, dx, dx_stride,
+                          dweight, dweight_stride, g_type, accumulate};
+    Arena ws(workspace);
+    return answer(linear_backward(k, ws, true, st));
+}
+
+moe_status moe_ffn_size(const moe_ffn_config* cfg, int64_t T, int32_t backward, size_t* bytes) {
+    using namespace moe;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (!ok_ffn(cfg, T) || (backward != 0 && backward != 1)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    FfnCall k = {};
+    k.c = cfg, k.T = T;
+    Arena ws(nullptr);
+    (void)(backward ? ffn_backward(k, ws, false, nullptr) : ffn_forward(k, ws, false, nullptr));
+    *bytes = ws.at;
+    return MOE_OK;
+}
+
+moe_status moe_ffn_forward(const moe_ffn_config* cfg, int64_t T, const void* x, int64_t x_stride, const moe_ffn_weights* w, void* y,
+                           int64_t y_stride, const moe_ffn_kept* kept, void* workspace, size_t workspace_bytes, void* stream) {
+    using namespace moe;
+    size_t need = 0;
+    const moe_status s = moe_ffn_size(cfg, T, 0, &need);
+    if (s != MOE_OK) return s;
+    const int64_t H = cfg->hidden, I = cfg->inter;
+    if (x_stride < H || y_stride < H) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!ok_rows(x, MOE_T_BF16, x_stride, H) || !ok_rows(y, MOE_T_BF16, y_stride, H) || !w || !ok_codes(&w->gate, H) ||
+        !ok_codes(&w->up, H) || !ok_codes(&w->down, I) || !ok_workspace(workspace, workspace_bytes, need))
+        return MOE_ERR_INVALID_ARG;
+    if (kept && (!ok_codes(&kept->x, H) || !ok_codes(&kept->gate, I) || !ok_codes(&kept->up, I))) return MOE_ERR_INVALID_ARG;
+    FfnCall k = {cfg, T, x, x_stride, codes_of(w->gate), codes_of(w->up), codes_of(w->down), kNone, kNone, kNone, y, y_stride, nullptr, 0, 0};
+    if (kept) k.kx = codes_of(kept->x), k.kg = codes_of(kept->gate), k.ku = codes_of(kept->up);
+    Arena ws(workspace);
+    return answer(ffn_forward(k, ws, true, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_ffn_backward(const moe_ffn_config* cfg, int64_t T, const void* dy, int64_t dy_stride, const moe_ffn_weights* w,
+                            const moe_ffn_kept* kept, void* dx, int64_t dx_stride, const moe_ffn_grads* grads, int32_t g_type,
+                            int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+    using namespace moe;
+    size_t need = 0;
+    const moe_status s = moe_ffn_size(cfg, T, 1, &need);
+    if (s != MOE_OK) return s;
+    const int64_t H = cfg->hidden, I = cfg->inter;
+    const int32_t gt = g_type == MOE_G_BF16 ? MOE_T_BF16 : MOE_T_FP32;
+    if (!ok_grad(g_type, accumulate) || dy_stride < H || (dx && dx_stride < H)) return MOE_ERR_INVALID_ARG;
+    if (grads && (!ok_rows(grads->gate, gt, grads->gate_stride, H) || !ok_rows(grads->up, gt, grads->up_stride, H) ||
+                  !ok_rows(grads->down, gt, grads->down_stride, I)))
+        return MOE_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        if (!grads) return MOE_OK;
+        cudaError_t e = no_rows(grads->gate, grads->gate_stride, I, H, g_type, accumulate, st);
+        if (e == cudaSuccess) e = no_rows(grads->up, grads->up_stride, I, H, g_type, accumulate, st);
+        if (e == cudaSuccess) e = no_rows(grads->down, grads->down_stride, H, I, g_type, accumulate, st);
+        return answer(e);
+    }
+    if (!ok_rows(dy, MOE_T_BF16, dy_stride, H) || (dx && !ok_rows(dx, MOE_T_BF16, dx_stride, H)) || !w || !ok_codes(&w->gate, H) ||
+        !ok_codes(&w->up, H) || !ok_codes(&w->down, I) || !kept || !ok_codes(&kept->x, H) || !ok_codes(&kept->gate, I) ||
+        !ok_codes(&kept->up, I) || !ok_workspace(workspace, workspace_bytes, need))
+        return MOE_ERR_INVALID_ARG;
+    const FfnCall k = {cfg, T, dy, dy_stride, codes_of(w->gate), codes_of(w->up), codes_of(w->down), codes_of(kept->x),
+                       codes_of(kept->gate), codes_of(kept->up), dx, dx_stride, grads, g_type, accumulate};
+    Arena ws(workspace);
+    return answer(ffn_backward(k, ws, true, st));
+}
+
+}  // extern "C"

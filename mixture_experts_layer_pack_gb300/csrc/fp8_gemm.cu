@@ -1,0 +1,706 @@
+// Products of E4M3 matrices with one fp32 scale for a block of 128 (sm_103a).
+//
+//   out[m,n] = sum over blocks kb of 128 of  sa(m,kb) sb(n,kb) sum over k in kb of qa[m,k] qb[n,k]
+//
+// The inner sums are tcgen05.mma products of one K block (four K = 32 steps) into a TMEM buffer; the
+// scales are arbitrary fp32 numbers, so the outer sum is the CUDA cores': the epilogue warps read each
+// block's sums from TMEM and add them, scaled, to fp32 accumulators in registers, while the tensor
+// cores fill the next buffer. At a 128 x 256 tile a block takes the tensor cores 512 cycles (8192 E4M3
+// multiply-adds a cycle and SM), and the reads and multiply-adds of the eight epilogue warps about 400.
+//
+// Warp 0 loads operands (TMA, 128-byte swizzle) and scales (4-byte cp.async, which take any
+// alignment) into two rings, warp 1 issues the products, warps 4..11 hold the accumulators: two warps a
+// quarter of the 128 TMEM lanes, half of the columns each. A weight is stored once: the product with it
+// and the one with its transpose read the same codes, K-major and MN-major (8-bit operands may be
+// either), and so do the two operands of a weight's gradient, whose K are the tokens.
+//
+// Every wait is bounded; after one that gave up the results are NaN (there is no status word to say it in).
+#include "device_common.cuh"
+#include "fp8.h"
+#include "fp8_device.cuh"
+#include "internal.h"
+
+#include <atomic>
+
+namespace moe {
+
+namespace {
+
+constexpr int kF8EpiWarps = 8;
+constexpr int kF8Threads = 128 + 32 * kF8EpiWarps;
+// Three warps share a quarter of the register file, 168 registers a thread at launch. An epilogue thread wants 128 accumulators and
+// two sets of 16 sums, so the first warpgroup (loads and products) gives up what the two others take: 56 + 2 * 224 = 3 * 168.
+constexpr int kFewRegs = 56, kManyRegs = 224;
+constexpr uint32_t kTileBytes = 128 * 128;   // 128 rows of 128 codes
+constexpr uint32_t kStageFloats = 32 * 16;   // an epilogue warp's staging: 32 rows x 16 columns
+
+template <int OP, int BN, int CG>
+struct F8Cfg {
+    static constexpr uint32_t A_BYTES = kTileBytes;
+    static constexpr uint32_t B_BYTES = BN / CG * 128;
+    static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES = int(196608 / STAGE_BYTES);
+    static constexpr int BUFS = 512 / BN;
+    // A block's scales are written when its stage is free, that is when the products of the block STAGES before it are
+    // complete, which began after the epilogue had read the sums (and the scales) of the block BUFS before that.
+    static constexpr int SLOTS = STAGES + BUFS + 2;
+    static constexpr int COL_SCALES = OP == F8_TN ? BN : 4;
+    static constexpr int SLOT_FLOATS = 128 + COL_SCALES;
+    static constexpr size_t SMEM = size_t(STAGES) * STAGE_BYTES + kF8EpiWarps * kStageFloats * 4 +
+                                   size_t(SLOTS) * SLOT_FLOATS * 4 + (OP == F8_GU ? 4 * 128 * 2 * 4 : 0) + 1024 + 512;
+    static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+};
+
+// ---------------------------------------------------------------- PTX
+__device__ __forceinline__ uint64_t f8_desc(uint32_t addr, uint32_t lbo) {  // 128-byte swizzle, 8-row groups 1024 bytes apart
+    return uint64_t((addr >> 4) & 0x3FFF) | (uint64_t((lbo >> 4) & 0x3FFF) << 16) | (uint64_t(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// shared::cluster address of the same place in the pair's first CTA
+__device__ __forceinline__ uint32_t in_leader(const void* p) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+
+template <int CG>
+__device__ __forceinline__ void f8_load(void* dst, const void* map, uint32_t bar, int x, int y) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+            "[%4];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void f8_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// arrives on `bar` (CG 2: at the same place in both CTAs) once the products issued so far are complete
+template <int CG>
+__device__ __forceinline__ void f8_commit(uint64_t* bar) {
+    if (CG == 1)
+        mma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"(uint16_t(3))
+            : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void f8_tmem_alloc(uint32_t* slot, uint32_t cols) {
+    if (CG == 1) {
+        tmem_alloc(slot, cols);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+
+template <int CG>
+__device__ __forceinline__ void f8_tmem_free(uint32_t addr, uint32_t cols) {
+    if (CG == 1)
+        tmem_dealloc(addr, cols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+
+// an arrival at a barrier of the pair's first CTA (its shared::cluster address)
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// bounded wait; gives up when another role of the CTA did, or after kWaitLimitNs
+template <int CG>
+__device__ __forceinline__ bool f8_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    auto ready = [&] { return CG == 1 ? mbar_try_wait(bar, parity) : try_wait_cluster(bar, parity); };
+    if (ready()) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        for (int i = 0; i < 16; ++i)
+            if (ready()) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+// the same while winding down: whatever the others did
+__device__ __forceinline__ void f8_drain(uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 <= kWaitLimitNs) {
+    }
+}
+
+__device__ __forceinline__ void copy4(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// this thread's copies so far arrive on `bar` when they are complete
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// 32 lanes x 16 columns; the registers are valid after tmem_ready
+__device__ __forceinline__ void tmem_ask16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ready(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+// ---------------------------------------------------------------- work items
+struct Item {
+    int p;          // product (F8_TN)
+    int m0, n0;     // first row of this CTA's 128 (its own of a pair), first column of the tile
+    int ks;         // which part of the K blocks, [k_lo, k_hi)
+    int k_lo, k_hi;
+};
+
+// Tiles go down the rows within a band of eight row tiles before they move to the next columns, so that the operands
+// of the tiles that run at one time stay in L2.
+template <int OP, int BN, int CG>
+__device__ __forceinline__ Item f8_item(int i, const F8Args& a, uint32_t rank) {
+    constexpr int TN = OP == F8_GU ? 128 : BN;
+    constexpr int kBand = 8;
+    Item t;
+    t.ks = i % a.splits;
+    int tile = i / a.splits;
+    t.p = 0;
+    if (OP == F8_TN)
+        while (t.p + 1 < a.products && tile >= a.o[t.p].m_tiles * a.o[t.p].n_tiles) {
+            tile -= a.o[t.p].m_tiles * a.o[t.p].n_tiles;
+            ++t.p;
+        }
+    const int mt = a.o[t.p].m_tiles, nt = a.o[t.p].n_tiles;
+    const int band = tile / (kBand * nt), in = tile - band * kBand * nt;
+    const int rows = min(kBand, mt - band * kBand);
+    t.m0 = ((band * kBand + in % rows) * CG + int(rank)) * 128;
+    t.n0 = in / rows * TN;
+    const int per = a.k_blocks / a.splits, more = a.k_blocks % a.splits;
+    t.k_lo = t.ks * per + min(t.ks, more);
+    t.k_hi = t.k_lo + per + (t.ks < more ? 1 : 0);
+    return t;
+}
+
+// ---------------------------------------------------------------- results
+// 16 columns of a warp's 32 rows through its staging: written a row a lane, read as pieces of rows (16-byte unit j of row r
+// lies at j ^ (r / 2 % 4): no bank conflict either way)
+__device__ __forceinline__ void put16(float* staging, const float* v) {
+    const int lane = threadIdx.x & 31;
+    float4* row = reinterpret_cast<float4*>(staging + lane * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) row[j ^ ((lane >> 1) & 3)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
+}
+
+__device__ __forceinline__ void f8_store16(const F8Out& o, void* out, int64_t ld, bool bf16, bool add, bool wide, int row0,
+                                           int col0, const float* v, float* staging) {
+    const int lane = threadIdx.x & 31;
+    put16(staging, v);
+    if (wide && col0 + 16 <= o.N) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2), j = lane & 3;
+            float4 x = reinterpret_cast<const float4*>(staging + r * 16)[j ^ ((r >> 1) & 3)];
+            if (row0 + r >= o.M) continue;
+            const int64_t at = int64_t(row0 + r) * ld + col0 + 4 * j;
+            if (bf16) {
+                uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at);
+                uint2 w = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+                if (add) {
+                    const uint2 old = *dst;
+                    float a0, a1, a2, a3, b0, b1, b2, b3;
+                    unpack_bf16x2(old.x, a0, a1), unpack_bf16x2(old.y, a2, a3);
+                    unpack_bf16x2(w.x, b0, b1), unpack_bf16x2(w.y, b2, b3);
+                    w = make_uint2(pack_bf16x2(a0 + b0, a1 + b1), pack_bf16x2(a2 + b2, a3 + b3));
+                }
+                *dst = w;
+            } else {
+                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+                if (add) {
+                    const float4 old = *dst;
+                    x = make_float4(old.x + x.x, old.y + x.y, old.z + x.z, old.w + x.w);
+                }
+                *dst = x;
+            }
+        }
+    } else {
+        const int c = lane & 15;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int r = i * 2 + (lane >> 4);
+            const float x = staging[r * 16 + 4 * ((c >> 2) ^ ((r >> 1) & 3)) + (c & 3)];
+            if (row0 + r < o.M && col0 + c < o.N) store_one(out, int64_t(row0 + r) * ld + col0 + c, bf16, add, x);
+        }
+    }
+    __syncwarp();
+}
+
+// 16 codes of one row; the row's bytes past N are not the product's to write
+__device__ __forceinline__ void put_codes(uint8_t* row, int col, int N, const float* v, float r) {
+    uint4 w;
+    w.x = e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r);
+    w.y = e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r);
+    w.z = e4m3x4(v[8] * r, v[9] * r, v[10] * r, v[11] * r);
+    w.w = e4m3x4(v[12] * r, v[13] * r, v[14] * r, v[15] * r);
+    if (col + 16 <= N) {
+        *reinterpret_cast<uint4*>(row + col) = w;
+    } else {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int z = 0; z < 16; ++z)
+            if (col + z < N) row[col + z] = uint8_t(x[z >> 2] >> (8 * (z & 3)));
+    }
+}
+
+// h = silu(g) u of a row's 64 columns (g in acc[0, 64), u in acc[64, 128)), stored as codes with the scale of the row's 128:
+// the other 64 are the partner warp's, and the two exchange their largest magnitudes through `most`. g and u are stored
+// first where they are kept, so that h can take g's registers: the logistic function's two slow instructions (16 a cycle and SM)
+// run once an element.
+__device__ __forceinline__ void gated_results(const F8Args& a, const Item& t, float (&acc)[128], int q, int half, float* most) {
+    const int lane = threadIdx.x & 31;
+    const int row = t.m0 + q * 32 + lane, col = t.n0 + 64 * half, N = a.o[0].N;
+    const bool store = row < a.o[0].M;
+    const int64_t sat = int64_t(t.n0 >> 7) * a.o[0].M + row;
+    float* mine = most + (half * 128 + q * 32 + lane);
+    const float* other = most + ((half ^ 1) * 128 + q * 32 + lane);
+    auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory"); };
+    if (a.g) {
+        float mg = 0.0f, mu = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) mg = fmaxf(mg, fabsf(acc[j])), mu = fmaxf(mu, fabsf(acc[64 + j]));
+        mine[0] = mg;
+        mine[256] = mu;
+        meet();
+        const float sg = block_scale(fmaxf(mg, other[0])), su = block_scale(fmaxf(mu, other[256]));
+        if (store) {
+            if (half == 0) a.gs[sat] = sg, a.us[sat] = su;
+            const float rg = __frcp_rn(sg), ru = __frcp_rn(su);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                put_codes(a.g + int64_t(row) * a.ld_g, col + 16 * c, N, acc + 16 * c, rg);
+                put_codes(a.u + int64_t(row) * a.ld_u, col + 16 * c, N, acc + 64 + 16 * c, ru);
+            }
+        }
+    }
+    float mh = 0.0f;
+    const bool clamp = a.limit > 0.0f;
+#pragma unroll
+    for (int j = 0; j < 64; ++j) {
+        float g = acc[j], u = acc[64 + j];
+        if (clamp) g = clamp_top(g, a.limit), u = clamp_both(u, a.limit);
+        acc[j] = g * sigmoidf_(g) * u;
+        mh = fmaxf(mh, fabsf(acc[j]));
+    }
+    mine[512] = mh;
+    meet();
+    const float sh = block_scale(fmaxf(mh, other[512]));
+    if (store) {
+        if (half == 0) a.hs[sat] = sh;
+        const float rh = __frcp_rn(sh);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) put_codes(a.h + int64_t(row) * a.ld_h, col + 16 * c, N, acc + 16 * c, rh);
+    }
+    meet();  // both have read before the next tile's are written
+}
+
+// ---------------------------------------------------------------- the kernel
+template <int OP, int BN, int CG>
+__global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_constant__ F8Maps maps, const __grid_constant__ F8Args a) {
+    using C = F8Cfg<OP, BN, CG>;
+    constexpr bool A_MN = OP == F8_TN, B_MN = OP == F8_TN || OP == F8_NN;
+    constexpr uint32_t IDESC = (1u << 4) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) | (uint32_t(BN >> 3) << 17) |
+                               (uint32_t(128 * CG >> 4) << 24);  // E4M3 operands, fp32 sums
+    constexpr int HALF = BN / 2;
+
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    float* staging = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES);
+    float* slots = staging + kF8EpiWarps * kStageFloats;
+    float* most = slots + C::SLOTS * C::SLOT_FLOATS;  // F8_GU: [3][2][128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(most + (OP == F8_GU ? 4 * 256 : 0));
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* tfull = empty + C::STAGES;
+    uint64_t* tempty = tfull + C::BUFS;
+    uint64_t* sfull = tempty + C::BUFS;
+    uint64_t* drain = sfull + C::SLOTS;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 1 ? 0 : cta_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+        for (int b = 0; b < C::BUFS; ++b) mbar_init(&tfull[b], 1), mbar_init(&tempty[b], CG * kF8EpiWarps);
+        for (int s = 0; s < C::SLOTS; ++s) mbar_init(&sfull[s], 32);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&maps.a[0]);
+        tma_prefetch_map(&maps.b[0]);
+    }
+    if (warp == 1) f8_tmem_alloc<CG>(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+
+    int items = a.o[0].m_tiles * a.o[0].n_tiles;
+    if (OP == F8_TN)
+        for (int p = 1; p < a.products; ++p) items += a.o[p].m_tiles * a.o[p].n_tiles;
+    items *= a.splits;
+    const int first = blockIdx.x / CG, step = gridDim.x / CG;
+
+    if (warp == 0) {
+        // ---------------- loads
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, filled = 0, fill_parity = 0;
+        bool ok = true;
+        for (int i = first; ok && i < items; i += step) {
+            const Item t = f8_item<OP, BN, CG>(i, a, rank);
+            const F8Out& o = a.o[t.p];
+            for (int kb = t.k_lo; kb < t.k_hi; ++kb) {
+                ok = __all_sync(0xffffffffu, f8_wait<CG>(&empty[stage], phase ^ 1, abort_flag));
+                if (!ok) break;
+                const int part = OP == F8_TN ? t.p : (OP == F8_NN && kb >= a.k_part ? 1 : 0);
+                const int kl = OP == F8_NN && part ? kb - a.k_part : kb;
+                const F8Scales& s = a.s[part];
+                float* sl = slots + slot * C::SLOT_FLOATS;
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                    copy4(sl + lane + 32 * z, s.a + int64_t(kl) * s.ld_a + min(t.m0 + lane + 32 * z, o.M - 1));
+                if (OP == F8_TN) {
+#pragma unroll
+                    for (int z = 0; z < BN / 32; ++z)
+                        copy4(sl + 128 + lane + 32 * z, s.b + int64_t(kl) * s.ld_b + min(t.n0 + lane + 32 * z, o.N - 1));
+                } else if (lane < BN / 128) {
+                    // F8_GU: the gate's scale and the up weight's; else those of the tile's one or two blocks of columns
+                    const F8Scales& w = OP == F8_GU ? a.s[lane] : s;
+                    const int nb = OP == F8_GU ? t.n0 >> 7 : min((t.n0 >> 7) + lane, (o.N - 1) >> 7);
+                    copy4(sl + 128 + lane, w.b + (OP == F8_NN ? int64_t(kl) * w.ld_b + nb : int64_t(nb) * w.ld_b + kl));
+                }
+                copies_arrive(&sfull[slot]);
+                if (lane == 0) {
+                    uint8_t* sa = smem + stage * C::STAGE_BYTES;
+                    uint8_t* sb = sa + C::A_BYTES;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * C::STAGE_BYTES);
+                    const uint32_t bar = CG == 1 ? smem_u32(&full[stage]) : in_leader(&full[stage]);
+                    const CUtensorMap* mA = &maps.a[part];
+                    const CUtensorMap* mB = &maps.b[part];
+                    const int k0 = kl * 128;
+                    if (A_MN)
+                        f8_load<CG>(sa, mA, bar, t.m0, k0);
+                    else
+                        f8_load<CG>(sa, mA, bar, k0, t.m0);
+#pragma unroll
+                    for (int c = 0; c < BN / 128 / CG; ++c) {
+                        const int chunk = c + int(rank) * (BN / 128 / CG);
+                        uint8_t* dst = sb + c * kTileBytes;
+                        if (OP == F8_GU)
+                            f8_load<CG>(dst, &maps.b[chunk], bar, k0, t.n0);
+                        else if (B_MN)
+                            f8_load<CG>(dst, mB, bar, t.n0 + 128 * chunk, k0);
+                        else
+                            f8_load<CG>(dst, mB, bar, k0, t.n0 + 128 * chunk);
+                    }
+                }
+                __syncwarp();
+                filled |= 1u << stage;
+                fill_parity = (fill_parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == C::STAGES) stage = 0, phase ^= 1;
+                if (++slot == C::SLOTS) slot = 0;
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!ok && rank == 0)  // every copy lands before the memory is given back (the first CTA's barriers count both CTAs')
+            for (int s = 0; s < C::STAGES; ++s)
+                if (filled & (1u << s)) f8_drain(&full[s], (fill_parity >> s) & 1);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- products
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (lane == 0 && rank == 0) {
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, bphase = 0;
+            bool ok = true;
+            for (int i = first; ok && i < items; i += step) {
+                const Item t = f8_item<OP, BN, CG>(i, a, rank);
+                for (int kb = t.k_lo; kb < t.k_hi; ++kb) {
+                    ok = f8_wait<CG>(&tempty[buf], bphase ^ 1, abort_flag) && f8_wait<CG>(&full[stage], phase, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a_addr = smem_u32(smem + stage * C::STAGE_BYTES), b_addr = a_addr + C::A_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        f8_mma<CG>(tmem + buf * BN, A_MN ? f8_desc(a_addr + kk * 4096, kTileBytes) : f8_desc(a_addr + kk * 32, 16),
+                                   B_MN ? f8_desc(b_addr + kk * 4096, kTileBytes) : f8_desc(b_addr + kk * 32, 16), IDESC,
+                                   kk != 0 ? 1u : 0u);
+                    f8_commit<CG>(&empty[stage]);
+                    f8_commit<CG>(&tfull[buf]);
+                    if (++stage == C::STAGES) stage = 0, phase ^= 1;
+                    if (++buf == C::BUFS) buf = 0, bphase ^= 1;
+                }
+            }
+            if (CG == 1)
+                mma_commit(drain);
+            else
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
+                             : "memory");
+            f8_drain(drain, 0);  // every product is complete before TMEM is released
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    } else {
+        // ---------------- sums over the blocks, and results
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        float* my_staging = staging + (warp - 4) * kStageFloats;
+        const uint32_t lanes = tmem + (uint32_t(q * 32) << 16);
+        int slot = 0, buf = 0;
+        uint32_t sphase = 0, bphase = 0;
+        bool ok = true;
+        for (int i = first; i < items; i += step) {
+            const Item t = f8_item<OP, BN, CG>(i, a, rank);
+            float acc[HALF];
+#pragma unroll
+            for (int j = 0; j < HALF; ++j) acc[j] = 0.0f;
+            for (int kb = t.k_lo; kb < t.k_hi; ++kb) {
+                if (ok) ok = __all_sync(0xffffffffu, f8_wait<1>(&sfull[slot], sphase, abort_flag) &&
+                                                         f8_wait<CG>(&tfull[buf], bphase, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                const float* sl = slots + slot * C::SLOT_FLOATS;
+                const float row = sl[q * 32 + lane];
+                // the columns' factor: one for each of the warp's two 64-column groups (F8_GU: gate and up), or a vector
+                const float f0 = OP == F8_TN ? row : row * sl[128 + (OP == F8_GU || BN == 128 ? 0 : half)];
+                const float f1 = OP == F8_GU ? row * sl[129] : f0;
+                const float4* cols = reinterpret_cast<const float4*>(sl + 128 + half * HALF);
+                auto at = [&](int c) {  // TMEM column of the warp's c-th group of 16
+                    return lanes + uint32_t(buf * BN) +
+                           uint32_t(OP == F8_GU ? (c < 4 ? 64 * half + 16 * c : 128 + 64 * half + 16 * (c - 4)) : half * HALF + 16 * c);
+                };
+                uint32_t v[2][16];
+                tmem_ask16(at(0), v[0]);
+#pragma unroll
+                for (int c = 0; c < HALF / 16; ++c) {
+                    tmem_ready(v[c & 1]);
+                    if (c + 1 < HALF / 16) {
+                        tmem_ask16(at(c + 1), v[(c + 1) & 1]);
+                    } else {  // the buffer is read
+                        tc_fence_before();
+                        __syncwarp();
+                    }
+                    const float f = c < HALF / 32 ? f0 : f1;
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        float4 cf = make_float4(f, f, f, f);
+                        if (OP == F8_TN) {
+                            const float4 w = cols[4 * c + z];
+                            cf = make_float4(f * w.x, f * w.y, f * w.z, f * w.w);
+                        }
+                        const uint32_t* x = v[c & 1] + 4 * z;
+                        float* y = acc + 16 * c + 4 * z;
+                        y[0] = fmaf(__uint_as_float(x[0]), cf.x, y[0]);
+                        y[1] = fmaf(__uint_as_float(x[1]), cf.y, y[1]);
+                        y[2] = fmaf(__uint_as_float(x[2]), cf.z, y[2]);
+                        y[3] = fmaf(__uint_as_float(x[3]), cf.w, y[3]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 1)
+                        mbar_arrive(&tempty[buf]);
+                    else
+                        arrive_cluster(in_leader(&tempty[buf]));
+                }
+                if (++slot == C::SLOTS) slot = 0, sphase ^= 1;
+                if (++buf == C::BUFS) buf = 0, bphase ^= 1;
+            }
+            if (!ok) {
+#pragma unroll
+                for (int j = 0; j < HALF; ++j) acc[j] = __uint_as_float(0x7fffffffu);
+            }
+            const F8Out& o = a.o[t.p];
+            if constexpr (OP == F8_GU) {
+                gated_results(a, t, acc, q, half, most);
+            } else {
+                const bool part = a.splits > 1;
+                void* out = part ? static_cast<void*>(o.partial + int64_t(t.ks) * o.M * o.ld_partial) : o.out;
+                const int64_t ld = part ? o.ld_partial : o.ld;
+                const bool bf16 = !part && o.bf16;
+                const bool wide = ((reinterpret_cast<uintptr_t>(out) | uintptr_t(ld) * (bf16 ? 2 : 4)) & (bf16 ? 7 : 15)) == 0;
+#pragma unroll
+                for (int c = 0; c < HALF / 16; ++c)
+                    if (t.n0 + half * HALF + 16 * c < o.N)
+                        f8_store16(o, out, ld, bf16, !part && o.accumulate, wide, t.m0 + q * 32, t.n0 + half * HALF + 16 * c,
+                                   acc + 16 * c, my_staging);
+            }
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        f8_tmem_free<CG>(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- sums of the parts
+// out = the partials' sum in their order (plus out); blockIdx.y: the product
+__global__ void __launch_bounds__(256) f8_reduce_kernel(const __grid_constant__ F8Args a) {
+    pdl_wait();
+    pdl_trigger();
+    const F8Out& o = a.o[blockIdx.y];
+    const int quads = (o.N + 3) / 4;
+    const int64_t total = int64_t(o.M) * quads, plane = int64_t(o.M) * o.ld_partial;
+    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += int64_t(gridDim.x) * blockDim.x) {
+        const int64_t m = i / quads;
+        const int n = int(i - m * quads) * 4;
+        float4 sum = make_float4(0, 0, 0, 0);
+        const float* src = o.partial + m * o.ld_partial + n;  // ld_partial is a multiple of 4: the last words past N are not used
+        for (int s = 0; s < a.splits; ++s) {
+            const float4 x = __ldcs(reinterpret_cast<const float4*>(src + s * plane));
+            sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+        }
+        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+            if (n + z < o.N) store_one(o.out, m * o.ld + n + z, o.bf16, o.accumulate, v[z]);
+    }
+}
+
+template <auto Kernel>
+cudaError_t allow(size_t smem) {  // said once for each device
+    static std::atomic<uint64_t> said{0};
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (device & 63);
+    if (device < 64 && (said.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e == cudaSuccess) said.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+template <int OP, int BN, int CG>
+cudaError_t launch_one(const F8Maps& maps, const F8Args& a, int sms, cudaStream_t st) {
+    using C = F8Cfg<OP, BN, CG>;
+    constexpr auto kernel = f8_gemm_kernel<OP, BN, CG>;
+    const cudaError_t e = allow<kernel>(C::SMEM);
+    if (e != cudaSuccess) return e;
+    int64_t items = 0;
+    for (int p = 0; p < (OP == F8_TN ? a.products : 1); ++p) items += int64_t(a.o[p].m_tiles) * a.o[p].n_tiles;
+    items *= a.splits;
+    const int grid = int(items < sms / CG ? items : sms / CG) * CG;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(kF8Threads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 1 ? 1 : 2;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, kernel, maps, a);
+}
+
+template <int OP>
+cudaError_t launch_op(int bn, int cg, const F8Maps& maps, const F8Args& a, int sms, cudaStream_t st) {
+    if (cg == 2) return launch_one<OP, 256, 2>(maps, a, sms, st);
+    if constexpr (OP != F8_GU)
+        if (bn == 128) return launch_one<OP, 128, 1>(maps, a, sms, st);
+    return launch_one<OP, 256, 1>(maps, a, sms, st);
+}
+
+}  // namespace
+
+cudaError_t launch_f8_gemm(int op, int bn, int cg, const F8Maps& maps, const F8Args& a, int sms, cudaStream_t st) {
+    switch (op) {
+        case F8_NT: return launch_op<F8_NT>(bn, cg, maps, a, sms, st);
+        case F8_NN: return launch_op<F8_NN>(bn, cg, maps, a, sms, st);
+        case F8_TN: return launch_op<F8_TN>(bn, cg, maps, a, sms, st);
+        default: return launch_op<F8_GU>(bn, cg, maps, a, sms, st);
+    }
+}
+
+cudaError_t launch_f8_reduce(const F8Args& a, cudaStream_t st) {
+    int64_t most = 0;
+    for (int p = 0; p < a.products; ++p) {
+        const int64_t n = int64_t(a.o[p].M) * ((a.o[p].N + 3) / 4);
+        most = n > most ? n : most;
+    }
+    const int64_t blocks = (most + 255) / 256;
+    count_launch();
+    return launch_pdl(f8_reduce_kernel, dim3(unsigned(blocks < 4096 ? blocks : 4096), unsigned(a.products)), dim3(256), 0, st, a);
+}
+
+}  // namespace moe
