@@ -435,10 +435,10 @@ Plan prepare(int op, F8Args& a, Arena& ws) {
     return pl;
 }
 
-// boxes of 128 bytes (columns) x 128 rows
-bool map_of(CUtensorMap& m, const void* q, int64_t ld, int64_t rows, int64_t cols) {
+// boxes of 128 bytes (columns) x box_rows
+bool map_of(CUtensorMap& m, const void* q, int64_t ld, int64_t rows, int64_t cols, uint32_t box_rows = 128) {
     const uint64_t dims[2] = {uint64_t(cols), uint64_t(rows)}, strides[1] = {uint64_t(ld)};
-    const uint32_t box[2] = {128, 128};
+    const uint32_t box[2] = {128, box_rows};
     return encode_map(&m, q, 2, dims, strides, box, MAP_U8);
 }
 
@@ -561,8 +561,8 @@ cudaError_t ffn_forward(const FfnCall& k, Arena& ws, bool run, cudaStream_t st) 
         a.u = k.ku.q, a.us = k.ku.s, a.ld_u = k.ku.ld;
         a.limit = k.c->swiglu_limit;
         F8Maps m;
-        if (!map_of(m.a[0], xq.q, xq.ld, T, H) || !map_of(m.b[0], k.gate.q, k.gate.ld, I, H) ||
-            !map_of(m.b[1], k.up.q, k.up.ld, I, H))
+        if (!map_of(m.a[0], xq.q, xq.ld, T, H) || !map_of(m.b[0], k.gate.q, k.gate.ld, I, H, 64) ||
+            !map_of(m.b[1], k.up.q, k.up.ld, I, H, 64))
             return cudaErrorInvalidValue;
         e = multiply(F8_GU, pl, m, a, st);
         if (e != cudaSuccess) return e;

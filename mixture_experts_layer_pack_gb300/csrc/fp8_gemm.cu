@@ -2,17 +2,20 @@
 //
 //   out[m,n] = sum over blocks kb of 128 of  sa(m,kb) sb(n,kb) sum over k in kb of qa[m,k] qb[n,k]
 //
-// The inner sums are tcgen05.mma products of one K block (four K = 32 steps) into a TMEM buffer; the
+// The inner sums are tcgen05.mma products of one K block (four K = 32 steps) into one of two TMEM buffers; the
 // scales are arbitrary fp32 numbers, so the outer sum is the CUDA cores': the epilogue warps read each
 // block's sums from TMEM and add them, scaled, to fp32 accumulators in registers, while the tensor
-// cores fill the next buffer. At a 128 x 256 tile a block takes the tensor cores 512 cycles (8192 E4M3
-// multiply-adds a cycle and SM), and the reads and multiply-adds of the eight epilogue warps about 400.
+// cores fill the other buffer. For a block of a 128 x 256 tile the tensor cores take 512 cycles (8192 E4M3
+// multiply-adds a cycle and SM), and the epilogue, if it is alone, 300: paired multiply-adds, as single ones leave the
+// thread that issues the products too few issue slots (a block 737 cycles instead of 512, measured with nothing else).
 //
-// Warp 0 loads operands (TMA, 128-byte swizzle) and scales (4-byte cp.async, which take any
-// alignment) into two rings, warp 1 issues the products, warps 4..11 hold the accumulators: two warps a
-// quarter of the 128 TMEM lanes, half of the columns each. A weight is stored once: the product with it
+// Warp 0 loads operands (TMA, 128-byte swizzle), warp 1 issues the products, warps 4..11 hold the accumulators: two warps a
+// quarter of the 128 TMEM lanes, half of the columns each. Rows' scales are read into their registers; for a weight's
+// gradient, whose columns have scales of their own, warp 2 brings those to shared memory (4-byte cp.async, which take any
+// alignment). A weight is stored once: the product with it
 // and the one with its transpose read the same codes, K-major and MN-major (8-bit operands may be
-// either), and so do the two operands of a weight's gradient, whose K are the tokens.
+// either), and so do the two operands of a weight's gradient, whose K are the tokens. A pair of CTAs shares a tile
+// of 256 x 256 where there are tiles enough: each loads half of it, half of what two tiles of 128 x 256 would.
 //
 // Every wait is bounded; after one that gave up the results are NaN (there is no status word to say it in).
 #include "device_common.cuh"
@@ -41,21 +44,18 @@ struct F8Cfg {
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = int(196608 / STAGE_BYTES);
     static constexpr int BUFS = 512 / BN;
-    // A block's scales are written when its stage is free, that is when the products of the block STAGES before it are
-    // complete, which began after the epilogue had read the sums (and the scales) of the block BUFS before that.
-    static constexpr int SLOTS = STAGES + BUFS + 2;
-    static constexpr int COL_SCALES = OP == F8_TN ? BN : 4;
-    static constexpr int SLOT_FLOATS = 128 + COL_SCALES;
+    static constexpr int SLOTS = 8;         // blocks whose scales are on their way or in use
+    static constexpr int SLOT_FLOATS = OP == F8_TN ? BN : 0;
     static constexpr size_t SMEM = size_t(STAGES) * STAGE_BYTES + kF8EpiWarps * kStageFloats * 4 +
                                    size_t(SLOTS) * SLOT_FLOATS * 4 + (OP == F8_GU ? 4 * 128 * 2 * 4 : 0) + 1024 + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
 
 // ---------------------------------------------------------------- PTX
-__device__ __forceinline__ uint64_t f8_desc(uint32_t addr, uint32_t lbo) {  // 128-byte swizzle, 8-row groups 1024 bytes apart
-    return uint64_t((addr >> 4) & 0x3FFF) | (uint64_t((lbo >> 4) & 0x3FFF) << 16) | (uint64_t(1024 >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
-}
+// Shared-memory descriptor, 128-byte swizzle, 8-row groups 1024 bytes apart: the low word's lowest 14 bits are the address / 16, so an
+// offset is added to it; the high word is a constant
+__device__ __forceinline__ uint32_t f8_desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4) << 16; }
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
 
 __device__ __forceinline__ uint32_t cta_rank() {
     uint32_t r;
@@ -91,18 +91,18 @@ __device__ __forceinline__ void f8_load(void* dst, const void* map, uint32_t bar
 }
 
 template <int CG>
-__device__ __forceinline__ void f8_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void f8_mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
     if (CG == 1)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(kDescHi), "r"(accumulate)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(kDescHi), "r"(accumulate)
             : "memory");
 }
 
@@ -137,38 +137,32 @@ __device__ __forceinline__ void f8_tmem_free(uint32_t addr, uint32_t cols) {
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 
-// an arrival at a barrier of the pair's first CTA (its shared::cluster address)
+// An arrival at a barrier of this CTA or of the pair's first (its shared::cluster address). What it orders are reads of TMEM, whose fence
+// is tcgen05's own: release and acquire of the cluster's scope beside it made every block wait for a memory barrier
+// (8192 x 7168 x 4096 forward: 519 us with them).
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // bounded wait; gives up when another role of the CTA did, or after kWaitLimitNs
-template <int CG>
 __device__ __forceinline__ bool f8_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    auto ready = [&] { return CG == 1 ? mbar_try_wait(bar, parity) : try_wait_cluster(bar, parity); };
-    if (ready()) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     while (true) {
         for (int i = 0; i < 16; ++i)
-            if (ready()) return true;
+            if (mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
             *abort = 1;
             return false;
         }
     }
+}
+
+// The same for a warp. All lanes ask: one that asks for the others, and their vote, lengthens the way round of a buffer (8192 x 7168 x 4096
+// forward 219 us, 204 like this).
+__device__ __forceinline__ bool f8_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, f8_wait(bar, parity, abort));
 }
 
 // the same while winding down: whatever the others did
@@ -187,7 +181,7 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// 32 lanes x 16 columns; the registers are valid after tmem_ready
+// 32 lanes x 16 columns; the registers are valid after tmem_wait
 __device__ __forceinline__ void tmem_ask16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -196,13 +190,22 @@ __device__ __forceinline__ void tmem_ask16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_ready(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// two fp32 numbers in a register pair, and the paired operations on them (one instruction each)
+__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(a), "r"(b));
+    return p;
 }
+__device__ __forceinline__ uint64_t pair(float a, float b) { return pair(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+    return p;
+}
+__device__ __forceinline__ void fma2(uint64_t& y, uint64_t a, uint64_t b) { asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(y) : "l"(a), "l"(b)); }
 
 // ---------------------------------------------------------------- work items
 struct Item {
@@ -379,7 +382,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
     uint64_t* tfull = empty + C::STAGES;
     uint64_t* tempty = tfull + C::BUFS;
     uint64_t* sfull = tempty + C::BUFS;
-    uint64_t* drain = sfull + C::SLOTS;
+    uint64_t* sempty = sfull + C::SLOTS;
+    uint64_t* drain = sempty + C::SLOTS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
         for (int b = 0; b < C::BUFS; ++b) mbar_init(&tfull[b], 1), mbar_init(&tempty[b], CG * kF8EpiWarps);
-        for (int s = 0; s < C::SLOTS; ++s) mbar_init(&sfull[s], 32);
+        for (int s = 0; s < C::SLOTS; ++s) mbar_init(&sfull[s], 32), mbar_init(&sempty[s], kF8EpiWarps);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -411,70 +415,45 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
     const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
     if (warp == 0) {
-        // ---------------- loads
+        // ---------------- operands
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-        int stage = 0, slot = 0;
-        uint32_t phase = 0, filled = 0, fill_parity = 0;
-        bool ok = true;
-        for (int i = first; ok && i < items; i += step) {
-            const Item t = f8_item<OP, BN, CG>(i, a, rank);
-            const F8Out& o = a.o[t.p];
-            for (int kb = t.k_lo; kb < t.k_hi; ++kb) {
-                ok = __all_sync(0xffffffffu, f8_wait<CG>(&empty[stage], phase ^ 1, abort_flag));
-                if (!ok) break;
-                const int part = OP == F8_TN ? t.p : (OP == F8_NN && kb >= a.k_part ? 1 : 0);
-                const int kl = OP == F8_NN && part ? kb - a.k_part : kb;
-                const F8Scales& s = a.s[part];
-                float* sl = slots + slot * C::SLOT_FLOATS;
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                    copy4(sl + lane + 32 * z, s.a + int64_t(kl) * s.ld_a + min(t.m0 + lane + 32 * z, o.M - 1));
-                if (OP == F8_TN) {
-#pragma unroll
-                    for (int z = 0; z < BN / 32; ++z)
-                        copy4(sl + 128 + lane + 32 * z, s.b + int64_t(kl) * s.ld_b + min(t.n0 + lane + 32 * z, o.N - 1));
-                } else if (lane < BN / 128) {
-                    // F8_GU: the gate's scale and the up weight's; else those of the tile's one or two blocks of columns
-                    const F8Scales& w = OP == F8_GU ? a.s[lane] : s;
-                    const int nb = OP == F8_GU ? t.n0 >> 7 : min((t.n0 >> 7) + lane, (o.N - 1) >> 7);
-                    copy4(sl + 128 + lane, w.b + (OP == F8_NN ? int64_t(kl) * w.ld_b + nb : int64_t(nb) * w.ld_b + kl));
-                }
-                copies_arrive(&sfull[slot]);
-                if (lane == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, filled = 0, fill_parity = 0;
+            bool ok = true;
+            const uint32_t bars = CG == 1 ? smem_u32(full) : in_leader(full);
+            for (int i = first; ok && i < items; i += step) {
+                const Item t = f8_item<OP, BN, CG>(i, a, rank);
+                const int b0 = OP == F8_GU ? t.n0 + 64 * int(rank) * (CG - 1) : t.n0 + 128 * int(rank);  // first of this CTA's part of B
+                for (int kb = t.k_lo; kb < t.k_hi; ++kb) {
+                    ok = f8_wait(&empty[stage], phase ^ 1, abort_flag);
+                    if (!ok) break;
+                    const int part = OP == F8_TN ? t.p : (OP == F8_NN && kb >= a.k_part ? 1 : 0);
+                    const int k0 = (OP == F8_NN && part ? kb - a.k_part : kb) * 128;
                     uint8_t* sa = smem + stage * C::STAGE_BYTES;
                     uint8_t* sb = sa + C::A_BYTES;
+                    const uint32_t bar = bars + 8 * stage;
                     if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * C::STAGE_BYTES);
-                    const uint32_t bar = CG == 1 ? smem_u32(&full[stage]) : in_leader(&full[stage]);
-                    const CUtensorMap* mA = &maps.a[part];
-                    const CUtensorMap* mB = &maps.b[part];
-                    const int k0 = kl * 128;
-                    if (A_MN)
-                        f8_load<CG>(sa, mA, bar, t.m0, k0);
-                    else
-                        f8_load<CG>(sa, mA, bar, k0, t.m0);
+                    f8_load<CG>(sa, &maps.a[part], bar, A_MN ? t.m0 : k0, A_MN ? k0 : t.m0);
 #pragma unroll
                     for (int c = 0; c < BN / 128 / CG; ++c) {
-                        const int chunk = c + int(rank) * (BN / 128 / CG);
                         uint8_t* dst = sb + c * kTileBytes;
-                        if (OP == F8_GU)
-                            f8_load<CG>(dst, &maps.b[chunk], bar, k0, t.n0);
-                        else if (B_MN)
-                            f8_load<CG>(dst, mB, bar, t.n0 + 128 * chunk, k0);
-                        else
-                            f8_load<CG>(dst, mB, bar, k0, t.n0 + 128 * chunk);
+                        if (OP == F8_GU) {  // 64 columns of the gate beside the same 64 of the up weight, so that a warp gets both
+                            f8_load<CG>(dst, &maps.b[0], bar, k0, b0 + 64 * c);
+                            f8_load<CG>(dst + 8192, &maps.b[1], bar, k0, b0 + 64 * c);
+                        } else {
+                            f8_load<CG>(dst, &maps.b[part], bar, B_MN ? b0 + 128 * c : k0, B_MN ? k0 : b0 + 128 * c);
+                        }
                     }
+                    filled |= 1u << stage;
+                    fill_parity = (fill_parity & ~(1u << stage)) | (phase << stage);
+                    if (++stage == C::STAGES) stage = 0, phase ^= 1;
                 }
-                __syncwarp();
-                filled |= 1u << stage;
-                fill_parity = (fill_parity & ~(1u << stage)) | (phase << stage);
-                if (++stage == C::STAGES) stage = 0, phase ^= 1;
-                if (++slot == C::SLOTS) slot = 0;
             }
+            if (!ok && rank == 0)  // every copy lands before the memory is given back (the first CTA's barriers count both CTAs')
+                for (int s = 0; s < C::STAGES; ++s)
+                    if (filled & (1u << s)) f8_drain(&full[s], (fill_parity >> s) & 1);
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (!ok && rank == 0)  // every copy lands before the memory is given back (the first CTA's barriers count both CTAs')
-            for (int s = 0; s < C::STAGES; ++s)
-                if (filled & (1u << s)) f8_drain(&full[s], (fill_parity >> s) & 1);
         __syncwarp();
     } else if (warp == 1) {
         // ---------------- products
@@ -483,22 +462,22 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
             int stage = 0, buf = 0;
             uint32_t phase = 0, bphase = 0;
             bool ok = true;
+            const uint32_t a_base = f8_desc_lo(smem_u32(smem), A_MN ? kTileBytes : 16);
+            const uint32_t b_base = f8_desc_lo(smem_u32(smem) + C::A_BYTES, B_MN ? kTileBytes : 16);
             for (int i = first; ok && i < items; i += step) {
                 const Item t = f8_item<OP, BN, CG>(i, a, rank);
                 for (int kb = t.k_lo; kb < t.k_hi; ++kb) {
-                    ok = f8_wait<CG>(&tempty[buf], bphase ^ 1, abort_flag) && f8_wait<CG>(&full[stage], phase, abort_flag);
+                    ok = f8_wait(&full[stage], phase, abort_flag) && f8_wait(&tempty[buf], bphase ^ 1, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(smem + stage * C::STAGE_BYTES), b_addr = a_addr + C::A_BYTES;
+                    const uint32_t d = tmem + buf * BN, al = a_base + stage * (C::STAGE_BYTES >> 4), bl = b_base + stage * (C::STAGE_BYTES >> 4);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        f8_mma<CG>(tmem + buf * BN, A_MN ? f8_desc(a_addr + kk * 4096, kTileBytes) : f8_desc(a_addr + kk * 32, 16),
-                                   B_MN ? f8_desc(b_addr + kk * 4096, kTileBytes) : f8_desc(b_addr + kk * 32, 16), IDESC,
-                                   kk != 0 ? 1u : 0u);
-                    f8_commit<CG>(&empty[stage]);
+                        f8_mma<CG>(d, al + kk * (A_MN ? 4096 >> 4 : 32 >> 4), bl + kk * (B_MN ? 4096 >> 4 : 32 >> 4), IDESC, kk != 0 ? 1u : 0u);
                     f8_commit<CG>(&tfull[buf]);
-                    if (++stage == C::STAGES) stage = 0, phase ^= 1;
+                    f8_commit<CG>(&empty[stage]);
                     if (++buf == C::BUFS) buf = 0, bphase ^= 1;
+                    if (++stage == C::STAGES) stage = 0, phase ^= 1;
                 }
             }
             if (CG == 1)
@@ -509,6 +488,31 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
             f8_drain(drain, 0);  // every product is complete before TMEM is released
         }
         __syncwarp();
+    } else if (OP == F8_TN && warp == 2) {
+        // ---------------- scales of the columns
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int i = first; ok && i < items; i += step) {
+            const Item t = f8_item<OP, BN, CG>(i, a, rank);
+            const F8Scales& s = a.s[t.p];
+            int at[BN / 32];  // columns past the last take its scale: nothing reads their sums
+#pragma unroll
+            for (int z = 0; z < BN / 32; ++z) at[z] = min(t.n0 + lane + 32 * z, a.o[t.p].N - 1);
+            const float* from = s.b + t.k_lo * s.ld_b;
+            for (int kb = t.k_lo; kb < t.k_hi; ++kb) {
+                ok = f8_wait_warp(&sempty[slot], phase ^ 1, abort_flag);
+                if (!ok) break;
+                float* sl = slots + slot * C::SLOT_FLOATS + lane;
+#pragma unroll
+                for (int z = 0; z < BN / 32; ++z) copy4(sl + 32 * z, from + at[z]);
+                copies_arrive(&sfull[slot]);
+                from += s.ld_b;
+                if (++slot == C::SLOTS) slot = 0, phase ^= 1;
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     } else {
@@ -520,70 +524,95 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
         int slot = 0, buf = 0;
         uint32_t sphase = 0, bphase = 0;
         bool ok = true;
+        const uint32_t given = CG == 1 ? smem_u32(tempty) : in_leader(tempty);
         for (int i = first; i < items; i += step) {
             const Item t = f8_item<OP, BN, CG>(i, a, rank);
-            float acc[HALF];
+            uint64_t acc[HALF / 2];
 #pragma unroll
-            for (int j = 0; j < HALF; ++j) acc[j] = 0.0f;
-            for (int kb = t.k_lo; kb < t.k_hi; ++kb) {
-                if (ok) ok = __all_sync(0xffffffffu, f8_wait<1>(&sfull[slot], sphase, abort_flag) &&
-                                                         f8_wait<CG>(&tfull[buf], bphase, abort_flag));
-                if (!ok) break;
-                tc_fence_after();
-                const float* sl = slots + slot * C::SLOT_FLOATS;
-                const float row = sl[q * 32 + lane];
-                // the columns' factor: one for each of the warp's two 64-column groups (F8_GU: gate and up), or a vector
-                const float f0 = OP == F8_TN ? row : row * sl[128 + (OP == F8_GU || BN == 128 ? 0 : half)];
-                const float f1 = OP == F8_GU ? row * sl[129] : f0;
-                const float4* cols = reinterpret_cast<const float4*>(sl + 128 + half * HALF);
-                auto at = [&](int c) {  // TMEM column of the warp's c-th group of 16
-                    return lanes + uint32_t(buf * BN) +
-                           uint32_t(OP == F8_GU ? (c < 4 ? 64 * half + 16 * c : 128 + 64 * half + 16 * (c - 4)) : half * HALF + 16 * c);
-                };
-                uint32_t v[2][16];
-                tmem_ask16(at(0), v[0]);
-#pragma unroll
-                for (int c = 0; c < HALF / 16; ++c) {
-                    tmem_ready(v[c & 1]);
-                    if (c + 1 < HALF / 16) {
-                        tmem_ask16(at(c + 1), v[(c + 1) & 1]);
-                    } else {  // the buffer is read
-                        tc_fence_before();
-                        __syncwarp();
-                    }
-                    const float f = c < HALF / 32 ? f0 : f1;
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        float4 cf = make_float4(f, f, f, f);
-                        if (OP == F8_TN) {
-                            const float4 w = cols[4 * c + z];
-                            cf = make_float4(f * w.x, f * w.y, f * w.z, f * w.w);
-                        }
-                        const uint32_t* x = v[c & 1] + 4 * z;
-                        float* y = acc + 16 * c + 4 * z;
-                        y[0] = fmaf(__uint_as_float(x[0]), cf.x, y[0]);
-                        y[1] = fmaf(__uint_as_float(x[1]), cf.y, y[1]);
-                        y[2] = fmaf(__uint_as_float(x[2]), cf.z, y[2]);
-                        y[3] = fmaf(__uint_as_float(x[3]), cf.w, y[3]);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 1)
-                        mbar_arrive(&tempty[buf]);
-                    else
-                        arrive_cluster(in_leader(&tempty[buf]));
-                }
-                if (++slot == C::SLOTS) slot = 0, sphase ^= 1;
-                if (++buf == C::BUFS) buf = 0, bphase ^= 1;
-            }
-            if (!ok) {
-#pragma unroll
-                for (int j = 0; j < HALF; ++j) acc[j] = __uint_as_float(0x7fffffffu);
-            }
+            for (int j = 0; j < HALF / 2; ++j) acc[j] = 0;
+            // The scales of this row, and those of the columns but for F8_TN's: read two blocks ahead, into registers (beside the products'
+            // reads of their operands a read of shared memory takes some hundred cycles).
             const F8Out& o = a.o[t.p];
+            const int row = min(t.m0 + q * 32 + lane, o.M - 1);  // rows past the last are not stored
+            const int nb = min((t.n0 + (OP == F8_GU ? 0 : HALF * half)) >> 7, (o.N - 1) >> 7);
+            const float *pr, *pc0, *pc1;
+            int64_t step_r, step_c;
+            auto from = [&](int part, int kl) {
+                const F8Scales& s = a.s[part];
+                step_r = s.ld_a, pr = s.a + kl * step_r + row;
+                step_c = OP == F8_NN ? s.ld_b : 1, pc0 = OP == F8_NN ? s.b + kl * step_c + nb : s.b + nb * s.ld_b + kl;
+                if (OP == F8_GU) pc1 = a.s[1].b + nb * a.s[1].ld_b + kl;
+            };
+            auto fetch = [&](float& r, float& c0, float& c1) {
+                r = __ldg(pr);
+                if (OP != F8_TN) c0 = __ldg(pc0);
+                if (OP == F8_GU) c1 = __ldg(pc1);
+            };
+            auto next = [&] {
+                pr += step_r, pc0 += step_c;
+                if (OP == F8_GU) pc1 += 1;
+            };
+            for (int kb = t.k_lo; kb < t.k_hi;) {  // once, or once for each part of K
+                const int part = OP == F8_TN ? t.p : OP == F8_NN && kb >= a.k_part ? 1 : 0;
+                const int end = OP == F8_NN && part == 0 ? min(t.k_hi, a.k_part) : t.k_hi;
+                from(part, OP == F8_NN && part ? kb - a.k_part : kb);
+                float r0, r1, c00 = 1.0f, c01 = 1.0f, c10 = 1.0f, c11 = 1.0f;
+                fetch(r0, c00, c10);
+                r1 = r0, c01 = c00, c11 = c10;
+                if (kb + 1 < end) next(), fetch(r1, c01, c11);
+                for (; kb < end; ++kb) {
+                    const float f0 = r0 * c00, f1 = OP == F8_GU ? r0 * c10 : f0;
+                    const uint64_t g0 = pair(f0, f0), g1 = OP == F8_GU ? pair(f1, f1) : g0;
+                    r0 = r1, c00 = c01, c10 = c11;
+                    if (kb + 2 < end) next(), fetch(r1, c01, c11);
+                    if (OP == F8_TN && ok) ok = f8_wait_warp(&sfull[slot], sphase, abort_flag);
+                    if (ok) ok = f8_wait_warp(&tfull[buf], bphase, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t v[2][16];
+                    const uint32_t at = lanes + uint32_t(buf * BN + HALF * half);
+                    tmem_ask16(at, v[0]);
+#pragma unroll
+                    for (int c = 0; c < HALF / 16; ++c) {
+                        tmem_wait();
+                        if (c + 1 < HALF / 16) {
+                            tmem_ask16(at + 16 * (c + 1), v[(c + 1) & 1]);
+                        } else {  // the buffer is read
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_cluster(given + 8 * buf);
+                        }
+                        const uint32_t(&x)[16] = v[c & 1];
+                        if (OP == F8_TN) {
+                            const float4* cols = reinterpret_cast<const float4*>(slots + slot * C::SLOT_FLOATS + HALF * half + 16 * c);
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                const float4 w = cols[z];
+                                fma2(acc[8 * c + 2 * z], pair(x[4 * z], x[4 * z + 1]), mul2(g0, pair(w.x, w.y)));
+                                fma2(acc[8 * c + 2 * z + 1], pair(x[4 * z + 2], x[4 * z + 3]), mul2(g0, pair(w.z, w.w)));
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) fma2(acc[8 * c + j], pair(x[2 * j], x[2 * j + 1]), c < HALF / 32 ? g0 : g1);
+                        }
+                    }
+                    if (OP == F8_TN) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sempty[slot]);
+                        if (++slot == C::SLOTS) slot = 0, sphase ^= 1;
+                    }
+                    if (++buf == C::BUFS) buf = 0, bphase ^= 1;
+                }
+                if (!ok) break;
+            }
+            float sum[HALF];
+#pragma unroll
+            for (int j = 0; j < HALF / 2; ++j) {
+                if (!ok) acc[j] = 0x7fffffff7fffffffull;
+                unpair(acc[j], sum[2 * j], sum[2 * j + 1]);
+            }
             if constexpr (OP == F8_GU) {
-                gated_results(a, t, acc, q, half, most);
+                gated_results(a, t, sum, q, half, most);
             } else {
                 const bool part = a.splits > 1;
                 void* out = part ? static_cast<void*>(o.partial + int64_t(t.ks) * o.M * o.ld_partial) : o.out;
@@ -591,10 +620,11 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
                 const bool bf16 = !part && o.bf16;
                 const bool wide = ((reinterpret_cast<uintptr_t>(out) | uintptr_t(ld) * (bf16 ? 2 : 4)) & (bf16 ? 7 : 15)) == 0;
 #pragma unroll
-                for (int c = 0; c < HALF / 16; ++c)
-                    if (t.n0 + half * HALF + 16 * c < o.N)
-                        f8_store16(o, out, ld, bf16, !part && o.accumulate, wide, t.m0 + q * 32, t.n0 + half * HALF + 16 * c,
-                                   acc + 16 * c, my_staging);
+                for (int c = 0; c < HALF / 16; ++c) {
+                    const int col = t.n0 + HALF * half + 16 * c;
+                    if (col < o.N)
+                        f8_store16(o, out, ld, bf16, !part && o.accumulate, wide, t.m0 + q * 32, col, sum + 16 * c, my_staging);
+                }
             }
         }
         __syncwarp();
