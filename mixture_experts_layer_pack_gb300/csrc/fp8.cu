@@ -4,7 +4,8 @@
 #include "fp8_device.cuh"
 #include "internal.h"
 
-#include <algorithm>
+#include <cuda_fp16.h>
+
 #include <cmath>
 
 namespace moe {
@@ -22,25 +23,71 @@ struct Codes {          // codes and compact scales; q null: not wanted
 };
 
 // ---------------------------------------------------------------- reading and writing eight columns
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, int n, bool wide, float (&v)[8]) {
-    if (wide && n >= 8) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-        unpack_bf16x2(w.x, v[0], v[1]), unpack_bf16x2(w.y, v[2], v[3]);
-        unpack_bf16x2(w.z, v[4], v[5]), unpack_bf16x2(w.w, v[6], v[7]);
-    } else {
+// Eight elements of a row as they were read, and the largest magnitudes of such: of bf16 two to a register, which the maximum
+// keeps (a NaN is not taken)
+template <typename X>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+    __nv_bfloat162 w[4];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int n, bool wide) {
+        if (wide && n >= 8) {
+            *reinterpret_cast<uint4*>(w) = __ldg(reinterpret_cast<const uint4*>(p));
+        } else {
+            const __nv_bfloat16 zero = __float2bfloat16(0.0f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < n ? __bfloat162float(p[j]) : 0.0f;
+            for (int j = 0; j < 4; ++j) w[j] = __nv_bfloat162(2 * j < n ? p[2 * j] : zero, 2 * j + 1 < n ? p[2 * j + 1] : zero);
+        }
     }
-}
-__device__ __forceinline__ void load8(const float* p, int n, bool wide, float (&v)[8]) {
-    if (wide && n >= 8) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
+    __device__ __forceinline__ void zero() { *reinterpret_cast<uint4*>(w) = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void most(Eight& m) const {  // m: magnitudes
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < n ? p[j] : 0.0f;
+        for (int j = 0; j < 4; ++j) m.w[j] = __hmax2(m.w[j], __habs2(w[j]));
     }
-}
+    __device__ __forceinline__ float most() const {
+        const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(w[0]), __habs2(w[1])), __hmax2(__habs2(w[2]), __habs2(w[3])));
+        const float a = __low2float(m), b = __high2float(m);
+        return fmaxf(fmaxf(a, b), 0.0f);  // two NaN are no maximum
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = __bfloat1622float2(w[j]);
+            v[2 * j] = f.x, v[2 * j + 1] = f.y;
+        }
+    }
+};
+template <>
+struct Eight<float> {
+    float w[8];
+    __device__ __forceinline__ void load(const float* p, int n, bool wide) {
+        if (wide && n >= 8) {
+            *reinterpret_cast<float4*>(w) = __ldg(reinterpret_cast<const float4*>(p));
+            *reinterpret_cast<float4*>(w + 4) = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = j < n ? p[j] : 0.0f;
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 0.0f;
+    }
+    __device__ __forceinline__ void most(Eight& m) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m.w[j] = fmaxf(m.w[j], fabsf(w[j]));
+    }
+    __device__ __forceinline__ float most() const {
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(w[j]));
+        return m;
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = w[j];
+    }
+};
 
 // eight codes of a row (8-byte aligned); its bytes past n are not ours
 __device__ __forceinline__ void store8(uint8_t* p, int n, uint32_t lo, uint32_t hi) {
@@ -53,19 +100,6 @@ __device__ __forceinline__ void store8(uint8_t* p, int n, uint32_t lo, uint32_t 
     }
 }
 
-__device__ __forceinline__ float most8(const float (&v)[8]) {
-    float m = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
-    return m;
-}
-
-__device__ __forceinline__ float most_of16(float m) {  // over 16 lanes that share a row
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    return m;
-}
-
 __device__ __forceinline__ void put8(uint8_t* p, int n, const float (&v)[8], const float (&r)[8]) {
     store8(p, n, e4m3x4(v[0] * r[0], v[1] * r[1], v[2] * r[2], v[3] * r[3]), e4m3x4(v[4] * r[4], v[5] * r[5], v[6] * r[6], v[7] * r[7]));
 }
@@ -73,15 +107,40 @@ __device__ __forceinline__ void put8(uint8_t* p, int n, const float (&v)[8], flo
     store8(p, n, e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r));
 }
 
+// Of N rows' (N = 4, 8) maxima over the 16 lanes that share them each lane gets one: that of row lane_row<N>(lane). Half of the rows go to the
+// other half of the lanes at every step, so that the sum of the exchanges is N and not 4 N.
+template <int N>
+__device__ __forceinline__ float spread_max(float (&m)[N]) {
+    const int lane = threadIdx.x & 15;
+    int d = 8;
+#pragma unroll
+    for (int n = N / 2; n >= 1; n /= 2, d /= 2) {
+        const bool high = lane & d;
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            const float other = __shfl_xor_sync(0xffffffffu, high ? m[j] : m[j + n], d);
+            m[j] = fmaxf(high ? m[j + n] : m[j], other);
+        }
+    }
+    for (; d >= 1; d /= 2) m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], d));
+    return m[0];
+}
+template <int N>  // the row of a lane, and the first lane that has a row (of 16)
+__device__ __forceinline__ int lane_row(int lane) { return N == 8 ? lane >> 1 & 7 : lane >> 2 & 3; }
+template <int N>
+__device__ __forceinline__ int row_lane(int row) { return N == 8 ? row << 1 : row << 2; }
+
 // ---------------------------------------------------------------- codes of a matrix
 // A block takes 128 x 128 elements, which it reads once and holds in registers: 16 threads a row with eight columns
 // each, a thread eight rows 16 apart. Rows' maxima go through 16 lanes, columns' through registers and shared memory.
+// Memory bounds it once enough blocks share an SM: bf16 is held as it was read, two to a register (64 registers a thread instead
+// of 116), and each scale's division is one lane's.
 template <typename X>
-__global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const X* __restrict__ x, int64_t rows, int cols, int64_t ld, bool wide,
-                                                                     Codes row, Codes col, Codes square) {
+__global__ void __launch_bounds__(kQuantThreads, sizeof(X) == 2 ? 4 : 2)
+    fp8_quantize_kernel(const X* __restrict__ x, int64_t rows, int cols, int64_t ld, bool wide, Codes row, Codes col, Codes square) {
     constexpr int W = kQuantThreads / 32;
     __shared__ float part[W][128];
-    __shared__ float scale[128], inv[128], row_scale[128];
+    __shared__ float scale[128], inv[128];
     pdl_wait();
     pdl_trigger();
     const int col_blocks = (cols + 127) >> 7;
@@ -89,47 +148,50 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const X* __
     const int cb = int(blockIdx.x - rb * col_blocks);
     const int c8 = threadIdx.x & 15, rg = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = cb * 128 + c8 * 8, n = cols - c0;  // n columns of this thread's (8 or more: all)
-    float v[8][8];
+    const int left = int(min(rows - rb * 128, int64_t(128)));
+    Eight<X> e[8];
+    const X* src = x + (rb * 128 + rg) * ld + c0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int64_t r = rb * 128 + rg + 16 * i;
-        if (r < rows && n > 0)
-            load8(x + r * ld + c0, n, wide, v[i]);
+        if (rg + 16 * i < left && n > 0)
+            e[i].load(src + 16 * i * ld, n, wide);
         else
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+            e[i].zero();
     }
     if (row.q) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t r = rb * 128 + rg + 16 * i;
-            const float s = block_scale(most_of16(most8(v[i])));
-            if (c8 == 0) row_scale[rg + 16 * i] = s;
-            if (r < rows && n > 0) put8(row.q + r * row.ld + c0, n, v[i], __frcp_rn(s));
-        }
-    }
-    if (col.q || square.q) {
         float m[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m[j] = 0.0f;
+        for (int i = 0; i < 8; ++i) m[i] = e[i].most();
+        const float s = block_scale(spread_max(m)), r = __frcp_rn(s);
+        const int mine = rg + 16 * lane_row<8>(c8);
+        if ((c8 & 1) == 0 && mine < left) row.s[cb * rows + rb * 128 + mine] = s;
+        uint8_t* dst = row.q + (rb * 128 + rg) * row.ld + c0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m[j] = fmaxf(m[j], fabsf(v[i][j]));
-            m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+        for (int i = 0; i < 8; ++i) {
+            float v[8];
+            e[i].values(v);
+            const float ri = __shfl_sync(0xffffffffu, r, row_lane<8>(i), 16);
+            if (rg + 16 * i < left && n > 0) put8(dst + 16 * i * row.ld, n, v, ri);
         }
-        if (lane < 16)
+    }
+    if (!col.q && !square.q) return;
+    Eight<X> most;
+    most.zero();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) part[warp][c8 * 8 + j] = m[j];
+    for (int i = 0; i < 8; ++i) e[i].most(most);
+    float m[8];
+    most.values(m);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+        if (lane < 16) part[warp][c8 * 8 + j] = m[j];
     }
     __syncthreads();
-    if (row.q && threadIdx.x < 128 && rb * 128 + threadIdx.x < rows)
-        row.s[cb * rows + rb * 128 + threadIdx.x] = row_scale[threadIdx.x];
-    if (!col.q && !square.q) return;
     if (threadIdx.x < 128) {
-        float m = 0.0f;
+        float t = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) m = fmaxf(m, part[w][threadIdx.x]);
-        const float s = block_scale(m);
+        for (int w = 0; w < W; ++w) t = fmaxf(t, part[w][threadIdx.x]);
+        const float s = block_scale(t);
         scale[threadIdx.x] = s;
         inv[threadIdx.x] = __frcp_rn(s);
         if (col.q && cb * 128 + int(threadIdx.x) < cols) col.s[rb * cols + cb * 128 + threadIdx.x] = s;
@@ -139,10 +201,12 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const X* __
         float r8[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) r8[j] = inv[c8 * 8 + j];
+        uint8_t* dst = col.q + (rb * 128 + rg) * col.ld + c0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int64_t r = rb * 128 + rg + 16 * i;
-            if (r < rows && n > 0) put8(col.q + r * col.ld + c0, n, v[i], r8);
+            float v[8];
+            e[i].values(v);
+            if (rg + 16 * i < left && n > 0) put8(dst + 16 * i * col.ld, n, v, r8);
         }
     }
     if (square.q) {
@@ -153,27 +217,33 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const X* __
         for (int d = 1; d < 32; d *= 2) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, d));
         if (threadIdx.x == 0) square.s[rb * col_blocks + cb] = s;
         const float rs = __frcp_rn(s);
+        uint8_t* dst = square.q + (rb * 128 + rg) * square.ld + c0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int64_t r = rb * 128 + rg + 16 * i;
-            if (r < rows && n > 0) put8(square.q + r * square.ld + c0, n, v[i], rs);
+            float v[8];
+            e[i].values(v);
+            if (rg + 16 * i < left && n > 0) put8(dst + 16 * i * square.ld, n, v, rs);
         }
     }
 }
 
 // ---------------------------------------------------------------- values of codes
-__device__ __forceinline__ void values8(const uint8_t* p, int n, float (&v)[8]) {
+__device__ __forceinline__ uint2 codes8(const uint8_t* p, int n) {
+    if (n >= 8) return __ldg(reinterpret_cast<const uint2*>(p));
     uint32_t w[2] = {0, 0};
-    if (n >= 8) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-        w[0] = x.x, w[1] = x.y;
-    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) w[j >> 2] |= uint32_t(p[j]) << (8 * (j & 3));
+    for (int j = 0; j < 8; ++j)
+        if (j < n) w[j >> 2] |= uint32_t(p[j]) << (8 * (j & 3));
+    return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void values8(uint2 w, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t((j < 2 ? w.x : w.y) >> (16 * (j & 1))), __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        v[2 * j] = f.x, v[2 * j + 1] = f.y;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = e4m3_value(w[j >> 2] >> (8 * (j & 3)));
 }
 
 template <typename Y>
@@ -186,32 +256,40 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_dequantize_kernel(const uin
     const int cb = int(blockIdx.x - rb * col_blocks);
     const int c8 = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const int c0 = cb * 128 + c8 * 8, n = cols - c0;
+    const int left = int(min(rows - rb * 128, int64_t(128)));
     if (n <= 0) return;
-    float s8[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        s8[j] = block == MOE_B_SQUARE ? s[rb * col_blocks + cb] : block == MOE_B_COL && j < n ? s[rb * cols + c0 + j] : 0.0f;
+    uint2 w[8];
+    float rs[8], s8[8];
+    const uint8_t* src = q + (rb * 128 + rg) * ldq + c0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int64_t r = rb * 128 + rg + 16 * i;
-        if (r >= rows) break;
-        float v[8];
-        values8(q + r * ldq + c0, n, v);
-        const float rs = block == MOE_B_ROW ? s[cb * rows + r] : 0.0f;
+        const bool in = rg + 16 * i < left;
+        w[i] = in ? codes8(src + 16 * i * ldq, n) : make_uint2(0, 0);
+        rs[i] = block == MOE_B_ROW && in ? __ldg(s + cb * rows + rb * 128 + rg + 16 * i) : 1.0f;
+    }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= block == MOE_B_ROW ? rs : s8[j];
-        Y* dst = out + r * ld + c0;
+    for (int j = 0; j < 8; ++j)
+        s8[j] = block == MOE_B_SQUARE ? __ldg(s + rb * col_blocks + cb) : block == MOE_B_COL && j < n ? __ldg(s + rb * cols + c0 + j) : 1.0f;
+    Y* dst = out + (rb * 128 + rg) * ld + c0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (rg + 16 * i >= left) continue;
+        float v[8];
+        values8(w[i], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= block == MOE_B_ROW ? rs[i] : s8[j];
+        Y* to = dst + 16 * i * ld;
         if (wide && n >= 8) {
             if constexpr (sizeof(Y) == 2) {
-                *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
             } else {
-                reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+                reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
             }
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (j < n) dst[j] = Y(v[j]);
+                if (j < n) to[j] = Y(v[j]);
         }
     }
 }
@@ -246,9 +324,9 @@ __device__ __forceinline__ void gated_back8(const float (&dh)[8], const float (&
 // 128 tokens x 128 columns a block; its inputs stay in registers, and the three results are computed twice, for the
 // maxima and for the codes (holding them would take 96 registers more).
 __global__ void __launch_bounds__(kGatedThreads) fp8_gated_back_kernel(const GatedBack a) {
-    constexpr int W = kGatedThreads / 32, R = 128 * 16 / kGatedThreads;
+    constexpr int W = kGatedThreads / 32, R = 128 * 16 / kGatedThreads, S = 128 / R;
     __shared__ float part[3][W][128];
-    __shared__ float inv[3][128], row_scale[2][128];
+    __shared__ float inv[3][128];
     pdl_wait();
     pdl_trigger();
     const int col_blocks = (a.I + 127) >> 7;
@@ -256,50 +334,47 @@ __global__ void __launch_bounds__(kGatedThreads) fp8_gated_back_kernel(const Gat
     const int cb = int(blockIdx.x - rb * col_blocks);
     const int c8 = threadIdx.x & 15, rg = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = cb * 128 + c8 * 8, n = a.I - c0;
-    float dh[R][8], sg[R], su[R];
+    const int left = int(min(a.T - rb * 128, int64_t(128)));
+    const int64_t row0 = rb * 128 + rg;
+    Eight<float> dh[R];
+    float sg[R], su[R];
     uint2 gq[R], uq[R];
-    float mc[3][8] = {};
-    auto eight = [](uint2 w, float (&v)[8]) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = e4m3_value((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
-    };
-    auto codes8 = [&](const uint8_t* p) {
-        if (n >= 8) return __ldg(reinterpret_cast<const uint2*>(p));
-        uint32_t w[2] = {0, 0};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) w[j >> 2] |= uint32_t(p[j]) << (8 * (j & 3));
-        return make_uint2(w[0], w[1]);
-    };
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int64_t r = rb * 128 + rg + (128 / R) * i;
-        const bool in = r < a.T && n > 0;
+        const int64_t r = row0 + S * i;
         gq[i] = uq[i] = make_uint2(0, 0);
         sg[i] = su[i] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dh[i][j] = 0.0f;
-        if (in) {
-            load8(a.dh + r * a.ld_dh + c0, n, true, dh[i]);
-            gq[i] = codes8(a.g.q + r * a.g.ld + c0);
-            uq[i] = codes8(a.u.q + r * a.u.ld + c0);
+        if (rg + S * i < left && n > 0) {
+            dh[i].load(a.dh + r * a.ld_dh + c0, n, true);
+            gq[i] = codes8(a.g.q + r * a.g.ld + c0, n);
+            uq[i] = codes8(a.u.q + r * a.u.ld + c0, n);
             sg[i] = __ldg(a.g.s + cb * a.T + r);
             su[i] = __ldg(a.u.s + cb * a.T + r);
+        } else {
+            dh[i].zero();
         }
     }
+    float mg[R], mu[R], mc[3][8] = {};
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         float g[8], u[8], dg[8], du[8], h[8];
-        eight(gq[i], g), eight(uq[i], u);
-        gated_back8(dh[i], g, sg[i], u, su[i], a.limit, dg, du, h);
-        const float s0 = block_scale(most_of16(most8(dg))), s1 = block_scale(most_of16(most8(du)));
-        if (c8 == 0) row_scale[0][rg + (128 / R) * i] = s0, row_scale[1][rg + (128 / R) * i] = s1;
+        values8(gq[i], g), values8(uq[i], u);
+        gated_back8(dh[i].w, g, sg[i], u, su[i], a.limit, dg, du, h);
+        mg[i] = mu[i] = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+            mg[i] = fmaxf(mg[i], fabsf(dg[j]));
+            mu[i] = fmaxf(mu[i], fabsf(du[j]));
             mc[0][j] = fmaxf(mc[0][j], fabsf(dg[j]));
             mc[1][j] = fmaxf(mc[1][j], fabsf(du[j]));
             mc[2][j] = fmaxf(mc[2][j], fabsf(h[j]));
         }
+    }
+    const float s0 = block_scale(spread_max(mg)), s1 = block_scale(spread_max(mu));
+    const float r0 = __frcp_rn(s0), r1 = __frcp_rn(s1);
+    if (a.dg_row.q && (c8 & 3) == 0) {
+        const int mine = rg + S * lane_row<R>(c8);
+        if (mine < left) a.dg_row.s[cb * a.T + rb * 128 + mine] = s0, a.du_row.s[cb * a.T + rb * 128 + mine] = s1;
     }
 #pragma unroll
     for (int z = 0; z < 3; ++z)
@@ -319,21 +394,18 @@ __global__ void __launch_bounds__(kGatedThreads) fp8_gated_back_kernel(const Gat
         float* to = z == 0 ? a.dg_col.s : z == 1 ? a.du_col.s : a.h_col.s;
         if (to && cb * 128 + c < a.I) to[rb * a.I + cb * 128 + c] = s;
     }
-    if (threadIdx.x < 256 && a.dg_row.q) {
-        const int z = threadIdx.x >> 7, r = threadIdx.x & 127;
-        if (rb * 128 + r < a.T) (z ? a.du_row.s : a.dg_row.s)[cb * a.T + rb * 128 + r] = row_scale[z][r];
-    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int64_t r = rb * 128 + rg + (128 / R) * i;
-        if (r >= a.T || n <= 0) continue;
+        const float q0 = __shfl_sync(0xffffffffu, r0, row_lane<R>(i), 16), q1 = __shfl_sync(0xffffffffu, r1, row_lane<R>(i), 16);
+        const int64_t r = row0 + S * i;
+        if (rg + S * i >= left || n <= 0) continue;
         float g[8], u[8], dg[8], du[8], h[8];
-        eight(gq[i], g), eight(uq[i], u);
-        gated_back8(dh[i], g, sg[i], u, su[i], a.limit, dg, du, h);
+        values8(gq[i], g), values8(uq[i], u);
+        gated_back8(dh[i].w, g, sg[i], u, su[i], a.limit, dg, du, h);
         if (a.dg_row.q) {
-            put8(a.dg_row.q + r * a.dg_row.ld + c0, n, dg, __frcp_rn(row_scale[0][rg + (128 / R) * i]));
-            put8(a.du_row.q + r * a.du_row.ld + c0, n, du, __frcp_rn(row_scale[1][rg + (128 / R) * i]));
+            put8(a.dg_row.q + r * a.dg_row.ld + c0, n, dg, q0);
+            put8(a.du_row.q + r * a.du_row.ld + c0, n, du, q1);
         }
         if (a.dg_col.q) {
             auto cols = [&](int z, const Codes& c, const float (&v)[8]) {
