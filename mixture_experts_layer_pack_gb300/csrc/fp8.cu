@@ -321,9 +321,10 @@ __device__ __forceinline__ void gated_back8(const float (&dh)[8], const float (&
 }
 
 // dh and the kept g, u -> dg and du as row blocks (for dx) and column blocks, h as column blocks (for the weights' gradients).
-// 128 tokens x 128 columns a block; its inputs stay in registers, and the three results are computed twice, for the
-// maxima and for the codes (holding them would take 96 registers more).
-__global__ void __launch_bounds__(kGatedThreads) fp8_gated_back_kernel(const GatedBack a) {
+// 128 tokens x 128 columns a block. The results are computed twice, for the maxima and for the codes, from inputs that are
+// read twice, the second time from L2: held in registers, they or the results leave room for one block an SM, whose reads,
+// arithmetic and writes then wait for one another (8192 x 8192: 335 us).
+__global__ void __launch_bounds__(kGatedThreads, 2) fp8_gated_back_kernel(const GatedBack a) {
     constexpr int W = kGatedThreads / 32, R = 128 * 16 / kGatedThreads, S = 128 / R;
     __shared__ float part[3][W][128];
     __shared__ float inv[3][128];
@@ -334,33 +335,26 @@ __global__ void __launch_bounds__(kGatedThreads) fp8_gated_back_kernel(const Gat
     const int cb = int(blockIdx.x - rb * col_blocks);
     const int c8 = threadIdx.x & 15, rg = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = cb * 128 + c8 * 8, n = a.I - c0;
-    const int left = int(min(a.T - rb * 128, int64_t(128)));
+    const int left = n > 0 ? int(min(a.T - rb * 128, int64_t(128))) : 0;  // rows of the block, for this thread
     const int64_t row0 = rb * 128 + rg;
-    Eight<float> dh[R];
-    float sg[R], su[R];
-    uint2 gq[R], uq[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
+    // dg, du, h of this thread's eight columns of its i-th row
+    auto results = [&](int i, float (&dg)[8], float (&du)[8], float (&h)[8]) {
         const int64_t r = row0 + S * i;
-        gq[i] = uq[i] = make_uint2(0, 0);
-        sg[i] = su[i] = 0.0f;
-        if (rg + S * i < left && n > 0) {
-            dh[i].load(a.dh + r * a.ld_dh + c0, n, true);
-            gq[i] = codes8(a.g.q + r * a.g.ld + c0, n);
-            uq[i] = codes8(a.u.q + r * a.u.ld + c0, n);
-            sg[i] = __ldg(a.g.s + cb * a.T + r);
-            su[i] = __ldg(a.u.s + cb * a.T + r);
-        } else {
-            dh[i].zero();
-        }
-    }
+        Eight<float> dh;
+        dh.load(a.dh + r * a.ld_dh + c0, n, true);
+        const uint2 gq = codes8(a.g.q + r * a.g.ld + c0, n), uq = codes8(a.u.q + r * a.u.ld + c0, n);
+        const float sg = __ldg(a.g.s + cb * a.T + r), su = __ldg(a.u.s + cb * a.T + r);
+        float g[8], u[8];
+        values8(gq, g), values8(uq, u);
+        gated_back8(dh.w, g, sg, u, su, a.limit, dg, du, h);
+    };
     float mg[R], mu[R], mc[3][8] = {};
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        float g[8], u[8], dg[8], du[8], h[8];
-        values8(gq[i], g), values8(uq[i], u);
-        gated_back8(dh[i].w, g, sg[i], u, su[i], a.limit, dg, du, h);
         mg[i] = mu[i] = 0.0f;
+        if (rg + S * i >= left) continue;
+        float dg[8], du[8], h[8];
+        results(i, dg, du, h);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             mg[i] = fmaxf(mg[i], fabsf(dg[j]));
@@ -373,8 +367,8 @@ __global__ void __launch_bounds__(kGatedThreads) fp8_gated_back_kernel(const Gat
     const float s0 = block_scale(spread_max(mg)), s1 = block_scale(spread_max(mu));
     const float r0 = __frcp_rn(s0), r1 = __frcp_rn(s1);
     if (a.dg_row.q && (c8 & 3) == 0) {
-        const int mine = rg + S * lane_row<R>(c8);
-        if (mine < left) a.dg_row.s[cb * a.T + rb * 128 + mine] = s0, a.du_row.s[cb * a.T + rb * 128 + mine] = s1;
+        const int64_t mine = rb * 128 + rg + S * lane_row<R>(c8);
+        if (mine < a.T) a.dg_row.s[cb * a.T + mine] = s0, a.du_row.s[cb * a.T + mine] = s1;
     }
 #pragma unroll
     for (int z = 0; z < 3; ++z)
@@ -399,10 +393,9 @@ __global__ void __launch_bounds__(kGatedThreads) fp8_gated_back_kernel(const Gat
     for (int i = 0; i < R; ++i) {
         const float q0 = __shfl_sync(0xffffffffu, r0, row_lane<R>(i), 16), q1 = __shfl_sync(0xffffffffu, r1, row_lane<R>(i), 16);
         const int64_t r = row0 + S * i;
-        if (rg + S * i >= left || n <= 0) continue;
-        float g[8], u[8], dg[8], du[8], h[8];
-        values8(gq[i], g), values8(uq[i], u);
-        gated_back8(dh[i].w, g, sg[i], u, su[i], a.limit, dg, du, h);
+        if (rg + S * i >= left) continue;
+        float dg[8], du[8], h[8];
+        results(i, dg, du, h);
         if (a.dg_row.q) {
             put8(a.dg_row.q + r * a.dg_row.ld + c0, n, dg, q0);
             put8(a.du_row.q + r * a.du_row.ld + c0, n, du, q1);

@@ -10,9 +10,7 @@
 // thread that issues the products too few issue slots (a block 737 cycles instead of 512, measured with nothing else).
 //
 // Warp 0 loads operands (TMA, 128-byte swizzle), warp 1 issues the products, warps 4..11 hold the accumulators: two warps a
-// quarter of the 128 TMEM lanes, half of the columns each. Rows' scales are read into their registers; for a weight's
-// gradient, whose columns have scales of their own, warp 2 brings those to shared memory (4-byte cp.async, which take any
-// alignment). A weight is stored once: the product with it
+// quarter of the 128 TMEM lanes, half of the columns each, and read their scales. A weight is stored once: the product with it
 // and the one with its transpose read the same codes, K-major and MN-major (8-bit operands may be
 // either), and so do the two operands of a weight's gradient, whose K are the tokens. A pair of CTAs shares a tile
 // of 256 x 256 where there are tiles enough: each loads half of it, half of what two tiles of 128 x 256 would.
@@ -44,10 +42,8 @@ struct F8Cfg {
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = int(196608 / STAGE_BYTES);
     static constexpr int BUFS = 512 / BN;
-    static constexpr int SLOTS = 8;         // blocks whose scales are on their way or in use
-    static constexpr int SLOT_FLOATS = OP == F8_TN ? BN : 0;
     static constexpr size_t SMEM = size_t(STAGES) * STAGE_BYTES + kF8EpiWarps * kStageFloats * 4 +
-                                   size_t(SLOTS) * SLOT_FLOATS * 4 + (OP == F8_GU ? 4 * 128 * 2 * 4 : 0) + 1024 + 512;
+                                   (OP == F8_GU ? 3 * 2 * 128 * 4 : 0) + 1024 + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -172,15 +168,6 @@ __device__ __forceinline__ void f8_drain(uint64_t* bar, uint32_t parity) {
     }
 }
 
-__device__ __forceinline__ void copy4(float* dst, const float* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-
-// this thread's copies so far arrive on `bar` when they are complete
-__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // 32 lanes x 16 columns; the registers are valid after tmem_wait
 __device__ __forceinline__ void tmem_ask16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -188,6 +175,14 @@ __device__ __forceinline__ void tmem_ask16(uint32_t taddr, uint32_t (&r)[16]) {
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
+}
+
+// 16 lanes x 16 columns, of which a thread gets rows lane / 4 (registers 0, 1, 4, 5) and lane / 4 + 8 (2, 3, 6, 7), columns 2 (lane % 4), + 1
+// of the first eight and of the second
+__device__ __forceinline__ void tmem_ask_pairs(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
 }
 
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -363,6 +358,119 @@ __device__ __forceinline__ void gated_results(const F8Args& a, const Item& t, fl
     meet();  // both have read before the next tile's are written
 }
 
+// ---------------------------------------------------------------- a weight's gradient
+// Its columns have scales of their own, a vector for each block of tokens. A thread therefore takes four rows (lane / 4 + 8 i) and
+// HALF / 4 columns, in adjacent pairs, instead of a row: HALF / 4 scales from global memory a block, not HALF from shared memory (which
+// the products keep busy: 1950 cycles a block). acc[4 g + i]: row i, columns 8 g + 2 (lane % 4), + 1.
+template <int BN, int CG>
+__device__ __forceinline__ bool column_sums(const F8Scales& s, const F8Out& o, const Item& t, uint64_t (&acc)[BN / 4], uint32_t lanes, int q,
+                                            int half, uint64_t* tfull, uint32_t given, int& buf, uint32_t& bphase, bool ok, volatile int* abort) {
+    constexpr int HALF = BN / 2, BUFS = 512 / BN;
+    const int lane = threadIdx.x & 31;
+    const int col = t.n0 + HALF * half + 2 * (lane & 3);
+    const float* pc = s.b + t.k_lo * s.ld_b + col;
+    const float* pr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pr[i] = s.a + t.k_lo * s.ld_a + min(t.m0 + q * 32 + (lane >> 2) + 8 * i, o.M - 1);
+    const bool paired = ((reinterpret_cast<uintptr_t>(s.b) & 7) | (s.ld_b & 1)) == 0 && t.n0 + BN <= o.N;
+    uint64_t cs[HALF / 8];
+    float r[4];
+    auto fetch = [&] {
+        if (paired) {
+#pragma unroll
+            for (int g = 0; g < HALF / 8; ++g) cs[g] = __ldg(reinterpret_cast<const unsigned long long*>(pc + 8 * g));
+        } else {
+#pragma unroll
+            for (int g = 0; g < HALF / 8; ++g)
+                cs[g] = pair(col + 8 * g < o.N ? __ldg(pc + 8 * g) : 0.0f, col + 8 * g + 1 < o.N ? __ldg(pc + 8 * g + 1) : 0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = __ldg(pr[i]);
+    };
+    if (t.k_lo < t.k_hi) fetch();
+    for (int kb = t.k_lo; kb < t.k_hi; ++kb) {
+        if (ok) ok = f8_wait_warp(&tfull[buf], bphase, abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = lanes + uint32_t(buf * BN + HALF * half);
+        uint64_t r2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r2[i] = pair(r[i], r[i]);
+#pragma unroll
+        for (int c = 0; c < HALF / 16; ++c) {
+            uint32_t v[16];
+            tmem_ask_pairs(at + 16 * c, v);
+            tmem_ask_pairs(at + 16 * c + (16u << 16), v + 8);
+            tmem_wait();
+            if (c == HALF / 16 - 1) {  // the buffer is read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(given + 8 * buf);
+            }
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t* x = v + 8 * (i >> 1) + 4 * z + 2 * (i & 1);
+                    fma2(acc[4 * (2 * c + z) + i], pair(x[0], x[1]), mul2(r2[i], cs[2 * c + z]));
+                }
+        }
+        if (kb + 1 < t.k_hi) {
+            pc += s.ld_b;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pr[i] += s.ld_a;
+            fetch();
+        }
+        if (++buf == BUFS) buf = 0, bphase ^= 1;
+    }
+    return ok;
+}
+
+// The sums of column_sums to the output (or the partial sums); four lanes write 8 adjacent columns of a row
+template <int HALF>
+__device__ __forceinline__ void column_store(const F8Out& o, bool split, const Item& t, const uint64_t (&acc)[HALF / 2], bool ok, int q, int half) {
+    const int lane = threadIdx.x & 31;
+    void* out = split ? static_cast<void*>(o.partial + int64_t(t.ks) * o.M * o.ld_partial) : o.out;
+    const int64_t ld = split ? o.ld_partial : o.ld;
+    const bool bf16 = !split && o.bf16, add = !split && o.accumulate;
+    const bool wide = ((reinterpret_cast<uintptr_t>(out) | uintptr_t(ld) * (bf16 ? 2 : 4)) & (bf16 ? 3 : 7)) == 0;
+    const int col = t.n0 + HALF * half + 2 * (lane & 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = t.m0 + q * 32 + (lane >> 2) + 8 * i;
+        if (row >= o.M) continue;
+#pragma unroll
+        for (int g = 0; g < HALF / 8; ++g) {
+            const int c = col + 8 * g;
+            float a, b;
+            unpair(ok ? acc[4 * g + i] : 0x7fffffff7fffffffull, a, b);
+            const int64_t at = int64_t(row) * ld + c;
+            if (wide && c + 1 < o.N) {
+                if (bf16) {
+                    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(out) + at);
+                    uint32_t w = pack_bf16x2(a, b);
+                    if (add) {
+                        float x, y, d, e;
+                        unpack_bf16x2(*dst, x, y), unpack_bf16x2(w, d, e);
+                        w = pack_bf16x2(x + d, y + e);
+                    }
+                    *dst = w;
+                } else {
+                    float2* dst = reinterpret_cast<float2*>(static_cast<float*>(out) + at);
+                    if (add) {
+                        const float2 old = *dst;
+                        a += old.x, b += old.y;
+                    }
+                    *dst = make_float2(a, b);
+                }
+            } else {
+                if (c < o.N) store_one(out, at, bf16, add, a);
+                if (c + 1 < o.N) store_one(out, at + 1, bf16, add, b);
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------- the kernel
 template <int OP, int BN, int CG>
 __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_constant__ F8Maps maps, const __grid_constant__ F8Args a) {
@@ -375,15 +483,12 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     float* staging = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES);
-    float* slots = staging + kF8EpiWarps * kStageFloats;
-    float* most = slots + C::SLOTS * C::SLOT_FLOATS;  // F8_GU: [3][2][128]
-    uint64_t* full = reinterpret_cast<uint64_t*>(most + (OP == F8_GU ? 4 * 256 : 0));
+    float* most = staging + kF8EpiWarps * kStageFloats;  // F8_GU: [3][2][128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(most + (OP == F8_GU ? 3 * 256 : 0));
     uint64_t* empty = full + C::STAGES;
     uint64_t* tfull = empty + C::STAGES;
     uint64_t* tempty = tfull + C::BUFS;
-    uint64_t* sfull = tempty + C::BUFS;
-    uint64_t* sempty = sfull + C::SLOTS;
-    uint64_t* drain = sempty + C::SLOTS;
+    uint64_t* drain = tempty + C::BUFS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -392,7 +497,6 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
         for (int b = 0; b < C::BUFS; ++b) mbar_init(&tfull[b], 1), mbar_init(&tempty[b], CG * kF8EpiWarps);
-        for (int s = 0; s < C::SLOTS; ++s) mbar_init(&sfull[s], 32), mbar_init(&sempty[s], kF8EpiWarps);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -488,31 +592,6 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
             f8_drain(drain, 0);  // every product is complete before TMEM is released
         }
         __syncwarp();
-    } else if (OP == F8_TN && warp == 2) {
-        // ---------------- scales of the columns
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-        int slot = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int i = first; ok && i < items; i += step) {
-            const Item t = f8_item<OP, BN, CG>(i, a, rank);
-            const F8Scales& s = a.s[t.p];
-            int at[BN / 32];  // columns past the last take its scale: nothing reads their sums
-#pragma unroll
-            for (int z = 0; z < BN / 32; ++z) at[z] = min(t.n0 + lane + 32 * z, a.o[t.p].N - 1);
-            const float* from = s.b + t.k_lo * s.ld_b;
-            for (int kb = t.k_lo; kb < t.k_hi; ++kb) {
-                ok = f8_wait_warp(&sempty[slot], phase ^ 1, abort_flag);
-                if (!ok) break;
-                float* sl = slots + slot * C::SLOT_FLOATS + lane;
-#pragma unroll
-                for (int z = 0; z < BN / 32; ++z) copy4(sl + 32 * z, from + at[z]);
-                copies_arrive(&sfull[slot]);
-                from += s.ld_b;
-                if (++slot == C::SLOTS) slot = 0, phase ^= 1;
-            }
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     } else {
@@ -521,8 +600,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
         const int q = warp & 3, half = (warp - 4) >> 2;
         float* my_staging = staging + (warp - 4) * kStageFloats;
         const uint32_t lanes = tmem + (uint32_t(q * 32) << 16);
-        int slot = 0, buf = 0;
-        uint32_t sphase = 0, bphase = 0;
+        int buf = 0;
+        uint32_t bphase = 0;
         bool ok = true;
         const uint32_t given = CG == 1 ? smem_u32(tempty) : in_leader(tempty);
         for (int i = first; i < items; i += step) {
@@ -530,9 +609,14 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
             uint64_t acc[HALF / 2];
 #pragma unroll
             for (int j = 0; j < HALF / 2; ++j) acc[j] = 0;
-            // The scales of this row, and those of the columns but for F8_TN's: read two blocks ahead, into registers (beside the products'
-            // reads of their operands a read of shared memory takes some hundred cycles).
             const F8Out& o = a.o[t.p];
+            if constexpr (OP == F8_TN) {
+                ok = column_sums<BN, CG>(a.s[t.p], o, t, acc, lanes, q, half, tfull, given, buf, bphase, ok, abort_flag);
+                column_store<HALF>(o, a.splits > 1, t, acc, ok, q, half);
+                continue;
+            }
+            // The scales of this row and of the columns: read two blocks ahead, into registers (beside the products'
+            // reads of their operands a read of shared memory takes some hundred cycles).
             const int row = min(t.m0 + q * 32 + lane, o.M - 1);  // rows past the last are not stored
             const int nb = min((t.n0 + (OP == F8_GU ? 0 : HALF * half)) >> 7, (o.N - 1) >> 7);
             const float *pr, *pc0, *pc1;
@@ -545,7 +629,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
             };
             auto fetch = [&](float& r, float& c0, float& c1) {
                 r = __ldg(pr);
-                if (OP != F8_TN) c0 = __ldg(pc0);
+                c0 = __ldg(pc0);
                 if (OP == F8_GU) c1 = __ldg(pc1);
             };
             auto next = [&] {
@@ -553,10 +637,10 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
                 if (OP == F8_GU) pc1 += 1;
             };
             for (int kb = t.k_lo; kb < t.k_hi;) {  // once, or once for each part of K
-                const int part = OP == F8_TN ? t.p : OP == F8_NN && kb >= a.k_part ? 1 : 0;
+                const int part = OP == F8_NN && kb >= a.k_part ? 1 : 0;
                 const int end = OP == F8_NN && part == 0 ? min(t.k_hi, a.k_part) : t.k_hi;
                 from(part, OP == F8_NN && part ? kb - a.k_part : kb);
-                float r0, r1, c00 = 1.0f, c01 = 1.0f, c10 = 1.0f, c11 = 1.0f;
+                float r0, r1, c00, c01, c10 = 1.0f, c11 = 1.0f;
                 fetch(r0, c00, c10);
                 r1 = r0, c01 = c00, c11 = c10;
                 if (kb + 1 < end) next(), fetch(r1, c01, c11);
@@ -565,7 +649,6 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
                     const uint64_t g0 = pair(f0, f0), g1 = OP == F8_GU ? pair(f1, f1) : g0;
                     r0 = r1, c00 = c01, c10 = c11;
                     if (kb + 2 < end) next(), fetch(r1, c01, c11);
-                    if (OP == F8_TN && ok) ok = f8_wait_warp(&sfull[slot], sphase, abort_flag);
                     if (ok) ok = f8_wait_warp(&tfull[buf], bphase, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
@@ -583,23 +666,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
                             if (lane == 0) arrive_cluster(given + 8 * buf);
                         }
                         const uint32_t(&x)[16] = v[c & 1];
-                        if (OP == F8_TN) {
-                            const float4* cols = reinterpret_cast<const float4*>(slots + slot * C::SLOT_FLOATS + HALF * half + 16 * c);
 #pragma unroll
-                            for (int z = 0; z < 4; ++z) {
-                                const float4 w = cols[z];
-                                fma2(acc[8 * c + 2 * z], pair(x[4 * z], x[4 * z + 1]), mul2(g0, pair(w.x, w.y)));
-                                fma2(acc[8 * c + 2 * z + 1], pair(x[4 * z + 2], x[4 * z + 3]), mul2(g0, pair(w.z, w.w)));
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) fma2(acc[8 * c + j], pair(x[2 * j], x[2 * j + 1]), c < HALF / 32 ? g0 : g1);
-                        }
-                    }
-                    if (OP == F8_TN) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sempty[slot]);
-                        if (++slot == C::SLOTS) slot = 0, sphase ^= 1;
+                        for (int j = 0; j < 8; ++j) fma2(acc[8 * c + j], pair(x[2 * j], x[2 * j + 1]), c < HALF / 32 ? g0 : g1);
                     }
                     if (++buf == C::BUFS) buf = 0, bphase ^= 1;
                 }
