@@ -244,24 +244,41 @@ __device__ __forceinline__ void put16(float* staging, const float* v) {
     float4* row = reinterpret_cast<float4*>(staging + lane * 16);
 #pragma unroll
     for (int j = 0; j < 4; ++j) row[j ^ ((lane >> 1) & 3)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    __syncwarp();
 }
 
-__device__ __forceinline__ void f8_store16(const F8Out& o, void* out, int64_t ld, bool bf16, bool add, bool wide, int row0,
-                                           int col0, const float* v, float* staging) {
+// Where a product's results go
+struct Sink {
+    void* out;
+    int64_t ld;
+    bool bf16, add, wide;  // wide: four adjacent results can be written at once
+};
+__device__ __forceinline__ Sink f8_sink(const F8Args& a, const Item& t) {
+    const F8Out& o = a.o[t.p];
+    const bool split = a.splits > 1;
+    Sink s;
+    s.out = split ? static_cast<void*>(o.partial + int64_t(t.ks) * o.M * o.ld_partial) : o.out;
+    s.ld = split ? o.ld_partial : o.ld;
+    s.bf16 = !split && o.bf16;
+    s.add = !split && o.accumulate;
+    s.wide = ((reinterpret_cast<uintptr_t>(s.out) | uintptr_t(s.ld) * (s.bf16 ? 2 : 4)) & (s.bf16 ? 7 : 15)) == 0;
+    return s;
+}
+
+// The 16 columns in `staging` of rows row0 .. + 31. (No unrolling here, nor of the loop around it: a tile's results are written once, by
+// instructions that are then fetched for the first time, and that took several times the writing.)
+__device__ __forceinline__ void f8_store16(const F8Out& o, const Sink& s, int row0, int col0, const float* staging) {
     const int lane = threadIdx.x & 31;
-    put16(staging, v);
-    if (wide && col0 + 16 <= o.N) {
-#pragma unroll
+    if (s.wide && col0 + 16 <= o.N) {
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
             const int r = i * 8 + (lane >> 2), j = lane & 3;
             float4 x = reinterpret_cast<const float4*>(staging + r * 16)[j ^ ((r >> 1) & 3)];
-            if (row0 + r >= o.M) continue;
-            const int64_t at = int64_t(row0 + r) * ld + col0 + 4 * j;
-            if (bf16) {
-                uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at);
+            if (row0 + r >= o.M) break;
+            const int64_t at = int64_t(row0 + r) * s.ld + col0 + 4 * j;
+            if (s.bf16) {
+                uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(s.out) + at);
                 uint2 w = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-                if (add) {
+                if (s.add) {
                     const uint2 old = *dst;
                     float a0, a1, a2, a3, b0, b1, b2, b3;
                     unpack_bf16x2(old.x, a0, a1), unpack_bf16x2(old.y, a2, a3);
@@ -270,8 +287,8 @@ __device__ __forceinline__ void f8_store16(const F8Out& o, void* out, int64_t ld
                 }
                 *dst = w;
             } else {
-                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-                if (add) {
+                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(s.out) + at);
+                if (s.add) {
                     const float4 old = *dst;
                     x = make_float4(old.x + x.x, old.y + x.y, old.z + x.z, old.w + x.w);
                 }
@@ -280,14 +297,47 @@ __device__ __forceinline__ void f8_store16(const F8Out& o, void* out, int64_t ld
         }
     } else {
         const int c = lane & 15;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 16; ++i) {
             const int r = i * 2 + (lane >> 4);
             const float x = staging[r * 16 + 4 * ((c >> 2) ^ ((r >> 1) & 3)) + (c & 3)];
-            if (row0 + r < o.M && col0 + c < o.N) store_one(out, int64_t(row0 + r) * ld + col0 + c, bf16, add, x);
+            if (row0 + r < o.M && col0 + c < o.N) store_one(s.out, int64_t(row0 + r) * s.ld + col0 + c, s.bf16, s.add, x);
         }
     }
     __syncwarp();
+}
+
+// 32 bytes, a whole sector, at once
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                 "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// A thread's N columns of its row, by whole sectors
+template <int N>
+__device__ __forceinline__ void row_store(const F8Out& o, const Sink& s, int row, int col, const float (&v)[N]) {
+    if (row >= o.M) return;
+    const int64_t at = int64_t(row) * s.ld + col;
+    if (s.bf16) {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(s.out) + at;
+#pragma unroll
+        for (int c = 0; c < N / 16; ++c) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(v[16 * c + 2 * j], v[16 * c + 2 * j + 1]);
+            store32(dst + 16 * c, w);
+        }
+    } else {
+        float* dst = static_cast<float*>(s.out) + at;
+#pragma unroll
+        for (int c = 0; c < N / 8; ++c) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * c + j]);
+            store32(dst + 8 * c, w);
+        }
+    }
 }
 
 // 16 codes of one row; the row's bytes past N are not the product's to write
@@ -426,14 +476,10 @@ __device__ __forceinline__ bool column_sums(const F8Scales& s, const F8Out& o, c
     return ok;
 }
 
-// The sums of column_sums to the output (or the partial sums); four lanes write 8 adjacent columns of a row
-template <int HALF>
-__device__ __forceinline__ void column_store(const F8Out& o, bool split, const Item& t, const uint64_t (&acc)[HALF / 2], bool ok, int q, int half) {
+// The sums of column_sums to their place; four lanes write 8 adjacent columns of a row. put(at, a, b) writes two adjacent results.
+template <int HALF, typename Put>
+__device__ __forceinline__ void column_each(const F8Out& o, const Item& t, int64_t ld, const uint64_t (&acc)[HALF / 2], int q, int half, Put put) {
     const int lane = threadIdx.x & 31;
-    void* out = split ? static_cast<void*>(o.partial + int64_t(t.ks) * o.M * o.ld_partial) : o.out;
-    const int64_t ld = split ? o.ld_partial : o.ld;
-    const bool bf16 = !split && o.bf16, add = !split && o.accumulate;
-    const bool wide = ((reinterpret_cast<uintptr_t>(out) | uintptr_t(ld) * (bf16 ? 2 : 4)) & (bf16 ? 3 : 7)) == 0;
     const int col = t.n0 + HALF * half + 2 * (lane & 3);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -441,33 +487,38 @@ __device__ __forceinline__ void column_store(const F8Out& o, bool split, const I
         if (row >= o.M) continue;
 #pragma unroll
         for (int g = 0; g < HALF / 8; ++g) {
-            const int c = col + 8 * g;
             float a, b;
-            unpair(ok ? acc[4 * g + i] : 0x7fffffff7fffffffull, a, b);
-            const int64_t at = int64_t(row) * ld + c;
-            if (wide && c + 1 < o.N) {
-                if (bf16) {
-                    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(out) + at);
-                    uint32_t w = pack_bf16x2(a, b);
-                    if (add) {
-                        float x, y, d, e;
-                        unpack_bf16x2(*dst, x, y), unpack_bf16x2(w, d, e);
-                        w = pack_bf16x2(x + d, y + e);
-                    }
-                    *dst = w;
-                } else {
-                    float2* dst = reinterpret_cast<float2*>(static_cast<float*>(out) + at);
-                    if (add) {
-                        const float2 old = *dst;
-                        a += old.x, b += old.y;
-                    }
-                    *dst = make_float2(a, b);
-                }
-            } else {
-                if (c < o.N) store_one(out, at, bf16, add, a);
-                if (c + 1 < o.N) store_one(out, at + 1, bf16, add, b);
-            }
+            unpair(acc[4 * g + i], a, b);
+            put(int64_t(row) * ld + col + 8 * g, col + 8 * g, a, b);
         }
+    }
+}
+
+// (One of the ways is taken as a whole: with the choice at each element the code is as long as all of them, and fetching it, once a tile,
+// took several times the writing.)
+template <int HALF>
+__device__ __forceinline__ void column_store(const F8Out& o, const Sink& s, const Item& t, const uint64_t (&acc)[HALF / 2], int q, int half) {
+    const bool whole = t.n0 + 2 * HALF <= o.N && ((reinterpret_cast<uintptr_t>(s.out) | uintptr_t(s.ld) * (s.bf16 ? 2 : 4)) & (s.bf16 ? 3 : 7)) == 0;
+    if (whole && !s.add) {
+        if (s.bf16)
+            column_each<HALF>(o, t, s.ld, acc, q, half, [&](int64_t at, int, float a, float b) {
+                *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(s.out) + at) = pack_bf16x2(a, b);
+            });
+        else
+            column_each<HALF>(o, t, s.ld, acc, q, half, [&](int64_t at, int, float a, float b) {
+                *reinterpret_cast<float2*>(static_cast<float*>(s.out) + at) = make_float2(a, b);
+            });
+    } else if (whole && !s.bf16) {
+        column_each<HALF>(o, t, s.ld, acc, q, half, [&](int64_t at, int, float a, float b) {
+            float2* dst = reinterpret_cast<float2*>(static_cast<float*>(s.out) + at);
+            const float2 old = *dst;
+            *dst = make_float2(old.x + a, old.y + b);
+        });
+    } else {
+        column_each<HALF>(o, t, s.ld, acc, q, half, [&](int64_t at, int c, float a, float b) {
+            if (c < o.N) store_one(s.out, at, s.bf16, s.add, a);
+            if (c + 1 < o.N) store_one(s.out, at + 1, s.bf16, s.add, b);
+        });
     }
 }
 
@@ -612,7 +663,10 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
             const F8Out& o = a.o[t.p];
             if constexpr (OP == F8_TN) {
                 ok = column_sums<BN, CG>(a.s[t.p], o, t, acc, lanes, q, half, tfull, given, buf, bphase, ok, abort_flag);
-                column_store<HALF>(o, a.splits > 1, t, acc, ok, q, half);
+#pragma unroll
+                for (int j = 0; j < HALF / 2; ++j)
+                    if (!ok) acc[j] = 0x7fffffff7fffffffull;
+                column_store<HALF>(o, f8_sink(a, t), t, acc, q, half);
                 continue;
             }
             // The scales of this row and of the columns: read two blocks ahead, into registers (beside the products'
@@ -682,16 +736,21 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
             if constexpr (OP == F8_GU) {
                 gated_results(a, t, sum, q, half, most);
             } else {
-                const bool part = a.splits > 1;
-                void* out = part ? static_cast<void*>(o.partial + int64_t(t.ks) * o.M * o.ld_partial) : o.out;
-                const int64_t ld = part ? o.ld_partial : o.ld;
-                const bool bf16 = !part && o.bf16;
-                const bool wide = ((reinterpret_cast<uintptr_t>(out) | uintptr_t(ld) * (bf16 ? 2 : 4)) & (bf16 ? 7 : 15)) == 0;
-#pragma unroll
+                const Sink sink = f8_sink(a, t);
+                if (!sink.add && t.n0 + HALF * (half + 1) <= o.N &&
+                    ((reinterpret_cast<uintptr_t>(sink.out) | uintptr_t(sink.ld) * (sink.bf16 ? 2 : 4)) & 31) == 0) {
+                    row_store<HALF>(o, sink, t.m0 + q * 32 + lane, t.n0 + HALF * half, sum);
+                    continue;
+                }
+#pragma unroll 1
                 for (int c = 0; c < HALF / 16; ++c) {
                     const int col = t.n0 + HALF * half + 16 * c;
-                    if (col < o.N)
-                        f8_store16(o, out, ld, bf16, !part && o.accumulate, wide, t.m0 + q * 32, col, sum + 16 * c, my_staging);
+                    if (col >= o.N) break;
+#pragma unroll
+                    for (int z = 0; z < HALF / 16; ++z)
+                        if (z == c) put16(my_staging, sum + 16 * z);
+                    __syncwarp();
+                    f8_store16(o, sink, t.m0 + q * 32, col, my_staging);
                 }
             }
         }
