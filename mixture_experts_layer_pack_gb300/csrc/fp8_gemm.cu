@@ -53,6 +53,12 @@ struct F8Cfg {
 __device__ __forceinline__ uint32_t f8_desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4) << 16; }
 constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
 
+// one lane of a warp, so that the compiler knows that its instructions are the warp's (a condition on the lane costs 3 % more)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ uint32_t cta_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -613,7 +619,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
     } else if (warp == 1) {
         // ---------------- products
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             int stage = 0, buf = 0;
             uint32_t phase = 0, bphase = 0;
             bool ok = true;
@@ -622,24 +628,30 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
             for (int i = first; ok && i < items; i += step) {
                 const Item t = f8_item<OP, BN, CG>(i, a, rank);
                 for (int kb = t.k_lo; kb < t.k_hi; ++kb) {
-                    ok = f8_wait(&full[stage], phase, abort_flag) && f8_wait(&tempty[buf], bphase ^ 1, abort_flag);
+                    ok = f8_wait_warp(&full[stage], phase, abort_flag) && f8_wait_warp(&tempty[buf], bphase ^ 1, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem + buf * BN, al = a_base + stage * (C::STAGE_BYTES >> 4), bl = b_base + stage * (C::STAGE_BYTES >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        f8_mma<CG>(d, al + kk * (A_MN ? 4096 >> 4 : 32 >> 4), bl + kk * (B_MN ? 4096 >> 4 : 32 >> 4), IDESC, kk != 0 ? 1u : 0u);
-                    f8_commit<CG>(&tfull[buf]);
-                    f8_commit<CG>(&empty[stage]);
+                        for (int kk = 0; kk < 4; ++kk)
+                            f8_mma<CG>(d, al + kk * (A_MN ? 4096 >> 4 : 32 >> 4), bl + kk * (B_MN ? 4096 >> 4 : 32 >> 4), IDESC, kk != 0 ? 1u : 0u);
+                        f8_commit<CG>(&tfull[buf]);
+                        f8_commit<CG>(&empty[stage]);
+                    }
+                    __syncwarp();
                     if (++buf == C::BUFS) buf = 0, bphase ^= 1;
                     if (++stage == C::STAGES) stage = 0, phase ^= 1;
                 }
             }
-            if (CG == 1)
-                mma_commit(drain);
-            else
-                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
-                             : "memory");
+            if (elect_one()) {
+                if (CG == 1)
+                    mma_commit(drain);
+                else
+                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
+                                 : "memory");
+            }
+            __syncwarp();
             f8_drain(drain, 0);  // every product is complete before TMEM is released
         }
         __syncwarp();
@@ -673,59 +685,44 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
             // reads of their operands a read of shared memory takes some hundred cycles).
             const int row = min(t.m0 + q * 32 + lane, o.M - 1);  // rows past the last are not stored
             const int nb = min((t.n0 + (OP == F8_GU ? 0 : HALF * half)) >> 7, (o.N - 1) >> 7);
-            const float *pr, *pc0, *pc1;
-            int64_t step_r, step_c;
-            auto from = [&](int part, int kl) {
-                const F8Scales& s = a.s[part];
-                step_r = s.ld_a, pr = s.a + kl * step_r + row;
-                step_c = OP == F8_NN ? s.ld_b : 1, pc0 = OP == F8_NN ? s.b + kl * step_c + nb : s.b + nb * s.ld_b + kl;
-                if (OP == F8_GU) pc1 = a.s[1].b + nb * a.s[1].ld_b + kl;
+            auto fetch = [&](int kb, float& r, float& c0, float& c1) {  // (addresses from the parameters: pointers kept would be spilled)
+                const bool second = OP == F8_NN && kb >= a.k_part;
+                const F8Scales& s = a.s[second ? 1 : 0];
+                const int64_t kl = second ? kb - a.k_part : kb;
+                r = __ldg(s.a + kl * s.ld_a + row);
+                c0 = __ldg(OP == F8_NN ? s.b + kl * s.ld_b + nb : s.b + nb * s.ld_b + kl);
+                if (OP == F8_GU) c1 = __ldg(a.s[1].b + nb * a.s[1].ld_b + kl);
             };
-            auto fetch = [&](float& r, float& c0, float& c1) {
-                r = __ldg(pr);
-                c0 = __ldg(pc0);
-                if (OP == F8_GU) c1 = __ldg(pc1);
-            };
-            auto next = [&] {
-                pr += step_r, pc0 += step_c;
-                if (OP == F8_GU) pc1 += 1;
-            };
-            for (int kb = t.k_lo; kb < t.k_hi;) {  // once, or once for each part of K
-                const int part = OP == F8_NN && kb >= a.k_part ? 1 : 0;
-                const int end = OP == F8_NN && part == 0 ? min(t.k_hi, a.k_part) : t.k_hi;
-                from(part, OP == F8_NN && part ? kb - a.k_part : kb);
-                float r0, r1, c00, c01, c10 = 1.0f, c11 = 1.0f;
-                fetch(r0, c00, c10);
-                r1 = r0, c01 = c00, c11 = c10;
-                if (kb + 1 < end) next(), fetch(r1, c01, c11);
-                for (; kb < end; ++kb) {
-                    const float f0 = r0 * c00, f1 = OP == F8_GU ? r0 * c10 : f0;
-                    const uint64_t g0 = pair(f0, f0), g1 = OP == F8_GU ? pair(f1, f1) : g0;
-                    r0 = r1, c00 = c01, c10 = c11;
-                    if (kb + 2 < end) next(), fetch(r1, c01, c11);
-                    if (ok) ok = f8_wait_warp(&tfull[buf], bphase, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    uint32_t v[2][16];
-                    const uint32_t at = lanes + uint32_t(buf * BN + HALF * half);
-                    tmem_ask16(at, v[0]);
-#pragma unroll
-                    for (int c = 0; c < HALF / 16; ++c) {
-                        tmem_wait();
-                        if (c + 1 < HALF / 16) {
-                            tmem_ask16(at + 16 * (c + 1), v[(c + 1) & 1]);
-                        } else {  // the buffer is read
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) arrive_cluster(given + 8 * buf);
-                        }
-                        const uint32_t(&x)[16] = v[c & 1];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) fma2(acc[8 * c + j], pair(x[2 * j], x[2 * j + 1]), c < HALF / 32 ? g0 : g1);
-                    }
-                    if (++buf == C::BUFS) buf = 0, bphase ^= 1;
-                }
+            float r0 = 0.0f, r1, c00 = 0.0f, c01, c10 = 0.0f, c11 = 0.0f;
+            if (t.k_lo < t.k_hi) fetch(t.k_lo, r0, c00, c10);
+            r1 = r0, c01 = c00, c11 = c10;
+            if (t.k_lo + 1 < t.k_hi) fetch(t.k_lo + 1, r1, c01, c11);
+            for (int kb = t.k_lo; kb < t.k_hi; ++kb) {
+                const float f0 = r0 * c00, f1 = OP == F8_GU ? r0 * c10 : f0;
+                const uint64_t g0 = pair(f0, f0), g1 = OP == F8_GU ? pair(f1, f1) : g0;
+                r0 = r1, c00 = c01, c10 = c11;
+                if (kb + 2 < t.k_hi) fetch(kb + 2, r1, c01, c11);
+                if (ok) ok = f8_wait_warp(&tfull[buf], bphase, abort_flag);
                 if (!ok) break;
+                tc_fence_after();
+                uint32_t v[2][16];
+                const uint32_t at = lanes + uint32_t(buf * BN + HALF * half);
+                tmem_ask16(at, v[0]);
+#pragma unroll
+                for (int c = 0; c < HALF / 16; ++c) {
+                    tmem_wait();
+                    if (c + 1 < HALF / 16) {
+                        tmem_ask16(at + 16 * (c + 1), v[(c + 1) & 1]);
+                    } else {  // the buffer is read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_cluster(given + 8 * buf);
+                    }
+                    const uint32_t(&x)[16] = v[c & 1];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) fma2(acc[8 * c + j], pair(x[2 * j], x[2 * j + 1]), c < HALF / 32 ? g0 : g1);
+                }
+                if (++buf == C::BUFS) buf = 0, bphase ^= 1;
             }
             float sum[HALF];
 #pragma unroll
