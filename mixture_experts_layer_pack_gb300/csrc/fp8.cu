@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) fp8_gated_back_kernel(const 
     const int64_t row0 = rb * 128 + rg;
     // dg, du, h of this thread's eight columns of its i-th row
     auto results = [&](int i, float (&dg)[8], float (&du)[8], float (&h)[8]) {
-        const int64_t r = row0 + S * i;
+        const int64_t r = min(row0 + S * i, a.T - 1);  // a row past the last is read as that one, so that the rows' reads have no branch between them
         Eight<float> dh;
         dh.load(a.dh + r * a.ld_dh + c0, n, true);
         const uint2 gq = codes8(a.g.q + r * a.g.ld + c0, n), uq = codes8(a.u.q + r * a.u.ld + c0, n);
@@ -351,10 +351,9 @@ __global__ void __launch_bounds__(kGatedThreads, 2) fp8_gated_back_kernel(const 
     float mg[R], mu[R], mc[3][8] = {};
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        mg[i] = mu[i] = 0.0f;
-        if (rg + S * i >= left) continue;
         float dg[8], du[8], h[8];
-        results(i, dg, du, h);
+        results(i, dg, du, h);  // of a row past the last: the last one's, which change no maximum of a column
+        mg[i] = mu[i] = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             mg[i] = fmaxf(mg[i], fabsf(dg[j]));
@@ -393,9 +392,9 @@ __global__ void __launch_bounds__(kGatedThreads, 2) fp8_gated_back_kernel(const 
     for (int i = 0; i < R; ++i) {
         const float q0 = __shfl_sync(0xffffffffu, r0, row_lane<R>(i), 16), q1 = __shfl_sync(0xffffffffu, r1, row_lane<R>(i), 16);
         const int64_t r = row0 + S * i;
-        if (rg + S * i >= left) continue;
         float dg[8], du[8], h[8];
         results(i, dg, du, h);
+        if (rg + S * i >= left) continue;
         if (a.dg_row.q) {
             put8(a.dg_row.q + r * a.dg_row.ld + c0, n, dg, q0);
             put8(a.du_row.q + r * a.du_row.ld + c0, n, du, q1);
@@ -410,6 +409,48 @@ __global__ void __launch_bounds__(kGatedThreads, 2) fp8_gated_back_kernel(const 
             cols(0, a.dg_col, dg), cols(1, a.du_col, du), cols(2, a.h_col, h);
         }
     }
+}
+
+// ---------------------------------------------------------------- the gate over partial sums
+// h = silu(g) u from the partial sums of g and u, as row blocks, and g and u themselves where they are kept: 16 threads a block of 128
+__global__ void __launch_bounds__(256) fp8_gated_sum_kernel(const __grid_constant__ F8Args a) {
+    pdl_wait();
+    pdl_trigger();
+    const F8Out& o = a.o[0];
+    const int64_t unit = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 4);
+    const int64_t row = min(unit / o.n_tiles, int64_t(o.M) - 1);
+    const int block = int(unit % o.n_tiles), c8 = threadIdx.x & 15, c0 = block * 128 + c8 * 8, n = o.N - c0;
+    const bool mine = unit < int64_t(o.M) * o.n_tiles;
+    float v[2][8] = {};
+    const int64_t plane = int64_t(o.M) * o.ld_partial;
+    const float* src = o.partial + row * o.ld_partial + c0;
+#pragma unroll 2
+    for (int s = 0; s < a.splits; ++s) {  // the rows of the partial sums have room for whole blocks
+        Eight<float> g, u;
+        g.load(src + 2 * s * plane, 8, true);
+        u.load(src + (2 * s + 1) * plane, 8, true);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[0][j] += g.w[j], v[1][j] += u.w[j];
+    }
+    auto put = [&](const float (&x)[8], uint8_t* q, int64_t ld, float* scales) {
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float s = block_scale(m);
+        if (!mine) return;
+        if (c8 == 0) scales[int64_t(block) * o.M + row] = s;
+        if (n > 0) put8(q + row * ld + c0, n, x, __frcp_rn(s));
+    };
+    if (a.g) put(v[0], a.g, a.ld_g, a.gs), put(v[1], a.u, a.ld_u, a.us);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float g = v[0][j], u = v[1][j];
+        if (a.limit > 0.0f) g = clamp_top(g, a.limit), u = clamp_both(u, a.limit);
+        v[0][j] = g * sigmoidf_(g) * u;
+    }
+    put(v[0], a.h, a.ld_h, a.hs);
 }
 
 // ---------------------------------------------------------------- launches
@@ -473,7 +514,13 @@ Plan plan(int op, const F8Args& a) {
             n += ((int64_t(a.o[p].M) + rows - 1) / rows) * ((int64_t(a.o[p].N) + cols - 1) / cols);
         return n;
     };
-    if (op == F8_GU) return {256, tiles(256, 128) >= sms / 2 ? 2 : 1, 1};
+    if (op == F8_GU) {
+        if (tiles(256, 128) >= sms / 2) return {256, 2, 1};
+        const int64_t n = tiles(128, 128);
+        int splits = 1;
+        while (splits < 16 && n * (splits + 1) <= sms && a.k_blocks >= 4 * (splits + 1)) ++splits;
+        return {256, 1, splits};
+    }
     if (tiles(256, 256) >= sms / 2) return {256, 2, 1};
     if (tiles(128, 256) >= sms) return {256, 1, 1};
     const int64_t n = tiles(128, 128);
@@ -483,7 +530,7 @@ Plan plan(int op, const F8Args& a) {
 }
 
 void set_out(F8Out& o, void* out, int64_t ld, bool bf16, bool accumulate, int64_t M, int64_t N) {
-    o = F8Out{out, ld, nullptr, up(N, 4), int(M), int(N), 0, 0, bf16 ? 1 : 0, accumulate ? 1 : 0};
+    o = F8Out{out, ld, nullptr, up(N, 256), int(M), int(N), 0, 0, bf16 ? 1 : 0, accumulate ? 1 : 0};
 }
 
 // completes `a` and takes the partial sums' memory from `ws`
@@ -495,7 +542,7 @@ Plan prepare(int op, F8Args& a, Arena& ws) {
         F8Out& o = a.o[p];
         o.m_tiles = (o.M + tm - 1) / tm;
         o.n_tiles = (o.N + tn - 1) / tn;
-        if (pl.splits > 1) o.partial = static_cast<float*>(ws.take(4 * int64_t(pl.splits) * o.M * o.ld_partial));
+        if (pl.splits > 1) o.partial = static_cast<float*>(ws.take(4 * int64_t(pl.splits) * (op == F8_GU ? 2 : 1) * o.M * o.ld_partial));
     }
     return pl;
 }
@@ -509,7 +556,11 @@ bool map_of(CUtensorMap& m, const void* q, int64_t ld, int64_t rows, int64_t col
 
 cudaError_t multiply(int op, const Plan& pl, const F8Maps& maps, const F8Args& a, cudaStream_t st) {
     const cudaError_t e = launch_f8_gemm(op, pl.bn, pl.cg, maps, a, sm_count(), st);
-    return e != cudaSuccess || pl.splits == 1 ? e : launch_f8_reduce(a, st);
+    if (e != cudaSuccess || pl.splits == 1) return e;
+    if (op != F8_GU) return launch_f8_reduce(a, st);
+    const int64_t units = int64_t(a.o[0].M) * a.o[0].n_tiles;  // blocks of 128 of a row, 16 threads each
+    count_launch();
+    return launch_pdl(fp8_gated_sum_kernel, dim3(unsigned((units + 15) / 16)), dim3(256), 0, st, a);
 }
 
 // A product of a linear layer. x, w: the operands' codes; sizes as in fp8.h. `run` false: its workspace alone.
@@ -572,8 +623,28 @@ struct LinearCall {
     int32_t g_type, accumulate;
 };
 
+// y = x W^T for a few tokens
+F8Few few(const Codes& w, const void* x, int64_t ld_x, int32_t x_type, void* out, int64_t ld_out, bool bf16, int64_t T, int64_t N, int64_t K) {
+    F8Few a = {};
+    a.w[0] = w.q, a.ld_w[0] = w.ld, a.ws[0] = w.s;
+    a.x = x, a.ld_x = ld_x, a.wide = rows_on(x, ld_x, size_of(x_type), 16);
+    a.out = out, a.ld_out = ld_out, a.bf16 = bf16;
+    a.T = int(T), a.N = int(N), a.K = int(K);
+    return a;
+}
+
 cudaError_t linear_forward(const LinearCall& k, Arena& ws, bool run, cudaStream_t st) {
     const int64_t T = k.T, K = k.c->in_features, N = k.c->out_features;
+    if (f8_few_fits(T, N, K, sm_count())) {
+        if (!run) return cudaSuccess;
+        if (k.kept.q) {
+            const cudaError_t e = quantize(k.in, k.c->x_type, T, K, k.in_stride, kNone, k.kept, kNone, st);
+            if (e != cudaSuccess) return e;
+        }
+        F8Few a = few(k.w, k.in, k.in_stride, k.c->x_type, k.out, k.out_stride, k.c->y_type == MOE_T_BF16, T, N, K);
+        a.early = k.kept.q != nullptr;
+        return launch_f8_few(a, k.c->x_type == MOE_T_BF16, st);
+    }
     const Codes xq = ws.codes(T, K, true);
     if (run) {
         const cudaError_t e = quantize(k.in, k.c->x_type, T, K, k.in_stride, xq, k.kept, kNone, st);
@@ -608,8 +679,24 @@ struct FfnCall {
     int32_t g_type, accumulate;
 };
 
+// Few tokens and nothing kept: h passes in fp32 from the first launch to the second, which quantises it
+cudaError_t ffn_few(const FfnCall& k, Arena& ws, bool run, cudaStream_t st) {
+    const int64_t T = k.T, H = k.c->hidden, I = k.c->inter, ld_h = up(I, 4);
+    float* h = static_cast<float*>(ws.take(4 * T * ld_h));
+    if (!run) return cudaSuccess;
+    F8Few g = few(k.gate, k.in, k.in_stride, MOE_T_BF16, h, ld_h, false, T, I, H);
+    g.w[1] = k.up.q, g.ld_w[1] = k.up.ld, g.ws[1] = k.up.s;
+    g.limit = k.c->swiglu_limit;
+    const cudaError_t e = launch_f8_few(g, true, st);
+    if (e != cudaSuccess) return e;
+    F8Few d = few(k.down, h, ld_h, MOE_T_FP32, k.out, k.out_stride, true, T, H, I);
+    d.early = 1;
+    return launch_f8_few(d, false, st);
+}
+
 cudaError_t ffn_forward(const FfnCall& k, Arena& ws, bool run, cudaStream_t st) {
     const int64_t T = k.T, H = k.c->hidden, I = k.c->inter;
+    if (!k.kx.q && f8_few_fits(T, I, H, sm_count()) && f8_few_fits(T, H, I, sm_count())) return ffn_few(k, ws, run, st);
     const Codes xq = ws.codes(T, H, true), h = ws.codes(T, I, true);
     F8Args a = {};
     a.products = 1;
@@ -800,6 +887,12 @@ moe_status moe_ffn_size(const moe_ffn_config* cfg, int64_t T, int32_t backward, 
     Arena ws(nullptr);
     (void)(backward ? ffn_backward(k, ws, false, nullptr) : ffn_forward(k, ws, false, nullptr));
     *bytes = ws.at;
+    if (!backward) {  // the way of a call that keeps
+        k.kx.q = reinterpret_cast<uint8_t*>(bytes);
+        Arena keeping(nullptr);
+        (void)ffn_forward(k, keeping, false, nullptr);
+        *bytes = keeping.at > ws.at ? keeping.at : ws.at;
+    }
     return MOE_OK;
 }
 

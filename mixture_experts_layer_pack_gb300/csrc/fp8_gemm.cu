@@ -21,8 +21,6 @@
 #include "fp8_device.cuh"
 #include "internal.h"
 
-#include <atomic>
-
 namespace moe {
 
 namespace {
@@ -258,11 +256,11 @@ struct Sink {
     int64_t ld;
     bool bf16, add, wide;  // wide: four adjacent results can be written at once
 };
-__device__ __forceinline__ Sink f8_sink(const F8Args& a, const Item& t) {
+__device__ __forceinline__ Sink f8_sink(const F8Args& a, const Item& t, int part = 0, int parts = 1) {
     const F8Out& o = a.o[t.p];
     const bool split = a.splits > 1;
     Sink s;
-    s.out = split ? static_cast<void*>(o.partial + int64_t(t.ks) * o.M * o.ld_partial) : o.out;
+    s.out = split ? static_cast<void*>(o.partial + int64_t(t.ks * parts + part) * o.M * o.ld_partial) : o.out;
     s.ld = split ? o.ld_partial : o.ld;
     s.bf16 = !split && o.bf16;
     s.add = !split && o.accumulate;
@@ -322,7 +320,7 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
 
 // A thread's N columns of its row, by whole sectors
 template <int N>
-__device__ __forceinline__ void row_store(const F8Out& o, const Sink& s, int row, int col, const float (&v)[N]) {
+__device__ __forceinline__ void row_store(const F8Out& o, const Sink& s, int row, int col, const float* v) {
     if (row >= o.M) return;
     const int64_t at = int64_t(row) * s.ld + col;
     if (s.bf16) {
@@ -504,7 +502,8 @@ __device__ __forceinline__ void column_each(const F8Out& o, const Item& t, int64
 // took several times the writing.)
 template <int HALF>
 __device__ __forceinline__ void column_store(const F8Out& o, const Sink& s, const Item& t, const uint64_t (&acc)[HALF / 2], int q, int half) {
-    const bool whole = t.n0 + 2 * HALF <= o.N && ((reinterpret_cast<uintptr_t>(s.out) | uintptr_t(s.ld) * (s.bf16 ? 2 : 4)) & (s.bf16 ? 3 : 7)) == 0;
+    // partial sums have room for whole tiles
+    const bool whole = (s.out != o.out || t.n0 + 2 * HALF <= o.N) && ((reinterpret_cast<uintptr_t>(s.out) | uintptr_t(s.ld) * (s.bf16 ? 2 : 4)) & (s.bf16 ? 3 : 7)) == 0;
     if (whole && !s.add) {
         if (s.bf16)
             column_each<HALF>(o, t, s.ld, acc, q, half, [&](int64_t at, int, float a, float b) {
@@ -731,24 +730,33 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
                 unpair(acc[j], sum[2 * j], sum[2 * j + 1]);
             }
             if constexpr (OP == F8_GU) {
-                gated_results(a, t, sum, q, half, most);
-            } else {
-                const Sink sink = f8_sink(a, t);
-                if (!sink.add && t.n0 + HALF * (half + 1) <= o.N &&
-                    ((reinterpret_cast<uintptr_t>(sink.out) | uintptr_t(sink.ld) * (sink.bf16 ? 2 : 4)) & 31) == 0) {
-                    row_store<HALF>(o, sink, t.m0 + q * 32 + lane, t.n0 + HALF * half, sum);
+                if (CG == 2 || a.splits == 1) {
+                    gated_results(a, t, sum, q, half, most);
                     continue;
                 }
-#pragma unroll 1
-                for (int c = 0; c < HALF / 16; ++c) {
-                    const int col = t.n0 + HALF * half + 16 * c;
-                    if (col >= o.N) break;
+            }
+            if (CG == 1 && a.splits > 1) {  // whole tiles: the partial sums' rows have room for them (a pair's tiles are not split)
+                constexpr int WIDTH = OP == F8_GU ? 64 : HALF;  // F8_GU: the first half is g's, the second u's
 #pragma unroll
-                    for (int z = 0; z < HALF / 16; ++z)
-                        if (z == c) put16(my_staging, sum + 16 * z);
-                    __syncwarp();
-                    f8_store16(o, sink, t.m0 + q * 32, col, my_staging);
-                }
+                for (int z = 0; z < HALF / WIDTH; ++z)
+                    row_store<WIDTH>(o, f8_sink(a, t, z, HALF / WIDTH), t.m0 + q * 32 + lane, t.n0 + WIDTH * half, sum + WIDTH * z);
+                continue;
+            }
+            const Sink sink = f8_sink(a, t);
+            if (!sink.add && t.n0 + HALF * (half + 1) <= o.N &&
+                ((reinterpret_cast<uintptr_t>(sink.out) | uintptr_t(sink.ld) * (sink.bf16 ? 2 : 4)) & 31) == 0) {
+                row_store<HALF>(o, sink, t.m0 + q * 32 + lane, t.n0 + HALF * half, sum);
+                continue;
+            }
+#pragma unroll 1
+            for (int c = 0; c < HALF / 16; ++c) {
+                const int col = t.n0 + HALF * half + 16 * c;
+                if (col >= o.N) break;
+#pragma unroll
+                for (int z = 0; z < HALF / 16; ++z)
+                    if (z == c) put16(my_staging, sum + 16 * z);
+                __syncwarp();
+                f8_store16(o, sink, t.m0 + q * 32, col, my_staging);
             }
         }
         __syncwarp();
@@ -775,7 +783,7 @@ __global__ void __launch_bounds__(256) f8_reduce_kernel(const __grid_constant__ 
         const int64_t m = i / quads;
         const int n = int(i - m * quads) * 4;
         float4 sum = make_float4(0, 0, 0, 0);
-        const float* src = o.partial + m * o.ld_partial + n;  // ld_partial is a multiple of 4: the last words past N are not used
+        const float* src = o.partial + m * o.ld_partial + n; 
         for (int s = 0; s < a.splits; ++s) {
             const float4 x = __ldcs(reinterpret_cast<const float4*>(src + s * plane));
             sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
@@ -787,24 +795,11 @@ __global__ void __launch_bounds__(256) f8_reduce_kernel(const __grid_constant__ 
     }
 }
 
-template <auto Kernel>
-cudaError_t allow(size_t smem) {  // said once for each device
-    static std::atomic<uint64_t> said{0};
-    int device = 0;
-    cudaError_t e = cudaGetDevice(&device);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (device & 63);
-    if (device < 64 && (said.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e == cudaSuccess) said.fetch_or(bit, std::memory_order_release);
-    return e;
-}
-
 template <int OP, int BN, int CG>
 cudaError_t launch_one(const F8Maps& maps, const F8Args& a, int sms, cudaStream_t st) {
     using C = F8Cfg<OP, BN, CG>;
     constexpr auto kernel = f8_gemm_kernel<OP, BN, CG>;
-    const cudaError_t e = allow<kernel>(C::SMEM);
+    const cudaError_t e = f8_allow_shared<kernel>(C::SMEM);
     if (e != cudaSuccess) return e;
     int64_t items = 0;
     for (int p = 0; p < (OP == F8_TN ? a.products : 1); ++p) items += int64_t(a.o[p].m_tiles) * a.o[p].n_tiles;
