@@ -23,6 +23,30 @@ struct Codes {          // codes and compact scales; q null: not wanted
 };
 
 // ---------------------------------------------------------------- reading and writing eight columns
+// Bytes [o, o + 16) of the 32 of a and b, 0 <= o < 16
+__device__ __forceinline__ uint4 bytes_from(uint4 a, uint4 b, int o) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (o & 8)
+#pragma unroll
+        for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+    if (o & 4)
+#pragma unroll
+        for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+    const int s = 8 * (o & 3);
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s), __funnelshift_r(w[3], w[4], s));
+}
+
+// 16 bytes at any address of which `bytes` (1 to 16) are the row's, the others as zeros: from the one or two aligned words that hold them
+__device__ __forceinline__ uint4 load16(const void* p, int bytes) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const int o = int(at & 15);
+    const uint4* src = reinterpret_cast<const uint4*>(at - o);
+    const uint4 a = __ldg(src), b = o + bytes > 16 ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+    const uint4 v = bytes_from(a, b, o);
+    auto own = [&](uint32_t w, int from) { return bytes >= from + 4 ? w : bytes <= from ? 0u : w & ((1u << 8 * (bytes - from)) - 1); };
+    return make_uint4(own(v.x, 0), own(v.y, 4), own(v.z, 8), own(v.w, 12));
+}
+
 // Eight elements of a row as they were read, and the largest magnitudes of such: of bf16 two to a register, which the maximum
 // keeps (a NaN is not taken)
 template <typename X>
@@ -33,10 +57,10 @@ struct Eight<__nv_bfloat16> {
     __device__ __forceinline__ void load(const __nv_bfloat16* p, int n, bool wide) {
         if (wide && n >= 8) {
             *reinterpret_cast<uint4*>(w) = __ldg(reinterpret_cast<const uint4*>(p));
+        } else if (n > 0) {
+            *reinterpret_cast<uint4*>(w) = load16(p, 2 * min(n, 8));
         } else {
-            const __nv_bfloat16 zero = __float2bfloat16(0.0f);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = __nv_bfloat162(2 * j < n ? p[2 * j] : zero, 2 * j + 1 < n ? p[2 * j + 1] : zero);
+            zero();
         }
     }
     __device__ __forceinline__ void zero() { *reinterpret_cast<uint4*>(w) = make_uint4(0, 0, 0, 0); }
@@ -64,9 +88,11 @@ struct Eight<float> {
         if (wide && n >= 8) {
             *reinterpret_cast<float4*>(w) = __ldg(reinterpret_cast<const float4*>(p));
             *reinterpret_cast<float4*>(w + 4) = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        } else if (n > 0) {
+            *reinterpret_cast<uint4*>(w) = load16(p, 4 * min(n, 4));
+            *reinterpret_cast<uint4*>(w + 4) = n > 4 ? load16(p + 4, 4 * min(n - 4, 4)) : make_uint4(0, 0, 0, 0);
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = j < n ? p[j] : 0.0f;
+            zero();
         }
     }
     __device__ __forceinline__ void zero() {
@@ -246,9 +272,51 @@ __device__ __forceinline__ void values8(uint2 w, float (&v)[8]) {
     }
 }
 
+// Eight results of each of the 16 lanes of a row, n of this one's to be written (a lane that has less than eight is the last).
+// Rows that do not start on 16 bytes are written in aligned words all the same: a lane's first word has the end of the lane before
+// it; only what is before the row's first whole word and behind its last goes element by element. All 16 lanes call it.
+template <typename Y>
+__device__ __forceinline__ void store_row(Y* to, int n, int c8, const uint4* x) {
+    constexpr int WORDS = sizeof(Y) / 2, PER = 16 / sizeof(Y);  // 16-byte words of eight results, results of a word
+    const int o = int(reinterpret_cast<uintptr_t>(to) & 15);
+    uint4 before;
+    before.x = __shfl_up_sync(0xffffffffu, x[WORDS - 1].x, 1, 16), before.y = __shfl_up_sync(0xffffffffu, x[WORDS - 1].y, 1, 16);
+    before.z = __shfl_up_sync(0xffffffffu, x[WORDS - 1].z, 1, 16), before.w = __shfl_up_sync(0xffffffffu, x[WORDS - 1].w, 1, 16);
+    auto each = [&](int from, int end) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint4& w = x[j / PER];
+            const uint32_t* half = &w.x;
+            const uint32_t v = half[(j % PER) * sizeof(Y) / 4];
+            if (j >= from && j < end) {
+                if constexpr (sizeof(Y) == 2)
+                    reinterpret_cast<unsigned short*>(to)[j] = static_cast<unsigned short>(j & 1 ? v >> 16 : v);
+                else
+                    reinterpret_cast<uint32_t*>(to)[j] = v;
+            }
+        }
+    };
+    if (n < 8) {
+        each(0, n);
+    } else if (o == 0) {
+#pragma unroll
+        for (int z = 0; z < WORDS; ++z) reinterpret_cast<uint4*>(to)[z] = x[z];
+    } else {
+        uint4* at = reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(to) - o);
+        const int head = (16 - o) / int(sizeof(Y));  // results before the first whole word
+        if (c8 == 0)
+            each(0, head);
+        else
+            at[0] = bytes_from(before, x[0], 16 - o);
+#pragma unroll
+        for (int z = 1; z < WORDS; ++z) at[z] = bytes_from(x[z - 1], x[z], 16 - o);
+        if (c8 == 15 || n < 16) each(8 - PER + head, 8);
+    }
+}
+
 template <typename Y>
 __global__ void __launch_bounds__(kQuantThreads) fp8_dequantize_kernel(const uint8_t* __restrict__ q, int64_t ldq, const float* __restrict__ s,
-                                                                       int block, int64_t rows, int cols, Y* __restrict__ out, int64_t ld, bool wide) {
+                                                                       int block, int64_t rows, int cols, Y* __restrict__ out, int64_t ld) {
     pdl_wait();
     pdl_trigger();
     const int col_blocks = (cols + 127) >> 7;
@@ -257,13 +325,12 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_dequantize_kernel(const uin
     const int c8 = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const int c0 = cb * 128 + c8 * 8, n = cols - c0;
     const int left = int(min(rows - rb * 128, int64_t(128)));
-    if (n <= 0) return;
     uint2 w[8];
     float rs[8], s8[8];
     const uint8_t* src = q + (rb * 128 + rg) * ldq + c0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const bool in = rg + 16 * i < left;
+        const bool in = rg + 16 * i < left && n > 0;
         w[i] = in ? codes8(src + 16 * i * ldq, n) : make_uint2(0, 0);
         rs[i] = block == MOE_B_ROW && in ? __ldg(s + cb * rows + rb * 128 + rg + 16 * i) : 1.0f;
     }
@@ -273,23 +340,18 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_dequantize_kernel(const uin
     Y* dst = out + (rb * 128 + rg) * ld + c0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (rg + 16 * i >= left) continue;
         float v[8];
         values8(w[i], v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= block == MOE_B_ROW ? rs[i] : s8[j];
         Y* to = dst + 16 * i * ld;
-        if (wide && n >= 8) {
-            if constexpr (sizeof(Y) == 2) {
-                *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-            } else {
-                reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
-            }
+        if constexpr (sizeof(Y) == 2) {
+            const uint4 x = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+            store_row(to, rg + 16 * i < left ? n : 0, c8, &x);
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) to[j] = Y(v[j]);
+            const uint4 x[2] = {make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])),
+                                make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]))};
+            store_row(to, rg + 16 * i < left ? n : 0, c8, x);
         }
     }
 }
@@ -812,16 +874,15 @@ moe_status moe_fp8_dequantize(const moe_fp8* v, int32_t block, int64_t rows, int
     if (rows == 0) return MOE_OK;
     if (!ok_codes(v, cols) || !ok_rows(out, out_type, out_stride, cols)) return MOE_ERR_INVALID_ARG;
     const dim3 grid(unsigned(blocks(rows) * blocks(cols)));
-    const bool wide = rows_on(out, out_stride, size_of(out_type), 16);
     const uint8_t* q = static_cast<const uint8_t*>(v->q);
     const float* s = v->scales;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     count_launch();
     if (out_type == MOE_T_BF16)
         return answer(launch_pdl(fp8_dequantize_kernel<__nv_bfloat16>, grid, dim3(kQuantThreads), 0, st, q, v->ld, s, block, rows, int(cols),
-                                 static_cast<__nv_bfloat16*>(out), out_stride, wide));
+                                 static_cast<__nv_bfloat16*>(out), out_stride));
     return answer(launch_pdl(fp8_dequantize_kernel<float>, grid, dim3(kQuantThreads), 0, st, q, v->ld, s, block, rows, int(cols),
-                             static_cast<float*>(out), out_stride, wide));
+                             static_cast<float*>(out), out_stride));
 }
 
 moe_status moe_linear_size(const moe_linear_config* cfg, int64_t T, int32_t backward, size_t* bytes) {

@@ -268,44 +268,34 @@ __device__ __forceinline__ Sink f8_sink(const F8Args& a, const Item& t, int part
     return s;
 }
 
-// The 16 columns in `staging` of rows row0 .. + 31. (No unrolling here, nor of the loop around it: a tile's results are written once, by
+// The 16 columns in `staging` of rows row0 .. + 31. (The loop around it is not unrolled: a tile's results are written once, by
 // instructions that are then fetched for the first time, and that took several times the writing.)
 __device__ __forceinline__ void f8_store16(const F8Out& o, const Sink& s, int row0, int col0, const float* staging) {
     const int lane = threadIdx.x & 31;
     if (s.wide && col0 + 16 <= o.N) {
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = i * 8 + (lane >> 2), j = lane & 3;
-            float4 x = reinterpret_cast<const float4*>(staging + r * 16)[j ^ ((r >> 1) & 3)];
-            if (row0 + r >= o.M) break;
+            const float4 x = reinterpret_cast<const float4*>(staging + r * 16)[j ^ ((r >> 1) & 3)];
             const int64_t at = int64_t(row0 + r) * s.ld + col0 + 4 * j;
-            if (s.bf16) {
-                uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(s.out) + at);
-                uint2 w = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-                if (s.add) {
-                    const uint2 old = *dst;
-                    float a0, a1, a2, a3, b0, b1, b2, b3;
-                    unpack_bf16x2(old.x, a0, a1), unpack_bf16x2(old.y, a2, a3);
-                    unpack_bf16x2(w.x, b0, b1), unpack_bf16x2(w.y, b2, b3);
-                    w = make_uint2(pack_bf16x2(a0 + b0, a1 + b1), pack_bf16x2(a2 + b2, a3 + b3));
-                }
-                *dst = w;
-            } else {
-                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(s.out) + at);
-                if (s.add) {
-                    const float4 old = *dst;
-                    x = make_float4(old.x + x.x, old.y + x.y, old.z + x.z, old.w + x.w);
-                }
-                *dst = x;
-            }
+            if (row0 + r >= o.M) continue;
+            if (s.bf16)
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(s.out) + at) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+            else
+                *reinterpret_cast<float4*>(static_cast<float*>(s.out) + at) = x;
         }
     } else {
         const int c = lane & 15;
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int r = i * 2 + (lane >> 4);
             const float x = staging[r * 16 + 4 * ((c >> 2) ^ ((r >> 1) & 3)) + (c & 3)];
-            if (row0 + r < o.M && col0 + c < o.N) store_one(s.out, int64_t(row0 + r) * s.ld + col0 + c, s.bf16, s.add, x);
+            const int64_t at = int64_t(row0 + r) * s.ld + col0 + c;
+            if (row0 + r >= o.M || col0 + c >= o.N) continue;
+            if (s.bf16)
+                static_cast<__nv_bfloat16*>(s.out)[at] = __float2bfloat16(x);
+            else
+                static_cast<float*>(s.out)[at] = x;
         }
     }
     __syncwarp();
@@ -519,10 +509,16 @@ __device__ __forceinline__ void column_store(const F8Out& o, const Sink& s, cons
             const float2 old = *dst;
             *dst = make_float2(old.x + a, old.y + b);
         });
+    } else if (!s.bf16) {
+        column_each<HALF>(o, t, s.ld, acc, q, half, [&](int64_t at, int c, float a, float b) {
+            float* dst = static_cast<float*>(s.out) + at;
+            if (c < o.N) dst[0] = s.add ? dst[0] + a : a;
+            if (c + 1 < o.N) dst[1] = s.add ? dst[1] + b : b;
+        });
     } else {
         column_each<HALF>(o, t, s.ld, acc, q, half, [&](int64_t at, int c, float a, float b) {
-            if (c < o.N) store_one(s.out, at, s.bf16, s.add, a);
-            if (c + 1 < o.N) store_one(s.out, at + 1, s.bf16, s.add, b);
+            if (c < o.N) store_one(s.out, at, true, s.add, a);
+            if (c + 1 < o.N) store_one(s.out, at + 1, true, s.add, b);
         });
     }
 }
@@ -743,7 +739,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
                 continue;
             }
             const Sink sink = f8_sink(a, t);
-            if (!sink.add && t.n0 + HALF * (half + 1) <= o.N &&
+            if (t.n0 + HALF * (half + 1) <= o.N &&
                 ((reinterpret_cast<uintptr_t>(sink.out) | uintptr_t(sink.ld) * (sink.bf16 ? 2 : 4)) & 31) == 0) {
                 row_store<HALF>(o, sink, t.m0 + q * 32 + lane, t.n0 + HALF * half, sum);
                 continue;
