@@ -549,8 +549,9 @@ typedef struct {
 } moe_fp8;
 
 /* Codes and scales of x[rows, cols] (x_type, any alignment, row stride x_stride >= cols in elements): any of the
- * three is NULL where it is not wanted, and several are made from one reading of x. 0 <= rows <= 2^24,
- * 1 <= cols <= 2^20. */
+ * three is NULL where it is not wanted, and several are made from one reading of x. They do not overlap one another or x.
+ * 0 <= rows <= 2^24, 1 <= cols <= 2^20. Rows that do not start on 16 bytes are read in whole 16-byte words: those that a row
+ * shares with its neighbours are read with it. */
 moe_status moe_fp8_quantize(const void* x, int32_t x_type, int64_t rows, int64_t cols, int64_t x_stride,
                             const moe_fp8* row, const moe_fp8* col, const moe_fp8* square, void* stream);
 
@@ -606,7 +607,7 @@ moe_status moe_ffn_forward(const moe_ffn_config* cfg, int64_t T, const void* x, 
  *   dh = Qrow(dy) Wd, dg = dh u silu'(g), du = dh silu(g) (with the clamp: 0 where g > L, where |u| > L)
  *   dx = Qrow(dg) Wg + Qrow(du) Wu
  *   grads: gate Qcol(dg)^T x, up Qcol(du)^T x [inter, hidden], down Qcol(dy)^T Qcol(h) [hidden, inter], written or added
- *   as moe_linear_backward's dweight.
+ *   as moe_linear_backward's dweight. They are written in one launch: three buffers that do not overlap.
  * dx NULL, grads NULL: not computed. */
 moe_status moe_ffn_backward(const moe_ffn_config* cfg, int64_t T, const void* dy, int64_t dy_stride, const moe_ffn_weights* w,
                             const moe_ffn_kept* kept, void* dx, int64_t dx_stride, const moe_ffn_grads* grads,

@@ -17,9 +17,9 @@ from .binding import (HostPipe, MoEDecoder, MoELayer, MoENorm, MoERouter, MoeErr
                       MOE_B_COL, MOE_B_ROW, MOE_B_SQUARE, FeedForwardWeights, MoEFeedForward, MoEFp8Linear, fp8_dequantize, fp8_quantize,
                       fp8_scales_shape, moe_ffn_config, moe_ffn_size, moe_linear_config, moe_linear_size,
                       weights_from_combined_mxfp8)
-from .block import BlockParams, MoEBlock
+from .block import BlockParams, DenseBlock, DenseParams, MoEBlock
 
-__all__ = ["BlockParams", "HostPipe", "MoEBlock", "MoEDecoder", "MoELayer", "MoENorm", "MoERouter", "MoeError", "load", "main_grads_from_combined", "moe_backward", "moe_config", "moe_create",
+__all__ = ["BlockParams", "DenseBlock", "DenseParams", "HostPipe", "MoEBlock", "MoEDecoder", "MoELayer", "MoENorm", "MoERouter", "MoeError", "load", "main_grads_from_combined", "moe_backward", "moe_config", "moe_create",
            "moe_handle_config", "moe_host_pipe_create", "moe_host_pipe_destroy", "moe_host_pipe_size", "moe_host_pipe_sync",
            "moe_host_step",
            "moe_destroy", "moe_device_status", "moe_export_routing", "moe_forward", "moe_forward_topk", "moe_kernel_name",

@@ -1126,6 +1126,12 @@ def _new_codes(torch, rows, cols, block, device):
     return (q if ld == cols else q[:, :cols]), torch.empty(fp8_scales_shape(rows, cols, block), dtype=torch.float32, device=device)
 
 
+def _as_view(pair) -> moe_fp8:
+    """The moe_fp8 of a pair that _new_codes made."""
+    q, s = pair
+    return moe_fp8(q.data_ptr(), q.stride(0), s.data_ptr())
+
+
 def _codes(torch, pair, rows, cols, block, index, what) -> moe_fp8:
     """The moe_fp8 of a (codes, scales) pair of the given size on the device `index`."""
     q, s = pair
@@ -1139,19 +1145,24 @@ def _codes(torch, pair, rows, cols, block, index, what) -> moe_fp8:
     return moe_fp8(q.data_ptr(), ld, s.data_ptr())
 
 
-_FP8_TYPES = {}
+@functools.lru_cache(maxsize=None)
+def _fp8_of_torch():
+    """(torch, moe_dtype of its types, current device, current stream of a device): looked up once."""
+    import torch
+    return torch, {torch.bfloat16: MOE_T_BF16, torch.float32: MOE_T_FP32}, _current_device_of(), _current_stream_of()
 
 
 def _fp8_types(torch):
-    if not _FP8_TYPES:
-        _FP8_TYPES.update({torch.bfloat16: MOE_T_BF16, torch.float32: MOE_T_FP32})
-    return _FP8_TYPES
+    return _fp8_of_torch()[1]
 
 
 def _as_rows(t, what):
-    """t, a 2-D tensor of bf16 or fp32 rows, with contiguous elements in them."""
+    """t, a 2-D tensor, with contiguous elements in its rows."""
     if t.dim() != 2 or t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
         raise ValueError(f"{what} must be rows with contiguous elements, bf16 or fp32")
+
+
+_BLOCKS = (MOE_B_ROW, MOE_B_COL, MOE_B_SQUARE)
 
 
 def fp8_quantize(x, block, out=None, stream=None):
@@ -1159,40 +1170,58 @@ def fp8_quantize(x, block, out=None, stream=None):
     down its columns, MOE_B_SQUARE both (a weight). codes uint8 [rows, cols] (E4M3), scales fp32 of fp8_scales_shape(rows,
     cols, block); `out`: a pair to write. An activation kept like this for a later pass takes half of its bf16 bytes.
     `stream`: where (the current stream)."""
-    import torch
+    torch, types, current, streams = _fp8_of_torch()
     if stream is not None:
         with torch.cuda.stream(stream):
             return fp8_quantize(x, block, out)
     _as_rows(x, "x")
-    xt = _fp8_types(torch).get(x.dtype)
-    if xt is None or block not in (MOE_B_ROW, MOE_B_COL, MOE_B_SQUARE):
+    xt, index = types.get(x.dtype), x.get_device()
+    if xt is None or block not in _BLOCKS:
         raise ValueError("x must be bf16 or fp32, and block one of MOE_B_ROW, MOE_B_COL, MOE_B_SQUARE")
-    with _on_one_device(x):
-        rows, cols = x.shape
-        pair = _new_codes(torch, rows, cols, block, x.device) if out is None else out
-        at = [None, None, None]
-        at[block] = _codes(torch, pair, rows, cols, block, x.get_device(), "out")
-        _check(load().moe_fp8_quantize(x.data_ptr(), xt, rows, cols, _ld(x), *at, _raw_stream(None, x.device)), "moe_fp8_quantize")
+    if index < 0:
+        raise ValueError("the tensors must be on one CUDA device")
+    if current() != index:  # kernels go to the current device
+        with torch.cuda.device(index):
+            return fp8_quantize(x, block, out)
+    rows, cols = x.shape
+    if out is None:
+        pair = _new_codes(torch, rows, cols, block, x.device)
+        v = _as_view(pair)
+    else:
+        pair, v = out, _codes(torch, out, rows, cols, block, index, "out")
+    status = load().moe_fp8_quantize(x.data_ptr(), xt, rows, cols, _ld(x), v if block == MOE_B_ROW else None, v if block == MOE_B_COL else None,
+                                     v if block == MOE_B_SQUARE else None, streams(index))
+    if status:
+        raise MoeError(status, "moe_fp8_quantize")
     return pair
 
 
 def fp8_dequantize(codes, scales, block, dtype=None, out=None, stream=None):
-    """The values [rows, cols] that codes and scales stand for, in `dtype` (bf16 by default) or the type of `out`."""
-    import torch
+    """The values [rows, cols] that codes and scales stand for, in `dtype` (bf16 by default) or the type of `out`.
+    `stream`: where (the current stream)."""
+    torch, types, current, streams = _fp8_of_torch()
     if stream is not None:
         with torch.cuda.stream(stream):
             return fp8_dequantize(codes, scales, block, dtype, out)
-    with _on_one_device(codes, scales, out):
-        rows, cols = codes.shape
-        if out is None:
-            out = torch.empty((rows, cols), dtype=torch.bfloat16 if dtype is None else dtype, device=codes.device)
-        _as_rows(out, "out")
-        yt = _fp8_types(torch).get(out.dtype)
-        if yt is None or out.shape != codes.shape or dtype not in (None, out.dtype) or block not in (MOE_B_ROW, MOE_B_COL, MOE_B_SQUARE):
-            raise ValueError("out must be bf16 or fp32 of the codes' shape, and block one of MOE_B_ROW, MOE_B_COL, MOE_B_SQUARE")
-        v = _codes(torch, (codes, scales), rows, cols, block, codes.get_device(), "codes and scales")
-        _check(load().moe_fp8_dequantize(v, block, rows, cols, out.data_ptr(), yt, _ld(out), _raw_stream(None, codes.device)),
-               "moe_fp8_dequantize")
+    index = codes.get_device()
+    if index < 0 or out is not None and out.get_device() != index:
+        raise ValueError("the tensors must be on one CUDA device")
+    if block not in _BLOCKS or codes.dim() != 2:
+        raise ValueError("codes must be [rows, cols], and block one of MOE_B_ROW, MOE_B_COL, MOE_B_SQUARE")
+    if current() != index:
+        with torch.cuda.device(index):
+            return fp8_dequantize(codes, scales, block, dtype, out)
+    rows, cols = codes.shape
+    v = _codes(torch, (codes, scales), rows, cols, block, index, "codes and scales")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.bfloat16 if dtype is None else dtype, device=codes.device)
+    yt = types.get(out.dtype)
+    if yt is None or out.shape != codes.shape or dtype not in (None, out.dtype):
+        raise ValueError("out must be bf16 or fp32, of the codes' shape")
+    _as_rows(out, "out")
+    status = load().moe_fp8_dequantize(v, block, rows, cols, out.data_ptr(), yt, _ld(out), streams(index))
+    if status:
+        raise MoeError(status, "moe_fp8_dequantize")
     return out
 
 
@@ -1245,9 +1274,8 @@ class MoEFp8Linear:
         y = torch.empty((T, self.N), dtype=yt, device=dev)
         kept = _new_codes(torch, T, K, MOE_B_COL, dev) if keep else None
         size = _sized(moe_linear_size, self._sizes, cfg, T)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-        status = self._forward(cfg, T, x.data_ptr(), _ld(x), w, y.data_ptr(), self.N,
-                               _codes(torch, kept, T, K, MOE_B_COL, index, "kept") if keep else None, workspace.data_ptr(), size,
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+        status = self._forward(cfg, T, x.data_ptr(), _ld(x), w, y.data_ptr(), self.N, _as_view(kept) if keep else None, _addr(workspace), size,
                                self._stream(index))
         if status:
             raise MoeError(status, "moe_linear_forward")
@@ -1360,7 +1388,7 @@ class MoEFeedForward:
         kept = views = None
         if keep:
             kept = (_new_codes(torch, T, H, MOE_B_COL, dev), _new_codes(torch, T, I, MOE_B_ROW, dev), _new_codes(torch, T, I, MOE_B_ROW, dev))
-            views = self._kept(kept, T, index)
+            views = moe_ffn_kept(*[_as_view(v) for v in kept])
         size = _sized(moe_ffn_size, self._sizes, self.cfg, T)
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
         status = self._forward(self.cfg, T, x.data_ptr(), _ld(x), w, y.data_ptr(), H, views, workspace.data_ptr(), size, self._stream(index))

@@ -1,4 +1,4 @@
-"""The expert block of a transformer: norm, router, experts and the residual stream around them.
+"""The blocks of a transformer: the expert block (norm, router, experts and the residual stream around them) and the dense one.
 
     s = x + residual            the residual stream, in x's type
     y = norm(s) w + b           bf16, the experts' input
@@ -150,3 +150,66 @@ class MoEBlock:
         for part in (self.layer, self.decoder):
             if part is not None:
                 part.close()
+
+
+@dataclasses.dataclass
+class DenseParams:
+    """Parameters of a dense block: norm_weight and norm_bias [H] (norm_bias may be None) and the feed-forward network's weights,
+    8-bit codes with a scale for each block of 128 (fp8_quantize(w, MOE_B_SQUARE) after every change of the master weights)."""
+    norm_weight: object
+    weights: B.FeedForwardWeights
+    norm_bias: object = None
+
+
+class DenseBlock:
+    """The dense sibling of MoEBlock, for the blocks of a model that have no experts, with 8-bit products:
+
+        s = x + residual
+        y = norm(s) w + b           bf16
+        out = feed-forward(y)       gate, up and down products, silu(g) u
+
+    ``forward`` keeps y, g and u in 8 bits for ``backward`` (``kept``: 3 bytes in place of 6 bf16 ones at the network's two
+    widths), ``decode`` keeps nothing. (out, s) are the next block's x and residual, as MoEBlock's. Every step may be captured into CUDA
+    graphs. One forward at a time waits for its backward."""
+
+    def __init__(self, hidden, inter, device="cuda", norm=B.MOE_NORM_RMS, eps=1e-6, swiglu_limit=0.0):
+        self.norm = B.MoENorm(hidden, eps, norm, device=device)
+        self.ffn = B.MoEFeedForward(hidden, inter, swiglu_limit, device=device)
+        self._kept = None
+
+    def _normed(self, x, residual, p):
+        import torch
+        return self.norm.forward(x, p.norm_weight, p.norm_bias, residual=residual, out_dtype=torch.bfloat16)
+
+    def forward(self, x, params: DenseParams, residual=None):
+        """(out [T,H] bf16, s [T,H] in x's type) of x and residual [T,H], bf16 or fp32; on the current stream."""
+        y, s, mean, rstd = self._normed(x, residual, params)
+        out, kept = self.ffn.forward(y, params.weights)
+        self._kept = (params, s, mean, rstd, kept)
+        return out, s
+
+    def backward(self, dout, ds=None, grads=None, accumulate=False):
+        """(dx, grads) for the gradients dout of out (bf16) and ds of s (x's type; None: zero): dx is that of x and of residual
+        alike; grads: norm_weight, norm_bias (None without one), gate, up and down. `grads`, `accumulate`: the last three's
+        buffers, as MoEFeedForward.backward's."""
+        if self._kept is None:
+            raise ValueError("backward without a forward before it")
+        p, s, mean, rstd, kept = self._kept
+        if dout.shape != s.shape or dout.device != s.device:
+            raise ValueError("dout must be [T, H] bf16 on the block's device")
+        if ds is not None:  # looked at before anything is added to grads
+            if ds.shape != s.shape or ds.dtype != s.dtype or ds.device != s.device:
+                raise ValueError("ds must be [T, H] of x's type on the block's device")
+            if ds.stride(1) != 1 or ds.stride(0) < ds.shape[1]:
+                ds = ds.contiguous()
+        if dout.stride(1) != 1 or dout.stride(0) < dout.shape[1]:
+            dout = dout.contiguous()
+        dy, (gate, up, down) = self.ffn.backward(dout, p.weights, kept, grads=grads, accumulate=accumulate)
+        self._kept = None
+        dx, dw, db = self.norm.backward(dy, s, p.norm_weight, mean, rstd, dsum=ds, bias=p.norm_bias is not None)
+        return dx, {"norm_weight": dw, "norm_bias": db, "gate": gate, "up": up, "down": down}
+
+    def decode(self, x, params: DenseParams, residual=None):
+        """(out, s) as forward's, with nothing kept."""
+        y, s, _, _ = self._normed(x, residual, params)
+        return self.ffn.forward(y, params.weights, keep=False)[0], s

@@ -133,6 +133,12 @@ __device__ __forceinline__ void put8(uint8_t* p, int n, const float (&v)[8], flo
     store8(p, n, e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r));
 }
 
+__device__ __forceinline__ float most_of16(float m) {  // over the 16 lanes that share a row
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    return m;
+}
+
 // Of N rows' (N = 4, 8) maxima over the 16 lanes that share them each lane gets one: that of row lane_row<N>(lane). Half of the rows go to the
 // other half of the lanes at every step, so that the sum of the exchanges is N and not 4 N.
 template <int N>
@@ -498,9 +504,7 @@ __global__ void __launch_bounds__(256) fp8_gated_sum_kernel(const __grid_constan
         float m = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
-#pragma unroll
-        for (int d = 1; d < 16; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float s = block_scale(m);
+        const float s = block_scale(most_of16(m));
         if (!mine) return;
         if (c8 == 0) scales[int64_t(block) * o.M + row] = s;
         if (n > 0) put8(q + row * ld + c0, n, x, __frcp_rn(s));
@@ -538,9 +542,13 @@ cudaError_t quantize(const void* x, int32_t type, int64_t rows, int64_t cols, in
                       wide, row, col, square);
 }
 
-int sm_count() {
+int sm_count() {  // of the current device
+    static std::atomic<int> known[64];
     int sms = 152, device = 0;
-    if (cudaGetDevice(&device) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+    if (cudaGetDevice(&device) != cudaSuccess) return sms;
+    if (device < 64 && (sms = known[device].load(std::memory_order_relaxed)) > 0) return sms;
+    sms = 152;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) == cudaSuccess && device < 64) known[device].store(sms, std::memory_order_relaxed);
     return sms;
 }
 
@@ -576,16 +584,21 @@ struct Plan {
 // whole, 10.4 in four parts, pairs 18.5; 6788 x 324, K 2900: pairs 18.8, 128 x 128 23.9. It goes by the sizes alone, as the workspace's size does.
 Plan plan(int op, const F8Args& a) {
     const int sms = sm_count();
-    double elements = 0;
-    for (int p = 0; p < a.products; ++p) elements += double(a.o[p].M) * a.o[p].N;
     const bool gated = op == F8_GU, slow = (op == F8_NT || op == F8_NN) && a.o[0].N % 16 != 0;
+    double elements = 0;
+    int64_t small = 0, wide = 0, pairs = 0;  // tiles
+    for (int p = 0; p < a.products; ++p) {
+        const int64_t M = a.o[p].M, N = a.o[p].N, n = (N + 127) / 128, n2 = gated ? n : (N + 255) / 256;
+        elements += double(M) * N;
+        small += (M + 127) / 128 * n;
+        wide += (M + 127) / 128 * n2;
+        pairs += (M + 255) / 256 * n2;
+    }
     Plan best = {256, 2, 1};
     double least = 1e30;
     auto look = [&](int bn, int cg, int splits) {
-        const int rows = 128 * cg, cols = gated ? 128 : bn, units = sms / cg;
-        int64_t items = 0;
-        for (int p = 0; p < a.products; ++p)
-            items += ((int64_t(a.o[p].M) + rows - 1) / rows) * ((int64_t(a.o[p].N) + cols - 1) / cols) * splits;
+        const int units = sms / cg;
+        const int64_t items = (cg == 2 ? pairs : bn == 256 ? wide : small) * splits;
         const double busy = items < units ? double(items) / units : 1.0;
         const double chain = (bn == 128 ? 0.3 + 0.25 * busy : cg == 2 ? 0.42 + 0.08 * busy : 0.45 + 0.15 * busy) + (op == F8_TN ? 0.35 : 0.0);
         const double ends = (bn == 128 ? 4.0 : (cg == 2 ? 6.0 : 5.5) * (slow && splits == 1 ? 2.0 : 1.0)) + (gated && splits == 1 ? 3.0 : 0.0);
@@ -594,7 +607,8 @@ Plan plan(int op, const F8Args& a) {
         if (us < least) least = us, best = {bn, cg, splits};
     };
     look(256, 2, 1);
-    for (int splits = 1; splits <= 16 && splits <= a.k_blocks; ++splits) {
+    for (const int splits : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16}) {
+        if (splits > a.k_blocks || (splits > 1 && wide > sms)) break;
         if (gated || splits == 1) look(256, 1, splits);
         if (!gated) look(128, 1, splits);
     }
@@ -997,7 +1011,8 @@ moe_status moe_ffn_backward(const moe_ffn_config* cfg, int64_t T, const void* dy
     const int32_t gt = g_type == MOE_G_BF16 ? MOE_T_BF16 : MOE_T_FP32;
     if (!ok_grad(g_type, accumulate) || dy_stride < H || (dx && dx_stride < H)) return MOE_ERR_INVALID_ARG;
     if (grads && (!ok_rows(grads->gate, gt, grads->gate_stride, H) || !ok_rows(grads->up, gt, grads->up_stride, H) ||
-                  !ok_rows(grads->down, gt, grads->down_stride, I)))
+                  !ok_rows(grads->down, gt, grads->down_stride, I) || grads->gate == grads->up || grads->gate == grads->down ||
+                  grads->up == grads->down))
         return MOE_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T == 0) {

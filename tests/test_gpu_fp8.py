@@ -465,3 +465,287 @@ def test_feed_forward(T, H, I, L, pad, shift):
         close(got, f.double() + r, t * (1 + 2.0 ** -8) + 2.0 ** -8 * r.abs(), name + " added to bf16")
     only, none = ffn.backward(dy, fw, kept, need_grads=False)
     assert none is None and torch.equal(only, dx)
+
+
+# ------------------------------------------------------------------ the calls that a program makes of them
+def ffn_setup(T, H, I, seed=0, limit=0.0):
+    gn = gen(seed)
+    x = activation(gn, T, H).bfloat16()
+    w = M.FeedForwardWeights(weight(gn, I, H), weight(gn, I, H), weight(gn, H, I))
+    return M.MoEFeedForward(H, I, limit), w, x, randn(gn, T, H).bfloat16()
+
+
+def ffn_step(ffn, w, x, dy, **kw):
+    y, kept = ffn.forward(x, w, **kw)
+    dx, grads = ffn.backward(dy, w, kept, **kw)
+    return (y, dx, *grads)
+
+
+@gpu
+@pytest.mark.parametrize("T,H,I", [(5, 256, 384), (300, 520, 400), (3000, 512, 1100)])
+def test_results_repeat_bitwise(T, H, I):
+    ffn, w, x, dy = ffn_setup(T, H, I)
+    first = ffn_step(ffn, w, x, dy)
+    for _ in range(3):
+        for a, b in zip(first, ffn_step(ffn, w, x, dy)):
+            assert torch.equal(a, b)
+
+
+@gpu
+def test_streams():
+    sets = [ffn_setup(200, 384, 512, seed) for seed in range(4)]
+    want = [ffn_step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = [ffn_step(*s, stream=st) for s, st in zip(sets, streams)]     # four at a time
+        for st in streams:
+            torch.cuda.current_stream().wait_stream(st)
+        for g, r in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, r))
+    q = M.fp8_quantize(sets[0][2], COL, stream=streams[0])
+    x = M.fp8_dequantize(*q, COL, stream=streams[0])
+    torch.cuda.current_stream().wait_stream(streams[0])
+    assert torch.equal(x, M.fp8_dequantize(*M.fp8_quantize(sets[0][2], COL), COL))
+
+
+@gpu
+@pytest.mark.parametrize("T", [3, 40, 700])
+def test_graphs(T):
+    """Two captured steps of one network, replayed in turn on other inputs, beside eager calls."""
+    sets = [ffn_setup(T, 300, 260, seed) for seed in range(2)]
+    ffn = sets[0][0]
+    graphs = []
+    for _, w, x, dy in sets:
+        ffn_step(ffn, w, x, dy)
+        ffn.forward(x, w, keep=False)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = ffn_step(ffn, w, x, dy)
+            alone = ffn.forward(x, w, keep=False)[0]
+        graphs.append((g, out, alone))
+    for turn in range(3):
+        for (_, w, x, dy), (g, out, alone) in zip(sets, graphs):
+            x.copy_(activation(gen(10 + turn), T, 300).bfloat16())
+            dy.copy_(randn(gen(20 + turn), T, 300).bfloat16())
+            g.replay()
+            eager = ffn_step(ffn, w, x, dy)
+            assert all(torch.equal(a, b) for a, b in zip(out, eager))
+            assert torch.equal(alone, ffn.forward(x, w, keep=False)[0])
+
+
+@gpu
+def test_no_rows():
+    ffn, w, x, dy = ffn_setup(4, 200, 130)
+    y, kept = ffn.forward(x[:0], w)
+    assert y.shape == (0, 200) and kept[0][1].shape == (0, 200)
+    dx, grads = ffn.backward(dy[:0], w, kept)
+    assert dx.shape == (0, 200) and all((g == 0).all() for g in grads)
+    bufs = [torch.full_like(g, 3.0) for g in grads]
+    ffn.backward(dy[:0], w, kept, grads=bufs, accumulate=True)
+    assert all((b == 3).all() for b in bufs)
+    lin, wl = M.MoEFp8Linear(200, 130), weight(gen(1), 130, 200)
+    y, kept = lin.forward(x[:0], wl)
+    dw = torch.full((130, 200), 5.0, device="cuda", dtype=BF16)
+    dx, _ = lin.backward(y, wl, kept, dweight=dw)
+    assert dx.shape == (0, 200) and (dw == 0).all()
+    q, s = M.fp8_quantize(x[:0], ROW)
+    assert q.shape == (0, 200) and s.shape == (2, 0) and M.fp8_dequantize(q, s, ROW).shape == (0, 200)
+
+
+@gpu
+@pytest.mark.parametrize("T", [4, 100, 600])
+def test_a_bad_token_stays_alone(T):
+    """NaN and infinities of one token reach its own rows only, and the weights' gradients as NaN."""
+    ffn, w, x, dy = ffn_setup(T, 384, 256)
+    for bad in (math.nan, math.inf):
+        xb = x.clone()
+        xb[1, 7] = bad
+        y, yb = ffn.forward(x, w, keep=False)[0], ffn.forward(xb, w, keep=False)[0]
+        assert torch.isnan(yb[1]).all()
+        others = torch.arange(T, device="cuda") != 1
+        assert torch.equal(y[others], yb[others])
+        _, kept = ffn.forward(x, w)
+        db = dy.clone()
+        db[1, 7] = bad
+        dx, _ = ffn.backward(dy, w, kept)
+        dxb, grads = ffn.backward(db, w, kept)
+        assert torch.isnan(dxb[1]).all() and torch.equal(dx[others], dxb[others])
+        assert all(torch.isnan(g).any() for g in grads)
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 9, 33, 200])
+def test_weights_in_wider_buffers(T):
+    """gate and up as halves of one matrix, rows with other bytes behind them (NaN codes): nothing of those is read as a value."""
+    H, I = 250, 256
+    gn = gen(T)
+    x = activation(gn, T, H).bfloat16()
+    q, s = M.fp8_quantize((randn(gn, 2 * I, H) * 0.05).bfloat16(), SQUARE)
+    wide = torch.full((2 * I, 288), 0x7F, dtype=torch.uint8, device="cuda")
+    wide[:, :H] = q
+    halves = [(wide[:I, :H], s[:2]), (wide[I:, :H], s[2:])]
+    down = weight(gn, H, I)
+    ffn = M.MoEFeedForward(H, I)
+    w = M.FeedForwardWeights(*halves, down)
+    plain = M.FeedForwardWeights((q[:I], s[:2].clone()), (q[I:], s[2:].clone()), down)
+    dy = randn(gn, T, H).bfloat16()
+    for a, b in zip(ffn_step(ffn, w, x, dy), ffn_step(ffn, plain, x, dy)):
+        assert torch.equal(a, b) and torch.isfinite(a).all()
+    assert torch.equal(ffn.forward(x, w, keep=False)[0], ffn.forward(x, plain, keep=False)[0])
+    lin = M.MoEFp8Linear(H, 2 * I)
+    assert torch.equal(lin.forward(x, (wide[:, :H], s))[0], lin.forward(x, (q, s))[0])
+
+
+@gpu
+@pytest.mark.parametrize("T", [3, 70, 500])
+def test_results_in_wider_buffers(T):
+    """Through the C entry points: y, dx and the kept codes in rows of wider buffers, whose other elements stay."""
+    K, N, L = 200, 330, M.load()
+    gn = gen(T)
+    x, dy, w = activation(gn, T, K).bfloat16(), randn(gn, T, N).bfloat16(), weight(gn, N, K)
+    lin = M.MoEFp8Linear(K, N)
+    y, kept = lin.forward(x, w)
+    dx, dw = lin.backward(dy, w, kept)
+    cfg, stream = lin._cfg(BF16, BF16), torch.cuda.current_stream().cuda_stream
+    for pad in (1, 8):
+        yb, xb = (torch.full((T + 1, n + pad), 7.0, dtype=BF16, device="cuda") for n in (N, K))
+        kq = torch.full((T + 1, 224), 0x55, dtype=torch.uint8, device="cuda")
+        ks = torch.full((kept[1].numel() + 8,), 9.0, device="cuda")
+        ws = torch.empty(M.moe_linear_size(cfg, T, True) + M.moe_linear_size(cfg, T), dtype=torch.uint8, device="cuda")
+        v = B._codes(torch, w, N, K, SQUARE, 0, "")
+        k = B.moe_fp8(kq.data_ptr(), 224, ks.data_ptr())
+        assert L.moe_linear_forward(cfg, T, x.data_ptr(), K, v, yb.data_ptr(), N + pad, k, ws.data_ptr(), ws.numel(), stream) == 0
+        assert L.moe_linear_backward(cfg, T, dy.data_ptr(), N, v, k, xb.data_ptr(), K + pad, None, 0, 0, 0, ws.data_ptr(), ws.numel(), stream) == 0
+        assert torch.equal(yb[:T, :N], y) and (yb[T] == 7).all() and (yb[:, N:] == 7).all()
+        assert torch.equal(xb[:T, :K], dx) and (xb[T] == 7).all() and (xb[:, K:] == 7).all()
+        assert torch.equal(kq[:T, :K], kept[0]) and (kq[T] == 0x55).all() and (kq[:, K:] == 0x55).all()
+        assert torch.equal(ks[:-8].view_as(kept[1]), kept[1]) and (ks[-8:] == 9).all()
+
+
+@gpu
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows of codes, values and a product's results."""
+    R, C = 2_150_000, 1016
+    x = torch.zeros(R, C, dtype=BF16, device="cuda")
+    x[-300:] = randn(gen(1), 300, C).bfloat16()
+    for block in (ROW, COL):
+        q, s = M.fp8_quantize(x, block)
+        back = M.fp8_dequantize(q, s, block)
+        lo = R // 128 * 128 - 128   # whole blocks of rows
+        rq, rs = ref_codes(x[lo:], block)
+        assert torch.equal(q[lo:], rq) and torch.equal(s[:, lo:] if block == ROW else s[lo // 128:], rs)
+        assert torch.equal(back[lo:], values((rq, rs), block).float().bfloat16()) and not back[:lo - 300].any()
+        del q, s, back
+    del x
+    T, K, N = 1_060_000, 64, 2040
+    x = torch.zeros(T, K, dtype=BF16, device="cuda")
+    x[-300:] = randn(gen(2), 300, K).bfloat16()
+    w = weight(gen(3), N, K)
+    y, _ = M.MoEFp8Linear(K, N).forward(x, w, keep=False)
+    X, W = values(ref_codes(x[-300:], ROW), ROW), values(w, SQUARE)
+    close(y[-300:], X @ W.t(), sum_tol(X.abs() @ W.abs().t(), K), "y")
+    assert not y[:-300].any()
+
+
+@gpu
+def test_more_refusals():
+    ffn, w, x, dy = ffn_setup(4, 64, 64)
+    _, kept = ffn.forward(x, w)
+    one = torch.zeros(64, 64, device="cuda")
+    with pytest.raises(B.MoeError):       # one buffer for two gradients
+        ffn.backward(dy, w, kept, grads=[one, one, torch.zeros_like(one)])
+    with pytest.raises(ValueError):
+        ffn.backward(dy, w, kept, grads=[one, one.clone(), one.bfloat16()])
+    with pytest.raises(ValueError):
+        ffn.backward(dy.float(), w, kept)
+    with pytest.raises(ValueError):
+        M.DenseBlock(64, 64).backward(dy)
+    block = M.DenseBlock(64, 64)
+    params = M.DenseParams(torch.ones(64, device="cuda"), w)
+    out, s = block.forward(x, params)
+    with pytest.raises(ValueError):
+        block.backward(dy[:2])
+    with pytest.raises(ValueError):
+        block.backward(dy, ds=dy.float())
+    with pytest.raises(ValueError):
+        block.backward(dy.float())
+    block.backward(dy)
+    with pytest.raises(ValueError):       # once for each forward
+        block.backward(dy)
+
+
+@gpu
+@pytest.mark.parametrize("T,xt,norm,bias", [(1, BF16, "rms", False), (20, F32, "layer", True), (500, BF16, "rms", True)])
+def test_dense_block(T, xt, norm, bias):
+    """The block is its operators one after the other; its forward and backward against the whole formula in 64 bits, normwise."""
+    H, I = 264, 520
+    gn = gen(T)
+    x, res = randn(gn, T, H).to(xt), randn(gn, T, H).to(xt)
+    p = M.DenseParams(1 + 0.1 * randn(gn, H), M.FeedForwardWeights(weight(gn, I, H), weight(gn, I, H), weight(gn, H, I)),
+                      0.1 * randn(gn, H) if bias else None)
+    kind = B.MOE_NORM_RMS if norm == "rms" else B.MOE_NORM_LAYER
+    block = M.DenseBlock(H, I, norm=kind, eps=1e-5)
+    out, s = block.forward(x, p, residual=res)
+    dout, ds = randn(gn, T, H).bfloat16(), randn(gn, T, H).to(xt)
+    dx, grads = block.backward(dout, ds=ds)
+    y, s2, mean, rstd = M.MoENorm(H, 1e-5, kind).forward(x, p.norm_weight, p.norm_bias, residual=res, out_dtype=BF16)
+    ffn = M.MoEFeedForward(H, I)
+    o2, kept = ffn.forward(y, p.weights)
+    assert torch.equal(out, o2) and torch.equal(s, s2)
+    dy, g2 = ffn.backward(dout, p.weights, kept)
+    dx2, dw2, db2 = M.MoENorm(H, 1e-5, kind).backward(dy, s2, p.norm_weight, mean, rstd, dsum=ds, bias=bias)
+    assert torch.equal(dx, dx2) and torch.equal(grads["norm_weight"], dw2) and (not bias or torch.equal(grads["norm_bias"], db2))
+    assert all(torch.equal(grads[n], g) for n, g in zip(("gate", "up", "down"), g2))
+
+    # without any quantisation of activations, the weights' values as they are: each storing in 8 bits moves a value by at most 2^-4 of itself (or
+    # of the smallest normal number, 2^-6 / 448 of its block's largest), and with independent signs by its 2-norm 2^-4 / sqrt(3) at most; y has two
+    # of them in a row (x, h), the gradients up to four. Bounds of 2^-4 and 2^-3 of the 2-norm, then.
+    wg, wu, wd = (values(v, SQUARE) for v in p.weights.tensors)
+    leaf = s.double().requires_grad_(True)
+    mu = leaf.mean(-1, keepdim=True) if norm == "layer" else 0
+    yy = (leaf - mu) / torch.sqrt((leaf - mu).pow(2).mean(-1, keepdim=True) + 1e-5) * p.norm_weight.double()
+    if bias:
+        yy = yy + p.norm_bias.double()
+    exact = (torch.nn.functional.silu(yy @ wg.t()) * (yy @ wu.t())) @ wd.t()
+    (dleaf,) = torch.autograd.grad(exact, leaf, dout.double())
+    assert (out.double() - exact).norm() <= 2.0 ** -4 * exact.norm()
+    assert (dx.double() - ds.double() - dleaf).norm() <= 2.0 ** -3 * dleaf.norm() + 2.0 ** -8 * dx.double().norm()
+
+    alone, s3 = block.decode(x, p, residual=res)
+    assert torch.equal(s3, s) and (alone.double() - exact).norm() <= 2.0 ** -4 * exact.norm()
+
+
+@gpu
+def test_expert_and_dense_blocks_in_turn():
+    """A dense block, an expert block and another dense one: the residual stream through all of them, forward, backward and decode."""
+    T, H, I, E, k = 96, 256, 128, 4, 2
+    gn = gen(5)
+    dense = [M.DenseBlock(H, I) for _ in range(2)]
+    dp = [M.DenseParams(torch.ones(H, device="cuda"), M.FeedForwardWeights(weight(gn, I, H), weight(gn, I, H), weight(gn, H, I))) for _ in dense]
+    fc1, fc2 = (randn(gn, E, 2 * I, H) * 0.05).bfloat16(), (randn(gn, E, H, I) * 0.05).bfloat16()
+    sfc1, sfc2 = (randn(gn, 2 * I, H) * 0.05).bfloat16(), (randn(gn, H, I) * 0.05).bfloat16()
+    moe = M.MoEBlock(T, H, E, k, I)
+    mp = M.BlockParams(torch.ones(H, device="cuda"), randn(gn, E, H) * 0.05, M.weights_from_combined(sfc1, sfc2, fc1, fc2))
+    mg = [torch.zeros_like(t, dtype=F32) for t in (sfc1, sfc2, fc1, fc2)]
+    x = randn(gn, T, H).bfloat16()
+
+    def forward():
+        a, s = dense[0].forward(x, dp[0])
+        b, s, _ = moe.forward(a, mp, residual=s)
+        return dense[1].forward(b, dp[1], residual=s)
+
+    out, s = forward()
+    dout, ds = randn(gn, T, H).bfloat16(), randn(gn, T, H).bfloat16()
+    db, last = dense[1].backward(dout, ds=ds)
+    da, _ = moe.backward(db, M.main_grads_from_combined(*mg), ds=db)
+    dx, first = dense[0].backward(da, ds=da)
+    for t in (out, s, dx, *[v for g in (first, last) for v in g.values() if v is not None], *mg):
+        assert torch.isfinite(t).all() and t.abs().max() > 0
+    again, s2 = forward()
+    assert torch.equal(out, again) and torch.equal(s, s2)
+    a, r = dense[0].decode(x, dp[0])
+    b, r = moe.decode(a, mp, residual=r)
+    alone, r = dense[1].decode(b, dp[1], residual=r)
+    assert (alone.double() - out.double()).norm() <= 2.0 ** -4 * out.double().norm()
