@@ -721,7 +721,7 @@ F8Few few(const Codes& w, const void* x, int64_t ld_x, int32_t x_type, void* out
 
 cudaError_t linear_forward(const LinearCall& k, Arena& ws, bool run, cudaStream_t st) {
     const int64_t T = k.T, K = k.c->in_features, N = k.c->out_features;
-    if (f8_few_fits(T, N, K, sm_count())) {
+    if (f8_few_fits(T, N, K, false, sm_count())) {
         if (!run) return cudaSuccess;
         if (k.kept.q) {
             const cudaError_t e = quantize(k.in, k.c->x_type, T, K, k.in_stride, kNone, k.kept, kNone, st);
@@ -729,7 +729,7 @@ cudaError_t linear_forward(const LinearCall& k, Arena& ws, bool run, cudaStream_
         }
         F8Few a = few(k.w, k.in, k.in_stride, k.c->x_type, k.out, k.out_stride, k.c->y_type == MOE_T_BF16, T, N, K);
         a.early = k.kept.q != nullptr;
-        return launch_f8_few(a, k.c->x_type == MOE_T_BF16, st);
+        return launch_f8_few(a, k.c->x_type == MOE_T_BF16, sm_count(), st);
     }
     const Codes xq = ws.codes(T, K, true);
     if (run) {
@@ -773,16 +773,16 @@ cudaError_t ffn_few(const FfnCall& k, Arena& ws, bool run, cudaStream_t st) {
     F8Few g = few(k.gate, k.in, k.in_stride, MOE_T_BF16, h, ld_h, false, T, I, H);
     g.w[1] = k.up.q, g.ld_w[1] = k.up.ld, g.ws[1] = k.up.s;
     g.limit = k.c->swiglu_limit;
-    const cudaError_t e = launch_f8_few(g, true, st);
+    const cudaError_t e = launch_f8_few(g, true, sm_count(), st);
     if (e != cudaSuccess) return e;
     F8Few d = few(k.down, h, ld_h, MOE_T_FP32, k.out, k.out_stride, true, T, H, I);
     d.early = 1;
-    return launch_f8_few(d, false, st);
+    return launch_f8_few(d, false, sm_count(), st);
 }
 
 cudaError_t ffn_forward(const FfnCall& k, Arena& ws, bool run, cudaStream_t st) {
     const int64_t T = k.T, H = k.c->hidden, I = k.c->inter;
-    if (!k.kx.q && f8_few_fits(T, I, H, sm_count()) && f8_few_fits(T, H, I, sm_count())) return ffn_few(k, ws, run, st);
+    if (!k.kx.q && f8_few_fits(T, I, H, true, sm_count()) && f8_few_fits(T, H, I, false, sm_count())) return ffn_few(k, ws, run, st);
     const Codes xq = ws.codes(T, H, true), h = ws.codes(T, I, true);
     F8Args a = {};
     a.products = 1;

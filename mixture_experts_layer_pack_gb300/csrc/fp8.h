@@ -86,7 +86,7 @@ struct F8Few {
     int early;             // the kernel before in the stream is one of the same call: it has not written the weights
     float limit;
 };
-bool f8_few_fits(int64_t T, int64_t N, int64_t K, int sms);
-cudaError_t launch_f8_few(const F8Few& a, bool x_bf16, cudaStream_t st);
+bool f8_few_fits(int64_t T, int64_t N, int64_t K, bool gated, int sms);
+cudaError_t launch_f8_few(const F8Few& a, bool x_bf16, int sms, cudaStream_t st);
 
 }  // namespace moe
