@@ -127,12 +127,15 @@ __device__ __forceinline__ void store8(uint8_t* p, int n, uint32_t lo, uint32_t 
 }
 
 __device__ __forceinline__ void put8(uint8_t* p, int n, const float (&v)[8], const float (&r)[8]) {
-    store8(p, n, e4m3x4(v[0] * r[0], v[1] * r[1], v[2] * r[2], v[3] * r[3]), e4m3x4(v[4] * r[4], v[5] * r[5], v[6] * r[6], v[7] * r[7]));
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) unpair(mul2(pair(v[j], v[j + 1]), pair(r[j], r[j + 1])), q[j], q[j + 1]);
+    store8(p, n, e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
 }
 __device__ __forceinline__ void put8(uint8_t* p, int n, const float (&v)[8], float r) {
-    store8(p, n, e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r));
+    const float r8[8] = {r, r, r, r, r, r, r, r};
+    put8(p, n, v, r8);
 }
-
 __device__ __forceinline__ float most_of16(float m) {  // over the 16 lanes that share a row
 #pragma unroll
     for (int d = 1; d < 16; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -373,25 +376,40 @@ struct GatedBack {
     float limit;
 };
 
-// dg, du and h of eight columns of a row
+// dg, du and h of eight columns of a row, two columns an instruction
+template <bool CLAMP>
 __device__ __forceinline__ void gated_back8(const float (&dh)[8], const float (&gq)[8], float sg, const float (&uq)[8], float su,
                                             float limit, float (&dg)[8], float (&du)[8], float (&h)[8]) {
-    const bool clamp = limit > 0.0f;
+    const uint64_t sg2 = pair(sg, sg), su2 = pair(su, su), one = pair(1.0f, 1.0f), minus = pair(-1.0f, -1.0f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float g = gq[j] * sg, u = uq[j] * su;
-        const float gc = clamp ? clamp_top(g, limit) : g, uc = clamp ? clamp_both(u, limit) : u;
-        const float sig = sigmoidf_(gc), silu = gc * sig;
-        h[j] = silu * uc;
-        dg[j] = clamp && g > limit ? 0.0f : dh[j] * uc * (sig * (1.0f + gc * (1.0f - sig)));
-        du[j] = clamp && fabsf(u) > limit ? 0.0f : dh[j] * silu;
+    for (int j = 0; j < 8; j += 2) {
+        const uint64_t g2 = mul2(pair(gq[j], gq[j + 1]), sg2), u2 = mul2(pair(uq[j], uq[j + 1]), su2), dh2 = pair(dh[j], dh[j + 1]);
+        float g[2], u[2], gc[2], uc[2];
+        unpair(g2, g[0], g[1]), unpair(u2, u[0], u[1]);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) gc[z] = CLAMP ? clamp_top(g[z], limit) : g[z], uc[z] = CLAMP ? clamp_both(u[z], limit) : u[z];
+        const uint64_t gc2 = pair(gc[0], gc[1]), uc2 = pair(uc[0], uc[1]);
+        const uint64_t sig = pair(sigmoidf_(gc[0]), sigmoidf_(gc[1])), silu = mul2(gc2, sig);
+        const uint64_t slope = mul2(sig, mad2(gc2, mad2(sig, minus, one), one));
+        unpair(mul2(silu, uc2), h[j], h[j + 1]);
+        unpair(mul2(mul2(dh2, uc2), slope), dg[j], dg[j + 1]);
+        unpair(mul2(dh2, silu), du[j], du[j + 1]);
+        if constexpr (CLAMP) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                dg[j + z] = g[z] > limit ? 0.0f : dg[j + z];
+                du[j + z] = fabsf(u[z]) > limit ? 0.0f : du[j + z];
+            }
+        }
     }
 }
 
 // dh and the kept g, u -> dg and du as row blocks (for dx) and column blocks, h as column blocks (for the weights' gradients).
 // 128 tokens x 128 columns a block. The results are computed twice, for the maxima and for the codes, from inputs that are
 // read twice, the second time from L2: held in registers, they or the results leave room for one block an SM, whose reads,
-// arithmetic and writes then wait for one another (8192 x 8192: 335 us).
+// arithmetic and writes then wait for one another (8192 x 8192: 335 us). Its instructions bound it: at 8192 x 8192 one column each 250 us and with
+// a clamp 288; two columns each, and the clamp compiled apart, 216 and 272.
+template <bool CLAMP>
 __global__ void __launch_bounds__(kGatedThreads, 2) fp8_gated_back_kernel(const GatedBack a) {
     constexpr int W = kGatedThreads / 32, R = 128 * 16 / kGatedThreads, S = 128 / R;
     __shared__ float part[3][W][128];
@@ -414,7 +432,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) fp8_gated_back_kernel(const 
         const float sg = __ldg(a.g.s + cb * a.T + r), su = __ldg(a.u.s + cb * a.T + r);
         float g[8], u[8];
         values8(gq, g), values8(uq, u);
-        gated_back8(dh.w, g, sg, u, su, a.limit, dg, du, h);
+        gated_back8<CLAMP>(dh.w, g, sg, u, su, a.limit, dg, du, h);
     };
     float mg[R], mu[R], mc[3][8] = {};
 #pragma unroll
@@ -824,7 +842,7 @@ cudaError_t ffn_backward(const FfnCall& k, Arena& ws, bool run, cudaStream_t st)
     if (e != cudaSuccess) return e;
     if (run) {
         count_launch();
-        e = launch_pdl(fp8_gated_back_kernel, dim3(unsigned(blocks(T) * blocks(I))), dim3(kGatedThreads), 0, st, b);
+        e = launch_pdl(b.limit > 0.0f ? fp8_gated_back_kernel<true> : fp8_gated_back_kernel<false>, dim3(unsigned(blocks(T) * blocks(I))), dim3(kGatedThreads), 0, st, b);
         if (e != cudaSuccess) return e;
     }
     if (x) {

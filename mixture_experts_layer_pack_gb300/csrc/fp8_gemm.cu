@@ -204,19 +204,7 @@ __device__ __forceinline__ void tmem_ask_pairs(uint32_t taddr, uint32_t* r) {
 
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// two fp32 numbers in a register pair, and the paired operations on them (one instruction each)
-__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) {
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(a), "r"(b));
-    return p;
-}
-__device__ __forceinline__ uint64_t pair(float a, float b) { return pair(__float_as_uint(a), __float_as_uint(b)); }
-__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t p;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
-    return p;
-}
+// y += a b, both numbers of a pair
 __device__ __forceinline__ void fma2(uint64_t& y, uint64_t a, uint64_t b) { asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(y) : "l"(a), "l"(b)); }
 
 // ---------------------------------------------------------------- work items
