@@ -1122,8 +1122,8 @@ def fp8_scales_shape(rows, cols, block):
 def _new_codes(torch, rows, cols, block, device):
     """A new (codes, scales) pair: codes uint8 [rows, cols] whose row stride is a multiple of 16."""
     ld = (cols + 15) // 16 * 16
-    q = torch.empty((rows, ld), dtype=torch.uint8, device=device)
-    return (q if ld == cols else q[:, :cols]), torch.empty(fp8_scales_shape(rows, cols, block), dtype=torch.float32, device=device)
+    q = torch.empty_strided((rows, cols), (ld, 1), dtype=torch.uint8, device=device)   # half the time of a slice of rows x ld
+    return q, torch.empty(fp8_scales_shape(rows, cols, block), dtype=torch.float32, device=device)
 
 
 def _as_view(pair) -> moe_fp8:

@@ -442,7 +442,7 @@ def test_feed_forward(T, H, I, L, pad, shift):
     y, kept = ffn.forward(x, fw)
     ref, tol, g, eg, u, eu = ffn_forward_ref(x, wg, wu, wd, L)
     close(y, ref, tol, "y")
-    alone, none = ffn.forward(x, fw, keep=False)    # up to 64 tokens by other kernels
+    alone, none = ffn.forward(x, fw, keep=False)    # few tokens by other kernels
     assert none is None
     close(alone, ref, tol, "y, nothing kept")
     rq, rs = ref_codes(x, COL)
@@ -465,6 +465,39 @@ def test_feed_forward(T, H, I, L, pad, shift):
         close(got, f.double() + r, t * (1 + 2.0 ** -8) + 2.0 ** -8 * r.abs(), name + " added to bf16")
     only, none = ffn.backward(dy, fw, kept, need_grads=False)
     assert none is None and torch.equal(only, dx)
+
+
+# ------------------------------------------------------------------ few tokens and weights of more rows than a block of them an SM
+@gpu
+@pytest.mark.parametrize("T,K,N,xt,pad,shift", [
+    (1, 300, 2432, BF16, 0, 0), (1, 4500, 2433, BF16, 0, 0), (3, 257, 8000, F32, 3, 1), (8, 5000, 2600, BF16, 3, 1),
+    (9, 700, 2600, BF16, 0, 0), (16, 1000, 5003, BF16, 8, 0), (16, 1, 4100, F32, 0, 0), (13, 2400, 2500, F32, 0, 0)])
+def test_linear_of_few_tokens(T, K, N, xt, pad, shift):
+    g = gen(T + K + N)
+    x = rows(activation(g, T, K).to(xt), pad, shift)
+    w = weight(g, N, K)
+    lin = M.MoEFp8Linear(K, N)
+    W, X = values(w, SQUARE), values(ref_codes(x, ROW), ROW)
+    ref, tol = X @ W.t(), sum_tol(X.abs() @ W.abs().t(), K)
+    for yt in (F32, BF16):
+        y, none = lin.forward(x, w, keep=False, out_dtype=yt)
+        assert none is None
+        close(y, ref, tol, f"y {yt}")
+        assert torch.equal(lin.forward(x, w, out_dtype=yt)[0], y)
+    if T > 1:                       # a token's result does not depend on the others'
+        assert torch.equal(lin.forward(x[1:2], w, keep=False, out_dtype=F32)[0], lin.forward(x, w, keep=False, out_dtype=F32)[0][1:2])
+
+
+@gpu
+@pytest.mark.parametrize("T,H,I,L", [(1, 2500, 1300, 0.0), (1, 4500, 1217, 2.0), (4, 300, 2600, 1.0), (9, 260, 1300, 0.0), (16, 700, 1500, 2.0)])
+def test_feed_forward_of_few_tokens(T, H, I, L):
+    gn = gen(T + H + I)
+    x = activation(gn, T, H).bfloat16()
+    w = [weight(gn, I, H), weight(gn, I, H), weight(gn, H, I)]
+    y, none = M.MoEFeedForward(H, I, swiglu_limit=L).forward(x, M.FeedForwardWeights(*w), keep=False)
+    assert none is None
+    ref, tol = ffn_forward_ref(x, *(values(v, SQUARE) for v in w), L)[:2]
+    close(y, ref, tol, "y")
 
 
 # ------------------------------------------------------------------ the calls that a program makes of them
