@@ -3,6 +3,8 @@
 
 #include "device_common.cuh"
 
+#include <type_traits>
+
 namespace moe {
 
 // Scale of a block whose largest magnitude is `most`: E4M3's largest value, 448, stands for it; at least the smallest
@@ -41,16 +43,49 @@ __device__ __forceinline__ uint64_t mad2(uint64_t a, uint64_t b, uint64_t c) {
     return p;
 }
 
-// out[at] = x, or out[at] + x; bf16: both the addend and the sum are rounded, as the layer's main_grads
-__device__ __forceinline__ void store_one(void* out, int64_t at, bool bf16, bool add, float x) {
-    if (bf16) {
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out) + at;
-        const __nv_bfloat16 w = __float2bfloat16(x);
-        *dst = add ? __float2bfloat16(__bfloat162float(*dst) + __bfloat162float(w)) : w;
-    } else {
-        float* dst = static_cast<float*>(out) + at;
-        *dst = add ? *dst + x : x;
+// Results and what they are added to. In bf16 both the addend and the sum are rounded, as the layer's main_grads.
+template <typename Y>
+using Two = std::conditional_t<sizeof(Y) == 2, uint32_t, float2>;  // two adjacent ones, the first on the pair's alignment
+__device__ __forceinline__ float load_one(const float* p) { return *p; }
+__device__ __forceinline__ float load_one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float2 load_two(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ uint32_t load_two(const __nv_bfloat16* p) { return *reinterpret_cast<const uint32_t*>(p); }
+__device__ __forceinline__ float2 load_first(const float* p) { return make_float2(*p, 0.0f); }
+__device__ __forceinline__ uint32_t load_first(const __nv_bfloat16* p) { return __bfloat16_as_ushort(*p); }
+__device__ __forceinline__ float first_of(float2 x) { return x.x; }
+__device__ __forceinline__ float first_of(uint32_t x) { return __uint_as_float(x << 16); }
+template <bool ADD>  // *p = x, or old + x
+__device__ __forceinline__ void save_one(float* p, float x, float old) { *p = ADD ? old + x : x; }
+template <bool ADD>
+__device__ __forceinline__ void save_one(__nv_bfloat16* p, float x, float old) {
+    const __nv_bfloat16 w = __float2bfloat16(x);
+    *p = ADD ? __float2bfloat16(old + __bfloat162float(w)) : w;
+}
+template <bool ADD>
+__device__ __forceinline__ void save_two(float* p, float x, float y, float2 old) {
+    *reinterpret_cast<float2*>(p) = ADD ? make_float2(old.x + x, old.y + y) : make_float2(x, y);
+}
+template <bool ADD>
+__device__ __forceinline__ void save_two(__nv_bfloat16* p, float x, float y, uint32_t old) {
+    uint32_t w = pack_bf16x2(x, y);
+    if (ADD) {
+        float a, b, c, d;
+        unpack_bf16x2(old, a, b), unpack_bf16x2(w, c, d);
+        w = pack_bf16x2(a + c, b + d);
     }
+    *reinterpret_cast<uint32_t*>(p) = w;
+}
+__device__ __forceinline__ void store_one(void* out, int64_t at, bool bf16, bool add, float x) {
+    auto put = [&](auto* p) {
+        if (add)
+            save_one<true>(p, x, load_one(p));
+        else
+            save_one<false>(p, x, 0.0f);
+    };
+    if (bf16)
+        put(static_cast<__nv_bfloat16*>(out) + at);
+    else
+        put(static_cast<float*>(out) + at);
 }
 
 }  // namespace moe
