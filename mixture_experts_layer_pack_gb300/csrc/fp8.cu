@@ -595,14 +595,14 @@ struct Plan {
 };
 
 // The cut with the least time, by what was measured of each (us): a round of tiles takes a start and an end (128 x 128 tiles 4, 128 x 256
-// 5.5, pairs 6, the gate's results 3 more; twice that where a row's results cannot be written by whole sectors) and its blocks along K, a chain
+// 5.5, pairs 6, the gate's results 3 more) and its blocks along K, a chain
 // of copy, product, read and release that is nearly as long for a small tile as for a large one, and longer the more SMs
 // work (128 columns 0.3 to 0.55 a block, 256 0.45 to 0.6, a pair's 0.42 to 0.5; a weight's gradient 0.35 more). K in parts fills the SMs of a few
 // tiles and shortens the chain, for a launch that sums the parts (2.7) and their way through memory. E.g. 512 x 1024, K 4096: 14.9
 // whole, 10.4 in four parts, pairs 18.5; 6788 x 324, K 2900: pairs 18.8, 128 x 128 23.9. It goes by the sizes alone, as the workspace's size does.
 Plan plan(int op, const F8Args& a) {
     const int sms = sm_count();
-    const bool gated = op == F8_GU, slow = (op == F8_NT || op == F8_NN) && a.o[0].N % 16 != 0;
+    const bool gated = op == F8_GU;
     double elements = 0;
     int64_t small = 0, wide = 0, pairs = 0;  // tiles
     for (int p = 0; p < a.products; ++p) {
@@ -619,7 +619,7 @@ Plan plan(int op, const F8Args& a) {
         const int64_t items = (cg == 2 ? pairs : bn == 256 ? wide : small) * splits;
         const double busy = items < units ? double(items) / units : 1.0;
         const double chain = (bn == 128 ? 0.3 + 0.25 * busy : cg == 2 ? 0.42 + 0.08 * busy : 0.45 + 0.15 * busy) + (op == F8_TN ? 0.35 : 0.0);
-        const double ends = (bn == 128 ? 4.0 : (cg == 2 ? 6.0 : 5.5) * (slow && splits == 1 ? 2.0 : 1.0)) + (gated && splits == 1 ? 3.0 : 0.0);
+        const double ends = (bn == 128 ? 4.0 : cg == 2 ? 6.0 : 5.5) + (gated && splits == 1 ? 3.0 : 0.0);
         double us = double((items + units - 1) / units) * (ends + chain * ((a.k_blocks + splits - 1) / splits));
         if (splits > 1) us += 2.7 + (gated ? 1.5 : 0.0) + elements * (gated ? 2 : 1) * splits * 0.8e-6;
         if (us < least) least = us, best = {bn, cg, splits};

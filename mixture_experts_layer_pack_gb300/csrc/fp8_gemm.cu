@@ -31,7 +31,6 @@ constexpr int kF8Threads = 128 + 32 * kF8EpiWarps;
 // two sets of 16 sums, so the first warpgroup (loads and products) gives up what the two others take: 56 + 2 * 224 = 3 * 168.
 constexpr int kFewRegs = 56, kManyRegs = 224;
 constexpr uint32_t kTileBytes = 128 * 128;   // 128 rows of 128 codes
-constexpr uint32_t kStageFloats = 32 * 16;   // an epilogue warp's staging: 32 rows x 16 columns
 
 template <int OP, int BN, int CG>
 struct F8Cfg {
@@ -40,8 +39,7 @@ struct F8Cfg {
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = int(196608 / STAGE_BYTES);
     static constexpr int BUFS = 512 / BN;
-    static constexpr size_t SMEM = size_t(STAGES) * STAGE_BYTES + kF8EpiWarps * kStageFloats * 4 +
-                                   (OP == F8_GU ? 3 * 2 * 128 * 4 : 0) + 1024 + 512;
+    static constexpr size_t SMEM = size_t(STAGES) * STAGE_BYTES + (OP == F8_GU ? 3 * 2 * 128 * 4 : 0) + 1024 + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -242,20 +240,11 @@ __device__ __forceinline__ Item f8_item(int i, const F8Args& a, uint32_t rank) {
 }
 
 // ---------------------------------------------------------------- results
-// 16 columns of a warp's 32 rows through its staging: written a row a lane, read as pieces of rows (16-byte unit j of row r
-// lies at j ^ (r / 2 % 4): no bank conflict either way)
-__device__ __forceinline__ void put16(float* staging, const float* v) {
-    const int lane = threadIdx.x & 31;
-    float4* row = reinterpret_cast<float4*>(staging + lane * 16);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) row[j ^ ((lane >> 1) & 3)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-}
-
 // Where a product's results go
 struct Sink {
     void* out;
     int64_t ld;
-    bool bf16, add, wide;  // wide: four adjacent results can be written at once
+    bool bf16, add;
 };
 __device__ __forceinline__ Sink f8_sink(const F8Args& a, const Item& t, int part = 0, int parts = 1) {
     const F8Out& o = a.o[t.p];
@@ -265,41 +254,7 @@ __device__ __forceinline__ Sink f8_sink(const F8Args& a, const Item& t, int part
     s.ld = split ? o.ld_partial : o.ld;
     s.bf16 = !split && o.bf16;
     s.add = !split && o.accumulate;
-    s.wide = ((reinterpret_cast<uintptr_t>(s.out) | uintptr_t(s.ld) * (s.bf16 ? 2 : 4)) & (s.bf16 ? 7 : 15)) == 0;
     return s;
-}
-
-// The 16 columns in `staging` of rows row0 .. + 31. (The loop around it is not unrolled: a tile's results are written once, by
-// instructions that are then fetched for the first time, and that took several times the writing.)
-__device__ __forceinline__ void f8_store16(const F8Out& o, const Sink& s, int row0, int col0, const float* staging) {
-    const int lane = threadIdx.x & 31;
-    if (s.wide && col0 + 16 <= o.N) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + (lane >> 2), j = lane & 3;
-            const float4 x = reinterpret_cast<const float4*>(staging + r * 16)[j ^ ((r >> 1) & 3)];
-            const int64_t at = int64_t(row0 + r) * s.ld + col0 + 4 * j;
-            if (row0 + r >= o.M) continue;
-            if (s.bf16)
-                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(s.out) + at) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-            else
-                *reinterpret_cast<float4*>(static_cast<float*>(s.out) + at) = x;
-        }
-    } else {
-        const int c = lane & 15;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int r = i * 2 + (lane >> 4);
-            const float x = staging[r * 16 + 4 * ((c >> 2) ^ ((r >> 1) & 3)) + (c & 3)];
-            const int64_t at = int64_t(row0 + r) * s.ld + col0 + c;
-            if (row0 + r >= o.M || col0 + c >= o.N) continue;
-            if (s.bf16)
-                static_cast<__nv_bfloat16*>(s.out)[at] = __float2bfloat16(x);
-            else
-                static_cast<float*>(s.out)[at] = x;
-        }
-    }
-    __syncwarp();
 }
 
 // 32 bytes, a whole sector, at once
@@ -331,6 +286,67 @@ __device__ __forceinline__ void row_store(const F8Out& o, const Sink& s, int row
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * c + j]);
             store32(dst + 8 * c, w);
+        }
+    }
+}
+
+// The same, `left` of the columns the matrix's, of a row that starts anywhere: the words move up by the row's offset in its first piece
+// of 32 bytes (bf16: 16, fewer results are single ones then), in steps of selections, and go out by whole pieces but for the ends. (Through shared memory, 16
+// columns at a time: 8192 x 2048 to 2050 81 us, so 53.)
+template <int N, typename Y>
+__device__ __forceinline__ void row_ragged(Y* to, int left, const float* v) {
+    constexpr int BYTES = sizeof(Y) == 4 ? 32 : 16;
+    constexpr int W = BYTES / 4, PER = BYTES / int(sizeof(Y)), WORDS = N * int(sizeof(Y)) / 4;  // words and results of a piece
+    const int o = int(reinterpret_cast<uintptr_t>(to) & (BYTES - 1)) / int(sizeof(Y));
+    to -= o;
+    const int end = min(left, N) + o;  // results [o, end) from there
+    const int s = sizeof(Y) == 2 ? o >> 1 : o;
+    auto word = [&](int i) -> uint32_t {
+        if (i >= WORDS) return 0u;
+        if constexpr (sizeof(Y) == 4)
+            return __float_as_uint(v[i]);
+        else
+            return pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    };
+    uint32_t last[W], before = 0;
+#pragma unroll
+    for (int j = 0; j < W; ++j) last[j] = 0;
+#pragma unroll
+    for (int k = 0; k <= N / PER; ++k) {
+        uint32_t w[2 * W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            w[j] = last[j];
+            uint32_t x = word(W * k + j);
+            if constexpr (sizeof(Y) == 2) {
+                const uint32_t y = x;
+                x = o & 1 ? __funnelshift_l(before, x, 16) : x;
+                before = y;
+            }
+            last[j] = w[W + j] = x;
+        }
+#pragma unroll
+        for (int bit = W / 2; bit >= 1; bit /= 2)
+#pragma unroll
+            for (int j = 2 * W - 1; j >= W - bit + 1; --j) w[j] = s & bit ? w[j - bit] : w[j];
+        const int from = k == 0 ? o : 0, to_end = end - k * PER;  // of this piece
+        Y* p = to + k * PER;
+        if (from == 0 && to_end >= PER) {
+            if constexpr (W == 8) {
+                const uint32_t x[8] = {w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]};
+                store32(p, x);
+            } else {
+                *reinterpret_cast<uint4*>(p) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (j >= from && j < to_end) {
+                    if constexpr (sizeof(Y) == 4)
+                        p[j] = __uint_as_float(w[W + j]);
+                    else
+                        reinterpret_cast<unsigned short*>(p)[j] = static_cast<unsigned short>(w[W + (j >> 1)] >> (16 * (j & 1)));
+                }
         }
     }
 }
@@ -575,8 +591,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
 
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    float* staging = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES);
-    float* most = staging + kF8EpiWarps * kStageFloats;  // F8_GU: [3][2][128]
+    float* most = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES);  // F8_GU: [3][2][128]
     uint64_t* full = reinterpret_cast<uint64_t*>(most + (OP == F8_GU ? 3 * 256 : 0));
     uint64_t* empty = full + C::STAGES;
     uint64_t* tfull = empty + C::STAGES;
@@ -697,13 +712,13 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
         // ---------------- sums over the blocks, and results
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         const int q = warp & 3, half = (warp - 4) >> 2;
-        float* my_staging = staging + (warp - 4) * kStageFloats;
         const uint32_t lanes = tmem + (uint32_t(q * 32) << 16);
         int buf = 0;
         uint32_t bphase = 0;
         bool ok = true;
         const uint32_t given = CG == 1 ? smem_u32(tempty) : in_leader(tempty);
         for (int i = first; i < items; i += step) {
+            __syncwarp();
             const Item t = f8_item<OP, BN, CG>(i, a, rank);
             uint64_t acc[HALF / 2];
 #pragma unroll
@@ -789,15 +804,13 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
                 row_store<HALF>(o, sink, t.m0 + q * 32 + lane, t.n0 + HALF * half, sum);
                 continue;
             }
-#pragma unroll 1
-            for (int c = 0; c < HALF / 16; ++c) {
-                const int col = t.n0 + HALF * half + 16 * c;
-                if (col >= o.N) break;
-#pragma unroll
-                for (int z = 0; z < HALF / 16; ++z)
-                    if (z == c) put16(my_staging, sum + 16 * z);
-                __syncwarp();
-                f8_store16(o, sink, t.m0 + q * 32, col, my_staging);
+            const int col = t.n0 + HALF * half;
+            if (t.m0 + q * 32 + lane < o.M && col < o.N) {
+                const int64_t at = int64_t(row) * sink.ld + col;
+                if (sink.bf16)
+                    row_ragged<HALF>(static_cast<__nv_bfloat16*>(sink.out) + at, o.N - col, sum);
+                else
+                    row_ragged<HALF>(static_cast<float*>(sink.out) + at, o.N - col, sum);
             }
         }
         __syncwarp();
