@@ -599,7 +599,8 @@ struct Plan {
 // of copy, product, read and release that is nearly as long for a small tile as for a large one, and longer the more SMs
 // work (128 columns 0.3 to 0.55 a block, 256 0.45 to 0.6, a pair's 0.42 to 0.5; a weight's gradient 0.35 more). K in parts fills the SMs of a few
 // tiles and shortens the chain, for a launch that sums the parts (2.7) and their way through memory. E.g. 512 x 1024, K 4096: 14.9
-// whole, 10.4 in four parts, pairs 18.5; 6788 x 324, K 2900: pairs 18.8, 128 x 128 23.9. It goes by the sizes alone, as the workspace's size does.
+// whole, 10.4 in four parts, pairs 18.5; 6788 x 324, K 2900: pairs 18.8, 128 x 128 23.9; three gradients of 1450 x 324, K 6788: 128 x 128 whole
+// 72, 128 x 256 in two parts 58. It goes by the sizes alone, as the workspace's size does.
 Plan plan(int op, const F8Args& a) {
     const int sms = sm_count();
     const bool gated = op == F8_GU;
@@ -627,7 +628,7 @@ Plan plan(int op, const F8Args& a) {
     look(256, 2, 1);
     for (const int splits : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16}) {
         if (splits > a.k_blocks || (splits > 1 && wide > sms)) break;
-        if (gated || splits == 1) look(256, 1, splits);
+        if (gated || op == F8_TN || splits == 1) look(256, 1, splits);
         if (!gated) look(128, 1, splits);
     }
     return best;
