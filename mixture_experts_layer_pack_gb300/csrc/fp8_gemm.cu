@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(256) f8_reduce_kernel(const __grid_constant__ 
         const int64_t m = i / quads;
         const int n = int(i - m * quads) * 4;
         float4 sum = make_float4(0, 0, 0, 0);
-        const float* src = o.partial + m * o.ld_partial + n; 
+        const float* src = o.partial + m * o.ld_partial + n;
         for (int s = 0; s < a.splits; ++s) {
             const float4 x = __ldcs(reinterpret_cast<const float4*>(src + s * plane));
             sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);

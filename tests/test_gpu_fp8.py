@@ -333,6 +333,9 @@ LINEAR = [
     (2500, 700, 2050, BF16, BF16, 0, 0),
     (2305, 2304, 2300, F32, F32, 0, 0),
     (5000, 130, 1300, BF16, BF16, 0, 0),
+    (40, 4099, 2100, BF16, BF16, 3, 1),
+    (2400, 200, 4099, BF16, BF16, 3, 1),
+    (2400, 257, 4099, F32, F32, 1, 1),
 ]
 
 
