@@ -30,6 +30,34 @@ import dataclasses
 from . import binding as B
 
 
+class _Kept:
+    """What a forward keeps for its backward. The tensors are of the stream that forward ran on, and the block alone holds them: once it
+    lets them go, that stream's next tensors get their memory."""
+
+    def __init__(self, params, s, *rest):
+        self.params, self.tensors = params, (s, *rest)
+        self.index = s.get_device()
+        self.stream = B._current_stream_of()(self.index)
+
+    def read(self):
+        """(params, *tensors), before a backward's first kernel: the allocator waits for the current stream too, where that is not
+        forward's."""
+        if B._current_stream_of()(self.index) != self.stream:
+            import torch
+            current = torch.cuda.current_stream(self.index)
+            for t in _each_tensor(self.tensors):
+                t.record_stream(current)
+        return (self.params, *self.tensors)
+
+
+def _each_tensor(kept):
+    for t in kept:
+        if isinstance(t, tuple):
+            yield from _each_tensor(t)
+        elif t is not None:
+            yield t
+
+
 @dataclasses.dataclass
 class BlockParams:
     """Parameters of a block: norm_weight and norm_bias [H] (norm_bias may be None), router_weight [E,H]
@@ -185,7 +213,7 @@ class DenseBlock:
         """(out [T,H] bf16, s [T,H] in x's type) of x and residual [T,H], bf16 or fp32; on the current stream."""
         y, s, mean, rstd = self._normed(x, residual, params)
         out, kept = self.ffn.forward(y, params.weights)
-        self._kept = (params, s, mean, rstd, kept)
+        self._kept = _Kept(params, s, mean, rstd, kept)
         return out, s
 
     def backward(self, dout, ds=None, grads=None, accumulate=False):
@@ -194,7 +222,7 @@ class DenseBlock:
         buffers, as MoEFeedForward.backward's."""
         if self._kept is None:
             raise ValueError("backward without a forward before it")
-        p, s, mean, rstd, kept = self._kept
+        p, s, mean, rstd, kept = self._kept.read()
         if dout.shape != s.shape or dout.device != s.device:
             raise ValueError("dout must be [T, H] bf16 on the block's device")
         if ds is not None:  # looked at before anything is added to grads

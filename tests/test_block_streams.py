@@ -1,0 +1,148 @@
+"""What a block's forward keeps is its backward's, whatever stream that runs on.
+
+The kept tensors are of the stream that forward ran on, and the block alone holds them. The allocator gives a tensor's memory to the next one of
+its stream as soon as it is let go, so a backward on another stream has to tell it of its reads (``record_stream``) before it lets them go.
+The first tests look at that on the CPU, with tensors that note what is said of them; the GPU ones look at the gradients.
+"""
+import pytest
+import torch
+
+import mixture_experts_layer_pack_gb300 as M
+from mixture_experts_layer_pack_gb300 import binding as B
+
+gpu = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+# ------------------------------------------------------------------ on the CPU: streams by name, operators that only pass tensors on
+class Noted(torch.Tensor):
+    """A tensor that notes the streams that it is recorded on."""
+
+    @classmethod
+    def new(cls, *shape, dtype=BF16):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(cls)
+
+    @property
+    def told(self):
+        return self.__dict__.setdefault("streams", [])
+
+    def record_stream(self, stream):
+        self.told.append(stream)
+
+    def get_device(self):
+        return 0
+
+
+class Streams:
+    """The current stream, as the blocks ask for it."""
+
+    def __init__(self, monkeypatch):
+        self.now, self.capturing = "A", False
+        monkeypatch.setattr(B, "_current_stream_of", lambda: lambda index: self.now)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.now)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.capturing)
+        B._fp8_of_torch.cache_clear()
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    yield Streams(monkeypatch)
+    monkeypatch.undo()
+    B._fp8_of_torch.cache_clear()
+
+
+T, H, I = 4, 8, 16
+
+
+class Norm:
+    def forward(self, x, weight, bias, residual=None, out_dtype=None):
+        self.made = [Noted.new(T, H), Noted.new(T, H), Noted.new(T, dtype=F32), Noted.new(T, dtype=F32)]
+        return tuple(self.made)
+
+    def backward(self, dy, s, weight, mean, rstd, dsum=None, bias=False):
+        self.seen = [list(t.told) for t in (s, mean, rstd)]
+        return Noted.new(T, H), Noted.new(H), None
+
+
+class FeedForward:
+    def forward(self, y, weights):
+        pair = [(Noted.new(T, n), Noted.new(T, dtype=F32)) for n in (H, I, I)]
+        self.made = [t for p in pair for t in p]
+        return Noted.new(T, H), tuple(pair)
+
+    def backward(self, dout, weights, kept, grads=None, accumulate=False):
+        self.seen = [list(t.told) for p in kept for t in p]
+        return Noted.new(T, H), (None, None, None)
+
+
+def dense_block():
+    block = M.DenseBlock(64, 64, device="cpu")
+    block.norm, block.ffn = Norm(), FeedForward()
+    return block, M.DenseParams(Noted.new(H), None)
+
+
+def backward(block, d):
+    return block.backward(d)
+
+
+@pytest.mark.parametrize("make", [dense_block])
+def test_a_backward_on_another_stream_is_told_to_the_allocator(make, streams):
+    block, params = make()
+    block.forward(Noted.new(T, H), params)
+    streams.now = "B"
+    backward(block, torch.zeros(T, H, dtype=BF16))
+    parts = [block.norm, block.ffn]
+    for part in parts:
+        assert part.seen and all(told == ["B"] for told in part.seen), "before the first of its reads"
+    made = [t for part in parts for t in part.made][1:]      # y itself is not kept
+    assert all(t.told == ["B"] for t in made)
+
+
+@pytest.mark.parametrize("make", [dense_block])
+def test_a_backward_on_the_same_stream_tells_nothing(make, streams):
+    block, params = make()
+    block.forward(Noted.new(T, H), params)
+    backward(block, torch.zeros(T, H, dtype=BF16))
+    for part in (block.norm, block.ffn):
+        assert all(t.told == [] for t in part.made)
+
+
+# ------------------------------------------------------------------ on the GPU
+def randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def dense(T, H, I, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = [M.fp8_quantize((randn(g, *n) * 0.05).bfloat16(), M.MOE_B_SQUARE) for n in ((I, H), (I, H), (H, I))]
+    p = M.DenseParams(1 + 0.1 * randn(g, H), M.FeedForwardWeights(*w), 0.1 * randn(g, H))
+    steps = [(randn(g, T, H).bfloat16(), randn(g, T, H).bfloat16(), randn(g, T, H).bfloat16()) for _ in range(2)]
+    return M.DenseBlock(H, I, norm=B.MOE_NORM_LAYER), p, steps
+
+
+def dense_step(block, p, x, res, dout):
+    out, s = block.forward(x, p, residual=res)
+    dx, grads = block.backward(dout)
+    return [out, s, dx, *grads.values()]
+
+
+@gpu
+def test_a_dense_backward_on_another_stream_beside_the_next_forward():
+    block, p, steps = dense(600, 520, 1100)
+    want = [dense_step(block, p, *step) for step in steps]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        (x, res, dout), (x2, res2, dout2) = steps
+        with torch.cuda.stream(a):
+            out, s = block.forward(x, p, residual=res)
+        b.wait_stream(a)
+        with torch.cuda.stream(b):
+            torch.cuda._sleep(200_000_000)          # some 0.1 s: the backward's kernels wait behind it
+            dx, grads = block.backward(dout)
+        with torch.cuda.stream(a):                  # at once, of the same sizes
+            out2, s2 = block.forward(x2, p, residual=res2)
+            dx2, grads2 = block.backward(dout2)
+        torch.cuda.synchronize()
+        for got, ref in zip(([out, s, dx, *grads.values()], [out2, s2, dx2, *grads2.values()]), want):
+            assert all(torch.equal(g, r) for g, r in zip(got, ref))
