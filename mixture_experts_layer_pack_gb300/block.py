@@ -30,24 +30,24 @@ import dataclasses
 from . import binding as B
 
 
-class _Kept:
-    """What a forward keeps for its backward. The tensors are of the stream that forward ran on, and the block alone holds them: once it
-    lets them go, that stream's next tensors get their memory."""
+class _Kept(tuple):
+    """(params, *tensors) that a forward keeps for its backward. The tensors are of the stream that forward ran on, and the block alone holds
+    them: once it lets them go, that stream's next tensors get their memory."""
 
-    def __init__(self, params, s, *rest):
-        self.params, self.tensors = params, (s, *rest)
-        self.index = s.get_device()
-        self.stream = B._current_stream_of()(self.index)
+    def __new__(cls, params, *tensors):
+        kept = super().__new__(cls, (params, *tensors))
+        kept.index = tensors[0].get_device()
+        kept.stream = B._current_stream_of()(kept.index)
+        return kept
 
     def read(self):
-        """(params, *tensors), before a backward's first kernel: the allocator waits for the current stream too, where that is not
-        forward's."""
+        """Itself, before a backward's first kernel: the allocator waits for the current stream too, where that is not forward's."""
         if B._current_stream_of()(self.index) != self.stream:
             import torch
             current = torch.cuda.current_stream(self.index)
-            for t in _each_tensor(self.tensors):
+            for t in _each_tensor(self[1:]):
                 t.record_stream(current)
-        return (self.params, *self.tensors)
+        return self
 
 
 def _each_tensor(kept):
@@ -133,7 +133,7 @@ class MoEBlock:
             raise ValueError("the block was made for decoding only (max_tokens 0)")
         y, s, mean, rstd, logits, (ids, probs, counts, losses) = self._routed(x, residual, params)
         out = self._on_layer(params, self.layer.forward_topk, y, ids, probs, params.weights)
-        self._kept = (params, y, s, mean, rstd, logits, ids, counts)
+        self._kept = _Kept(params, y, s, mean, rstd, logits, ids, counts)
         return out, s, losses
 
     def backward(self, dout, main_grads: B.moe_main_grads, ds=None, loss_grad=1.0):
@@ -144,7 +144,7 @@ class MoEBlock:
         import torch
         if self._kept is None:
             raise ValueError("backward without a forward before it")
-        p, y, s, mean, rstd, logits, ids, counts = self._kept
+        p, y, s, mean, rstd, logits, ids, counts = self._kept.read()
         if dout.shape != y.shape or dout.dtype != y.dtype or dout.device != y.device:
             raise ValueError("dout must be [T, H] bf16 on the block's device")
         if ds is not None:  # looked at before anything is added to main_grads

@@ -51,7 +51,7 @@ def streams(monkeypatch):
     B._fp8_of_torch.cache_clear()
 
 
-T, H, I = 4, 8, 16
+T, H, I, E, K = 4, 8, 16, 3, 2
 
 
 class Norm:
@@ -81,29 +81,58 @@ def dense_block():
     return block, M.DenseParams(Noted.new(H), None)
 
 
+class Router:
+    def forward(self, logits, select_bias=None):
+        self.made = [Noted.new(T, K, dtype=torch.int32), Noted.new(E, dtype=torch.int32)]
+        return self.made[0], Noted.new(T, K, dtype=F32), self.made[1], None
+
+    def backward(self, logits, ids, dprobs, counts=None, loss_grad=1.0):
+        self.seen = [list(t.told) for t in (logits, ids, counts)]
+        return torch.zeros(T, E, dtype=BF16)
+
+
+class Layer:
+    prepared = None
+
+    def forward_topk(self, y, ids, probs, weights):
+        return Noted.new(T, H)
+
+    def backward(self, dout, main_grads):
+        return torch.zeros(T, H, dtype=BF16), torch.zeros(T, K)
+
+
+def expert_block():
+    block = M.MoEBlock.__new__(M.MoEBlock)      # (its constructor allocates on a GPU)
+    block.norm, block.router, block.layer, block.decoder, block.decode_tokens = Norm(), Router(), Layer(), None, 0
+    block._mx, block._kept, block._captured = False, None, None
+    return block, M.BlockParams(Noted.new(H), torch.zeros(E, H, dtype=BF16), B.moe_weights())
+
+
 def backward(block, d):
-    return block.backward(d)
+    return block.backward(d, None) if isinstance(block, M.MoEBlock) else block.backward(d)
 
 
-@pytest.mark.parametrize("make", [dense_block])
+@pytest.mark.parametrize("make", [dense_block, expert_block])
 def test_a_backward_on_another_stream_is_told_to_the_allocator(make, streams):
     block, params = make()
     block.forward(Noted.new(T, H), params)
     streams.now = "B"
     backward(block, torch.zeros(T, H, dtype=BF16))
-    parts = [block.norm, block.ffn]
+    parts = [block.norm, block.ffn if make is dense_block else block.router]
     for part in parts:
         assert part.seen and all(told == ["B"] for told in part.seen), "before the first of its reads"
-    made = [t for part in parts for t in part.made][1:]      # y itself is not kept
+    made = [t for part in parts for t in part.made]
+    if make is dense_block:
+        made = made[1:]                # y itself is not kept
     assert all(t.told == ["B"] for t in made)
 
 
-@pytest.mark.parametrize("make", [dense_block])
+@pytest.mark.parametrize("make", [dense_block, expert_block])
 def test_a_backward_on_the_same_stream_tells_nothing(make, streams):
     block, params = make()
     block.forward(Noted.new(T, H), params)
     backward(block, torch.zeros(T, H, dtype=BF16))
-    for part in (block.norm, block.ffn):
+    for part in (block.norm, block.ffn if make is dense_block else block.router):
         assert all(t.told == [] for t in part.made)
 
 
@@ -146,3 +175,42 @@ def test_a_dense_backward_on_another_stream_beside_the_next_forward():
         torch.cuda.synchronize()
         for got, ref in zip(([out, s, dx, *grads.values()], [out2, s2, dx2, *grads2.values()]), want):
             assert all(torch.equal(g, r) for g, r in zip(got, ref))
+
+
+@gpu
+def test_an_expert_backward_on_another_stream_beside_new_tensors():
+    """The layer's steps are ordered, so that the first stream's next work is tensors of the sizes that the block kept. The library products in the
+    block (logits, dy, the router's gradient) may be split otherwise on another stream: results whose bf16 rounding may go the other way, 2^-8 of an
+    element each, doubled by the norm's projection at most: 2^-6 for all of them."""
+    T, H, I, E, k = 300, 256, 128, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w = [(randn(g, *n) * 0.06).bfloat16() for n in ((2 * I, H), (H, I), (E, 2 * I, H), (E, H, I))]
+    p = M.BlockParams(1 + 0.1 * randn(g, H), (randn(g, E, H) * 0.1).bfloat16(), M.weights_from_combined(*w))
+    block = M.MoEBlock(T, H, E, k, I, aux_coeff=0.01)
+    x, res, dout = (randn(g, T, H).bfloat16() for _ in range(3))
+
+    def gradients(before=lambda: None):
+        mg = [torch.zeros_like(t, dtype=F32) for t in w]
+        before()
+        dx, grads = block.backward(dout, M.main_grads_from_combined(*mg))
+        return [dx, grads["norm_weight"], grads["router_weight"], *mg]
+
+    block.forward(x, p, residual=res)
+    want = gradients()
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(a):
+            block.forward(x, p, residual=res)
+        b.wait_stream(a)
+        with torch.cuda.stream(b):
+            got = gradients(lambda: torch.cuda._sleep(200_000_000))
+        with torch.cuda.stream(a):
+            junk = [torch.full(n, float("nan"), dtype=t, device="cuda") for _ in range(6)
+                    for n, t in (((T, H), BF16), ((T, E), BF16), ((T,), F32))]
+            junk += [torch.full((T, k), E - 1, dtype=torch.int32, device="cuda") for _ in range(6)]
+        torch.cuda.synchronize()
+        for t, ref in zip(got, want):
+            assert (t.double() - ref.double()).norm() <= 2.0 ** -6 * ref.double().norm()
+        del junk
+    block.close()
