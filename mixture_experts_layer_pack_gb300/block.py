@@ -18,7 +18,8 @@ it holds for one set of weights: ``prepare`` converts them, before the first
 forward with a set and after every change of its scales. The decoder reads the
 weights as they are.
 
-Steps may be captured into CUDA graphs. The decoder's replays keep the expert
+Steps may be captured into CUDA graphs (a backward without its forward: the block
+then holds what that kept as long as it lives). The decoder's replays keep the expert
 tables that were captured with them, whatever else it decodes; the layer has one
 set of tables, so a block that had a step through it captured takes no other
 weights there.
@@ -38,16 +39,25 @@ class _Kept(tuple):
         kept = super().__new__(cls, (params, *tensors))
         kept.index = tensors[0].get_device()
         kept.stream = B._current_stream_of()(kept.index)
+        kept.captured = _capturing()
         return kept
 
-    def read(self):
-        """Itself, before a backward's first kernel: the allocator waits for the current stream too, where that is not forward's."""
+    def read(self, held):
+        """Itself, before a backward's first kernel: the allocator waits for the current stream too, where that is not forward's. A graph that has the
+        backward without its forward reads at every replay what an eager forward kept: it goes into `held`, the block's."""
+        if not self.captured and _capturing():
+            held.append(self)
         if B._current_stream_of()(self.index) != self.stream:
             import torch
             current = torch.cuda.current_stream(self.index)
             for t in _each_tensor(self[1:]):
                 t.record_stream(current)
         return self
+
+
+def _capturing():
+    import torch
+    return torch.cuda.is_current_stream_capturing()
 
 
 def _each_tensor(kept):
@@ -94,6 +104,7 @@ class MoEBlock:
         self.decode_tokens = decode_tokens
         self._mx = routed_wtype == B.MOE_W_MXFP8
         self._kept = self._captured = None
+        self._held = []                 # what captured backward passes read
 
     def prepare(self, params: BlockParams):
         """Converts the scales of params' MXFP8 experts for the layer (nothing to do for BF16 ones, or for a block that
@@ -144,7 +155,7 @@ class MoEBlock:
         import torch
         if self._kept is None:
             raise ValueError("backward without a forward before it")
-        p, y, s, mean, rstd, logits, ids, counts = self._kept.read()
+        p, y, s, mean, rstd, logits, ids, counts = self._kept.read(self._held)
         if dout.shape != y.shape or dout.dtype != y.dtype or dout.device != y.device:
             raise ValueError("dout must be [T, H] bf16 on the block's device")
         if ds is not None:  # looked at before anything is added to main_grads
@@ -198,12 +209,14 @@ class DenseBlock:
 
     ``forward`` keeps y, g and u in 8 bits for ``backward`` (``kept``: 3 bytes in place of 6 bf16 ones at the network's two
     widths), ``decode`` keeps nothing. (out, s) are the next block's x and residual, as MoEBlock's. Every step may be captured into CUDA
-    graphs. One forward at a time waits for its backward."""
+    graphs; what an eager forward kept for a backward that is captured by itself stays as long as the block. One forward at a time
+    waits for its backward."""
 
     def __init__(self, hidden, inter, device="cuda", norm=B.MOE_NORM_RMS, eps=1e-6, swiglu_limit=0.0):
         self.norm = B.MoENorm(hidden, eps, norm, device=device)
         self.ffn = B.MoEFeedForward(hidden, inter, swiglu_limit, device=device)
         self._kept = None
+        self._held = []                 # what captured backward passes read
 
     def _normed(self, x, residual, p):
         import torch
@@ -222,7 +235,7 @@ class DenseBlock:
         buffers, as MoEFeedForward.backward's."""
         if self._kept is None:
             raise ValueError("backward without a forward before it")
-        p, s, mean, rstd, kept = self._kept.read()
+        p, s, mean, rstd, kept = self._kept.read(self._held)
         if dout.shape != s.shape or dout.device != s.device:
             raise ValueError("dout must be [T, H] bf16 on the block's device")
         if ds is not None:  # looked at before anything is added to grads

@@ -4,6 +4,9 @@ The kept tensors are of the stream that forward ran on, and the block alone hold
 its stream as soon as it is let go, so a backward on another stream has to tell it of its reads (``record_stream``) before it lets them go.
 The first tests look at that on the CPU, with tensors that note what is said of them; the GPU ones look at the gradients.
 """
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -104,7 +107,7 @@ class Layer:
 def expert_block():
     block = M.MoEBlock.__new__(M.MoEBlock)      # (its constructor allocates on a GPU)
     block.norm, block.router, block.layer, block.decoder, block.decode_tokens = Norm(), Router(), Layer(), None, 0
-    block._mx, block._kept, block._captured = False, None, None
+    block._mx, block._kept, block._captured, block._held = False, None, None, []
     return block, M.BlockParams(Noted.new(H), torch.zeros(E, H, dtype=BF16), B.moe_weights())
 
 
@@ -134,6 +137,32 @@ def test_a_backward_on_the_same_stream_tells_nothing(make, streams):
     backward(block, torch.zeros(T, H, dtype=BF16))
     for part in (block.norm, block.ffn if make is dense_block else block.router):
         assert all(t.told == [] for t in part.made)
+
+
+def left_alive(block, made):
+    """Which of the tensors that `block`'s operators made are still held, once those have let them go."""
+    refs = [weakref.ref(t) for t in made]
+    for part in (block.norm, getattr(block, "ffn", None), getattr(block, "router", None)):
+        if part is not None:
+            part.made = None
+    made.clear()
+    gc.collect()
+    return [r() is not None for r in refs]
+
+
+@pytest.mark.parametrize("make", [dense_block, expert_block])
+@pytest.mark.parametrize("captured_forward", [False, True])
+def test_what_a_captured_backward_reads_outlives_it(make, captured_forward, streams):
+    """The replays of a backward that was captured by itself read what an eager forward kept. Where forward is of the capture too, the tensors are of the
+    graph's own memory, which the rest of the capture may use again."""
+    block, params = make()
+    streams.capturing = captured_forward
+    block.forward(Noted.new(T, H), params)
+    streams.capturing = True
+    backward(block, torch.zeros(T, H, dtype=BF16))
+    made = block.norm.made[2:] + (block.ffn.made if make is dense_block else block.router.made)
+    alive = left_alive(block, made)
+    assert all(alive) if not captured_forward else not any(alive)
 
 
 # ------------------------------------------------------------------ on the GPU
@@ -214,3 +243,23 @@ def test_an_expert_backward_on_another_stream_beside_new_tensors():
             assert (t.double() - ref.double()).norm() <= 2.0 ** -6 * ref.double().norm()
         del junk
     block.close()
+
+
+@gpu
+def test_a_dense_backward_captured_by_itself():
+    """Its replays take other dout at what the eager forward kept, whatever the program allocates meanwhile."""
+    T, H, I = 300, 264, 520
+    block, p, ((x, res, dout), (_, _, dout2)) = dense(T, H, I)
+    want = [dense_step(block, p, x, res, d)[2:] for d in (dout, dout2)]
+    given = dout.clone()
+    block.forward(x, p, residual=res)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dx, grads = block.backward(given)
+    junk = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for n in (T * H, T * I, 2 * T * H, 4 * T, 4 * T * 3, 4 * T * 5) for _ in range(8)]
+    for d, ref in zip((dout, dout2), want):
+        given.copy_(d)
+        graph.replay()
+        assert all(torch.equal(g, r) for g, r in zip([dx, *grads.values()], ref))
+    del junk
