@@ -567,7 +567,8 @@ typedef struct {
     int32_t y_type;  /* moe_dtype of y and dy */
 } moe_linear_config;
 
-/* Bytes of device workspace (256-byte aligned) that a call for T rows needs; calls that share one must be ordered. */
+/* Bytes of device workspace (256-byte aligned) that a call for T rows on the current device needs (it goes by the device's number of
+ * SMs); calls that share one must be ordered. */
 moe_status moe_linear_size(const moe_linear_config* cfg, int64_t T, int32_t backward, size_t* bytes);
 
 /* y[T, out] = Qrow(x) W^T. `kept` (NULL: none): column blocks of x [T, in], the 8-bit copy of x that the backward
@@ -596,6 +597,7 @@ typedef struct { moe_fp8 gate, up, down; } moe_ffn_weights;
 typedef struct { moe_fp8 x, gate, up; } moe_ffn_kept;
 typedef struct { void *gate, *up, *down; int64_t gate_stride, up_stride, down_stride; } moe_ffn_grads;
 
+/* As moe_linear_size. */
 moe_status moe_ffn_size(const moe_ffn_config* cfg, int64_t T, int32_t backward, size_t* bytes);
 
 /* kept NULL: nothing is kept. y must not overlap x. */

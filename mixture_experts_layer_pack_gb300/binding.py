@@ -454,9 +454,10 @@ def moe_norm_forward(cfg: moe_norm_config, x, weight, y, bias=None, residual=Non
                                        _addr(mean), _addr(rstd), _raw_stream(stream, x.device)), "moe_norm_forward")
 
 
-def _sized(size, sizes, cfg, T):
-    """size(cfg, T), which depends on nothing else, from the dict of those asked for before."""
-    key = (id(cfg), T)  # an object keeps its configurations as long as its sizes
+def _sized(size, sizes, cfg, T, index=0):
+    """size(cfg, T) from the dict of those asked for before; `index`: the current device, where the size depends on its number of
+    SMs (it depends on nothing else)."""
+    key = (id(cfg), T, index)  # an object keeps its configurations as long as its sizes
     n = sizes.get(key)
     if n is None:
         if len(sizes) > 4096:
@@ -1273,7 +1274,7 @@ class MoEFp8Linear:
         w = _codes(torch, weight, self.N, K, MOE_B_SQUARE, index, "weight")
         y = torch.empty((T, self.N), dtype=yt, device=dev)
         kept = _new_codes(torch, T, K, MOE_B_COL, dev) if keep else None
-        size = _sized(moe_linear_size, self._sizes, cfg, T)
+        size = _sized(moe_linear_size, self._sizes, cfg, T, index)
         workspace = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
         status = self._forward(cfg, T, x.data_ptr(), _ld(x), w, y.data_ptr(), self.N, _as_view(kept) if keep else None, _addr(workspace), size,
                                self._stream(index))
@@ -1317,7 +1318,7 @@ class MoEFp8Linear:
                 if gt is None:
                     raise ValueError("dweight must be fp32 or bf16")
                 gt = MOE_G_BF16 if gt == MOE_T_BF16 else MOE_G_FP32
-        size = _sized(_linear_back_size, self._back_sizes, cfg, T)
+        size = _sized(_linear_back_size, self._back_sizes, cfg, T, index)
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
         status = self._backward(cfg, T, dy.data_ptr(), _ld(dy), w, k, _addr(dx), K, _addr(dweight), _ld(dweight) if need_dweight else 0,
                                 gt, 1 if accumulate else 0, workspace.data_ptr(), size, self._stream(index))
@@ -1389,7 +1390,7 @@ class MoEFeedForward:
         if keep:
             kept = (_new_codes(torch, T, H, MOE_B_COL, dev), _new_codes(torch, T, I, MOE_B_ROW, dev), _new_codes(torch, T, I, MOE_B_ROW, dev))
             views = moe_ffn_kept(*[_as_view(v) for v in kept])
-        size = _sized(moe_ffn_size, self._sizes, self.cfg, T)
+        size = _sized(moe_ffn_size, self._sizes, self.cfg, T, index)
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
         status = self._forward(self.cfg, T, x.data_ptr(), _ld(x), w, y.data_ptr(), H, views, workspace.data_ptr(), size, self._stream(index))
         if status:
@@ -1438,7 +1439,7 @@ class MoEFeedForward:
                 raise ValueError("grads must be three buffers, all fp32 or all bf16")
             gt = MOE_G_BF16 if torch.bfloat16 in dtypes else MOE_G_FP32
             at = moe_ffn_grads(*[t.data_ptr() for t in grads], *[_ld(t) for t in grads])
-        size = _sized(_ffn_back_size, self._back_sizes, self.cfg, T)
+        size = _sized(_ffn_back_size, self._back_sizes, self.cfg, T, index)
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
         status = self._backward(self.cfg, T, dy.data_ptr(), _ld(dy), w, views, _addr(dx), H, at, gt, 1 if accumulate else 0,
                                 workspace.data_ptr(), size, self._stream(index))
