@@ -540,7 +540,8 @@ moe_status moe_router_backward(const moe_router_config* cfg, int64_t T, const vo
  *   MOE_B_SQUARE  blocks of 128 x 128              scales [ceil(rows/128), ceil(cols/128)]   (a weight, both ways)
  * (This is not the layer's MXFP8, whose blocks are of 32 and whose scales are powers of two.)
  * Sums over a block of 128 are the tensor cores' fp32 ones, and their scaled sum is fp32 as well.
- * A wait inside a product that gave up (2 s) leaves NaN in its results. */
+ * A wait inside a product that gave up (2 s) leaves NaN in its results (and in a gradient that they are added to), and
+ * moe_fp8_status says so. */
 typedef enum { MOE_B_ROW = 0, MOE_B_COL = 1, MOE_B_SQUARE = 2 } moe_block;
 typedef struct {
     void* q;       /* codes [rows, cols], 16-byte aligned */
@@ -614,6 +615,15 @@ moe_status moe_ffn_forward(const moe_ffn_config* cfg, int64_t T, const void* x, 
 moe_status moe_ffn_backward(const moe_ffn_config* cfg, int64_t T, const void* dy, int64_t dy_stride, const moe_ffn_weights* w,
                             const moe_ffn_kept* kept, void* dx, int64_t dx_stride, const moe_ffn_grads* grads,
                             int32_t g_type, int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Synchronises `stream` and returns MOE_ERR_TIMEOUT if a wait inside a product of 8-bit matrices (moe_linear_*, moe_ffn_*) gave up on the
+ * current device since the last status, else MOE_OK, and clears it before it returns: one word a device, whatever the stream
+ * and the caller. Not for a stream under capture. */
+moe_status moe_fp8_status(void* stream);
+
+/* Test hook for it: enqueues one warp that waits as the products do on a barrier that nothing completes. The wait gives up
+ * after the library's limit (2 s), which moe_fp8_status tells. Asynchronous on `stream`. */
+moe_status moe_fp8_selftest_timeout(void* stream);
 
 /* Number of kernels this library has launched in this process. */
 uint64_t moe_launch_count(void);

@@ -15,7 +15,7 @@ from .binding import (HostPipe, MoEDecoder, MoELayer, MoENorm, MoERouter, MoeErr
                       moe_norm_backward, moe_norm_backward_size, moe_norm_config, moe_norm_forward,
                       moe_router_backward, moe_router_config, moe_router_forward, moe_router_size,
                       MOE_B_COL, MOE_B_ROW, MOE_B_SQUARE, FeedForwardWeights, MoEFeedForward, MoEFp8Linear, fp8_dequantize, fp8_quantize,
-                      fp8_scales_shape, moe_ffn_config, moe_ffn_size, moe_linear_config, moe_linear_size,
+                      fp8_scales_shape, moe_ffn_config, moe_ffn_size, moe_fp8_selftest_timeout, moe_fp8_status, moe_linear_config, moe_linear_size,
                       weights_from_combined_mxfp8)
 from .block import BlockParams, DenseBlock, DenseParams, MoEBlock
 
@@ -31,5 +31,5 @@ __all__ = ["BlockParams", "DenseBlock", "DenseParams", "HostPipe", "MoEBlock", "
            "moe_norm_backward", "moe_norm_backward_size", "moe_norm_config", "moe_norm_forward",
            "moe_router_backward", "moe_router_config", "moe_router_forward", "moe_router_size",
            "MOE_B_COL", "MOE_B_ROW", "MOE_B_SQUARE", "FeedForwardWeights", "MoEFeedForward", "MoEFp8Linear", "fp8_dequantize", "fp8_quantize",
-           "fp8_scales_shape", "moe_ffn_config", "moe_ffn_size", "moe_linear_config", "moe_linear_size",
+           "fp8_scales_shape", "moe_ffn_config", "moe_ffn_size", "moe_fp8_selftest_timeout", "moe_fp8_status", "moe_linear_config", "moe_linear_size",
            "weights_from_combined_mxfp8"]

@@ -104,7 +104,7 @@ EXPORTED = ("moe_workspace_size", "moe_create", "moe_destroy", "moe_saved_size",
             "moe_norm_forward", "moe_norm_backward_size", "moe_norm_backward",
             "moe_router_size", "moe_router_forward", "moe_router_backward",
             "moe_fp8_quantize", "moe_fp8_dequantize", "moe_linear_size", "moe_linear_forward", "moe_linear_backward",
-            "moe_ffn_size", "moe_ffn_forward", "moe_ffn_backward")
+            "moe_ffn_size", "moe_ffn_forward", "moe_ffn_backward", "moe_fp8_status", "moe_fp8_selftest_timeout")
 MOE_K_COUNT = 20
 
 
@@ -189,8 +189,9 @@ def load(build_if_missing: bool = True):
         L.moe_ffn_forward.argtypes = [P(moe_ffn_config), I64, V, I64, P(moe_ffn_weights), V, I64, P(moe_ffn_kept), V, c_size_t, V]
         L.moe_ffn_backward.argtypes = [P(moe_ffn_config), I64, V, I64, P(moe_ffn_weights), P(moe_ffn_kept), V, I64,
                                        P(moe_ffn_grads), I32, I32, V, c_size_t, V]
+        L.moe_fp8_status.argtypes = L.moe_fp8_selftest_timeout.argtypes = [V]
         for name in ("moe_fp8_quantize", "moe_fp8_dequantize", "moe_linear_size", "moe_linear_forward", "moe_linear_backward",
-                     "moe_ffn_size", "moe_ffn_forward", "moe_ffn_backward"):
+                     "moe_ffn_size", "moe_ffn_forward", "moe_ffn_backward", "moe_fp8_status", "moe_fp8_selftest_timeout"):
             getattr(L, name).restype = c_int32
         for name in ("moe_decode_size", "moe_decode_create", "moe_decode", "moe_decode_status", "moe_norm_forward",
                      "moe_norm_backward_size", "moe_norm_backward", "moe_router_size", "moe_router_forward",
@@ -516,6 +517,16 @@ def moe_ffn_size(cfg: moe_ffn_config, T: int, backward=False) -> int:
     n = c_size_t(0)
     _check(load().moe_ffn_size(cfg, T, 1 if backward else 0, ctypes.byref(n)), "moe_ffn_size")
     return n.value
+
+
+def moe_fp8_status(stream=None) -> int:
+    """MOE_ERR_TIMEOUT if a wait inside an 8-bit product gave up on the current device since the last call, else 0 (include/moe.h)."""
+    return int(load().moe_fp8_status(_stream_ptr(stream)))
+
+
+def moe_fp8_selftest_timeout(stream=None):
+    """Enqueues the test of it: one wait of the 8-bit products' that gives up (2 s)."""
+    _check(load().moe_fp8_selftest_timeout(_stream_ptr(stream)), "moe_fp8_selftest_timeout")
 
 
 def moe_launch_count() -> int:

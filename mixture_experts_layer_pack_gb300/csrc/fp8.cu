@@ -1051,4 +1051,12 @@ moe_status moe_ffn_backward(const moe_ffn_config* cfg, int64_t T, const void* dy
     return answer(ffn_backward(k, ws, true, st));
 }
 
+moe_status moe_fp8_status(void* stream) {
+    bool gave_up = false;
+    const cudaError_t e = moe::f8_status(gave_up, static_cast<cudaStream_t>(stream));
+    return gave_up ? MOE_ERR_TIMEOUT : moe::answer(e);
+}
+
+moe_status moe_fp8_selftest_timeout(void* stream) { return moe::answer(moe::launch_f8_wait_selftest(static_cast<cudaStream_t>(stream))); }
+
 }  // extern "C"

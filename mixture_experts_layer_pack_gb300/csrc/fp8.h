@@ -56,6 +56,9 @@ struct F8Maps {
 cudaError_t launch_f8_gemm(int op, int bn, int cg, const F8Maps& maps, const F8Args& args, int sms, cudaStream_t st);
 // sums the partials of every product of `args` into its output
 cudaError_t launch_f8_reduce(const F8Args& args, cudaStream_t st);
+// whether a wait of a product on the current device gave up since the last call; synchronises `st`
+cudaError_t f8_status(bool& gave_up, cudaStream_t st);
+cudaError_t launch_f8_wait_selftest(cudaStream_t st);
 
 // The shared memory that a kernel may ask for, said once for each device
 template <auto Kernel>

@@ -15,7 +15,7 @@
 // either), and so do the two operands of a weight's gradient, whose K are the tokens. A pair of CTAs shares a tile
 // of 256 x 256 where there are tiles enough: each loads half of it, half of what two tiles of 128 x 256 would.
 //
-// Every wait is bounded; after one that gave up the results are NaN (there is no status word to say it in).
+// Every wait is bounded; after one that gave up the results are NaN, and the device's status word says so.
 #include "device_common.cuh"
 #include "fp8.h"
 #include "fp8_device.cuh"
@@ -31,6 +31,8 @@ constexpr int kF8Threads = 128 + 32 * kF8EpiWarps;
 // two sets of 16 sums, so the first warpgroup (loads and products) gives up what the two others take: 56 + 2 * 224 = 3 * 168.
 constexpr int kFewRegs = 56, kManyRegs = 224;
 constexpr uint32_t kTileBytes = 128 * 128;   // 128 rows of 128 codes
+
+__device__ int f8_gave_up;  // a wait on this device gave up since the status was last asked for
 
 template <int OP, int BN, int CG>
 struct F8Cfg {
@@ -818,11 +820,27 @@ __global__ void __launch_bounds__(kF8Threads, 1) f8_gemm_kernel(const __grid_con
 
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) f8_gave_up = 1;
     if (CG == 2) cluster_sync();
     if (warp == 1) {
         tc_fence_after();
         f8_tmem_free<CG>(tmem, 512);
     }
+}
+
+// a warp that waits as the kernel's do, on a barrier that nothing arrives at
+__global__ void __launch_bounds__(32) f8_wait_selftest_kernel() {
+    __shared__ uint64_t bar;
+    __shared__ int abort_flag;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncwarp();
+    (void)f8_wait_warp(&bar, 0, &abort_flag);
+    __syncwarp();
+    if (threadIdx.x == 0 && abort_flag) f8_gave_up = 1;
 }
 
 // ---------------------------------------------------------------- sums of the parts
@@ -893,6 +911,24 @@ cudaError_t launch_f8_gemm(int op, int bn, int cg, const F8Maps& maps, const F8A
         case F8_TN: return launch_op<F8_TN>(bn, cg, maps, a, sms, st);
         default: return launch_op<F8_GU>(bn, cg, maps, a, sms, st);
     }
+}
+
+cudaError_t f8_status(bool& gave_up, cudaStream_t st) {
+    int v = 0;
+    void* word = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(&word, f8_gave_up);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&v, word, sizeof v, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    gave_up = v != 0;
+    if (e != cudaSuccess || !gave_up) return e;
+    e = cudaMemsetAsync(word, 0, sizeof v, st);
+    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;  // the next call may be on another stream
+}
+
+cudaError_t launch_f8_wait_selftest(cudaStream_t st) {
+    f8_wait_selftest_kernel<<<1, 32, 0, st>>>();
+    count_launch();
+    return cudaGetLastError();
 }
 
 cudaError_t launch_f8_reduce(const F8Args& a, cudaStream_t st) {
