@@ -539,7 +539,9 @@ moe_status moe_router_backward(const moe_router_config* cfg, int64_t T, const vo
  *   MOE_B_COL     blocks of 128 down a column      scales [ceil(rows/128), cols]   (a product along the rows)
  *   MOE_B_SQUARE  blocks of 128 x 128              scales [ceil(rows/128), ceil(cols/128)]   (a weight, both ways)
  * (This is not the layer's MXFP8, whose blocks are of 32 and whose scales are powers of two.)
- * Sums over a block of 128 are the tensor cores' fp32 ones, and their scaled sum is fp32 as well.
+ * Sums over a block of 128 are the tensor cores' fp32 ones, and their scaled sum is fp32 as well. The two scales of a block are
+ * multiplied first, in fp32: below 2^-126 their product loses bits (2^-125 of a result for each block along K, at most), above
+ * 2^128 it is infinite (two blocks whose largest magnitudes multiply to 6.8e43 or more), and the result infinite or NaN.
  * A wait inside a product that gave up (2 s) leaves NaN in its results (and in a gradient that they are added to), and
  * moe_fp8_status says so. */
 typedef enum { MOE_B_ROW = 0, MOE_B_COL = 1, MOE_B_SQUARE = 2 } moe_block;

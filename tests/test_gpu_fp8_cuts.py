@@ -88,3 +88,22 @@ def test_backward_offsets_past_32_bits():
     assert not dx[:-300].any()
     for got, name in zip((dx[lo:], *grads), ("dx", "dgate", "dup", "ddown")):
         F.close(got, *want[name], name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N", [(1, 700, 300), (12, 700, 300), (90, 1500, 140), (400, 520, 400)])
+def test_scales_whose_product_is_below_the_normal_range(T, K, N):
+    """Rows of some 1e-36 against weights of 0.05: the product of two blocks' scales is rounded below 2^-126, by 2^-150 at most, which counts as often as the
+    largest sum of a block's codes, 448^2 128: 2^-125.3 for each block along K beside the sums' own bound, and 2^-149 for each rounding of a result there."""
+    g = F.gen(T)
+    x, dy, w = (F.randn(g, T, K) * 1e-36), (F.randn(g, T, N) * 1e-36), F.weight(g, N, K)
+    lin = M.MoEFp8Linear(K, N)
+    y, kept = lin.forward(x, w)
+    dx, _ = lin.backward(dy, w, kept, need_dweight=False)
+    W = F.values(w, F.SQUARE)
+    for got, a, b, k in ((y, x, W.t(), K), (dx, dy, W, N)):
+        a = F.values(F.ref_codes(a, F.ROW), F.ROW)
+        ref, tol = a @ b, F.sum_tol(a.abs() @ b.abs(), k)
+        n = -(-k // 128)
+        err = (got.double() - ref).abs() - tol - n * (448 ** 2 * 128 * 2.0 ** -150 + 20 * 2.0 ** -149)
+        assert float(err.max()) <= 0.0 and got.any()
