@@ -1238,7 +1238,7 @@ def fp8_dequantize(codes, scales, block, dtype=None, out=None, stream=None):
 
 
 def _grad_buffer(t, shape, what):
-    """moe_gtype of a weight's gradient buffer."""
+    """Checks the buffer of a weight's gradient."""
     _as_rows(t, what)
     if t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}")

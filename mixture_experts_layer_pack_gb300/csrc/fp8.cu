@@ -169,7 +169,7 @@ __device__ __forceinline__ int row_lane(int row) { return N == 8 ? row << 1 : ro
 // A block takes 128 x 128 elements, which it reads once and holds in registers: 16 threads a row with eight columns
 // each, a thread eight rows 16 apart. Rows' maxima go through 16 lanes, columns' through registers and shared memory.
 // Memory bounds it once enough blocks share an SM: bf16 is held as it was read, two to a register (64 registers a thread instead
-// of 116), and each scale's division is one lane's.
+// of 116, 36 bytes of them spilled), and each scale's division is one lane's.
 template <typename X>
 __global__ void __launch_bounds__(kQuantThreads, sizeof(X) == 2 ? 4 : 2)
     fp8_quantize_kernel(const X* __restrict__ x, int64_t rows, int cols, int64_t ld, bool wide, Codes row, Codes col, Codes square) {
@@ -407,7 +407,8 @@ __device__ __forceinline__ void gated_back8(const float (&dh)[8], const float (&
 // dh and the kept g, u -> dg and du as row blocks (for dx) and column blocks, h as column blocks (for the weights' gradients).
 // 128 tokens x 128 columns a block. The results are computed twice, for the maxima and for the codes, from inputs that are
 // read twice, the second time from L2: held in registers, they or the results leave room for one block an SM, whose reads,
-// arithmetic and writes then wait for one another (8192 x 8192: 335 us). Its instructions bound it: at 8192 x 8192 one column each 250 us and with
+// arithmetic and writes then wait for one another (8192 x 8192: 335 us). Two blocks an SM leave 64 registers a thread, of which 88 bytes are spilled (108
+// with a clamp). Its instructions bound it: at 8192 x 8192 one column each 250 us and with
 // a clamp 288; two columns each, and the clamp compiled apart, 216 and 272.
 template <bool CLAMP>
 __global__ void __launch_bounds__(kGatedThreads, 2) fp8_gated_back_kernel(const GatedBack a) {
